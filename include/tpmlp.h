@@ -99,7 +99,12 @@ typedef enum { TPMLP_F32 = 0, TPMLP_BF16 = 1 } tpmlp_dtype;
  *   see tpmlp_gemm_plan.) */
 typedef enum { TPMLP_REDUCE_PARTIALS = 0, TPMLP_REDUCE_SPLITK = 1 } tpmlp_reduce_mode;
 
-typedef enum { TPMLP_OP_FORWARD = 0, TPMLP_OP_BACKWARD = 1 } tpmlp_op;
+/* SWIGLU_BACKWARD: tpmlp_swiglu_backward (tpmlp_swiglu_forward sizes as FORWARD). */
+typedef enum {
+    TPMLP_OP_FORWARD = 0,
+    TPMLP_OP_BACKWARD = 1,
+    TPMLP_OP_SWIGLU_BACKWARD = 2
+} tpmlp_op;
 
 /* Forward of one block (§01-§05).
  *   X   [N, D]            input, replicated to every shard (read once)
@@ -152,6 +157,30 @@ tpmlp_status tpmlp_backward(tpmlp_dtype dt, int64_t N, int64_t D, int64_t F, int
                             void* dX, void* const* dW1, void* const* dW2,
                             void* const* db1, void* db2, tpmlp_reduce_mode mode,
                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Backward of the gated block, for upstream gradient dY [N, D]. With
+ * s = 1 / (1 + exp(-G)), per shard r:
+ *   dH = dY Wd^T,  dU = dH * G s,  dG = dH * U s (1 + G (1 - s)),
+ *   dWd = H^T dY,  dWg = X^T dG,  dWu = X^T dU,
+ *   dX = sum_r (dG^(r) Wg^(r)^T + dU^(r) Wu^(r)^T)
+ * dG and dU leave the product dY Wd^T's epilogue directly; they are stored
+ * (dt) because three products read them. dX runs as ONE product whose K loop
+ * walks (r, gate | up, k).
+ *   inputs: X [N, D]; Wg, Wu T x [D, F/T]; Wd T x [F/T, D]; H, G, U
+ *           T x [N, F/T] as tpmlp_swiglu_forward wrote them; dY [N, D]
+ *   outputs: dX [N, D]; dWg, dWu T x [D, F/T]; dWd T x [F/T, D]
+ * Workspace: dG (T x [N, F/T] of dt, shard r at byte
+ * r * round_up(N*(F/T)*sizeof(dt), 256)), dU after those in the same layout,
+ * then in PARTIALS mode the T fp32 dX partials; its size is
+ * tpmlp_workspace_bytes(TPMLP_OP_SWIGLU_BACKWARD, ...). N = 0 writes zeros to
+ * dWg, dWu and dWd. Errors as tpmlp_backward. */
+tpmlp_status tpmlp_swiglu_backward(tpmlp_dtype dt, int64_t N, int64_t D, int64_t F, int T,
+                                   const void* X, const void* const* Wg, const void* const* Wu,
+                                   const void* const* Wd, const void* const* H,
+                                   const void* const* G, const void* const* U, const void* dY,
+                                   void* dX, void* const* dWg, void* const* dWu, void* const* dWd,
+                                   tpmlp_reduce_mode mode, void* workspace, size_t workspace_bytes,
+                                   void* stream);
 
 /* Block-end reduction alone (§04-§05): Y = sum_{r=0}^{T-1} P^(r) + b2, summed
  * in fp32 in shard order, b2 (element type dt, or NULL) added once, the result
@@ -230,6 +259,128 @@ tpmlp_status tpmlp_vocab_ce(int64_t N, int64_t V, int T, const float* logits,
 tpmlp_status tpmlp_vocab_ce_backward(int64_t N, int64_t V, int T, const float* logits,
                                      const int64_t* targets, const float* loss_per_token,
                                      float grad_scale, float* dlogits, void* stream);
+
+/* ---- vocabulary-side operators of training and serving --------------------
+ * Library extensions; the source pages have no counterpart. Logits here are
+ * dt (fp32 or bf16) with a row pitch of ld elements (ld >= V), any alignment
+ * of their element type; everything computed from them is fp32. A logit of
+ * -inf is a masked token: probability 0, whatever else the row holds. A row
+ * with a NaN or +inf logit gives NaN wherever the row's distribution enters
+ * (such a row's top ids are in range and otherwise unspecified). */
+
+/* Longest list tpmlp_vocab_logprobs returns, and the longest teacher list. */
+#define TPMLP_MAX_TOP 128
+#define TPMLP_MAX_TEACHER 1024
+
+/* Log probabilities of given tokens, with the distribution's entropy and its K
+ * most likely tokens. With lse_n = ln sum_v exp(z[n, v]):
+ *   logprob[n] = z[n, t_n] - lse_n
+ *   rank[n]    = 1 + #{v: z[n, v] > z[n, t_n]} + #{v < t_n: z[n, v] = z[n, t_n]}
+ *   entropy[n] = -sum_{v: p_v > 0} p_v ln p_v,  p_v = exp(z[n, v] - lse_n)
+ *   top_ids[n, :], top_logprobs[n, :]: the first K tokens by falling logit,
+ *              equal logits by rising index (rank is the place in that order)
+ * A row without a finite logit has lse = -inf, log probabilities -inf and
+ * entropy 0. Shard k owns columns [k V/T, (k+1) V/T); the result does not
+ * depend on T.
+ *   logits        [N, V] of dt, row pitch ld
+ *   targets       [N] int64 in [0, V), or NULL (logprob and rank must be NULL)
+ *   logprob       [N] fp32 out, or NULL
+ *   rank          [N] int32 out, or NULL
+ *   entropy       [N] fp32 out, or NULL
+ *   lse           [N] fp32 out, or NULL
+ *   top_ids       [N, K] int32 out, top_logprobs [N, K] fp32 out (unused for K = 0)
+ * Errors: TPMLP_ERR_SHAPE if V % T != 0, ld < V, K outside
+ * [0, min(V, TPMLP_MAX_TOP)]; TPMLP_ERR_ALIGN if logits is not aligned to its
+ * element. A target outside [0, V) writes NaN (rank 0) for that token and sets
+ * TPMLP_ERR_ARG in the device error word. */
+tpmlp_status tpmlp_vocab_logprobs(tpmlp_dtype dt, int64_t N, int64_t V, int T, int K,
+                                  const void* logits, int64_t ld, const int64_t* targets,
+                                  float* logprob, int32_t* rank, float* entropy, float* lse,
+                                  int32_t* top_ids, float* top_logprobs, void* stream);
+
+/* Distillation from a teacher's K most likely tokens: per token the
+ * Kullback-Leibler divergence of the student's distribution from the
+ * teacher's, the teacher renormalised over its K tokens, at temperature tau:
+ *   q_k = softmax over the row's slots of teacher_logits[n, k] / tau
+ *   ln p_v = z[n, v] / tau - lse_n,   lse_n = ln sum_v exp(z[n, v] / tau)
+ *   loss[n] = tau^2 sum_{k: q_k > 0} q_k (ln q_k - ln p_{id_k})
+ * teacher_ids / teacher_logits take tpmlp_vocab_logprobs' top_ids and
+ * top_logprobs as they are (softmax forgets the constant lse). A slot with id
+ * -1 is empty; ids may repeat (each slot counts). A row whose slots are all
+ * empty, or all hold -inf, is a padding position: loss 0, lse 0, gradient 0,
+ * and its logits are not read.
+ *   logits          [N, V] of dt, row pitch ld
+ *   teacher_ids     [N, K] int32 in [-1, V)
+ *   teacher_logits  [N, K] fp32
+ *   loss_per_token  [N] fp32 out
+ *   loss_mean       [1] fp32 out, or NULL: (1/N) sum_n loss_n (fixed order)
+ *   lse             [N] fp32 out, or NULL (the backward's input)
+ * Errors: TPMLP_ERR_ARG for tau not finite or <= 0; TPMLP_ERR_SHAPE if
+ * V % T != 0, ld < V, K outside [1, TPMLP_MAX_TEACHER]; TPMLP_ERR_ALIGN if a
+ * pointer is not aligned to its element. An id outside [-1, V) writes NaN for
+ * that row (loss and gradient) and sets TPMLP_ERR_ARG in the device error word. */
+tpmlp_status tpmlp_vocab_distill(tpmlp_dtype dt, int64_t N, int64_t V, int T, int K,
+                                 const void* logits, int64_t ld, const int32_t* teacher_ids,
+                                 const float* teacher_logits, float tau, float* loss_per_token,
+                                 float* loss_mean, float* lse, void* stream);
+
+/* Gradient of grad_scale * sum_n grad_tokens[n] * loss[n] with respect to the
+ * logits, from the forward's lse:
+ *   dlogits[n, v] = w_n (p_v - sum_{k: id_k = v} q_k),
+ *   w_n = grad_scale * grad_tokens[n] * tau       (grad_tokens NULL: all ones)
+ * computed in fp32 and rounded once to dt.
+ *   lse          [N] fp32 as written by tpmlp_vocab_distill
+ *   grad_tokens  [N] fp32 or NULL
+ *   dlogits      [N, V] of dt out, row pitch ldd >= V; may be the logits
+ *                buffer itself (in place, ldd = ld)
+ * Errors as tpmlp_vocab_distill. */
+tpmlp_status tpmlp_vocab_distill_backward(tpmlp_dtype dt, int64_t N, int64_t V, int T, int K,
+                                          const void* logits, int64_t ld,
+                                          const int32_t* teacher_ids, const float* teacher_logits,
+                                          float tau, const float* lse, const float* grad_tokens,
+                                          float grad_scale, void* dlogits, int64_t ldd,
+                                          void* stream);
+
+/* Both of the above in one launch, for callers that know the upstream
+ * gradient beforehand: the logits come from memory once. Outputs are those of
+ * the two calls (lse may be NULL; dlogits may be the logits buffer). */
+tpmlp_status tpmlp_vocab_distill_with_grad(tpmlp_dtype dt, int64_t N, int64_t V, int T, int K,
+                                           const void* logits, int64_t ld,
+                                           const int32_t* teacher_ids, const float* teacher_logits,
+                                           float tau, float* loss_per_token, float* loss_mean,
+                                           float* lse, const float* grad_tokens, float grad_scale,
+                                           void* dlogits, int64_t ldd, void* stream);
+
+/* tpmlp_vocab_embedding times a factor: out[n] = scale * table[ids[n]],
+ * multiplied in fp32 and rounded once to dt. Arguments, shards and errors as
+ * tpmlp_vocab_embedding. */
+tpmlp_status tpmlp_vocab_embedding_scaled(tpmlp_dtype dt, int64_t N, int64_t V, int64_t Hd, int T,
+                                          const int64_t* ids, const void* const* table,
+                                          float scale, void* out, void* stream);
+
+/* Gradient of tpmlp_vocab_embedding_scaled with respect to the table:
+ *   dtable[v] = scale * sum_{n: ids[n] = v} dout[n]
+ * The tokens are sorted by id first, so each table row is written once, its
+ * sum taken in fp32 in an order that depends on the sizes and ids alone (the
+ * same bits on every run) and rounded once. Every row of every shard is
+ * written: rows no token names get zeros.
+ * With accumulate != 0 the sum is added to what dtable holds (in fp32, one
+ * rounding) and rows no token names are left alone.
+ *   ids        [N] int64
+ *   dout       [N, Hd] of dt
+ *   dtable     host array of T device pointers, each [V/T, Hd] of grad_dt
+ *   workspace  tpmlp_vocab_embedding_backward_workspace_bytes(N, V, Hd) bytes,
+ *              16-byte aligned
+ * Errors: TPMLP_ERR_SHAPE if V % T != 0, or N or V above 2^31 - 2;
+ * TPMLP_ERR_WORKSPACE. An id outside [0, V) contributes to no row and sets
+ * TPMLP_ERR_ARG in the device error word. */
+tpmlp_status tpmlp_vocab_embedding_backward(tpmlp_dtype dt, tpmlp_dtype grad_dt, int64_t N,
+                                            int64_t V, int64_t Hd, int T, const int64_t* ids,
+                                            const void* dout, float scale, int accumulate,
+                                            void* const* dtable, void* workspace,
+                                            size_t workspace_bytes, void* stream);
+/* Workspace bytes of the call above; (size_t)-1 for invalid sizes. */
+size_t tpmlp_vocab_embedding_backward_workspace_bytes(int64_t N, int64_t V, int64_t Hd);
 
 /* Size in bytes of the library's own scratch array (see tpmlp_forward_noalloc). */
 #define TPMLP_NOALLOC_SCRATCH_BYTES (8u << 20)

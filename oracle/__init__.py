@@ -22,6 +22,10 @@ What it computes (plain definitions, no blocking, fusion or reordering):
   (same page, §08 gated MLP).
 - ``ce.vocab_ce_backward``: grad_scale * (softmax(z) - onehot(t)) (course
   notes §3.6.4).
+- ``mlp.swiglu_backward``: the gated block's gradients by the chain rule.
+- ``vocab``: token log probabilities with entropy, rank and top tokens;
+  distillation from a teacher's top tokens and its gradient; the embedding
+  table's gradient.
 - ``embedding.vocab_embedding``: out[n] = E[ids[n]] (textbook §4.2.3, course
   notes §3.4 "TP for Embedding").
 - ``sharded``: the per-shard algorithm (column shard -> local activation ->
@@ -38,4 +42,4 @@ torch.logsumexp for the cross-entropy. Every function here has at least one
 pin; none is "parity unpinned".
 """
 
-from . import mlp, ce, sharded, embedding  # noqa: F401
+from . import mlp, ce, sharded, embedding, vocab  # noqa: F401

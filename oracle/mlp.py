@@ -153,3 +153,18 @@ def swiglu_forward(X, Wg, Wu, Wd):
     U = X @ Wu
     H = silu(G) * U
     return {"G": G, "U": U, "H": H, "Y": H @ Wd}
+
+
+def swiglu_backward(X, Wg, Wu, Wd, H, G, U, dY):
+    """Gradients of <dY, Y> of the gated block from its saved H, G and U:
+    dH = dY Wd^T, dU = dH SiLU(G), dG = dH U s (1 + G (1 - s)) with
+    s = 1 / (1 + exp(-G)), dWd = H^T dY, dWg = X^T dG, dWu = X^T dU,
+    dX = dG Wg^T + dU Wu^T."""
+    X, Wg, Wu, Wd = as_f64(X), as_f64(Wg), as_f64(Wu), as_f64(Wd)
+    H, G, U, dY = as_f64(H), as_f64(G), as_f64(U), as_f64(dY)
+    dH = dY @ Wd.T
+    s = 1.0 / (1.0 + np.exp(-G))
+    dU = dH * G * s
+    dG = dH * U * s * (1.0 + G * (1.0 - s))
+    return {"dH": dH, "dG": dG, "dU": dU, "dX": dG @ Wg.T + dU @ Wu.T, "dWg": X.T @ dG,
+            "dWu": X.T @ dU, "dWd": H.T @ dY}

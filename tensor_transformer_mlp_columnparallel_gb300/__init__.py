@@ -26,13 +26,21 @@ from ._binding import (  # noqa: F401
     tpmlp_selftest_gemm_stall,
     tpmlp_selftest_wait_timeout,
     tpmlp_set_wait_timeout_ns,
+    tpmlp_swiglu_backward,
     tpmlp_swiglu_forward,
     tpmlp_timing_enable,
     tpmlp_timing_read,
     tpmlp_timing_reset,
     tpmlp_vocab_ce,
     tpmlp_vocab_ce_backward,
+    tpmlp_vocab_distill,
+    tpmlp_vocab_distill_backward,
+    tpmlp_vocab_distill_with_grad,
     tpmlp_vocab_embedding,
+    tpmlp_vocab_embedding_backward,
+    tpmlp_vocab_embedding_backward_workspace_bytes,
+    tpmlp_vocab_embedding_scaled,
+    tpmlp_vocab_logprobs,
     tpmlp_workspace_bytes,
     tpmlp_workspace_bytes_balanced,
 )
@@ -151,3 +159,115 @@ def swiglu_forward(X, Wg, Wu, Wd, mode: str = "splitk", save_gate_up: bool = Fal
     ws = _workspace(tpmlp_workspace_bytes_balanced(_binding.OP_FORWARD, dt, N, D, Fs * T, T, mode), dev)
     tpmlp_swiglu_forward(X, list(Wg), list(Wu), list(Wd), Y, H, G, U, mode, ws)
     return Y, H, G, U
+
+
+def swiglu_backward(X, Wg, Wu, Wd, H, G, U, dY, mode: str = "splitk",
+                    workspace: Optional[torch.Tensor] = None):
+    """Backward of the gated MLP from swiglu_forward's H, G and U. Returns
+    (dX, dWg list, dWu list, dWd list)."""
+    T = len(Wg)
+    N, D = X.shape
+    Fs = Wg[0].shape[1]
+    dev, dt = X.device, X.dtype
+    dX = torch.empty((N, D), dtype=dt, device=dev)
+    dWg = [torch.empty((D, Fs), dtype=dt, device=dev) for _ in range(T)]
+    dWu = [torch.empty((D, Fs), dtype=dt, device=dev) for _ in range(T)]
+    dWd = [torch.empty((Fs, D), dtype=dt, device=dev) for _ in range(T)]
+    if workspace is None:
+        workspace = _workspace(tpmlp_workspace_bytes_balanced(_binding.OP_SWIGLU_BACKWARD, dt, N, D,
+                                                              Fs * T, T, mode), dev)
+    tpmlp_swiglu_backward(X, list(Wg), list(Wu), list(Wd), list(H), list(G), list(U), dY, dX, dWg,
+                          dWu, dWd, mode, workspace)
+    return dX, dWg, dWu, dWd
+
+
+def vocab_logprobs(logits: torch.Tensor, targets: torch.Tensor, T: int, top_k: int = 0):
+    """Log probabilities of `targets` under fp32 or bf16 logits. Returns
+    (logprob [N], rank [N] int32 from 1, entropy [N], top_ids [N, top_k] int32,
+    top_logprobs [N, top_k])."""
+    N = logits.shape[0]
+    dev = logits.device
+    logprob = torch.empty((N,), dtype=torch.float32, device=dev)
+    rank = torch.empty((N,), dtype=torch.int32, device=dev)
+    entropy = torch.empty((N,), dtype=torch.float32, device=dev)
+    ids = torch.empty((N, top_k), dtype=torch.int32, device=dev)
+    top = torch.empty((N, top_k), dtype=torch.float32, device=dev)
+    tpmlp_vocab_logprobs(logits, targets, T, top_k, logprob, rank, entropy, None, ids, top)
+    return logprob, rank, entropy, ids, top
+
+
+def _dlogits_like(logits: torch.Tensor, in_place: bool) -> torch.Tensor:
+    """A gradient in rows of the logits' pitch, so that both sides of a row
+    have the same alignment."""
+    if in_place:
+        return logits
+    N, V = logits.shape
+    ld = logits.stride(0) if N > 1 else V
+    return torch.empty((N, ld), dtype=logits.dtype, device=logits.device)[:, :V]
+
+
+def vocab_distill(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
+                  T: int, temperature: float = 1.0):
+    """Distillation loss from a teacher's top tokens (teacher_ids [N, K] int32,
+    -1 for an empty slot; teacher_logits [N, K] fp32: logits or log
+    probabilities). Returns (loss_per_token [N], loss_mean [1], lse [N])."""
+    N = logits.shape[0]
+    loss = torch.empty((N,), dtype=torch.float32, device=logits.device)
+    mean = torch.empty((1,), dtype=torch.float32, device=logits.device)
+    lse = torch.empty((N,), dtype=torch.float32, device=logits.device)
+    tpmlp_vocab_distill(logits, teacher_ids, teacher_logits, T, temperature, loss, mean, lse)
+    return loss, mean, lse
+
+
+def vocab_distill_backward(logits: torch.Tensor, teacher_ids: torch.Tensor,
+                           teacher_logits: torch.Tensor, T: int, lse: torch.Tensor,
+                           temperature: float = 1.0, grad_scale: float = 1.0,
+                           grad_tokens: Optional[torch.Tensor] = None, in_place: bool = False):
+    """Gradient of grad_scale * sum_n grad_tokens[n] * loss[n] with respect to
+    the logits, from vocab_distill's lse."""
+    d = _dlogits_like(logits, in_place)
+    tpmlp_vocab_distill_backward(logits, teacher_ids, teacher_logits, T, temperature, lse,
+                                 grad_tokens, grad_scale, d)
+    return d
+
+
+def vocab_distill_with_grad(logits: torch.Tensor, teacher_ids: torch.Tensor,
+                            teacher_logits: torch.Tensor, T: int, temperature: float = 1.0,
+                            grad_scale: float = 1.0, grad_tokens: Optional[torch.Tensor] = None,
+                            in_place: bool = False):
+    """vocab_distill and vocab_distill_backward in one launch. Returns
+    (loss_per_token, loss_mean, lse, dlogits)."""
+    N = logits.shape[0]
+    loss = torch.empty((N,), dtype=torch.float32, device=logits.device)
+    mean = torch.empty((1,), dtype=torch.float32, device=logits.device)
+    lse = torch.empty((N,), dtype=torch.float32, device=logits.device)
+    d = _dlogits_like(logits, in_place)
+    tpmlp_vocab_distill_with_grad(logits, teacher_ids, teacher_logits, T, temperature, loss, mean,
+                                  lse, grad_tokens, grad_scale, d)
+    return loss, mean, lse, d
+
+
+def vocab_embedding_scaled(ids: torch.Tensor, table: Sequence[torch.Tensor], scale: float):
+    """Embedding rows of `ids` times `scale`, rounded once."""
+    out = torch.empty((ids.shape[0], table[0].shape[1]), dtype=table[0].dtype, device=ids.device)
+    tpmlp_vocab_embedding_scaled(ids, list(table), scale, out)
+    return out
+
+
+def vocab_embedding_backward(ids: torch.Tensor, dout: torch.Tensor, V: int, T: int,
+                             scale: float = 1.0, grad_dtype: torch.dtype = torch.float32,
+                             accumulate_into: Optional[Sequence[torch.Tensor]] = None,
+                             workspace: Optional[torch.Tensor] = None):
+    """Table gradient of vocab_embedding_scaled: T shards [V/T, Hd], new ones of
+    grad_dtype, or `accumulate_into` with the sums added to it."""
+    N, Hd = dout.shape
+    if T < 1 or V % T != 0:
+        raise TpmlpError(_binding.ERR_SHAPE, _binding.status_str(_binding.ERR_SHAPE))
+    if accumulate_into is not None and [tuple(t.shape) for t in accumulate_into] != [(V // T, Hd)] * T:
+        raise ValueError("accumulate_into must hold T shards of [V/T, Hd]")
+    dtable = list(accumulate_into) if accumulate_into is not None else [
+        torch.empty((V // T, Hd), dtype=grad_dtype, device=dout.device) for _ in range(T)]
+    if workspace is None:
+        workspace = _workspace(tpmlp_vocab_embedding_backward_workspace_bytes(N, V, Hd), dout.device)
+    tpmlp_vocab_embedding_backward(ids, dout, scale, accumulate_into is not None, dtable, workspace)
+    return dtable

@@ -23,7 +23,8 @@ OK, ERR_ARG, ERR_SHAPE, ERR_ALIGN, ERR_DTYPE, ERR_CUDA, ERR_TIMEOUT, ERR_WORKSPA
 ACT = {"relu": 0, "gelu_tanh": 1, "gelu_erf": 2, "gelu_sigmoid": 3}
 DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 MODE = {"partials": 0, "splitk": 1}
-OP_FORWARD, OP_BACKWARD = 0, 1
+OP_FORWARD, OP_BACKWARD, OP_SWIGLU_BACKWARD = 0, 1, 2
+MAX_TOP, MAX_TEACHER = 128, 1024
 
 
 class TpmlpError(RuntimeError):
@@ -42,6 +43,7 @@ _lib = None
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
+_f32 = ctypes.c_float
 _PP = ctypes.POINTER(ctypes.c_void_p)
 
 _SIGNATURES = {
@@ -53,6 +55,20 @@ _SIGNATURES = {
                                     _PP, _int, _vp, ctypes.c_size_t, _vp]),
     "tpmlp_backward": (_int, [_int, _i64, _i64, _i64, _int, _int, _vp, _PP, _PP, _PP, _PP, _vp,
                               _vp, _PP, _PP, _PP, _vp, _int, _vp, ctypes.c_size_t, _vp]),
+    "tpmlp_swiglu_backward": (_int, [_int, _i64, _i64, _i64, _int, _vp, _PP, _PP, _PP, _PP, _PP,
+                                     _PP, _vp, _vp, _PP, _PP, _PP, _int, _vp, ctypes.c_size_t, _vp]),
+    "tpmlp_vocab_logprobs": (_int, [_int, _i64, _i64, _int, _int, _vp, _i64, _vp, _vp, _vp, _vp,
+                                    _vp, _vp, _vp, _vp]),
+    "tpmlp_vocab_distill": (_int, [_int, _i64, _i64, _int, _int, _vp, _i64, _vp, _vp, _f32, _vp,
+                                   _vp, _vp, _vp]),
+    "tpmlp_vocab_distill_backward": (_int, [_int, _i64, _i64, _int, _int, _vp, _i64, _vp, _vp,
+                                            _f32, _vp, _vp, _f32, _vp, _i64, _vp]),
+    "tpmlp_vocab_distill_with_grad": (_int, [_int, _i64, _i64, _int, _int, _vp, _i64, _vp, _vp,
+                                             _f32, _vp, _vp, _vp, _vp, _f32, _vp, _i64, _vp]),
+    "tpmlp_vocab_embedding_scaled": (_int, [_int, _i64, _i64, _i64, _int, _vp, _PP, _f32, _vp, _vp]),
+    "tpmlp_vocab_embedding_backward": (_int, [_int, _int, _i64, _i64, _i64, _int, _vp, _vp, _f32,
+                                              _int, _PP, _vp, ctypes.c_size_t, _vp]),
+    "tpmlp_vocab_embedding_backward_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
     "tpmlp_block_reduce": (_int, [_int, _i64, _i64, _int, _PP, _vp, _vp, _vp]),
     "tpmlp_block_reduce_scatter": (_int, [_int, _i64, _i64, _int, _PP, _vp, _PP, _vp]),
     "tpmlp_forward_reduce_scatter": (_int, [_int, _i64, _i64, _i64, _int, _int, _vp, _PP, _PP, _PP,
@@ -145,6 +161,27 @@ def _require(ts, device, dtype):
             raise TypeError(f"expected {dtype}, got {t.dtype}")
         if not t.is_contiguous():
             raise ValueError("tensors must be contiguous (row-major)")
+
+
+def _require_rows(t, what: str) -> int:
+    """Row pitch of a [N, V] matrix whose rows are contiguous."""
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be a matrix")
+    N, V = t.shape
+    if not t.is_cuda:
+        raise ValueError("all tensors must live on the same CUDA device")
+    if V > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {what} must be contiguous")
+    if N <= 1:
+        return max(V, 1)
+    if t.stride(0) < V:
+        raise ValueError(f"the rows of {what} must not overlap")
+    return t.stride(0)
+
+
+def _require_len(t, n: int, what: str):
+    if t is not None and t.numel() != n:
+        raise ValueError(f"{what} must hold {n} elements")
 
 
 # ---------------------------------------------------------------------------
@@ -286,6 +323,141 @@ def tpmlp_vocab_ce_backward(logits, targets, T: int, loss_per_token, grad_scale:
     _require([targets], logits.device, torch.int64)
     _check(lib().tpmlp_vocab_ce_backward(N, V, T, _ptr(logits), _ptr(targets), _ptr(loss_per_token),
                                          float(grad_scale), _ptr(dlogits), _stream(logits)))
+
+
+def tpmlp_swiglu_backward(X, Wg, Wu, Wd, H, G, U, dY, dX, dWg, dWu, dWd, mode: str, workspace):
+    """Gradients of the gated block for upstream dY (see include/tpmlp.h)."""
+    T = len(Wg)
+    N, D = X.shape
+    Fs = Wg[0].shape[1]
+    _require([X, dY, dX, *Wg, *Wu, *Wd, *H, *G, *U, *dWg, *dWu, *dWd], X.device, X.dtype)
+    _require([workspace], X.device, None)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().tpmlp_swiglu_backward(_dtype_code(X), N, D, Fs * T, T, _ptr(X), _ptrs(Wg),
+                                       _ptrs(Wu), _ptrs(Wd), _ptrs(H), _ptrs(G), _ptrs(U), _ptr(dY),
+                                       _ptr(dX), _ptrs(dWg), _ptrs(dWu), _ptrs(dWd), MODE[mode],
+                                       _ptr(workspace), ws_bytes, _stream(X)))
+
+
+def tpmlp_vocab_logprobs(logits, targets, T: int, K: int, logprob=None, rank=None, entropy=None,
+                         lse=None, top_ids=None, top_logprobs=None):
+    """Log probabilities and ranks of `targets`, entropies and the K most
+    likely tokens of each row (see include/tpmlp.h)."""
+    ld = _require_rows(logits, "logits")
+    N, V = logits.shape
+    _require([targets], logits.device, torch.int64)
+    _require([logprob, entropy, lse, top_logprobs], logits.device, torch.float32)
+    _require([rank, top_ids], logits.device, torch.int32)
+    for t in (targets, logprob, rank, entropy, lse):
+        _require_len(t, N, "a per-token tensor")
+    for t in (top_ids, top_logprobs):
+        _require_len(t, N * K, "a top list")
+    _check(lib().tpmlp_vocab_logprobs(_dtype_code(logits), N, V, T, K, _ptr(logits), ld,
+                                      _ptr(targets), _ptr(logprob), _ptr(rank), _ptr(entropy),
+                                      _ptr(lse), _ptr(top_ids), _ptr(top_logprobs),
+                                      _stream(logits)))
+
+
+def _require_teacher(logits, teacher_ids, teacher_logits) -> int:
+    _require([teacher_ids], logits.device, torch.int32)
+    _require([teacher_logits], logits.device, torch.float32)
+    N = logits.shape[0]
+    if teacher_ids.dim() != 2 or teacher_ids.shape[0] != N or teacher_ids.shape != teacher_logits.shape:
+        raise ValueError("teacher_ids and teacher_logits must be [N, K]")
+    return teacher_ids.shape[1]
+
+
+def tpmlp_vocab_distill(logits, teacher_ids, teacher_logits, T: int, tau: float, loss_per_token,
+                        loss_mean=None, lse=None):
+    """Distillation loss per token from the teacher's top tokens."""
+    ld = _require_rows(logits, "logits")
+    N, V = logits.shape
+    K = _require_teacher(logits, teacher_ids, teacher_logits)
+    _require([loss_per_token, loss_mean, lse], logits.device, torch.float32)
+    for t in (loss_per_token, lse):
+        _require_len(t, N, "a per-token tensor")
+    _check(lib().tpmlp_vocab_distill(_dtype_code(logits), N, V, T, K, _ptr(logits), ld,
+                                     _ptr(teacher_ids), _ptr(teacher_logits), float(tau),
+                                     _ptr(loss_per_token), _ptr(loss_mean), _ptr(lse),
+                                     _stream(logits)))
+
+
+def _require_dlogits(logits, dlogits) -> int:
+    ldd = _require_rows(dlogits, "dlogits")
+    if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype or dlogits.device != logits.device:
+        raise ValueError("dlogits must have the shape, type and device of logits")
+    return ldd
+
+
+def tpmlp_vocab_distill_backward(logits, teacher_ids, teacher_logits, T: int, tau: float, lse,
+                                 grad_tokens, grad_scale: float, dlogits):
+    """Gradient of the distillation loss from the forward's lse; dlogits may be
+    logits itself (in place)."""
+    ld = _require_rows(logits, "logits")
+    N, V = logits.shape
+    K = _require_teacher(logits, teacher_ids, teacher_logits)
+    ldd = _require_dlogits(logits, dlogits)
+    _require([lse, grad_tokens], logits.device, torch.float32)
+    for t in (lse, grad_tokens):
+        _require_len(t, N, "a per-token tensor")
+    _check(lib().tpmlp_vocab_distill_backward(_dtype_code(logits), N, V, T, K, _ptr(logits), ld,
+                                              _ptr(teacher_ids), _ptr(teacher_logits), float(tau),
+                                              _ptr(lse), _ptr(grad_tokens), float(grad_scale),
+                                              _ptr(dlogits), ldd, _stream(logits)))
+
+
+def tpmlp_vocab_distill_with_grad(logits, teacher_ids, teacher_logits, T: int, tau: float,
+                                  loss_per_token, loss_mean, lse, grad_tokens, grad_scale: float,
+                                  dlogits):
+    """Loss and gradient in one launch; dlogits may be logits itself."""
+    ld = _require_rows(logits, "logits")
+    N, V = logits.shape
+    K = _require_teacher(logits, teacher_ids, teacher_logits)
+    ldd = _require_dlogits(logits, dlogits)
+    _require([loss_per_token, loss_mean, lse, grad_tokens], logits.device, torch.float32)
+    for t in (loss_per_token, lse, grad_tokens):
+        _require_len(t, N, "a per-token tensor")
+    _check(lib().tpmlp_vocab_distill_with_grad(
+        _dtype_code(logits), N, V, T, K, _ptr(logits), ld, _ptr(teacher_ids), _ptr(teacher_logits),
+        float(tau), _ptr(loss_per_token), _ptr(loss_mean), _ptr(lse), _ptr(grad_tokens),
+        float(grad_scale), _ptr(dlogits), ldd, _stream(logits)))
+
+
+def tpmlp_vocab_embedding_scaled(ids, table: Sequence[torch.Tensor], scale: float, out):
+    """out[n] = scale * table row ids[n] (table split by rows into len(table) shards)."""
+    T = len(table)
+    Vs, Hd = table[0].shape
+    _require([ids], out.device, torch.int64)
+    _require([*table, out], out.device, out.dtype)
+    _require_len(out, ids.numel() * Hd, "out")
+    _check(lib().tpmlp_vocab_embedding_scaled(_dtype_code(out), ids.numel(), Vs * T, Hd, T,
+                                              _ptr(ids), _ptrs(table), float(scale), _ptr(out),
+                                              _stream(out)))
+
+
+def tpmlp_vocab_embedding_backward_workspace_bytes(N: int, V: int, Hd: int) -> int:
+    return int(lib().tpmlp_vocab_embedding_backward_workspace_bytes(N, V, Hd))
+
+
+def tpmlp_vocab_embedding_backward(ids, dout, scale: float, accumulate: bool,
+                                   dtable: Sequence[torch.Tensor], workspace):
+    """dtable[v] = scale * sum of dout rows whose id is v (added to dtable with
+    `accumulate`); dtable is split by rows into len(dtable) shards."""
+    T = len(dtable)
+    Vs, Hd = dtable[0].shape
+    _require([ids], dout.device, torch.int64)
+    _require([dout], dout.device, None)
+    _require([*dtable], dout.device, dtable[0].dtype)
+    _require([workspace], dout.device, None)
+    _require_len(dout, ids.numel() * Hd, "dout")
+    for t in dtable:
+        _require_len(t, Vs * Hd, "a shard of dtable")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().tpmlp_vocab_embedding_backward(_dtype_code(dout), _dtype_code(dtable[0]),
+                                                ids.numel(), Vs * T, Hd, T, _ptr(ids), _ptr(dout),
+                                                float(scale), 1 if accumulate else 0,
+                                                _ptrs(dtable), _ptr(workspace), ws_bytes,
+                                                _stream(dout)))
 
 
 def tpmlp_check_device_error(device=None) -> int:

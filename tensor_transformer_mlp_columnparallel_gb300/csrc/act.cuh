@@ -51,6 +51,18 @@ __device__ __forceinline__ float act_grad(int act, float z) {
 // SiLU(z) = z / (1 + exp(-z)), the gate nonlinearity of the gated MLP.
 __device__ __forceinline__ float silu_f(float z) { return z / (1.f + expf(-z)); }
 
+// Derivatives of h = SiLU(g) u for an upstream dh, s = 1 / (1 + exp(-g)):
+//   du = dh g s,  dg = dh u s (1 + g (1 - s)),  and 1 - s = e s with e = exp(-g).
+// The exponent is clamped at 80 so that e stays finite (e s is at most 1, so
+// it is formed before the product with g); for g < -80 both derivatives are
+// below 1e-34 |g dh| (1 + |u|) either way.
+__device__ __forceinline__ void dswiglu(float dh, float g, float u, float& dg, float& du) {
+    const float e = expf(fminf(-g, 80.f));
+    const float s = 1.f / (1.f + e);
+    du = dh * (g * s);
+    dg = dh * u * (s * fmaf(g, e * s, 1.f));
+}
+
 // Forms for the tensor-core epilogue, whose outputs are rounded to bf16
 // (relative step 2^-8). They cut the epilogue's instruction count, which
 // matters because the epilogue warps share issue slots with the TMA and MMA
@@ -91,6 +103,13 @@ __device__ __forceinline__ float act_grad_bf16(int act, float z) {
 
 __device__ __forceinline__ float silu_bf16(float z) {
     return __fdividef(z, 1.f + __expf(fminf(-z, 80.f)));
+}
+
+__device__ __forceinline__ void dswiglu_bf16(float dh, float g, float u, float& dg, float& du) {
+    const float e = __expf(fminf(-g, 80.f));
+    const float s = __fdividef(1.f, 1.f + e);
+    du = dh * (g * s);
+    dg = dh * u * (s * fmaf(g, e * s, 1.f));
 }
 
 __device__ __forceinline__ float bf2f(__nv_bfloat16 v) { return __bfloat162float(v); }

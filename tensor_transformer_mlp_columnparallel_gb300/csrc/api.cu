@@ -226,9 +226,11 @@ int64_t sk_units_bound(int64_t D, int64_t Fs, int T) {
     const int64_t b = ((D + 127) / 128) * ((Fs + 63) / 64);
     return (int64_t)T * (a > b ? a : b);
 }
-size_t sk_bytes(tpmlp_dtype dt, int64_t N, int64_t D, int64_t F, int T) {
+// The gated backward's dX walks two operand pairs: twice the units.
+size_t sk_bytes(tpmlp_op op, tpmlp_dtype dt, int64_t N, int64_t D, int64_t F, int T) {
     if (dt != TPMLP_BF16 || N < 1) return 0;
-    return sk_cnt_bytes(N, D, F / T, T) + sk_part_bytes_for(N, sk_units_bound(D, F / T, T));
+    const int64_t pairs = op == TPMLP_OP_SWIGLU_BACKWARD ? 2 : 1;
+    return sk_cnt_bytes(N, D, F / T, T) + sk_part_bytes_for(N, pairs * sk_units_bound(D, F / T, T));
 }
 
 struct SkArea {
@@ -241,9 +243,9 @@ struct SkArea {
 // The stream-K scratch at round256(base) bytes into the workspace, if the
 // caller's workspace is that large (see tpmlp_workspace_bytes_balanced).
 SkArea sk_area(void* ws, size_t ws_bytes, size_t base, tpmlp_dtype dt, int64_t N, int64_t D,
-               int64_t F, int T) {
+               int64_t F, int T, tpmlp_op op = TPMLP_OP_FORWARD) {
     SkArea a;
-    const size_t need = sk_bytes(dt, N, D, F, T);
+    const size_t need = sk_bytes(op, dt, N, D, F, T);
     const size_t off = round256(base);
     if (need == 0 || ws == nullptr || !aligned16(ws) || ws_bytes < off + need) return a;
     char* p = static_cast<char*>(ws) + off;
@@ -295,6 +297,7 @@ size_t tpmlp_workspace_bytes(tpmlp_op op, tpmlp_dtype dt, int64_t N, int64_t D, 
     const size_t part = mode == TPMLP_REDUCE_PARTIALS ? partials_bytes(N, D, T) : 0;
     if (op == TPMLP_OP_FORWARD) return part;
     if (op == TPMLP_OP_BACKWARD) return dz_bytes(dt, N, F / T, T) + part;
+    if (op == TPMLP_OP_SWIGLU_BACKWARD) return 2 * dz_bytes(dt, N, F / T, T) + part;
     return (size_t)-1;
 }
 
@@ -302,7 +305,7 @@ size_t tpmlp_workspace_bytes_balanced(tpmlp_op op, tpmlp_dtype dt, int64_t N, in
                                       int T, tpmlp_reduce_mode mode) {
     const size_t base = tpmlp_workspace_bytes(op, dt, N, D, F, T, mode);
     if (base == (size_t)-1) return base;
-    const size_t sk = sk_bytes(dt, N, D, F, T);
+    const size_t sk = sk_bytes(op, dt, N, D, F, T);
     return sk == 0 ? base : round256(base) + sk;
 }
 
@@ -630,6 +633,127 @@ tpmlp_status tpmlp_backward(tpmlp_dtype dt, int64_t N, int64_t D, int64_t F, int
     return TPMLP_OK;
 }
 
+tpmlp_status tpmlp_swiglu_backward(tpmlp_dtype dt, int64_t N, int64_t D, int64_t F, int T,
+                                   const void* X, const void* const* Wg, const void* const* Wu,
+                                   const void* const* Wd, const void* const* H,
+                                   const void* const* G, const void* const* U, const void* dY,
+                                   void* dX, void* const* dWg, void* const* dWu, void* const* dWd,
+                                   tpmlp_reduce_mode mode, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+    TPMLP_TRY(check_dims(dt, N, D, F, T, TPMLP_ACT_RELU));
+    if (mode != TPMLP_REDUCE_PARTIALS && mode != TPMLP_REDUCE_SPLITK) return TPMLP_ERR_ARG;
+    const bool bf = dt == TPMLP_BF16;
+    TPMLP_TRY(check_shards(reinterpret_cast<const void* const*>(dWg), T, bf));
+    TPMLP_TRY(check_shards(reinterpret_cast<const void* const*>(dWu), T, bf));
+    TPMLP_TRY(check_shards(reinterpret_cast<const void* const*>(dWd), T, bf));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int Fs = (int)(F / T);
+    const int f32 = bf ? 0 : 1;
+    const size_t esz = bf ? 2 : 4;
+    if (N == 0) {   // sums over an empty token set
+        const size_t bytes = (size_t)D * Fs * esz;
+        for (int r = 0; r < T; ++r)
+            if (cudaMemsetAsync(dWg[r], 0, bytes, s) != cudaSuccess ||
+                cudaMemsetAsync(dWu[r], 0, bytes, s) != cudaSuccess ||
+                cudaMemsetAsync(dWd[r], 0, bytes, s) != cudaSuccess)
+                return TPMLP_ERR_CUDA;
+        return TPMLP_OK;
+    }
+    TPMLP_TRY(check_ptr(X, bf));
+    TPMLP_TRY(check_ptr(dY, bf));
+    TPMLP_TRY(check_ptr(dX, bf));
+    TPMLP_TRY(check_shards(Wg, T, bf));
+    TPMLP_TRY(check_shards(Wu, T, bf));
+    TPMLP_TRY(check_shards(Wd, T, bf));
+    TPMLP_TRY(check_shards(H, T, bf));
+    TPMLP_TRY(check_shards(G, T, bf));
+    TPMLP_TRY(check_shards(U, T, bf));
+    const size_t need = tpmlp_workspace_bytes(TPMLP_OP_SWIGLU_BACKWARD, dt, N, D, F, T, mode);
+    if (workspace == nullptr || workspace_bytes < need) return TPMLP_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return TPMLP_ERR_ALIGN;
+    const SkArea sk =
+        sk_area(workspace, workspace_bytes, need, dt, N, D, F, T, TPMLP_OP_SWIGLU_BACKWARD);
+
+    const size_t d_stride = round256((size_t)N * Fs * esz);
+    void *dG[kMaxG], *dU[kMaxG];
+    for (int r = 0; r < T; ++r) {
+        dG[r] = static_cast<char*>(workspace) + r * d_stride;
+        dU[r] = static_cast<char*>(workspace) + (T + r) * d_stride;
+    }
+
+    // 1. dG^(r), dU^(r) from dH^(r) = dY Wd^(r)^T in the epilogue; B(k, n) =
+    //    Wd^(r)[n, k]: K-major
+    GemmProblem g1 = problem((int)N, Fs, (int)D, T, 0, D, 0, D, 0, "bwd_gated_gemm_dswiglu");
+    g1.epi.kind = EPI_DSWIGLU;
+    g1.epi.out_f32 = f32;
+    g1.epi.ldc = Fs;
+    g1.epi.ldaux = Fs;
+    for (int r = 0; r < T; ++r) {
+        g1.A[r] = dY;
+        g1.B[r] = Wd[r];
+        g1.epi.C[r] = dG[r];
+        g1.epi.C2[r] = dU[r];
+        g1.epi.aux[r] = const_cast<void*>(G[r]);
+        g1.epi.aux2[r] = const_cast<void*>(U[r]);
+    }
+    TPMLP_TRY(run_gemm(dt, g1, s, sk));
+
+    // 2. dWd^(r) = H^(r)^T dY: A(m, k) = H^(r)[k, m] (MN-major), B(k, n) = dY[k, n]
+    GemmProblem g2 = problem(Fs, (int)D, (int)N, T, 0, Fs, 1, D, 1, "bwd_gated_dwd_gemm");
+    g2.epi.kind = EPI_STORE;
+    g2.epi.out_f32 = f32;
+    g2.epi.ldc = D;
+    for (int r = 0; r < T; ++r) {
+        g2.A[r] = H[r];
+        g2.B[r] = dY;
+        g2.epi.C[r] = dWd[r];
+    }
+    TPMLP_TRY(run_gemm(dt, g2, s, sk));
+
+    // 3. dWg^(r) = X^T dG^(r), dWu^(r) = X^T dU^(r): A(m, k) = X[k, m] (MN-major)
+    for (int half = 0; half < 2; ++half) {
+        GemmProblem g3 = problem((int)D, Fs, (int)N, T, 0, D, 1, Fs, 1,
+                                 half ? "bwd_gated_dwu_gemm" : "bwd_gated_dwg_gemm");
+        g3.epi.kind = EPI_STORE;
+        g3.epi.out_f32 = f32;
+        g3.epi.ldc = Fs;
+        for (int r = 0; r < T; ++r) {
+            g3.A[r] = X;
+            g3.B[r] = half ? dU[r] : dG[r];
+            g3.epi.C[r] = half ? dWu[r] : dWg[r];
+        }
+        TPMLP_TRY(run_gemm(dt, g3, s, sk));
+    }
+
+    // 4. dX = sum_r dG^(r) Wg^(r)^T + dU^(r) Wu^(r)^T, the K loop over (r, pair, k)
+    const bool split = mode == TPMLP_REDUCE_SPLITK;
+    GemmProblem g4 = problem((int)N, (int)D, Fs, T, split ? 1 : 0, Fs, 0, Fs, 0,
+                             split ? "bwd_gated_dx_gemm_splitk" : "bwd_gated_dx_gemm_partials");
+    g4.chain = 1;
+    g4.epi.kind = EPI_STORE;
+    g4.epi.out_f32 = split ? f32 : 1;
+    g4.epi.ldc = D;
+    const size_t pstride = round256((size_t)N * D * 4);
+    const float* parts[kMaxG];
+    for (int r = 0; r < T; ++r) {
+        g4.A[r] = dG[r];
+        g4.B[r] = Wg[r];
+        g4.A2[r] = dU[r];
+        g4.B2[r] = Wu[r];
+        if (!split) {
+            float* pr = reinterpret_cast<float*>(static_cast<char*>(workspace) + 2 * T * d_stride +
+                                                 r * pstride);
+            g4.epi.C[r] = pr;
+            parts[r] = pr;
+        }
+    }
+    if (split) g4.epi.C[0] = dX;
+    TPMLP_TRY(run_gemm(dt, g4, s, sk));
+    if (!split)
+        TPMLP_TRY(run_block_reduce(f32, N, D, T, parts, nullptr, dX, s, "block_reduce_gated_dx"));
+    return TPMLP_OK;
+}
+
 tpmlp_status tpmlp_block_reduce(tpmlp_dtype dt, int64_t N, int64_t D, int T,
                                 const float* const* partials, const void* b2, void* Y,
                                 void* stream) {
@@ -693,6 +817,168 @@ tpmlp_status tpmlp_vocab_ce_backward(int64_t N, int64_t V, int T, const float* l
         return TPMLP_ERR_ARG;
     return run_vocab_ce_backward(N, V, logits, targets, loss_per_token, grad_scale, dlogits,
                                  static_cast<cudaStream_t>(stream));
+}
+
+// Sizes and pointers the row operators share: [N, V] logits of dt in rows of ld
+static tpmlp_status check_rows(tpmlp_dtype dt, int64_t N, int64_t V, int T, const void* logits,
+                               int64_t ld) {
+    if (dt != TPMLP_F32 && dt != TPMLP_BF16) return TPMLP_ERR_DTYPE;
+    if (N < 0) return TPMLP_ERR_ARG;
+    if (V <= 0 || T < 1 || T > TPMLP_MAX_SHARDS || V % T != 0 || ld < V) return TPMLP_ERR_SHAPE;
+    if (V > 0x7fffffffLL || N > 0x7fffffffLL || ld > (1LL << 40)) return TPMLP_ERR_SHAPE;
+    if (N > 0) {
+        if (logits == nullptr) return TPMLP_ERR_ARG;
+        if (reinterpret_cast<uintptr_t>(logits) % (dt == TPMLP_F32 ? 4 : 2) != 0)
+            return TPMLP_ERR_ALIGN;
+    }
+    return TPMLP_OK;
+}
+
+tpmlp_status tpmlp_vocab_logprobs(tpmlp_dtype dt, int64_t N, int64_t V, int T, int K,
+                                  const void* logits, int64_t ld, const int64_t* targets,
+                                  float* logprob, int32_t* rank, float* entropy, float* lse,
+                                  int32_t* top_ids, float* top_logprobs, void* stream) {
+    TPMLP_TRY(check_rows(dt, N, V, T, logits, ld));
+    if (K < 0 || K > TPMLP_MAX_TOP || K > V) return TPMLP_ERR_SHAPE;
+    if (N == 0) return TPMLP_OK;
+    if (targets == nullptr && (logprob != nullptr || rank != nullptr)) return TPMLP_ERR_ARG;
+    if (K > 0 && (top_ids == nullptr || top_logprobs == nullptr)) return TPMLP_ERR_ARG;
+    LogprobArgs a{};
+    a.logits = logits;
+    a.ld = ld;
+    a.N = N;
+    a.V = V;
+    a.K = K;
+    a.targets = targets;
+    a.logprob = logprob;
+    a.rank = rank;
+    a.entropy = entropy;
+    a.lse = lse;
+    a.top_ids = top_ids;
+    a.top_logprobs = top_logprobs;
+    return run_vocab_logprobs(dt == TPMLP_F32, a, static_cast<cudaStream_t>(stream));
+}
+
+// The checks of the three distillation calls, and their common arguments
+static tpmlp_status distill_args(tpmlp_dtype dt, int64_t N, int64_t V, int T, int K,
+                                 const void* logits, int64_t ld, const int32_t* teacher_ids,
+                                 const float* teacher_logits, float tau, DistillArgs& a) {
+    TPMLP_TRY(check_rows(dt, N, V, T, logits, ld));
+    if (K < 1 || K > TPMLP_MAX_TEACHER) return TPMLP_ERR_SHAPE;
+    if (!(tau > 0.f) || !(tau < 3.4e38f)) return TPMLP_ERR_ARG;
+    if (N > 0 && (teacher_ids == nullptr || teacher_logits == nullptr)) return TPMLP_ERR_ARG;
+    a = DistillArgs{};
+    a.logits = logits;
+    a.ld = ld;
+    a.N = N;
+    a.V = V;
+    a.K = K;
+    a.ids = teacher_ids;
+    a.teacher = teacher_logits;
+    a.tau = tau;
+    return TPMLP_OK;
+}
+
+static tpmlp_status distill_grad_args(tpmlp_dtype dt, const float* grad_tokens, float grad_scale,
+                                      void* dlogits, int64_t ldd, DistillArgs& a) {
+    if (ldd < a.V || ldd > (1LL << 40)) return TPMLP_ERR_SHAPE;
+    if (a.N > 0) {
+        if (dlogits == nullptr) return TPMLP_ERR_ARG;
+        if (reinterpret_cast<uintptr_t>(dlogits) % (dt == TPMLP_F32 ? 4 : 2) != 0)
+            return TPMLP_ERR_ALIGN;
+        if (dlogits == a.logits && ldd != a.ld) return TPMLP_ERR_ARG;   // in place: the same rows
+    }
+    a.grad_tokens = grad_tokens;
+    a.grad_scale = grad_scale;
+    a.dlogits = dlogits;
+    a.ldd = ldd;
+    return TPMLP_OK;
+}
+
+tpmlp_status tpmlp_vocab_distill(tpmlp_dtype dt, int64_t N, int64_t V, int T, int K,
+                                 const void* logits, int64_t ld, const int32_t* teacher_ids,
+                                 const float* teacher_logits, float tau, float* loss_per_token,
+                                 float* loss_mean, float* lse, void* stream) {
+    DistillArgs a;
+    TPMLP_TRY(distill_args(dt, N, V, T, K, logits, ld, teacher_ids, teacher_logits, tau, a));
+    if (N > 0 && loss_per_token == nullptr) return TPMLP_ERR_ARG;
+    a.loss = loss_per_token;
+    a.lse = lse;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    TPMLP_TRY(run_vocab_distill(dt == TPMLP_F32, a, s));
+    return loss_mean != nullptr ? run_mean(loss_per_token, N, loss_mean, s) : TPMLP_OK;
+}
+
+tpmlp_status tpmlp_vocab_distill_backward(tpmlp_dtype dt, int64_t N, int64_t V, int T, int K,
+                                          const void* logits, int64_t ld,
+                                          const int32_t* teacher_ids, const float* teacher_logits,
+                                          float tau, const float* lse, const float* grad_tokens,
+                                          float grad_scale, void* dlogits, int64_t ldd,
+                                          void* stream) {
+    DistillArgs a;
+    TPMLP_TRY(distill_args(dt, N, V, T, K, logits, ld, teacher_ids, teacher_logits, tau, a));
+    TPMLP_TRY(distill_grad_args(dt, grad_tokens, grad_scale, dlogits, ldd, a));
+    if (N > 0 && lse == nullptr) return TPMLP_ERR_ARG;
+    a.lse_in = lse;
+    return run_vocab_distill(dt == TPMLP_F32, a, static_cast<cudaStream_t>(stream));
+}
+
+tpmlp_status tpmlp_vocab_distill_with_grad(tpmlp_dtype dt, int64_t N, int64_t V, int T, int K,
+                                           const void* logits, int64_t ld,
+                                           const int32_t* teacher_ids, const float* teacher_logits,
+                                           float tau, float* loss_per_token, float* loss_mean,
+                                           float* lse, const float* grad_tokens, float grad_scale,
+                                           void* dlogits, int64_t ldd, void* stream) {
+    DistillArgs a;
+    TPMLP_TRY(distill_args(dt, N, V, T, K, logits, ld, teacher_ids, teacher_logits, tau, a));
+    TPMLP_TRY(distill_grad_args(dt, grad_tokens, grad_scale, dlogits, ldd, a));
+    if (N > 0 && loss_per_token == nullptr) return TPMLP_ERR_ARG;
+    a.loss = loss_per_token;
+    a.lse = lse;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    TPMLP_TRY(run_vocab_distill(dt == TPMLP_F32, a, s));
+    return loss_mean != nullptr ? run_mean(loss_per_token, N, loss_mean, s) : TPMLP_OK;
+}
+
+tpmlp_status tpmlp_vocab_embedding_scaled(tpmlp_dtype dt, int64_t N, int64_t V, int64_t Hd, int T,
+                                          const int64_t* ids, const void* const* table,
+                                          float scale, void* out, void* stream) {
+    if (dt != TPMLP_F32 && dt != TPMLP_BF16) return TPMLP_ERR_DTYPE;
+    if (N < 0) return TPMLP_ERR_ARG;
+    if (V <= 0 || Hd <= 0 || T < 1 || T > TPMLP_MAX_SHARDS || V % T != 0) return TPMLP_ERR_SHAPE;
+    if (N == 0) return TPMLP_OK;
+    if (ids == nullptr || out == nullptr || table == nullptr) return TPMLP_ERR_ARG;
+    for (int k = 0; k < T; ++k)
+        if (table[k] == nullptr) return TPMLP_ERR_ARG;
+    return run_vocab_embedding_scaled(dt == TPMLP_F32, N, V, Hd, T, ids, table, scale, out,
+                                      static_cast<cudaStream_t>(stream));
+}
+
+size_t tpmlp_vocab_embedding_backward_workspace_bytes(int64_t N, int64_t V, int64_t Hd) {
+    if (N < 0 || V <= 0 || Hd <= 0 || N > 0x7ffffffeLL || V > 0x7ffffffeLL || Hd > 0x7ffffffeLL)
+        return (size_t)-1;
+    return embedding_grad_bytes(N, V, Hd);
+}
+
+tpmlp_status tpmlp_vocab_embedding_backward(tpmlp_dtype dt, tpmlp_dtype grad_dt, int64_t N,
+                                            int64_t V, int64_t Hd, int T, const int64_t* ids,
+                                            const void* dout, float scale, int accumulate,
+                                            void* const* dtable, void* workspace,
+                                            size_t workspace_bytes, void* stream) {
+    if ((dt != TPMLP_F32 && dt != TPMLP_BF16) || (grad_dt != TPMLP_F32 && grad_dt != TPMLP_BF16))
+        return TPMLP_ERR_DTYPE;
+    if (N < 0) return TPMLP_ERR_ARG;
+    if (V <= 0 || Hd <= 0 || T < 1 || T > TPMLP_MAX_SHARDS || V % T != 0) return TPMLP_ERR_SHAPE;
+    const size_t need = tpmlp_vocab_embedding_backward_workspace_bytes(N, V, Hd);
+    if (need == (size_t)-1) return TPMLP_ERR_SHAPE;
+    if (dtable == nullptr || (N > 0 && (ids == nullptr || dout == nullptr))) return TPMLP_ERR_ARG;
+    for (int k = 0; k < T; ++k)
+        if (dtable[k] == nullptr) return TPMLP_ERR_ARG;
+    if (workspace == nullptr || workspace_bytes < need) return TPMLP_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return TPMLP_ERR_ALIGN;
+    return run_vocab_embedding_backward(dt == TPMLP_F32, grad_dt == TPMLP_F32, N, V, Hd, T, ids,
+                                        dout, scale, accumulate != 0, dtable, workspace,
+                                        static_cast<cudaStream_t>(stream));
 }
 
 tpmlp_status tpmlp_gemm_plan(int64_t M, int64_t N, int64_t K, int G, int fold, int dual,

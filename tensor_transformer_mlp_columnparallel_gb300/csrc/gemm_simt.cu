@@ -32,7 +32,9 @@ constexpr int MAX_KS = 8;   // CTAs of a K-split cluster (the portable cluster l
 struct SimtParams {
     const float* A[kMaxG];
     const float* B[kMaxG];
-    const float* B2[kMaxG];   // DUAL: the up projection
+    const float* B2[kMaxG];   // DUAL: the up projection; chain: the second pair's B
+    const float* A2[kMaxG];   // chain: the second pair's A
+    int chain;                // the K loop walks (A, B), then (A2, B2), per group
     int64_t lda, ldb;
     int M, N, K, G, fold;
     int ks;   // CTAs per tile (a cluster along z) sharing its K chunks
@@ -46,6 +48,13 @@ __device__ __forceinline__ void epi_scalar(const EpiArgs& e, int g, int m, int n
         v = act_fwd(e.act, v);
     } else if (e.kind == EPI_DACT) {
         v *= act_grad(e.act, static_cast<const float*>(e.aux[g])[(int64_t)m * e.ldaux + n]);
+    } else if (e.kind == EPI_DSWIGLU) {
+        const float gv = static_cast<const float*>(e.aux[g])[(int64_t)m * e.ldaux + n];
+        const float uv = static_cast<const float*>(e.aux2[g])[(int64_t)m * e.ldaux + n];
+        float dg, du;
+        dswiglu(v, gv, uv, dg, du);
+        static_cast<float*>(e.C2[g])[(int64_t)m * e.ldc + n] = du;
+        v = dg;
     }
     int cg = g;
     int64_t crow = m;
@@ -86,7 +95,8 @@ __global__ void __launch_bounds__(256) simt_gemm_kernel(const SimtParams p) {
     // The K loop (over (shard, k) when folded) walks chunks of TK; the global
     // loads of chunk c + 1 go to registers while chunk c is computed from
     // shared memory, so a CTA waits for memory once, not once per chunk.
-    const int ngroups = p.fold ? p.G : 1;
+    const int pairs = p.chain ? 2 : 1;
+    const int ngroups = (p.fold ? p.G : 1) * pairs;   // operand pairs of one output
     const int kchunks = (p.K + TK - 1) / TK;
     const int nchunks = ngroups * kchunks;
     // this CTA's chunks [c_lo, c_hi) (all of them unless K is split)
@@ -98,9 +108,10 @@ __global__ void __launch_bounds__(256) simt_gemm_kernel(const SimtParams p) {
     auto fetch = [&](int c) {
         const int gi = c / kchunks;
         const int k0 = (c - gi * kchunks) * TK;
-        const int g = p.fold ? gi : gz;
-        const float* A = p.A[g];
-        const float* B = p.B[g];
+        const int g = p.fold ? gi / pairs : gz;
+        const bool second = p.chain && (gi & 1);
+        const float* A = second ? p.A2[g] : p.A[g];
+        const float* B = second ? p.B2[g] : p.B[g];
         const float* B2 = p.B2[g];
 #pragma unroll
         for (int u = 0; u < PER; ++u) {
@@ -218,7 +229,9 @@ tpmlp_status run_gemm_simt(const GemmProblem& pr, cudaStream_t s) {
         kp.A[g] = static_cast<const float*>(pr.A[g]);
         kp.B[g] = static_cast<const float*>(pr.B[g]);
         kp.B2[g] = static_cast<const float*>(pr.B2[g]);
+        kp.A2[g] = static_cast<const float*>(pr.A2[g]);
     }
+    kp.chain = pr.chain;
     kp.lda = pr.lda;
     kp.ldb = pr.ldb;
     kp.M = pr.M;
@@ -236,7 +249,8 @@ tpmlp_status run_gemm_simt(const GemmProblem& pr, cudaStream_t s) {
     int ks = 1;
     if (!pr.dual) {
         const int64_t ctas = gx * (int64_t)gy * gz;
-        const int64_t nchunks = (int64_t)(pr.fold ? pr.G : 1) * ((pr.K + TK - 1) / TK);
+        const int64_t nchunks =
+            (int64_t)(pr.fold ? pr.G : 1) * (pr.chain ? 2 : 1) * ((pr.K + TK - 1) / TK);
         int64_t k = device_sm_count() / (ctas > 0 ? ctas : 1);
         if (k > MAX_KS) k = MAX_KS;
         if (k > nchunks) k = nchunks;

@@ -110,9 +110,10 @@ struct Cfg {
 struct TcParams {
     CUtensorMap tmA[kMaxG];
     CUtensorMap tmB[kMaxG];
-    CUtensorMap tmB2[kMaxG];   // dual: the second B (up projection)
+    CUtensorMap tmB2[kMaxG];   // dual: the second B (up projection); chain: the second pair's B
     CUtensorMap tmC[kMaxG];    // tma_out: the output of each group (box 32 x 32)
-    CUtensorMap tmAux[kMaxG];  // tma_out, EPI_ACT with Z saved: Z of each group
+    CUtensorMap tmAux[kMaxG];  // tma_out, EPI_ACT with Z saved: Z of each group;
+                               // chain (which has no auxiliary tensor): the second pair's A
     int M, N, K;
     int G, fold;
     int a_mn, b_mn;
@@ -121,6 +122,7 @@ struct TcParams {
     int num_tiles;
     int dual;         // tile = BN/2 outputs of A B (accumulator columns [0, BN/2)) and of
                       // A B2 (columns [BN/2, BN)); N counts outputs
+    int chain;        // the K loop of a group walks (tmA, tmB), then (tmAux, tmB2)
     int raster;       // tile order, see decode_tile
     int band;         // band width in tiles
     int ksplit;       // CTAs of a cluster sharing one tile's K range (single-CTA
@@ -371,6 +373,45 @@ __device__ __forceinline__ void pack_row_bf16(const float (&v)[32], uint4 (&w)[4
     }
 }
 
+// Gated-MLP backward epilogue of one thread: v = dH over 32 columns from col0
+// of row `row`; dG replaces v, dU goes to C2 (G and U read, all per thread).
+__device__ __forceinline__ void epilogue_dswiglu_thread(const EpiArgs& e, int g, int row, int col0,
+                                                        int M, int N, float (&v)[32]) {
+    if (row >= M) return;
+    const int64_t off = (int64_t)row * e.ldaux + col0;
+    const __nv_bfloat16* ga = static_cast<const __nv_bfloat16*>(e.aux[g]) + off;
+    const __nv_bfloat16* ua = static_cast<const __nv_bfloat16*>(e.aux2[g]) + off;
+    __nv_bfloat16* du = static_cast<__nv_bfloat16*>(e.C2[g]) + (int64_t)row * e.ldc + col0;
+    if (col0 + 32 <= N) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint4 gw = *(reinterpret_cast<const uint4*>(ga) + q);
+            const uint4 uw = *(reinterpret_cast<const uint4*>(ua) + q);
+            const uint32_t gs[4] = {gw.x, gw.y, gw.z, gw.w}, us[4] = {uw.x, uw.y, uw.z, uw.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const int j = q * 8 + 2 * h;
+                float g0, g1, u0, u1, d0, d1;
+                unpack_bf16x2(gs[h], g0, g1);
+                unpack_bf16x2(us[h], u0, u1);
+                dswiglu_bf16(v[j], g0, u0, v[j], d0);
+                dswiglu_bf16(v[j + 1], g1, u1, v[j + 1], d1);
+                o[h] = pack_bf16x2(d0, d1);
+            }
+            reinterpret_cast<uint4*>(du)[q] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (col0 + j < N) {
+                float d;
+                dswiglu_bf16(v[j], bf2f(ga[j]), bf2f(ua[j]), v[j], d);
+                du[j] = __float2bfloat16_rn(d);
+            }
+    }
+}
+
 // Per-thread global stores of one row chunk (the form without staging):
 // Z (bf16, EPI_ACT with aux) and C (bf16 or fp32; by row blocks for the
 // reduce-scatter).
@@ -578,7 +619,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
         for (int g = 0; g < p.G; ++g) {
             prefetch_tmap(&p.tmA[g]);
             prefetch_tmap(&p.tmB[g]);
-            if (p.dual) prefetch_tmap(&p.tmB2[g]);
+            if (p.dual || p.chain) prefetch_tmap(&p.tmB2[g]);
+            if (p.chain) prefetch_tmap(&p.tmAux[g]);
         }
     }
     if (warp == 1) {
@@ -603,7 +645,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
     if (warp != 0 || lane != 0) pdl_wait();
 
     const int kb_per_group = p.k_blocks;
-    const int kb_total = p.fold ? p.G * kb_per_group : kb_per_group;
+    const int pairs = p.chain ? 2 : 1;   // operand pairs a group's K loop walks
+    const int kb_total = (p.fold ? p.G * kb_per_group : kb_per_group) * pairs;
     // this CTA's k-blocks of each tile (all of them unless K is split)
     const int kb_lo = (int)((int64_t)kb_total * krank / ks);
     const int kb_hi = (int)((int64_t)kb_total * (krank + 1) / ks);
@@ -618,9 +661,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
             // even CTA's full barrier
             const uint32_t full0 = PAIR ? mapa_shared(bar(FULL), 0) : bar(FULL);
             const int k_group = kb_per_group * C::BK;   // K extent of one shard
-            // Loads of one k-block into stage st: the A and B boxes of shard gk
-            // at K offset k0, completing on the stage's full barrier.
+            // Loads of one k-block into stage st: the A and B boxes of operand
+            // pair gk (the shard; with chain, shard gk / 2 and its first or
+            // second pair) at K offset k0, completing on the stage's full barrier.
             auto issue = [&](int st, int gk, int k0, int am0, int bn0, int n0) {
+                const int gs = p.chain ? gk >> 1 : gk;
+                const bool second = p.chain && (gk & 1);
+                const CUtensorMap* mapA = second ? &p.tmAux[gs] : &p.tmA[gs];
+                const CUtensorMap* mapB = second ? &p.tmB2[gs] : &p.tmB[gs];
                 const uint32_t fb = full0 + 8u * (uint32_t)st;
                 const uint32_t a_dst = sA0 + st * C::A_BYTES;
                 const uint32_t b_dst = sB0 + st * C::B_BYTES;
@@ -639,13 +687,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
                 if (!p.a_mn) {
 #pragma unroll
                     for (int h = 0; h < C::BK / BKB; ++h)
-                        load(a_dst + h * C::A_SUB, &p.tmA[gk], k0 + h * BKB, am0);
+                        load(a_dst + h * C::A_SUB, mapA, k0 + h * BKB, am0);
                 } else if (p.a_3d) {
-                    load3(a_dst, &p.tmA[gk], 0, k0, am0 / BOX_MN);
+                    load3(a_dst, mapA, 0, k0, am0 / BOX_MN);
                 } else {
 #pragma unroll
                     for (int j = 0; j < BM / BOX_MN; ++j)
-                        load(a_dst + j * C::MN_BOX_BYTES, &p.tmA[gk], am0 + j * BOX_MN, k0);
+                        load(a_dst + j * C::MN_BOX_BYTES, mapA, am0 + j * BOX_MN, k0);
                 }
                 // `rows` B rows (N index) starting at n_start from map m into dst
                 auto load_b = [&](uint32_t dst, const CUtensorMap* m, int n_start, int rows) {
@@ -661,7 +709,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
                     }
                 };
                 if (!p.dual) {
-                    load_b(b_dst, &p.tmB[gk], bn0, C::B_ROWS);
+                    load_b(b_dst, mapB, bn0, C::B_ROWS);
                 } else if constexpr (PAIR) {
                     // the even CTA stages the gate rows, the odd CTA the up rows
                     load_b(b_dst, rank == 0 ? &p.tmB[gk] : &p.tmB2[gk], n0 / 2, BN / 2);
@@ -689,9 +737,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
                 // only, so the order is the producer's alone.
                 const bool down = (p.alt & 1) && !w.sk && ((w.t / w.step) & 1);
                 const int kb_first = down ? w.kb1 - 1 : w.kb0;
-                // shard of the first k-block and its K offset inside the shard
-                int gk = p.fold ? kb_first / kb_per_group : g;
-                int k0 = (p.fold ? kb_first - (kb_first / kb_per_group) * kb_per_group : kb_first) * C::BK;
+                // operand pair of the first k-block and its K offset inside the pair
+                const int q_first = kb_first / kb_per_group;
+                int gk = (p.fold ? 0 : g * pairs) + q_first;
+                int k0 = (kb_first - q_first * kb_per_group) * C::BK;
                 for (int kb = w.kb0; kb < w.kb1; ++kb) {
                     if (!wait_fast(bar(EMPTY + s), ph ^ 1u, abort_flag, p.err, p.timeout_ns, true)) {
                         ok = false;
@@ -904,6 +953,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
                 oset ^= 1u;
             } else {
                 if (z_out) store_z_thread(p.epi, g, row, col0, p.M, p.N, v);
+                if (p.epi.kind == EPI_DSWIGLU) epilogue_dswiglu_thread(p.epi, g, row, col0, p.M, p.N, v);
                 epilogue_act(p.epi, g, row, col0, p.M, p.N, v);
                 store_c_thread(p.epi, g, row, col0, p.M, p.N, v);
             }
@@ -1230,6 +1280,9 @@ bool make_map_mn_chunks(CUtensorMap* m, const void* base, int64_t mn, int64_t k,
     return r == CUDA_SUCCESS;
 }
 
+// Operand pairs the K loop of one output walks
+int k_groups(const GemmProblem& pr) { return (pr.fold ? pr.G : 1) * (pr.chain ? 2 : 1); }
+
 // Co-resident CTAs (cl = 1) or clusters of cl CTAs of one kernel instance on
 // the current device; 0 when the queries fail. Cached per device and cl.
 template <int BN, bool PAIR>
@@ -1348,11 +1401,14 @@ tpmlp_status launch(const GemmProblem& pr, cudaStream_t s, int ks = 1) {
     const int b_rows = pr.dual ? BN / 2 : C::B_ROWS;
     kp.a_3d = pr.a_mn && pr.M % BOX_MN == 0;
     kp.b_3d = pr.b_mn && pr.N % BOX_MN == 0;
-    for (int g = 0; g < G && kp.a_3d; ++g)
+    for (int g = 0; g < G && kp.a_3d; ++g) {
         kp.a_3d = make_map_mn_chunks(&kp.tmA[g], pr.A[g], pr.M, pr.K, pr.lda, BM, C::BK);
+        if (kp.a_3d && pr.chain)
+            kp.a_3d = make_map_mn_chunks(&kp.tmAux[g], pr.A2[g], pr.M, pr.K, pr.lda, BM, C::BK);
+    }
     for (int g = 0; g < G && kp.b_3d; ++g) {
         kp.b_3d = make_map_mn_chunks(&kp.tmB[g], pr.B[g], pr.N, pr.K, pr.ldb, b_rows, C::BK);
-        if (kp.b_3d && pr.dual)
+        if (kp.b_3d && (pr.dual || pr.chain))
             kp.b_3d = make_map_mn_chunks(&kp.tmB2[g], pr.B2[g], pr.N, pr.K, pr.ldb, b_rows, C::BK);
     }
     for (int g = 0; g < G; ++g) {
@@ -1361,7 +1417,13 @@ tpmlp_status launch(const GemmProblem& pr, cudaStream_t s, int ks = 1) {
             ok = make_map(&kp.tmA[g], pr.A[g], pr.K, pr.M, pr.lda, BKB, BM);
         else if (!kp.a_3d)
             ok = make_map(&kp.tmA[g], pr.A[g], pr.M, pr.K, pr.lda, BOX_MN, C::BK);
-        for (int d = 0; d < (pr.dual ? 2 : 1); ++d) {
+        if (pr.chain) {
+            if (!pr.a_mn)
+                ok = ok && make_map(&kp.tmAux[g], pr.A2[g], pr.K, pr.M, pr.lda, BKB, BM);
+            else if (!kp.a_3d)
+                ok = ok && make_map(&kp.tmAux[g], pr.A2[g], pr.M, pr.K, pr.lda, BOX_MN, C::BK);
+        }
+        for (int d = 0; d < (pr.dual || pr.chain ? 2 : 1); ++d) {
             CUtensorMap* m = d == 0 ? &kp.tmB[g] : &kp.tmB2[g];
             const void* b = d == 0 ? pr.B[g] : pr.B2[g];
             if (!pr.b_mn)
@@ -1381,6 +1443,7 @@ tpmlp_status launch(const GemmProblem& pr, cudaStream_t s, int ks = 1) {
     kp.m_tiles = (pr.M + C::TILE_M - 1) / C::TILE_M;
     kp.dual = pr.dual;
     kp.n_tiles = pr.dual ? (pr.N + BN / 2 - 1) / (BN / 2) : (pr.N + BN - 1) / BN;
+    kp.chain = pr.chain;
     kp.k_blocks = (pr.K + C::BK - 1) / C::BK;
     kp.num_tiles = (pr.fold ? 1 : G) * kp.m_tiles * kp.n_tiles;
     {
@@ -1399,12 +1462,12 @@ tpmlp_status launch(const GemmProblem& pr, cudaStream_t s, int ks = 1) {
     if (sk) ks = 1;
     kp.ksplit = ks;
     if (ks > 1 && (PAIR || pr.dual || pr.M > KSPLIT_ROWS || ks > C::MAX_KSPLIT || ks > 8 ||
-                   ks > (pr.fold ? G : 1) * kp.k_blocks))
+                   ks > k_groups(pr) * kp.k_blocks))
         return TPMLP_ERR_SHAPE;
     int sk_grid = 0;
     size_t sk_cnt_bytes = 0;
     if (sk) {
-        const SkShape sh = sk_shape<BN, PAIR>(pr, kp.num_tiles, (int64_t)(pr.fold ? G : 1) * kp.k_blocks);
+        const SkShape sh = sk_shape<BN, PAIR>(pr, kp.num_tiles, (int64_t)k_groups(pr) * kp.k_blocks);
         if (!sh.ok) return TPMLP_ERR_SHAPE;
         sk_grid = sh.units;
         kp.sk = 1;
@@ -1424,7 +1487,8 @@ tpmlp_status launch(const GemmProblem& pr, cudaStream_t s, int ks = 1) {
     // configuration has room for the staging and every output has a map (not
     // the gated epilogue, nor the reduce-scatter's row blocks)
     kp.tma_out = 0;
-    if (C::TMA_OUT && !pr.dual && pr.epi.kind != EPI_SWIGLU && pr.epi.row_shard == 0) {
+    if (C::TMA_OUT && !pr.dual && pr.epi.kind != EPI_SWIGLU && pr.epi.kind != EPI_DSWIGLU &&
+        pr.epi.row_shard == 0) {
         bool ok = true;
         for (int g = 0; g < (pr.fold ? 1 : G) && ok; ++g) {
             ok = make_map_out(&kp.tmC[g], pr.epi.C[g], pr.N, pr.M, pr.epi.ldc, pr.epi.out_f32 != 0);
@@ -1525,7 +1589,7 @@ Plan choose_plan(const GemmProblem& pr) {
                           {192, false, 3, 0.95}, {192, false, 4, 0.95}};
     const int ncand = (int)(sizeof(cands) / sizeof(cands[0]));
     const int groups = pr.fold ? 1 : pr.G;
-    const int64_t kb_total = (int64_t)(pr.fold ? pr.G : 1) * ((pr.K + BKB - 1) / BKB);
+    const int64_t kb_total = (int64_t)k_groups(pr) * ((pr.K + BKB - 1) / BKB);
     constexpr double kHbm = 6.6e12;     // B/s
     constexpr double kSkEff = 0.87;
     constexpr double kStart = 5e-6;     // s: launch, set-up and pipeline fill
@@ -1554,8 +1618,8 @@ Plan choose_plan(const GemmProblem& pr) {
         double cost;
         if (c.ks == 0) {
             // the candidate's own k-block depth (128 for a pair, else 64)
-            const int64_t kbt = c.pair ? (int64_t)(pr.fold ? pr.G : 1) * ((pr.K + 2 * BKB - 1) / (2 * BKB))
-                                       : kb_total;
+            const int64_t kbt =
+                c.pair ? (int64_t)k_groups(pr) * ((pr.K + 2 * BKB - 1) / (2 * BKB)) : kb_total;
             const SkShape sh = c.pair ? sk_shape<256, true>(pr, tiles, kbt)
                                : c.bn == 128 ? sk_shape<128, false>(pr, tiles, kbt)
                                : c.bn == 192 ? sk_shape<192, false>(pr, tiles, kbt)

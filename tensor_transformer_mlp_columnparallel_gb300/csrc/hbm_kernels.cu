@@ -887,6 +887,14 @@ tpmlp_status run_vocab_ce(int64_t N, int64_t V, int T, const float* logits,
     return cudaGetLastError() == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
 }
 
+tpmlp_status run_mean(const float* loss, int64_t N, float* out, cudaStream_t s) {
+    {
+        LaunchScope ls("loss_mean", s);
+        mean_kernel<<<1, 1024, 0, s>>>(loss, N, out);
+    }
+    return cudaGetLastError() == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
+}
+
 tpmlp_status run_vocab_ce_backward(int64_t N, int64_t V, const float* logits,
                                    const int64_t* targets, const float* loss, float grad_scale,
                                    float* dlogits, cudaStream_t s) {

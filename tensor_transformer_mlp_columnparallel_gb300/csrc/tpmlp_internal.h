@@ -17,7 +17,9 @@ constexpr int kMaxG = TPMLP_MAX_SHARDS;
 //   EPI_DACT:  C = v * act'(aux[m, n])
 //   EPI_SWIGLU (dual GEMMs): g, u = the two accumulators at (m, n);
 //              aux = g, aux2 = u (each if not NULL); C = SiLU(g) * u
-enum EpiKind { EPI_STORE = 0, EPI_ACT = 1, EPI_DACT = 2, EPI_SWIGLU = 3 };
+//   EPI_DSWIGLU: g = aux[m, n], u = aux2[m, n], s = sigmoid(g);
+//              C = v u s (1 + g (1 - s)) (dG), C2 = v g s (dU)
+enum EpiKind { EPI_STORE = 0, EPI_ACT = 1, EPI_DACT = 2, EPI_SWIGLU = 3, EPI_DSWIGLU = 4 };
 
 struct EpiArgs {
     int kind;
@@ -28,7 +30,8 @@ struct EpiArgs {
     void* C[kMaxG];            // per group (FOLD: group 0 only)
     const void* bias[kMaxG];   // per output column, compute element type; NULL: none
     void* aux[kMaxG];          // Z (compute element type), see EpiKind
-    void* aux2[kMaxG];         // U of EPI_SWIGLU
+    void* aux2[kMaxG];         // U of EPI_SWIGLU and EPI_DSWIGLU
+    void* C2[kMaxG];           // dU of EPI_DSWIGLU, row pitch ldc
     // > 0: C is split by rows into blocks of row_shard rows, block i at C[i]
     // (the reduce-scatter output of the block end); 0: C[g] as above
     int64_t row_shard;
@@ -55,6 +58,11 @@ struct GemmProblem {
     // A B and A B2, for the gated MLP's gate and up projections
     int dual;
     const void* B2[kMaxG];
+    // chain = 1: the K loop of each group runs over two operand pairs, A B
+    // and then A2 B2 (same layouts), into one accumulator: the gated MLP's
+    // dX. With fold the order is (g, pair, k). Not with dual.
+    int chain;
+    const void* A2[kMaxG];
     EpiArgs epi;
     const char* name;          // kernel kind, for the timing records
     // Scratch for work-balanced few-token GEMMs (stream-K, M <= 64): partial
@@ -102,6 +110,53 @@ tpmlp_status run_vocab_ce(int64_t N, int64_t V, int T, const float* logits,
 tpmlp_status run_vocab_ce_backward(int64_t N, int64_t V, const float* logits,
                                    const int64_t* targets, const float* loss, float grad_scale,
                                    float* dlogits, cudaStream_t s);
+// mean of loss[0..N), fixed order (NaN for N = 0)
+tpmlp_status run_mean(const float* loss, int64_t N, float* out, cudaStream_t s);
+
+// Token log probabilities, rank, entropy, lse and the K most likely tokens.
+struct LogprobArgs {
+    const void* logits;
+    int64_t ld, N, V;
+    int K;
+    const int64_t* targets;    // NULL: no logprob, no rank
+    float* logprob;
+    int32_t* rank;
+    float* entropy;
+    float* lse;
+    int32_t* top_ids;
+    float* top_logprobs;
+};
+tpmlp_status run_vocab_logprobs(int f32, const LogprobArgs& a, cudaStream_t s);
+
+// Distillation from a teacher's top tokens; what is NULL is not computed:
+// loss (with lse) is the forward, dlogits the gradient. The gradient alone
+// reads the forward's lse_in.
+struct DistillArgs {
+    const void* logits;
+    int64_t ld, N, V;
+    int K;
+    const int32_t* ids;
+    const float* teacher;
+    float tau;
+    float* loss;
+    float* lse;
+    const float* lse_in;
+    const float* grad_tokens;
+    float grad_scale;
+    void* dlogits;
+    int64_t ldd;
+};
+tpmlp_status run_vocab_distill(int f32, const DistillArgs& a, cudaStream_t s);
+
+tpmlp_status run_vocab_embedding_scaled(int f32, int64_t N, int64_t V, int64_t H, int T,
+                                        const int64_t* ids, const void* const* table, float scale,
+                                        void* out, cudaStream_t s);
+// Table gradient by sorted tokens (workspace laid out by embedding_grad_bytes).
+size_t embedding_grad_bytes(int64_t N, int64_t V, int64_t H);
+tpmlp_status run_vocab_embedding_backward(int f32, int grad_f32, int64_t N, int64_t V, int64_t H,
+                                          int T, const int64_t* ids, const void* dout, float scale,
+                                          int accumulate, void* const* dtable, void* workspace,
+                                          cudaStream_t s);
 tpmlp_status run_selftest_wait(uint64_t timeout_ns, cudaStream_t s);
 
 // ---- services of the API translation unit --------------------------------
