@@ -825,7 +825,7 @@ static tpmlp_status check_rows(tpmlp_dtype dt, int64_t N, int64_t V, int T, cons
     if (dt != TPMLP_F32 && dt != TPMLP_BF16) return TPMLP_ERR_DTYPE;
     if (N < 0) return TPMLP_ERR_ARG;
     if (V <= 0 || T < 1 || T > TPMLP_MAX_SHARDS || V % T != 0 || ld < V) return TPMLP_ERR_SHAPE;
-    if (V > 0x7fffffffLL || N > 0x7fffffffLL || ld > (1LL << 40)) return TPMLP_ERR_SHAPE;
+    if (V > 0x7fffff00LL || N > 0x7fffffffLL || ld > (1LL << 40)) return TPMLP_ERR_SHAPE;
     if (N > 0) {
         if (logits == nullptr) return TPMLP_ERR_ARG;
         if (reinterpret_cast<uintptr_t>(logits) % (dt == TPMLP_F32 ? 4 : 2) != 0)

@@ -5,6 +5,15 @@
 //   with e = exp(z - m), and the K largest logits.
 // vocab_distill: q = softmax of the teacher's slots over tau, p = softmax(z / tau),
 //   loss = tau^2 sum q (ln q - ln p), dz = w (p - q) with w = g tau.
+//
+// Both read a row once. A row belongs to a cluster of 1, 2, 4 or 8 CTAs, each
+// taking a contiguous slice in 16-byte vectors; a thread keeps VPT vectors in
+// registers at a time (32 KB a CTA in flight), so the maximum of what it
+// holds is known before the first exponential. Exponentials are 2^((z - m) c)
+// with c = log2(e) / tau and m the running maximum, so the largest token's is
+// exactly 1 and a certain token's log probability exactly 0. m starts at the
+// lowest finite number: no finite logit is below it, and a thread that has
+// seen only masked tokens (-inf) meets no inf - inf.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -17,6 +26,13 @@ namespace tpmlp {
 namespace {
 
 constexpr int ROW_THREADS = 256;
+constexpr int ROW_WARPS = ROW_THREADS / 32;
+constexpr int VPT = 8;                        // 16-byte vectors a thread holds
+constexpr int CHUNK = ROW_THREADS * VPT;      // vectors a CTA holds
+constexpr int MAX_SPLIT = 8;                  // CTAs of a row (the portable cluster size)
+constexpr float kLowest = -3.402823466e38f;   // FLT_MAX's negative
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 template <typename T> __device__ __forceinline__ float to_f32(T v);
 template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
@@ -34,24 +50,309 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Two fp32 values in a 64-bit register pair: one issue slot for two results.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split(F2 x, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
+// A 16-byte vector of logits: its pairs as fp32, its largest element, how many
+// elements beat a given one.
+template <typename T> struct Vec;
+
+template <> struct Vec<__nv_bfloat16> {
+    static constexpr int N = 8, PAIRS = 4;
+    static constexpr uint32_t MASKED = 0xff80ff80u;   // a pair of -inf
+    static __device__ __forceinline__ float lowest() { return __uint_as_float(0xff7f0000u); }
+    using Wide = __nv_bfloat162;                       // packed running maximum or count
+    static __device__ __forceinline__ uint32_t word(const uint4& x, int k) {
+        return k == 0 ? x.x : k == 1 ? x.y : k == 2 ? x.z : x.w;
+    }
+    static __device__ __forceinline__ Wide as2(uint32_t w) { return *reinterpret_cast<Wide*>(&w); }
+    static __device__ __forceinline__ F2 pair(const uint4& x, int k) {
+        const uint32_t w = word(x, k);
+        return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    // pairs no lower than the lowest finite value, so that e (z - m) is 0 for masked tokens
+    static __device__ __forceinline__ F2 pair_floor(const uint4& x, int k) {
+        const Wide m = __hmax2_nan(as2(word(x, k)), as2(0xff7fff7fu));
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(&m);
+        return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    static __device__ __forceinline__ float elem(const uint4& x, int j) {
+        const uint32_t w = word(x, j >> 1);
+        return __uint_as_float((j & 1) ? (w & 0xffff0000u) : (w << 16));
+    }
+    template <int R> static __device__ __forceinline__ float largest(const uint4 (&x)[R]) {
+        Wide m = __hmax2_nan(__hmax2_nan(as2(x[0].x), as2(x[0].y)), __hmax2_nan(as2(x[0].z), as2(x[0].w)));
+#pragma unroll
+        for (int r = 1; r < R; ++r)
+            m = __hmax2_nan(m, __hmax2_nan(__hmax2_nan(as2(x[r].x), as2(x[r].y)),
+                                           __hmax2_nan(as2(x[r].z), as2(x[r].w))));
+        return max_nan(__low2float(m), __high2float(m));
+    }
+    // packed counts: whole numbers up to 256 are exact in bf16
+    struct Count {
+        Wide c;
+        __device__ __forceinline__ Count() : c(__float2bfloat162_rn(0.f)) {}
+        __device__ __forceinline__ void gt(const uint4& x, Wide t) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) c = __hadd2(c, __hgt2(as2(word(x, k)), t));
+        }
+        __device__ __forceinline__ void ge(const uint4& x, Wide t) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) c = __hadd2(c, __hge2(as2(word(x, k)), t));
+        }
+        __device__ __forceinline__ int total() const { return (int)(__low2float(c) + __high2float(c)); }
+    };
+    static __device__ __forceinline__ Wide wide(float z) { return __float2bfloat162_rn(z); }
+    static __device__ __forceinline__ uint4 pack(const float (&v)[8]) {
+        return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                          pack_bf16x2(v[6], v[7]));
+    }
+    static __device__ __forceinline__ void set(uint4& x, int j, __nv_bfloat16 v) {
+        reinterpret_cast<__nv_bfloat16*>(&x)[j] = v;
+    }
+};
+
+template <> struct Vec<float> {
+    static constexpr int N = 4, PAIRS = 2;
+    static constexpr uint32_t MASKED = 0xff800000u;
+    static __device__ __forceinline__ float lowest() { return kLowest; }
+    using Wide = float;
+    static __device__ __forceinline__ F2 pair(const uint4& x, int k) {
+        return k == 0 ? f2(__uint_as_float(x.x), __uint_as_float(x.y))
+                      : f2(__uint_as_float(x.z), __uint_as_float(x.w));
+    }
+    static __device__ __forceinline__ F2 pair_floor(const uint4& x, int k) {
+        return k == 0 ? f2(max_nan(__uint_as_float(x.x), kLowest), max_nan(__uint_as_float(x.y), kLowest))
+                      : f2(max_nan(__uint_as_float(x.z), kLowest), max_nan(__uint_as_float(x.w), kLowest));
+    }
+    static __device__ __forceinline__ float elem(const uint4& x, int j) {
+        return __uint_as_float(j == 0 ? x.x : j == 1 ? x.y : j == 2 ? x.z : x.w);
+    }
+    template <int R> static __device__ __forceinline__ float largest(const uint4 (&x)[R]) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            m = max_nan(m, max_nan(max_nan(elem(x[r], 0), elem(x[r], 1)), max_nan(elem(x[r], 2), elem(x[r], 3))));
+        return m;
+    }
+    struct Count {
+        int c;
+        __device__ __forceinline__ Count() : c(0) {}
+        __device__ __forceinline__ void gt(const uint4& x, float t) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c += elem(x, j) > t;
+        }
+        __device__ __forceinline__ void ge(const uint4& x, float t) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c += elem(x, j) >= t;
+        }
+        __device__ __forceinline__ int total() const { return c; }
+    };
+    static __device__ __forceinline__ Wide wide(float z) { return z; }
+    static __device__ __forceinline__ uint4 pack(const float (&v)[4]) {
+        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                          __float_as_uint(v[3]));
+    }
+    static __device__ __forceinline__ void set(uint4& x, int j, float v) {
+        reinterpret_cast<float*>(&x)[j] = v;
+    }
+};
+
+// A row in 16-byte vectors. Vector i holds elements head + i N ... + N - 1;
+// vector -1 is the part before the first 16-byte boundary, vector `full` the
+// part after the last whole one; elements outside the row read as -inf. The
+// cluster's CTA `rank` owns vectors [lo, hi).
+template <typename T>
+struct Row {
+    using V4 = Vec<T>;
+    const T* z;
+    int head, full, len;
+    int lo, hi;
+    __device__ __forceinline__ Row(const void* base, int64_t row, int64_t ld, int64_t V, int rank, int split) {
+        z = static_cast<const T*>(base) + row * ld;
+        len = (int)V;
+        const int off = (int)((16 - (reinterpret_cast<uintptr_t>(z) & 15)) & 15) / (int)sizeof(T);
+        head = off < len ? off : len;
+        full = (len - head) / V4::N;
+        const int first = head > 0 ? -1 : 0;
+        const int last = full + ((len - head) % V4::N != 0 ? 1 : 0);
+        const int64_t n = last - first;
+        lo = first + (int)(n * rank / split);
+        hi = first + (int)(n * (rank + 1) / split);
+    }
+    __device__ __forceinline__ int start(int i) const { return head + i * V4::N; }
+    __device__ __forceinline__ bool whole(int i) const { return i >= 0 && i < full; }
+    __device__ __forceinline__ int vector_of(int e) const { return (e - head + V4::N) / V4::N - 1; }
+    __device__ __forceinline__ bool mine(int e) const {
+        const int i = vector_of(e);
+        return i >= lo && i < hi;
+    }
+    __device__ __forceinline__ uint4 load(int i) const {
+        if (whole(i)) return __ldcs(reinterpret_cast<const uint4*>(z + start(i)));
+        uint4 x = make_uint4(V4::MASKED, V4::MASKED, V4::MASKED, V4::MASKED);
+        const int e0 = start(i);
+#pragma unroll
+        for (int j = 0; j < V4::N; ++j)
+            if (e0 + j >= 0 && e0 + j < len) V4::set(x, j, z[e0 + j]);
+        return x;
+    }
+    // the vectors lo + base + r ROW_THREADS + thread of this CTA (-inf beyond hi)
+    __device__ __forceinline__ void load_chunk(int base, uint4 (&x)[VPT]) const {
+#pragma unroll
+        for (int r = 0; r < VPT; ++r) {
+            const int i = lo + base + r * ROW_THREADS + (int)threadIdx.x;
+            x[r] = i < hi ? load(i) : make_uint4(V4::MASKED, V4::MASKED, V4::MASKED, V4::MASKED);
+        }
+    }
+};
+
+// sum of e = 2^((z - ref) c) and sum of e (z - ref)
+struct Soft {
+    float ref, s, e;
+};
+
+// The state relative to another reference, not below its own.
+__device__ __forceinline__ void rebase(Soft& a, float ref, float c) {
+    const float d = fmaxf(a.ref - ref, kLowest);   // finite: an empty state stays 0
+    const float f = a.ref == ref ? 1.f : ex2((a.ref - ref) * c);   // NaN with ref
+    a.e = f * fmaf(a.s, d, a.e);
+    a.s *= f;
+    a.ref = ref;
+}
+
+// One chunk in registers added to a thread's state; ENT: with the entropy's sum.
+template <typename T, bool ENT>
+__device__ __forceinline__ void soft_chunk(Soft& st, const uint4 (&x)[VPT], float largest, float c) {
+    const float ref = max_nan(st.ref, largest);
+    rebase(st, ref, c);
+    const F2 c2 = f2(c, c), r2 = f2(-ref, -ref);
+    F2 s0 = f2(0.f, 0.f), s1 = s0, e0 = s0, e1 = s0;
+#pragma unroll
+    for (int r = 0; r < VPT; ++r)
+#pragma unroll
+        for (int k = 0; k < Vec<T>::PAIRS; ++k) {
+            const F2 z = ENT ? Vec<T>::pair_floor(x[r], k) : Vec<T>::pair(x[r], k);
+            const F2 t = add2(z, r2);
+            float a, b;
+            split(mul2(t, c2), a, b);
+            const F2 p = f2(ex2(a), ex2(b));
+            if (k & 1) {
+                s1 = add2(s1, p);
+                if (ENT) e1 = fma2(p, t, e1);
+            } else {
+                s0 = add2(s0, p);
+                if (ENT) e0 = fma2(p, t, e0);
+            }
+        }
+    float a, b;
+    split(add2(s0, s1), a, b);
+    st.s += a + b;
+    if (ENT) {
+        split(add2(e0, e1), a, b);
+        st.e += a + b;
+    }
+}
+
+// What the CTAs of a row tell one another.
+struct __align__(16) Part {
+    Soft soft;
+    int before;   // entries in front of the target
+};
+
+__device__ __forceinline__ Part combine(const Part* parts, int n, float c) {
+    float m = parts[0].soft.ref;
+    for (int i = 1; i < n; ++i) m = max_nan(m, parts[i].soft.ref);
+    Part r{Soft{m, 0.f, 0.f}, 0};
+    for (int i = 0; i < n; ++i) {
+        Soft o = parts[i].soft;
+        rebase(o, m, c);
+        r.soft.s += o.s;
+        r.soft.e += o.e;
+        r.before += parts[i].before;
+    }
+    return r;
+}
+
+// The block's state from its threads' (fixed order), in every thread.
+__device__ __forceinline__ Part block_part(Soft st, int before, Part* red, float c) {
+    float m = st.ref;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
+    rebase(st, m, c);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        st.s += __shfl_xor_sync(0xffffffffu, st.s, off);
+        st.e += __shfl_xor_sync(0xffffffffu, st.e, off);
+        before += __shfl_xor_sync(0xffffffffu, before, off);
+    }
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = Part{st, before};
+    __syncthreads();
+    return combine(red, ROW_WARPS, c);
+}
+
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
+// `part` into slot `slot` of the array at `dst` in CTA `to` of the cluster
+__device__ __forceinline__ void send_part(Part* dst, int slot, uint32_t to, const Part& part) {
+    const uint32_t a = mapa_shared(smem_u32(dst + slot), to);
+    st_cluster_v4(a, part.soft.ref, part.soft.s, part.soft.e, __int_as_float(part.before));
+}
+
 // Whole-block reduction in a fixed order; every thread gets the result.
 template <typename T, typename Op>
-__device__ __forceinline__ T block_reduce(T v, Op op, T* red) {
+__device__ T block_reduce(T v, Op op, T* red) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, off));
     __syncthreads();   // red may hold an earlier reduction's values
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
     T r = red[0];
-    for (int w = 1; w < (int)(blockDim.x >> 5); ++w) r = op(r, red[w]);
+    for (int w = 1; w < ROW_WARPS; ++w) r = op(r, red[w]);
+    __syncthreads();
     return r;
 }
 
 struct Sum {
     template <typename T> __device__ T operator()(T a, T b) const { return a + b; }
-};
-struct MaxNan {
-    __device__ float operator()(float a, float b) const { return max_nan(a, b); }
 };
 struct MaxU64 {
     __device__ unsigned long long operator()(unsigned long long a, unsigned long long b) const {
@@ -59,161 +360,521 @@ struct MaxU64 {
     }
 };
 
-// One number per entry that falls with the logit, then rises with the index:
-// the list's order. (z + 0 turns -0 into +0.)
-__device__ __forceinline__ unsigned long long order_key(float z, uint32_t v) {
+// A row's distribution: ln p = (z - ref) / tau - ln s; nothing: no finite logit,
+// every ln p = -inf.
+struct Dist {
+    float ref, s, ln_s, c, inv_tau;
+    bool nothing;
+    __device__ __forceinline__ float exponent(float z) const { return (z - ref) * c; }
+    __device__ __forceinline__ float ln_p(float z) const {
+        return nothing ? -INFINITY : fmaf(z - ref, inv_tau, -ln_s);
+    }
+    __device__ __forceinline__ float lse() const {   // of z / tau
+        return nothing ? -INFINITY : fmaf(ref, inv_tau, ln_s);
+    }
+};
+
+__device__ __forceinline__ Dist distribution(const Soft& t, float c, float inv_tau) {
+    Dist d;
+    d.ref = t.ref;
+    d.s = t.s;
+    d.ln_s = logf(t.s);
+    d.c = c;
+    d.inv_tau = inv_tau;
+    d.nothing = t.s == 0.f;
+    return d;
+}
+
+// Entries with a probability in a row whose maximum is the lowest finite value
+// or -inf: they all hold that value.
+template <typename T>
+__device__ __noinline__ float count_finite(const T* z, int64_t V, float* red) {
+    float n = 0.f;
+    for (int64_t i = threadIdx.x; i < V; i += ROW_THREADS) n += to_f32(z[i]) != -INFINITY ? 1.f : 0.f;
+    return block_reduce(n, Sum(), red);
+}
+
+// sum e (z - ref) over a whole row a plain element at a time, for a row whose
+// (z - ref) overflows at a masked token (a maximum near the type's largest value)
+template <typename T>
+__device__ __noinline__ float slow_esum(const T* z, int64_t V, const Dist& d, float* red) {
+    float es = 0.f;
+    for (int64_t i = threadIdx.x; i < V; i += ROW_THREADS) {
+        const float x = to_f32(z[i]), p = ex2(d.exponent(x));
+        es += p == 0.f ? 0.f : p * (x - d.ref);
+    }
+    return block_reduce(es, Sum(), red);
+}
+
+// ------------------------------------------------------- top tokens ------
+
+constexpr int MAX_CAND = 1024;
+
+// An order of all floats (NaN with its sign bit clear on top); -0 = +0.
+__device__ __forceinline__ uint32_t order32(float z) {
     const uint32_t b = __float_as_uint(z + 0.f);
-    const uint32_t o = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t o) {
+    return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+}
+// One number per entry that falls with the logit, then rises with the index:
+// the list's order.
+__device__ __forceinline__ unsigned long long order_key(uint32_t o, uint32_t v) {
     return ((unsigned long long)o << 32) | (0xffffffffu - v);
 }
 
-// z - lse where lse = -inf (no finite logit) leaves nothing but -inf
-__device__ __forceinline__ float log_prob(float z, float m, float ln_s, float lse) {
-    return lse == -INFINITY ? -INFINITY : (z - m) - ln_s;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(ROW_THREADS) logprobs_kernel(const LogprobArgs a, int* err) {
-    __shared__ float red[ROW_THREADS / 32];
-    __shared__ int redi[ROW_THREADS / 32];
-    __shared__ unsigned long long redk[ROW_THREADS / 32];
-    const int64_t row = blockIdx.x;
-    const T* z = static_cast<const T*>(a.logits) + row * a.ld;
-    float m = -INFINITY;
-    for (int64_t i = threadIdx.x; i < a.V; i += ROW_THREADS) m = max_nan(m, to_f32(z[i]));
-    m = block_reduce(m, MaxNan(), red);
-    const float ms = m == -INFINITY ? 0.f : m;
-    const int64_t t = a.targets ? a.targets[row] : 0;
-    const bool good = t >= 0 && t < a.V;
-    const float zt = good ? to_f32(z[t]) : 0.f;
-    float s = 0.f, es = 0.f;
-    int before = 0;
-    for (int64_t i = threadIdx.x; i < a.V; i += ROW_THREADS) {
-        const float x = to_f32(z[i]);
-        const float d = x - ms, e = expf(d);
-        s += e;
-        es += e == 0.f ? 0.f : e * d;
-        before += x > zt || (x == zt && i < t);
-    }
-    s = block_reduce(s, Sum(), red);
-    es = block_reduce(es, Sum(), red);
-    before = block_reduce(before, Sum(), redi);
-    const float ln_s = logf(s), lse = ms + ln_s;
-    if (threadIdx.x == 0) {
-        if (a.targets && !good) atomicCAS(err, 0, (int)TPMLP_ERR_ARG);
-        if (a.lse) a.lse[row] = lse;
-        if (a.entropy) a.entropy[row] = s == 0.f ? 0.f : ln_s - es / s;
-        if (a.logprob) a.logprob[row] = good ? log_prob(zt, ms, ln_s, lse) : NAN;
-        if (a.rank) a.rank[row] = good ? before + 1 : 0;
-    }
-    unsigned long long last = ~0ull;
-    for (int k = 0; k < a.K; ++k) {
-        unsigned long long best = 0;
-        for (int64_t i = threadIdx.x; i < a.V; i += ROW_THREADS) {
-            const unsigned long long key = order_key(to_f32(z[i]), (uint32_t)i);
-            if (key < last && key > best) best = key;
-        }
-        last = block_reduce(best, MaxU64(), redk);
-        if (threadIdx.x == 0) {
-            const uint32_t v = 0xffffffffu - (uint32_t)last;
-            a.top_ids[row * a.K + k] = (int32_t)v;
-            a.top_logprobs[row * a.K + k] = log_prob(to_f32(z[v]), ms, ln_s, lse);
-        }
-    }
-}
-
-// The teacher's distribution of one row: slot k has q_k = exp(t_k / tau - tm) / sum.
-struct Teacher {
-    float tm, sum;
-    bool some;   // a slot with a probability
-    bool bad;    // an id outside [-1, V)
+struct TopShared {
+    unsigned long long cand[MAX_CAND];
+    unsigned long long list[TPMLP_MAX_TOP];                  // this CTA's first K, in order
+    unsigned long long all[MAX_SPLIT * TPMLP_MAX_TOP];       // the leader's copy of every CTA's list
+    unsigned long long red[ROW_WARPS];
+    uint32_t thr[ROW_WARPS];
+    int threads[ROW_THREADS];
+    int n_threads, n_cand;
 };
 
-__device__ __forceinline__ Teacher teacher_stats(const DistillArgs& a, int64_t row, float* red) {
-    const int32_t* ids = a.ids + row * a.K;
-    const float* tl = a.teacher + row * a.K;
-    float mx = -INFINITY, bad = 0.f;
-    for (int k = threadIdx.x; k < a.K; k += blockDim.x) {
-        const int id = ids[k];
-        if (id != -1) mx = max_nan(mx, tl[k] / a.tau);
-        if (id < -1 || id >= a.V) bad = 1.f;
+// The elements of vector i that are in the row and at least `thr` (strictly
+// above with `above`) join the candidates; beyond MAX_CAND they are only counted.
+template <typename T>
+__device__ __forceinline__ void offer(const Row<T>& row, int i, const uint4& x, uint32_t thr, bool above,
+                                      TopShared& sh) {
+    const int e0 = row.start(i);
+#pragma unroll
+    for (int j = 0; j < Vec<T>::N; ++j) {
+        const uint32_t o = order32(Vec<T>::elem(x, j));
+        if ((above ? o > thr : o >= thr) && e0 + j >= 0 && e0 + j < row.len) {
+            const int at = atomicAdd(&sh.n_cand, 1);
+            if (at < MAX_CAND) sh.cand[at] = order_key(o, (uint32_t)(e0 + j));
+        }
     }
-    Teacher r;
-    r.tm = block_reduce(mx, MaxNan(), red);
-    r.bad = block_reduce(bad, MaxNan(), red) != 0.f;
-    r.some = r.tm != -INFINITY;
+}
+
+// The slice's first K entries into sh.list (0: fewer than K entries).
+//
+// `raw` is the largest element the thread saw. With g = ceil(K / warps), the
+// g-th largest of a warp's 32 such maxima is reached by g different entries,
+// so the least of the warps' g-th maxima is reached by at least K entries:
+// only entries at or above it can be in the list. They sit with the few
+// threads whose maximum reaches it (some 2 K of 256 for K = 20), whose vectors
+// are still in registers (one chunk) or read again. Where more than MAX_CAND
+// entries reach the bound (a mask that leaves fewer than K tokens, rows of
+// equal values), the entries above it are taken alone and equal ones follow
+// by index; where even those are too many, K rounds over the slice.
+template <typename T>
+__device__ void slice_top(const Row<T>& row, int K, float raw, const uint4 (&x)[VPT], TopShared& sh) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t mine = order32(raw);
+    uint32_t left = mine, g_th = 0;
+    for (int g = 0; g < (K + ROW_WARPS - 1) / ROW_WARPS; ++g) {
+        g_th = __reduce_max_sync(0xffffffffu, left);
+        const uint32_t who = __ballot_sync(0xffffffffu, left == g_th);
+        if (lane == __ffs(who) - 1) left = 0u;
+    }
+    if (lane == 0) sh.thr[warp] = g_th;
+    if (threadIdx.x == 0) sh.n_threads = sh.n_cand = 0;
+    for (int k = threadIdx.x; k < K; k += ROW_THREADS) sh.list[k] = 0ull;
+    __syncthreads();
+    uint32_t thr = sh.thr[0];
+    for (int w = 1; w < ROW_WARPS; ++w) thr = min(thr, sh.thr[w]);
+    const int n = row.hi - row.lo;
+    const int per = (n + ROW_THREADS - 1) / ROW_THREADS;   // vectors of a thread
+    if (n <= CHUNK) {
+        if (mine >= thr) {
+#pragma unroll
+            for (int r = 0; r < VPT; ++r) {
+                const int i = row.lo + r * ROW_THREADS + (int)threadIdx.x;
+                if (i < row.hi) offer(row, i, x[r], thr, false, sh);
+            }
+        }
+    } else {
+        if (mine >= thr) sh.threads[atomicAdd(&sh.n_threads, 1)] = (int)threadIdx.x;
+        __syncthreads();
+        const int items = sh.n_threads * per;
+        for (int a = threadIdx.x; a < items; a += ROW_THREADS) {
+            const int i = row.lo + (a % per) * ROW_THREADS + sh.threads[a / per];
+            if (i < row.hi) offer(row, i, row.load(i), thr, false, sh);
+        }
+    }
+    __syncthreads();
+    int count = sh.n_cand;
+    if (count > MAX_CAND) {
+        __syncthreads();
+        if (threadIdx.x == 0) sh.n_cand = 0;
+        __syncthreads();
+        for (int i = row.lo + (int)threadIdx.x; i < row.hi; i += ROW_THREADS)
+            offer(row, i, row.load(i), thr, true, sh);
+        __syncthreads();
+        count = sh.n_cand;
+        if (count <= MAX_CAND - K) {
+            // entries equal to the bound, in index order, until there are K
+            const int e_lo = max(row.start(row.lo), 0), e_hi = min(row.start(row.hi), row.len);
+            for (int e = e_lo; e < e_hi && count < K; e += ROW_THREADS) {
+                const int at = e + (int)threadIdx.x;
+                const bool hit = at < e_hi && order32(to_f32(row.z[at])) == thr;
+                const uint32_t b = __ballot_sync(0xffffffffu, hit);
+                if (lane == 0) sh.thr[warp] = __popc(b);
+                __syncthreads();
+                int pos = count + __popc(b & ((1u << lane) - 1u));
+                for (int w = 0; w < warp; ++w) pos += (int)sh.thr[w];
+                for (int w = 0; w < ROW_WARPS; ++w) count += (int)sh.thr[w];
+                if (hit && pos < MAX_CAND) sh.cand[pos] = order_key(thr, (uint32_t)at);
+                __syncthreads();
+            }
+            count = min(count, MAX_CAND);
+        } else {
+            unsigned long long last = ~0ull;
+            for (int k = 0; k < K; ++k) {
+                unsigned long long best = 0ull;
+                for (int i = row.lo + (int)threadIdx.x; i < row.hi; i += ROW_THREADS) {
+                    const uint4 y = row.load(i);
+                    const int e0 = row.start(i);
+                    for (int j = 0; j < Vec<T>::N; ++j) {
+                        if (e0 + j < 0 || e0 + j >= row.len) continue;
+                        const unsigned long long key = order_key(order32(Vec<T>::elem(y, j)), (uint32_t)(e0 + j));
+                        if (key < last && key > best) best = key;
+                    }
+                }
+                last = block_reduce(best, MaxU64(), sh.red);
+                if (threadIdx.x == 0) sh.list[k] = last;
+                if (last == 0ull) break;
+            }
+            __syncthreads();
+            return;
+        }
+    }
+    for (int a = threadIdx.x; a < count; a += ROW_THREADS) {
+        const unsigned long long key = sh.cand[a];
+        int place = 0;
+        for (int b = 0; b < count; ++b) place += sh.cand[b] > key;
+        if (place < K) sh.list[place] = key;
+    }
+    __syncthreads();
+}
+
+// ---------------------------------------------------- log probabilities --
+
+template <typename T>
+__global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobArgs a, int split, int* err) {
+    __shared__ Part red[ROW_WARPS];
+    __shared__ Part parts[MAX_SPLIT];
+    __shared__ float redf[ROW_WARPS];
+    __shared__ TopShared sh;
+    const int64_t row_i = blockIdx.x / (unsigned)split;
+    const int rank = (int)(blockIdx.x - row_i * split);
+    if (split > 1) cluster_arrive();   // this CTA runs: its shared memory may be written
+    const Row<T> row(a.logits, row_i, a.ld, a.V, rank, split);
+    const int64_t t = a.targets ? a.targets[row_i] : -1;
+    const bool good = t >= 0 && t < a.V;
+    const float zt = good ? to_f32(row.z[t]) : INFINITY;
+    // entries in front of the target: above it anywhere, equal to it before it.
+    // Vectors before the target's count equals; inside its own vector they
+    // are added below. A masked target is counted apart.
+    const bool counted = good && zt > -INFINITY;
+    const int tvec = counted ? row.vector_of((int)t) : row.lo;
+    const auto zw = Vec<T>::wide(counted ? zt : INFINITY);
+
+    Soft st{Vec<T>::lowest(), 0.f, 0.f};
+    int before = 0;
+    float raw = -INFINITY;
+    uint4 x[VPT];
+    const int n = row.hi - row.lo;
+    for (int base = 0; base < n; base += CHUNK) {
+        row.load_chunk(base, x);
+        const float largest = Vec<T>::largest(x);
+        raw = max_nan(raw, largest);
+        soft_chunk<T, true>(st, x, largest, kLog2e);
+        typename Vec<T>::Count cnt;
+#pragma unroll
+        for (int r = 0; r < VPT; ++r) {
+            if (row.lo + base + r * ROW_THREADS + (int)threadIdx.x < tvec)
+                cnt.ge(x[r], zw);
+            else
+                cnt.gt(x[r], zw);
+        }
+        before += cnt.total();
+    }
+    if (counted && threadIdx.x == 0 && tvec >= row.lo && tvec < row.hi)
+        for (int e = max(row.start(tvec), 0); e < (int)t; ++e) before += to_f32(row.z[e]) == zt;
+    if (good && !counted) {   // -inf (or NaN) given: every other entry is compared
+        before = 0;
+        const int e_lo = max(row.start(row.lo), 0), e_hi = min(row.start(row.hi), row.len);
+        for (int e = e_lo + (int)threadIdx.x; e < e_hi; e += ROW_THREADS) {
+            const float v = to_f32(row.z[e]);
+            before += v > zt || (v == zt && e < (int)t);
+        }
+    }
+    Part part = block_part(st, before, red, kLog2e);
+    if (a.K > 0) slice_top(row, a.K, raw, x, sh);
+    if (split > 1) {
+        cluster_wait();
+        if (threadIdx.x == 0) send_part(parts, rank, 0u, part);
+        for (int k = threadIdx.x; k < a.K; k += ROW_THREADS)
+            st_cluster_u64(mapa_shared(smem_u32(&sh.all[rank * a.K + k]), 0u), sh.list[k]);
+        cluster_arrive();
+        cluster_wait();
+        if (rank != 0) return;
+        part = combine(parts, split, kLog2e);
+    }
+    // masked tokens were summed as the lowest finite value, which tells
+    // nothing only where the row has no larger one
+    if (part.soft.ref == Vec<T>::lowest()) {
+        part.soft.s = count_finite(row.z, a.V, redf);
+        part.soft.e = 0.f;
+    }
+    const Dist d = distribution(part.soft, kLog2e, 1.f);
+    float esum = part.soft.e;
+    if (isnan(esum) && !isnan(d.s)) esum = slow_esum(row.z, a.V, d, redf);
+    if (threadIdx.x == 0) {
+        if (a.targets && !good) atomicCAS(err, 0, (int)TPMLP_ERR_ARG);
+        if (a.lse) a.lse[row_i] = d.lse();
+        if (a.entropy) a.entropy[row_i] = d.nothing ? 0.f : d.ln_s - esum / d.s;
+        if (a.logprob) a.logprob[row_i] = good ? d.ln_p(zt) : NAN;
+        if (a.rank) a.rank[row_i] = good ? part.before + 1 : 0;
+    }
+    const unsigned long long* all = split > 1 ? sh.all : sh.list;
+    const int m = split * a.K;
+    for (int i = threadIdx.x; i < m; i += ROW_THREADS) {
+        const unsigned long long key = all[i];
+        int place = i;
+        if (split > 1) {
+            place = 0;
+            for (int j = 0; j < m; ++j) place += all[j] > key;
+        }
+        if (key != 0ull && place < a.K) {
+            a.top_ids[row_i * a.K + place] = (int32_t)(0xffffffffu - (uint32_t)key);
+            a.top_logprobs[row_i * a.K + place] = d.ln_p(order_value((uint32_t)(key >> 32)));
+        }
+    }
+}
+
+// --------------------------------------------------------- distillation --
+
+// The teacher's slots of one row that are this CTA's, and its distribution:
+// slot k has q_k = exp(t_k / tau - tm) / sum.
+struct TeacherShared {
+    int id[TPMLP_MAX_TEACHER];
+    float q[TPMLP_MAX_TEACHER];
+    float fix[TPMLP_MAX_TEACHER];   // the gradient at id
+    float tm, sum;
+    int some, bad, n;               // n: slots of this CTA
+};
+
+// Warp 0: statistics over the K slots, then the slots whose id is in the
+// CTA's slice, in slot order.
+template <typename T>
+__device__ void teacher_row(const DistillArgs& a, int64_t row_i, const Row<T>& row, bool lists, TeacherShared& sh) {
+    const int lane = threadIdx.x;
+    const int32_t* ids = a.ids + row_i * a.K;
+    const float* tl = a.teacher + row_i * a.K;
+    const float ct = kLog2e / a.tau;
+    float mx = -INFINITY;
+    int bad = 0;
+    for (int k = lane; k < a.K; k += 32) {
+        const int id = ids[k];
+        if (id != -1) mx = max_nan(mx, tl[k]);
+        bad |= id < -1 || id >= a.V;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    bad = __any_sync(0xffffffffu, bad);
+    const bool some = mx != -INFINITY;
     float s = 0.f;
-    if (r.some)
-        for (int k = threadIdx.x; k < a.K; k += blockDim.x)
-            if (ids[k] != -1) s += expf(tl[k] / a.tau - r.tm);
-    r.sum = block_reduce(s, Sum(), red);
-    return r;
+    if (some)
+        for (int k = lane; k < a.K; k += 32)
+            if (ids[k] != -1) s += ex2((tl[k] - mx) * ct);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    int n = 0;
+    if (lists && some && !bad)
+        for (int k0 = 0; k0 < a.K; k0 += 32) {
+            const int k = k0 + lane;
+            const int id = k < a.K ? ids[k] : -1;
+            const bool hit = id != -1 && row.mine(id);
+            const uint32_t b = __ballot_sync(0xffffffffu, hit);
+            if (hit) {
+                const int at = n + __popc(b & ((1u << lane) - 1u));
+                sh.id[at] = id;
+                sh.q[at] = ex2((tl[k] - mx) * ct) / s;
+            }
+            n += __popc(b);
+        }
+    if (lane == 0) {
+        sh.tm = mx;
+        sh.sum = s;
+        sh.some = some;
+        sh.bad = bad;
+        sh.n = n;
+    }
+}
+
+// LOSS: loss and lse; GRAD: the gradient (with LOSS from this launch's
+// statistics, else from the given lse).
+template <typename T, bool LOSS, bool GRAD>
+__global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillArgs a, int split, int* err) {
+    __shared__ Part red[ROW_WARPS];
+    __shared__ Part parts[MAX_SPLIT];
+    __shared__ float redf[ROW_WARPS];
+    __shared__ TeacherShared te;
+    const int64_t row_i = blockIdx.x / (unsigned)split;
+    const int rank = (int)(blockIdx.x - row_i * split);
+    if (LOSS && split > 1) cluster_arrive();
+    const Row<T> row(a.logits, row_i, a.ld, a.V, rank, split);
+    T* d = GRAD ? static_cast<T*>(a.dlogits) + row_i * a.ldd : nullptr;
+    if (threadIdx.x < 32) teacher_row(a, row_i, row, GRAD, te);
+    __syncthreads();
+    const bool dead = te.bad || !te.some;
+    const float c = kLog2e / a.tau;
+    const int n = row.hi - row.lo;
+    uint4 x[VPT];
+    Dist dist{};
+    if (LOSS) {
+        Soft st{kLowest, 0.f, 0.f};
+        if (!dead)
+            for (int base = 0; base < n; base += CHUNK) {
+                row.load_chunk(base, x);
+                soft_chunk<T, false>(st, x, Vec<T>::largest(x), c);
+            }
+        // the leader's loss: (ln q - ln p) needs the student's logits at the
+        // teacher's tokens, read before anything is written in place
+        constexpr int LPT = TPMLP_MAX_TEACHER / ROW_THREADS;
+        float zk[LPT];
+        if (rank == 0 && !dead) {
+#pragma unroll
+            for (int u = 0; u < LPT; ++u) {
+                const int k = threadIdx.x + u * ROW_THREADS;
+                const int id = k < a.K ? a.ids[row_i * a.K + k] : -1;
+                zk[u] = id != -1 ? to_f32(row.z[id]) : 0.f;
+            }
+        }
+        Part part = block_part(st, 0, red, c);
+        if (split > 1) {
+            cluster_wait();
+            if ((int)threadIdx.x < split) send_part(parts, rank, threadIdx.x, part);
+            cluster_arrive();
+            cluster_wait();
+            part = combine(parts, split, c);
+        }
+        dist = distribution(part.soft, c, 1.f / a.tau);
+        if (rank == 0) {
+            float loss = 0.f;
+            if (!dead) {
+                const float log2_sum = log2f(te.sum);
+#pragma unroll
+                for (int u = 0; u < LPT; ++u) {
+                    const int k = threadIdx.x + u * ROW_THREADS;
+                    if (k >= a.K || a.ids[row_i * a.K + k] == -1) continue;
+                    const float lq = (a.teacher[row_i * a.K + k] - te.tm) * c - log2_sum;
+                    const float q = ex2(lq);
+                    if (q != 0.f) loss += q * (kLn2 * lq - dist.ln_p(zk[u]));
+                }
+            }
+            loss = block_reduce(loss, Sum(), redf);
+            if (threadIdx.x == 0) {
+                if (te.bad) atomicCAS(err, 0, (int)TPMLP_ERR_ARG);
+                a.loss[row_i] = te.bad ? NAN : a.tau * a.tau * loss;
+                if (a.lse) a.lse[row_i] = te.bad ? NAN : dead ? 0.f : dist.lse();
+            }
+        }
+    } else {
+        if (te.bad && rank == 0 && threadIdx.x == 0) atomicCAS(err, 0, (int)TPMLP_ERR_ARG);
+        const float lse = a.lse_in[row_i];
+        dist.c = c;   // p = 2^((z - lse tau) c)
+        dist.nothing = lse == -INFINITY;
+        dist.ref = lse * a.tau;
+        dist.s = 1.f;
+    }
+    if (!GRAD) return;
+    const float w = te.bad ? NAN : a.grad_scale * (a.grad_tokens ? a.grad_tokens[row_i] : 1.f) * a.tau;
+    const float ws = w / dist.s;   // times 2^exponent: w p
+    const float fill = te.bad ? NAN : 0.f;
+    const bool flat = dead || dist.nothing;   // no probabilities: the gradient is `fill` and the teacher's part
+    auto grad = [&](float z) { return flat ? fill : ws * ex2(dist.exponent(z)); };
+    // the CTA's teacher tokens, from the logits as they are before the sweep;
+    // slots of one id all get the row's full value
+    for (int k = threadIdx.x; k < te.n; k += ROW_THREADS) {
+        const int id = te.id[k];
+        float q = 0.f;
+        for (int j = 0; j < te.n; ++j)
+            if (te.id[j] == id) q += te.q[j];
+        te.fix[k] = fmaf(-w, q, grad(to_f32(row.z[id])));
+    }
+    __syncthreads();
+    const bool kept = LOSS && !dead && n <= CHUNK;   // the slice is still in registers
+    const bool same = ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(row.z)) & 15) == 0;
+    for (int base = 0; base < n; base += CHUNK) {
+        if (!kept && !dead) row.load_chunk(base, x);
+#pragma unroll
+        for (int r = 0; r < VPT; ++r) {
+            const int i = row.lo + base + r * ROW_THREADS + (int)threadIdx.x;
+            if (i >= row.hi) break;
+            float v[Vec<T>::N];
+#pragma unroll
+            for (int j = 0; j < Vec<T>::N; ++j) v[j] = grad(Vec<T>::elem(x[r], j));
+            const int e0 = row.start(i);
+            if (same && row.whole(i)) {
+                __stcs(reinterpret_cast<uint4*>(d + e0), Vec<T>::pack(v));
+            } else {
+#pragma unroll
+                for (int j = 0; j < Vec<T>::N; ++j)
+                    if (e0 + j >= 0 && e0 + j < row.len) d[e0 + j] = from_f32<T>(v[j]);
+            }
+        }
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < te.n; k += ROW_THREADS) d[te.id[k]] = from_f32<T>(te.fix[k]);
+}
+
+// ---------------------------------------------------------------- launch --
+
+// CTAs per row. Few rows: enough CTAs to occupy the SMs twice over, while a
+// slice still has a vector for every thread. With `hold` the slice should
+// also fit the registers, so that the gradient needs no second read.
+int row_split(int64_t N, int64_t row_bytes, bool hold) {
+    const int64_t want = 4LL * device_sm_count();
+    if (N * MAX_SPLIT > 0x7fffffffLL) return 1;
+    int split = 1;
+    while (split < MAX_SPLIT && N * split < want && row_bytes / (2 * split) >= ROW_THREADS * 16) split *= 2;
+    if (hold && row_bytes + 32 <= (int64_t)MAX_SPLIT * CHUNK * 16)
+        while ((row_bytes + 32 + split - 1) / split > CHUNK * 16) split *= 2;
+    return split;
+}
+
+template <typename... P, typename... A>
+tpmlp_status launch_rows(void (*kernel)(P...), int64_t N, int split, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)(N * split));
+    cfg.blockDim = dim3(ROW_THREADS);
+    cfg.stream = s;
+    if (split > 1) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)split;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return TPMLP_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(ROW_THREADS) distill_kernel(const DistillArgs a, int* err) {
-    __shared__ float red[ROW_THREADS / 32];
-    __shared__ float fix[TPMLP_MAX_TEACHER];
-    const int64_t row = blockIdx.x;
-    const T* z = static_cast<const T*>(a.logits) + row * a.ld;
-    T* d = a.dlogits ? static_cast<T*>(a.dlogits) + row * a.ldd : nullptr;
-    const int32_t* ids = a.ids + row * a.K;
-    const float* tl = a.teacher + row * a.K;
-    const Teacher te = teacher_stats(a, row, red);
-    if (te.bad || !te.some) {
-        const float fill = te.bad ? NAN : 0.f;
-        if (threadIdx.x == 0) {
-            if (te.bad) atomicCAS(err, 0, (int)TPMLP_ERR_ARG);
-            if (a.loss) a.loss[row] = fill;
-            if (a.lse) a.lse[row] = fill;
-        }
-        if (d)
-            for (int64_t i = threadIdx.x; i < a.V; i += ROW_THREADS) d[i] = from_f32<T>(fill);
-        return;
+tpmlp_status distill_launch(const DistillArgs& a, cudaStream_t s, int* err) {
+    const int64_t bytes = a.V * (int64_t)sizeof(T);
+    if (a.dlogits == nullptr) {
+        const int split = row_split(a.N, bytes, false);
+        LaunchScope ls("vocab_distill", s);
+        return launch_rows(distill_kernel<T, true, false>, a.N, split, s, a, split, err);
     }
-    float lse;
-    if (a.loss) {
-        float m = -INFINITY;
-        for (int64_t i = threadIdx.x; i < a.V; i += ROW_THREADS) m = max_nan(m, to_f32(z[i]));
-        m = block_reduce(m, MaxNan(), red);
-        const float ms = m == -INFINITY ? 0.f : m / a.tau;
-        float s = 0.f;
-        for (int64_t i = threadIdx.x; i < a.V; i += ROW_THREADS) s += expf(to_f32(z[i]) / a.tau - ms);
-        s = block_reduce(s, Sum(), red);
-        lse = ms + logf(s);
-        float loss = 0.f;
-        for (int k = threadIdx.x; k < a.K; k += ROW_THREADS) {
-            if (ids[k] == -1) continue;
-            const float lq = tl[k] / a.tau - te.tm - logf(te.sum);
-            const float q = expf(lq);
-            if (q == 0.f) continue;
-            loss += q * (lq - log_prob(to_f32(z[ids[k]]) / a.tau, ms, logf(s), lse));
-        }
-        loss = block_reduce(loss, Sum(), red);
-        if (threadIdx.x == 0) {
-            a.loss[row] = a.tau * a.tau * loss;
-            if (a.lse) a.lse[row] = lse;
-        }
-    } else {
-        lse = a.lse_in[row];
+    if (a.loss == nullptr) {
+        const int split = row_split(a.N, bytes, false);
+        LaunchScope ls("vocab_distill_backward", s);
+        return launch_rows(distill_kernel<T, false, true>, a.N, split, s, a, split, err);
     }
-    if (!d) return;
-    const float w = a.grad_scale * (a.grad_tokens ? a.grad_tokens[row] : 1.f) * a.tau;
-    auto prob = [&](float x) { return lse == -INFINITY ? 0.f : expf(x / a.tau - lse); };
-    // the teacher's tokens, from the logits as they are before an in-place sweep
-    for (int k = threadIdx.x; k < a.K; k += ROW_THREADS) {
-        const int id = ids[k];
-        float q = 0.f;
-        if (id != -1)
-            for (int j = 0; j < a.K; ++j)
-                if (ids[j] == id) q += expf(tl[j] / a.tau - te.tm) / te.sum;
-        fix[k] = id != -1 ? w * (prob(to_f32(z[id])) - q) : 0.f;
-    }
-    __syncthreads();
-    for (int64_t i = threadIdx.x; i < a.V; i += ROW_THREADS) d[i] = from_f32<T>(w * prob(to_f32(z[i])));
-    __syncthreads();
-    for (int k = threadIdx.x; k < a.K; k += ROW_THREADS)
-        if (ids[k] != -1) d[ids[k]] = from_f32<T>(fix[k]);   // slots of one id hold one value
+    const int split = row_split(a.N, bytes, true);
+    LaunchScope ls("vocab_distill_with_grad", s);
+    return launch_rows(distill_kernel<T, true, true>, a.N, split, s, a, split, err);
 }
 
 }  // namespace
@@ -222,29 +883,17 @@ tpmlp_status run_vocab_logprobs(int f32, const LogprobArgs& a, cudaStream_t s) {
     if (a.N == 0) return TPMLP_OK;
     int* err = device_error_word();
     if (err == nullptr) return TPMLP_ERR_CUDA;
-    {
-        LaunchScope ls("vocab_logprobs", s);
-        if (f32)
-            logprobs_kernel<float><<<(unsigned)a.N, ROW_THREADS, 0, s>>>(a, err);
-        else
-            logprobs_kernel<__nv_bfloat16><<<(unsigned)a.N, ROW_THREADS, 0, s>>>(a, err);
-    }
-    return cudaGetLastError() == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
+    const int split = row_split(a.N, a.V * (f32 ? 4 : 2), false);
+    LaunchScope ls("vocab_logprobs", s);
+    return f32 ? launch_rows(logprobs_kernel<float>, a.N, split, s, a, split, err)
+               : launch_rows(logprobs_kernel<__nv_bfloat16>, a.N, split, s, a, split, err);
 }
 
 tpmlp_status run_vocab_distill(int f32, const DistillArgs& a, cudaStream_t s) {
     if (a.N == 0) return TPMLP_OK;
     int* err = device_error_word();
     if (err == nullptr) return TPMLP_ERR_CUDA;
-    {
-        LaunchScope ls(a.dlogits == nullptr ? "vocab_distill" : a.loss ? "vocab_distill_with_grad"
-                                                                       : "vocab_distill_backward", s);
-        if (f32)
-            distill_kernel<float><<<(unsigned)a.N, ROW_THREADS, 0, s>>>(a, err);
-        else
-            distill_kernel<__nv_bfloat16><<<(unsigned)a.N, ROW_THREADS, 0, s>>>(a, err);
-    }
-    return cudaGetLastError() == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
+    return f32 ? distill_launch<float>(a, s, err) : distill_launch<__nv_bfloat16>(a, s, err);
 }
 
 }  // namespace tpmlp
