@@ -65,7 +65,7 @@ __device__ __forceinline__ F2 f2(float a, float b) {
     asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
     return r;
 }
-__device__ __forceinline__ void split(F2 x, float& a, float& b) {
+__device__ __forceinline__ void split2(F2 x, float& a, float& b) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v));
 }
 __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
@@ -166,18 +166,24 @@ template <> struct Vec<float> {
             m = max_nan(m, max_nan(max_nan(elem(x[r], 0), elem(x[r], 1)), max_nan(elem(x[r], 2), elem(x[r], 3))));
         return m;
     }
-    struct Count {
-        int c;
-        __device__ __forceinline__ Count() : c(0) {}
+    struct Count {   // counts of one chunk as fp32 pairs
+        F2 c;
+        __device__ __forceinline__ Count() : c(f2(0.f, 0.f)) {}
         __device__ __forceinline__ void gt(const uint4& x, float t) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) c += elem(x, j) > t;
+            for (int j = 0; j < 4; j += 2)
+                c = add2(c, f2(elem(x, j) > t ? 1.f : 0.f, elem(x, j + 1) > t ? 1.f : 0.f));
         }
         __device__ __forceinline__ void ge(const uint4& x, float t) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) c += elem(x, j) >= t;
+            for (int j = 0; j < 4; j += 2)
+                c = add2(c, f2(elem(x, j) >= t ? 1.f : 0.f, elem(x, j + 1) >= t ? 1.f : 0.f));
         }
-        __device__ __forceinline__ int total() const { return c; }
+        __device__ __forceinline__ int total() const {
+            float a, b;
+            split2(c, a, b);
+            return (int)(a + b);
+        }
     };
     static __device__ __forceinline__ Wide wide(float z) { return z; }
     static __device__ __forceinline__ uint4 pack(const float (&v)[4]) {
@@ -189,51 +195,72 @@ template <> struct Vec<float> {
     }
 };
 
-// A row in 16-byte vectors. Vector i holds elements head + i N ... + N - 1;
-// vector -1 is the part before the first 16-byte boundary, vector `full` the
-// part after the last whole one; elements outside the row read as -inf. The
-// cluster's CTA `rank` owns vectors [lo, hi).
+// A row in 16-byte vectors. Vector i holds elements head + i N ... + N - 1, for
+// 0 <= i < full; the elements before the first 16-byte boundary are vector -1,
+// those after the last whole vector are vector `full` (the row's edges), with
+// -inf for what lies outside the row. The row's CTA `rank` owns the whole
+// vectors [lo, hi), elements [e_lo, e_hi): the first CTA with the front
+// edge, the last with the back edge.
 template <typename T>
 struct Row {
     using V4 = Vec<T>;
     const T* z;
     int head, full, len;
     int lo, hi;
-    __device__ __forceinline__ Row(const void* base, int64_t row, int64_t ld, int64_t V, int rank, int split) {
+    int e_lo, e_hi;
+    __device__ __forceinline__ Row(const void* base, int64_t row, int64_t ld, int64_t V, int rank, int log_split) {
         z = static_cast<const T*>(base) + row * ld;
         len = (int)V;
         const int off = (int)((16 - (reinterpret_cast<uintptr_t>(z) & 15)) & 15) / (int)sizeof(T);
         head = off < len ? off : len;
         full = (len - head) / V4::N;
-        const int first = head > 0 ? -1 : 0;
-        const int last = full + ((len - head) % V4::N != 0 ? 1 : 0);
-        const int64_t n = last - first;
-        lo = first + (int)(n * rank / split);
-        hi = first + (int)(n * (rank + 1) / split);
+        lo = (int)(((int64_t)full * rank) >> log_split);
+        hi = (int)(((int64_t)full * (rank + 1)) >> log_split);
+        e_lo = rank == 0 ? 0 : start(lo);
+        e_hi = rank == (1 << log_split) - 1 ? len : start(hi);
     }
     __device__ __forceinline__ int start(int i) const { return head + i * V4::N; }
-    __device__ __forceinline__ bool whole(int i) const { return i >= 0 && i < full; }
     __device__ __forceinline__ int vector_of(int e) const { return (e - head + V4::N) / V4::N - 1; }
-    __device__ __forceinline__ bool mine(int e) const {
-        const int i = vector_of(e);
-        return i >= lo && i < hi;
+    __device__ __forceinline__ bool mine(int e) const { return e >= e_lo && e < e_hi; }
+    __device__ __forceinline__ bool edges() const { return e_lo < start(lo) || e_hi > start(hi); }
+    // the edge that this thread looks after (full + 1: none)
+    __device__ __forceinline__ int edge() const {
+        if (threadIdx.x == 0 && e_lo < start(lo)) return -1;
+        if (threadIdx.x == 1 && e_hi > start(hi)) return full;
+        return full + 1;
     }
-    __device__ __forceinline__ uint4 load(int i) const {
-        if (whole(i)) return __ldcs(reinterpret_cast<const uint4*>(z + start(i)));
+    __device__ __forceinline__ uint4 load_edge(int i) const {
         uint4 x = make_uint4(V4::MASKED, V4::MASKED, V4::MASKED, V4::MASKED);
+        if (i > full) return x;
         const int e0 = start(i);
 #pragma unroll
         for (int j = 0; j < V4::N; ++j)
             if (e0 + j >= 0 && e0 + j < len) V4::set(x, j, z[e0 + j]);
         return x;
     }
-    // the vectors lo + base + r ROW_THREADS + thread of this CTA (-inf beyond hi)
+    __device__ __forceinline__ uint4 load(int i) const {
+        return __ldcs(reinterpret_cast<const uint4*>(z + head) + i);
+    }
+    // this thread's vectors of the chunk at `base`: base + r ROW_THREADS + thread
     __device__ __forceinline__ void load_chunk(int base, uint4 (&x)[VPT]) const {
+        const uint4* p = reinterpret_cast<const uint4*>(z + head) + base + threadIdx.x;
+#pragma unroll
+        for (int r = 0; r < VPT; ++r) x[r] = __ldcs(p + r * ROW_THREADS);
+    }
+    // the same for the slice's last chunk, -inf beyond it
+    __device__ __forceinline__ void load_rest(int base, uint4 (&x)[VPT]) const {
+        const uint4* p = reinterpret_cast<const uint4*>(z + head) + base + threadIdx.x;
+        const int left = hi - base - (int)threadIdx.x;
 #pragma unroll
         for (int r = 0; r < VPT; ++r) {
-            const int i = lo + base + r * ROW_THREADS + (int)threadIdx.x;
-            x[r] = i < hi ? load(i) : make_uint4(V4::MASKED, V4::MASKED, V4::MASKED, V4::MASKED);
+            x[r] = make_uint4(V4::MASKED, V4::MASKED, V4::MASKED, V4::MASKED);
+            if (r * ROW_THREADS < left) x[r] = __ldcs(p + r * ROW_THREADS);
         }
+    }
+    // where the last chunk starts: it has 1 to CHUNK vectors (none in an empty slice)
+    __device__ __forceinline__ int rest() const {
+        const int n = hi - lo;
+        return n > 0 ? lo + (n - 1) / CHUNK * CHUNK : lo;
     }
 };
 
@@ -244,28 +271,28 @@ struct Soft {
 
 // The state relative to another reference, not below its own.
 __device__ __forceinline__ void rebase(Soft& a, float ref, float c) {
-    const float d = fmaxf(a.ref - ref, kLowest);   // finite: an empty state stays 0
-    const float f = a.ref == ref ? 1.f : ex2((a.ref - ref) * c);   // NaN with ref
-    a.e = f * fmaf(a.s, d, a.e);
+    const float d = a.ref - ref;
+    const float f = ex2(d * c);   // NaN with ref
+    a.e = f == 0.f ? 0.f : f * fmaf(a.s, d, a.e);   // d may be -inf with f = 0
     a.s *= f;
     a.ref = ref;
 }
 
 // One chunk in registers added to a thread's state; ENT: with the entropy's sum.
-template <typename T, bool ENT>
-__device__ __forceinline__ void soft_chunk(Soft& st, const uint4 (&x)[VPT], float largest, float c) {
+template <typename T, bool ENT, int R>
+__device__ __forceinline__ void soft_chunk(Soft& st, const uint4 (&x)[R], float largest, float c) {
     const float ref = max_nan(st.ref, largest);
     rebase(st, ref, c);
     const F2 c2 = f2(c, c), r2 = f2(-ref, -ref);
     F2 s0 = f2(0.f, 0.f), s1 = s0, e0 = s0, e1 = s0;
 #pragma unroll
-    for (int r = 0; r < VPT; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int k = 0; k < Vec<T>::PAIRS; ++k) {
             const F2 z = ENT ? Vec<T>::pair_floor(x[r], k) : Vec<T>::pair(x[r], k);
             const F2 t = add2(z, r2);
             float a, b;
-            split(mul2(t, c2), a, b);
+            split2(mul2(t, c2), a, b);
             const F2 p = f2(ex2(a), ex2(b));
             if (k & 1) {
                 s1 = add2(s1, p);
@@ -276,10 +303,10 @@ __device__ __forceinline__ void soft_chunk(Soft& st, const uint4 (&x)[VPT], floa
             }
         }
     float a, b;
-    split(add2(s0, s1), a, b);
+    split2(add2(s0, s1), a, b);
     st.s += a + b;
     if (ENT) {
-        split(add2(e0, e1), a, b);
+        split2(add2(e0, e1), a, b);
         st.e += a + b;
     }
 }
@@ -430,8 +457,11 @@ struct TopShared {
     unsigned long long all[MAX_SPLIT * TPMLP_MAX_TOP];       // the leader's copy of every CTA's list
     unsigned long long red[ROW_WARPS];
     uint32_t thr[ROW_WARPS];
-    int threads[ROW_THREADS];
-    int n_threads, n_cand;
+    uint32_t max_of[ROW_THREADS];    // maxima that reach the first bound, and their threads
+    int thread_of[ROW_THREADS];
+    int owner[ROW_THREADS];          // the threads whose entries are looked at
+    uint32_t bound;
+    int n_max, n_owner, n_cand;
 };
 
 // The elements of vector i that are in the row and at least `thr` (strictly
@@ -452,15 +482,17 @@ __device__ __forceinline__ void offer(const Row<T>& row, int i, const uint4& x, 
 
 // The slice's first K entries into sh.list (0: fewer than K entries).
 //
-// `raw` is the largest element the thread saw. With g = ceil(K / warps), the
-// g-th largest of a warp's 32 such maxima is reached by g different entries,
-// so the least of the warps' g-th maxima is reached by at least K entries:
-// only entries at or above it can be in the list. They sit with the few
-// threads whose maximum reaches it (some 2 K of 256 for K = 20), whose vectors
-// are still in registers (one chunk) or read again. Where more than MAX_CAND
-// entries reach the bound (a mask that leaves fewer than K tokens, rows of
-// equal values), the entries above it are taken alone and equal ones follow
-// by index; where even those are too many, K rounds over the slice.
+// `raw` is the largest element the thread saw. The K-th largest of the 256
+// maxima is reached by K different entries, so only entries at or above it can
+// be in the list, and they sit with the threads whose maximum reaches it: K of
+// 256 unless maxima are equal. Their vectors are still in registers (one
+// chunk) or read again (K / 256 of the slice). The K-th largest maximum comes
+// in two steps: with g = ceil(K / warps), the least of the warps' g-th largest
+// maxima leaves a few dozen, and those are ranked by counting.
+// Where more than MAX_CAND entries reach the bound (a mask that leaves fewer
+// than K tokens, rows of equal values), the entries above it are taken alone
+// and equal ones follow by index; where even those are too many, K rounds
+// over the slice.
 template <typename T>
 __device__ void slice_top(const Row<T>& row, int K, float raw, const uint4 (&x)[VPT], TopShared& sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -472,13 +504,34 @@ __device__ void slice_top(const Row<T>& row, int K, float raw, const uint4 (&x)[
         if (lane == __ffs(who) - 1) left = 0u;
     }
     if (lane == 0) sh.thr[warp] = g_th;
-    if (threadIdx.x == 0) sh.n_threads = sh.n_cand = 0;
+    if (threadIdx.x == 0) sh.n_max = sh.n_owner = sh.n_cand = 0;
     for (int k = threadIdx.x; k < K; k += ROW_THREADS) sh.list[k] = 0ull;
     __syncthreads();
     uint32_t thr = sh.thr[0];
     for (int w = 1; w < ROW_WARPS; ++w) thr = min(thr, sh.thr[w]);
+    if (mine >= thr) {
+        const int at = atomicAdd(&sh.n_max, 1);
+        sh.max_of[at] = mine;
+        sh.thread_of[at] = (int)threadIdx.x;
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < sh.n_max) {
+        const uint32_t me = sh.max_of[threadIdx.x];
+        int above = 0, reach = 0;
+        for (int j = 0; j < sh.n_max; ++j) {
+            above += sh.max_of[j] > me;
+            reach += sh.max_of[j] >= me;
+        }
+        if (above < K) {
+            sh.owner[atomicAdd(&sh.n_owner, 1)] = sh.thread_of[threadIdx.x];
+            if (reach >= K) sh.bound = me;   // the K-th largest: one value
+        }
+    }
+    __syncthreads();
+    thr = sh.bound;
     const int n = row.hi - row.lo;
     const int per = (n + ROW_THREADS - 1) / ROW_THREADS;   // vectors of a thread
+    if (mine >= thr && row.edge() <= row.full) offer(row, row.edge(), row.load_edge(row.edge()), thr, false, sh);
     if (n <= CHUNK) {
         if (mine >= thr) {
 #pragma unroll
@@ -488,11 +541,9 @@ __device__ void slice_top(const Row<T>& row, int K, float raw, const uint4 (&x)[
             }
         }
     } else {
-        if (mine >= thr) sh.threads[atomicAdd(&sh.n_threads, 1)] = (int)threadIdx.x;
-        __syncthreads();
-        const int items = sh.n_threads * per;
+        const int items = sh.n_owner * per;
         for (int a = threadIdx.x; a < items; a += ROW_THREADS) {
-            const int i = row.lo + (a % per) * ROW_THREADS + sh.threads[a / per];
+            const int i = row.lo + (a % per) * ROW_THREADS + sh.owner[a / per];
             if (i < row.hi) offer(row, i, row.load(i), thr, false, sh);
         }
     }
@@ -502,16 +553,16 @@ __device__ void slice_top(const Row<T>& row, int K, float raw, const uint4 (&x)[
         __syncthreads();
         if (threadIdx.x == 0) sh.n_cand = 0;
         __syncthreads();
+        if (row.edge() <= row.full) offer(row, row.edge(), row.load_edge(row.edge()), thr, true, sh);
         for (int i = row.lo + (int)threadIdx.x; i < row.hi; i += ROW_THREADS)
             offer(row, i, row.load(i), thr, true, sh);
         __syncthreads();
         count = sh.n_cand;
         if (count <= MAX_CAND - K) {
             // entries equal to the bound, in index order, until there are K
-            const int e_lo = max(row.start(row.lo), 0), e_hi = min(row.start(row.hi), row.len);
-            for (int e = e_lo; e < e_hi && count < K; e += ROW_THREADS) {
+            for (int e = row.e_lo; e < row.e_hi && count < K; e += ROW_THREADS) {
                 const int at = e + (int)threadIdx.x;
-                const bool hit = at < e_hi && order32(to_f32(row.z[at])) == thr;
+                const bool hit = at < row.e_hi && order32(to_f32(row.z[at])) == thr;
                 const uint32_t b = __ballot_sync(0xffffffffu, hit);
                 if (lane == 0) sh.thr[warp] = __popc(b);
                 __syncthreads();
@@ -526,14 +577,9 @@ __device__ void slice_top(const Row<T>& row, int K, float raw, const uint4 (&x)[
             unsigned long long last = ~0ull;
             for (int k = 0; k < K; ++k) {
                 unsigned long long best = 0ull;
-                for (int i = row.lo + (int)threadIdx.x; i < row.hi; i += ROW_THREADS) {
-                    const uint4 y = row.load(i);
-                    const int e0 = row.start(i);
-                    for (int j = 0; j < Vec<T>::N; ++j) {
-                        if (e0 + j < 0 || e0 + j >= row.len) continue;
-                        const unsigned long long key = order_key(order32(Vec<T>::elem(y, j)), (uint32_t)(e0 + j));
-                        if (key < last && key > best) best = key;
-                    }
+                for (int e = row.e_lo + (int)threadIdx.x; e < row.e_hi; e += ROW_THREADS) {
+                    const unsigned long long key = order_key(order32(to_f32(row.z[e])), (uint32_t)e);
+                    if (key < last && key > best) best = key;
                 }
                 last = block_reduce(best, MaxU64(), sh.red);
                 if (threadIdx.x == 0) sh.list[k] = last;
@@ -555,15 +601,16 @@ __device__ void slice_top(const Row<T>& row, int K, float raw, const uint4 (&x)[
 // ---------------------------------------------------- log probabilities --
 
 template <typename T>
-__global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobArgs a, int split, int* err) {
+__global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobArgs a, int log_split, int* err) {
     __shared__ Part red[ROW_WARPS];
     __shared__ Part parts[MAX_SPLIT];
     __shared__ float redf[ROW_WARPS];
     __shared__ TopShared sh;
-    const int64_t row_i = blockIdx.x / (unsigned)split;
-    const int rank = (int)(blockIdx.x - row_i * split);
+    const int split = 1 << log_split;
+    const int64_t row_i = blockIdx.x >> log_split;
+    const int rank = (int)(blockIdx.x & (unsigned)(split - 1));
     if (split > 1) cluster_arrive();   // this CTA runs: its shared memory may be written
-    const Row<T> row(a.logits, row_i, a.ld, a.V, rank, split);
+    const Row<T> row(a.logits, row_i, a.ld, a.V, rank, log_split);
     const int64_t t = a.targets ? a.targets[row_i] : -1;
     const bool good = t >= 0 && t < a.V;
     const float zt = good ? to_f32(row.z[t]) : INFINITY;
@@ -571,35 +618,60 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
     // Vectors before the target's count equals; inside its own vector they
     // are added below. A masked target is counted apart.
     const bool counted = good && zt > -INFINITY;
-    const int tvec = counted ? row.vector_of((int)t) : row.lo;
+    const int tvec = counted ? row.vector_of((int)t) : -1;
     const auto zw = Vec<T>::wide(counted ? zt : INFINITY);
 
     Soft st{Vec<T>::lowest(), 0.f, 0.f};
     int before = 0;
     float raw = -INFINITY;
     uint4 x[VPT];
-    const int n = row.hi - row.lo;
-    for (int base = 0; base < n; base += CHUNK) {
-        row.load_chunk(base, x);
+    auto chunk = [&](int base) {
         const float largest = Vec<T>::largest(x);
         raw = max_nan(raw, largest);
         soft_chunk<T, true>(st, x, largest, kLog2e);
         typename Vec<T>::Count cnt;
+        if (base + CHUNK <= tvec) {
 #pragma unroll
-        for (int r = 0; r < VPT; ++r) {
-            if (row.lo + base + r * ROW_THREADS + (int)threadIdx.x < tvec)
-                cnt.ge(x[r], zw);
-            else
-                cnt.gt(x[r], zw);
+            for (int r = 0; r < VPT; ++r) cnt.ge(x[r], zw);
+        } else if (base >= tvec) {
+#pragma unroll
+            for (int r = 0; r < VPT; ++r) cnt.gt(x[r], zw);
+        } else {
+#pragma unroll
+            for (int r = 0; r < VPT; ++r) {
+                if (base + r * ROW_THREADS + (int)threadIdx.x < tvec)
+                    cnt.ge(x[r], zw);
+                else
+                    cnt.gt(x[r], zw);
+            }
         }
         before += cnt.total();
+    };
+    if (row.edges()) {
+        const uint4 e[1] = {row.load_edge(row.edge())};
+        raw = Vec<T>::largest(e);
+        soft_chunk<T, true>(st, e, raw, kLog2e);
+        typename Vec<T>::Count cnt;
+        if (row.edge() < tvec)
+            cnt.ge(e[0], zw);
+        else
+            cnt.gt(e[0], zw);
+        before += cnt.total();
     }
-    if (counted && threadIdx.x == 0 && tvec >= row.lo && tvec < row.hi)
+    const int rest = row.rest();
+    for (int base = row.lo; base < rest; base += CHUNK) {
+        row.load_chunk(base, x);
+        chunk(base);
+    }
+    if (rest < row.hi) {
+        row.load_rest(rest, x);
+        chunk(rest);
+    }
+    if (counted && threadIdx.x == 0 && row.mine((int)t))
         for (int e = max(row.start(tvec), 0); e < (int)t; ++e) before += to_f32(row.z[e]) == zt;
     if (good && !counted) {   // -inf (or NaN) given: every other entry is compared
         before = 0;
-        const int e_lo = max(row.start(row.lo), 0), e_hi = min(row.start(row.hi), row.len);
-        for (int e = e_lo + (int)threadIdx.x; e < e_hi; e += ROW_THREADS) {
+        for (int e = row.e_lo + (int)threadIdx.x; e < row.e_hi; e += ROW_THREADS) {
             const float v = to_f32(row.z[e]);
             before += v > zt || (v == zt && e < (int)t);
         }
@@ -708,63 +780,115 @@ __device__ void teacher_row(const DistillArgs& a, int64_t row_i, const Row<T>& r
     }
 }
 
+// (reference, sum) of every warp of the row's CTAs, in one place of each CTA
+struct __align__(8) WarpSoft {
+    float ref, s;
+};
+
 // LOSS: loss and lse; GRAD: the gradient (with LOSS from this launch's
 // statistics, else from the given lse).
 template <typename T, bool LOSS, bool GRAD>
-__global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillArgs a, int split, int* err) {
-    __shared__ Part red[ROW_WARPS];
-    __shared__ Part parts[MAX_SPLIT];
+__global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillArgs a, int log_split, int* err) {
+    __shared__ WarpSoft parts[MAX_SPLIT * ROW_WARPS];
     __shared__ float redf[ROW_WARPS];
     __shared__ TeacherShared te;
-    const int64_t row_i = blockIdx.x / (unsigned)split;
-    const int rank = (int)(blockIdx.x - row_i * split);
-    if (LOSS && split > 1) cluster_arrive();
-    const Row<T> row(a.logits, row_i, a.ld, a.V, rank, split);
+    const int split = 1 << log_split;
+    const int64_t row_i = blockIdx.x >> log_split;
+    const int rank = (int)(blockIdx.x & (unsigned)(split - 1));
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (LOSS && split > 1) cluster_arrive();   // this CTA runs: its shared memory may be written
+    const Row<T> row(a.logits, row_i, a.ld, a.V, rank, log_split);
     T* d = GRAD ? static_cast<T*>(a.dlogits) + row_i * a.ldd : nullptr;
-    if (threadIdx.x < 32) teacher_row(a, row_i, row, GRAD, te);
-    __syncthreads();
-    const bool dead = te.bad || !te.some;
+    const int32_t* ids = a.ids + row_i * a.K;
+    const float* tl = a.teacher + row_i * a.K;
     const float c = kLog2e / a.tau;
-    const int n = row.hi - row.lo;
+    const int rest = row.rest();
+
+    // A row without a live slot is not read. Every warp looks for one by
+    // itself (the first 32 slots, as a rule), so that its loads of the row
+    // are on their way before warp 0 takes the teacher's statistics.
+    bool live = false;
+    for (int k = lane; __any_sync(0xffffffffu, k < a.K); k += 32) {
+        const int id = k < a.K ? ids[k] : -1;
+        live = __any_sync(0xffffffffu, id != -1 && (tl[k] != -INFINITY || id < -1 || id >= a.V));
+        if (live) break;
+    }
     uint4 x[VPT];
+    const bool single = rest == row.lo;   // the slice is one chunk, which stays in registers
+    if (live && single) row.load_rest(rest, x);
+    if (warp == 0) teacher_row(a, row_i, row, GRAD, te);
+
     Dist dist{};
     if (LOSS) {
         Soft st{kLowest, 0.f, 0.f};
-        if (!dead)
-            for (int base = 0; base < n; base += CHUNK) {
+        if (live) {
+            if (row.edges()) {
+                const uint4 e[1] = {row.load_edge(row.edge())};
+                soft_chunk<T, false>(st, e, Vec<T>::largest(e), c);
+            }
+            for (int base = row.lo; base < rest; base += CHUNK) {
                 row.load_chunk(base, x);
                 soft_chunk<T, false>(st, x, Vec<T>::largest(x), c);
             }
+            if (!single) row.load_rest(rest, x);
+            soft_chunk<T, false>(st, x, Vec<T>::largest(x), c);
+        }
         // the leader's loss: (ln q - ln p) needs the student's logits at the
         // teacher's tokens, read before anything is written in place
         constexpr int LPT = TPMLP_MAX_TEACHER / ROW_THREADS;
         float zk[LPT];
-        if (rank == 0 && !dead) {
+        if (rank == 0 && live) {
 #pragma unroll
             for (int u = 0; u < LPT; ++u) {
                 const int k = threadIdx.x + u * ROW_THREADS;
-                const int id = k < a.K ? a.ids[row_i * a.K + k] : -1;
-                zk[u] = id != -1 ? to_f32(row.z[id]) : 0.f;
+                if (k >= a.K) break;
+                const int id = ids[k];
+                zk[u] = id >= 0 && id < a.V ? to_f32(row.z[id]) : 0.f;
             }
         }
-        Part part = block_part(st, 0, red, c);
+        // every warp's sums to every CTA of the row; all of them add the same
+        // numbers in the same order
+        float m = st.ref;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
+        rebase(st, m, c);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) st.s += __shfl_xor_sync(0xffffffffu, st.s, off);
         if (split > 1) {
             cluster_wait();
-            if ((int)threadIdx.x < split) send_part(parts, rank, threadIdx.x, part);
+            if (lane < split) {
+                const uint32_t at = mapa_shared(smem_u32(&parts[rank * ROW_WARPS + warp]), (uint32_t)lane);
+                asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(m), "f"(st.s) : "memory");
+            }
             cluster_arrive();
             cluster_wait();
-            part = combine(parts, split, c);
+        } else {
+            if (lane == 0) parts[warp] = WarpSoft{m, st.s};
+            __syncthreads();
         }
-        dist = distribution(part.soft, c, 1.f / a.tau);
+        const int total = split * ROW_WARPS;
+        WarpSoft p0 = lane < total ? parts[lane] : WarpSoft{kLowest, 0.f};
+        WarpSoft p1 = lane + 32 < total ? parts[lane + 32] : WarpSoft{kLowest, 0.f};
+        m = max_nan(p0.ref, p1.ref);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
+        Soft s0{p0.ref, p0.s, 0.f}, s1{p1.ref, p1.s, 0.f};
+        rebase(s0, m, c);
+        rebase(s1, m, c);
+        s0.s += s1.s;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) s0.s += __shfl_xor_sync(0xffffffffu, s0.s, off);
+        dist = distribution(s0, c, 1.f / a.tau);
         if (rank == 0) {
             float loss = 0.f;
-            if (!dead) {
+            if (te.some && !te.bad) {
                 const float log2_sum = log2f(te.sum);
 #pragma unroll
                 for (int u = 0; u < LPT; ++u) {
                     const int k = threadIdx.x + u * ROW_THREADS;
-                    if (k >= a.K || a.ids[row_i * a.K + k] == -1) continue;
-                    const float lq = (a.teacher[row_i * a.K + k] - te.tm) * c - log2_sum;
+                    if (k >= a.K) break;
+                    if (ids[k] == -1) continue;
+                    const float lq = (tl[k] - te.tm) * c - log2_sum;
                     const float q = ex2(lq);
                     if (q != 0.f) loss += q * (kLn2 * lq - dist.ln_p(zk[u]));
                 }
@@ -773,10 +897,11 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillAr
             if (threadIdx.x == 0) {
                 if (te.bad) atomicCAS(err, 0, (int)TPMLP_ERR_ARG);
                 a.loss[row_i] = te.bad ? NAN : a.tau * a.tau * loss;
-                if (a.lse) a.lse[row_i] = te.bad ? NAN : dead ? 0.f : dist.lse();
+                if (a.lse) a.lse[row_i] = te.bad ? NAN : te.some ? dist.lse() : 0.f;
             }
         }
     } else {
+        __syncthreads();   // the teacher's statistics
         if (te.bad && rank == 0 && threadIdx.x == 0) atomicCAS(err, 0, (int)TPMLP_ERR_ARG);
         const float lse = a.lse_in[row_i];
         dist.c = c;   // p = 2^((z - lse tau) c)
@@ -785,11 +910,11 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillAr
         dist.s = 1.f;
     }
     if (!GRAD) return;
-    const float w = te.bad ? NAN : a.grad_scale * (a.grad_tokens ? a.grad_tokens[row_i] : 1.f) * a.tau;
+    const float w = a.grad_scale * (a.grad_tokens ? a.grad_tokens[row_i] : 1.f) * a.tau;
     const float ws = w / dist.s;   // times 2^exponent: w p
+    // rows without probabilities hold `fill` and, where the teacher has some, its part
+    const bool flat = te.bad || !te.some || dist.nothing;
     const float fill = te.bad ? NAN : 0.f;
-    const bool flat = dead || dist.nothing;   // no probabilities: the gradient is `fill` and the teacher's part
-    auto grad = [&](float z) { return flat ? fill : ws * ex2(dist.exponent(z)); };
     // the CTA's teacher tokens, from the logits as they are before the sweep;
     // slots of one id all get the row's full value
     for (int k = threadIdx.x; k < te.n; k += ROW_THREADS) {
@@ -797,28 +922,56 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillAr
         float q = 0.f;
         for (int j = 0; j < te.n; ++j)
             if (te.id[j] == id) q += te.q[j];
-        te.fix[k] = fmaf(-w, q, grad(to_f32(row.z[id])));
+        te.fix[k] = fmaf(-w, q, flat ? fill : ws * ex2(dist.exponent(to_f32(row.z[id]))));
     }
     __syncthreads();
-    const bool kept = LOSS && !dead && n <= CHUNK;   // the slice is still in registers
     const bool same = ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(row.z)) & 15) == 0;
-    for (int base = 0; base < n; base += CHUNK) {
-        if (!kept && !dead) row.load_chunk(base, x);
+    const F2 c2 = f2(c, c), r2 = f2(-dist.ref, -dist.ref), w2 = f2(ws, ws);
+    auto gradient = [&](const uint4& z, float (&v)[Vec<T>::N]) {
+#pragma unroll
+        for (int k = 0; k < Vec<T>::PAIRS; ++k) {
+            float e0, e1;
+            split2(mul2(add2(Vec<T>::pair(z, k), r2), c2), e0, e1);
+            split2(mul2(f2(ex2(e0), ex2(e1)), w2), v[2 * k], v[2 * k + 1]);
+            if (flat) v[2 * k] = v[2 * k + 1] = fill;
+        }
+    };
+    auto store = [&](int i, const float (&v)[Vec<T>::N]) {
+        T* at = d + row.start(i);
+        if (same) {
+            __stcs(reinterpret_cast<uint4*>(at), Vec<T>::pack(v));
+        } else {
+#pragma unroll
+            for (int j = 0; j < Vec<T>::N; ++j) at[j] = from_f32<T>(v[j]);
+        }
+    };
+    if (row.edge() <= row.full) {
+        const int i = row.edge(), e0 = row.start(i);
+        float v[Vec<T>::N];
+        gradient(live ? row.load_edge(i) : make_uint4(0, 0, 0, 0), v);
+#pragma unroll
+        for (int j = 0; j < Vec<T>::N; ++j)
+            if (e0 + j >= 0 && e0 + j < row.len) d[e0 + j] = from_f32<T>(v[j]);
+    }
+    // Back to front: the last chunk is still in registers, what was read last is
+    // the likeliest to be in L2.
+    if (live && !LOSS && !single) row.load_rest(rest, x);
+#pragma unroll
+    for (int r = 0; r < VPT; ++r) {
+        const int i = rest + r * ROW_THREADS + (int)threadIdx.x;
+        if (i < row.hi) {
+            float v[Vec<T>::N];
+            gradient(x[r], v);
+            store(i, v);
+        }
+    }
+    for (int base = rest - CHUNK; base >= row.lo; base -= CHUNK) {
+        if (live) row.load_chunk(base, x);
 #pragma unroll
         for (int r = 0; r < VPT; ++r) {
-            const int i = row.lo + base + r * ROW_THREADS + (int)threadIdx.x;
-            if (i >= row.hi) break;
             float v[Vec<T>::N];
-#pragma unroll
-            for (int j = 0; j < Vec<T>::N; ++j) v[j] = grad(Vec<T>::elem(x[r], j));
-            const int e0 = row.start(i);
-            if (same && row.whole(i)) {
-                __stcs(reinterpret_cast<uint4*>(d + e0), Vec<T>::pack(v));
-            } else {
-#pragma unroll
-                for (int j = 0; j < Vec<T>::N; ++j)
-                    if (e0 + j >= 0 && e0 + j < row.len) d[e0 + j] = from_f32<T>(v[j]);
-            }
+            gradient(x[r], v);
+            store(base + r * ROW_THREADS + (int)threadIdx.x, v);
         }
     }
     __syncthreads();
@@ -827,21 +980,22 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillAr
 
 // ---------------------------------------------------------------- launch --
 
-// CTAs per row. Few rows: enough CTAs to occupy the SMs twice over, while a
+// CTAs per row, as a power of two. Few rows: enough CTAs to occupy the SMs twice over, while a
 // slice still has a vector for every thread. With `hold` the slice should
 // also fit the registers, so that the gradient needs no second read.
 int row_split(int64_t N, int64_t row_bytes, bool hold) {
     const int64_t want = 4LL * device_sm_count();
-    if (N * MAX_SPLIT > 0x7fffffffLL) return 1;
-    int split = 1;
-    while (split < MAX_SPLIT && N * split < want && row_bytes / (2 * split) >= ROW_THREADS * 16) split *= 2;
+    if (N * MAX_SPLIT > 0x7fffffffLL) return 0;
+    int l = 0;
+    while ((1 << l) < MAX_SPLIT && (N << l) < want && (row_bytes >> (l + 1)) >= ROW_THREADS * 16) ++l;
     if (hold && row_bytes + 32 <= (int64_t)MAX_SPLIT * CHUNK * 16)
-        while ((row_bytes + 32 + split - 1) / split > CHUNK * 16) split *= 2;
-    return split;
+        while (((row_bytes + 32) >> l) > CHUNK * 16) ++l;
+    return l;
 }
 
 template <typename... P, typename... A>
-tpmlp_status launch_rows(void (*kernel)(P...), int64_t N, int split, cudaStream_t s, A... args) {
+tpmlp_status launch_rows(void (*kernel)(P...), int64_t N, int log_split, cudaStream_t s, A... args) {
+    const int split = 1 << log_split;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3((unsigned)(N * split));
