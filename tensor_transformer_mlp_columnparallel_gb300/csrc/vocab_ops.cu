@@ -28,7 +28,6 @@ namespace {
 constexpr int ROW_THREADS = 256;
 constexpr int ROW_WARPS = ROW_THREADS / 32;
 constexpr int VPT = 8;                        // 16-byte vectors a thread holds
-constexpr int CHUNK = ROW_THREADS * VPT;      // vectors a CTA holds
 constexpr int MAX_SPLIT = 8;                  // CTAs of a row (the portable cluster size)
 constexpr float kLowest = -3.402823466e38f;   // FLT_MAX's negative
 constexpr float kLog2e = 1.4426950408889634f;
@@ -201,9 +200,10 @@ template <> struct Vec<float> {
 // -inf for what lies outside the row. The row's CTA `rank` owns the whole
 // vectors [lo, hi), elements [e_lo, e_hi): the first CTA with the front
 // edge, the last with the back edge.
-template <typename T>
+template <typename T, int NT>
 struct Row {
     using V4 = Vec<T>;
+    static constexpr int CHUNK = NT * VPT;   // vectors the CTA's registers hold
     const T* z;
     int head, full, len;
     int lo, hi;
@@ -238,23 +238,22 @@ struct Row {
             if (e0 + j >= 0 && e0 + j < len) V4::set(x, j, z[e0 + j]);
         return x;
     }
-    __device__ __forceinline__ uint4 load(int i) const {
-        return __ldcs(reinterpret_cast<const uint4*>(z + head) + i);
-    }
-    // this thread's vectors of the chunk at `base`: base + r ROW_THREADS + thread
+    __device__ __forceinline__ const uint4* vectors() const { return reinterpret_cast<const uint4*>(z + head); }
+    __device__ __forceinline__ uint4 load(int i) const { return __ldcs(vectors() + i); }
+    // this thread's vectors of the chunk at `base`: base + r NT + thread
     __device__ __forceinline__ void load_chunk(int base, uint4 (&x)[VPT]) const {
-        const uint4* p = reinterpret_cast<const uint4*>(z + head) + base + threadIdx.x;
+        const uint4* p = vectors() + base + threadIdx.x;
 #pragma unroll
-        for (int r = 0; r < VPT; ++r) x[r] = __ldcs(p + r * ROW_THREADS);
+        for (int r = 0; r < VPT; ++r) x[r] = __ldcs(p + r * NT);
     }
     // the same for the slice's last chunk, -inf beyond it
     __device__ __forceinline__ void load_rest(int base, uint4 (&x)[VPT]) const {
-        const uint4* p = reinterpret_cast<const uint4*>(z + head) + base + threadIdx.x;
+        const uint4* p = vectors() + base + threadIdx.x;
         const int left = hi - base - (int)threadIdx.x;
 #pragma unroll
         for (int r = 0; r < VPT; ++r) {
             x[r] = make_uint4(V4::MASKED, V4::MASKED, V4::MASKED, V4::MASKED);
-            if (r * ROW_THREADS < left) x[r] = __ldcs(p + r * ROW_THREADS);
+            if (r * NT < left) x[r] = __ldcs(p + r * NT);
         }
     }
     // where the last chunk starts: it has 1 to CHUNK vectors (none in an empty slice)
@@ -373,7 +372,7 @@ __device__ T block_reduce(T v, Op op, T* red) {
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
     T r = red[0];
-    for (int w = 1; w < ROW_WARPS; ++w) r = op(r, red[w]);
+    for (int w = 1; w < (int)(blockDim.x >> 5); ++w) r = op(r, red[w]);
     __syncthreads();
     return r;
 }
@@ -467,7 +466,7 @@ struct TopShared {
 // The elements of vector i that are in the row and at least `thr` (strictly
 // above with `above`) join the candidates; beyond MAX_CAND they are only counted.
 template <typename T>
-__device__ __forceinline__ void offer(const Row<T>& row, int i, const uint4& x, uint32_t thr, bool above,
+__device__ __forceinline__ void offer(const Row<T, ROW_THREADS>& row, int i, const uint4& x, uint32_t thr, bool above,
                                       TopShared& sh) {
     const int e0 = row.start(i);
 #pragma unroll
@@ -494,7 +493,7 @@ __device__ __forceinline__ void offer(const Row<T>& row, int i, const uint4& x, 
 // and equal ones follow by index; where even those are too many, K rounds
 // over the slice.
 template <typename T>
-__device__ void slice_top(const Row<T>& row, int K, float raw, const uint4 (&x)[VPT], TopShared& sh) {
+__device__ void slice_top(const Row<T, ROW_THREADS>& row, int K, float raw, const uint4 (&x)[VPT], TopShared& sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t mine = order32(raw);
     uint32_t left = mine, g_th = 0;
@@ -532,7 +531,7 @@ __device__ void slice_top(const Row<T>& row, int K, float raw, const uint4 (&x)[
     const int n = row.hi - row.lo;
     const int per = (n + ROW_THREADS - 1) / ROW_THREADS;   // vectors of a thread
     if (mine >= thr && row.edge() <= row.full) offer(row, row.edge(), row.load_edge(row.edge()), thr, false, sh);
-    if (n <= CHUNK) {
+    if (n <= Row<T, ROW_THREADS>::CHUNK) {
         if (mine >= thr) {
 #pragma unroll
             for (int r = 0; r < VPT; ++r) {
@@ -610,7 +609,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
     const int64_t row_i = blockIdx.x >> log_split;
     const int rank = (int)(blockIdx.x & (unsigned)(split - 1));
     if (split > 1) cluster_arrive();   // this CTA runs: its shared memory may be written
-    const Row<T> row(a.logits, row_i, a.ld, a.V, rank, log_split);
+    const Row<T, ROW_THREADS> row(a.logits, row_i, a.ld, a.V, rank, log_split);
     const int64_t t = a.targets ? a.targets[row_i] : -1;
     const bool good = t >= 0 && t < a.V;
     const float zt = good ? to_f32(row.z[t]) : INFINITY;
@@ -624,6 +623,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
     Soft st{Vec<T>::lowest(), 0.f, 0.f};
     int before = 0;
     float raw = -INFINITY;
+    constexpr int CHUNK = Row<T, ROW_THREADS>::CHUNK;
     uint4 x[VPT];
     auto chunk = [&](int base) {
         const float largest = Vec<T>::largest(x);
@@ -734,8 +734,9 @@ struct TeacherShared {
 
 // Warp 0: statistics over the K slots, then the slots whose id is in the
 // CTA's slice, in slot order.
-template <typename T>
-__device__ void teacher_row(const DistillArgs& a, int64_t row_i, const Row<T>& row, bool lists, TeacherShared& sh) {
+template <typename T, int NT>
+__device__ void teacher_row(const DistillArgs& a, int64_t row_i, const Row<T, NT>& row, bool lists,
+                            TeacherShared& sh) {
     const int lane = threadIdx.x;
     const int32_t* ids = a.ids + row_i * a.K;
     const float* tl = a.teacher + row_i * a.K;
@@ -785,19 +786,35 @@ struct __align__(8) WarpSoft {
     float ref, s;
 };
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // LOSS: loss and lse; GRAD: the gradient (with LOSS from this launch's
 // statistics, else from the given lse).
-template <typename T, bool LOSS, bool GRAD>
-__global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillArgs a, int log_split, int* err) {
-    __shared__ WarpSoft parts[MAX_SPLIT * ROW_WARPS];
-    __shared__ float redf[ROW_WARPS];
+//
+// With both, the row is read once and stays on the chip: the slice's last
+// chunk in registers, the one before it in shared memory (a thread's own
+// vectors, so no barrier), 64 KB a CTA and 256 KB an SM. A slice that is
+// longer reads its other chunks again, last one first. (4096 rows of 128000
+// bf16 logits on GB300: 384 us with four 256-thread CTAs an SM, 405 us with
+// two of 512; 440 us with the second pass from L2, of which half went back
+// to DRAM.)
+template <typename T, int NT, bool LOSS, bool GRAD>
+__global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArgs a, int log_split, int* err) {
+    constexpr bool STAGE = LOSS && GRAD;
+    constexpr int WARPS = NT / 32, CHUNK = Row<T, NT>::CHUNK;
+    extern __shared__ uint4 stage[];   // STAGE: one chunk
+    __shared__ WarpSoft parts[MAX_SPLIT * WARPS];
+    __shared__ float redf[WARPS];
     __shared__ TeacherShared te;
     const int split = 1 << log_split;
     const int64_t row_i = blockIdx.x >> log_split;
     const int rank = (int)(blockIdx.x & (unsigned)(split - 1));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (LOSS && split > 1) cluster_arrive();   // this CTA runs: its shared memory may be written
-    const Row<T> row(a.logits, row_i, a.ld, a.V, rank, log_split);
+    const Row<T, NT> row(a.logits, row_i, a.ld, a.V, rank, log_split);
     T* d = GRAD ? static_cast<T*>(a.dlogits) + row_i * a.ldd : nullptr;
     const int32_t* ids = a.ids + row_i * a.K;
     const float* tl = a.teacher + row_i * a.K;
@@ -814,8 +831,16 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillAr
         if (live) break;
     }
     uint4 x[VPT];
-    const bool single = rest == row.lo;   // the slice is one chunk, which stays in registers
-    if (live && single) row.load_rest(rest, x);
+    const int staged = STAGE && rest > row.lo ? rest - CHUNK : rest;   // where the chunk in shared memory starts
+    const bool early = staged == row.lo;   // nothing is read through the registers before the last chunk
+    if (live) {
+        if (staged < rest) {
+            const uint4* p = row.vectors() + staged + threadIdx.x;
+#pragma unroll
+            for (int r = 0; r < VPT; ++r) cp_async16(smem_u32(stage + r * NT + threadIdx.x), p + r * NT);
+        }
+        if (early) row.load_rest(rest, x);
+    }
     if (warp == 0) teacher_row(a, row_i, row, GRAD, te);
 
     Dist dist{};
@@ -826,21 +851,29 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillAr
                 const uint4 e[1] = {row.load_edge(row.edge())};
                 soft_chunk<T, false>(st, e, Vec<T>::largest(e), c);
             }
-            for (int base = row.lo; base < rest; base += CHUNK) {
+            for (int base = row.lo; base < staged; base += CHUNK) {
                 row.load_chunk(base, x);
                 soft_chunk<T, false>(st, x, Vec<T>::largest(x), c);
             }
-            if (!single) row.load_rest(rest, x);
+            if (!early) row.load_rest(rest, x);
             soft_chunk<T, false>(st, x, Vec<T>::largest(x), c);
+            if (staged < rest) {
+                cp_async_wait();
+#pragma unroll 1
+                for (int r = 0; r < VPT; r += 2) {
+                    const uint4 y[2] = {stage[r * NT + threadIdx.x], stage[(r + 1) * NT + threadIdx.x]};
+                    soft_chunk<T, false>(st, y, Vec<T>::largest(y), c);
+                }
+            }
         }
         // the leader's loss: (ln q - ln p) needs the student's logits at the
         // teacher's tokens, read before anything is written in place
-        constexpr int LPT = TPMLP_MAX_TEACHER / ROW_THREADS;
+        constexpr int LPT = (TPMLP_MAX_TEACHER + NT - 1) / NT;
         float zk[LPT];
         if (rank == 0 && live) {
 #pragma unroll
             for (int u = 0; u < LPT; ++u) {
-                const int k = threadIdx.x + u * ROW_THREADS;
+                const int k = threadIdx.x + u * NT;
                 if (k >= a.K) break;
                 const int id = ids[k];
                 zk[u] = id >= 0 && id < a.V ? to_f32(row.z[id]) : 0.f;
@@ -857,7 +890,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillAr
         if (split > 1) {
             cluster_wait();
             if (lane < split) {
-                const uint32_t at = mapa_shared(smem_u32(&parts[rank * ROW_WARPS + warp]), (uint32_t)lane);
+                const uint32_t at = mapa_shared(smem_u32(&parts[rank * WARPS + warp]), (uint32_t)lane);
                 asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(m), "f"(st.s) : "memory");
             }
             cluster_arrive();
@@ -866,16 +899,20 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillAr
             if (lane == 0) parts[warp] = WarpSoft{m, st.s};
             __syncthreads();
         }
-        const int total = split * ROW_WARPS;
-        WarpSoft p0 = lane < total ? parts[lane] : WarpSoft{kLowest, 0.f};
-        WarpSoft p1 = lane + 32 < total ? parts[lane + 32] : WarpSoft{kLowest, 0.f};
-        m = max_nan(p0.ref, p1.ref);
+        constexpr int PPL = MAX_SPLIT * WARPS / 32;   // parts a lane takes
+        const int total = split * WARPS;
+        WarpSoft part[PPL];
+        m = kLowest;
+#pragma unroll
+        for (int u = 0; u < PPL; ++u) {
+            part[u] = lane + 32 * u < total ? parts[lane + 32 * u] : WarpSoft{kLowest, 0.f};
+            m = max_nan(m, part[u].ref);
+        }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
-        Soft s0{p0.ref, p0.s, 0.f}, s1{p1.ref, p1.s, 0.f};
-        rebase(s0, m, c);
-        rebase(s1, m, c);
-        s0.s += s1.s;
+        Soft s0{m, 0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < PPL; ++u) s0.s = fmaf(part[u].s, ex2((part[u].ref - m) * c), s0.s);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) s0.s += __shfl_xor_sync(0xffffffffu, s0.s, off);
         dist = distribution(s0, c, 1.f / a.tau);
@@ -885,7 +922,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillAr
                 const float log2_sum = log2f(te.sum);
 #pragma unroll
                 for (int u = 0; u < LPT; ++u) {
-                    const int k = threadIdx.x + u * ROW_THREADS;
+                    const int k = threadIdx.x + u * NT;
                     if (k >= a.K) break;
                     if (ids[k] == -1) continue;
                     const float lq = (tl[k] - te.tm) * c - log2_sum;
@@ -917,7 +954,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillAr
     const float fill = te.bad ? NAN : 0.f;
     // the CTA's teacher tokens, from the logits as they are before the sweep;
     // slots of one id all get the row's full value
-    for (int k = threadIdx.x; k < te.n; k += ROW_THREADS) {
+    for (int k = threadIdx.x; k < te.n; k += NT) {
         const int id = te.id[k];
         float q = 0.f;
         for (int j = 0; j < te.n; ++j)
@@ -955,51 +992,60 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillAr
     }
     // Back to front: the last chunk is still in registers, what was read last is
     // the likeliest to be in L2.
-    if (live && !LOSS && !single) row.load_rest(rest, x);
+    if (live && !LOSS && !early) row.load_rest(rest, x);
 #pragma unroll
     for (int r = 0; r < VPT; ++r) {
-        const int i = rest + r * ROW_THREADS + (int)threadIdx.x;
+        const int i = rest + r * NT + (int)threadIdx.x;
         if (i < row.hi) {
             float v[Vec<T>::N];
             gradient(x[r], v);
             store(i, v);
         }
     }
-    for (int base = rest - CHUNK; base >= row.lo; base -= CHUNK) {
+    if (staged < rest) {
+#pragma unroll
+        for (int r = 0; r < VPT; ++r) {
+            float v[Vec<T>::N];
+            gradient(stage[r * NT + threadIdx.x], v);
+            store(staged + r * NT + (int)threadIdx.x, v);
+        }
+    }
+    for (int base = staged - CHUNK; base >= row.lo; base -= CHUNK) {
         if (live) row.load_chunk(base, x);
 #pragma unroll
         for (int r = 0; r < VPT; ++r) {
             float v[Vec<T>::N];
             gradient(x[r], v);
-            store(base + r * ROW_THREADS + (int)threadIdx.x, v);
+            store(base + r * NT + (int)threadIdx.x, v);
         }
     }
     __syncthreads();
-    for (int k = threadIdx.x; k < te.n; k += ROW_THREADS) d[te.id[k]] = from_f32<T>(te.fix[k]);
+    for (int k = threadIdx.x; k < te.n; k += NT) d[te.id[k]] = from_f32<T>(te.fix[k]);
 }
 
 // ---------------------------------------------------------------- launch --
 
-// CTAs per row, as a power of two. Few rows: enough CTAs to occupy the SMs twice over, while a
-// slice still has a vector for every thread. With `hold` the slice should
-// also fit the registers, so that the gradient needs no second read.
-int row_split(int64_t N, int64_t row_bytes, bool hold) {
+// CTAs per row, as a power of two. Few rows: enough CTAs to occupy the SMs
+// four times over, while a slice still has a vector for every thread. A
+// slice should also be no longer than `hold` vectors (0: any length).
+int row_split(int64_t N, int64_t row_bytes, int threads, int64_t hold) {
     const int64_t want = 4LL * device_sm_count();
     if (N * MAX_SPLIT > 0x7fffffffLL) return 0;
     int l = 0;
-    while ((1 << l) < MAX_SPLIT && (N << l) < want && (row_bytes >> (l + 1)) >= ROW_THREADS * 16) ++l;
-    if (hold && row_bytes + 32 <= (int64_t)MAX_SPLIT * CHUNK * 16)
-        while (((row_bytes + 32) >> l) > CHUNK * 16) ++l;
+    while ((1 << l) < MAX_SPLIT && (N << l) < want && (row_bytes >> (l + 1)) >= threads * 16) ++l;
+    while ((1 << l) < MAX_SPLIT && hold > 0 && (row_bytes >> l) > hold * 16) ++l;
     return l;
 }
 
 template <typename... P, typename... A>
-tpmlp_status launch_rows(void (*kernel)(P...), int64_t N, int log_split, cudaStream_t s, A... args) {
+tpmlp_status launch_rows(void (*kernel)(P...), int threads, size_t smem, int64_t N, int log_split,
+                         cudaStream_t s, A... args) {
     const int split = 1 << log_split;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3((unsigned)(N * split));
-    cfg.blockDim = dim3(ROW_THREADS);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     if (split > 1) {
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1009,6 +1055,9 @@ tpmlp_status launch_rows(void (*kernel)(P...), int64_t N, int log_split, cudaStr
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return TPMLP_ERR_CUDA;
     if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return TPMLP_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
 }
@@ -1017,18 +1066,22 @@ template <typename T>
 tpmlp_status distill_launch(const DistillArgs& a, cudaStream_t s, int* err) {
     const int64_t bytes = a.V * (int64_t)sizeof(T);
     if (a.dlogits == nullptr) {
-        const int split = row_split(a.N, bytes, false);
+        const int split = row_split(a.N, bytes, ROW_THREADS, 0);
         LaunchScope ls("vocab_distill", s);
-        return launch_rows(distill_kernel<T, true, false>, a.N, split, s, a, split, err);
+        return launch_rows(distill_kernel<T, ROW_THREADS, true, false>, ROW_THREADS, 0, a.N, split, s, a,
+                           split, err);
     }
     if (a.loss == nullptr) {
-        const int split = row_split(a.N, bytes, false);
+        const int split = row_split(a.N, bytes, ROW_THREADS, 0);
         LaunchScope ls("vocab_distill_backward", s);
-        return launch_rows(distill_kernel<T, false, true>, a.N, split, s, a, split, err);
+        return launch_rows(distill_kernel<T, ROW_THREADS, false, true>, ROW_THREADS, 0, a.N, split, s, a,
+                           split, err);
     }
-    const int split = row_split(a.N, bytes, true);
+    constexpr int CHUNK = Row<T, ROW_THREADS>::CHUNK;
+    const int split = row_split(a.N, bytes, ROW_THREADS, 2 * CHUNK);
     LaunchScope ls("vocab_distill_with_grad", s);
-    return launch_rows(distill_kernel<T, true, true>, a.N, split, s, a, split, err);
+    return launch_rows(distill_kernel<T, ROW_THREADS, true, true>, ROW_THREADS, CHUNK * sizeof(uint4), a.N,
+                       split, s, a, split, err);
 }
 
 }  // namespace
@@ -1037,10 +1090,10 @@ tpmlp_status run_vocab_logprobs(int f32, const LogprobArgs& a, cudaStream_t s) {
     if (a.N == 0) return TPMLP_OK;
     int* err = device_error_word();
     if (err == nullptr) return TPMLP_ERR_CUDA;
-    const int split = row_split(a.N, a.V * (f32 ? 4 : 2), false);
+    const int split = row_split(a.N, a.V * (f32 ? 4 : 2), ROW_THREADS, 0);
     LaunchScope ls("vocab_logprobs", s);
-    return f32 ? launch_rows(logprobs_kernel<float>, a.N, split, s, a, split, err)
-               : launch_rows(logprobs_kernel<__nv_bfloat16>, a.N, split, s, a, split, err);
+    return f32 ? launch_rows(logprobs_kernel<float>, ROW_THREADS, 0, a.N, split, s, a, split, err)
+               : launch_rows(logprobs_kernel<__nv_bfloat16>, ROW_THREADS, 0, a.N, split, s, a, split, err);
 }
 
 tpmlp_status run_vocab_distill(int f32, const DistillArgs& a, cudaStream_t s) {
