@@ -353,7 +353,7 @@ tpmlp_status tpmlp_vocab_distill_with_grad(tpmlp_dtype dt, int64_t N, int64_t V,
 
 /* tpmlp_vocab_embedding times a factor: out[n] = scale * table[ids[n]],
  * multiplied in fp32 and rounded once to dt. Arguments, shards and errors as
- * tpmlp_vocab_embedding. */
+ * tpmlp_vocab_embedding; V and Hd at most 2^31 - 1. */
 tpmlp_status tpmlp_vocab_embedding_scaled(tpmlp_dtype dt, int64_t N, int64_t V, int64_t Hd, int T,
                                           const int64_t* ids, const void* const* table,
                                           float scale, void* out, void* stream);

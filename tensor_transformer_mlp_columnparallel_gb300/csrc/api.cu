@@ -946,6 +946,7 @@ tpmlp_status tpmlp_vocab_embedding_scaled(tpmlp_dtype dt, int64_t N, int64_t V, 
     if (dt != TPMLP_F32 && dt != TPMLP_BF16) return TPMLP_ERR_DTYPE;
     if (N < 0) return TPMLP_ERR_ARG;
     if (V <= 0 || Hd <= 0 || T < 1 || T > TPMLP_MAX_SHARDS || V % T != 0) return TPMLP_ERR_SHAPE;
+    if (V > 0x7fffffffLL || Hd > 0x7fffffffLL) return TPMLP_ERR_SHAPE;
     if (N == 0) return TPMLP_OK;
     if (ids == nullptr || out == nullptr || table == nullptr) return TPMLP_ERR_ARG;
     for (int k = 0; k < T; ++k)

@@ -1,14 +1,20 @@
 // Embedding lookup times a factor, and the table's gradient by sorted tokens.
 //
-// Lookup: out[n] = c E[id_n]; a warp per token, one read and one write of the row.
+// Lookup: out[n] = c E[id_n], one read and one write of the row.
 // Gradient: dE[v] = c sum_{n: id_n = v} dout[n]. The tokens are sorted by id
-//   (stable, least significant digit first, RADIX_BITS a pass), which gives
-//   every table row a contiguous segment of tokens in rising order; each
-//   table row is then written once from its segment's fp32 sum. No
-//   floating-point atomics, so the bits are the same on every run.
+//   (stable, least significant digit first, RADIX_BITS a pass), so every table
+//   row has a contiguous segment of sorted positions, in token order. The
+//   positions are cut into blocks of SPAN. A segment inside one block is
+//   summed by the CTA that writes its table row. A segment that crosses
+//   blocks is summed block by block into fp32 pieces (at most two a block: the
+//   run that began earlier and the run that goes on), which are then added in
+//   order; so a token that fills half the batch is no one CTA's work. Sums
+//   are fp32, in an order that the ids alone decide: no floating-point atomics.
+//   What bounds it is the table: every row is written once, most as zeros.
 #include <cuda_bf16.h>
 
 #include "act.cuh"
+#include "ptx.cuh"
 #include "tpmlp_internal.h"
 
 namespace tpmlp {
@@ -23,6 +29,27 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
     return __float2bfloat16_rn(v);
 }
 
+// N consecutive elements moved as one access where N sizeof(T) is a vector
+// size (2, 4, 8 or 16 bytes), as two 16-byte ones for 32.
+template <typename T, int N>
+struct __align__(N * sizeof(T) < 16 ? N * sizeof(T) : 16) Pack {
+    T v[N];
+};
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> load_pack(const T* p) {
+    return *reinterpret_cast<const Pack<T, N>*>(p);
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_pack(T* p, const Pack<T, N>& x) {
+    constexpr int B = N * sizeof(T);
+    if constexpr (B == 16)
+        __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(&x));
+    else if constexpr (B == 8)
+        __stcs(reinterpret_cast<uint2*>(p), *reinterpret_cast<const uint2*>(&x));
+    else
+        *reinterpret_cast<Pack<T, N>*>(p) = x;
+}
+
 // ---------------------------------------------------------------- lookup --
 
 struct LookupArgs {
@@ -30,31 +57,56 @@ struct LookupArgs {
     const void* table[kMaxG];
     void* out;
     int64_t N, V, Vs, H;
+    int packs;        // packs of a row
+    int segs;         // CTAs of a row
+    int log_lanes;    // threads of a row within a CTA, as a power of two
     float scale;
     int* err;
 };
 
-template <typename T>
-__global__ void __launch_bounds__(256) embedding_scaled_kernel(const LookupArgs p) {
-    const int64_t n = blockIdx.x;
+constexpr int LOOKUP_THREADS = 256;
+constexpr int LOOKUP_UNROLL = 4;
+
+// A row is taken by 2^log_lanes threads, LOOKUP_UNROLL packs each, their loads
+// in flight together; short rows share a CTA, long ones take several.
+template <typename T, int N>
+__global__ void __launch_bounds__(LOOKUP_THREADS) embedding_scaled_kernel(const LookupArgs p) {
+    const int lanes = 1 << p.log_lanes;
+    const int64_t group = blockIdx.x / (unsigned)p.segs;
+    const int seg = (int)(blockIdx.x - (unsigned)group * (unsigned)p.segs);
+    const int64_t n = group * (LOOKUP_THREADS >> p.log_lanes) + ((int)threadIdx.x >> p.log_lanes);
+    if (n >= p.N) return;
+    const int lane = (int)threadIdx.x & (lanes - 1);
     const int64_t id = p.ids[n];
     const bool good = id >= 0 && id < p.V;
-    if (!good && threadIdx.x == 0) atomicCAS(p.err, 0, (int)TPMLP_ERR_ARG);
-    const int64_t k = good ? id / p.Vs : 0;
-    const T* src = good ? static_cast<const T*>(p.table[k]) + (id - k * p.Vs) * p.H : nullptr;
+    if (!good && lane == 0 && seg == 0) atomicCAS(p.err, 0, (int)TPMLP_ERR_ARG);
+    const uint32_t k = good ? (uint32_t)id / (uint32_t)p.Vs : 0u;
+    const T* src = static_cast<const T*>(p.table[k]) + (good ? (id - (int64_t)k * p.Vs) * p.H : 0);
     T* dst = static_cast<T*>(p.out) + n * p.H;
-    for (int64_t c = threadIdx.x; c < p.H; c += 256)
-        dst[c] = from_f32<T>(good ? p.scale * to_f32(src[c]) : 0.f);
+    const int c0 = seg * lanes * LOOKUP_UNROLL + lane;
+    Pack<T, N> x[LOOKUP_UNROLL];
+#pragma unroll
+    for (int u = 0; u < LOOKUP_UNROLL; ++u)
+        if (c0 + u * lanes < p.packs) x[u] = load_pack<T, N>(src + (int64_t)(c0 + u * lanes) * N);
+#pragma unroll
+    for (int u = 0; u < LOOKUP_UNROLL; ++u) {
+        if (c0 + u * lanes >= p.packs) break;
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[u].v[j] = from_f32<T>(good ? p.scale * to_f32(x[u].v[j]) : 0.f);
+        store_pack<T, N>(dst + (int64_t)(c0 + u * lanes) * N, x[u]);
+    }
 }
 
 // ------------------------------------------------------------------ sort --
 
 constexpr int RADIX_BITS = 9;
 constexpr int BINS = 1 << RADIX_BITS;
-constexpr int SORT_THREADS = 512;
-constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int SORT_ROUNDS = 8;                               // tokens per lane
-constexpr int SORT_TILE = SORT_THREADS * SORT_ROUNDS;        // tokens per CTA
+constexpr int SORT_THREADS = 512;                            // of the sort over several CTAs
+constexpr int SORT_TILE = SORT_THREADS * SORT_ROUNDS;        // its tokens per CTA
+constexpr int ONE_THREADS = 1024;                            // of the sort in one CTA
+constexpr int ONE_MAX = ONE_THREADS * SORT_ROUNDS;           // its tokens at most
+constexpr int ONE_SMEM = (ONE_THREADS / 32) * BINS * 4 + ONE_MAX * 8;
 static_assert(SORT_THREADS == BINS, "one thread per digit");
 
 struct SortArgs {
@@ -62,20 +114,125 @@ struct SortArgs {
     const uint2* in;        // later passes: (key, token)
     uint2* out;
     int* hist;              // [CTAs][BINS]
+    int2* seg;              // zeroed beside the first pass
     int64_t N, V;
-    int shift;
+    int shift, bits;
     int* err;
 };
 
-// Pair of sorted position i before this pass. An id outside [0, V) gets key V
+// Pair of position i before the first pass. An id outside [0, V) gets key V
 // and lands behind every row's segment.
-__device__ __forceinline__ uint2 sort_item(const SortArgs& p, int64_t i) {
-    if (p.ids == nullptr) return p.in[i];
+__device__ __forceinline__ uint2 first_pair(const SortArgs& p, int64_t i) {
     const int64_t id = p.ids[i];
-    return make_uint2(id >= 0 && id < p.V ? (uint32_t)id : (uint32_t)p.V, (uint32_t)i);
+    const bool good = id >= 0 && id < p.V;
+    if (!good) atomicCAS(p.err, 0, (int)TPMLP_ERR_ARG);
+    return make_uint2(good ? (uint32_t)id : (uint32_t)p.V, (uint32_t)i);
+}
+__device__ __forceinline__ uint2 sort_pair(const SortArgs& p, int64_t i) {
+    return p.ids == nullptr ? p.in[i] : first_pair(p, i);
 }
 
-__global__ void __launch_bounds__(SORT_THREADS) sort_hist_kernel(const SortArgs p) {
+__device__ __forceinline__ void zero_segments(const SortArgs& p, int first, int ctas) {
+    for (int64_t v = (int64_t)(blockIdx.x - first) * blockDim.x + threadIdx.x; v < p.V;
+         v += (int64_t)ctas * blockDim.x)
+        p.seg[v] = make_int2(0, 0);
+}
+
+// Ranks of a warp's 32 x SORT_ROUNDS consecutive pairs within their digits: lanes
+// with one digit rank themselves by lane, behind the warp's count so far.
+__device__ __forceinline__ void warp_ranks(const uint2 (&item)[SORT_ROUNDS], const bool (&in)[SORT_ROUNDS],
+                                           int shift, int* cnt, int (&rank)[SORT_ROUNDS]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int r = 0; r < SORT_ROUNDS; ++r) {
+        const uint32_t digit = in[r] ? (item[r].x >> shift) & (BINS - 1) : (uint32_t)BINS;
+        const uint32_t peers = __match_any_sync(0xffffffffu, digit);
+        const int mine = __popc(peers & ((1u << lane) - 1u));
+        const int seen = in[r] ? cnt[digit] : 0;
+        rank[r] = seen + mine;
+        __syncwarp();
+        if (in[r] && mine == 0) cnt[digit] = seen + __popc(peers);
+        __syncwarp();
+    }
+}
+
+// Exclusive scan of one value a thread over the first BINS threads.
+__device__ __forceinline__ int scan_bins(int x, int* warp_sum) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int inc = x;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += y;
+    }
+    if (threadIdx.x < BINS && lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    int start = inc - x;
+    if (threadIdx.x < BINS)
+        for (int w = 0; w < warp; ++w) start += warp_sum[w];
+    return start;
+}
+
+// All passes in one CTA (N <= ONE_MAX), the pairs in registers and exchanged
+// through shared memory; the other CTAs zero the segments.
+__global__ void __launch_bounds__(ONE_THREADS) sort_one_kernel(const SortArgs p) {
+    pdl_wait();
+    pdl_launch_dependents();
+    if (blockIdx.x > 0) {
+        zero_segments(p, 1, (int)gridDim.x - 1);
+        return;
+    }
+    extern __shared__ uint2 exchange[];   // [ONE_MAX], then the warps' counts
+    int* cnt = reinterpret_cast<int*>(exchange + ONE_MAX);
+    __shared__ int warp_sum[BINS / 32];
+    const int warp = threadIdx.x >> 5;
+    const int base = warp * 32 * SORT_ROUNDS + (threadIdx.x & 31);
+    uint2 item[SORT_ROUNDS];
+    bool in[SORT_ROUNDS];
+    int rank[SORT_ROUNDS];
+#pragma unroll
+    for (int r = 0; r < SORT_ROUNDS; ++r) {
+        in[r] = base + r * 32 < p.N;
+        item[r] = in[r] ? first_pair(p, base + r * 32) : make_uint2(0u, 0u);
+    }
+    for (int shift = 0; shift < p.bits; shift += RADIX_BITS) {
+        for (int i = threadIdx.x; i < (ONE_THREADS / 32) * BINS; i += ONE_THREADS) cnt[i] = 0;
+        __syncthreads();
+        warp_ranks(item, in, shift, cnt + warp * BINS, rank);
+        __syncthreads();
+        int total = 0;
+        if (threadIdx.x < BINS)
+#pragma unroll 8
+            for (int w = 0; w < ONE_THREADS / 32; ++w) {   // each warp's first place within the digit
+                const int c = cnt[w * BINS + threadIdx.x];
+                cnt[w * BINS + threadIdx.x] = total;
+                total += c;
+            }
+        const int start = scan_bins(total, warp_sum);
+        if (threadIdx.x < BINS)
+#pragma unroll 8
+            for (int w = 0; w < ONE_THREADS / 32; ++w) cnt[w * BINS + threadIdx.x] += start;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < SORT_ROUNDS; ++r)
+            if (in[r]) exchange[cnt[warp * BINS + ((item[r].x >> shift) & (BINS - 1))] + rank[r]] = item[r];
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < SORT_ROUNDS; ++r)
+            if (in[r]) item[r] = exchange[base + r * 32];
+    }
+#pragma unroll
+    for (int r = 0; r < SORT_ROUNDS; ++r)
+        if (in[r]) p.out[base + r * 32] = item[r];
+}
+
+__global__ void __launch_bounds__(SORT_THREADS) sort_hist_kernel(const SortArgs p, int ctas) {
+    pdl_wait();
+    pdl_launch_dependents();
+    if ((int)blockIdx.x >= ctas) {   // first pass: the rest of the grid
+        zero_segments(p, ctas, (int)gridDim.x - ctas);
+        return;
+    }
     __shared__ int cnt[BINS];
     cnt[threadIdx.x] = 0;
     __syncthreads();
@@ -83,118 +240,263 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_hist_kernel(const SortArgs 
     for (int r = 0; r < SORT_ROUNDS; ++r) {
         const int64_t i = base + r * SORT_THREADS + threadIdx.x;
         if (i >= p.N) break;
-        const uint32_t key = sort_item(p, i).x;
-        if (p.ids != nullptr && key == (uint32_t)p.V) atomicCAS(p.err, 0, (int)TPMLP_ERR_ARG);
-        atomicAdd(&cnt[(key >> p.shift) & (BINS - 1)], 1);
+        atomicAdd(&cnt[(sort_pair(p, i).x >> p.shift) & (BINS - 1)], 1);
     }
     __syncthreads();
     p.hist[(int64_t)blockIdx.x * BINS + threadIdx.x] = cnt[threadIdx.x];
 }
 
-// Stable: a warp takes 32 x SORT_ROUNDS consecutive tokens, 32 at a time; lanes
-// with one digit rank themselves by lane (match), behind the warp's count of
-// earlier rounds; then warps, CTAs and digits follow in order.
+// Stable: a pair goes behind every smaller digit, its digit in earlier CTAs, in
+// earlier warps, and in its warp's earlier pairs.
 __global__ void __launch_bounds__(SORT_THREADS) sort_scatter_kernel(const SortArgs p) {
-    __shared__ int cnt[SORT_WARPS][BINS];
-    __shared__ int scan[SORT_WARPS];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int w = 0; w < SORT_WARPS; ++w) cnt[w][threadIdx.x] = 0;
-    // digit threadIdx.x: all its tokens, and those in CTAs before this one
+    pdl_wait();
+    pdl_launch_dependents();
+    constexpr int WARPS = SORT_THREADS / 32;
+    __shared__ int cnt[WARPS][BINS];
+    __shared__ int warp_sum[BINS / 32];
+    const int warp = threadIdx.x >> 5;
+    for (int w = 0; w < WARPS; ++w) cnt[w][threadIdx.x] = 0;
+    // digit threadIdx.x: all its pairs, and those in CTAs before this one
     int total = 0, before = 0;
     for (int b = 0; b < (int)gridDim.x; ++b) {
         const int h = p.hist[(int64_t)b * BINS + threadIdx.x];
         total += h;
         if (b < (int)blockIdx.x) before += h;
     }
-    int inc = total;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, inc, off);
-        if (lane >= off) inc += x;
-    }
-    if (lane == 31) scan[warp] = inc;
-    __syncthreads();
-    int start = inc - total + before;
-    for (int w = 0; w < warp; ++w) start += scan[w];
+    int start = scan_bins(total, warp_sum) + before;
 
-    const int64_t base = (int64_t)blockIdx.x * SORT_TILE + warp * (32 * SORT_ROUNDS);
+    const int64_t base = (int64_t)blockIdx.x * SORT_TILE + warp * (32 * SORT_ROUNDS) + (threadIdx.x & 31);
     uint2 item[SORT_ROUNDS];
+    bool in[SORT_ROUNDS];
     int rank[SORT_ROUNDS];
 #pragma unroll
     for (int r = 0; r < SORT_ROUNDS; ++r) {
-        const int64_t i = base + r * 32 + lane;
-        const bool in = i < p.N;
-        item[r] = in ? sort_item(p, i) : make_uint2(0u, 0u);
-        const uint32_t digit = in ? (item[r].x >> p.shift) & (BINS - 1) : (uint32_t)BINS;
-        const uint32_t peers = __match_any_sync(0xffffffffu, digit);
-        const int mine = __popc(peers & ((1u << lane) - 1u));
-        const int seen = in ? cnt[warp][digit] : 0;
-        rank[r] = seen + mine;
-        __syncwarp();
-        if (in && mine == 0) cnt[warp][digit] = seen + __popc(peers);
-        __syncwarp();
+        in[r] = base + r * 32 < p.N;
+        item[r] = in[r] ? sort_pair(p, base + r * 32) : make_uint2(0u, 0u);
     }
+    warp_ranks(item, in, p.shift, cnt[warp], rank);
     __syncthreads();
-    for (int w = 0; w < SORT_WARPS; ++w) {   // digit threadIdx.x: each warp's first place
+    for (int w = 0; w < WARPS; ++w) {   // digit threadIdx.x: each warp's first place
         const int c = cnt[w][threadIdx.x];
         cnt[w][threadIdx.x] = start;
         start += c;
     }
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < SORT_ROUNDS; ++r) {
-        const int64_t i = base + r * 32 + lane;
-        if (i < p.N) p.out[cnt[warp][(item[r].x >> p.shift) & (BINS - 1)] + rank[r]] = item[r];
-    }
-}
-
-// seg[v] = [first, last + 1) of row v's tokens in sorted order ({0, 0}: none)
-__global__ void __launch_bounds__(256) segment_kernel(const uint2* sorted, int64_t N, int64_t V, int2* seg) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= N) return;
-    const uint32_t key = sorted[i].x;
-    if (key >= (uint32_t)V) return;
-    if (i == 0 || sorted[i - 1].x != key) seg[key].x = (int)i;
-    if (i == N - 1 || sorted[i + 1].x != key) seg[key].y = (int)i + 1;
+    for (int r = 0; r < SORT_ROUNDS; ++r)
+        if (in[r]) p.out[cnt[warp][(item[r].x >> p.shift) & (BINS - 1)] + rank[r]] = item[r];
 }
 
 // -------------------------------------------------------------- gradient --
 
+constexpr int SPAN = 32;          // sorted positions of a block
+constexpr int GRAD_THREADS = 256;
+constexpr int GRAD_WARPS = GRAD_THREADS / 32;
+constexpr int GRAD_ROWS = 8;      // table rows of a CTA
+constexpr int JOIN_COLS = 128;    // columns of a CTA that joins pieces
+
 struct GradArgs {
     const uint2* sorted;
-    const int2* seg;
+    int2* seg;                    // [V): a row's sorted positions {first, last + 1}; {0, 0}: none
     const void* dout;
     void* dtable[kMaxG];
-    int64_t V, Vs, H;
+    float* pieces;                // [2 blocks][Hp]
+    int64_t N, V, Vs, H, Hp;
+    int blocks;                   // of SPAN positions
+    int packs;                    // packs of a row
+    int join_cols;                // CTAs per block that join pieces
     float scale;
     int accumulate;
 };
 
-template <typename T, typename GT>
-__global__ void __launch_bounds__(256) embedding_grad_kernel(const GradArgs p) {
-    const int64_t v = blockIdx.x;
-    const int2 sg = p.seg[v];
-    if (p.accumulate && sg.y == sg.x) return;
-    const int64_t k = v / p.Vs;
-    GT* dst = static_cast<GT*>(p.dtable[k]) + (v - k * p.Vs) * p.H;
-    for (int64_t c = threadIdx.x; c < p.H; c += 256) {
-        float acc = 0.f;
-        for (int i = sg.x; i < sg.y; ++i)
-            acc += to_f32(static_cast<const T*>(p.dout)[(int64_t)p.sorted[i].y * p.H + c]);
-        acc *= p.scale;
-        if (p.accumulate) acc += to_f32(dst[c]);
-        dst[c] = from_f32<GT>(acc);
+template <typename T, int N>
+__device__ __forceinline__ void add_rows(const GradArgs& p, const uint32_t* tok, int n, int64_t col,
+                                         float (&acc)[N]) {
+    const T* base = static_cast<const T*>(p.dout) + col;
+    int i = 0;
+    for (; i + 4 <= n; i += 4) {   // four rows in flight, added in order
+        Pack<T, N> x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = load_pack<T, N>(base + (int64_t)tok[i + u] * p.H);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int j = 0; j < N; ++j) acc[j] += to_f32(x[u].v[j]);
+    }
+    for (; i < n; ++i) {
+        const Pack<T, N> x = load_pack<T, N>(base + (int64_t)tok[i] * p.H);
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[j] += to_f32(x.v[j]);
+    }
+}
+
+// Segments' ends, and the pieces of segments that cross blocks. Block b of
+// SPAN sorted positions: piece 2 b is the run that began in an earlier block,
+// piece 2 b + 1 the run that goes on into the next (and began here).
+template <typename T, int N>
+__global__ void __launch_bounds__(GRAD_THREADS) embedding_grad_pieces_kernel(const GradArgs p) {
+    pdl_wait();
+    pdl_launch_dependents();
+    __shared__ uint32_t key[SPAN + 2];   // with the neighbours on either side
+    __shared__ uint32_t tok[SPAN];
+    const int b = (int)blockIdx.x;
+    const int64_t first = (int64_t)b * SPAN;
+    const int n = (int)min((int64_t)SPAN, p.N - first);
+    const uint32_t none = 0xffffffffu;
+    for (int i = threadIdx.x; i < n + 2; i += GRAD_THREADS) {
+        const int64_t at = first + i - 1;
+        const uint2 x = at >= 0 && at < p.N ? p.sorted[at] : make_uint2(none, 0u);
+        key[i] = x.x;
+        if (i >= 1 && i <= n) tok[i - 1] = x.y;
+    }
+    __syncthreads();
+    if (blockIdx.y == 0 && (int)threadIdx.x < n) {
+        const int i = (int)threadIdx.x;
+        const uint32_t k = key[i + 1];
+        if (k < (uint32_t)p.V) {
+            if (key[i] != k) p.seg[k].x = (int)(first + i);
+            if (key[i + 2] != k) p.seg[k].y = (int)(first + i) + 1;
+        }
+    }
+    int head = 0, tail = n;   // the two runs: [0, head) and [tail, n)
+    if (key[0] == key[1] && key[1] < (uint32_t)p.V)
+        while (head < n && key[head + 1] == key[0]) ++head;
+    if (n == SPAN && key[n + 1] == key[n] && key[n] < (uint32_t)p.V)
+        while (tail > head && key[tail] == key[n + 1]) --tail;
+    const int c = (int)(blockIdx.y * GRAD_THREADS + threadIdx.x);
+    if (c >= p.packs) return;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+        const int lo = side ? tail : 0, hi = side ? n : head;
+        if (lo >= hi) continue;
+        float acc[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[j] = 0.f;
+        add_rows<T, N>(p, tok + lo, hi - lo, (int64_t)c * N, acc);
+        float* dst = p.pieces + (int64_t)(2 * b + side) * p.Hp + (int64_t)c * N;
+#pragma unroll
+        for (int j = 0; j < N; ++j) dst[j] = acc[j];
+    }
+}
+
+template <typename GT>
+__device__ __forceinline__ GT* table_row(const GradArgs& p, uint32_t v) {
+    const uint32_t k = v / (uint32_t)p.Vs;
+    return static_cast<GT*>(p.dtable[k]) + (int64_t)(v - k * (uint32_t)p.Vs) * p.H;
+}
+
+// Table rows from segments inside one block of positions (zeros where there is
+// none), and, in the grid's first CTAs, from the pieces of the others.
+template <typename T, int N, typename GT, int ZN>
+__global__ void __launch_bounds__(GRAD_THREADS) embedding_grad_kernel(const GradArgs p) {
+    pdl_wait();
+    __shared__ float4 part[GRAD_WARPS][32];
+    __shared__ int2 segs[GRAD_ROWS];
+    __shared__ uint32_t tok[GRAD_ROWS][SPAN];
+    const unsigned joins = (unsigned)p.blocks * (unsigned)p.join_cols;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (blockIdx.x < joins) {
+        // the segment that begins in block b and goes on
+        const int b = (int)(blockIdx.x / (unsigned)p.join_cols);
+        const int64_t next = (int64_t)(b + 1) * SPAN;
+        if (next >= p.N) return;
+        const uint32_t key = p.sorted[next].x;
+        if (key >= (uint32_t)p.V) return;
+        const int2 sg = p.seg[key];
+        if (sg.x / SPAN != b) return;
+        const int last = (sg.y - 1) / SPAN;
+        const int count = last - b + 1;
+        const int64_t col = (int64_t)(blockIdx.x - (unsigned)b * (unsigned)p.join_cols) * JOIN_COLS + lane * 4;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (col < p.Hp) {
+            const int lo = (int)((int64_t)count * warp / GRAD_WARPS), hi = (int)((int64_t)count * (warp + 1) / GRAD_WARPS);
+#pragma unroll 4
+            for (int i = lo; i < hi; ++i) {
+                const int64_t slot = 2 * (int64_t)(b + i) + (i == 0 ? 1 : 0);
+                const float4 x = *reinterpret_cast<const float4*>(p.pieces + slot * p.Hp + col);
+                acc.x += x.x;
+                acc.y += x.y;
+                acc.z += x.z;
+                acc.w += x.w;
+            }
+        }
+        part[warp][lane] = acc;
+        __syncthreads();
+        if (warp == 0 && col < p.Hp) {
+            for (int w = 1; w < GRAD_WARPS; ++w) {
+                const float4 x = part[w][lane];
+                acc.x += x.x;
+                acc.y += x.y;
+                acc.z += x.z;
+                acc.w += x.w;
+            }
+            GT* dst = table_row<GT>(p, key) + col;
+            const float v[4] = {acc.x, acc.y, acc.z, acc.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (col + j < p.H)
+                    dst[j] = from_f32<GT>(p.accumulate ? fmaf(p.scale, v[j], to_f32(dst[j])) : p.scale * v[j]);
+        }
+        return;
+    }
+    const int64_t v0 = (int64_t)(blockIdx.x - joins) * GRAD_ROWS;
+    if (threadIdx.x < GRAD_ROWS)
+        segs[threadIdx.x] = p.N > 0 && v0 + threadIdx.x < p.V ? p.seg[v0 + threadIdx.x] : make_int2(0, 0);
+    __syncthreads();
+    {   // a warp per row: the row's tokens
+        const int2 sg = segs[warp];
+        if (sg.y - sg.x > lane && sg.x / SPAN == (sg.y - 1) / SPAN) tok[warp][lane] = p.sorted[sg.x + lane].y;
+    }
+    __syncthreads();
+    for (int r = 0; r < GRAD_ROWS; ++r) {
+        if (v0 + r >= p.V) break;
+        const int2 sg = segs[r];
+        const int n = sg.y - sg.x;
+        if (n == 0 && p.accumulate) continue;
+        if (n > 0 && sg.x / SPAN != (sg.y - 1) / SPAN) continue;   // joined from pieces
+        GT* dst = table_row<GT>(p, (uint32_t)(v0 + r));
+        if (n == 0) {
+            Pack<GT, ZN> zero;
+#pragma unroll
+            for (int j = 0; j < ZN; ++j) zero.v[j] = from_f32<GT>(0.f);
+            const int packs = (int)(p.H / ZN);
+#pragma unroll 4
+            for (int c = threadIdx.x; c < packs; c += GRAD_THREADS) store_pack<GT, ZN>(dst + (int64_t)c * ZN, zero);
+            continue;
+        }
+        for (int c = threadIdx.x; c < p.packs; c += GRAD_THREADS) {
+            float acc[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) acc[j] = 0.f;
+            add_rows<T, N>(p, tok[r], n, (int64_t)c * N, acc);
+            GT* at = dst + (int64_t)c * N;
+            Pack<GT, N> o;
+            if (p.accumulate) o = load_pack<GT, N>(at);
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                o.v[j] = from_f32<GT>(p.accumulate ? fmaf(p.scale, acc[j], to_f32(o.v[j])) : p.scale * acc[j]);
+            if constexpr (N * sizeof(GT) == 32) {
+                const uint4* w = reinterpret_cast<const uint4*>(&o);
+                __stcs(reinterpret_cast<uint4*>(at), w[0]);
+                __stcs(reinterpret_cast<uint4*>(at) + 1, w[1]);
+            } else {
+                store_pack<GT, N>(at, o);
+            }
+        }
     }
 }
 
 inline size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 inline int64_t sort_ctas(int64_t N) { return (N + SORT_TILE - 1) / SORT_TILE; }
+inline int64_t grad_blocks(int64_t N) { return (N + SPAN - 1) / SPAN; }
+inline int64_t piece_pitch(int64_t H) { return (H + 3) / 4 * 4; }
 
-// Workspace: two arrays of (key, token) pairs, the digit counts, the segments.
+// Workspace: two arrays of (key, token) pairs, the digit counts, the segments,
+// the pieces.
 struct GradLayout {
-    size_t pairs[2], hist, seg, total;
+    size_t pairs[2], hist, seg, pieces, total;
 };
-GradLayout grad_layout(int64_t N, int64_t V) {
+GradLayout grad_layout(int64_t N, int64_t V, int64_t H) {
     GradLayout l;
     size_t o = 0;
     l.pairs[0] = o;
@@ -205,8 +507,76 @@ GradLayout grad_layout(int64_t N, int64_t V) {
     o += round256((size_t)sort_ctas(N) * BINS * sizeof(int));
     l.seg = o;
     o += round256((size_t)V * sizeof(int2));
+    l.pieces = o;
+    o += round256((size_t)(2 * grad_blocks(N)) * piece_pitch(H) * sizeof(float));
     l.total = o;
     return l;
+}
+
+// Elements per access that pointers of `align` bytes' alignment and rows of H
+// elements of `size` bytes allow, up to 16 bytes.
+int pack_elems(uintptr_t align, int64_t H, int size) {
+    int n = 16 / size;
+    while (n > 1 && (H % n != 0 || align % (uintptr_t)(n * size) != 0)) n /= 2;
+    return n;
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename T, int N, typename GT, int ZN>
+cudaError_t grad_launch(const GradArgs& g, cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
+    if (g.N > 0) {
+        LaunchScope ls("embedding_grad_pieces", s);
+        e = launch_pdl(embedding_grad_pieces_kernel<T, N>,
+                       dim3((unsigned)g.blocks, (unsigned)((g.packs + GRAD_THREADS - 1) / GRAD_THREADS)),
+                       GRAD_THREADS, 0, s, g);
+    }
+    if (e != cudaSuccess) return e;
+    LaunchScope ls("embedding_grad", s);
+    const int64_t grid = (int64_t)g.blocks * g.join_cols + (g.V + GRAD_ROWS - 1) / GRAD_ROWS;
+    return launch_pdl(embedding_grad_kernel<T, N, GT, ZN>, dim3((unsigned)grid), GRAD_THREADS, 0, s, g);
+}
+
+template <typename T, typename GT>
+cudaError_t grad_dispatch(const GradArgs& g, int n, int zn, cudaStream_t s) {
+    constexpr int Z = 16 / (int)sizeof(GT);
+    if (n == 8) {
+        if constexpr (sizeof(T) == 2) return grad_launch<T, 8, GT, Z>(g, s);
+    }
+    if (n == 4) return zn == Z ? grad_launch<T, 4, GT, Z>(g, s) : grad_launch<T, 4, GT, 4>(g, s);
+    if (n == 2) return grad_launch<T, 2, GT, 2>(g, s);
+    return grad_launch<T, 1, GT, 1>(g, s);
+}
+
+template <typename T>
+cudaError_t lookup_dispatch(const LookupArgs& p, int n, unsigned grid, cudaStream_t s) {
+    if (n == 8) {
+        if constexpr (sizeof(T) == 2) {
+            embedding_scaled_kernel<T, 8><<<grid, LOOKUP_THREADS, 0, s>>>(p);
+            return cudaGetLastError();
+        }
+    }
+    if (n >= 4)
+        embedding_scaled_kernel<T, 4><<<grid, LOOKUP_THREADS, 0, s>>>(p);
+    else if (n == 2)
+        embedding_scaled_kernel<T, 2><<<grid, LOOKUP_THREADS, 0, s>>>(p);
+    else
+        embedding_scaled_kernel<T, 1><<<grid, LOOKUP_THREADS, 0, s>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -215,100 +585,129 @@ tpmlp_status run_vocab_embedding_scaled(int f32, int64_t N, int64_t V, int64_t H
                                         const int64_t* ids, const void* const* table, float scale,
                                         void* out, cudaStream_t s) {
     if (N == 0) return TPMLP_OK;
-    if (N > 0x7fffffffLL) return TPMLP_ERR_SHAPE;
     LookupArgs p{};
+    const int size = f32 ? 4 : 2;
+    uintptr_t align = reinterpret_cast<uintptr_t>(out);
     p.ids = ids;
-    for (int k = 0; k < T; ++k) p.table[k] = table[k];
+    for (int k = 0; k < T; ++k) {
+        p.table[k] = table[k];
+        align |= reinterpret_cast<uintptr_t>(table[k]);
+    }
+    const int n = pack_elems(align, H, size);
     p.out = out;
     p.N = N;
     p.V = V;
     p.Vs = V / T;
     p.H = H;
+    p.packs = (int)(H / n);
+    p.log_lanes = 5;   // at least a warp a row
+    while ((1 << p.log_lanes) < LOOKUP_THREADS && (LOOKUP_UNROLL << p.log_lanes) < p.packs) ++p.log_lanes;
+    p.segs = (p.packs + (LOOKUP_UNROLL << p.log_lanes) - 1) / (LOOKUP_UNROLL << p.log_lanes);
     p.scale = scale;
     p.err = device_error_word();
     if (p.err == nullptr) return TPMLP_ERR_CUDA;
+    const int64_t rows = LOOKUP_THREADS >> p.log_lanes;
+    const int64_t grid = (N + rows - 1) / rows * p.segs;
+    if (grid > 0x7fffffffLL) return TPMLP_ERR_SHAPE;
+    cudaError_t e;
     {
         LaunchScope ls("vocab_embedding_scaled", s);
-        if (f32)
-            embedding_scaled_kernel<float><<<(unsigned)N, 256, 0, s>>>(p);
-        else
-            embedding_scaled_kernel<__nv_bfloat16><<<(unsigned)N, 256, 0, s>>>(p);
+        e = f32 ? lookup_dispatch<float>(p, n, (unsigned)grid, s)
+                : lookup_dispatch<__nv_bfloat16>(p, n, (unsigned)grid, s);
     }
-    return cudaGetLastError() == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
+    return e == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
 }
 
-size_t embedding_grad_bytes(int64_t N, int64_t V, int64_t H) {
-    (void)H;
-    return grad_layout(N, V).total;
-}
+size_t embedding_grad_bytes(int64_t N, int64_t V, int64_t H) { return grad_layout(N, V, H).total; }
 
 tpmlp_status run_vocab_embedding_backward(int f32, int grad_f32, int64_t N, int64_t V, int64_t H,
                                           int T, const int64_t* ids, const void* dout, float scale,
                                           int accumulate, void* const* dtable, void* workspace,
                                           cudaStream_t s) {
-    const GradLayout l = grad_layout(N, V);
+    if (N == 0 && accumulate) return TPMLP_OK;
+    const GradLayout l = grad_layout(N, V, H);
     char* ws = static_cast<char*>(workspace);
-    int2* seg = reinterpret_cast<int2*>(ws + l.seg);
     int* err = device_error_word();
     if (err == nullptr) return TPMLP_ERR_CUDA;
-    if (N == 0 && accumulate) return TPMLP_OK;
-    {
-        LaunchScope ls("embedding_grad_sort", s);
-        if (cudaMemsetAsync(seg, 0, (size_t)V * sizeof(int2), s) != cudaSuccess) return TPMLP_ERR_CUDA;
-    }
-    const uint2* sorted = nullptr;
+    GradArgs g{};
+    g.seg = reinterpret_cast<int2*>(ws + l.seg);
     if (N > 0) {
-        int bits = 1;
-        while ((V >> bits) != 0) ++bits;   // keys 0..V
         SortArgs p{};
         p.ids = ids;
         p.hist = reinterpret_cast<int*>(ws + l.hist);
+        p.seg = g.seg;
         p.N = N;
         p.V = V;
+        p.bits = 1;
+        while ((V >> p.bits) != 0) ++p.bits;   // keys 0..V
         p.err = err;
-        int which = 0;
-        for (p.shift = 0; p.shift < bits; p.shift += RADIX_BITS) {
-            p.out = reinterpret_cast<uint2*>(ws + l.pairs[which]);
-            const unsigned g = (unsigned)sort_ctas(N);
-            {
-                LaunchScope ls("embedding_grad_sort", s);
-                sort_hist_kernel<<<g, SORT_THREADS, 0, s>>>(p);
+        if (N <= ONE_MAX) {
+            // one launch for all passes
+            p.out = reinterpret_cast<uint2*>(ws + l.pairs[0]);
+            if (cudaFuncSetAttribute(sort_one_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ONE_SMEM) !=
+                cudaSuccess)
+                return TPMLP_ERR_CUDA;
+            const unsigned zero_ctas = (unsigned)(V / (ONE_THREADS * 4) + 1 < 64 ? V / (ONE_THREADS * 4) + 1 : 64);
+            LaunchScope ls("embedding_grad_sort", s);
+            if (launch_pdl(sort_one_kernel, dim3(1 + zero_ctas), ONE_THREADS, ONE_SMEM, s, p) != cudaSuccess)
+                return TPMLP_ERR_CUDA;
+            g.sorted = p.out;
+        } else {
+            const int ctas = (int)sort_ctas(N);
+            int which = 0;
+            for (p.shift = 0; p.shift < p.bits; p.shift += RADIX_BITS) {
+                p.out = reinterpret_cast<uint2*>(ws + l.pairs[which]);
+                {
+                    LaunchScope ls("embedding_grad_sort", s);
+                    if (launch_pdl(sort_hist_kernel, dim3((unsigned)(ctas + (p.shift == 0 ? 64 : 0))),
+                                   SORT_THREADS, 0, s, p, ctas) != cudaSuccess)
+                        return TPMLP_ERR_CUDA;
+                }
+                {
+                    LaunchScope ls("embedding_grad_sort", s);
+                    if (launch_pdl(sort_scatter_kernel, dim3((unsigned)ctas), SORT_THREADS, 0, s, p) != cudaSuccess)
+                        return TPMLP_ERR_CUDA;
+                }
+                g.sorted = p.out;
+                p.ids = nullptr;
+                p.in = p.out;
+                which ^= 1;
             }
-            {
-                LaunchScope ls("embedding_grad_sort", s);
-                sort_scatter_kernel<<<g, SORT_THREADS, 0, s>>>(p);
-            }
-            sorted = p.out;
-            p.ids = nullptr;
-            p.in = p.out;
-            which ^= 1;
         }
-        LaunchScope ls("embedding_grad_sort", s);
-        segment_kernel<<<(unsigned)((N + 255) / 256), 256, 0, s>>>(sorted, N, V, seg);
     }
-    GradArgs g{};
-    g.sorted = sorted;
-    g.seg = seg;
+    uintptr_t in_align = reinterpret_cast<uintptr_t>(dout), out_align = 0;
+    for (int k = 0; k < T; ++k) {
+        g.dtable[k] = dtable[k];
+        out_align |= reinterpret_cast<uintptr_t>(dtable[k]);
+    }
+    // the same elements per access on both sides (a bf16 pack of 8 is two
+    // 16-byte stores of fp32)
+    const int gsize = grad_f32 ? 4 : 2;
+    const int zn = pack_elems(out_align, H, gsize);
+    int n = pack_elems(in_align, H, f32 ? 4 : 2);
+    if (n > zn && !(n == 8 && zn == 4 && grad_f32)) n = zn;
     g.dout = dout;
-    for (int k = 0; k < T; ++k) g.dtable[k] = dtable[k];
+    g.pieces = reinterpret_cast<float*>(ws + l.pieces);
+    g.N = N;
     g.V = V;
     g.Vs = V / T;
     g.H = H;
+    g.Hp = piece_pitch(H);
+    g.blocks = (int)grad_blocks(N);
+    g.packs = (int)(H / n);
+    g.join_cols = (int)((H + JOIN_COLS - 1) / JOIN_COLS);
     g.scale = scale;
     g.accumulate = accumulate;
-    {
-        LaunchScope ls("embedding_grad", s);
-        const unsigned grid = (unsigned)V;
-        if (f32 && grad_f32)
-            embedding_grad_kernel<float, float><<<grid, 256, 0, s>>>(g);
-        else if (f32)
-            embedding_grad_kernel<float, __nv_bfloat16><<<grid, 256, 0, s>>>(g);
-        else if (grad_f32)
-            embedding_grad_kernel<__nv_bfloat16, float><<<grid, 256, 0, s>>>(g);
-        else
-            embedding_grad_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, 256, 0, s>>>(g);
-    }
-    return cudaGetLastError() == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
+    if ((int64_t)g.blocks * g.join_cols + V / GRAD_ROWS + 1 > 0x7fffffffLL ||
+        (g.packs + GRAD_THREADS - 1) / GRAD_THREADS > 65535)
+        return TPMLP_ERR_SHAPE;
+    cudaError_t e;
+    if (f32)
+        e = grad_f32 ? grad_dispatch<float, float>(g, n, zn, s) : grad_dispatch<float, __nv_bfloat16>(g, n, zn, s);
+    else
+        e = grad_f32 ? grad_dispatch<__nv_bfloat16, float>(g, n, zn, s)
+                     : grad_dispatch<__nv_bfloat16, __nv_bfloat16>(g, n, zn, s);
+    return e == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
 }
 
 }  // namespace tpmlp
