@@ -110,9 +110,12 @@ struct Cfg {
 struct TcParams {
     CUtensorMap tmA[kMaxG];
     CUtensorMap tmB[kMaxG];
-    CUtensorMap tmB2[kMaxG];   // dual: the second B (up projection); chain: the second pair's B
-    CUtensorMap tmC[kMaxG];    // tma_out: the output of each group (box 32 x 32)
+    CUtensorMap tmB2[kMaxG];   // dual: the second B (up projection); chain: the second pair's B;
+                               // EPI_DSWIGLU (neither): U of each group
+    CUtensorMap tmC[kMaxG];    // tma_out: the output of each group (box 32 x 32); EPI_DSWIGLU:
+                               // dG and dU of each group as one 3-D tensor {N, M, 2}
     CUtensorMap tmAux[kMaxG];  // tma_out, EPI_ACT with Z saved: Z of each group;
+                               // EPI_DSWIGLU: G of each group;
                                // chain (which has no auxiliary tensor): the second pair's A
     int M, N, K;
     int G, fold;
@@ -912,12 +915,63 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
             }
             zpend |= 1u << set;
         };
+        // gated backward epilogue with staging: G and U of a chunk arrive in the
+        // two halves of its staging set, dG and dU take their places (each
+        // lane its own row) and leave from there. So the next chunk's loads
+        // go out once the stores that last used the other set have read it,
+        // and the first chunk's before the tile's accumulator is ready.
+        const bool gin = C::TMA_OUT && p.tma_out && p.epi.kind == EPI_DSWIGLU;
+        auto gload = [&](uint32_t set, int g, int col0, int row0) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(zbar(set), 4096u);
+                const uint32_t dst = obuf0 + set * (uint32_t)C::OUT_BUF;
+                tma_load_2d(dst, &p.tmAux[g], zbar(set), col0, row0);
+                tma_load_2d(dst + 2048u, &p.tmB2[g], zbar(set), col0, row0);
+            }
+            zpend |= 1u << set;
+        };
         // next_col0: the next chunk this warp emits for the same rows, or -1
         auto emit = [&](int g, int row, int row0, int col0, const uint32_t (&r)[32], int next_col0) {
             float v[32];
             epilogue_bias(p.epi, g, col0, p.N, r, v);
             const bool z_out = p.epi.kind == EPI_ACT && p.epi.aux[g] != nullptr;
-            if (C::TMA_OUT && p.tma_out) {
+            if (gin) {
+                const uint32_t buf = obuf0 + oset * (uint32_t)C::OUT_BUF;
+                if (!((zpend >> oset) & 1u)) {
+                    if (lane == 0) bulk_wait_read_all();
+                    __syncwarp();
+                    gload(oset, g, col0, row0);
+                }
+                const uint32_t par = (zph >> oset) & 1u;
+                int okz = 1;
+                if (lane == 0) okz = wait_fast(zbar(oset), par, abort_flag, p.err, p.timeout_ns, true);
+                okz = __shfl_sync(0xffffffffu, okz, 0);
+                if (okz) {
+                    mbar_try_wait(zbar(oset), par);   // each lane acquires the completed loads
+                    zpend &= ~(1u << oset);
+                    zph ^= 1u << oset;
+                }
+                float gv[32], uv[32];
+                load_row_bf16_smem(buf, lane, gv);
+                load_row_bf16_smem(buf + 2048u, lane, uv);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) dswiglu_bf16(v[j], gv[j], uv[j], v[j], uv[j]);
+                stage_row(buf, lane, false, v);
+                stage_row(buf + 2048u, lane, false, uv);
+                fence_proxy_async_smem();   // the staged rows, to the tensor-store proxy
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_3d(&p.tmC[g], buf, col0, row0, 0);
+                    tma_store_3d(&p.tmC[g], buf + 2048u, col0, row0, 1);
+                    bulk_commit();
+                }
+                if (next_col0 >= 0) {
+                    if (lane == 0) bulk_wait_read_all_but_one();   // the other set's stores have read it
+                    __syncwarp();
+                    gload(oset ^ 1u, g, next_col0, row0);
+                }
+                oset ^= 1u;
+            } else if (C::TMA_OUT && p.tma_out) {
                 const uint32_t buf = obuf0 + oset * (uint32_t)C::OUT_BUF;
                 if (zin) {
                     if (!((zpend >> oset) & 1u)) zload(oset, g, col0, row0);
@@ -967,6 +1021,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
             // act' epilogue: the tile's first Z chunk loads while the accumulator fills
             if (zin && !w.partial() && !p.dual && ks == 1 && !((zpend >> oset) & 1u))
                 zload(oset, g, n0, m0 + (int)rank * BM + quarter * 32);
+            if (gin && !w.partial() && ks == 1 && !((zpend >> oset) & 1u)) {
+                if (lane == 0) bulk_wait_read_all();
+                __syncwarp();
+                gload(oset, g, n0, m0 + (int)rank * BM + quarter * 32);
+            }
             // one lane waits; the warp stays converged for the .sync.aligned TMEM loads
             int ok = 1;
             // (sleeping 1 us between polls: 0.4-1.4% fewer cycles for the GEMM)
@@ -1261,6 +1320,23 @@ bool make_map_out(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, 
     return r == CUDA_SUCCESS;
 }
 
+// dG and dU of the gated backward, `second` behind `first` by a fixed positive
+// distance: one 3-D tensor {cols, rows, 2} stored in boxes of 32 x 32 bf16.
+bool make_map_out_pair(CUtensorMap* m, const void* first, const void* second, int64_t cols,
+                       int64_t rows, int64_t ld) {
+    auto fn = encode_fn();
+    const int64_t apart = static_cast<const char*>(second) - static_cast<const char*>(first);
+    if (!fn || apart < rows * ld * 2 || apart % 16 != 0 || apart >= (1LL << 40)) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, 2};
+    cuuint64_t strides[2] = {(cuuint64_t)(ld * 2), (cuuint64_t)apart};
+    cuuint32_t box[3] = {32, 32, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(first), dims, strides, box,
+                    estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 // An MN-major operand ([K rows] x [mn columns], row pitch ld, mn % 64 == 0)
 // seen as 64-wide column chunks: dims {64, K, mn/64} with strides {ld*2, 128}
 // bytes. A box {64, bk, rows/64} lands in shared memory chunk by chunk, each
@@ -1487,8 +1563,15 @@ tpmlp_status launch(const GemmProblem& pr, cudaStream_t s, int ks = 1) {
     // configuration has room for the staging and every output has a map (not
     // the gated epilogue, nor the reduce-scatter's row blocks)
     kp.tma_out = 0;
-    if (C::TMA_OUT && !pr.dual && pr.epi.kind != EPI_SWIGLU && pr.epi.kind != EPI_DSWIGLU &&
-        pr.epi.row_shard == 0) {
+    if (C::TMA_OUT && pr.epi.kind == EPI_DSWIGLU && !pr.dual && !pr.chain && !pr.fold) {
+        bool ok = true;
+        for (int g = 0; g < G && ok; ++g)
+            ok = make_map_out_pair(&kp.tmC[g], pr.epi.C[g], pr.epi.C2[g], pr.N, pr.M, pr.epi.ldc) &&
+                 make_map_out(&kp.tmAux[g], pr.epi.aux[g], pr.N, pr.M, pr.epi.ldaux, false) &&
+                 make_map_out(&kp.tmB2[g], pr.epi.aux2[g], pr.N, pr.M, pr.epi.ldaux, false);
+        kp.tma_out = ok ? 1 : 0;
+    } else if (C::TMA_OUT && !pr.dual && pr.epi.kind != EPI_SWIGLU && pr.epi.kind != EPI_DSWIGLU &&
+               pr.epi.row_shard == 0) {
         bool ok = true;
         for (int g = 0; g < (pr.fold ? 1 : G) && ok; ++g) {
             ok = make_map_out(&kp.tmC[g], pr.epi.C[g], pr.N, pr.M, pr.epi.ldc, pr.epi.out_f32 != 0);
