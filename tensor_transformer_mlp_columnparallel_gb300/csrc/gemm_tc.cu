@@ -917,9 +917,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
         };
         // gated backward epilogue with staging: G and U of a chunk arrive in the
         // two halves of its staging set, dG and dU take their places (each
-        // lane its own row) and leave from there. So the next chunk's loads
-        // go out once the stores that last used the other set have read it,
-        // and the first chunk's before the tile's accumulator is ready.
+        // lane its own row) and leave from there. The next chunk's loads go
+        // out at the start of a chunk, once the stores of the chunk before
+        // have read the other set, and the first chunk's before the tile's
+        // accumulator is ready.
         const bool gin = C::TMA_OUT && p.tma_out && p.epi.kind == EPI_DSWIGLU;
         auto gload = [&](uint32_t set, int g, int col0, int row0) {
             if (lane == 0) {
@@ -937,11 +938,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
             const bool z_out = p.epi.kind == EPI_ACT && p.epi.aux[g] != nullptr;
             if (gin) {
                 const uint32_t buf = obuf0 + oset * (uint32_t)C::OUT_BUF;
-                if (!((zpend >> oset) & 1u)) {
-                    if (lane == 0) bulk_wait_read_all();
-                    __syncwarp();
-                    gload(oset, g, col0, row0);
-                }
+                if (lane == 0) bulk_wait_read_all();
+                __syncwarp();
+                if (!((zpend >> oset) & 1u)) gload(oset, g, col0, row0);
+                if (next_col0 >= 0) gload(oset ^ 1u, g, next_col0, row0);
                 const uint32_t par = (zph >> oset) & 1u;
                 int okz = 1;
                 if (lane == 0) okz = wait_fast(zbar(oset), par, abort_flag, p.err, p.timeout_ns, true);
@@ -964,11 +964,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
                     tma_store_3d(&p.tmC[g], buf, col0, row0, 0);
                     tma_store_3d(&p.tmC[g], buf + 2048u, col0, row0, 1);
                     bulk_commit();
-                }
-                if (next_col0 >= 0) {
-                    if (lane == 0) bulk_wait_read_all_but_one();   // the other set's stores have read it
-                    __syncwarp();
-                    gload(oset ^ 1u, g, next_col0, row0);
                 }
                 oset ^= 1u;
             } else if (C::TMA_OUT && p.tma_out) {
