@@ -698,31 +698,40 @@ tpmlp_status tpmlp_swiglu_backward(tpmlp_dtype dt, int64_t N, int64_t D, int64_t
     }
     TPMLP_TRY(run_gemm(dt, g1, s, sk));
 
-    // 2. dWd^(r) = H^(r)^T dY: A(m, k) = H^(r)[k, m] (MN-major), B(k, n) = dY[k, n]
-    GemmProblem g2 = problem(Fs, (int)D, (int)N, T, 0, Fs, 1, D, 1, "bwd_gated_dwd_gemm");
-    g2.epi.kind = EPI_STORE;
-    g2.epi.out_f32 = f32;
-    g2.epi.ldc = D;
-    for (int r = 0; r < T; ++r) {
-        g2.A[r] = H[r];
-        g2.B[r] = dY;
-        g2.epi.C[r] = dWd[r];
-    }
-    TPMLP_TRY(run_gemm(dt, g2, s, sk));
-
-    // 3. dWg^(r) = X^T dG^(r), dWu^(r) = X^T dU^(r): A(m, k) = X[k, m] (MN-major)
-    for (int half = 0; half < 2; ++half) {
-        GemmProblem g3 = problem((int)D, Fs, (int)N, T, 0, D, 1, Fs, 1,
-                                 half ? "bwd_gated_dwu_gemm" : "bwd_gated_dwg_gemm");
-        g3.epi.kind = EPI_STORE;
-        g3.epi.out_f32 = f32;
-        g3.epi.ldc = Fs;
+    // 2. dWd^(r) = H^(r)^T dY, 3. dWg^(r) = X^T dG^(r), dWu^(r) = X^T dU^(r)
+    if (bf && N <= kFewTokens) {
+        // few tokens: writing the gradients bounds it
+        WeightGradProduct w[kMaxWeightGrads];
+        int n = 0;
+        for (int r = 0; r < T; ++r) w[n++] = WeightGradProduct{H[r], dY, dWd[r], Fs, D, D, Fs, (int)D};
+        for (int r = 0; r < T; ++r) w[n++] = WeightGradProduct{X, dG[r], dWg[r], D, Fs, Fs, (int)D, Fs};
+        for (int r = 0; r < T; ++r) w[n++] = WeightGradProduct{X, dU[r], dWu[r], D, Fs, Fs, (int)D, Fs};
+        TPMLP_TRY(run_weight_grads(w, n, (int)N, s, "bwd_gated_weight_grads"));
+    } else {
+        // A(m, k) = H^(r)[k, m] or X[k, m] (MN-major), B(k, n) = dY, dG or dU[k, n]
+        GemmProblem g2 = problem(Fs, (int)D, (int)N, T, 0, Fs, 1, D, 1, "bwd_gated_dwd_gemm");
+        g2.epi.kind = EPI_STORE;
+        g2.epi.out_f32 = f32;
+        g2.epi.ldc = D;
         for (int r = 0; r < T; ++r) {
-            g3.A[r] = X;
-            g3.B[r] = half ? dU[r] : dG[r];
-            g3.epi.C[r] = half ? dWu[r] : dWg[r];
+            g2.A[r] = H[r];
+            g2.B[r] = dY;
+            g2.epi.C[r] = dWd[r];
         }
-        TPMLP_TRY(run_gemm(dt, g3, s, sk));
+        TPMLP_TRY(run_gemm(dt, g2, s, sk));
+        for (int half = 0; half < 2; ++half) {
+            GemmProblem g3 = problem((int)D, Fs, (int)N, T, 0, D, 1, Fs, 1,
+                                     half ? "bwd_gated_dwu_gemm" : "bwd_gated_dwg_gemm");
+            g3.epi.kind = EPI_STORE;
+            g3.epi.out_f32 = f32;
+            g3.epi.ldc = Fs;
+            for (int r = 0; r < T; ++r) {
+                g3.A[r] = X;
+                g3.B[r] = half ? dU[r] : dG[r];
+                g3.epi.C[r] = half ? dWu[r] : dWg[r];
+            }
+            TPMLP_TRY(run_gemm(dt, g3, s, sk));
+        }
     }
 
     // 4. dX = sum_r dG^(r) Wg^(r)^T + dU^(r) Wu^(r)^T, the K loop over (r, pair, k)

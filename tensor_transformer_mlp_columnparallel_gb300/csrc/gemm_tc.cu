@@ -39,13 +39,13 @@
 // leaves its loop. The producer then waits for its own loads in flight, the
 // MMA thread for its own MMAs, and the TMEM owner frees the accumulator.
 #include <cuda_bf16.h>
-#include <cudaTypedefs.h>
 
 #include <cstdio>
 #include <mutex>
 
 #include "act.cuh"
 #include "ptx.cuh"
+#include "tc_desc.cuh"
 #include "tpmlp_internal.h"
 
 namespace tpmlp {
@@ -146,26 +146,6 @@ struct TcParams {
     int alt;             // bit 0: whole tiles of odd waves walk their K range from the top
                          // down; bit 1: odd bands walk their tiles in reverse (decode_tile)
 };
-
-// Shared-memory matrix descriptor, 128-byte swizzle (tcgen05 format: start
-// address, leading- and stride-dimension byte offsets in 16-byte units,
-// descriptor version 1 at bit 46, swizzle mode 2 at bit 61).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)((lbo & 0x3FFFFu) >> 4) << 16;
-    d |= (uint64_t)((sbo & 0x3FFFFu) >> 4) << 32;
-    d |= 1ull << 46;
-    d |= 2ull << 61;
-    return d;
-}
-
-// Instruction descriptor of kind::f16: fp32 accumulator (bits 4-5 = 1), bf16
-// A and B (bits 7-9, 10-12 = 1), operand majorness (bits 15, 16: 1 = MN-major),
-// N >> 3 at bit 17, M >> 4 at bit 24.
-__host__ __device__ constexpr uint32_t instr_desc(int M, int N, int a_mn, int b_mn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
-           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
 
 // Tile order. Consecutive tile indices run on CTAs that are resident at the
 // same time, so the order decides what L2 can reuse.
@@ -1265,36 +1245,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    });
-    return fn;
-}
-
-// Row-major bf16 matrix of `outer` rows x `inner` elements, row pitch `ld`
-// elements, read in boxes of box_inner x box_outer with 128-byte swizzle.
-bool make_map(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t ld,
-              int box_inner, int box_outer) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
-    cuuint64_t strides[1] = {(cuuint64_t)(ld * 2)};
-    cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_outer};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
-                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
 
 // Output map of the epilogue's tensor stores: `rows` x `cols` elements (bf16,
 // or fp32 with f32), row pitch ld elements, boxes of 32 x 32 with the swizzle

@@ -66,7 +66,7 @@ def check(m, out, dt):
     (1, 8, 8, 1, "bf16"), (1, 64, 128, 2, "bf16"), (7, 72, 3 * 40, 3, "bf16"), (16, 512, 2048, 4, "bf16"),
     (33, 264, 2 * 136, 2, "bf16"), (64, 256, 16 * 64, 16, "bf16"), (65, 200, 2 * 328, 2, "bf16"),
     (130, 136, 272, 2, "bf16"), (300, 520, 2 * 264, 2, "bf16"), (257, 384, 8 * 72, 8, "bf16"),
-    (640, 1024, 4 * 768, 4, "bf16"), (1024, 512, 16 * 128, 16, "bf16"),
+    (640, 1024, 4 * 768, 4, "bf16"), (768, 264, 2 * 200, 2, "bf16"), (800, 392, 3 * 136, 3, "bf16"), (1024, 512, 16 * 128, 16, "bf16"),
     (1, 3, 5, 1, "f32"), (5, 17, 3 * 7, 3, "f32"), (64, 256, 1024, 2, "f32"), (130, 70, 2 * 65, 2, "f32"),
     (200, 128, 16 * 12, 16, "f32")])
 def test_shapes(N, D, F, T, dt, mode):
