@@ -126,23 +126,30 @@ def _check(status: int):
         raise TpmlpError(status, status_str(status))
 
 
+# Marshalling is on the clock of every small call (a call's kernels may take 4
+# us), hence integers instead of ctypes objects, arrays instead of casts, and
+# the stream's handle without a stream object where torch offers that.
+
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _ptrs(ts: Optional[Sequence[torch.Tensor]]):
+    """Host array of the tensors' addresses (a POINTER(c_void_p) argument)."""
     if ts is None:
         return None
-    arr = (ctypes.c_void_p * len(ts))()
-    for i, t in enumerate(ts):
-        arr[i] = t.data_ptr()
-    return ctypes.cast(arr, _PP)
+    return (ctypes.c_void_p * len(ts))(*[t.data_ptr() for t in ts])
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(t: torch.Tensor):
-    if t.is_cuda:
-        return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
-    return None
+    if not t.is_cuda:
+        return None
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -152,12 +159,13 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 
 def _require(ts, device, dtype):
+    index = device.index   # None for the host
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda or t.device != device:
+        if t.get_device() != index:   # -1 for a host tensor
             raise ValueError("all tensors must live on the same CUDA device")
-        if dtype is not None and t.dtype != dtype:
+        if dtype is not None and t.dtype is not dtype:
             raise TypeError(f"expected {dtype}, got {t.dtype}")
         if not t.is_contiguous():
             raise ValueError("tensors must be contiguous (row-major)")
@@ -384,7 +392,8 @@ def tpmlp_vocab_distill(logits, teacher_ids, teacher_logits, T: int, tau: float,
 
 def _require_dlogits(logits, dlogits) -> int:
     ldd = _require_rows(dlogits, "dlogits")
-    if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype or dlogits.device != logits.device:
+    if (dlogits.shape != logits.shape or dlogits.dtype is not logits.dtype
+            or dlogits.get_device() != logits.get_device()):
         raise ValueError("dlogits must have the shape, type and device of logits")
     return ldd
 
