@@ -610,6 +610,14 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
     const int rank = (int)(blockIdx.x & (unsigned)(split - 1));
     if (split > 1) cluster_arrive();   // this CTA runs: its shared memory may be written
     const Row<T, ROW_THREADS> row(a.logits, row_i, a.ld, a.V, rank, log_split);
+    // the row's loads go out before anything waits for the target's
+    constexpr int CHUNK = Row<T, ROW_THREADS>::CHUNK;
+    const int rest = row.rest();
+    uint4 x[VPT];
+    if (row.lo < rest)
+        row.load_chunk(row.lo, x);
+    else
+        row.load_rest(rest, x);
     const int64_t t = a.targets ? a.targets[row_i] : -1;
     const bool good = t >= 0 && t < a.V;
     const float zt = good ? to_f32(row.z[t]) : INFINITY;
@@ -623,8 +631,6 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
     Soft st{Vec<T>::lowest(), 0.f, 0.f};
     int before = 0;
     float raw = -INFINITY;
-    constexpr int CHUNK = Row<T, ROW_THREADS>::CHUNK;
-    uint4 x[VPT];
     auto chunk = [&](int base) {
         const float largest = Vec<T>::largest(x);
         raw = max_nan(raw, largest);
@@ -658,15 +664,14 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
             cnt.gt(e[0], zw);
         before += cnt.total();
     }
-    const int rest = row.rest();
     for (int base = row.lo; base < rest; base += CHUNK) {
-        row.load_chunk(base, x);
         chunk(base);
+        if (base + CHUNK < rest)
+            row.load_chunk(base + CHUNK, x);
+        else
+            row.load_rest(rest, x);
     }
-    if (rest < row.hi) {
-        row.load_rest(rest, x);
-        chunk(rest);
-    }
+    if (rest < row.hi) chunk(rest);
     if (counted && threadIdx.x == 0 && row.mine((int)t))
         for (int e = max(row.start(tvec), 0); e < (int)t; ++e) before += to_f32(row.z[e]) == zt;
     if (good && !counted) {   // -inf (or NaN) given: every other entry is compared
@@ -727,7 +732,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
 struct TeacherShared {
     int id[TPMLP_MAX_TEACHER];
     float q[TPMLP_MAX_TEACHER];
-    float fix[TPMLP_MAX_TEACHER];   // the gradient at id
+    float z[TPMLP_MAX_TEACHER];     // the student's logit at id, as it is before an in-place sweep
     float tm, sum;
     int some, bad, n;               // n: slots of this CTA
 };
@@ -769,6 +774,7 @@ __device__ void teacher_row(const DistillArgs& a, int64_t row_i, const Row<T, NT
                 const int at = n + __popc(b & ((1u << lane) - 1u));
                 sh.id[at] = id;
                 sh.q[at] = ex2((tl[k] - mx) * ct) / s;
+                sh.z[at] = to_f32(row.z[id]);
             }
             n += __popc(b);
         }
@@ -841,6 +847,19 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
         }
         if (early) row.load_rest(rest, x);
     }
+    // the leader's loss needs the student's logits at the teacher's tokens,
+    // which are on their way with the row (before anything is written in place)
+    constexpr int LPT = (TPMLP_MAX_TEACHER + NT - 1) / NT;
+    float zk[LPT];
+    if (LOSS && rank == 0 && live) {
+#pragma unroll
+        for (int u = 0; u < LPT; ++u) {
+            const int k = threadIdx.x + u * NT;
+            if (k >= a.K) break;
+            const int id = ids[k];
+            zk[u] = id >= 0 && id < a.V ? to_f32(row.z[id]) : 0.f;
+        }
+    }
     if (warp == 0) teacher_row(a, row_i, row, GRAD, te);
 
     Dist dist{};
@@ -864,19 +883,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
                     const uint4 y[2] = {stage[r * NT + threadIdx.x], stage[(r + 1) * NT + threadIdx.x]};
                     soft_chunk<T, false>(st, y, Vec<T>::largest(y), c);
                 }
-            }
-        }
-        // the leader's loss: (ln q - ln p) needs the student's logits at the
-        // teacher's tokens, read before anything is written in place
-        constexpr int LPT = (TPMLP_MAX_TEACHER + NT - 1) / NT;
-        float zk[LPT];
-        if (rank == 0 && live) {
-#pragma unroll
-            for (int u = 0; u < LPT; ++u) {
-                const int k = threadIdx.x + u * NT;
-                if (k >= a.K) break;
-                const int id = ids[k];
-                zk[u] = id >= 0 && id < a.V ? to_f32(row.z[id]) : 0.f;
             }
         }
         // every warp's sums to every CTA of the row; all of them add the same
@@ -915,112 +921,123 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
         for (int u = 0; u < PPL; ++u) s0.s = fmaf(part[u].s, ex2((part[u].ref - m) * c), s0.s);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) s0.s += __shfl_xor_sync(0xffffffffu, s0.s, off);
-        dist = distribution(s0, c, 1.f / a.tau);
-        if (rank == 0) {
-            float loss = 0.f;
-            if (te.some && !te.bad) {
-                const float log2_sum = log2f(te.sum);
-#pragma unroll
-                for (int u = 0; u < LPT; ++u) {
-                    const int k = threadIdx.x + u * NT;
-                    if (k >= a.K) break;
-                    if (ids[k] == -1) continue;
-                    const float lq = (tl[k] - te.tm) * c - log2_sum;
-                    const float q = ex2(lq);
-                    if (q != 0.f) loss += q * (kLn2 * lq - dist.ln_p(zk[u]));
-                }
-            }
-            loss = block_reduce(loss, Sum(), redf);
-            if (threadIdx.x == 0) {
-                if (te.bad) atomicCAS(err, 0, (int)TPMLP_ERR_ARG);
-                a.loss[row_i] = te.bad ? NAN : a.tau * a.tau * loss;
-                if (a.lse) a.lse[row_i] = te.bad ? NAN : te.some ? dist.lse() : 0.f;
-            }
-        }
+        dist.ref = s0.ref;
+        dist.s = s0.s;
+        dist.c = c;
+        dist.nothing = s0.s == 0.f;
     } else {
         __syncthreads();   // the teacher's statistics
-        if (te.bad && rank == 0 && threadIdx.x == 0) atomicCAS(err, 0, (int)TPMLP_ERR_ARG);
         const float lse = a.lse_in[row_i];
         dist.c = c;   // p = 2^((z - lse tau) c)
         dist.nothing = lse == -INFINITY;
         dist.ref = lse * a.tau;
         dist.s = 1.f;
     }
-    if (!GRAD) return;
-    const float w = a.grad_scale * (a.grad_tokens ? a.grad_tokens[row_i] : 1.f) * a.tau;
-    const float ws = w / dist.s;   // times 2^exponent: w p
-    // rows without probabilities hold `fill` and, where the teacher has some, its part
-    const bool flat = te.bad || !te.some || dist.nothing;
-    const float fill = te.bad ? NAN : 0.f;
-    // the CTA's teacher tokens, from the logits as they are before the sweep;
-    // slots of one id all get the row's full value
-    for (int k = threadIdx.x; k < te.n; k += NT) {
-        const int id = te.id[k];
-        float q = 0.f;
-        for (int j = 0; j < te.n; ++j)
-            if (te.id[j] == id) q += te.q[j];
-        te.fix[k] = fmaf(-w, q, flat ? fill : ws * ex2(dist.exponent(to_f32(row.z[id]))));
-    }
-    __syncthreads();
-    const bool same = ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(row.z)) & 15) == 0;
-    const F2 c2 = f2(c, c), r2 = f2(-dist.ref, -dist.ref), w2 = f2(ws, ws);
-    auto gradient = [&](const uint4& z, float (&v)[Vec<T>::N]) {
+    if (GRAD) {
+        const float w = a.grad_scale * (a.grad_tokens ? a.grad_tokens[row_i] : 1.f) * a.tau;
+        const float ws = w / dist.s;   // times 2^exponent: w p
+        // rows without probabilities hold `fill` and, where the teacher has some, its part
+        const bool flat = te.bad || !te.some || dist.nothing;
+        const float fill = te.bad ? NAN : 0.f;
+        const bool same = ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(row.z)) & 15) == 0;
+        const F2 c2 = f2(c, c), r2 = f2(-dist.ref, -dist.ref), w2 = f2(ws, ws);
+        auto store = [&](int i, const float (&v)[Vec<T>::N]) {
+            T* at = d + row.start(i);
+            if (same) {
+                __stcs(reinterpret_cast<uint4*>(at), Vec<T>::pack(v));
+            } else {
 #pragma unroll
-        for (int k = 0; k < Vec<T>::PAIRS; ++k) {
-            float e0, e1;
-            split2(mul2(add2(Vec<T>::pair(z, k), r2), c2), e0, e1);
-            split2(mul2(f2(ex2(e0), ex2(e1)), w2), v[2 * k], v[2 * k + 1]);
-            if (flat) v[2 * k] = v[2 * k + 1] = fill;
+                for (int j = 0; j < Vec<T>::N; ++j) at[j] = from_f32<T>(v[j]);
+            }
+        };
+        auto gradient = [&](const uint4& z, float (&v)[Vec<T>::N]) {
+#pragma unroll
+            for (int k = 0; k < Vec<T>::PAIRS; ++k) {
+                float e0, e1;
+                split2(mul2(add2(Vec<T>::pair(z, k), r2), c2), e0, e1);
+                split2(mul2(f2(ex2(e0), ex2(e1)), w2), v[2 * k], v[2 * k + 1]);
+            }
+        };
+        if (row.edge() <= row.full) {
+            const int i = row.edge(), e0 = row.start(i);
+            float v[Vec<T>::N];
+            if (!flat) gradient(row.load_edge(i), v);
+#pragma unroll
+            for (int j = 0; j < Vec<T>::N; ++j)
+                if (e0 + j >= 0 && e0 + j < row.len) d[e0 + j] = from_f32<T>(flat ? fill : v[j]);
         }
-    };
-    auto store = [&](int i, const float (&v)[Vec<T>::N]) {
-        T* at = d + row.start(i);
-        if (same) {
-            __stcs(reinterpret_cast<uint4*>(at), Vec<T>::pack(v));
+        if (flat) {
+            float v[Vec<T>::N];
+#pragma unroll
+            for (int j = 0; j < Vec<T>::N; ++j) v[j] = fill;
+            for (int i = row.lo + (int)threadIdx.x; i < row.hi; i += NT) store(i, v);
         } else {
+            // Back to front: the last chunk is still in registers, what was read
+            // last is the likeliest to be in L2.
+            if (!LOSS && !early) row.load_rest(rest, x);
 #pragma unroll
-            for (int j = 0; j < Vec<T>::N; ++j) at[j] = from_f32<T>(v[j]);
+            for (int r = 0; r < VPT; ++r) {
+                const int i = rest + r * NT + (int)threadIdx.x;
+                if (i < row.hi) {
+                    float v[Vec<T>::N];
+                    gradient(x[r], v);
+                    store(i, v);
+                }
+            }
+            if (staged < rest) {
+#pragma unroll
+                for (int r = 0; r < VPT; ++r) {
+                    float v[Vec<T>::N];
+                    gradient(stage[r * NT + threadIdx.x], v);
+                    store(staged + r * NT + (int)threadIdx.x, v);
+                }
+            }
+            for (int base = staged - CHUNK; base >= row.lo; base -= CHUNK) {
+                row.load_chunk(base, x);
+#pragma unroll
+                for (int r = 0; r < VPT; ++r) {
+                    float v[Vec<T>::N];
+                    gradient(x[r], v);
+                    store(base + r * NT + (int)threadIdx.x, v);
+                }
+            }
         }
-    };
-    if (row.edge() <= row.full) {
-        const int i = row.edge(), e0 = row.start(i);
-        float v[Vec<T>::N];
-        gradient(live ? row.load_edge(i) : make_uint4(0, 0, 0, 0), v);
-#pragma unroll
-        for (int j = 0; j < Vec<T>::N; ++j)
-            if (e0 + j >= 0 && e0 + j < row.len) d[e0 + j] = from_f32<T>(v[j]);
-    }
-    // Back to front: the last chunk is still in registers, what was read last is
-    // the likeliest to be in L2.
-    if (live && !LOSS && !early) row.load_rest(rest, x);
-#pragma unroll
-    for (int r = 0; r < VPT; ++r) {
-        const int i = rest + r * NT + (int)threadIdx.x;
-        if (i < row.hi) {
-            float v[Vec<T>::N];
-            gradient(x[r], v);
-            store(i, v);
+        // the teacher's tokens over the sweep; slots of one id all write the
+        // row's full value
+        if (te.n > 0) {
+            __syncthreads();
+            for (int k = threadIdx.x; k < te.n; k += NT) {
+                const int id = te.id[k];
+                float q = 0.f;
+                for (int j = 0; j < te.n; ++j)
+                    if (te.id[j] == id) q += te.q[j];
+                d[id] = from_f32<T>(fmaf(-w, q, flat ? fill : ws * ex2(dist.exponent(te.z[k]))));
+            }
         }
     }
-    if (staged < rest) {
+    if (LOSS && rank == 0) {
+        dist.inv_tau = 1.f / a.tau;
+        dist.ln_s = logf(dist.s);
+        float loss = 0.f;
+        if (te.some && !te.bad) {
+            const float log2_sum = log2f(te.sum);
 #pragma unroll
-        for (int r = 0; r < VPT; ++r) {
-            float v[Vec<T>::N];
-            gradient(stage[r * NT + threadIdx.x], v);
-            store(staged + r * NT + (int)threadIdx.x, v);
+            for (int u = 0; u < LPT; ++u) {
+                const int k = threadIdx.x + u * NT;
+                if (k >= a.K) break;
+                if (ids[k] == -1) continue;
+                const float lq = (tl[k] - te.tm) * c - log2_sum;
+                const float q = ex2(lq);
+                if (q != 0.f) loss += q * (kLn2 * lq - dist.ln_p(zk[u]));
+            }
+        }
+        loss = block_reduce(loss, Sum(), redf);
+        if (threadIdx.x == 0) {
+            a.loss[row_i] = te.bad ? NAN : a.tau * a.tau * loss;
+            if (a.lse) a.lse[row_i] = te.bad ? NAN : te.some ? dist.lse() : 0.f;
         }
     }
-    for (int base = staged - CHUNK; base >= row.lo; base -= CHUNK) {
-        if (live) row.load_chunk(base, x);
-#pragma unroll
-        for (int r = 0; r < VPT; ++r) {
-            float v[Vec<T>::N];
-            gradient(x[r], v);
-            store(base + r * NT + (int)threadIdx.x, v);
-        }
-    }
-    __syncthreads();
-    for (int k = threadIdx.x; k < te.n; k += NT) d[te.id[k]] = from_f32<T>(te.fix[k]);
+    if (rank == 0 && threadIdx.x == 0 && te.bad) atomicCAS(err, 0, (int)TPMLP_ERR_ARG);
 }
 
 // ---------------------------------------------------------------- launch --
