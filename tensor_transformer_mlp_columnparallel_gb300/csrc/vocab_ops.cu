@@ -737,47 +737,84 @@ struct TeacherShared {
     int some, bad, n;               // n: slots of this CTA
 };
 
+// A lane's first slots (k = lane + 32 u), loaded at once: all of them for K <=
+// 32 SLOTS. What lies beyond is read again where it is needed.
+constexpr int SLOTS = 4;
+struct LaneSlots {
+    int id[SLOTS];       // -1: empty, or no such slot
+    float t[SLOTS];
+};
+__device__ __forceinline__ LaneSlots load_slots(const int32_t* ids, const float* tl, int K) {
+    const int lane = threadIdx.x & 31;
+    LaneSlots r;
+#pragma unroll
+    for (int u = 0; u < SLOTS; ++u) {
+        const int k = lane + 32 * u;
+        r.id[u] = k < K ? ids[k] : -1;
+        r.t[u] = k < K ? tl[k] : -INFINITY;
+    }
+    return r;
+}
+
 // Warp 0: statistics over the K slots, then the slots whose id is in the
-// CTA's slice, in slot order.
+// CTA's slice, in slot order. The student's logits at those are loaded first.
 template <typename T, int NT>
-__device__ void teacher_row(const DistillArgs& a, int64_t row_i, const Row<T, NT>& row, bool lists,
-                            TeacherShared& sh) {
+__device__ __forceinline__ void teacher_row(const DistillArgs& a, const int32_t* ids, const float* tl,
+                                            const LaneSlots& slots, const Row<T, NT>& row, bool lists,
+                                            TeacherShared& sh) {
     const int lane = threadIdx.x;
-    const int32_t* ids = a.ids + row_i * a.K;
-    const float* tl = a.teacher + row_i * a.K;
     const float ct = kLog2e / a.tau;
+    float z[SLOTS];
+    if (lists)
+#pragma unroll
+        for (int u = 0; u < SLOTS; ++u)
+            z[u] = slots.id[u] >= 0 && row.mine(slots.id[u]) ? to_f32(row.z[slots.id[u]]) : 0.f;
     float mx = -INFINITY;
     int bad = 0;
-    for (int k = lane; k < a.K; k += 32) {
-        const int id = ids[k];
-        if (id != -1) mx = max_nan(mx, tl[k]);
+    auto look = [&](int id, float t) {
+        if (id != -1) mx = max_nan(mx, t);
         bad |= id < -1 || id >= a.V;
-    }
+    };
+#pragma unroll
+    for (int u = 0; u < SLOTS; ++u) look(slots.id[u], slots.t[u]);
+    for (int k = lane + 32 * SLOTS; k < a.K; k += 32) look(ids[k], tl[k]);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
     bad = __any_sync(0xffffffffu, bad);
     const bool some = mx != -INFINITY;
     float s = 0.f;
-    if (some)
-        for (int k = lane; k < a.K; k += 32)
-            if (ids[k] != -1) s += ex2((tl[k] - mx) * ct);
+    auto weight = [&](int id, float t) { return some && id != -1 ? ex2((t - mx) * ct) : 0.f; };
+    float e[SLOTS];
+#pragma unroll
+    for (int u = 0; u < SLOTS; ++u) {
+        e[u] = weight(slots.id[u], slots.t[u]);
+        s += e[u];
+    }
+    for (int k = lane + 32 * SLOTS; k < a.K; k += 32) s += weight(ids[k], tl[k]);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     int n = 0;
-    if (lists && some && !bad)
-        for (int k0 = 0; k0 < a.K; k0 += 32) {
-            const int k = k0 + lane;
-            const int id = k < a.K ? ids[k] : -1;
-            const bool hit = id != -1 && row.mine(id);
+    if (lists && some && !bad) {
+        const float inv = 1.f / s;
+        auto keep = [&](bool hit, int id, float ek, float zk) {
             const uint32_t b = __ballot_sync(0xffffffffu, hit);
             if (hit) {
                 const int at = n + __popc(b & ((1u << lane) - 1u));
                 sh.id[at] = id;
-                sh.q[at] = ex2((tl[k] - mx) * ct) / s;
-                sh.z[at] = to_f32(row.z[id]);
+                sh.q[at] = ek * inv;
+                sh.z[at] = zk;
             }
             n += __popc(b);
+        };
+#pragma unroll
+        for (int u = 0; u < SLOTS; ++u)
+            keep(slots.id[u] != -1 && row.mine(slots.id[u]), slots.id[u], e[u], z[u]);
+        for (int k0 = 32 * SLOTS; k0 < a.K; k0 += 32) {
+            const int id = k0 + lane < a.K ? ids[k0 + lane] : -1;
+            const bool hit = id != -1 && row.mine(id);
+            keep(hit, id, hit ? weight(id, tl[k0 + lane]) : 0.f, hit ? to_f32(row.z[id]) : 0.f);
         }
+    }
     if (lane == 0) {
         sh.tm = mx;
         sh.sum = s;
@@ -828,14 +865,16 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
     const int rest = row.rest();
 
     // A row without a live slot is not read. Every warp looks for one by
-    // itself (the first 32 slots, as a rule), so that its loads of the row
+    // itself (among the first slots, as a rule), so that its loads of the row
     // are on their way before warp 0 takes the teacher's statistics.
+    const LaneSlots slots = load_slots(ids, tl, a.K);
     bool live = false;
-    for (int k = lane; __any_sync(0xffffffffu, k < a.K); k += 32) {
-        const int id = k < a.K ? ids[k] : -1;
-        live = __any_sync(0xffffffffu, id != -1 && (tl[k] != -INFINITY || id < -1 || id >= a.V));
-        if (live) break;
-    }
+    auto counts = [&](int id, float t) { return id != -1 && (t != -INFINITY || id < -1 || id >= a.V); };
+#pragma unroll
+    for (int u = 0; u < SLOTS; ++u) live = live || counts(slots.id[u], slots.t[u]);
+    live = __any_sync(0xffffffffu, live);
+    for (int k = 32 * SLOTS; !live && k < a.K; k += 32)
+        live = __any_sync(0xffffffffu, k + lane < a.K && counts(ids[k + lane], tl[k + lane]));
     uint4 x[VPT];
     const int staged = STAGE && rest > row.lo ? rest - CHUNK : rest;   // where the chunk in shared memory starts
     const bool early = staged == row.lo;   // nothing is read through the registers before the last chunk
@@ -860,7 +899,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
             zk[u] = id >= 0 && id < a.V ? to_f32(row.z[id]) : 0.f;
         }
     }
-    if (warp == 0) teacher_row(a, row_i, row, GRAD, te);
+    if (warp == 0) teacher_row(a, ids, tl, slots, row, GRAD, te);
 
     Dist dist{};
     if (LOSS) {
