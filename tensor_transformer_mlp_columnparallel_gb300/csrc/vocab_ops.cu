@@ -728,12 +728,15 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
 // --------------------------------------------------------- distillation --
 
 // The teacher's slots of one row that are this CTA's, and its distribution:
-// slot k has q_k = exp(t_k / tau - tm) / sum.
+// slot k has q_k = 2^((t_k - max t) c) / sum. The loss is
+//   tau^2 (sum q ln q - sum q ln p),  ln p_v = (z_v - m) / tau - ln S,
+// and needs no more of the slots than sum q ln q, their largest logit zmax and
+// sum q (z - zmax), all known before the row's m and S.
 struct TeacherShared {
     int id[TPMLP_MAX_TEACHER];
     float q[TPMLP_MAX_TEACHER];
     float z[TPMLP_MAX_TEACHER];     // the student's logit at id, as it is before an in-place sweep
-    float tm, sum;
+    float q_ln_q, zmax, q_z;
     int some, bad, n;               // n: slots of this CTA
 };
 
@@ -756,19 +759,21 @@ __device__ __forceinline__ LaneSlots load_slots(const int32_t* ids, const float*
     return r;
 }
 
-// Warp 0: statistics over the K slots, then the slots whose id is in the
-// CTA's slice, in slot order. The student's logits at those are loaded first.
+// Warp 0: statistics over the K slots (for the loss with LOSS), then the slots
+// whose id is in the CTA's slice, in slot order. The student's logits they
+// need are loaded first, as they are before an in-place sweep.
 template <typename T, int NT>
 __device__ __forceinline__ void teacher_row(const DistillArgs& a, const int32_t* ids, const float* tl,
-                                            const LaneSlots& slots, const Row<T, NT>& row, bool lists,
+                                            const LaneSlots& slots, const Row<T, NT>& row, bool loss, bool lists,
                                             TeacherShared& sh) {
     const int lane = threadIdx.x;
     const float ct = kLog2e / a.tau;
+    auto logit = [&](int id) {
+        return id >= 0 && id < a.V && (loss || row.mine(id)) ? to_f32(row.z[id]) : -INFINITY;
+    };
     float z[SLOTS];
-    if (lists)
 #pragma unroll
-        for (int u = 0; u < SLOTS; ++u)
-            z[u] = slots.id[u] >= 0 && row.mine(slots.id[u]) ? to_f32(row.z[slots.id[u]]) : 0.f;
+    for (int u = 0; u < SLOTS; ++u) z[u] = logit(slots.id[u]);
     float mx = -INFINITY;
     int bad = 0;
     auto look = [&](int id, float t) {
@@ -793,9 +798,38 @@ __device__ __forceinline__ void teacher_row(const DistillArgs& a, const int32_t*
     for (int k = lane + 32 * SLOTS; k < a.K; k += 32) s += weight(ids[k], tl[k]);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    const float inv = 1.f / s;
+    float q_ln_q = 0.f, zmax = -INFINITY, q_z = 0.f;
+    if (loss && some && !bad) {
+        const float log2_sum = log2f(s);
+        auto entropy = [&](float ek, float t) {
+            if (ek != 0.f) q_ln_q = fmaf(ek * inv, kLn2 * ((t - mx) * ct - log2_sum), q_ln_q);
+        };
+        auto cross = [&](float ek, float zk) {
+            if (ek != 0.f) q_z = fmaf(ek * inv, zk - zmax, q_z);
+        };
+#pragma unroll
+        for (int u = 0; u < SLOTS; ++u) {
+            zmax = max_nan(zmax, z[u]);
+            entropy(e[u], slots.t[u]);
+        }
+        for (int k = lane + 32 * SLOTS; k < a.K; k += 32) {
+            zmax = max_nan(zmax, logit(ids[k]));
+            entropy(weight(ids[k], tl[k]), tl[k]);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) zmax = max_nan(zmax, __shfl_xor_sync(0xffffffffu, zmax, off));
+#pragma unroll
+        for (int u = 0; u < SLOTS; ++u) cross(e[u], z[u]);
+        for (int k = lane + 32 * SLOTS; k < a.K; k += 32) cross(weight(ids[k], tl[k]), logit(ids[k]));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            q_ln_q += __shfl_xor_sync(0xffffffffu, q_ln_q, off);
+            q_z += __shfl_xor_sync(0xffffffffu, q_z, off);
+        }
+    }
     int n = 0;
     if (lists && some && !bad) {
-        const float inv = 1.f / s;
         auto keep = [&](bool hit, int id, float ek, float zk) {
             const uint32_t b = __ballot_sync(0xffffffffu, hit);
             if (hit) {
@@ -816,8 +850,9 @@ __device__ __forceinline__ void teacher_row(const DistillArgs& a, const int32_t*
         }
     }
     if (lane == 0) {
-        sh.tm = mx;
-        sh.sum = s;
+        sh.q_ln_q = q_ln_q;
+        sh.zmax = zmax;
+        sh.q_z = q_z;
         sh.some = some;
         sh.bad = bad;
         sh.n = n;
@@ -850,7 +885,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
     constexpr int WARPS = NT / 32, CHUNK = Row<T, NT>::CHUNK;
     extern __shared__ uint4 stage[];   // STAGE: one chunk
     __shared__ WarpSoft parts[MAX_SPLIT * WARPS];
-    __shared__ float redf[WARPS];
     __shared__ TeacherShared te;
     const int split = 1 << log_split;
     const int64_t row_i = blockIdx.x >> log_split;
@@ -886,20 +920,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
         }
         if (early) row.load_rest(rest, x);
     }
-    // the leader's loss needs the student's logits at the teacher's tokens,
-    // which are on their way with the row (before anything is written in place)
-    constexpr int LPT = (TPMLP_MAX_TEACHER + NT - 1) / NT;
-    float zk[LPT];
-    if (LOSS && rank == 0 && live) {
-#pragma unroll
-        for (int u = 0; u < LPT; ++u) {
-            const int k = threadIdx.x + u * NT;
-            if (k >= a.K) break;
-            const int id = ids[k];
-            zk[u] = id >= 0 && id < a.V ? to_f32(row.z[id]) : 0.f;
-        }
-    }
-    if (warp == 0) teacher_row(a, ids, tl, slots, row, GRAD, te);
+    if (warp == 0) teacher_row(a, ids, tl, slots, row, LOSS && rank == 0, GRAD, te);
 
     Dist dist{};
     if (LOSS) {
@@ -964,6 +985,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
         dist.s = s0.s;
         dist.c = c;
         dist.nothing = s0.s == 0.f;
+        if (rank == 0 && threadIdx.x == 0) {
+            const float inv_tau = 1.f / a.tau, ln_s = logf(dist.s);
+            // a masked token that the teacher wants: ln p = -inf
+            const float cross = te.zmax == -INFINITY ? INFINITY : ln_s - (te.q_z + (te.zmax - dist.ref)) * inv_tau;
+            a.loss[row_i] = te.bad ? NAN : te.some ? a.tau * a.tau * (te.q_ln_q + cross) : 0.f;
+            if (a.lse)
+                a.lse[row_i] = te.bad ? NAN : !te.some ? 0.f : dist.nothing ? -INFINITY : fmaf(dist.ref, inv_tau, ln_s);
+        }
     } else {
         __syncthreads();   // the teacher's statistics
         const float lse = a.lse_in[row_i];
@@ -1052,28 +1081,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
                     if (te.id[j] == id) q += te.q[j];
                 d[id] = from_f32<T>(fmaf(-w, q, flat ? fill : ws * ex2(dist.exponent(te.z[k]))));
             }
-        }
-    }
-    if (LOSS && rank == 0) {
-        dist.inv_tau = 1.f / a.tau;
-        dist.ln_s = logf(dist.s);
-        float loss = 0.f;
-        if (te.some && !te.bad) {
-            const float log2_sum = log2f(te.sum);
-#pragma unroll
-            for (int u = 0; u < LPT; ++u) {
-                const int k = threadIdx.x + u * NT;
-                if (k >= a.K) break;
-                if (ids[k] == -1) continue;
-                const float lq = (tl[k] - te.tm) * c - log2_sum;
-                const float q = ex2(lq);
-                if (q != 0.f) loss += q * (kLn2 * lq - dist.ln_p(zk[u]));
-            }
-        }
-        loss = block_reduce(loss, Sum(), redf);
-        if (threadIdx.x == 0) {
-            a.loss[row_i] = te.bad ? NAN : a.tau * a.tau * loss;
-            if (a.lse) a.lse[row_i] = te.bad ? NAN : te.some ? dist.lse() : 0.f;
         }
     }
     if (rank == 0 && threadIdx.x == 0 && te.bad) atomicCAS(err, 0, (int)TPMLP_ERR_ARG);
