@@ -27,7 +27,8 @@ namespace {
 
 constexpr int ROW_THREADS = 256;
 constexpr int ROW_WARPS = ROW_THREADS / 32;
-constexpr int VPT = 8;                        // 16-byte vectors a thread holds
+constexpr int LP_VPT = 7;                     // 16-byte vectors a thread holds: log probabilities
+constexpr int KD_VPT = 8;                     // and distillation
 constexpr int MAX_SPLIT = 8;                  // CTAs of a row (the portable cluster size)
 constexpr float kLowest = -3.402823466e38f;   // FLT_MAX's negative
 constexpr float kLog2e = 1.4426950408889634f;
@@ -133,6 +134,7 @@ template <> struct Vec<__nv_bfloat16> {
         __device__ __forceinline__ int total() const { return (int)(__low2float(c) + __high2float(c)); }
     };
     static __device__ __forceinline__ Wide wide(float z) { return __float2bfloat162_rn(z); }
+    static __device__ __forceinline__ float narrow(Wide w) { return __low2float(w); }
     static __device__ __forceinline__ uint4 pack(const float (&v)[8]) {
         return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                           pack_bf16x2(v[6], v[7]));
@@ -185,6 +187,7 @@ template <> struct Vec<float> {
         }
     };
     static __device__ __forceinline__ Wide wide(float z) { return z; }
+    static __device__ __forceinline__ float narrow(Wide w) { return w; }
     static __device__ __forceinline__ uint4 pack(const float (&v)[4]) {
         return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
                           __float_as_uint(v[3]));
@@ -200,7 +203,7 @@ template <> struct Vec<float> {
 // -inf for what lies outside the row. The row's CTA `rank` owns the whole
 // vectors [lo, hi), elements [e_lo, e_hi): the first CTA with the front
 // edge, the last with the back edge.
-template <typename T, int NT>
+template <typename T, int NT, int VPT>
 struct Row {
     using V4 = Vec<T>;
     static constexpr int CHUNK = NT * VPT;   // vectors the CTA's registers hold
@@ -456,17 +459,17 @@ struct TopShared {
     unsigned long long all[MAX_SPLIT * TPMLP_MAX_TOP];       // the leader's copy of every CTA's list
     unsigned long long red[ROW_WARPS];
     uint32_t thr[ROW_WARPS];
-    uint32_t max_of[ROW_THREADS];    // maxima that reach the first bound, and their threads
-    int thread_of[ROW_THREADS];
-    int owner[ROW_THREADS];          // the threads whose entries are looked at
+    uint32_t max_of[ROW_THREADS];    // maxima that reach the first bound
+    int chunk_of[ROW_THREADS];       // (chunk, thread) whose vectors are looked at
+    int whole_of[ROW_THREADS];       // threads all of whose vectors are
     uint32_t bound;
-    int n_max, n_owner, n_cand;
+    int n_max, n_chunk, n_whole, n_cand;
 };
 
 // The elements of vector i that are in the row and at least `thr` (strictly
 // above with `above`) join the candidates; beyond MAX_CAND they are only counted.
 template <typename T>
-__device__ __forceinline__ void offer(const Row<T, ROW_THREADS>& row, int i, const uint4& x, uint32_t thr, bool above,
+__device__ __forceinline__ void offer(const Row<T, ROW_THREADS, LP_VPT>& row, int i, const uint4& x, uint32_t thr, bool above,
                                       TopShared& sh) {
     const int e0 = row.start(i);
 #pragma unroll
@@ -481,21 +484,33 @@ __device__ __forceinline__ void offer(const Row<T, ROW_THREADS>& row, int i, con
 
 // The slice's first K entries into sh.list (0: fewer than K entries).
 //
-// `raw` is the largest element the thread saw. The K-th largest of the 256
+// What a thread remembers of its part of the slice.
+struct Peaks {
+    float best;     // the largest in one of its chunks, the one at `base`
+    float other;    // the largest of all else, the row's edges among it; NaN where a NaN was seen
+    int base;
+};
+
+// The K-th largest of the 256
 // maxima is reached by K different entries, so only entries at or above it can
 // be in the list, and they sit with the threads whose maximum reaches it: K of
 // 256 unless maxima are equal. Their vectors are still in registers (one
-// chunk) or read again (K / 256 of the slice). The K-th largest maximum comes
-// in two steps: with g = ceil(K / warps), the least of the warps' g-th largest
-// maxima leaves a few dozen, and those are ranked by counting.
+// chunk) or read again: of the chunk with the thread's maximum alone, unless
+// another of its chunks reaches the bound too. (Reading all of a thread's
+// vectors, K / 256 of the slice, from DRAM as a rule, took 45% of the kernel's
+// time at K = 20 and 8192 x 128000 bf16 logits; this way the list takes 14%.) The K-th
+// largest maximum comes in two steps: with g = ceil(K / warps), the least of
+// the warps' g-th largest maxima leaves a few dozen, and those are ranked by
+// counting.
 // Where more than MAX_CAND entries reach the bound (a mask that leaves fewer
 // than K tokens, rows of equal values), the entries above it are taken alone
 // and equal ones follow by index; where even those are too many, K rounds
 // over the slice.
 template <typename T>
-__device__ void slice_top(const Row<T, ROW_THREADS>& row, int K, float raw, const uint4 (&x)[VPT], TopShared& sh) {
+__device__ void slice_top(const Row<T, ROW_THREADS, LP_VPT>& row, int K, const Peaks& peaks, const uint4 (&x)[LP_VPT],
+                          TopShared& sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t mine = order32(raw);
+    const uint32_t mine = order32(max_nan(peaks.best, peaks.other));
     uint32_t left = mine, g_th = 0;
     for (int g = 0; g < (K + ROW_WARPS - 1) / ROW_WARPS; ++g) {
         g_th = __reduce_max_sync(0xffffffffu, left);
@@ -503,7 +518,7 @@ __device__ void slice_top(const Row<T, ROW_THREADS>& row, int K, float raw, cons
         if (lane == __ffs(who) - 1) left = 0u;
     }
     if (lane == 0) sh.thr[warp] = g_th;
-    if (threadIdx.x == 0) sh.n_max = sh.n_owner = sh.n_cand = 0;
+    if (threadIdx.x == 0) sh.n_max = sh.n_chunk = sh.n_whole = sh.n_cand = 0;
     for (int k = threadIdx.x; k < K; k += ROW_THREADS) sh.list[k] = 0ull;
     __syncthreads();
     uint32_t thr = sh.thr[0];
@@ -511,7 +526,6 @@ __device__ void slice_top(const Row<T, ROW_THREADS>& row, int K, float raw, cons
     if (mine >= thr) {
         const int at = atomicAdd(&sh.n_max, 1);
         sh.max_of[at] = mine;
-        sh.thread_of[at] = (int)threadIdx.x;
     }
     __syncthreads();
     if ((int)threadIdx.x < sh.n_max) {
@@ -521,28 +535,35 @@ __device__ void slice_top(const Row<T, ROW_THREADS>& row, int K, float raw, cons
             above += sh.max_of[j] > me;
             reach += sh.max_of[j] >= me;
         }
-        if (above < K) {
-            sh.owner[atomicAdd(&sh.n_owner, 1)] = sh.thread_of[threadIdx.x];
-            if (reach >= K) sh.bound = me;   // the K-th largest: one value
-        }
+        if (above < K && reach >= K) sh.bound = me;   // the K-th largest: one value
     }
     __syncthreads();
     thr = sh.bound;
     const int n = row.hi - row.lo;
     const int per = (n + ROW_THREADS - 1) / ROW_THREADS;   // vectors of a thread
     if (mine >= thr && row.edge() <= row.full) offer(row, row.edge(), row.load_edge(row.edge()), thr, false, sh);
-    if (n <= Row<T, ROW_THREADS>::CHUNK) {
+    if (n <= Row<T, ROW_THREADS, LP_VPT>::CHUNK) {
         if (mine >= thr) {
 #pragma unroll
-            for (int r = 0; r < VPT; ++r) {
+            for (int r = 0; r < LP_VPT; ++r) {
                 const int i = row.lo + r * ROW_THREADS + (int)threadIdx.x;
                 if (i < row.hi) offer(row, i, x[r], thr, false, sh);
             }
         }
     } else {
-        const int items = sh.n_owner * per;
-        for (int a = threadIdx.x; a < items; a += ROW_THREADS) {
-            const int i = row.lo + (a % per) * ROW_THREADS + sh.owner[a / per];
+        if (mine >= thr) {
+            if (order32(peaks.other) >= thr)
+                sh.whole_of[atomicAdd(&sh.n_whole, 1)] = (int)threadIdx.x;
+            else if (order32(peaks.best) >= thr)
+                sh.chunk_of[atomicAdd(&sh.n_chunk, 1)] = peaks.base + (int)threadIdx.x;
+        }
+        __syncthreads();
+        for (int a = threadIdx.x; a < sh.n_chunk * LP_VPT; a += ROW_THREADS) {
+            const int i = sh.chunk_of[a / LP_VPT] + (a % LP_VPT) * ROW_THREADS;
+            if (i < row.hi) offer(row, i, row.load(i), thr, false, sh);
+        }
+        for (int a = threadIdx.x; a < sh.n_whole * per; a += ROW_THREADS) {
+            const int i = row.lo + (a % per) * ROW_THREADS + sh.whole_of[a / per];
             if (i < row.hi) offer(row, i, row.load(i), thr, false, sh);
         }
     }
@@ -609,80 +630,95 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
     const int64_t row_i = blockIdx.x >> log_split;
     const int rank = (int)(blockIdx.x & (unsigned)(split - 1));
     if (split > 1) cluster_arrive();   // this CTA runs: its shared memory may be written
-    const Row<T, ROW_THREADS> row(a.logits, row_i, a.ld, a.V, rank, log_split);
-    // the row's loads go out before anything waits for the target's
-    constexpr int CHUNK = Row<T, ROW_THREADS>::CHUNK;
-    const int rest = row.rest();
-    uint4 x[VPT];
-    if (row.lo < rest)
-        row.load_chunk(row.lo, x);
-    else
-        row.load_rest(rest, x);
-    const int64_t t = a.targets ? a.targets[row_i] : -1;
-    const bool good = t >= 0 && t < a.V;
-    const float zt = good ? to_f32(row.z[t]) : INFINITY;
-    // entries in front of the target: above it anywhere, equal to it before it.
-    // Vectors before the target's count equals; inside its own vector they
-    // are added below. A masked target is counted apart.
-    const bool counted = good && zt > -INFINITY;
-    const int tvec = counted ? row.vector_of((int)t) : -1;
-    const auto zw = Vec<T>::wide(counted ? zt : INFINITY);
-
+    constexpr int CHUNK = Row<T, ROW_THREADS, LP_VPT>::CHUNK;
+    uint4 x[LP_VPT];
     Soft st{Vec<T>::lowest(), 0.f, 0.f};
     int before = 0;
-    float raw = -INFINITY;
-    auto chunk = [&](int base) {
-        const float largest = Vec<T>::largest(x);
-        raw = max_nan(raw, largest);
-        soft_chunk<T, true>(st, x, largest, kLog2e);
-        typename Vec<T>::Count cnt;
-        if (base + CHUNK <= tvec) {
-#pragma unroll
-            for (int r = 0; r < VPT; ++r) cnt.ge(x[r], zw);
-        } else if (base >= tvec) {
-#pragma unroll
-            for (int r = 0; r < VPT; ++r) cnt.gt(x[r], zw);
-        } else {
-#pragma unroll
-            for (int r = 0; r < VPT; ++r) {
-                if (base + r * ROW_THREADS + (int)threadIdx.x < tvec)
-                    cnt.ge(x[r], zw);
-                else
-                    cnt.gt(x[r], zw);
-            }
-        }
-        before += cnt.total();
-    };
-    if (row.edges()) {
-        const uint4 e[1] = {row.load_edge(row.edge())};
-        raw = Vec<T>::largest(e);
-        soft_chunk<T, true>(st, e, raw, kLog2e);
-        typename Vec<T>::Count cnt;
-        if (row.edge() < tvec)
-            cnt.ge(e[0], zw);
-        else
-            cnt.gt(e[0], zw);
-        before += cnt.total();
-    }
-    for (int base = row.lo; base < rest; base += CHUNK) {
-        chunk(base);
-        if (base + CHUNK < rest)
-            row.load_chunk(base + CHUNK, x);
+    Peaks peaks{-INFINITY, -INFINITY, 0};
+    int t = -1;                                      // the target; -1: none, or out of range
+    auto zw = Vec<T>::wide(INFINITY);                // its logit; +inf: not counted in the loop
+    {
+        const Row<T, ROW_THREADS, LP_VPT> row(a.logits, row_i, a.ld, a.V, rank, log_split);
+        // the row's loads go out before anything waits for the target's
+        const int rest = row.rest();
+        if (row.lo < rest)
+            row.load_chunk(row.lo, x);
         else
             row.load_rest(rest, x);
+        const int64_t given = a.targets ? a.targets[row_i] : -1;
+        if (given >= 0 && given < a.V) {
+            t = (int)given;
+            const float z = to_f32(row.z[t]);
+            if (z > -INFINITY) zw = Vec<T>::wide(z);
+        }
+        // entries in front of the target: above it anywhere, equal to it before it.
+        // Vectors before the target's count equals; inside its own vector they
+        // are added below. A masked target is counted apart.
+        const int tvec = row.vector_of(t);
+        auto chunk = [&](int base) {
+            const float largest = Vec<T>::largest(x);
+            const bool better = largest > peaks.best;
+            peaks.other = max_nan(peaks.other, better ? peaks.best : largest);
+            peaks.best = better ? largest : peaks.best;
+            peaks.base = better ? base : peaks.base;
+            soft_chunk<T, true>(st, x, largest, kLog2e);
+            typename Vec<T>::Count cnt;
+            if (base + CHUNK <= tvec) {
+#pragma unroll
+                for (int r = 0; r < LP_VPT; ++r) cnt.ge(x[r], zw);
+            } else if (base >= tvec) {
+#pragma unroll
+                for (int r = 0; r < LP_VPT; ++r) cnt.gt(x[r], zw);
+            } else {
+#pragma unroll
+                for (int r = 0; r < LP_VPT; ++r) {
+                    if (base + r * ROW_THREADS + (int)threadIdx.x < tvec)
+                        cnt.ge(x[r], zw);
+                    else
+                        cnt.gt(x[r], zw);
+                }
+            }
+            before += cnt.total();
+        };
+        if (row.edges()) {
+            const uint4 e[1] = {row.load_edge(row.edge())};
+            peaks.other = Vec<T>::largest(e);
+            soft_chunk<T, true>(st, e, peaks.other, kLog2e);
+            typename Vec<T>::Count cnt;
+            if (row.edge() < tvec)
+                cnt.ge(e[0], zw);
+            else
+                cnt.gt(e[0], zw);
+            before += cnt.total();
+        }
+        for (int base = row.lo; base < rest; base += CHUNK) {
+            chunk(base);
+            if (base + CHUNK < rest)
+                row.load_chunk(base + CHUNK, x);
+            else
+                row.load_rest(rest, x);
+        }
+        if (rest < row.hi) chunk(rest);
     }
-    if (rest < row.hi) chunk(rest);
-    if (counted && threadIdx.x == 0 && row.mine((int)t))
-        for (int e = max(row.start(tvec), 0); e < (int)t; ++e) before += to_f32(row.z[e]) == zt;
-    if (good && !counted) {   // -inf (or NaN) given: every other entry is compared
+    // Once more, from an index the compiler takes for new: kept over the loop,
+    // the row's sizes would not fit the registers.
+    int64_t row_j = row_i;
+    asm volatile("" : "+l"(row_j));
+    const Row<T, ROW_THREADS, LP_VPT> row(a.logits, row_j, a.ld, a.V, rank, log_split);
+    const bool good = t >= 0, counted = good && Vec<T>::narrow(zw) < INFINITY;
+    const float zt = counted ? Vec<T>::narrow(zw) : -INFINITY;
+    if (counted && threadIdx.x == 0 && row.mine(t))
+        for (int e = max(row.start(row.vector_of(t)), 0); e < t; ++e) before += to_f32(row.z[e]) == zt;
+    if (good && !counted) {   // a masked target (or a NaN): every entry is compared
         before = 0;
+        const float z = to_f32(row.z[t]);
         for (int e = row.e_lo + (int)threadIdx.x; e < row.e_hi; e += ROW_THREADS) {
             const float v = to_f32(row.z[e]);
-            before += v > zt || (v == zt && e < (int)t);
+            before += v > z || (v == z && e < t);
         }
     }
     Part part = block_part(st, before, red, kLog2e);
-    if (a.K > 0) slice_top(row, a.K, raw, x, sh);
+    if (a.K > 0) slice_top(row, a.K, peaks, x, sh);
     if (split > 1) {
         cluster_wait();
         if (threadIdx.x == 0) send_part(parts, rank, 0u, part);
@@ -704,10 +740,10 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
     if (isnan(esum) && !isnan(d.s)) esum = slow_esum(row.z, a.V, d, redf);
     if (threadIdx.x == 0) {
         if (a.targets && !good) atomicCAS(err, 0, (int)TPMLP_ERR_ARG);
-        if (a.lse) a.lse[row_i] = d.lse();
-        if (a.entropy) a.entropy[row_i] = d.nothing ? 0.f : d.ln_s - esum / d.s;
-        if (a.logprob) a.logprob[row_i] = good ? d.ln_p(zt) : NAN;
-        if (a.rank) a.rank[row_i] = good ? part.before + 1 : 0;
+        if (a.lse) a.lse[row_j] = d.lse();
+        if (a.entropy) a.entropy[row_j] = d.nothing ? 0.f : d.ln_s - esum / d.s;
+        if (a.logprob) a.logprob[row_j] = good ? d.ln_p(zt) : NAN;
+        if (a.rank) a.rank[row_j] = good ? part.before + 1 : 0;
     }
     const unsigned long long* all = split > 1 ? sh.all : sh.list;
     const int m = split * a.K;
@@ -719,8 +755,8 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
             for (int j = 0; j < m; ++j) place += all[j] > key;
         }
         if (key != 0ull && place < a.K) {
-            a.top_ids[row_i * a.K + place] = (int32_t)(0xffffffffu - (uint32_t)key);
-            a.top_logprobs[row_i * a.K + place] = d.ln_p(order_value((uint32_t)(key >> 32)));
+            a.top_ids[row_j * a.K + place] = (int32_t)(0xffffffffu - (uint32_t)key);
+            a.top_logprobs[row_j * a.K + place] = d.ln_p(order_value((uint32_t)(key >> 32)));
         }
     }
 }
@@ -764,7 +800,7 @@ __device__ __forceinline__ LaneSlots load_slots(const int32_t* ids, const float*
 // need are loaded first, as they are before an in-place sweep.
 template <typename T, int NT>
 __device__ __forceinline__ void teacher_row(const DistillArgs& a, const int32_t* ids, const float* tl,
-                                            const LaneSlots& slots, const Row<T, NT>& row, bool loss, bool lists,
+                                            const LaneSlots& slots, const Row<T, NT, KD_VPT>& row, bool loss, bool lists,
                                             TeacherShared& sh) {
     const int lane = threadIdx.x;
     const float ct = kLog2e / a.tau;
@@ -882,7 +918,7 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_al
 template <typename T, int NT, bool LOSS, bool GRAD>
 __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArgs a, int log_split, int* err) {
     constexpr bool STAGE = LOSS && GRAD;
-    constexpr int WARPS = NT / 32, CHUNK = Row<T, NT>::CHUNK;
+    constexpr int WARPS = NT / 32, CHUNK = Row<T, NT, KD_VPT>::CHUNK;
     extern __shared__ uint4 stage[];   // STAGE: one chunk
     __shared__ WarpSoft parts[MAX_SPLIT * WARPS];
     __shared__ TeacherShared te;
@@ -891,7 +927,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
     const int rank = (int)(blockIdx.x & (unsigned)(split - 1));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (LOSS && split > 1) cluster_arrive();   // this CTA runs: its shared memory may be written
-    const Row<T, NT> row(a.logits, row_i, a.ld, a.V, rank, log_split);
+    const Row<T, NT, KD_VPT> row(a.logits, row_i, a.ld, a.V, rank, log_split);
     T* d = GRAD ? static_cast<T*>(a.dlogits) + row_i * a.ldd : nullptr;
     const int32_t* ids = a.ids + row_i * a.K;
     const float* tl = a.teacher + row_i * a.K;
@@ -909,14 +945,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
     live = __any_sync(0xffffffffu, live);
     for (int k = 32 * SLOTS; !live && k < a.K; k += 32)
         live = __any_sync(0xffffffffu, k + lane < a.K && counts(ids[k + lane], tl[k + lane]));
-    uint4 x[VPT];
+    uint4 x[KD_VPT];
     const int staged = STAGE && rest > row.lo ? rest - CHUNK : rest;   // where the chunk in shared memory starts
     const bool early = staged == row.lo;   // nothing is read through the registers before the last chunk
     if (live) {
         if (staged < rest) {
             const uint4* p = row.vectors() + staged + threadIdx.x;
 #pragma unroll
-            for (int r = 0; r < VPT; ++r) cp_async16(smem_u32(stage + r * NT + threadIdx.x), p + r * NT);
+            for (int r = 0; r < KD_VPT; ++r) cp_async16(smem_u32(stage + r * NT + threadIdx.x), p + r * NT);
         }
         if (early) row.load_rest(rest, x);
     }
@@ -939,7 +975,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
             if (staged < rest) {
                 cp_async_wait();
 #pragma unroll 1
-                for (int r = 0; r < VPT; r += 2) {
+                for (int r = 0; r < KD_VPT; r += 2) {
                     const uint4 y[2] = {stage[r * NT + threadIdx.x], stage[(r + 1) * NT + threadIdx.x]};
                     soft_chunk<T, false>(st, y, Vec<T>::largest(y), c);
                 }
@@ -1044,7 +1080,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
             // last is the likeliest to be in L2.
             if (!LOSS && !early) row.load_rest(rest, x);
 #pragma unroll
-            for (int r = 0; r < VPT; ++r) {
+            for (int r = 0; r < KD_VPT; ++r) {
                 const int i = rest + r * NT + (int)threadIdx.x;
                 if (i < row.hi) {
                     float v[Vec<T>::N];
@@ -1054,7 +1090,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
             }
             if (staged < rest) {
 #pragma unroll
-                for (int r = 0; r < VPT; ++r) {
+                for (int r = 0; r < KD_VPT; ++r) {
                     float v[Vec<T>::N];
                     gradient(stage[r * NT + threadIdx.x], v);
                     store(staged + r * NT + (int)threadIdx.x, v);
@@ -1063,7 +1099,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
             for (int base = staged - CHUNK; base >= row.lo; base -= CHUNK) {
                 row.load_chunk(base, x);
 #pragma unroll
-                for (int r = 0; r < VPT; ++r) {
+                for (int r = 0; r < KD_VPT; ++r) {
                     float v[Vec<T>::N];
                     gradient(x[r], v);
                     store(base + r * NT + (int)threadIdx.x, v);
@@ -1140,7 +1176,7 @@ tpmlp_status distill_launch(const DistillArgs& a, cudaStream_t s, int* err) {
         return launch_rows(distill_kernel<T, ROW_THREADS, false, true>, ROW_THREADS, 0, a.N, split, s, a,
                            split, err);
     }
-    constexpr int CHUNK = Row<T, ROW_THREADS>::CHUNK;
+    constexpr int CHUNK = Row<T, ROW_THREADS, KD_VPT>::CHUNK;
     const int split = row_split(a.N, bytes, ROW_THREADS, 2 * CHUNK);
     LaunchScope ls("vocab_distill_with_grad", s);
     return launch_rows(distill_kernel<T, ROW_THREADS, true, true>, ROW_THREADS, CHUNK * sizeof(uint4), a.N,
