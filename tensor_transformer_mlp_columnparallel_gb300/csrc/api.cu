@@ -719,16 +719,20 @@ tpmlp_status tpmlp_swiglu_backward(tpmlp_dtype dt, int64_t N, int64_t D, int64_t
             g2.epi.C[r] = dWd[r];
         }
         TPMLP_TRY(run_gemm(dt, g2, s, sk));
-        for (int half = 0; half < 2; ++half) {
-            GemmProblem g3 = problem((int)D, Fs, (int)N, T, 0, D, 1, Fs, 1,
-                                     half ? "bwd_gated_dwu_gemm" : "bwd_gated_dwg_gemm");
+        // gate and up as the groups of one launch where they fit
+        const int launches = 2 * T <= kMaxG ? 1 : 2;
+        for (int l = 0; l < launches; ++l) {
+            const int G = launches == 1 ? 2 * T : T;
+            GemmProblem g3 = problem((int)D, Fs, (int)N, G, 0, D, 1, Fs, 1, "bwd_gated_dwg_dwu_gemm");
             g3.epi.kind = EPI_STORE;
             g3.epi.out_f32 = f32;
             g3.epi.ldc = Fs;
-            for (int r = 0; r < T; ++r) {
-                g3.A[r] = X;
-                g3.B[r] = half ? dU[r] : dG[r];
-                g3.epi.C[r] = half ? dWu[r] : dWg[r];
+            for (int i = 0; i < G; ++i) {
+                const bool up = l * T + i >= T;
+                const int r = (l * T + i) % T;
+                g3.A[i] = X;
+                g3.B[i] = up ? dU[r] : dG[r];
+                g3.epi.C[i] = up ? dWu[r] : dWg[r];
             }
             TPMLP_TRY(run_gemm(dt, g3, s, sk));
         }

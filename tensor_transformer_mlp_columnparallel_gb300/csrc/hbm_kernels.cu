@@ -588,6 +588,7 @@ __global__ void __launch_bounds__(256) vocab_ce_bwd_kernel(const CEBwdParams p) 
 // mean of the per-token losses, one CTA, fixed summation order, fp64 accumulator
 __global__ void __launch_bounds__(1024) mean_kernel(const float* loss, int64_t N, float* out) {
     __shared__ double red[1024];
+    pdl_wait();
     double s = 0.0;
     for (int64_t i = threadIdx.x; i < N; i += 1024) s += (double)loss[i];
     red[threadIdx.x] = s;
@@ -888,11 +889,18 @@ tpmlp_status run_vocab_ce(int64_t N, int64_t V, int T, const float* logits,
 }
 
 tpmlp_status run_mean(const float* loss, int64_t N, float* out, cudaStream_t s) {
-    {
-        LaunchScope ls("loss_mean", s);
-        mean_kernel<<<1, 1024, 0, s>>>(loss, N, out);
-    }
-    return cudaGetLastError() == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
+    // waits in place for the losses, its launch hidden behind their kernel
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    LaunchScope ls("loss_mean", s);
+    return cudaLaunchKernelEx(&cfg, mean_kernel, loss, N, out) == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
 }
 
 tpmlp_status run_vocab_ce_backward(int64_t N, int64_t V, const float* logits,

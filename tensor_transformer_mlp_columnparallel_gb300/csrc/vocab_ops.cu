@@ -630,6 +630,8 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
     const int64_t row_i = blockIdx.x >> log_split;
     const int rank = (int)(blockIdx.x & (unsigned)(split - 1));
     if (split > 1) cluster_arrive();   // this CTA runs: its shared memory may be written
+    pdl_wait();
+    pdl_launch_dependents();
     constexpr int CHUNK = Row<T, ROW_THREADS, LP_VPT>::CHUNK;
     uint4 x[LP_VPT];
     Soft st{Vec<T>::lowest(), 0.f, 0.f};
@@ -927,6 +929,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
     const int rank = (int)(blockIdx.x & (unsigned)(split - 1));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (LOSS && split > 1) cluster_arrive();   // this CTA runs: its shared memory may be written
+    pdl_wait();
+    pdl_launch_dependents();
     const Row<T, NT, KD_VPT> row(a.logits, row_i, a.ld, a.V, rank, log_split);
     T* d = GRAD ? static_cast<T*>(a.dlogits) + row_i * a.ldd : nullptr;
     const int32_t* ids = a.ids + row_i * a.K;
@@ -1141,18 +1145,23 @@ tpmlp_status launch_rows(void (*kernel)(P...), int threads, size_t smem, int64_t
                          cudaStream_t s, A... args) {
     const int split = 1 << log_split;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3((unsigned)(N * split));
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
+    // the kernel waits for what runs before it, and lets what runs after it
+    // be launched while its last rows are on their way
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     if (split > 1) {
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)split;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)split;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
     }
     if (smem > 48 * 1024 &&
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
