@@ -74,7 +74,7 @@ class BlockLM:
             w -= (step * d.float()).to(w.dtype)
 
 
-def distil(steps=60, tokens=512, V=4096, D=256, F=1024, T=4, K=32, tau=1.5, rate=0.1, seed=0):
+def distil(steps=60, tokens=512, V=4096, D=256, F=1024, T=4, K=32, tau=1.5, rate=0.05, seed=0):
     """Returns (loss of each step, and before and after: mean log probability and
     median rank of the teacher's most likely tokens under the student, and the
     student's mean entropy)."""
@@ -93,14 +93,14 @@ def distil(steps=60, tokens=512, V=4096, D=256, F=1024, T=4, K=32, tau=1.5, rate
         return float(lp.mean()), float(rank.float().median()), float(entropy.mean())
 
     before, losses = score(), []
-    for _ in range(steps):
+    for i in range(steps):
         ids = batch()
         z_teacher, _ = teacher.forward(ids)
         _, _, _, top, top_lp = tp.vocab_logprobs(z_teacher, ids, T, top_k=K)
         logits, saved = student.forward(ids)
         _, mean, _, dlogits = tp.vocab_distill_with_grad(logits, top, top_lp, T, temperature=tau,
                                                          grad_scale=1.0 / tokens, in_place=True)
-        student.descend(student.backward(dlogits, saved), rate)
+        student.descend(student.backward(dlogits, saved), rate * (1 - i / steps))
         losses.append(mean)
     after = score()
     assert tp.tpmlp_check_device_error() == 0
