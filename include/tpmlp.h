@@ -435,6 +435,9 @@ size_t tpmlp_workspace_bytes(tpmlp_op op, tpmlp_dtype dt, int64_t N, int64_t D, 
  * - with more, a GEMM whose last wave of tiles would leave SMs idle cuts
  *   those tiles into equal K chunks run side by side and summed the same
  *   way;
+ * - the gated backward uses it for N > 64 alone, for the weight gradients (of
+ *   more tokens than its few-token launch takes) and dX; for N <= 64 its
+ *   balanced size is the required one;
  * - the backward's bias gradients (db1, db2), which run after its GEMMs,
  *   sum row chunks of contiguous column ranges into the scratch and then
  *   add the chunks in order.
