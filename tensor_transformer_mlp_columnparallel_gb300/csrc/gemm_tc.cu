@@ -1364,6 +1364,10 @@ struct SkShape {
     bool ok = false;
 };
 
+// Time of a 64-deep k-block of a 256-column tile, and of adding one chunk's
+// 128 x 256 partial rows (us, GB300).
+constexpr double kKbUs = 0.33, kJoinUs = 2.6;
+
 template <int BN, bool PAIR>
 SkShape sk_shape(const GemmProblem& pr, int64_t tiles, int64_t kb_total) {
     SkShape r;
@@ -1386,6 +1390,13 @@ SkShape sk_shape(const GemmProblem& pr, int64_t tiles, int64_t kb_total) {
         r.sk_tiles = tiles % P;
         int64_t chunks = P / r.sk_tiles;
         if (chunks > kb_total) chunks = kb_total;
+        // The tile's last unit adds the chunks' partial rows one after the other.
+        // With few tiles and a long K (the gated backward's dX of a narrow
+        // block) that would outlast the products: at most sqrt(products / join).
+        if (pr.chain) {
+            const double products = (double)kb_total * Cfg<BN, PAIR>::BK / BKB * kKbUs * BN / 256;
+            while (chunks > 2 && (double)chunks * chunks * kJoinUs * BN / 256 > products) --chunks;
+        }
         if (chunks < 2) return SkShape();
         r.parts = (int)(r.sk_tiles * chunks);
         r.dp_tiles = (int)(tiles - r.sk_tiles);
@@ -1630,6 +1641,9 @@ Plan choose_plan(const GemmProblem& pr) {
         const Cand& c = cands[i];
         if (c.pair && pr.M <= 128) continue;   // a pair covers 256 rows
         if (c.bn == 192 && (pr.M > KSPLIT_ROWS || pr.dual)) continue;
+        // the gated backward's epilogue moves four times what a plain one does,
+        // per thread where there is no staging: 128-column tiles fall behind pairs
+        if (c.bn == 128 && pr.epi.kind == EPI_DSWIGLU && pr.M > BM) continue;
         if (c.ks > 1 && (!pr.fold || pr.M > KSPLIT_ROWS || pr.dual || c.ks > kb_total)) continue;
         const int64_t tile_m = c.pair ? 256 : 128;
         const int64_t n_out = pr.dual ? c.bn / 2 : c.bn;   // outputs per tile along N
@@ -1655,7 +1669,9 @@ Plan choose_plan(const GemmProblem& pr) {
             if (!sh.ok) continue;
             if (pr.M > KSPLIT_ROWS) {
                 // full waves, then one K chunk of a part-wave tile per unit
-                const double part = ((double)sh.sk_units / sh.parts + kSkFillKb) / (double)kbt * kSkSlow;
+                double part = ((double)sh.sk_units / sh.parts + kSkFillKb) / (double)kbt * kSkSlow;
+                if (pr.chain)   // the joins, in tiles' time
+                    part += (double)sh.parts / sh.sk_tiles * kJoinUs / (kKbUs * (c.pair ? 2 : 1) * (double)kbt);
                 cost = ((double)(tiles / sh.units) + part) * 128.0 * c.bn / c.rate;
             } else {
                 const int64_t P = sh.units;
