@@ -494,21 +494,21 @@ struct Peaks {
 // The K-th largest of the 256
 // maxima is reached by K different entries, so only entries at or above it can
 // be in the list, and they sit with the threads whose maximum reaches it: K of
-// 256 unless maxima are equal. Their vectors are still in registers (one
-// chunk) or read again: of the chunk with the thread's maximum alone, unless
-// another of its chunks reaches the bound too. (Reading all of a thread's
-// vectors, K / 256 of the slice, from DRAM as a rule, took 45% of the kernel's
-// time at K = 20 and 8192 x 128000 bf16 logits; this way the list takes 14%.) The K-th
-// largest maximum comes in two steps: with g = ceil(K / warps), the least of
-// the warps' g-th largest maxima leaves a few dozen, and those are ranked by
-// counting.
+// 256 unless maxima are equal. Of their vectors those of the chunk with the
+// maximum are read again, spread over all threads, and a thread's others only
+// if one of them reaches the bound too. (Reading all of a thread's vectors,
+// K / 256 of the slice, from DRAM as a rule, took 45% of the kernel's time at
+// K = 20 and 8192 x 128000 bf16 logits, this way the list takes 14%; going
+// through the registers of the few threads, where the slice is one chunk,
+// took twice as long as reading it again.) The K-th largest maximum comes in
+// two steps: with g = ceil(K / warps), the least of the warps' g-th largest
+// maxima leaves a few dozen, and those are ranked by counting.
 // Where more than MAX_CAND entries reach the bound (a mask that leaves fewer
 // than K tokens, rows of equal values), the entries above it are taken alone
 // and equal ones follow by index; where even those are too many, K rounds
 // over the slice.
 template <typename T>
-__device__ void slice_top(const Row<T, ROW_THREADS, LP_VPT>& row, int K, const Peaks& peaks, const uint4 (&x)[LP_VPT],
-                          TopShared& sh) {
+__device__ void slice_top(const Row<T, ROW_THREADS, LP_VPT>& row, int K, const Peaks& peaks, TopShared& sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t mine = order32(max_nan(peaks.best, peaks.other));
     uint32_t left = mine, g_th = 0;
@@ -542,30 +542,20 @@ __device__ void slice_top(const Row<T, ROW_THREADS, LP_VPT>& row, int K, const P
     const int n = row.hi - row.lo;
     const int per = (n + ROW_THREADS - 1) / ROW_THREADS;   // vectors of a thread
     if (mine >= thr && row.edge() <= row.full) offer(row, row.edge(), row.load_edge(row.edge()), thr, false, sh);
-    if (n <= Row<T, ROW_THREADS, LP_VPT>::CHUNK) {
-        if (mine >= thr) {
-#pragma unroll
-            for (int r = 0; r < LP_VPT; ++r) {
-                const int i = row.lo + r * ROW_THREADS + (int)threadIdx.x;
-                if (i < row.hi) offer(row, i, x[r], thr, false, sh);
-            }
-        }
-    } else {
-        if (mine >= thr) {
-            if (order32(peaks.other) >= thr)
-                sh.whole_of[atomicAdd(&sh.n_whole, 1)] = (int)threadIdx.x;
-            else if (order32(peaks.best) >= thr)
-                sh.chunk_of[atomicAdd(&sh.n_chunk, 1)] = peaks.base + (int)threadIdx.x;
-        }
-        __syncthreads();
-        for (int a = threadIdx.x; a < sh.n_chunk * LP_VPT; a += ROW_THREADS) {
-            const int i = sh.chunk_of[a / LP_VPT] + (a % LP_VPT) * ROW_THREADS;
-            if (i < row.hi) offer(row, i, row.load(i), thr, false, sh);
-        }
-        for (int a = threadIdx.x; a < sh.n_whole * per; a += ROW_THREADS) {
-            const int i = row.lo + (a % per) * ROW_THREADS + sh.whole_of[a / per];
-            if (i < row.hi) offer(row, i, row.load(i), thr, false, sh);
-        }
+    if (mine >= thr) {
+        if (order32(peaks.other) >= thr)
+            sh.whole_of[atomicAdd(&sh.n_whole, 1)] = (int)threadIdx.x;
+        else if (order32(peaks.best) >= thr)
+            sh.chunk_of[atomicAdd(&sh.n_chunk, 1)] = peaks.base + (int)threadIdx.x;
+    }
+    __syncthreads();
+    for (int a = threadIdx.x; a < sh.n_chunk * LP_VPT; a += ROW_THREADS) {
+        const int i = sh.chunk_of[a / LP_VPT] + (a % LP_VPT) * ROW_THREADS;
+        if (i < row.hi) offer(row, i, row.load(i), thr, false, sh);
+    }
+    for (int a = threadIdx.x; a < sh.n_whole * per; a += ROW_THREADS) {
+        const int i = row.lo + (a % per) * ROW_THREADS + sh.whole_of[a / per];
+        if (i < row.hi) offer(row, i, row.load(i), thr, false, sh);
     }
     __syncthreads();
     int count = sh.n_cand;
@@ -720,7 +710,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
         }
     }
     Part part = block_part(st, before, red, kLog2e);
-    if (a.K > 0) slice_top(row, a.K, peaks, x, sh);
+    if (a.K > 0) slice_top(row, a.K, peaks, sh);
     if (split > 1) {
         cluster_wait();
         if (threadIdx.x == 0) send_part(parts, rank, 0u, part);
