@@ -292,7 +292,9 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_scatter_kernel(const SortAr
 constexpr int SPAN = 32;          // sorted positions of a block
 constexpr int GRAD_THREADS = 256;
 constexpr int GRAD_WARPS = GRAD_THREADS / 32;
-constexpr int GRAD_ROWS = 8;      // table rows of a CTA
+constexpr int GRAD_ROWS = 64;     // table rows of a CTA at most
+constexpr int GRAD_BYTES = 32768; // and of table, where rows are short
+constexpr int WARP_ROW = 4096;    // bytes of a table row up to which a warp takes it, not the CTA
 constexpr int JOIN_COLS = 128;    // columns of a CTA that joins pieces
 
 struct GradArgs {
@@ -303,6 +305,8 @@ struct GradArgs {
     float* pieces;                // [2 blocks][Hp]
     int64_t N, V, Vs, H, Hp;
     int blocks;                   // of SPAN positions
+    int rows;                     // table rows of a CTA
+    int by_warp;                  // a warp to a row
     int packs;                    // packs of a row
     int join_cols;                // CTAs per block that join pieces
     float scale;
@@ -385,14 +389,53 @@ __device__ __forceinline__ GT* table_row(const GradArgs& p, uint32_t v) {
     return static_cast<GT*>(p.dtable[k]) + (int64_t)(v - k * (uint32_t)p.Vs) * p.H;
 }
 
+// Zeros over a row that may begin anywhere, by `nt` threads: whole 16-byte
+// words, then the elements at the row's two ends.
+template <typename GT>
+__device__ __forceinline__ void zero_row(GT* dst, int H, int t, int nt) {
+    constexpr int N = 16 / (int)sizeof(GT);
+    const int off = (int)((16 - (reinterpret_cast<uintptr_t>(dst) & 15)) & 15) / (int)sizeof(GT);
+    const int head = min(off, H), body = (H - head) / N;
+    uint4* v = reinterpret_cast<uint4*>(dst + head);
+#pragma unroll 4
+    for (int c = t; c < body; c += nt) __stcs(v + c, make_uint4(0u, 0u, 0u, 0u));
+    const int ends = H - body * N;   // fewer than 2 N
+    if (t < ends) dst[t < head ? t : t + body * N] = from_f32<GT>(0.f);
+}
+
+// One row from its segment's tokens, by `nt` threads.
+template <typename T, int N, typename GT>
+__device__ __forceinline__ void sum_row(const GradArgs& p, GT* dst, const uint32_t* tok, int n, int t, int nt) {
+    for (int c = t; c < p.packs; c += nt) {
+        float acc[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[j] = 0.f;
+        add_rows<T, N>(p, tok, n, (int64_t)c * N, acc);
+        GT* at = dst + (int64_t)c * N;
+        Pack<GT, N> o;
+        if (p.accumulate) o = load_pack<GT, N>(at);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            o.v[j] = from_f32<GT>(p.accumulate ? fmaf(p.scale, acc[j], to_f32(o.v[j])) : p.scale * acc[j]);
+        if constexpr (N * sizeof(GT) == 32) {
+            const uint4* w = reinterpret_cast<const uint4*>(&o);
+            __stcs(reinterpret_cast<uint4*>(at), w[0]);
+            __stcs(reinterpret_cast<uint4*>(at) + 1, w[1]);
+        } else {
+            store_pack<GT, N>(at, o);
+        }
+    }
+}
+
 // Table rows from segments inside one block of positions (zeros where there is
-// none), and, in the grid's first CTAs, from the pieces of the others.
-template <typename T, int N, typename GT, int ZN>
+// none), and, in the grid's first CTAs, from the pieces of the others. Short
+// rows go to a warp each.
+template <typename T, int N, typename GT>
 __global__ void __launch_bounds__(GRAD_THREADS) embedding_grad_kernel(const GradArgs p) {
     pdl_wait();
     __shared__ float4 part[GRAD_WARPS][32];
     __shared__ int2 segs[GRAD_ROWS];
-    __shared__ uint32_t tok[GRAD_ROWS][SPAN];
+    __shared__ uint32_t tok[GRAD_WARPS][SPAN];
     const unsigned joins = (unsigned)p.blocks * (unsigned)p.join_cols;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x < joins) {
@@ -439,49 +482,34 @@ __global__ void __launch_bounds__(GRAD_THREADS) embedding_grad_kernel(const Grad
         }
         return;
     }
-    const int64_t v0 = (int64_t)(blockIdx.x - joins) * GRAD_ROWS;
-    if (threadIdx.x < GRAD_ROWS)
-        segs[threadIdx.x] = p.N > 0 && v0 + threadIdx.x < p.V ? p.seg[v0 + threadIdx.x] : make_int2(0, 0);
+    const int64_t v0 = (int64_t)(blockIdx.x - joins) * p.rows;
+    const int rows = (int)min((int64_t)p.rows, p.V - v0);
+    if ((int)threadIdx.x < rows) segs[threadIdx.x] = p.N > 0 ? p.seg[v0 + threadIdx.x] : make_int2(0, 0);
     __syncthreads();
-    {   // a warp per row: the row's tokens
-        const int2 sg = segs[warp];
+    if (!p.by_warp) {   // at most GRAD_WARPS rows: every row's tokens at once, a warp to a row
+        const int2 sg = warp < rows ? segs[warp] : make_int2(0, 0);
         if (sg.y - sg.x > lane && sg.x / SPAN == (sg.y - 1) / SPAN) tok[warp][lane] = p.sorted[sg.x + lane].y;
+        __syncthreads();
     }
-    __syncthreads();
-    for (int r = 0; r < GRAD_ROWS; ++r) {
-        if (v0 + r >= p.V) break;
+    for (int r = p.by_warp ? warp : 0; r < rows; r += p.by_warp ? GRAD_WARPS : 1) {
         const int2 sg = segs[r];
         const int n = sg.y - sg.x;
-        if (n == 0 && p.accumulate) continue;
         if (n > 0 && sg.x / SPAN != (sg.y - 1) / SPAN) continue;   // joined from pieces
+        if (n == 0 && p.accumulate) continue;
         GT* dst = table_row<GT>(p, (uint32_t)(v0 + r));
-        if (n == 0) {
-            Pack<GT, ZN> zero;
-#pragma unroll
-            for (int j = 0; j < ZN; ++j) zero.v[j] = from_f32<GT>(0.f);
-            const int packs = (int)(p.H / ZN);
-#pragma unroll 4
-            for (int c = threadIdx.x; c < packs; c += GRAD_THREADS) store_pack<GT, ZN>(dst + (int64_t)c * ZN, zero);
-            continue;
-        }
-        for (int c = threadIdx.x; c < p.packs; c += GRAD_THREADS) {
-            float acc[N];
-#pragma unroll
-            for (int j = 0; j < N; ++j) acc[j] = 0.f;
-            add_rows<T, N>(p, tok[r], n, (int64_t)c * N, acc);
-            GT* at = dst + (int64_t)c * N;
-            Pack<GT, N> o;
-            if (p.accumulate) o = load_pack<GT, N>(at);
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                o.v[j] = from_f32<GT>(p.accumulate ? fmaf(p.scale, acc[j], to_f32(o.v[j])) : p.scale * acc[j]);
-            if constexpr (N * sizeof(GT) == 32) {
-                const uint4* w = reinterpret_cast<const uint4*>(&o);
-                __stcs(reinterpret_cast<uint4*>(at), w[0]);
-                __stcs(reinterpret_cast<uint4*>(at) + 1, w[1]);
-            } else {
-                store_pack<GT, N>(at, o);
+        if (p.by_warp) {
+            if (n == 0) {
+                zero_row(dst, (int)p.H, lane, 32);
+                continue;
             }
+            __syncwarp();
+            if (lane < n) tok[warp][lane] = p.sorted[sg.x + lane].y;
+            __syncwarp();
+            sum_row<T, N, GT>(p, dst, tok[warp], n, lane, 32);
+        } else if (n == 0) {
+            zero_row(dst, (int)p.H, (int)threadIdx.x, GRAD_THREADS);
+        } else {
+            sum_row<T, N, GT>(p, dst, tok[r], n, (int)threadIdx.x, GRAD_THREADS);
         }
     }
 }
@@ -536,7 +564,7 @@ cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, size_t smem
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <typename T, int N, typename GT, int ZN>
+template <typename T, int N, typename GT>
 cudaError_t grad_launch(const GradArgs& g, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
     if (g.N > 0) {
@@ -547,19 +575,18 @@ cudaError_t grad_launch(const GradArgs& g, cudaStream_t s) {
     }
     if (e != cudaSuccess) return e;
     LaunchScope ls("embedding_grad", s);
-    const int64_t grid = (int64_t)g.blocks * g.join_cols + (g.V + GRAD_ROWS - 1) / GRAD_ROWS;
-    return launch_pdl(embedding_grad_kernel<T, N, GT, ZN>, dim3((unsigned)grid), GRAD_THREADS, 0, s, g);
+    const int64_t grid = (int64_t)g.blocks * g.join_cols + (g.V + g.rows - 1) / g.rows;
+    return launch_pdl(embedding_grad_kernel<T, N, GT>, dim3((unsigned)grid), GRAD_THREADS, 0, s, g);
 }
 
 template <typename T, typename GT>
-cudaError_t grad_dispatch(const GradArgs& g, int n, int zn, cudaStream_t s) {
-    constexpr int Z = 16 / (int)sizeof(GT);
+cudaError_t grad_dispatch(const GradArgs& g, int n, cudaStream_t s) {
     if (n == 8) {
-        if constexpr (sizeof(T) == 2) return grad_launch<T, 8, GT, Z>(g, s);
+        if constexpr (sizeof(T) == 2) return grad_launch<T, 8, GT>(g, s);
     }
-    if (n == 4) return zn == Z ? grad_launch<T, 4, GT, Z>(g, s) : grad_launch<T, 4, GT, 4>(g, s);
-    if (n == 2) return grad_launch<T, 2, GT, 2>(g, s);
-    return grad_launch<T, 1, GT, 1>(g, s);
+    if (n >= 4) return grad_launch<T, 4, GT>(g, s);
+    if (n == 2) return grad_launch<T, 2, GT>(g, s);
+    return grad_launch<T, 1, GT>(g, s);
 }
 
 template <typename T>
@@ -696,17 +723,21 @@ tpmlp_status run_vocab_embedding_backward(int f32, int grad_f32, int64_t N, int6
     g.blocks = (int)grad_blocks(N);
     g.packs = (int)(H / n);
     g.join_cols = (int)((H + JOIN_COLS - 1) / JOIN_COLS);
+    // long rows: eight a CTA, all its threads on one after the other
+    const int64_t row_bytes = H * gsize;
+    g.by_warp = row_bytes <= WARP_ROW;
+    g.rows = !g.by_warp ? GRAD_WARPS : row_bytes * GRAD_ROWS <= GRAD_BYTES ? GRAD_ROWS : (int)(GRAD_BYTES / row_bytes);
     g.scale = scale;
     g.accumulate = accumulate;
-    if ((int64_t)g.blocks * g.join_cols + V / GRAD_ROWS + 1 > 0x7fffffffLL ||
+    if ((int64_t)g.blocks * g.join_cols + V / GRAD_WARPS + 1 > 0x7fffffffLL ||
         (g.packs + GRAD_THREADS - 1) / GRAD_THREADS > 65535)
         return TPMLP_ERR_SHAPE;
     cudaError_t e;
     if (f32)
-        e = grad_f32 ? grad_dispatch<float, float>(g, n, zn, s) : grad_dispatch<float, __nv_bfloat16>(g, n, zn, s);
+        e = grad_f32 ? grad_dispatch<float, float>(g, n, s) : grad_dispatch<float, __nv_bfloat16>(g, n, s);
     else
-        e = grad_f32 ? grad_dispatch<__nv_bfloat16, float>(g, n, zn, s)
-                     : grad_dispatch<__nv_bfloat16, __nv_bfloat16>(g, n, zn, s);
+        e = grad_f32 ? grad_dispatch<__nv_bfloat16, float>(g, n, s)
+                     : grad_dispatch<__nv_bfloat16, __nv_bfloat16>(g, n, s);
     return e == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
 }
 

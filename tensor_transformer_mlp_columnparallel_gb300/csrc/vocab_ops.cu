@@ -27,8 +27,7 @@ namespace {
 
 constexpr int ROW_THREADS = 256;
 constexpr int ROW_WARPS = ROW_THREADS / 32;
-constexpr int LP_VPT = 7;                     // 16-byte vectors a thread holds: log probabilities
-constexpr int KD_VPT = 8;                     // and distillation
+constexpr int VPT = 8;                        // 16-byte vectors a thread holds
 constexpr int MAX_SPLIT = 8;                  // CTAs of a row (the portable cluster size)
 constexpr float kLowest = -3.402823466e38f;   // FLT_MAX's negative
 constexpr float kLog2e = 1.4426950408889634f;
@@ -203,7 +202,7 @@ template <> struct Vec<float> {
 // -inf for what lies outside the row. The row's CTA `rank` owns the whole
 // vectors [lo, hi), elements [e_lo, e_hi): the first CTA with the front
 // edge, the last with the back edge.
-template <typename T, int NT, int VPT>
+template <typename T, int NT>
 struct Row {
     using V4 = Vec<T>;
     static constexpr int CHUNK = NT * VPT;   // vectors the CTA's registers hold
@@ -469,7 +468,7 @@ struct TopShared {
 // The elements of vector i that are in the row and at least `thr` (strictly
 // above with `above`) join the candidates; beyond MAX_CAND they are only counted.
 template <typename T>
-__device__ __forceinline__ void offer(const Row<T, ROW_THREADS, LP_VPT>& row, int i, const uint4& x, uint32_t thr, bool above,
+__device__ __forceinline__ void offer(const Row<T, ROW_THREADS>& row, int i, const uint4& x, uint32_t thr, bool above,
                                       TopShared& sh) {
     const int e0 = row.start(i);
 #pragma unroll
@@ -508,7 +507,7 @@ struct Peaks {
 // and equal ones follow by index; where even those are too many, K rounds
 // over the slice.
 template <typename T>
-__device__ void slice_top(const Row<T, ROW_THREADS, LP_VPT>& row, int K, const Peaks& peaks, TopShared& sh) {
+__device__ void slice_top(const Row<T, ROW_THREADS>& row, int K, const Peaks& peaks, TopShared& sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t mine = order32(max_nan(peaks.best, peaks.other));
     uint32_t left = mine, g_th = 0;
@@ -549,8 +548,8 @@ __device__ void slice_top(const Row<T, ROW_THREADS, LP_VPT>& row, int K, const P
             sh.chunk_of[atomicAdd(&sh.n_chunk, 1)] = peaks.base + (int)threadIdx.x;
     }
     __syncthreads();
-    for (int a = threadIdx.x; a < sh.n_chunk * LP_VPT; a += ROW_THREADS) {
-        const int i = sh.chunk_of[a / LP_VPT] + (a % LP_VPT) * ROW_THREADS;
+    for (int a = threadIdx.x; a < sh.n_chunk * VPT; a += ROW_THREADS) {
+        const int i = sh.chunk_of[a / VPT] + (a % VPT) * ROW_THREADS;
         if (i < row.hi) offer(row, i, row.load(i), thr, false, sh);
     }
     for (int a = threadIdx.x; a < sh.n_whole * per; a += ROW_THREADS) {
@@ -622,15 +621,15 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
     if (split > 1) cluster_arrive();   // this CTA runs: its shared memory may be written
     pdl_wait();
     pdl_launch_dependents();
-    constexpr int CHUNK = Row<T, ROW_THREADS, LP_VPT>::CHUNK;
-    uint4 x[LP_VPT];
+    constexpr int CHUNK = Row<T, ROW_THREADS>::CHUNK;
+    uint4 x[VPT];
     Soft st{Vec<T>::lowest(), 0.f, 0.f};
     int before = 0;
     Peaks peaks{-INFINITY, -INFINITY, 0};
     int t = -1;                                      // the target; -1: none, or out of range
     auto zw = Vec<T>::wide(INFINITY);                // its logit; +inf: not counted in the loop
     {
-        const Row<T, ROW_THREADS, LP_VPT> row(a.logits, row_i, a.ld, a.V, rank, log_split);
+        const Row<T, ROW_THREADS> row(a.logits, row_i, a.ld, a.V, rank, log_split);
         // the row's loads go out before anything waits for the target's
         const int rest = row.rest();
         if (row.lo < rest)
@@ -657,13 +656,13 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
             typename Vec<T>::Count cnt;
             if (base + CHUNK <= tvec) {
 #pragma unroll
-                for (int r = 0; r < LP_VPT; ++r) cnt.ge(x[r], zw);
+                for (int r = 0; r < VPT; ++r) cnt.ge(x[r], zw);
             } else if (base >= tvec) {
 #pragma unroll
-                for (int r = 0; r < LP_VPT; ++r) cnt.gt(x[r], zw);
+                for (int r = 0; r < VPT; ++r) cnt.gt(x[r], zw);
             } else {
 #pragma unroll
-                for (int r = 0; r < LP_VPT; ++r) {
+                for (int r = 0; r < VPT; ++r) {
                     if (base + r * ROW_THREADS + (int)threadIdx.x < tvec)
                         cnt.ge(x[r], zw);
                     else
@@ -696,7 +695,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
     // the row's sizes would not fit the registers.
     int64_t row_j = row_i;
     asm volatile("" : "+l"(row_j));
-    const Row<T, ROW_THREADS, LP_VPT> row(a.logits, row_j, a.ld, a.V, rank, log_split);
+    const Row<T, ROW_THREADS> row(a.logits, row_j, a.ld, a.V, rank, log_split);
     const bool good = t >= 0, counted = good && Vec<T>::narrow(zw) < INFINITY;
     const float zt = counted ? Vec<T>::narrow(zw) : -INFINITY;
     if (counted && threadIdx.x == 0 && row.mine(t))
@@ -792,7 +791,7 @@ __device__ __forceinline__ LaneSlots load_slots(const int32_t* ids, const float*
 // need are loaded first, as they are before an in-place sweep.
 template <typename T, int NT>
 __device__ __forceinline__ void teacher_row(const DistillArgs& a, const int32_t* ids, const float* tl,
-                                            const LaneSlots& slots, const Row<T, NT, KD_VPT>& row, bool loss, bool lists,
+                                            const LaneSlots& slots, const Row<T, NT>& row, bool loss, bool lists,
                                             TeacherShared& sh) {
     const int lane = threadIdx.x;
     const float ct = kLog2e / a.tau;
@@ -910,7 +909,7 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_al
 template <typename T, int NT, bool LOSS, bool GRAD>
 __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArgs a, int log_split, int* err) {
     constexpr bool STAGE = LOSS && GRAD;
-    constexpr int WARPS = NT / 32, CHUNK = Row<T, NT, KD_VPT>::CHUNK;
+    constexpr int WARPS = NT / 32, CHUNK = Row<T, NT>::CHUNK;
     extern __shared__ uint4 stage[];   // STAGE: one chunk
     __shared__ WarpSoft parts[MAX_SPLIT * WARPS];
     __shared__ TeacherShared te;
@@ -921,7 +920,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
     if (LOSS && split > 1) cluster_arrive();   // this CTA runs: its shared memory may be written
     pdl_wait();
     pdl_launch_dependents();
-    const Row<T, NT, KD_VPT> row(a.logits, row_i, a.ld, a.V, rank, log_split);
+    const Row<T, NT> row(a.logits, row_i, a.ld, a.V, rank, log_split);
     T* d = GRAD ? static_cast<T*>(a.dlogits) + row_i * a.ldd : nullptr;
     const int32_t* ids = a.ids + row_i * a.K;
     const float* tl = a.teacher + row_i * a.K;
@@ -939,14 +938,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
     live = __any_sync(0xffffffffu, live);
     for (int k = 32 * SLOTS; !live && k < a.K; k += 32)
         live = __any_sync(0xffffffffu, k + lane < a.K && counts(ids[k + lane], tl[k + lane]));
-    uint4 x[KD_VPT];
+    uint4 x[VPT];
     const int staged = STAGE && rest > row.lo ? rest - CHUNK : rest;   // where the chunk in shared memory starts
     const bool early = staged == row.lo;   // nothing is read through the registers before the last chunk
     if (live) {
         if (staged < rest) {
             const uint4* p = row.vectors() + staged + threadIdx.x;
 #pragma unroll
-            for (int r = 0; r < KD_VPT; ++r) cp_async16(smem_u32(stage + r * NT + threadIdx.x), p + r * NT);
+            for (int r = 0; r < VPT; ++r) cp_async16(smem_u32(stage + r * NT + threadIdx.x), p + r * NT);
         }
         if (early) row.load_rest(rest, x);
     }
@@ -969,7 +968,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
             if (staged < rest) {
                 cp_async_wait();
 #pragma unroll 1
-                for (int r = 0; r < KD_VPT; r += 2) {
+                for (int r = 0; r < VPT; r += 2) {
                     const uint4 y[2] = {stage[r * NT + threadIdx.x], stage[(r + 1) * NT + threadIdx.x]};
                     soft_chunk<T, false>(st, y, Vec<T>::largest(y), c);
                 }
@@ -1074,7 +1073,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
             // last is the likeliest to be in L2.
             if (!LOSS && !early) row.load_rest(rest, x);
 #pragma unroll
-            for (int r = 0; r < KD_VPT; ++r) {
+            for (int r = 0; r < VPT; ++r) {
                 const int i = rest + r * NT + (int)threadIdx.x;
                 if (i < row.hi) {
                     float v[Vec<T>::N];
@@ -1084,7 +1083,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
             }
             if (staged < rest) {
 #pragma unroll
-                for (int r = 0; r < KD_VPT; ++r) {
+                for (int r = 0; r < VPT; ++r) {
                     float v[Vec<T>::N];
                     gradient(stage[r * NT + threadIdx.x], v);
                     store(staged + r * NT + (int)threadIdx.x, v);
@@ -1093,7 +1092,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
             for (int base = staged - CHUNK; base >= row.lo; base -= CHUNK) {
                 row.load_chunk(base, x);
 #pragma unroll
-                for (int r = 0; r < KD_VPT; ++r) {
+                for (int r = 0; r < VPT; ++r) {
                     float v[Vec<T>::N];
                     gradient(x[r], v);
                     store(base + r * NT + (int)threadIdx.x, v);
@@ -1175,7 +1174,7 @@ tpmlp_status distill_launch(const DistillArgs& a, cudaStream_t s, int* err) {
         return launch_rows(distill_kernel<T, ROW_THREADS, false, true>, ROW_THREADS, 0, a.N, split, s, a,
                            split, err);
     }
-    constexpr int CHUNK = Row<T, ROW_THREADS, KD_VPT>::CHUNK;
+    constexpr int CHUNK = Row<T, ROW_THREADS>::CHUNK;
     const int split = row_split(a.N, bytes, ROW_THREADS, 2 * CHUNK);
     LaunchScope ls("vocab_distill_with_grad", s);
     return launch_rows(distill_kernel<T, ROW_THREADS, true, true>, ROW_THREADS, CHUNK * sizeof(uint4), a.N,
