@@ -197,6 +197,14 @@ size_t dz_bytes(tpmlp_dtype dt, int64_t N, int64_t Fs, int T) {
     return (size_t)T * round256((size_t)N * Fs * (dt == TPMLP_BF16 ? 2 : 4));
 }
 
+// The gated backward of a few bf16 tokens also keeps what rounding dG and dU
+// left over, for dWg and dWu. A gradient made from rounded factors is off by
+// their rounding on top of its own, 1.4 times the latter over many terms and
+// 1.6 times where a few terms rule the sum (N = 2, F = 1984); with both parts
+// it is rounded once. They cost no time there, as writing the gradients bounds
+// the launch (D = 4096, F = 14336, N = 16: 67 us with and without).
+bool keeps_rest(tpmlp_dtype dt, int64_t N) { return dt == TPMLP_BF16 && N <= 64; }
+
 // Optional scratch of the bf16 GEMMs' stream-K form
 // (tpmlp_workspace_bytes_balanced): per-tile arrival counters, then fp32
 // partial-accumulator slots, two per CTA.
@@ -298,7 +306,7 @@ size_t tpmlp_workspace_bytes(tpmlp_op op, tpmlp_dtype dt, int64_t N, int64_t D, 
     const size_t part = mode == TPMLP_REDUCE_PARTIALS ? partials_bytes(N, D, T) : 0;
     if (op == TPMLP_OP_FORWARD) return part;
     if (op == TPMLP_OP_BACKWARD) return dz_bytes(dt, N, F / T, T) + part;
-    if (op == TPMLP_OP_SWIGLU_BACKWARD) return 2 * dz_bytes(dt, N, F / T, T) + part;
+    if (op == TPMLP_OP_SWIGLU_BACKWARD) return (keeps_rest(dt, N) ? 4 : 2) * dz_bytes(dt, N, F / T, T) + part;
     return (size_t)-1;
 }
 
@@ -676,6 +684,7 @@ tpmlp_status tpmlp_swiglu_backward(tpmlp_dtype dt, int64_t N, int64_t D, int64_t
         sk_area(workspace, workspace_bytes, need, dt, N, D, F, T, TPMLP_OP_SWIGLU_BACKWARD);
 
     const size_t d_stride = round256((size_t)N * Fs * esz);
+    const size_t rest = keeps_rest(dt, N) ? 2 * T * d_stride : 0;   // from a shard's dG (dU) to what its rounding left
     void *dG[kMaxG], *dU[kMaxG];
     for (int r = 0; r < T; ++r) {
         dG[r] = static_cast<char*>(workspace) + r * d_stride;
@@ -691,6 +700,7 @@ tpmlp_status tpmlp_swiglu_backward(tpmlp_dtype dt, int64_t N, int64_t D, int64_t
     g1.epi.out_f32 = f32;
     g1.epi.ldc = Fs;
     g1.epi.ldaux = Fs;
+    g1.epi.lo_off = (int64_t)rest;
     for (int r = 0; r < T; ++r) {
         g1.A[r] = dY;
         g1.B[r] = Wd[r];
@@ -706,9 +716,10 @@ tpmlp_status tpmlp_swiglu_backward(tpmlp_dtype dt, int64_t N, int64_t D, int64_t
         // few tokens: writing the gradients bounds it
         WeightGradProduct w[kMaxWeightGrads];
         int n = 0;
-        for (int r = 0; r < T; ++r) w[n++] = WeightGradProduct{H[r], dY, dWd[r], Fs, D, D, Fs, (int)D};
-        for (int r = 0; r < T; ++r) w[n++] = WeightGradProduct{X, dG[r], dWg[r], D, Fs, Fs, (int)D, Fs};
-        for (int r = 0; r < T; ++r) w[n++] = WeightGradProduct{X, dU[r], dWu[r], D, Fs, Fs, (int)D, Fs};
+        auto left = [&](void* x) { return rest > 0 ? static_cast<char*>(x) + rest : nullptr; };
+        for (int r = 0; r < T; ++r) w[n++] = WeightGradProduct{H[r], dY, nullptr, dWd[r], Fs, D, D, Fs, (int)D};
+        for (int r = 0; r < T; ++r) w[n++] = WeightGradProduct{X, dG[r], left(dG[r]), dWg[r], D, Fs, Fs, (int)D, Fs};
+        for (int r = 0; r < T; ++r) w[n++] = WeightGradProduct{X, dU[r], left(dU[r]), dWu[r], D, Fs, Fs, (int)D, Fs};
         TPMLP_TRY(run_weight_grads(w, n, (int)N, s, "bwd_gated_weight_grads"));
     } else {
         // A(m, k) = H^(r)[k, m] or X[k, m] (MN-major), B(k, n) = dY, dG or dU[k, n]
@@ -758,7 +769,7 @@ tpmlp_status tpmlp_swiglu_backward(tpmlp_dtype dt, int64_t N, int64_t D, int64_t
         g4.B2[r] = Wu[r];
         if (!split) {
             float* pr = reinterpret_cast<float*>(static_cast<char*>(workspace) + 2 * T * d_stride +
-                                                 r * pstride);
+                                                 rest + r * pstride);
             g4.epi.C[r] = pr;
             parts[r] = pr;
         }

@@ -357,21 +357,28 @@ __device__ __forceinline__ void pack_row_bf16(const float (&v)[32], uint4 (&w)[4
 }
 
 // Gated-MLP backward epilogue of one thread: v = dH over 32 columns from col0
-// of row `row`; dG replaces v, dU goes to C2 (G and U read, all per thread).
+// of row `row`; dG replaces v, dU goes to C2 (G and U read, all per thread),
+// and what their rounding leaves over behind both if asked for.
 __device__ __forceinline__ void epilogue_dswiglu_thread(const EpiArgs& e, int g, int row, int col0,
                                                         int M, int N, float (&v)[32]) {
     if (row >= M) return;
     const int64_t off = (int64_t)row * e.ldaux + col0;
     const __nv_bfloat16* ga = static_cast<const __nv_bfloat16*>(e.aux[g]) + off;
     const __nv_bfloat16* ua = static_cast<const __nv_bfloat16*>(e.aux2[g]) + off;
-    __nv_bfloat16* du = static_cast<__nv_bfloat16*>(e.C2[g]) + (int64_t)row * e.ldc + col0;
+    const int64_t out = (int64_t)row * e.ldc + col0;
+    __nv_bfloat16* du = static_cast<__nv_bfloat16*>(e.C2[g]) + out;
+    auto left = [](float x, uint32_t rounded, bool hi) {
+        return x - __uint_as_float(hi ? rounded & 0xffff0000u : rounded << 16);
+    };
+    __nv_bfloat16* dg_lo = reinterpret_cast<__nv_bfloat16*>(static_cast<char*>(e.C[g]) + e.lo_off) + out;
+    __nv_bfloat16* du_lo = reinterpret_cast<__nv_bfloat16*>(static_cast<char*>(e.C2[g]) + e.lo_off) + out;
     if (col0 + 32 <= N) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const uint4 gw = *(reinterpret_cast<const uint4*>(ga) + q);
             const uint4 uw = *(reinterpret_cast<const uint4*>(ua) + q);
             const uint32_t gs[4] = {gw.x, gw.y, gw.z, gw.w}, us[4] = {uw.x, uw.y, uw.z, uw.w};
-            uint32_t o[4];
+            uint32_t o[4], gl[4], ul[4];
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
                 const int j = q * 8 + 2 * h;
@@ -381,8 +388,15 @@ __device__ __forceinline__ void epilogue_dswiglu_thread(const EpiArgs& e, int g,
                 dswiglu_bf16(v[j], g0, u0, v[j], d0);
                 dswiglu_bf16(v[j + 1], g1, u1, v[j + 1], d1);
                 o[h] = pack_bf16x2(d0, d1);
+                const uint32_t r = pack_bf16x2(v[j], v[j + 1]);
+                gl[h] = pack_bf16x2(left(v[j], r, false), left(v[j + 1], r, true));
+                ul[h] = pack_bf16x2(left(d0, o[h], false), left(d1, o[h], true));
             }
             reinterpret_cast<uint4*>(du)[q] = make_uint4(o[0], o[1], o[2], o[3]);
+            if (e.lo_off > 0) {
+                reinterpret_cast<uint4*>(dg_lo)[q] = make_uint4(gl[0], gl[1], gl[2], gl[3]);
+                reinterpret_cast<uint4*>(du_lo)[q] = make_uint4(ul[0], ul[1], ul[2], ul[3]);
+            }
         }
     } else {
 #pragma unroll
@@ -391,6 +405,10 @@ __device__ __forceinline__ void epilogue_dswiglu_thread(const EpiArgs& e, int g,
                 float d;
                 dswiglu_bf16(v[j], bf2f(ga[j]), bf2f(ua[j]), v[j], d);
                 du[j] = __float2bfloat16_rn(d);
+                if (e.lo_off > 0) {
+                    dg_lo[j] = __float2bfloat16_rn(v[j] - bf2f(__float2bfloat16_rn(v[j])));
+                    du_lo[j] = __float2bfloat16_rn(d - bf2f(__float2bfloat16_rn(d)));
+                }
             }
     }
 }
@@ -1519,7 +1537,7 @@ tpmlp_status launch(const GemmProblem& pr, cudaStream_t s, int ks = 1) {
     // configuration has room for the staging and every output has a map (not
     // the gated epilogue, nor the reduce-scatter's row blocks)
     kp.tma_out = 0;
-    if (C::TMA_OUT && pr.epi.kind == EPI_DSWIGLU && !pr.dual && !pr.chain && !pr.fold) {
+    if (C::TMA_OUT && pr.epi.kind == EPI_DSWIGLU && pr.epi.lo_off == 0 && !pr.dual && !pr.chain && !pr.fold) {
         bool ok = true;
         for (int g = 0; g < G && ok; ++g)
             ok = make_map_out_pair(&kp.tmC[g], pr.epi.C[g], pr.epi.C2[g], pr.N, pr.M, pr.epi.ldc) &&

@@ -32,6 +32,9 @@ struct EpiArgs {
     void* aux[kMaxG];          // Z (compute element type), see EpiKind
     void* aux2[kMaxG];         // U of EPI_SWIGLU and EPI_DSWIGLU
     void* C2[kMaxG];           // dU of EPI_DSWIGLU, row pitch ldc
+    // EPI_DSWIGLU, > 0: what rounding dG and dU to bf16 left over, itself in
+    // bf16, this many bytes behind C and C2
+    int64_t lo_off;
     // > 0: C is split by rows into blocks of row_shard rows, block i at C[i]
     // (the reduce-scatter output of the block end); 0: C[g] as above
     int64_t row_shard;
@@ -87,12 +90,13 @@ tpmlp_status plan_gemm_tc(const GemmProblem& p, int* bn, int* mma_ctas, int* ksp
 // fp32 inputs on CUDA cores (exact fp32 FMA, no TF32).
 tpmlp_status run_gemm_simt(const GemmProblem& p, cudaStream_t s);
 
-// bf16 weight gradients C[m, n] = sum_{k < K} A[k, m] B[k, n] of a few tokens k
-// (M and N multiples of 8, pointers and pitches of 16 bytes), all products of
-// the list in one launch.
+// bf16 weight gradients C[m, n] = sum_{k < K} A[k, m] (B + B2)[k, n] of few tokens
+// k (M and N multiples of 8, pointers and pitches of 16 bytes; B2 NULL: none),
+// all products of the list in one launch.
 struct WeightGradProduct {
     const void* A;
     const void* B;
+    const void* B2;
     void* C;
     int64_t lda, ldb, ldc;
     int M, N;

@@ -1,6 +1,7 @@
-// Weight gradients of few tokens: C[m, n] = sum_{k < K} A[k, m] B[k, n] in bf16
-// with K (tokens) small against M and N, for a list of such products in one
-// launch.
+// Weight gradients of few tokens: C[m, n] = sum_{k < K} A[k, m] (B + B2)[k, n] in
+// bf16 with K (tokens) small against M and N, for a list of such products in
+// one launch. B2 is what B's rounding to bf16 left over (or absent): a second
+// walk over the tokens into the same accumulator.
 //
 // Writing C bounds it: at K = 16 a 128 x 256 tile reads 12 KB of operands
 // (from L2) for 64 KB of output, and its product is one K step. So the CTA is
@@ -35,8 +36,9 @@ constexpr int WG_SMEM = 1024 + WG_STAGES * WG_STAGE + WG_EPI_WARPS * 2 * WG_OUT 
 static_assert(WG_SMEM <= 232448, "shared memory");
 
 struct WgParams {
-    CUtensorMap maps[3 * kMaxWeightGrads];      // operands, then outputs
+    CUtensorMap maps[4 * kMaxWeightGrads];      // operands and outputs
     int16_t a_map[kMaxWeightGrads], b_map[kMaxWeightGrads], c_map[kMaxWeightGrads];
+    int16_t b2_map[kMaxWeightGrads];            // -1: none
     int M[kMaxWeightGrads], N[kMaxWeightGrads];
     int first_tile[kMaxWeightGrads + 1];        // tiles in front of each product
     int products, K, bk;                        // bk: tokens of a stage (a multiple of 16)
@@ -112,8 +114,10 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_kernel(const __grid
             for (int t = (int)blockIdx.x; ok && t < tiles; t += (int)gridDim.x) {
                 const WgTile w = wg_tile(p, t);
                 const CUtensorMap* ma = &p.maps[p.a_map[w.q]];
-                const CUtensorMap* mb = &p.maps[p.b_map[w.q]];
-                for (int kb = 0; kb < k_blocks; ++kb) {
+                const int walks = p.b2_map[w.q] >= 0 ? 2 : 1;
+                for (int i = 0; i < k_blocks * walks; ++i) {
+                    const CUtensorMap* mb = &p.maps[i < k_blocks ? p.b_map[w.q] : p.b2_map[w.q]];
+                    const int kb = i < k_blocks ? i : i - k_blocks;
                     if (!wait_fast(bar(EMPTY + s), ph ^ 1u, abort_flag, p.err, p.timeout_ns, true)) {
                         ok = false;
                         break;
@@ -149,7 +153,9 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_kernel(const __grid
             for (int t = (int)blockIdx.x; ok && t < tiles; t += (int)gridDim.x) {
                 if (!wait_fast(bar(TEMPTY + acc), aph ^ 1u, abort_flag, p.err, p.timeout_ns, true)) break;
                 tc_fence_after();
-                for (int kb = 0; kb < k_blocks; ++kb) {
+                const int walks = p.b2_map[wg_tile(p, t).q] >= 0 ? 2 : 1;
+                for (int i = 0; i < k_blocks * walks; ++i) {
+                    const int kb = i < k_blocks ? i : i - k_blocks;
                     if (!wait_fast(bar(FULL + s), ph, abort_flag, p.err, p.timeout_ns, true)) {
                         ok = false;
                         break;
@@ -159,7 +165,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_kernel(const __grid
                     const int steps = (min(p.bk, p.K - kb * p.bk) + 15) / 16;
                     for (int k = 0; k < steps; ++k)   // 16 rows of 128 bytes a step
                         tc_mma_f16(tmem + (uint32_t)(acc * WG_N), da + off + (uint64_t)(k * 128),
-                                   db + off + (uint64_t)(k * 128), idesc, (kb | k) != 0 ? 1u : 0u);
+                                   db + off + (uint64_t)(k * 128), idesc, (i | k) != 0 ? 1u : 0u);
                     tc_commit(bar(EMPTY + s));
                     if (++s == WG_STAGES) {
                         s = 0;
@@ -266,6 +272,8 @@ tpmlp_status run_weight_grads(const WeightGradProduct* products, int count, int 
         p.a_map[q] = (int16_t)(same_a ? p.a_map[q - 1] : maps++);
         if (!same_b) ok = ok && make_map(&p.maps[maps], w.B, w.N, K, w.ldb, 64, p.bk);
         p.b_map[q] = (int16_t)(same_b ? p.b_map[q - 1] : maps++);
+        if (w.B2 != nullptr) ok = ok && make_map(&p.maps[maps], w.B2, w.N, K, w.ldb, 64, p.bk);
+        p.b2_map[q] = (int16_t)(w.B2 != nullptr ? maps++ : -1);
         ok = ok && make_map(&p.maps[maps], w.C, w.N, w.M, w.ldc, 64, 32);
         p.c_map[q] = (int16_t)maps++;
         if (!ok) return TPMLP_ERR_CUDA;

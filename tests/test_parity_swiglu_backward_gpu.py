@@ -154,3 +154,32 @@ def test_same_bits_again_and_on_another_stream():
     for i in (1, 2, 3):
         for a, b in zip(ref[i], got[i]):
             assert torch.equal(a, b)
+
+
+def rounded_once_excess(m, o, dWg, dWu):
+    """How far dWg and dWu are beyond one rounding of the exact gradient, in
+    units of what their computation may add (at most 1 where it is sound).
+    A computed v = exact + d is rounded to a value no further from v than the
+    exact value's own rounding is: the error is at most that rounding's + 2|d|.
+    |d| is at most 2^-16 of the terms' sizes for a factor in two bf16 parts
+    (2^-8 of 2^-8), and 2^-24 of them for each fp32 addition (D for dH, N
+    here) and 2^-20 for the gate's factors."""
+    a = {k: np.abs(oracle.mlp.as_f64(v)) for k, v in m.items()}
+    N, D = a["X"].shape
+    dH = a["dY"] @ a["Wd"].T
+    gate = 1.1 * a["U"], a["G"]                 # |silu'| < 1.1, |silu(g)| <= |g|
+    rel = 2.0 ** -16 + (D + N) * 2.0 ** -24 + 2.0 ** -20
+    worst = []
+    for got, ref, f in ((dWg, o["dWg"], gate[0]), (dWu, o["dWu"], gate[1])):
+        own = np.abs(torch.from_numpy(ref).to(torch.bfloat16).double().numpy() - ref)
+        worst.append(np.max((np.abs(got - ref) - own) / (2 * rel * (a["X"].T @ (dH * f)))))
+    return max(worst)
+
+
+@pytest.mark.parametrize("N", [1, 2, 3, 16, 64])
+def test_weight_gradients_of_few_tokens_are_rounded_once(N):
+    m, s = make(N, 264, 2 * 136, 2, "bf16", 70 + N)
+    o = oracle.mlp.swiglu_backward(m["X"], m["Wg"], m["Wu"], m["Wd"], m["H"], m["G"], m["U"], m["dY"])
+    _, dWg, dWu, _ = run(s, "splitk")
+    f64 = lambda parts: torch.cat(parts, 1).double().cpu().numpy()
+    assert rounded_once_excess(m, o, f64(dWg), f64(dWu)) <= 1
