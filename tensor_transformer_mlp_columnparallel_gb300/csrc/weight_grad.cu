@@ -10,7 +10,9 @@
 // tensor memory, and 4 KB tensor stores whose rows are whole 128-byte lines,
 // two in flight a warp. Warp 8 loads (TMA, a ring of 64-token stages), one
 // thread of warp 9 issues the MMAs (tcgen05, M = 128, N = 256) into one of two
-// accumulators, so the next tile is ready when an epilogue ends.
+// accumulators, so the next tile is ready when an epilogue ends. (GB300, D =
+// 4096, F = 16384, T = 4, 403 MB of gradients: 61 us at N = 16, 6.6 TB/s; 70
+// at N = 64.)
 //
 // Every wait is bounded in time, as in the block's GEMM: one that runs out
 // records TPMLP_ERR_TIMEOUT and raises the CTA's abort flag; loads and MMAs in

@@ -175,3 +175,12 @@ def test_gradient_matches_the_lookup():
     f = lambda M: float((dout.double() * tp.vocab_embedding_scaled(ids, sh(M), 2.0).double()).sum())
     dE = torch.cat(tp.vocab_embedding_backward(ids, dout, V, T, scale=2.0)).cpu()
     assert f(E + D) - f(E) == float((dE.double() * D.double()).sum())
+
+
+@pytest.mark.parametrize("dt,gdt", [("bf16", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("kind", ["zipf", "last", "one"])
+def test_wide_rows_joined_by_few_ctas(kind, dt, gdt):
+    # more columns than a block's joining CTAs take at a time
+    N, V, H, T = 8300, 40, 1300, 2
+    g = torch.Generator().manual_seed(5)
+    check(tokens(N, V, kind, 5), torch.randn(N, H, generator=g).to(TYPES[dt]), V, T, 0.5, gdt)
