@@ -171,6 +171,20 @@ def _require(ts, device, dtype):
             raise ValueError("tensors must be contiguous (row-major)")
 
 
+def _shards(ts, T: int, shape, device, dtype):
+    """_require and _ptrs of T shards of one shape."""
+    if len(ts) != T:
+        raise ValueError(f"expected {T} shards, got {len(ts)}")
+    index = device.index
+    at = (ctypes.c_void_p * T)()
+    for k, t in enumerate(ts):
+        if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+            _require([t], device, dtype)
+            raise ValueError(f"expected a shard of {tuple(shape)}, got {tuple(t.shape)}")
+        at[k] = t.data_ptr()
+    return at
+
+
 def _require_rows(t, what: str) -> int:
     """Row pitch of a [N, V] matrix whose rows are contiguous."""
     if t.dim() != 2:
@@ -338,13 +352,19 @@ def tpmlp_swiglu_backward(X, Wg, Wu, Wd, H, G, U, dY, dX, dWg, dWu, dWd, mode: s
     T = len(Wg)
     N, D = X.shape
     Fs = Wg[0].shape[1]
-    _require([X, dY, dX, *Wg, *Wu, *Wd, *H, *G, *U, *dWg, *dWu, *dWd], X.device, X.dtype)
-    _require([workspace], X.device, None)
+    dev, dt = X.device, X.dtype
+    _require([X, dY, dX], dev, dt)
+    if dY.shape != X.shape or dX.shape != X.shape:
+        raise ValueError("dY and dX must have the shape of X")
+    _require([workspace], dev, None)
+    up, down, act = (D, Fs), (Fs, D), (N, Fs)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().tpmlp_swiglu_backward(_dtype_code(X), N, D, Fs * T, T, _ptr(X), _ptrs(Wg),
-                                       _ptrs(Wu), _ptrs(Wd), _ptrs(H), _ptrs(G), _ptrs(U), _ptr(dY),
-                                       _ptr(dX), _ptrs(dWg), _ptrs(dWu), _ptrs(dWd), MODE[mode],
-                                       _ptr(workspace), ws_bytes, _stream(X)))
+    _check(lib().tpmlp_swiglu_backward(
+        _dtype_code(X), N, D, Fs * T, T, X.data_ptr(), _shards(Wg, T, up, dev, dt),
+        _shards(Wu, T, up, dev, dt), _shards(Wd, T, down, dev, dt), _shards(H, T, act, dev, dt),
+        _shards(G, T, act, dev, dt), _shards(U, T, act, dev, dt), dY.data_ptr(), dX.data_ptr(),
+        _shards(dWg, T, up, dev, dt), _shards(dWu, T, up, dev, dt), _shards(dWd, T, down, dev, dt),
+        MODE[mode], _ptr(workspace), ws_bytes, _stream(X)))
 
 
 def tpmlp_vocab_logprobs(logits, targets, T: int, K: int, logprob=None, rank=None, entropy=None,
@@ -437,10 +457,11 @@ def tpmlp_vocab_embedding_scaled(ids, table: Sequence[torch.Tensor], scale: floa
     T = len(table)
     Vs, Hd = table[0].shape
     _require([ids], out.device, torch.int64)
-    _require([*table, out], out.device, out.dtype)
+    _require([out], out.device, out.dtype)
+    shards = _shards(table, T, (Vs, Hd), out.device, out.dtype)
     _require_len(out, ids.numel() * Hd, "out")
     _check(lib().tpmlp_vocab_embedding_scaled(_dtype_code(out), ids.numel(), Vs * T, Hd, T,
-                                              _ptr(ids), _ptrs(table), float(scale), _ptr(out),
+                                              _ptr(ids), shards, float(scale), _ptr(out),
                                               _stream(out)))
 
 
@@ -456,16 +477,14 @@ def tpmlp_vocab_embedding_backward(ids, dout, scale: float, accumulate: bool,
     Vs, Hd = dtable[0].shape
     _require([ids], dout.device, torch.int64)
     _require([dout], dout.device, None)
-    _require([*dtable], dout.device, dtable[0].dtype)
+    shards = _shards(dtable, T, (Vs, Hd), dout.device, dtable[0].dtype)
     _require([workspace], dout.device, None)
     _require_len(dout, ids.numel() * Hd, "dout")
-    for t in dtable:
-        _require_len(t, Vs * Hd, "a shard of dtable")
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().tpmlp_vocab_embedding_backward(_dtype_code(dout), _dtype_code(dtable[0]),
                                                 ids.numel(), Vs * T, Hd, T, _ptr(ids), _ptr(dout),
                                                 float(scale), 1 if accumulate else 0,
-                                                _ptrs(dtable), _ptr(workspace), ws_bytes,
+                                                shards, _ptr(workspace), ws_bytes,
                                                 _stream(dout)))
 
 

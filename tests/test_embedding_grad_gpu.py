@@ -184,3 +184,16 @@ def test_wide_rows_joined_by_few_ctas(kind, dt, gdt):
     N, V, H, T = 8300, 40, 1300, 2
     g = torch.Generator().manual_seed(5)
     check(tokens(N, V, kind, 5), torch.randn(N, H, generator=g).to(TYPES[dt]), V, T, 0.5, gdt)
+
+
+def test_wrong_shards_are_refused():
+    ids = torch.zeros(3, dtype=torch.int64, device=dev())
+    E = [torch.zeros(4, 8, device=dev()), torch.zeros(3, 8, device=dev())]
+    launches = tp.tpmlp_launch_count()
+    with pytest.raises(ValueError):
+        tp.vocab_embedding_scaled(ids, E, 1.0)
+    with pytest.raises(ValueError):
+        tp.vocab_embedding_backward(ids, torch.zeros(3, 8, device=dev()), 8, 2, accumulate_into=E)
+    with pytest.raises(TypeError):
+        tp.vocab_embedding_scaled(ids, [E[0], E[0].bfloat16()], 1.0)
+    assert tp.tpmlp_launch_count() == launches

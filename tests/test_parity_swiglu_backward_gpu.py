@@ -183,3 +183,20 @@ def test_weight_gradients_of_few_tokens_are_rounded_once(N):
     _, dWg, dWu, _ = run(s, "splitk")
     f64 = lambda parts: torch.cat(parts, 1).double().cpu().numpy()
     assert rounded_once_excess(m, o, f64(dWg), f64(dWu)) <= 1
+
+
+def test_wrong_shapes_and_lists_are_refused():
+    m, s = make(8, 64, 2 * 32, 2, "bf16", 1)
+    run(s, "splitk")
+    other = {"X": s["X"][:, :32].contiguous(), "dY": s["dY"][:4], "H": s["H"][:1], "G": [s["G"][0]] * 3,
+             "U": [s["U"][0], s["U"][1][:4]], "Wu": [s["Wu"][0], s["Wu"][1].t().contiguous()],
+             "Wd": [s["Wd"][0], s["Wd"][1].t().contiguous()], "Wg": [s["Wg"][0], s["Wg"][1][:, :16].contiguous()]}
+    launches = tp.tpmlp_launch_count()
+    for name, value in other.items():
+        with pytest.raises(ValueError):
+            run(dict(s, **{name: value}), "splitk")
+    with pytest.raises(TypeError):
+        run(dict(s, H=[h.float() for h in s["H"]]), "splitk")
+    with pytest.raises(ValueError):
+        run(dict(s, U=[u.t().contiguous().t() for u in s["U"]]), "splitk")
+    assert tp.tpmlp_launch_count() == launches

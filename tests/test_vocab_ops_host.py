@@ -150,3 +150,12 @@ def test_binding_refuses_host_tensors_and_wrong_lists(lib):
         tp.vocab_embedding_backward(torch.zeros(3, dtype=torch.int64), torch.zeros(3, 8), 12, 2)
     with pytest.raises(tp.TpmlpError):
         tp.vocab_embedding_backward(torch.zeros(3, dtype=torch.int64), torch.zeros(3, 8), 13, 2)
+
+
+def test_binding_refuses_wrong_shard_counts(lib):
+    x = torch.zeros(3, 8)
+    w, wd, h = [torch.zeros(8, 4)] * 2, [torch.zeros(4, 8)] * 2, [torch.zeros(3, 4)] * 2
+    for bad in ({"Wu": w[:1]}, {"Wd": wd + wd}, {"H": []}, {"G": h[:1]}, {"U": h * 2}):
+        a = dict({"Wg": w, "Wu": w, "Wd": wd, "H": h, "G": h, "U": h}, **bad)
+        with pytest.raises(ValueError):
+            tp.swiglu_backward(x, a["Wg"], a["Wu"], a["Wd"], a["H"], a["G"], a["U"], x, workspace=x)
