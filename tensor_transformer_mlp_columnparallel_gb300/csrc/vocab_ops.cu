@@ -19,8 +19,8 @@
 // GB300, where a copy runs at 6.8 TB/s):
 //   log probabilities, 8192 x 128000 bf16: 317 us without a top list (6.6
 //   TB/s), 343 with 5 tokens, 365 with 20 (5.7 TB/s: the list's own work);
-//   2048 rows with 5: 97 us (5.4 TB/s: 13 rounds of 608 CTAs, a start, a tail);
-//   distillation with its gradient, 4096 x 128000 bf16: 347 us (6.0 TB/s).
+//   2048 rows with 5: 97 us (5.4 TB/s: 3.4 rounds of 608 CTAs, a start, a tail);
+//   distillation with its gradient, 4096 x 128000 bf16: 350 us (6.0 TB/s).
 // Few rows take 4 to 9 us, a launch and a cluster's two exchanges.
 #include <cuda_bf16.h>
 
@@ -768,11 +768,15 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
 // and needs no more of the slots than sum q ln q, their largest logit zmax and
 // sum q (z - zmax), all known before the row's m and S.
 struct TeacherShared {
-    int id[TPMLP_MAX_TEACHER];
-    float q[TPMLP_MAX_TEACHER];
-    float z[TPMLP_MAX_TEACHER];     // the student's logit at id, as it is before an in-place sweep
+    float sum;                      // of e over all slots
     float q_ln_q, zmax, q_z;
     int some, bad, n;               // n: slots of this CTA
+};
+// one of them, in dynamic shared memory ([K])
+struct TeacherSlot {
+    int id;
+    float e;                        // q times the sum over all slots
+    float z;                        // the student's logit at id, as it is before an in-place sweep
 };
 
 // A lane's first slots (k = lane + 32 u), loaded at once: all of them for K <=
@@ -800,7 +804,7 @@ __device__ __forceinline__ LaneSlots load_slots(const int32_t* ids, const float*
 template <typename T, int NT>
 __device__ __forceinline__ void teacher_row(const DistillArgs& a, const int32_t* ids, const float* tl,
                                             const LaneSlots& slots, const Row<T, NT>& row, bool loss, bool lists,
-                                            TeacherShared& sh) {
+                                            TeacherShared& sh, TeacherSlot* list) {
     const int lane = threadIdx.x;
     const float ct = kLog2e / a.tau;
     auto logit = [&](int id) {
@@ -869,9 +873,7 @@ __device__ __forceinline__ void teacher_row(const DistillArgs& a, const int32_t*
             const uint32_t b = __ballot_sync(0xffffffffu, hit);
             if (hit) {
                 const int at = n + __popc(b & ((1u << lane) - 1u));
-                sh.id[at] = id;
-                sh.q[at] = ek * inv;
-                sh.z[at] = zk;
+                list[at] = TeacherSlot{id, ek, zk};
             }
             n += __popc(b);
         };
@@ -885,6 +887,7 @@ __device__ __forceinline__ void teacher_row(const DistillArgs& a, const int32_t*
         }
     }
     if (lane == 0) {
+        sh.sum = s;
         sh.q_ln_q = q_ln_q;
         sh.zmax = zmax;
         sh.q_z = q_z;
@@ -911,14 +914,15 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_al
 // chunk in registers, the one before it in shared memory (a thread's own
 // vectors, so no barrier), 64 KB a CTA and 256 KB an SM. A slice that is
 // longer reads its other chunks again, last one first. (4096 rows of 128000
-// bf16 logits on GB300: 347 us, and DRAM moves what the algorithm has to. Of
+// bf16 logits on GB300: 350 us, and DRAM moves what the algorithm has to. Of
 // its first form, 384 us, two 512-thread CTAs an SM took 405 us, and a second
 // pass from L2 440, as half of it came from DRAM again.)
 template <typename T, int NT, bool LOSS, bool GRAD>
 __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArgs a, int log_split, int* err) {
     constexpr bool STAGE = LOSS && GRAD;
     constexpr int WARPS = NT / 32, CHUNK = Row<T, NT>::CHUNK;
-    extern __shared__ uint4 stage[];   // STAGE: one chunk
+    extern __shared__ uint4 stage[];   // STAGE: one chunk; GRAD: then the teacher's slots
+    TeacherSlot* list = reinterpret_cast<TeacherSlot*>(stage + (STAGE ? CHUNK : 0));
     __shared__ WarpSoft parts[MAX_SPLIT * WARPS];
     __shared__ TeacherShared te;
     const int split = 1 << log_split;
@@ -957,7 +961,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
         }
         if (early) row.load_rest(rest, x);
     }
-    if (warp == 0) teacher_row(a, ids, tl, slots, row, LOSS && rank == 0, GRAD, te);
+    if (warp == 0) teacher_row(a, ids, tl, slots, row, LOSS && rank == 0, GRAD, te, list);
 
     Dist dist{};
     if (LOSS) {
@@ -1002,7 +1006,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
             if (lane == 0) parts[warp] = WarpSoft{m, st.s};
             __syncthreads();
         }
-        constexpr int PPL = MAX_SPLIT * WARPS / 32;   // parts a lane takes
+        constexpr int PPL = (MAX_SPLIT * WARPS + 31) / 32;   // parts a lane takes
         const int total = split * WARPS;
         WarpSoft part[PPL];
         m = kLowest;
@@ -1112,11 +1116,12 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
         if (te.n > 0) {
             __syncthreads();
             for (int k = threadIdx.x; k < te.n; k += NT) {
-                const int id = te.id[k];
-                float q = 0.f;
+                const int id = list[k].id;
+                float e = 0.f;
                 for (int j = 0; j < te.n; ++j)
-                    if (te.id[j] == id) q += te.q[j];
-                d[id] = from_f32<T>(fmaf(-w, q, flat ? fill : ws * ex2(dist.exponent(te.z[k]))));
+                    if (list[j].id == id) e += list[j].e;
+                // divided, not times 1 / sum: 1 exactly where the sum is this token's alone
+                d[id] = from_f32<T>(fmaf(-w, e / te.sum, flat ? fill : ws * ex2(dist.exponent(list[k].z))));
             }
         }
     }
@@ -1167,26 +1172,40 @@ tpmlp_status launch_rows(void (*kernel)(P...), int threads, size_t smem, int64_t
     return cudaGetLastError() == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
 }
 
-template <typename T>
-tpmlp_status distill_launch(const DistillArgs& a, cudaStream_t s, int* err) {
+template <typename T, int NT>
+tpmlp_status distill_rows(const DistillArgs& a, cudaStream_t s, int* err) {
     const int64_t bytes = a.V * (int64_t)sizeof(T);
+    const size_t list = a.K * sizeof(TeacherSlot);
     if (a.dlogits == nullptr) {
-        const int split = row_split(a.N, bytes, ROW_THREADS, 0);
+        const int split = row_split(a.N, bytes, NT, 0);
         LaunchScope ls("vocab_distill", s);
-        return launch_rows(distill_kernel<T, ROW_THREADS, true, false>, ROW_THREADS, 0, a.N, split, s, a,
-                           split, err);
+        return launch_rows(distill_kernel<T, NT, true, false>, NT, 0, a.N, split, s, a, split, err);
     }
     if (a.loss == nullptr) {
-        const int split = row_split(a.N, bytes, ROW_THREADS, 0);
+        const int split = row_split(a.N, bytes, NT, 0);
         LaunchScope ls("vocab_distill_backward", s);
-        return launch_rows(distill_kernel<T, ROW_THREADS, false, true>, ROW_THREADS, 0, a.N, split, s, a,
-                           split, err);
+        return launch_rows(distill_kernel<T, NT, false, true>, NT, list, a.N, split, s, a, split, err);
     }
-    constexpr int CHUNK = Row<T, ROW_THREADS>::CHUNK;
-    const int split = row_split(a.N, bytes, ROW_THREADS, 2 * CHUNK);
+    constexpr int CHUNK = Row<T, NT>::CHUNK;
+    const int split = row_split(a.N, bytes, NT, 2 * CHUNK);
     LaunchScope ls("vocab_distill_with_grad", s);
-    return launch_rows(distill_kernel<T, ROW_THREADS, true, true>, ROW_THREADS, CHUNK * sizeof(uint4), a.N,
-                       split, s, a, split, err);
+    return launch_rows(distill_kernel<T, NT, true, true>, NT, CHUNK * sizeof(uint4) + list, a.N, split, s, a,
+                       split, err);
+}
+
+// Many short rows: the fewest threads whose two chunks hold the row, for more
+// rows an SM; a row of a few KB is latency for 256 threads. (4000 bf16 rows on
+// GB300, loss and gradient, 64 / 128 / 256 threads: 8 KB 25 / 29 / 45 us, 16 KB
+// 35 / 37 / 49, 32 KB 71 / 55 / 60, 64 KB 129 / 97 / 91; loss alone, 8 KB 16 /
+// 21 / 31.) Few rows are split over more CTAs instead.
+template <typename T>
+tpmlp_status distill_launch(const DistillArgs& a, cudaStream_t s, int* err) {
+    const int64_t vectors = a.V * (int64_t)sizeof(T) / 16;
+    if (a.N >= 4LL * device_sm_count()) {
+        if (vectors <= 2 * Row<T, 64>::CHUNK) return distill_rows<T, 64>(a, s, err);
+        if (vectors <= 2 * Row<T, 128>::CHUNK) return distill_rows<T, 128>(a, s, err);
+    }
+    return distill_rows<T, ROW_THREADS>(a, s, err);
 }
 
 }  // namespace

@@ -223,3 +223,46 @@ def test_refusals_on_the_device():
         tp.vocab_distill(z, ids, tl[:, :2].contiguous(), 4)
     with pytest.raises(ValueError):
         tp.tpmlp_vocab_distill_backward(z, ids, tl, 4, 1.0, w, None, 1.0, z[:2])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("V,T,K,ld", [
+    (3, 3, 1, 4), (515, 5, 40, 517), (1000, 8, 200, None), (4096, 1, 33, None),
+    (8199, 3, 7, 8201), (12001, 1, 130, 12001), (16384, 2, 5, None), (16400, 4, 5, None)])
+def test_many_short_rows(V, T, K, ld, dt):
+    """More rows than the device holds CTAs at a time; masked tokens, empty
+    slots, empty rows and repeated ids among them."""
+    N = 650
+    z, ids, tl, w = make(N, V, K, dt, V + K, ld)
+    g = torch.Generator().manual_seed(V)
+    z[::5].masked_fill_((torch.rand(V, generator=g) < 0.5).to(dev()), -INF)
+    z.scatter_(1, ids.long(), 1.0)                       # the teacher's tokens are not masked
+    ids[1::7, K // 2:] = -1
+    ids[2::9] = -1
+    ids[3::4, K - 1] = ids[3::4, 0]
+    check(z, ids, tl, w, T, 1.5, scale=0.3)
+
+
+def test_many_short_rows_with_nan_and_bad_ids():
+    z, ids, tl, w = make(700, 900, 6, "bf16", 8)
+    z[5, 17] = float("nan")
+    z[6] = -INF
+    ids[7, 2] = 900
+    loss, _, lse, d = tp.vocab_distill_with_grad(z, ids, tl, 3, grad_tokens=w)
+    assert tp.tpmlp_check_device_error() == _binding.ERR_ARG
+    one = [tp.vocab_distill_with_grad(z[n:n + 1], ids[n:n + 1], tl[n:n + 1], 3, grad_tokens=w[n:n + 1])
+           for n in (4, 6, 8)]
+    assert torch.isnan(loss[[5, 7]]).all() and torch.isnan(lse[[5, 7]]).all()
+    assert torch.isnan(d[5]).all() and torch.isnan(d[7]).all()
+    for n, o in zip((4, 6, 8), one):
+        close(loss[n:n + 1], o[0].double().cpu().numpy(), "loss")
+        close(d[n:n + 1], o[3].double().cpu().numpy(), "dlogits")
+
+
+@pytest.mark.parametrize("N", [3, 700])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_vocabulary_of_one_token(N, dt):
+    # p = q = 1 whatever the logits, however many slots share the token
+    z, ids, tl, w = make(N, 1, 2, dt, 3)
+    d = tp.vocab_distill_with_grad(z, ids, tl, 1, temperature=1.5, grad_tokens=w)[3]
+    assert torch.equal(d, torch.zeros_like(d))
