@@ -8,7 +8,7 @@
 //
 // Both read a row once. A row belongs to a cluster of 1, 2, 4 or 8 CTAs, each
 // taking a contiguous slice in 16-byte vectors; a thread keeps VPT vectors in
-// registers at a time (32 KB a CTA in flight), so the maximum of what it
+// registers at a time (128 KB an SM in flight), so the maximum of what it
 // holds is known before the first exponential. Exponentials are 2^((z - m) c)
 // with c = log2(e) / tau and m the running maximum, so the largest token's is
 // exactly 1 and a certain token's log probability exactly 0. m starts at the
@@ -17,9 +17,9 @@
 //
 // HBM bounds both on many rows (what they read and write, over the time, on
 // GB300, where a copy runs at 6.8 TB/s):
-//   log probabilities, 8192 x 128000 bf16: 317 us without a top list (6.6
-//   TB/s), 343 with 5 tokens, 365 with 20 (5.7 TB/s: the list's own work);
-//   2048 rows with 5: 97 us (5.4 TB/s: 3.4 rounds of 608 CTAs, a start, a tail);
+//   log probabilities, 8192 x 128000 bf16: 295 us without a top list (7.1
+//   TB/s), 315 with 5 tokens, 359 with 20 (5.8 TB/s: the list's own work);
+//   2048 rows with 5: 96 us (5.5 TB/s: a start and a tail);
 //   distillation with its gradient, 4096 x 128000 bf16: 350 us (6.0 TB/s).
 // Few rows take 4 to 9 us, a launch and a cluster's two exchanges.
 #include <cuda_bf16.h>
@@ -34,7 +34,6 @@ namespace tpmlp {
 namespace {
 
 constexpr int ROW_THREADS = 256;
-constexpr int ROW_WARPS = ROW_THREADS / 32;
 constexpr int VPT = 8;                        // 16-byte vectors a thread holds
 constexpr int MAX_SPLIT = 8;                  // CTAs of a row (the portable cluster size)
 constexpr float kLowest = -3.402823466e38f;   // FLT_MAX's negative
@@ -341,6 +340,7 @@ __device__ __forceinline__ Part combine(const Part* parts, int n, float c) {
 }
 
 // The block's state from its threads' (fixed order), in every thread.
+template <int WARPS>
 __device__ __forceinline__ Part block_part(Soft st, int before, Part* red, float c) {
     float m = st.ref;
 #pragma unroll
@@ -354,7 +354,7 @@ __device__ __forceinline__ Part block_part(Soft st, int before, Part* red, float
     }
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = Part{st, before};
     __syncthreads();
-    return combine(red, ROW_WARPS, c);
+    return combine(red, WARPS, c);
 }
 
 __device__ __forceinline__ void cluster_arrive() {
@@ -423,19 +423,19 @@ __device__ __forceinline__ Dist distribution(const Soft& t, float c, float inv_t
 
 // Entries with a probability in a row whose maximum is the lowest finite value
 // or -inf: they all hold that value.
-template <typename T>
+template <typename T, int NT>
 __device__ __noinline__ float count_finite(const T* z, int64_t V, float* red) {
     float n = 0.f;
-    for (int64_t i = threadIdx.x; i < V; i += ROW_THREADS) n += to_f32(z[i]) != -INFINITY ? 1.f : 0.f;
+    for (int64_t i = threadIdx.x; i < V; i += NT) n += to_f32(z[i]) != -INFINITY ? 1.f : 0.f;
     return block_reduce(n, Sum(), red);
 }
 
 // sum e (z - ref) over a whole row a plain element at a time, for a row whose
 // (z - ref) overflows at a masked token (a maximum near the type's largest value)
-template <typename T>
+template <typename T, int NT>
 __device__ __noinline__ float slow_esum(const T* z, int64_t V, const Dist& d, float* red) {
     float es = 0.f;
-    for (int64_t i = threadIdx.x; i < V; i += ROW_THREADS) {
+    for (int64_t i = threadIdx.x; i < V; i += NT) {
         const float x = to_f32(z[i]), p = ex2(d.exponent(x));
         es += p == 0.f ? 0.f : p * (x - d.ref);
     }
@@ -443,8 +443,6 @@ __device__ __noinline__ float slow_esum(const T* z, int64_t V, const Dist& d, fl
 }
 
 // ------------------------------------------------------- top tokens ------
-
-constexpr int MAX_CAND = 1024;
 
 // An order of all floats (NaN with its sign bit clear on top); -0 = +0.
 __device__ __forceinline__ uint32_t order32(float z) {
@@ -460,31 +458,35 @@ __device__ __forceinline__ unsigned long long order_key(uint32_t o, uint32_t v) 
     return ((unsigned long long)o << 32) | (0xffffffffu - v);
 }
 
+template <int NT>
 struct TopShared {
+    static constexpr int MAX_CAND = 4 * NT;
+    // lists of several CTAs: rows that are split have CTAs of ROW_THREADS
+    static constexpr int ALL = NT == ROW_THREADS ? MAX_SPLIT * TPMLP_MAX_TOP : 1;
     unsigned long long cand[MAX_CAND];
     unsigned long long list[TPMLP_MAX_TOP];                  // this CTA's first K, in order
-    unsigned long long all[MAX_SPLIT * TPMLP_MAX_TOP];       // the leader's copy of every CTA's list
-    unsigned long long red[ROW_WARPS];
-    uint32_t thr[ROW_WARPS];
-    uint32_t max_of[ROW_THREADS];    // maxima that reach the first bound
-    int chunk_of[ROW_THREADS];       // (chunk, thread) whose vectors are looked at
-    int whole_of[ROW_THREADS];       // threads all of whose vectors are
+    unsigned long long all[ALL];       // the leader's copy of every CTA's list
+    unsigned long long red[NT / 32];
+    uint32_t thr[NT / 32];
+    uint32_t max_of[NT];    // maxima that reach the first bound
+    int chunk_of[NT];       // (chunk, thread) whose vectors are looked at
+    int whole_of[NT];       // threads all of whose vectors are
     uint32_t bound;
     int n_max, n_chunk, n_whole, n_cand;
 };
 
 // The elements of vector i that are in the row and at least `thr` (strictly
 // above with `above`) join the candidates; beyond MAX_CAND they are only counted.
-template <typename T>
-__device__ __forceinline__ void offer(const Row<T, ROW_THREADS>& row, int i, const uint4& x, uint32_t thr, bool above,
-                                      TopShared& sh) {
+template <typename T, int NT>
+__device__ __forceinline__ void offer(const Row<T, NT>& row, int i, const uint4& x, uint32_t thr, bool above,
+                                      TopShared<NT>& sh) {
     const int e0 = row.start(i);
 #pragma unroll
     for (int j = 0; j < Vec<T>::N; ++j) {
         const uint32_t o = order32(Vec<T>::elem(x, j));
         if ((above ? o > thr : o >= thr) && e0 + j >= 0 && e0 + j < row.len) {
             const int at = atomicAdd(&sh.n_cand, 1);
-            if (at < MAX_CAND) sh.cand[at] = order_key(o, (uint32_t)(e0 + j));
+            if (at < TopShared<NT>::MAX_CAND) sh.cand[at] = order_key(o, (uint32_t)(e0 + j));
         }
     }
 }
@@ -498,14 +500,14 @@ struct Peaks {
     int base;
 };
 
-// The K-th largest of the 256
-// maxima is reached by K different entries, so only entries at or above it can
-// be in the list, and they sit with the threads whose maximum reaches it: K of
-// 256 unless maxima are equal. Of their vectors those of the chunk with the
+// The K-th largest of the threads' NT (at least K) maxima is reached by K
+// different entries, so only entries at or above it can be in the list, and
+// they sit with the threads whose maximum reaches it: K of
+// NT unless maxima are equal. Of their vectors those of the chunk with the
 // maximum are read again, spread over all threads, and a thread's others only
 // if one of them reaches the bound too. (Reading all of a thread's vectors,
-// K / 256 of the slice, from DRAM as a rule, took 45% of the kernel's time at
-// K = 20 and 8192 x 128000 bf16 logits, this way the list takes 14%; going
+// K / NT of the slice, from DRAM as a rule, took 45% of the kernel's time at
+// K = 20 and 8192 x 128000 bf16 logits, this way the list takes 18%; going
 // through the registers of the few threads, where the slice is one chunk,
 // took twice as long as reading it again.) The K-th largest maximum comes in
 // two steps: with g = ceil(K / warps), the least of the warps' g-th largest
@@ -514,22 +516,23 @@ struct Peaks {
 // than K tokens, rows of equal values), the entries above it are taken alone
 // and equal ones follow by index; where even those are too many, K rounds
 // over the slice.
-template <typename T>
-__device__ void slice_top(const Row<T, ROW_THREADS>& row, int K, const Peaks& peaks, TopShared& sh) {
+template <typename T, int NT>
+__device__ void slice_top(const Row<T, NT>& row, int K, const Peaks& peaks, TopShared<NT>& sh) {
+    constexpr int MAX_CAND = TopShared<NT>::MAX_CAND;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t mine = order32(max_nan(peaks.best, peaks.other));
     uint32_t left = mine, g_th = 0;
-    for (int g = 0; g < (K + ROW_WARPS - 1) / ROW_WARPS; ++g) {
+    for (int g = 0; g < (K + NT / 32 - 1) / (NT / 32); ++g) {
         g_th = __reduce_max_sync(0xffffffffu, left);
         const uint32_t who = __ballot_sync(0xffffffffu, left == g_th);
         if (lane == __ffs(who) - 1) left = 0u;
     }
     if (lane == 0) sh.thr[warp] = g_th;
     if (threadIdx.x == 0) sh.n_max = sh.n_chunk = sh.n_whole = sh.n_cand = 0;
-    for (int k = threadIdx.x; k < K; k += ROW_THREADS) sh.list[k] = 0ull;
+    for (int k = threadIdx.x; k < K; k += NT) sh.list[k] = 0ull;
     __syncthreads();
     uint32_t thr = sh.thr[0];
-    for (int w = 1; w < ROW_WARPS; ++w) thr = min(thr, sh.thr[w]);
+    for (int w = 1; w < NT / 32; ++w) thr = min(thr, sh.thr[w]);
     if (mine >= thr) {
         const int at = atomicAdd(&sh.n_max, 1);
         sh.max_of[at] = mine;
@@ -547,7 +550,7 @@ __device__ void slice_top(const Row<T, ROW_THREADS>& row, int K, const Peaks& pe
     __syncthreads();
     thr = sh.bound;
     const int n = row.hi - row.lo;
-    const int per = (n + ROW_THREADS - 1) / ROW_THREADS;   // vectors of a thread
+    const int per = (n + NT - 1) / NT;   // vectors of a thread
     if (mine >= thr && row.edge() <= row.full) offer(row, row.edge(), row.load_edge(row.edge()), thr, false, sh);
     if (mine >= thr) {
         if (order32(peaks.other) >= thr)
@@ -556,12 +559,12 @@ __device__ void slice_top(const Row<T, ROW_THREADS>& row, int K, const Peaks& pe
             sh.chunk_of[atomicAdd(&sh.n_chunk, 1)] = peaks.base + (int)threadIdx.x;
     }
     __syncthreads();
-    for (int a = threadIdx.x; a < sh.n_chunk * VPT; a += ROW_THREADS) {
-        const int i = sh.chunk_of[a / VPT] + (a % VPT) * ROW_THREADS;
+    for (int a = threadIdx.x; a < sh.n_chunk * VPT; a += NT) {
+        const int i = sh.chunk_of[a / VPT] + (a % VPT) * NT;
         if (i < row.hi) offer(row, i, row.load(i), thr, false, sh);
     }
-    for (int a = threadIdx.x; a < sh.n_whole * per; a += ROW_THREADS) {
-        const int i = row.lo + (a % per) * ROW_THREADS + sh.whole_of[a / per];
+    for (int a = threadIdx.x; a < sh.n_whole * per; a += NT) {
+        const int i = row.lo + (a % per) * NT + sh.whole_of[a / per];
         if (i < row.hi) offer(row, i, row.load(i), thr, false, sh);
     }
     __syncthreads();
@@ -571,13 +574,13 @@ __device__ void slice_top(const Row<T, ROW_THREADS>& row, int K, const Peaks& pe
         if (threadIdx.x == 0) sh.n_cand = 0;
         __syncthreads();
         if (row.edge() <= row.full) offer(row, row.edge(), row.load_edge(row.edge()), thr, true, sh);
-        for (int i = row.lo + (int)threadIdx.x; i < row.hi; i += ROW_THREADS)
+        for (int i = row.lo + (int)threadIdx.x; i < row.hi; i += NT)
             offer(row, i, row.load(i), thr, true, sh);
         __syncthreads();
         count = sh.n_cand;
         if (count <= MAX_CAND - K) {
             // entries equal to the bound, in index order, until there are K
-            for (int e = row.e_lo; e < row.e_hi && count < K; e += ROW_THREADS) {
+            for (int e = row.e_lo; e < row.e_hi && count < K; e += NT) {
                 const int at = e + (int)threadIdx.x;
                 const bool hit = at < row.e_hi && order32(to_f32(row.z[at])) == thr;
                 const uint32_t b = __ballot_sync(0xffffffffu, hit);
@@ -585,7 +588,7 @@ __device__ void slice_top(const Row<T, ROW_THREADS>& row, int K, const Peaks& pe
                 __syncthreads();
                 int pos = count + __popc(b & ((1u << lane) - 1u));
                 for (int w = 0; w < warp; ++w) pos += (int)sh.thr[w];
-                for (int w = 0; w < ROW_WARPS; ++w) count += (int)sh.thr[w];
+                for (int w = 0; w < NT / 32; ++w) count += (int)sh.thr[w];
                 if (hit && pos < MAX_CAND) sh.cand[pos] = order_key(thr, (uint32_t)at);
                 __syncthreads();
             }
@@ -594,7 +597,7 @@ __device__ void slice_top(const Row<T, ROW_THREADS>& row, int K, const Peaks& pe
             unsigned long long last = ~0ull;
             for (int k = 0; k < K; ++k) {
                 unsigned long long best = 0ull;
-                for (int e = row.e_lo + (int)threadIdx.x; e < row.e_hi; e += ROW_THREADS) {
+                for (int e = row.e_lo + (int)threadIdx.x; e < row.e_hi; e += NT) {
                     const unsigned long long key = order_key(order32(to_f32(row.z[e])), (uint32_t)e);
                     if (key < last && key > best) best = key;
                 }
@@ -606,7 +609,7 @@ __device__ void slice_top(const Row<T, ROW_THREADS>& row, int K, const Peaks& pe
             return;
         }
     }
-    for (int a = threadIdx.x; a < count; a += ROW_THREADS) {
+    for (int a = threadIdx.x; a < count; a += NT) {
         const unsigned long long key = sh.cand[a];
         int place = 0;
         for (int b = 0; b < count; ++b) place += sh.cand[b] > key;
@@ -617,19 +620,19 @@ __device__ void slice_top(const Row<T, ROW_THREADS>& row, int K, const Peaks& pe
 
 // ---------------------------------------------------- log probabilities --
 
-template <typename T>
-__global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobArgs a, int log_split, int* err) {
-    __shared__ Part red[ROW_WARPS];
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const LogprobArgs a, int log_split, int* err) {
+    __shared__ Part red[NT / 32];
     __shared__ Part parts[MAX_SPLIT];
-    __shared__ float redf[ROW_WARPS];
-    __shared__ TopShared sh;
+    __shared__ float redf[NT / 32];
+    __shared__ TopShared<NT> sh;
     const int split = 1 << log_split;
     const int64_t row_i = blockIdx.x >> log_split;
     const int rank = (int)(blockIdx.x & (unsigned)(split - 1));
     if (split > 1) cluster_arrive();   // this CTA runs: its shared memory may be written
     pdl_wait();
     pdl_launch_dependents();
-    constexpr int CHUNK = Row<T, ROW_THREADS>::CHUNK;
+    constexpr int CHUNK = Row<T, NT>::CHUNK;
     uint4 x[VPT];
     Soft st{Vec<T>::lowest(), 0.f, 0.f};
     int before = 0;
@@ -637,7 +640,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
     int t = -1;                                      // the target; -1: none, or out of range
     auto zw = Vec<T>::wide(INFINITY);                // its logit; +inf: not counted in the loop
     {
-        const Row<T, ROW_THREADS> row(a.logits, row_i, a.ld, a.V, rank, log_split);
+        const Row<T, NT> row(a.logits, row_i, a.ld, a.V, rank, log_split);
         // the row's loads go out before anything waits for the target's
         const int rest = row.rest();
         if (row.lo < rest)
@@ -671,7 +674,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
             } else {
 #pragma unroll
                 for (int r = 0; r < VPT; ++r) {
-                    if (base + r * ROW_THREADS + (int)threadIdx.x < tvec)
+                    if (base + r * NT + (int)threadIdx.x < tvec)
                         cnt.ge(x[r], zw);
                     else
                         cnt.gt(x[r], zw);
@@ -703,7 +706,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
     // the row's sizes would not fit the registers.
     int64_t row_j = row_i;
     asm volatile("" : "+l"(row_j));
-    const Row<T, ROW_THREADS> row(a.logits, row_j, a.ld, a.V, rank, log_split);
+    const Row<T, NT> row(a.logits, row_j, a.ld, a.V, rank, log_split);
     const bool good = t >= 0, counted = good && Vec<T>::narrow(zw) < INFINITY;
     const float zt = counted ? Vec<T>::narrow(zw) : -INFINITY;
     if (counted && threadIdx.x == 0 && row.mine(t))
@@ -711,17 +714,17 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
     if (good && !counted) {   // a masked target (or a NaN): every entry is compared
         before = 0;
         const float z = to_f32(row.z[t]);
-        for (int e = row.e_lo + (int)threadIdx.x; e < row.e_hi; e += ROW_THREADS) {
+        for (int e = row.e_lo + (int)threadIdx.x; e < row.e_hi; e += NT) {
             const float v = to_f32(row.z[e]);
             before += v > z || (v == z && e < t);
         }
     }
-    Part part = block_part(st, before, red, kLog2e);
+    Part part = block_part<NT / 32>(st, before, red, kLog2e);
     if (a.K > 0) slice_top(row, a.K, peaks, sh);
     if (split > 1) {
         cluster_wait();
         if (threadIdx.x == 0) send_part(parts, rank, 0u, part);
-        for (int k = threadIdx.x; k < a.K; k += ROW_THREADS)
+        for (int k = threadIdx.x; k < a.K; k += NT)
             st_cluster_u64(mapa_shared(smem_u32(&sh.all[rank * a.K + k]), 0u), sh.list[k]);
         cluster_arrive();
         cluster_wait();
@@ -731,12 +734,12 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
     // masked tokens were summed as the lowest finite value, which tells
     // nothing only where the row has no larger one
     if (part.soft.ref == Vec<T>::lowest()) {
-        part.soft.s = count_finite(row.z, a.V, redf);
+        part.soft.s = count_finite<T, NT>(row.z, a.V, redf);
         part.soft.e = 0.f;
     }
     const Dist d = distribution(part.soft, kLog2e, 1.f);
     float esum = part.soft.e;
-    if (isnan(esum) && !isnan(d.s)) esum = slow_esum(row.z, a.V, d, redf);
+    if (isnan(esum) && !isnan(d.s)) esum = slow_esum<T, NT>(row.z, a.V, d, redf);
     if (threadIdx.x == 0) {
         if (a.targets && !good) atomicCAS(err, 0, (int)TPMLP_ERR_ARG);
         if (a.lse) a.lse[row_j] = d.lse();
@@ -746,7 +749,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) logprobs_kernel(const LogprobA
     }
     const unsigned long long* all = split > 1 ? sh.all : sh.list;
     const int m = split * a.K;
-    for (int i = threadIdx.x; i < m; i += ROW_THREADS) {
+    for (int i = threadIdx.x; i < m; i += NT) {
         const unsigned long long key = all[i];
         int place = i;
         if (split > 1) {
@@ -1208,6 +1211,25 @@ tpmlp_status distill_launch(const DistillArgs& a, cudaStream_t s, int* err) {
     return distill_rows<T, ROW_THREADS>(a, s, err);
 }
 
+// Many rows take smaller CTAs, for more rows an SM: 64 threads where their two
+// chunks hold the row, else 128. The list's bound is the K-th largest of the
+// threads' maxima, so fewer threads leave more candidates: at most one
+// token of the list for two threads, in rows of more chunks one for six. (bf16 on GB300, 64 /
+// 128 / 256 threads: 4000 rows of 8 KB, K = 0 16 / 22 / 37 us, K = 20 29 / 36 /
+// 56; of 32 KB, K = 20 51 / 53 / 61; 8192 rows of 256 KB, K = 0 335 / 321 / 326,
+// K = 20 503 / 386 / 376, K = 64 35 ms / 654 / 467.)
+template <typename T>
+tpmlp_status logprobs_launch(const LogprobArgs& a, int log_split, cudaStream_t s, int* err) {
+    const int64_t vectors = a.V * (int64_t)sizeof(T) / 16;
+    if (a.N >= 4LL * device_sm_count()) {   // not split
+        if (vectors <= 2 * Row<T, 64>::CHUNK && a.K * 2 <= 64)
+            return launch_rows(logprobs_kernel<T, 64>, 64, 0, a.N, log_split, s, a, log_split, err);
+        if (a.K * (vectors <= 2 * Row<T, 128>::CHUNK ? 2 : 6) <= 128)
+            return launch_rows(logprobs_kernel<T, 128>, 128, 0, a.N, log_split, s, a, log_split, err);
+    }
+    return launch_rows(logprobs_kernel<T, ROW_THREADS>, ROW_THREADS, 0, a.N, log_split, s, a, log_split, err);
+}
+
 }  // namespace
 
 tpmlp_status run_vocab_logprobs(int f32, const LogprobArgs& a, cudaStream_t s) {
@@ -1216,8 +1238,7 @@ tpmlp_status run_vocab_logprobs(int f32, const LogprobArgs& a, cudaStream_t s) {
     if (err == nullptr) return TPMLP_ERR_CUDA;
     const int split = row_split(a.N, a.V * (f32 ? 4 : 2), ROW_THREADS, 0);
     LaunchScope ls("vocab_logprobs", s);
-    return f32 ? launch_rows(logprobs_kernel<float>, ROW_THREADS, 0, a.N, split, s, a, split, err)
-               : launch_rows(logprobs_kernel<__nv_bfloat16>, ROW_THREADS, 0, a.N, split, s, a, split, err);
+    return f32 ? logprobs_launch<float>(a, split, s, err) : logprobs_launch<__nv_bfloat16>(a, split, s, err);
 }
 
 tpmlp_status run_vocab_distill(int f32, const DistillArgs& a, cudaStream_t s) {

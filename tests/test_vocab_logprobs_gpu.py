@@ -200,3 +200,27 @@ def test_refusals_on_the_device():
         tp.vocab_logprobs(z.half(), t, 4)
     with pytest.raises(TypeError):
         tp.vocab_logprobs(z, t.int(), 4)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("V,T,ld,K", [
+    (1, 1, None, 1), (5, 5, 7, 3), (40, 1, None, 20), (64, 2, None, 64), (515, 5, 517, 32), (1000, 8, None, 64),
+    (1000, 8, 1001, 128), (4096, 1, None, 32), (8199, 3, 8201, 20), (8192, 2, None, 33), (16384, 4, None, 64),
+    (16401, 3, None, 64), (20001, 3, 20004, 21), (20001, 3, None, 22), (40000, 8, None, 5), (33000, 8, None, 0)])
+def test_many_rows(V, T, ld, K, dt):
+    """More rows than the device holds CTAs at a time, of every size that has
+    its own number of threads, with lists up to its limit; masks, equal logits
+    and ordered rows among them."""
+    N = 640
+    z, t = rows(N, V, dt, V + K, ld)
+    g = torch.Generator().manual_seed(V)
+    some = (torch.rand(V, generator=g) < 0.7).to(dev())
+    z[::6].masked_fill_(some, -INF)
+    z[1::12] = -INF
+    z[2::12] = 0.5
+    z[3::12] = torch.finfo(TYPES[dt]).min
+    z[4::12] = torch.sort(z[4::12], dim=1).values
+    z[5::12] = torch.sort(z[5::12], dim=1, descending=True).values
+    z[7::12, V // 2:] = -INF
+    z[8::12] = (z[8::12] * 4).round()                 # many equal ones
+    check(z, t, T, K)
