@@ -11,8 +11,8 @@
 //   order; so a token that fills half the batch is no one CTA's work. Sums
 //   are fp32, in an order that the ids alone decide: no floating-point atomics.
 //   What bounds it is the table: every row is written once, most as zeros.
-//   On GB300, 8192 bf16 tokens into 128000 x 4096 fp32: 354 us, of which the
-//   sort takes 18 and the pieces 9; 6.1 TB/s over the whole, 6.9 over the
+//   On GB300, 8192 bf16 tokens into 128000 x 4096 fp32: 338 us, of which the
+//   sort takes 10 and the pieces 9; 6.4 TB/s over the whole, 6.9 over the
 //   table's launch. A few tokens: three launches, 15 us for a small table.
 #include <cuda_bf16.h>
 
@@ -108,7 +108,12 @@ constexpr int RADIX_BITS = 9;
 constexpr int BINS = 1 << RADIX_BITS;
 constexpr int SORT_ROUNDS = 8;                               // tokens per lane
 constexpr int SORT_THREADS = 512;                            // of the sort over several CTAs
-constexpr int SORT_TILE = SORT_THREADS * SORT_ROUNDS;        // its tokens per CTA
+// Its rounds while the CTAs are few: ranking a round takes a warp up to 32 steps,
+// one for every digit among its lanes, so more SMs have it sooner. Beyond
+// FEW_TOKENS every CTA would add up too many others' counts. (8192 tokens in
+// CTAs of 1024 / 4096 / one CTA on GB300: table gradient 345 / 358 / 357 us.)
+constexpr int FEW_ROUNDS = 2;
+constexpr int64_t FEW_TOKENS = 65536;
 constexpr int ONE_THREADS = 1024;                            // of the sort in one CTA
 constexpr int ONE_MAX = ONE_THREADS * SORT_ROUNDS;           // its tokens at most
 constexpr int ONE_SMEM = (ONE_THREADS / 32) * BINS * 4 + ONE_MAX * 8;
@@ -143,13 +148,14 @@ __device__ __forceinline__ void zero_segments(const SortArgs& p, int first, int 
         p.seg[v] = make_int2(0, 0);
 }
 
-// Ranks of a warp's 32 x SORT_ROUNDS consecutive pairs within their digits: lanes
+// Ranks of a warp's 32 x R consecutive pairs within their digits: lanes
 // with one digit rank themselves by lane, behind the warp's count so far.
-__device__ __forceinline__ void warp_ranks(const uint2 (&item)[SORT_ROUNDS], const bool (&in)[SORT_ROUNDS],
-                                           int shift, int* cnt, int (&rank)[SORT_ROUNDS]) {
+template <int R>
+__device__ __forceinline__ void warp_ranks(const uint2 (&item)[R], const bool (&in)[R], int shift, int* cnt,
+                                           int (&rank)[R]) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int r = 0; r < SORT_ROUNDS; ++r) {
+    for (int r = 0; r < R; ++r) {
         const uint32_t digit = in[r] ? (item[r].x >> shift) & (BINS - 1) : (uint32_t)BINS;
         const uint32_t peers = __match_any_sync(0xffffffffu, digit);
         const int mine = __popc(peers & ((1u << lane) - 1u));
@@ -231,6 +237,7 @@ __global__ void __launch_bounds__(ONE_THREADS) sort_one_kernel(const SortArgs p)
         if (in[r]) p.out[base + r * 32] = item[r];
 }
 
+template <int R>
 __global__ void __launch_bounds__(SORT_THREADS) sort_hist_kernel(const SortArgs p, int ctas) {
     pdl_wait();
     pdl_launch_dependents();
@@ -241,8 +248,8 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_hist_kernel(const SortArgs 
     __shared__ int cnt[BINS];
     cnt[threadIdx.x] = 0;
     __syncthreads();
-    const int64_t base = (int64_t)blockIdx.x * SORT_TILE;
-    for (int r = 0; r < SORT_ROUNDS; ++r) {
+    const int64_t base = (int64_t)blockIdx.x * (SORT_THREADS * R);
+    for (int r = 0; r < R; ++r) {
         const int64_t i = base + r * SORT_THREADS + threadIdx.x;
         if (i >= p.N) break;
         atomicAdd(&cnt[(sort_pair(p, i).x >> p.shift) & (BINS - 1)], 1);
@@ -253,6 +260,7 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_hist_kernel(const SortArgs 
 
 // Stable: a pair goes behind every smaller digit, its digit in earlier CTAs, in
 // earlier warps, and in its warp's earlier pairs.
+template <int R>
 __global__ void __launch_bounds__(SORT_THREADS) sort_scatter_kernel(const SortArgs p) {
     pdl_wait();
     pdl_launch_dependents();
@@ -263,6 +271,7 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_scatter_kernel(const SortAr
     for (int w = 0; w < WARPS; ++w) cnt[w][threadIdx.x] = 0;
     // digit threadIdx.x: all its pairs, and those in CTAs before this one
     int total = 0, before = 0;
+#pragma unroll 8
     for (int b = 0; b < (int)gridDim.x; ++b) {
         const int h = p.hist[(int64_t)b * BINS + threadIdx.x];
         total += h;
@@ -270,12 +279,12 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_scatter_kernel(const SortAr
     }
     int start = scan_bins(total, warp_sum) + before;
 
-    const int64_t base = (int64_t)blockIdx.x * SORT_TILE + warp * (32 * SORT_ROUNDS) + (threadIdx.x & 31);
-    uint2 item[SORT_ROUNDS];
-    bool in[SORT_ROUNDS];
-    int rank[SORT_ROUNDS];
+    const int64_t base = (int64_t)blockIdx.x * (SORT_THREADS * R) + warp * (32 * R) + (threadIdx.x & 31);
+    uint2 item[R];
+    bool in[R];
+    int rank[R];
 #pragma unroll
-    for (int r = 0; r < SORT_ROUNDS; ++r) {
+    for (int r = 0; r < R; ++r) {
         in[r] = base + r * 32 < p.N;
         item[r] = in[r] ? sort_pair(p, base + r * 32) : make_uint2(0u, 0u);
     }
@@ -288,7 +297,7 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_scatter_kernel(const SortAr
     }
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < SORT_ROUNDS; ++r)
+    for (int r = 0; r < R; ++r)
         if (in[r]) p.out[cnt[warp][(item[r].x >> p.shift) & (BINS - 1)] + rank[r]] = item[r];
 }
 
@@ -302,8 +311,8 @@ constexpr int GRAD_BYTES = 32768; // and of table, where rows are short
 constexpr int WARP_ROW = 4096;    // bytes of a table row up to which a warp takes it, not the CTA
 constexpr int JOIN_COLS = 128;    // columns that a CTA joins at a time
 // CTAs that join pieces, unless a block's would be fewer than 8: most find
-// nothing to join (8192 tokens into 128000 x 4096: 352 us, with one for every
-// block and 128 columns 361)
+// nothing to join (8192 tokens into 128000 x 4096, before the sort was sped up:
+// 352 us, with one for every block and 128 columns 361)
 constexpr int JOIN_CTAS = 2048;
 
 struct GradArgs {
@@ -528,7 +537,10 @@ __global__ void __launch_bounds__(GRAD_THREADS) embedding_grad_kernel(const Grad
 }
 
 inline size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-inline int64_t sort_ctas(int64_t N) { return (N + SORT_TILE - 1) / SORT_TILE; }
+inline int64_t sort_ctas(int64_t N) {
+    const int64_t tile = (int64_t)SORT_THREADS * (N <= FEW_TOKENS ? FEW_ROUNDS : SORT_ROUNDS);
+    return (N + tile - 1) / tile;
+}
 inline int64_t grad_blocks(int64_t N) { return (N + SPAN - 1) / SPAN; }
 inline int64_t piece_pitch(int64_t H) { return (H + 3) / 4 * 4; }
 
@@ -681,8 +693,12 @@ tpmlp_status run_vocab_embedding_backward(int f32, int grad_f32, int64_t N, int6
         p.bits = 1;
         while ((V >> p.bits) != 0) ++p.bits;   // keys 0..V
         p.err = err;
-        if (N <= ONE_MAX) {
-            // one launch for all passes
+        // One launch for all passes where there is little to do: what bounds a
+        // small table is issuing the launches (4099 fp32 tokens into 9999 x 1030:
+        // 36 us with one, 38 to 45 with four; 4235 into 38549 x 1464: 72 / 69).
+        const double work = (double)H * ((double)N * (f32 ? 4 : 2) +
+                                         (accumulate ? 0.0 : (double)V * (grad_f32 ? 4 : 2)));
+        if (N <= ONE_MAX / 4 || (N <= ONE_MAX && work < 64e6)) {
             p.out = reinterpret_cast<uint2*>(ws + l.pairs[0]);
             if (cudaFuncSetAttribute(sort_one_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ONE_SMEM) !=
                 cudaSuccess)
@@ -694,18 +710,21 @@ tpmlp_status run_vocab_embedding_backward(int f32, int grad_f32, int64_t N, int6
             g.sorted = p.out;
         } else {
             const int ctas = (int)sort_ctas(N);
+            const bool few = N <= FEW_TOKENS;
             int which = 0;
             for (p.shift = 0; p.shift < p.bits; p.shift += RADIX_BITS) {
                 p.out = reinterpret_cast<uint2*>(ws + l.pairs[which]);
                 {
                     LaunchScope ls("embedding_grad_sort", s);
-                    if (launch_pdl(sort_hist_kernel, dim3((unsigned)(ctas + (p.shift == 0 ? 64 : 0))),
-                                   SORT_THREADS, 0, s, p, ctas) != cudaSuccess)
+                    if (launch_pdl(few ? sort_hist_kernel<FEW_ROUNDS> : sort_hist_kernel<SORT_ROUNDS>,
+                                   dim3((unsigned)(ctas + (p.shift == 0 ? 64 : 0))), SORT_THREADS, 0, s, p,
+                                   ctas) != cudaSuccess)
                         return TPMLP_ERR_CUDA;
                 }
                 {
                     LaunchScope ls("embedding_grad_sort", s);
-                    if (launch_pdl(sort_scatter_kernel, dim3((unsigned)ctas), SORT_THREADS, 0, s, p) != cudaSuccess)
+                    if (launch_pdl(few ? sort_scatter_kernel<FEW_ROUNDS> : sort_scatter_kernel<SORT_ROUNDS>,
+                                   dim3((unsigned)ctas), SORT_THREADS, 0, s, p) != cudaSuccess)
                         return TPMLP_ERR_CUDA;
                 }
                 g.sorted = p.out;

@@ -197,3 +197,14 @@ def test_wrong_shards_are_refused():
     with pytest.raises(TypeError):
         tp.vocab_embedding_scaled(ids, [E[0], E[0].bfloat16()], 1.0)
     assert tp.tpmlp_launch_count() == launches
+
+
+@pytest.mark.parametrize("dt,gdt", [("bf16", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("N,V,H,kind", [
+    (2049, 9000, 2056, "zipf"), (8192, 9000, 2056, "last"), (4100, 33000, 1030, "flat"),
+    (65536, 700, 8, "zipf"), (65537, 700, 8, "zipf"), (5000, 7, 3200, "one"), (65000, 270000, 8, "flat")])
+def test_sorted_by_several_ctas(N, V, H, kind, dt, gdt):
+    """Tables large enough for the sort over several CTAs at few tokens, and its
+    two tile sizes."""
+    g = torch.Generator().manual_seed(N)
+    check(tokens(N, V, kind, N), torch.randn(N, H, generator=g).to(TYPES[dt]), V, 1, 1.5, gdt)
