@@ -169,10 +169,10 @@ tpmlp_status tpmlp_backward(tpmlp_dtype dt, int64_t N, int64_t D, int64_t F, int
  *   inputs: X [N, D]; Wg, Wu T x [D, F/T]; Wd T x [F/T, D]; H, G, U
  *           T x [N, F/T] as tpmlp_swiglu_forward wrote them; dY [N, D]
  *   outputs: dX [N, D]; dWg, dWu T x [D, F/T]; dWd T x [F/T, D]
- * Workspace: dG (T x [N, F/T] of dt, shard r at byte
- * r * round_up(N*(F/T)*sizeof(dt), 256)), dU after those in the same layout,
- * with bf16 and N <= 64 what rounding left over of dG and of dU in the same
- * layout again (dWg and dWu take both parts),
+ * Workspace: dG (T x [R, F/T] of dt, shard r at byte
+ * r * round_up(R*(F/T)*sizeof(dt), 256)), dU after those in the same layout.
+ * R is N, or with bf16 and N <= 64 it is 2 N: what rounding the first N rows
+ * left over (dWg and dWu take both parts, dX does for N <= 16);
  * then in PARTIALS mode the T fp32 dX partials; its size is
  * tpmlp_workspace_bytes(TPMLP_OP_SWIGLU_BACKWARD, ...). N = 0 writes zeros to
  * dWg, dWu and dWd. Errors as tpmlp_backward. */

@@ -198,7 +198,8 @@ size_t dz_bytes(tpmlp_dtype dt, int64_t N, int64_t Fs, int T) {
 }
 
 // The gated backward of a few bf16 tokens also keeps what rounding dG and dU
-// left over, for dWg and dWu. A gradient made from rounded factors is off by
+// left over, in N rows behind a shard's, for dWg and dWu and up to kRestRows
+// tokens for dX (whose 128-row tiles have the rows to spare). A gradient made from rounded factors is off by
 // their rounding on top of its own, 1.4 times the latter over many terms and
 // 1.6 times where a few terms rule the sum (N = 2, F = 1984); with both parts
 // it is rounded once. They cost no time there, as writing the gradients bounds
@@ -306,7 +307,7 @@ size_t tpmlp_workspace_bytes(tpmlp_op op, tpmlp_dtype dt, int64_t N, int64_t D, 
     const size_t part = mode == TPMLP_REDUCE_PARTIALS ? partials_bytes(N, D, T) : 0;
     if (op == TPMLP_OP_FORWARD) return part;
     if (op == TPMLP_OP_BACKWARD) return dz_bytes(dt, N, F / T, T) + part;
-    if (op == TPMLP_OP_SWIGLU_BACKWARD) return (keeps_rest(dt, N) ? 4 : 2) * dz_bytes(dt, N, F / T, T) + part;
+    if (op == TPMLP_OP_SWIGLU_BACKWARD) return 2 * dz_bytes(dt, keeps_rest(dt, N) ? 2 * N : N, F / T, T) + part;
     return (size_t)-1;
 }
 
@@ -683,8 +684,8 @@ tpmlp_status tpmlp_swiglu_backward(tpmlp_dtype dt, int64_t N, int64_t D, int64_t
     const SkArea sk =
         sk_area(workspace, workspace_bytes, need, dt, N, D, F, T, TPMLP_OP_SWIGLU_BACKWARD);
 
-    const size_t d_stride = round256((size_t)N * Fs * esz);
-    const size_t rest = keeps_rest(dt, N) ? 2 * T * d_stride : 0;   // from a shard's dG (dU) to what its rounding left
+    const size_t rest = keeps_rest(dt, N) ? (size_t)N * Fs * esz : 0;   // from dG (dU) to what its rounding left
+    const size_t d_stride = round256((size_t)N * Fs * esz + rest);
     void *dG[kMaxG], *dU[kMaxG];
     for (int r = 0; r < T; ++r) {
         dG[r] = static_cast<char*>(workspace) + r * d_stride;
@@ -757,6 +758,7 @@ tpmlp_status tpmlp_swiglu_backward(tpmlp_dtype dt, int64_t N, int64_t D, int64_t
     GemmProblem g4 = problem((int)N, (int)D, Fs, T, split ? 1 : 0, Fs, 0, Fs, 0,
                              split ? "bwd_gated_dx_gemm_splitk" : "bwd_gated_dx_gemm_partials");
     g4.chain = 1;
+    g4.rest_rows = rest > 0 && N <= kRestRows ? (int)N : 0;
     g4.epi.kind = EPI_STORE;
     g4.epi.out_f32 = split ? f32 : 1;
     g4.epi.ldc = D;
@@ -769,7 +771,7 @@ tpmlp_status tpmlp_swiglu_backward(tpmlp_dtype dt, int64_t N, int64_t D, int64_t
         g4.B2[r] = Wu[r];
         if (!split) {
             float* pr = reinterpret_cast<float*>(static_cast<char*>(workspace) + 2 * T * d_stride +
-                                                 rest + r * pstride);
+                                                 r * pstride);
             g4.epi.C[r] = pr;
             parts[r] = pr;
         }

@@ -126,6 +126,7 @@ struct TcParams {
     int dual;         // tile = BN/2 outputs of A B (accumulator columns [0, BN/2)) and of
                       // A B2 (columns [BN/2, BN)); N counts outputs
     int chain;        // the K loop of a group walks (tmA, tmB), then (tmAux, tmB2)
+    int rest_rows;    // > 0: accumulator row m + rest_rows is added to row m < rest_rows (<= 16)
     int raster;       // tile order, see decode_tile
     int band;         // band width in tiles
     int ksplit;       // CTAs of a cluster sharing one tile's K range (single-CTA
@@ -933,6 +934,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
         auto emit = [&](int g, int row, int row0, int col0, const uint32_t (&r)[32], int next_col0) {
             float v[32];
             epilogue_bias(p.epi, g, col0, p.N, r, v);
+            if (!PAIR && p.rest_rows > 0) {   // other rows are not stored
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] += __shfl_down_sync(0xffffffffu, v[j], p.rest_rows);
+            }
             const bool z_out = p.epi.kind == EPI_ACT && p.epi.aux[g] != nullptr;
             if (gin) {
                 const uint32_t buf = obuf0 + oset * (uint32_t)C::OUT_BUF;
@@ -1464,12 +1469,12 @@ tpmlp_status launch(const GemmProblem& pr, cudaStream_t s, int ks = 1) {
     for (int g = 0; g < G; ++g) {
         bool ok = true;
         if (!pr.a_mn)
-            ok = make_map(&kp.tmA[g], pr.A[g], pr.K, pr.M, pr.lda, BKB, BM);
+            ok = make_map(&kp.tmA[g], pr.A[g], pr.K, pr.M + pr.rest_rows, pr.lda, BKB, BM);
         else if (!kp.a_3d)
             ok = make_map(&kp.tmA[g], pr.A[g], pr.M, pr.K, pr.lda, BOX_MN, C::BK);
         if (pr.chain) {
             if (!pr.a_mn)
-                ok = ok && make_map(&kp.tmAux[g], pr.A2[g], pr.K, pr.M, pr.lda, BKB, BM);
+                ok = ok && make_map(&kp.tmAux[g], pr.A2[g], pr.K, pr.M + pr.rest_rows, pr.lda, BKB, BM);
             else if (!kp.a_3d)
                 ok = ok && make_map(&kp.tmAux[g], pr.A2[g], pr.M, pr.K, pr.lda, BOX_MN, C::BK);
         }
@@ -1494,6 +1499,9 @@ tpmlp_status launch(const GemmProblem& pr, cudaStream_t s, int ks = 1) {
     kp.dual = pr.dual;
     kp.n_tiles = pr.dual ? (pr.N + BN / 2 - 1) / (BN / 2) : (pr.N + BN - 1) / BN;
     kp.chain = pr.chain;
+    kp.rest_rows = pr.rest_rows;
+    if (pr.rest_rows > 0 && (PAIR || pr.a_mn || !pr.chain || pr.rest_rows != pr.M || pr.M > kRestRows))
+        return TPMLP_ERR_ARG;
     kp.k_blocks = (pr.K + C::BK - 1) / C::BK;
     kp.num_tiles = (pr.fold ? 1 : G) * kp.m_tiles * kp.n_tiles;
     {

@@ -66,6 +66,9 @@ struct GemmProblem {
     // dX. With fold the order is (g, pair, k). Not with dual.
     int chain;
     const void* A2[kMaxG];
+    // > 0 (chain, K-major A, M <= kRestRows): that many rows, M, behind A's (and
+    // A2's) M hold what A's rounding left over, to be added to its products
+    int rest_rows;
     EpiArgs epi;
     const char* name;          // kernel kind, for the timing records
     // Scratch for work-balanced few-token GEMMs (stream-K, M <= 64): partial
@@ -102,6 +105,7 @@ struct WeightGradProduct {
     int M, N;
 };
 constexpr int kMaxWeightGrads = 3 * kMaxG;
+constexpr int kRestRows = 16;   // both parts of a row among one warp's 32 accumulator rows
 // Up to here the list's launch beats the grouped GEMMs (three products of 4096
 // x 4096 by 4 shards on GB300: 61 us against 222 us at 16 tokens, 184 / 246 at
 // 512, 311 / 280 at 1024): writing the outputs bounds it, not the MMAs.

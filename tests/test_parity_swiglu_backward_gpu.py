@@ -185,6 +185,27 @@ def test_weight_gradients_of_few_tokens_are_rounded_once(N):
     assert rounded_once_excess(m, o, f64(dWg), f64(dWu)) <= 1
 
 
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("N,D,F,T", [(1, 264, 272, 2), (2, 64, 1024, 1), (3, 72, 2048, 8), (15, 520, 272, 2),
+                                     (16, 264, 4096, 4), (16, 2056, 136, 1)])
+def test_input_gradient_of_few_tokens_is_rounded_once(N, D, F, T, mode):
+    """As for the weight gradients: up to 16 tokens dX takes dG and dU in two
+    parts, its fp32 additions are D for dH and 4 F here (both parts of both
+    pairs)."""
+    m, s = make(N, D, F, T, "bf16", 90 + N)
+    o = oracle.mlp.swiglu_backward(m["X"], m["Wg"], m["Wu"], m["Wd"], m["H"], m["G"], m["U"], m["dY"])
+    ref = o["dX"]
+    got = run(s, mode)[0].double().cpu().numpy()
+    a = {k: np.abs(oracle.mlp.as_f64(v)) for k, v in m.items()}
+    dH = a["dY"] @ a["Wd"].T
+    terms = (1.1 * dH * a["U"]) @ a["Wg"].T + (dH * a["G"]) @ a["Wu"].T
+    rel = 2.0 ** -16 + (D + 4 * F) * 2.0 ** -24 + 2.0 ** -20
+    own = np.abs(torch.from_numpy(ref).to(torch.bfloat16).double().numpy() - ref)
+    assert np.all(np.abs(got - ref) <= own + 2 * rel * terms)
+    # and well below it on the whole: the rounding's own error, to a tenth
+    assert np.linalg.norm(got - ref) <= 1.1 * np.linalg.norm(own)
+
+
 def test_wrong_shapes_and_lists_are_refused():
     m, s = make(8, 64, 2 * 32, 2, "bf16", 1)
     run(s, "splitk")

@@ -121,7 +121,7 @@ def test_gated_backward_refusals(lib):
                                          dX, s(dWg), sh(), sh(), mode, ws, n, None)
     need = size(2, 1, 4, 16, 32, 2, 1)
     r256 = lambda x: (x + 255) // 256 * 256
-    assert need == 4 * 2 * r256(4 * 16 * 2)      # dG, dU, and what their rounding left over
+    assert need == 2 * 2 * r256(2 * 4 * 16 * 2)      # dG, dU, each with what its rounding left over
     assert size(2, 1, 65, 16, 32, 2, 1) == 2 * 2 * r256(65 * 16 * 2)
     assert size(2, 1, 4, 16, 32, 2, 0) == need + 2 * r256(4 * 16 * 4)
     assert size(2, 0, 4, 16, 32, 2, 0) == 2 * 2 * r256(4 * 16 * 4) + 2 * r256(4 * 16 * 4)
