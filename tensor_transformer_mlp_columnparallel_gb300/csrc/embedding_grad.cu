@@ -76,6 +76,8 @@ constexpr int LOOKUP_UNROLL = 4;
 // which 131 come from DRAM or go there in that time (the rest stays in L2).
 template <typename T, int N>
 __global__ void __launch_bounds__(LOOKUP_THREADS) embedding_scaled_kernel(const LookupArgs p) {
+    pdl_wait();
+    pdl_launch_dependents();
     const int lanes = 1 << p.log_lanes;
     const int64_t group = blockIdx.x / (unsigned)p.segs;
     const int seg = (int)(blockIdx.x - (unsigned)group * (unsigned)p.segs);
@@ -617,18 +619,12 @@ cudaError_t grad_dispatch(const GradArgs& g, int n, cudaStream_t s) {
 template <typename T>
 cudaError_t lookup_dispatch(const LookupArgs& p, int n, unsigned grid, cudaStream_t s) {
     if (n == 8) {
-        if constexpr (sizeof(T) == 2) {
-            embedding_scaled_kernel<T, 8><<<grid, LOOKUP_THREADS, 0, s>>>(p);
-            return cudaGetLastError();
-        }
+        if constexpr (sizeof(T) == 2)
+            return launch_pdl(embedding_scaled_kernel<T, 8>, dim3(grid), LOOKUP_THREADS, 0, s, p);
     }
-    if (n >= 4)
-        embedding_scaled_kernel<T, 4><<<grid, LOOKUP_THREADS, 0, s>>>(p);
-    else if (n == 2)
-        embedding_scaled_kernel<T, 2><<<grid, LOOKUP_THREADS, 0, s>>>(p);
-    else
-        embedding_scaled_kernel<T, 1><<<grid, LOOKUP_THREADS, 0, s>>>(p);
-    return cudaGetLastError();
+    if (n >= 4) return launch_pdl(embedding_scaled_kernel<T, 4>, dim3(grid), LOOKUP_THREADS, 0, s, p);
+    if (n == 2) return launch_pdl(embedding_scaled_kernel<T, 2>, dim3(grid), LOOKUP_THREADS, 0, s, p);
+    return launch_pdl(embedding_scaled_kernel<T, 1>, dim3(grid), LOOKUP_THREADS, 0, s, p);
 }
 
 }  // namespace
