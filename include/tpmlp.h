@@ -331,7 +331,10 @@ tpmlp_status tpmlp_vocab_distill(tpmlp_dtype dt, int64_t N, int64_t V, int T, in
  *   dlogits[n, v] = w_n (p_v - sum_{k: id_k = v} q_k),
  *   w_n = grad_scale * grad_tokens[n] * tau       (grad_tokens NULL: all ones)
  * computed in fp32 and rounded once to dt.
- *   lse          [N] fp32 as written by tpmlp_vocab_distill
+ *   lse          [N] fp32 as written by tpmlp_vocab_distill. p is taken from it
+ *                where its rounding is 2^-19 of p at most (fp32 logits, |lse|
+ *                up to 32; bf16: 2^-15, up to 512); a row beyond is read twice,
+ *                first for its maximum and sum
  *   grad_tokens  [N] fp32 or NULL
  *   dlogits      [N, V] of dt out, row pitch ldd >= V; may be the logits
  *                buffer itself (in place, ldd = ld)
@@ -345,7 +348,8 @@ tpmlp_status tpmlp_vocab_distill_backward(tpmlp_dtype dt, int64_t N, int64_t V, 
 
 /* Both of the above in one launch, for callers that know the upstream
  * gradient beforehand: the logits come from memory once. Outputs are those of
- * the two calls (lse may be NULL; dlogits may be the logits buffer). */
+ * the two calls, up to the order of fp32 sums and the rounding of lse that is
+ * given there (lse may be NULL; dlogits may be the logits buffer). */
 tpmlp_status tpmlp_vocab_distill_with_grad(tpmlp_dtype dt, int64_t N, int64_t V, int T, int K,
                                            const void* logits, int64_t ld,
                                            const int32_t* teacher_ids, const float* teacher_logits,

@@ -156,7 +156,7 @@ tpmlp_status run_vocab_logprobs(int f32, const LogprobArgs& a, cudaStream_t s);
 
 // Distillation from a teacher's top tokens; what is NULL is not computed:
 // loss (with lse) is the forward, dlogits the gradient. The gradient alone
-// reads the forward's lse_in.
+// takes p from the forward's lse_in, where that is precise enough.
 struct DistillArgs {
     const void* logits;
     int64_t ld, N, V;

@@ -910,8 +910,23 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// LOSS: loss and lse; GRAD: the gradient (with LOSS from this launch's
-// statistics, else from the given lse).
+// Up to which |lse| the gradient takes p from lse. It is one fp32 number, and
+// next to a maximum of some size it holds ln S to half an ulp of itself:
+// 2^-24 |lse| of every p, at most 2^-19 here for an fp32 gradient and 2^-15 for
+// a bf16 one, whose own rounding is 2^-8. (Of a row whose tokens all hold a
+// huge value nothing is left of ln S.)
+template <typename T> constexpr float kFarLse = sizeof(T) == 2 ? 512.f : 32.f;
+
+// The gradient of a row beyond, its statistics taken again by a reading of its
+// own. Not inlined, and called where lse is needed first: the other rows are
+// not to pay for it. (bf16 on GB300, all rows near / all beyond: 4096 x 128000
+// 332 / 464 us, 16384 x 32000 327 / 457; fp32, 1003 x 50001: 71 / 96. Always
+// taking them again in one reading, as the fused form does, costs 369, 348
+// and 93. lse read at the kernel's start: 333 near for 16384 x 32000.)
+template <typename T, int NT> __device__ __noinline__ void far_row(const DistillArgs& a, int log_split, int* err);
+
+// One row, of this CTA's cluster. LOSS: loss and lse; GRAD: the gradient, with
+// SUMS (LOSS has them) from this reading's statistics, else from the given lse.
 //
 // With both, the row is read once and stays on the chip: the slice's last
 // chunk in registers, the one before it in shared memory (a thread's own
@@ -920,8 +935,8 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_al
 // bf16 logits on GB300: 350 us, and DRAM moves what the algorithm has to. Of
 // its first form, 384 us, two 512-thread CTAs an SM took 405 us, and a second
 // pass from L2 440, as half of it came from DRAM again.)
-template <typename T, int NT, bool LOSS, bool GRAD>
-__global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArgs a, int log_split, int* err) {
+template <typename T, int NT, bool LOSS, bool SUMS, bool GRAD>
+__device__ __forceinline__ void distill_row(const DistillArgs& a, int log_split, int* err) {
     constexpr bool STAGE = LOSS && GRAD;
     constexpr int WARPS = NT / 32, CHUNK = Row<T, NT>::CHUNK;
     extern __shared__ uint4 stage[];   // STAGE: one chunk; GRAD: then the teacher's slots
@@ -932,9 +947,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
     const int64_t row_i = blockIdx.x >> log_split;
     const int rank = (int)(blockIdx.x & (unsigned)(split - 1));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (LOSS && split > 1) cluster_arrive();   // this CTA runs: its shared memory may be written
-    pdl_wait();
-    pdl_launch_dependents();
+    if (SUMS && split > 1) cluster_arrive();   // this CTA runs: its shared memory may be written
+    if (LOSS || !SUMS) {   // (a far row's kernel has done both)
+        pdl_wait();
+        pdl_launch_dependents();
+    }
     const Row<T, NT> row(a.logits, row_i, a.ld, a.V, rank, log_split);
     T* d = GRAD ? static_cast<T*>(a.dlogits) + row_i * a.ldd : nullptr;
     const int32_t* ids = a.ids + row_i * a.K;
@@ -967,7 +984,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
     if (warp == 0) teacher_row(a, ids, tl, slots, row, LOSS && rank == 0, GRAD, te, list);
 
     Dist dist{};
-    if (LOSS) {
+    if constexpr (SUMS) {
         Soft st{kLowest, 0.f, 0.f};
         if (live) {
             if (row.edges()) {
@@ -1029,21 +1046,30 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
         dist.s = s0.s;
         dist.c = c;
         dist.nothing = s0.s == 0.f;
-        if (rank == 0 && threadIdx.x == 0) {
+        if (LOSS && rank == 0 && threadIdx.x == 0) {
             const float inv_tau = 1.f / a.tau, ln_s = logf(dist.s);
             // a masked token that the teacher wants: ln p = -inf
             const float cross = te.zmax == -INFINITY ? INFINITY : ln_s - (te.q_z + (te.zmax - dist.ref)) * inv_tau;
             a.loss[row_i] = te.bad ? NAN : te.some ? a.tau * a.tau * (te.q_ln_q + cross) : 0.f;
-            if (a.lse)
-                a.lse[row_i] = te.bad ? NAN : !te.some ? 0.f : dist.nothing ? -INFINITY : fmaf(dist.ref, inv_tau, ln_s);
+            if (a.lse) {
+                // ref / tau + ln S: what the quotient's rounding left over joins ln S
+                const float quot = dist.ref * inv_tau, over = fmaf(-quot, a.tau, dist.ref) * inv_tau;
+                a.lse[row_i] = te.bad ? NAN : !te.some ? 0.f : dist.nothing ? -INFINITY
+                               : isinf(quot) ? quot : quot + (over + ln_s);
+            }
         }
     } else {
         __syncthreads();   // the teacher's statistics
+        // p = 2^((z - lse tau) c); what the product's rounding left over is in s
+        dist.c = c;
+        dist.nothing = false;
         const float lse = a.lse_in[row_i];
-        dist.c = c;   // p = 2^((z - lse tau) c)
-        dist.nothing = lse == -INFINITY;
+        if (!(fabsf(lse) <= kFarLse<T>)) {
+            far_row<T, NT>(a, log_split, err);
+            return;
+        }
         dist.ref = lse * a.tau;
-        dist.s = 1.f;
+        dist.s = ex2(fmaf(lse, a.tau, -dist.ref) * c);
     }
     if (GRAD) {
         const float w = a.grad_scale * (a.grad_tokens ? a.grad_tokens[row_i] : 1.f) * a.tau;
@@ -1086,7 +1112,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
         } else {
             // Back to front: the last chunk is still in registers, what was read
             // last is the likeliest to be in L2.
-            if (!LOSS && !early) row.load_rest(rest, x);
+            if (!SUMS && !early) row.load_rest(rest, x);
 #pragma unroll
             for (int r = 0; r < VPT; ++r) {
                 const int i = rest + r * NT + (int)threadIdx.x;
@@ -1129,6 +1155,23 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistillArg
         }
     }
     if (rank == 0 && threadIdx.x == 0 && te.bad) atomicCAS(err, 0, (int)TPMLP_ERR_ARG);
+}
+
+template <typename T, int NT>
+__device__ __noinline__ void far_row(const DistillArgs& a, int log_split, int* err) {
+    distill_row<T, NT, false, true, true>(a, log_split, err);
+}
+
+template <typename T, int NT, bool GRAD>
+__global__ void __launch_bounds__(NT, 1024 / NT) distill_loss_kernel(const DistillArgs a, int log_split, int* err) {
+    distill_row<T, NT, true, true, GRAD>(a, log_split, err);
+}
+
+// __grid_constant__: the far rows' call takes the arguments by address.
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT)
+    distill_grad_kernel(const __grid_constant__ DistillArgs a, int log_split, int* err) {
+    distill_row<T, NT, false, false, true>(a, log_split, err);
 }
 
 // ---------------------------------------------------------------- launch --
@@ -1182,17 +1225,17 @@ tpmlp_status distill_rows(const DistillArgs& a, cudaStream_t s, int* err) {
     if (a.dlogits == nullptr) {
         const int split = row_split(a.N, bytes, NT, 0);
         LaunchScope ls("vocab_distill", s);
-        return launch_rows(distill_kernel<T, NT, true, false>, NT, 0, a.N, split, s, a, split, err);
+        return launch_rows(distill_loss_kernel<T, NT, false>, NT, 0, a.N, split, s, a, split, err);
     }
     if (a.loss == nullptr) {
         const int split = row_split(a.N, bytes, NT, 0);
         LaunchScope ls("vocab_distill_backward", s);
-        return launch_rows(distill_kernel<T, NT, false, true>, NT, list, a.N, split, s, a, split, err);
+        return launch_rows(distill_grad_kernel<T, NT>, NT, list, a.N, split, s, a, split, err);
     }
     constexpr int CHUNK = Row<T, NT>::CHUNK;
     const int split = row_split(a.N, bytes, NT, 2 * CHUNK);
     LaunchScope ls("vocab_distill_with_grad", s);
-    return launch_rows(distill_kernel<T, NT, true, true>, NT, CHUNK * sizeof(uint4) + list, a.N, split, s, a,
+    return launch_rows(distill_loss_kernel<T, NT, true>, NT, CHUNK * sizeof(uint4) + list, a.N, split, s, a,
                        split, err);
 }
 
