@@ -197,13 +197,13 @@ def vocab_logprobs(logits: torch.Tensor, targets: torch.Tensor, T: int, top_k: i
 
 
 def _dlogits_like(logits: torch.Tensor, in_place: bool) -> torch.Tensor:
-    """A gradient in rows of the logits' pitch, so that both sides of a row
-    have the same alignment."""
+    """A gradient in the shortest rows that have the logits' alignment, row by
+    row (the pitch modulo a 128-byte line decides it, not the pitch)."""
     if in_place:
         return logits
     N, V = logits.shape
-    ld = logits.stride(0) if N > 1 else V
-    return torch.empty((N, ld), dtype=logits.dtype, device=logits.device)[:, :V]
+    pad = (logits.stride(0) - V) % (128 // logits.element_size()) if N > 1 else 0
+    return torch.empty((N, V + pad), dtype=logits.dtype, device=logits.device)[:, :V]
 
 
 def vocab_distill(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
