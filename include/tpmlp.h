@@ -292,7 +292,7 @@ tpmlp_status tpmlp_vocab_ce_backward(int64_t N, int64_t V, int T, const float* l
  *   lse           [N] fp32 out, or NULL
  *   top_ids       [N, K] int32 out, top_logprobs [N, K] fp32 out (unused for K = 0)
  * Errors: TPMLP_ERR_SHAPE if V % T != 0, ld < V, K outside
- * [0, min(V, TPMLP_MAX_TOP)]; TPMLP_ERR_ALIGN if logits is not aligned to its
+ * [0, min(V, TPMLP_MAX_TOP)]; TPMLP_ERR_ALIGN if a pointer is not aligned to its
  * element. A target outside [0, V) writes NaN (rank 0) for that token and sets
  * TPMLP_ERR_ARG in the device error word. */
 tpmlp_status tpmlp_vocab_logprobs(tpmlp_dtype dt, int64_t N, int64_t V, int T, int K,
@@ -359,7 +359,8 @@ tpmlp_status tpmlp_vocab_distill_with_grad(tpmlp_dtype dt, int64_t N, int64_t V,
 
 /* tpmlp_vocab_embedding times a factor: out[n] = scale * table[ids[n]],
  * multiplied in fp32 and rounded once to dt. Arguments, shards and errors as
- * tpmlp_vocab_embedding; V and Hd at most 2^31 - 1. */
+ * tpmlp_vocab_embedding; V and Hd at most 2^31 - 1; TPMLP_ERR_ALIGN if a pointer
+ * is not aligned to its element. */
 tpmlp_status tpmlp_vocab_embedding_scaled(tpmlp_dtype dt, int64_t N, int64_t V, int64_t Hd, int T,
                                           const int64_t* ids, const void* const* table,
                                           float scale, void* out, void* stream);
@@ -376,9 +377,9 @@ tpmlp_status tpmlp_vocab_embedding_scaled(tpmlp_dtype dt, int64_t N, int64_t V, 
  *   dout       [N, Hd] of dt
  *   dtable     host array of T device pointers, each [V/T, Hd] of grad_dt
  *   workspace  tpmlp_vocab_embedding_backward_workspace_bytes(N, V, Hd) bytes,
- *              16-byte aligned
+ *              16-byte aligned (the other pointers: to their element)
  * Errors: TPMLP_ERR_SHAPE if V % T != 0, or N or V above 2^31 - 2;
- * TPMLP_ERR_WORKSPACE. An id outside [0, V) contributes to no row and sets
+ * TPMLP_ERR_WORKSPACE; TPMLP_ERR_ALIGN. An id outside [0, V) contributes to no row and sets
  * TPMLP_ERR_ARG in the device error word. */
 tpmlp_status tpmlp_vocab_embedding_backward(tpmlp_dtype dt, tpmlp_dtype grad_dt, int64_t N,
                                             int64_t V, int64_t Hd, int T, const int64_t* ids,

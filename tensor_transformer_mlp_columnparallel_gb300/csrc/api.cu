@@ -17,6 +17,7 @@
 #include <atomic>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <string>
@@ -848,6 +849,14 @@ tpmlp_status tpmlp_vocab_ce_backward(int64_t N, int64_t V, int T, const float* l
                                  static_cast<cudaStream_t>(stream));
 }
 
+// every pointer (or NULL) at a multiple of `size` bytes: a kernel's access elsewhere would fault
+static tpmlp_status check_align(size_t size, std::initializer_list<const void*> ptrs) {
+    for (const void* p : ptrs)
+        if (reinterpret_cast<uintptr_t>(p) % size != 0) return TPMLP_ERR_ALIGN;
+    return TPMLP_OK;
+}
+static size_t elem_size(tpmlp_dtype dt) { return dt == TPMLP_F32 ? 4 : 2; }
+
 // Sizes and pointers the row operators share: [N, V] logits of dt in rows of ld
 static tpmlp_status check_rows(tpmlp_dtype dt, int64_t N, int64_t V, int T, const void* logits,
                                int64_t ld) {
@@ -857,8 +866,7 @@ static tpmlp_status check_rows(tpmlp_dtype dt, int64_t N, int64_t V, int T, cons
     if (V > 0x7fffff00LL || N > 0x7fffffffLL || ld > (1LL << 40)) return TPMLP_ERR_SHAPE;
     if (N > 0) {
         if (logits == nullptr) return TPMLP_ERR_ARG;
-        if (reinterpret_cast<uintptr_t>(logits) % (dt == TPMLP_F32 ? 4 : 2) != 0)
-            return TPMLP_ERR_ALIGN;
+        TPMLP_TRY(check_align(elem_size(dt), {logits}));
     }
     return TPMLP_OK;
 }
@@ -872,6 +880,9 @@ tpmlp_status tpmlp_vocab_logprobs(tpmlp_dtype dt, int64_t N, int64_t V, int T, i
     if (N == 0) return TPMLP_OK;
     if (targets == nullptr && (logprob != nullptr || rank != nullptr)) return TPMLP_ERR_ARG;
     if (K > 0 && (top_ids == nullptr || top_logprobs == nullptr)) return TPMLP_ERR_ARG;
+    TPMLP_TRY(check_align(8, {targets}));
+    TPMLP_TRY(check_align(4, {logprob, rank, entropy, lse}));
+    if (K > 0) TPMLP_TRY(check_align(4, {top_ids, top_logprobs}));
     LogprobArgs a{};
     a.logits = logits;
     a.ld = ld;
@@ -896,6 +907,7 @@ static tpmlp_status distill_args(tpmlp_dtype dt, int64_t N, int64_t V, int T, in
     if (K < 1 || K > TPMLP_MAX_TEACHER) return TPMLP_ERR_SHAPE;
     if (!(tau > 0.f) || !(tau < 3.4e38f)) return TPMLP_ERR_ARG;
     if (N > 0 && (teacher_ids == nullptr || teacher_logits == nullptr)) return TPMLP_ERR_ARG;
+    TPMLP_TRY(check_align(4, {teacher_ids, teacher_logits}));
     a = DistillArgs{};
     a.logits = logits;
     a.ld = ld;
@@ -908,15 +920,23 @@ static tpmlp_status distill_args(tpmlp_dtype dt, int64_t N, int64_t V, int T, in
     return TPMLP_OK;
 }
 
+static tpmlp_status distill_loss_args(float* loss_per_token, float* loss_mean, float* lse, DistillArgs& a) {
+    if (a.N > 0 && loss_per_token == nullptr) return TPMLP_ERR_ARG;
+    TPMLP_TRY(check_align(4, {loss_per_token, loss_mean, lse}));
+    a.loss = loss_per_token;
+    a.lse = lse;
+    return TPMLP_OK;
+}
+
 static tpmlp_status distill_grad_args(tpmlp_dtype dt, const float* grad_tokens, float grad_scale,
                                       void* dlogits, int64_t ldd, DistillArgs& a) {
     if (ldd < a.V || ldd > (1LL << 40)) return TPMLP_ERR_SHAPE;
     if (a.N > 0) {
         if (dlogits == nullptr) return TPMLP_ERR_ARG;
-        if (reinterpret_cast<uintptr_t>(dlogits) % (dt == TPMLP_F32 ? 4 : 2) != 0)
-            return TPMLP_ERR_ALIGN;
+        TPMLP_TRY(check_align(elem_size(dt), {dlogits}));
         if (dlogits == a.logits && ldd != a.ld) return TPMLP_ERR_ARG;   // in place: the same rows
     }
+    TPMLP_TRY(check_align(4, {grad_tokens}));
     a.grad_tokens = grad_tokens;
     a.grad_scale = grad_scale;
     a.dlogits = dlogits;
@@ -930,9 +950,7 @@ tpmlp_status tpmlp_vocab_distill(tpmlp_dtype dt, int64_t N, int64_t V, int T, in
                                  float* loss_mean, float* lse, void* stream) {
     DistillArgs a;
     TPMLP_TRY(distill_args(dt, N, V, T, K, logits, ld, teacher_ids, teacher_logits, tau, a));
-    if (N > 0 && loss_per_token == nullptr) return TPMLP_ERR_ARG;
-    a.loss = loss_per_token;
-    a.lse = lse;
+    TPMLP_TRY(distill_loss_args(loss_per_token, loss_mean, lse, a));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     TPMLP_TRY(run_vocab_distill(dt == TPMLP_F32, a, s));
     return loss_mean != nullptr ? run_mean(loss_per_token, N, loss_mean, s) : TPMLP_OK;
@@ -948,6 +966,7 @@ tpmlp_status tpmlp_vocab_distill_backward(tpmlp_dtype dt, int64_t N, int64_t V, 
     TPMLP_TRY(distill_args(dt, N, V, T, K, logits, ld, teacher_ids, teacher_logits, tau, a));
     TPMLP_TRY(distill_grad_args(dt, grad_tokens, grad_scale, dlogits, ldd, a));
     if (N > 0 && lse == nullptr) return TPMLP_ERR_ARG;
+    TPMLP_TRY(check_align(4, {lse}));
     a.lse_in = lse;
     return run_vocab_distill(dt == TPMLP_F32, a, static_cast<cudaStream_t>(stream));
 }
@@ -961,9 +980,7 @@ tpmlp_status tpmlp_vocab_distill_with_grad(tpmlp_dtype dt, int64_t N, int64_t V,
     DistillArgs a;
     TPMLP_TRY(distill_args(dt, N, V, T, K, logits, ld, teacher_ids, teacher_logits, tau, a));
     TPMLP_TRY(distill_grad_args(dt, grad_tokens, grad_scale, dlogits, ldd, a));
-    if (N > 0 && loss_per_token == nullptr) return TPMLP_ERR_ARG;
-    a.loss = loss_per_token;
-    a.lse = lse;
+    TPMLP_TRY(distill_loss_args(loss_per_token, loss_mean, lse, a));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     TPMLP_TRY(run_vocab_distill(dt == TPMLP_F32, a, s));
     return loss_mean != nullptr ? run_mean(loss_per_token, N, loss_mean, s) : TPMLP_OK;
@@ -978,8 +995,12 @@ tpmlp_status tpmlp_vocab_embedding_scaled(tpmlp_dtype dt, int64_t N, int64_t V, 
     if (V > 0x7fffffffLL || Hd > 0x7fffffffLL) return TPMLP_ERR_SHAPE;
     if (N == 0) return TPMLP_OK;
     if (ids == nullptr || out == nullptr || table == nullptr) return TPMLP_ERR_ARG;
-    for (int k = 0; k < T; ++k)
+    for (int k = 0; k < T; ++k) {
         if (table[k] == nullptr) return TPMLP_ERR_ARG;
+        TPMLP_TRY(check_align(elem_size(dt), {table[k]}));
+    }
+    TPMLP_TRY(check_align(8, {ids}));
+    TPMLP_TRY(check_align(elem_size(dt), {out}));
     return run_vocab_embedding_scaled(dt == TPMLP_F32, N, V, Hd, T, ids, table, scale, out,
                                       static_cast<cudaStream_t>(stream));
 }
@@ -1002,8 +1023,14 @@ tpmlp_status tpmlp_vocab_embedding_backward(tpmlp_dtype dt, tpmlp_dtype grad_dt,
     const size_t need = tpmlp_vocab_embedding_backward_workspace_bytes(N, V, Hd);
     if (need == (size_t)-1) return TPMLP_ERR_SHAPE;
     if (dtable == nullptr || (N > 0 && (ids == nullptr || dout == nullptr))) return TPMLP_ERR_ARG;
-    for (int k = 0; k < T; ++k)
+    for (int k = 0; k < T; ++k) {
         if (dtable[k] == nullptr) return TPMLP_ERR_ARG;
+        TPMLP_TRY(check_align(elem_size(grad_dt), {dtable[k]}));
+    }
+    if (N > 0) {
+        TPMLP_TRY(check_align(8, {ids}));
+        TPMLP_TRY(check_align(elem_size(dt), {dout}));
+    }
     if (workspace == nullptr || workspace_bytes < need) return TPMLP_ERR_WORKSPACE;
     if (!aligned16(workspace)) return TPMLP_ERR_ALIGN;
     return run_vocab_embedding_backward(dt == TPMLP_F32, grad_dt == TPMLP_F32, N, V, Hd, T, ids,
@@ -1037,7 +1064,7 @@ const char* tpmlp_status_str(tpmlp_status s) {
         case TPMLP_OK: return "TPMLP_OK";
         case TPMLP_ERR_ARG: return "TPMLP_ERR_ARG: invalid argument";
         case TPMLP_ERR_SHAPE: return "TPMLP_ERR_SHAPE: invalid shape (F % T, V % T, T range, zero width)";
-        case TPMLP_ERR_ALIGN: return "TPMLP_ERR_ALIGN: pointer or row pitch not 16-byte aligned";
+        case TPMLP_ERR_ALIGN: return "TPMLP_ERR_ALIGN: pointer or row pitch not aligned (16 bytes, or its element)";
         case TPMLP_ERR_DTYPE: return "TPMLP_ERR_DTYPE: unknown element type";
         case TPMLP_ERR_CUDA: return "TPMLP_ERR_CUDA: CUDA call failed";
         case TPMLP_ERR_TIMEOUT: return "TPMLP_ERR_TIMEOUT: a bounded device wait expired";
