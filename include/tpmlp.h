@@ -491,6 +491,11 @@ tpmlp_status tpmlp_selftest_wait_timeout(uint64_t timeout_ns, void* stream);
  * other thread launches GEMMs. Library extension for tests. */
 tpmlp_status tpmlp_selftest_gemm_stall(int role);
 
+/* The same for the gated backward's launch of few-token weight gradients
+ * alone: the GEMMs around it run as ever, so what the error word says is this
+ * launch's own (it also takes part in the GEMMs' stall above). */
+tpmlp_status tpmlp_selftest_weight_grad_stall(int role);
+
 /* ---- instrumentation ---------------------------------------------------- */
 
 /* Launch configuration the bf16 tensor-core GEMM chooses on the current

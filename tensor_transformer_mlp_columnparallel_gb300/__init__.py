@@ -25,6 +25,7 @@ from ._binding import (  # noqa: F401
     tpmlp_launch_count,
     tpmlp_selftest_gemm_stall,
     tpmlp_selftest_wait_timeout,
+    tpmlp_selftest_weight_grad_stall,
     tpmlp_set_wait_timeout_ns,
     tpmlp_swiglu_backward,
     tpmlp_swiglu_forward,

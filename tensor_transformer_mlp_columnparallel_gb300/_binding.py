@@ -83,6 +83,7 @@ _SIGNATURES = {
     "tpmlp_set_wait_timeout_ns": (None, [ctypes.c_uint64]),
     "tpmlp_selftest_wait_timeout": (_int, [ctypes.c_uint64, _vp]),
     "tpmlp_selftest_gemm_stall": (_int, [_int]),
+    "tpmlp_selftest_weight_grad_stall": (_int, [_int]),
     "tpmlp_launch_count": (ctypes.c_int64, []),
     "tpmlp_gemm_plan": (_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _int, _int, _int,
                                _int, ctypes.POINTER(_int), ctypes.POINTER(_int),
@@ -509,6 +510,11 @@ def tpmlp_selftest_gemm_stall(role: int):
     bf16 GEMM launch makes that role stall on a barrier nothing completes
     until the bounded wait runs out; 0 turns it off."""
     _check(lib().tpmlp_selftest_gemm_stall(int(role)))
+
+
+def tpmlp_selftest_weight_grad_stall(role: int):
+    """The same for the launch of few-token weight gradients alone."""
+    _check(lib().tpmlp_selftest_weight_grad_stall(int(role)))
 
 
 def tpmlp_launch_count() -> int:

@@ -40,6 +40,7 @@ int* g_err_ptr[kMaxDevices] = {};
 int g_sms[kMaxDevices] = {};
 std::atomic<uint64_t> g_timeout_ns{2000000000ull};
 std::atomic<int> g_gemm_stall{0};
+std::atomic<int> g_weight_grad_stall{0};
 std::atomic<int64_t> g_launches{0};
 
 int current_device() {
@@ -64,6 +65,11 @@ int* device_error_word() {
 uint64_t wait_timeout_ns() { return g_timeout_ns.load(); }
 
 int gemm_stall_role() { return g_gemm_stall.load(); }
+
+int weight_grad_stall_role() {
+    const int own = g_weight_grad_stall.load();
+    return own != 0 ? own : g_gemm_stall.load();
+}
 
 bool pdl_enabled() {
     // TPMLP_PDL=0 in the environment launches every kernel fully serialized
@@ -1093,6 +1099,12 @@ tpmlp_status tpmlp_selftest_wait_timeout(uint64_t timeout_ns, void* stream) {
 tpmlp_status tpmlp_selftest_gemm_stall(int role) {
     if (role < 0 || role > 3) return TPMLP_ERR_ARG;
     g_gemm_stall.store(role);
+    return TPMLP_OK;
+}
+
+tpmlp_status tpmlp_selftest_weight_grad_stall(int role) {
+    if (role < 0 || role > 3) return TPMLP_ERR_ARG;
+    g_weight_grad_stall.store(role);
     return TPMLP_OK;
 }
 

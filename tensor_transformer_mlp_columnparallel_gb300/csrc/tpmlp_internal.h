@@ -189,6 +189,7 @@ tpmlp_status run_selftest_wait(uint64_t timeout_ns, cudaStream_t s);
 int* device_error_word();          // per current device; NULL on failure
 uint64_t wait_timeout_ns();
 int gemm_stall_role();             // failure-detection self test of the GEMM (0: off)
+int weight_grad_stall_role();      // of the few-token weight gradients: their own, else the GEMM's
 bool pdl_enabled();                // programmatic dependent launch (TPMLP_PDL != 0)
 bool alternate_orders();           // odd waves walk K down, odd bands their tiles back (TPMLP_ALT_ORDER != 0)
 int device_sm_count();

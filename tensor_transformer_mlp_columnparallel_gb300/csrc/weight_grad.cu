@@ -291,7 +291,7 @@ tpmlp_status run_weight_grads(const WeightGradProduct* products, int count, int 
     p.err = device_error_word();
     if (p.err == nullptr) return TPMLP_ERR_CUDA;
     p.timeout_ns = wait_timeout_ns();
-    p.inject = gemm_stall_role();
+    p.inject = weight_grad_stall_role();
     p.drain_ns = p.timeout_ns > 100000000ull ? p.timeout_ns : 100000000ull;
     if (cudaFuncSetAttribute(weight_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, WG_SMEM) != cudaSuccess)
         return TPMLP_ERR_CUDA;
