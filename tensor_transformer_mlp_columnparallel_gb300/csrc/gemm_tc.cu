@@ -1450,20 +1450,18 @@ tpmlp_status launch(const GemmProblem& pr, cudaStream_t s, int ks = 1) {
     std::lock_guard<std::mutex> lock(mu);
     memset(&kp, 0, sizeof(kp));
     const int G = pr.G;
+    if (pr.chain && (pr.dual || pr.a_mn || pr.b_mn)) return TPMLP_ERR_ARG;   // its maps are K-major
     // MN-major operands whose MN extent is a multiple of 64 use one 3-D box per
     // stage; if the driver refuses that map, the 2-D boxes are used instead
     // B rows staged per map: half the tile's N for a dual GEMM
     const int b_rows = pr.dual ? BN / 2 : C::B_ROWS;
     kp.a_3d = pr.a_mn && pr.M % BOX_MN == 0;
     kp.b_3d = pr.b_mn && pr.N % BOX_MN == 0;
-    for (int g = 0; g < G && kp.a_3d; ++g) {
+    for (int g = 0; g < G && kp.a_3d; ++g)
         kp.a_3d = make_map_mn_chunks(&kp.tmA[g], pr.A[g], pr.M, pr.K, pr.lda, BM, C::BK);
-        if (kp.a_3d && pr.chain)
-            kp.a_3d = make_map_mn_chunks(&kp.tmAux[g], pr.A2[g], pr.M, pr.K, pr.lda, BM, C::BK);
-    }
     for (int g = 0; g < G && kp.b_3d; ++g) {
         kp.b_3d = make_map_mn_chunks(&kp.tmB[g], pr.B[g], pr.N, pr.K, pr.ldb, b_rows, C::BK);
-        if (kp.b_3d && (pr.dual || pr.chain))
+        if (kp.b_3d && pr.dual)
             kp.b_3d = make_map_mn_chunks(&kp.tmB2[g], pr.B2[g], pr.N, pr.K, pr.ldb, b_rows, C::BK);
     }
     for (int g = 0; g < G; ++g) {
@@ -1472,12 +1470,8 @@ tpmlp_status launch(const GemmProblem& pr, cudaStream_t s, int ks = 1) {
             ok = make_map(&kp.tmA[g], pr.A[g], pr.K, pr.M + pr.rest_rows, pr.lda, BKB, BM);
         else if (!kp.a_3d)
             ok = make_map(&kp.tmA[g], pr.A[g], pr.M, pr.K, pr.lda, BOX_MN, C::BK);
-        if (pr.chain) {
-            if (!pr.a_mn)
-                ok = ok && make_map(&kp.tmAux[g], pr.A2[g], pr.K, pr.M + pr.rest_rows, pr.lda, BKB, BM);
-            else if (!kp.a_3d)
-                ok = ok && make_map(&kp.tmAux[g], pr.A2[g], pr.M, pr.K, pr.lda, BOX_MN, C::BK);
-        }
+        if (pr.chain)
+            ok = ok && make_map(&kp.tmAux[g], pr.A2[g], pr.K, pr.M + pr.rest_rows, pr.lda, BKB, BM);
         for (int d = 0; d < (pr.dual || pr.chain ? 2 : 1); ++d) {
             CUtensorMap* m = d == 0 ? &kp.tmB[g] : &kp.tmB2[g];
             const void* b = d == 0 ? pr.B[g] : pr.B2[g];
@@ -1500,7 +1494,7 @@ tpmlp_status launch(const GemmProblem& pr, cudaStream_t s, int ks = 1) {
     kp.n_tiles = pr.dual ? (pr.N + BN / 2 - 1) / (BN / 2) : (pr.N + BN - 1) / BN;
     kp.chain = pr.chain;
     kp.rest_rows = pr.rest_rows;
-    if (pr.rest_rows > 0 && (PAIR || pr.a_mn || !pr.chain || pr.rest_rows != pr.M || pr.M > kRestRows))
+    if (pr.rest_rows > 0 && (PAIR || !pr.chain || pr.rest_rows != pr.M || pr.M > kRestRows))
         return TPMLP_ERR_ARG;
     kp.k_blocks = (pr.K + C::BK - 1) / C::BK;
     kp.num_tiles = (pr.fold ? 1 : G) * kp.m_tiles * kp.n_tiles;
