@@ -1211,9 +1211,6 @@ tpmlp_status launch_rows(void (*kernel)(P...), int threads, size_t smem, int64_t
         attr[1].val.clusterDim.z = 1;
         cfg.numAttrs = 2;
     }
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return TPMLP_ERR_CUDA;
     if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return TPMLP_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
 }
@@ -1233,6 +1230,10 @@ tpmlp_status distill_rows(const DistillArgs& a, cudaStream_t s, int* err) {
         return launch_rows(distill_grad_kernel<T, NT>, NT, list, a.N, split, s, a, split, err);
     }
     constexpr int CHUNK = Row<T, NT>::CHUNK;
+    // what a launch has without asking for more
+    static_assert(CHUNK * sizeof(uint4) + TPMLP_MAX_TEACHER * sizeof(TeacherSlot) +
+                          MAX_SPLIT * (NT / 32) * sizeof(WarpSoft) + sizeof(TeacherShared) <= 48 * 1024,
+                  "shared memory");
     const int split = row_split(a.N, bytes, NT, 2 * CHUNK);
     LaunchScope ls("vocab_distill_with_grad", s);
     return launch_rows(distill_loss_kernel<T, NT, true>, NT, CHUNK * sizeof(uint4) + list, a.N, split, s, a,
