@@ -378,7 +378,8 @@ tpmlp_status tpmlp_vocab_embedding_scaled(tpmlp_dtype dt, int64_t N, int64_t V, 
  *   dtable     host array of T device pointers, each [V/T, Hd] of grad_dt
  *   workspace  tpmlp_vocab_embedding_backward_workspace_bytes(N, V, Hd) bytes,
  *              16-byte aligned (the other pointers: to their element)
- * Errors: TPMLP_ERR_SHAPE if V % T != 0, or N or V above 2^31 - 2;
+ * Errors: TPMLP_ERR_SHAPE if V % T != 0, N or V above 2^31 - 2, or Hd above
+ * 16776960 accesses (of 1 to 8 elements, as alignment allows);
  * TPMLP_ERR_WORKSPACE; TPMLP_ERR_ALIGN. An id outside [0, V) contributes to no row and sets
  * TPMLP_ERR_ARG in the device error word. */
 tpmlp_status tpmlp_vocab_embedding_backward(tpmlp_dtype dt, tpmlp_dtype grad_dt, int64_t N,

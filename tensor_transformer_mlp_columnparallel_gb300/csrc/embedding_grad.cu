@@ -602,6 +602,7 @@ cudaError_t grad_launch(const GradArgs& g, cudaStream_t s) {
     }
     if (e != cudaSuccess) return e;
     LaunchScope ls("embedding_grad", s);
+    // N, V < 2^31, at most 8 joining CTAs a block or 2048, at least 8 rows a CTA: below 2^30
     const int64_t grid = (int64_t)g.blocks * g.join_ctas + (g.V + g.rows - 1) / g.rows;
     return launch_pdl(embedding_grad_kernel<T, N, GT>, dim3((unsigned)grid), GRAD_THREADS, 0, s, g);
 }
@@ -673,11 +674,24 @@ tpmlp_status run_vocab_embedding_backward(int f32, int grad_f32, int64_t N, int6
                                           int accumulate, void* const* dtable, void* workspace,
                                           cudaStream_t s) {
     if (N == 0 && accumulate) return TPMLP_OK;
+    GradArgs g{};
+    uintptr_t in_align = reinterpret_cast<uintptr_t>(dout), out_align = 0;
+    for (int k = 0; k < T; ++k) {
+        g.dtable[k] = dtable[k];
+        out_align |= reinterpret_cast<uintptr_t>(dtable[k]);
+    }
+    // the same elements per access on both sides (a bf16 pack of 8 is two
+    // 16-byte stores of fp32)
+    const int gsize = grad_f32 ? 4 : 2;
+    const int zn = pack_elems(out_align, H, gsize);
+    int n = pack_elems(in_align, H, f32 ? 4 : 2);
+    if (n > zn && !(n == 8 && zn == 4 && grad_f32)) n = zn;
+    g.packs = (int)(H / n);
+    if ((g.packs + (int64_t)GRAD_THREADS - 1) / GRAD_THREADS > 65535) return TPMLP_ERR_SHAPE;   // the grid's y
     const GradLayout l = grad_layout(N, V, H);
     char* ws = static_cast<char*>(workspace);
     int* err = device_error_word();
     if (err == nullptr) return TPMLP_ERR_CUDA;
-    GradArgs g{};
     g.seg = reinterpret_cast<int2*>(ws + l.seg);
     if (N > 0) {
         SortArgs p{};
@@ -730,17 +744,6 @@ tpmlp_status run_vocab_embedding_backward(int f32, int grad_f32, int64_t N, int6
             }
         }
     }
-    uintptr_t in_align = reinterpret_cast<uintptr_t>(dout), out_align = 0;
-    for (int k = 0; k < T; ++k) {
-        g.dtable[k] = dtable[k];
-        out_align |= reinterpret_cast<uintptr_t>(dtable[k]);
-    }
-    // the same elements per access on both sides (a bf16 pack of 8 is two
-    // 16-byte stores of fp32)
-    const int gsize = grad_f32 ? 4 : 2;
-    const int zn = pack_elems(out_align, H, gsize);
-    int n = pack_elems(in_align, H, f32 ? 4 : 2);
-    if (n > zn && !(n == 8 && zn == 4 && grad_f32)) n = zn;
     g.dout = dout;
     g.pieces = reinterpret_cast<float*>(ws + l.pieces);
     g.N = N;
@@ -749,7 +752,6 @@ tpmlp_status run_vocab_embedding_backward(int f32, int grad_f32, int64_t N, int6
     g.H = H;
     g.Hp = piece_pitch(H);
     g.blocks = (int)grad_blocks(N);
-    g.packs = (int)(H / n);
     // a block's columns over up to 8 CTAs, and over more where the blocks are few
     const int64_t join_cols = (H + JOIN_COLS - 1) / JOIN_COLS;
     const int64_t most = g.blocks > 0 && JOIN_CTAS / g.blocks > 8 ? JOIN_CTAS / g.blocks : 8;
@@ -760,9 +762,6 @@ tpmlp_status run_vocab_embedding_backward(int f32, int grad_f32, int64_t N, int6
     g.rows = !g.by_warp ? GRAD_WARPS : row_bytes * GRAD_ROWS <= GRAD_BYTES ? GRAD_ROWS : (int)(GRAD_BYTES / row_bytes);
     g.scale = scale;
     g.accumulate = accumulate;
-    if ((int64_t)g.blocks * g.join_ctas + V / GRAD_WARPS + 1 > 0x7fffffffLL ||
-        (g.packs + GRAD_THREADS - 1) / GRAD_THREADS > 65535)
-        return TPMLP_ERR_SHAPE;
     cudaError_t e;
     if (f32)
         e = grad_f32 ? grad_dispatch<float, float>(g, n, s) : grad_dispatch<float, __nv_bfloat16>(g, n, s);

@@ -92,3 +92,12 @@ def test_a_table_without_tokens_is_checked_too(lib):
     need = lib.tpmlp_vocab_embedding_backward_workspace_bytes(0, 12, 8)
     assert lib.tpmlp_vocab_embedding_backward(F32, F32, 0, 12, 8, 1, None, None, 1.0, 0, ptrs(FAKE + 2), FAKE,
                                               need, None) == B.ERR_ALIGN
+
+
+@pytest.mark.parametrize("H,off", [((1 << 31) - 2, 0), (16776961, 0), (4 * 16776960, 4)])
+def test_rows_beyond_the_launch_are_refused_before_it(lib, H, off):
+    """More accesses in a row than the grid has columns for: odd rows, rows whose
+    pointers allow only single elements."""
+    need = lib.tpmlp_vocab_embedding_backward_workspace_bytes(4, 12, H)
+    assert lib.tpmlp_vocab_embedding_backward(F32, F32, 4, 12, H, 2, FAKE, FAKE + off, 1.0, 0, ptrs(FAKE, FAKE),
+                                              FAKE, need, None) == B.ERR_SHAPE
