@@ -317,7 +317,7 @@ tpmlp_status tpmlp_vocab_logprobs(tpmlp_dtype dt, int64_t N, int64_t V, int T, i
  *   loss_per_token  [N] fp32 out
  *   loss_mean       [1] fp32 out, or NULL: (1/N) sum_n loss_n (fixed order)
  *   lse             [N] fp32 out, or NULL (the backward's input)
- * Errors: TPMLP_ERR_ARG for tau not finite or <= 0; TPMLP_ERR_SHAPE if
+ * Errors: TPMLP_ERR_ARG for tau outside [2^-60, 2^60]; TPMLP_ERR_SHAPE if
  * V % T != 0, ld < V, K outside [1, TPMLP_MAX_TEACHER]; TPMLP_ERR_ALIGN if a
  * pointer is not aligned to its element. An id outside [-1, V) writes NaN for
  * that row (loss and gradient) and sets TPMLP_ERR_ARG in the device error word. */

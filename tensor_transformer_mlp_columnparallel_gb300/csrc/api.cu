@@ -911,7 +911,7 @@ static tpmlp_status distill_args(tpmlp_dtype dt, int64_t N, int64_t V, int T, in
                                  const float* teacher_logits, float tau, DistillArgs& a) {
     TPMLP_TRY(check_rows(dt, N, V, T, logits, ld));
     if (K < 1 || K > TPMLP_MAX_TEACHER) return TPMLP_ERR_SHAPE;
-    if (!(tau > 0.f) || !(tau < 3.4e38f)) return TPMLP_ERR_ARG;
+    if (!(tau >= 0x1p-60f && tau <= 0x1p60f)) return TPMLP_ERR_ARG;   // log2(e) / tau and tau^2 are finite, not 0
     if (N > 0 && (teacher_ids == nullptr || teacher_logits == nullptr)) return TPMLP_ERR_ARG;
     TPMLP_TRY(check_align(4, {teacher_ids, teacher_logits}));
     a = DistillArgs{};
