@@ -116,8 +116,15 @@ constexpr int SORT_THREADS = 512;                            // of the sort over
 // CTAs of 1024 / 4096 / one CTA on GB300: table gradient 345 / 358 / 357 us.)
 constexpr int FEW_ROUNDS = 2;
 constexpr int64_t FEW_TOKENS = 65536;
-constexpr int ONE_THREADS = 1024;                            // of the sort in one CTA
-constexpr int ONE_MAX = ONE_THREADS * SORT_ROUNDS;           // its tokens at most
+// The sort in one CTA, for a batch that small: all passes in one launch instead
+// of two each. Up to 2048 tokens it was faster for every table (GB300, whole
+// call, one CTA / several: 256 tokens into 2000 x 512 fp32 13.0 / 18.0 us, from
+// a captured graph 11.7 / 13.0; 1024 into 9999 x 1030 23.4 / 26.4; 2048 into
+// 38549 x 1464 54.8 / 55.5). Ranking more tokens on one SM is not: 4099 into
+// 9999 x 1030 38.4 / 36.0, 8192 into 2000 x 512 32.1 / 23.9.
+constexpr int ONE_THREADS = 1024;
+constexpr int ONE_ROUNDS = 2;
+constexpr int ONE_MAX = ONE_THREADS * ONE_ROUNDS;            // its tokens at most
 constexpr int ONE_SMEM = (ONE_THREADS / 32) * BINS * 4 + ONE_MAX * 8;
 static_assert(SORT_THREADS == BINS, "one thread per digit");
 
@@ -199,12 +206,12 @@ __global__ void __launch_bounds__(ONE_THREADS) sort_one_kernel(const SortArgs p)
     int* cnt = reinterpret_cast<int*>(exchange + ONE_MAX);
     __shared__ int warp_sum[BINS / 32];
     const int warp = threadIdx.x >> 5;
-    const int base = warp * 32 * SORT_ROUNDS + (threadIdx.x & 31);
-    uint2 item[SORT_ROUNDS];
-    bool in[SORT_ROUNDS];
-    int rank[SORT_ROUNDS];
+    const int base = warp * 32 * ONE_ROUNDS + (threadIdx.x & 31);
+    uint2 item[ONE_ROUNDS];
+    bool in[ONE_ROUNDS];
+    int rank[ONE_ROUNDS];
 #pragma unroll
-    for (int r = 0; r < SORT_ROUNDS; ++r) {
+    for (int r = 0; r < ONE_ROUNDS; ++r) {
         in[r] = base + r * 32 < p.N;
         item[r] = in[r] ? first_pair(p, base + r * 32) : make_uint2(0u, 0u);
     }
@@ -227,15 +234,15 @@ __global__ void __launch_bounds__(ONE_THREADS) sort_one_kernel(const SortArgs p)
             for (int w = 0; w < ONE_THREADS / 32; ++w) cnt[w * BINS + threadIdx.x] += start;
         __syncthreads();
 #pragma unroll
-        for (int r = 0; r < SORT_ROUNDS; ++r)
+        for (int r = 0; r < ONE_ROUNDS; ++r)
             if (in[r]) exchange[cnt[warp * BINS + ((item[r].x >> shift) & (BINS - 1))] + rank[r]] = item[r];
         __syncthreads();
 #pragma unroll
-        for (int r = 0; r < SORT_ROUNDS; ++r)
+        for (int r = 0; r < ONE_ROUNDS; ++r)
             if (in[r]) item[r] = exchange[base + r * 32];
     }
 #pragma unroll
-    for (int r = 0; r < SORT_ROUNDS; ++r)
+    for (int r = 0; r < ONE_ROUNDS; ++r)
         if (in[r]) p.out[base + r * 32] = item[r];
 }
 
@@ -703,12 +710,7 @@ tpmlp_status run_vocab_embedding_backward(int f32, int grad_f32, int64_t N, int6
         p.bits = 1;
         while ((V >> p.bits) != 0) ++p.bits;   // keys 0..V
         p.err = err;
-        // One launch for all passes where there is little to do: what bounds a
-        // small table is issuing the launches (4099 fp32 tokens into 9999 x 1030:
-        // 36 us with one, 38 to 45 with four; 4235 into 38549 x 1464: 72 / 69).
-        const double work = (double)H * ((double)N * (f32 ? 4 : 2) +
-                                         (accumulate ? 0.0 : (double)V * (grad_f32 ? 4 : 2)));
-        if (N <= ONE_MAX / 4 || (N <= ONE_MAX && work < 64e6)) {
+        if (N <= ONE_MAX) {
             p.out = reinterpret_cast<uint2*>(ws + l.pairs[0]);
             if (cudaFuncSetAttribute(sort_one_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ONE_SMEM) !=
                 cudaSuccess)
