@@ -559,7 +559,12 @@ __device__ __forceinline__ void epilogue_swiglu_chunk(const EpiArgs& e, int g, i
     }
 }
 
-template <int BN, bool PAIR>
+// GATED: what only the gated backward asks for, two operand pairs in the K loop
+// (p.chain, p.rest_rows) and the EPI_DSWIGLU epilogue. An instance of its own:
+// their branches cost the other GEMMs 0.3 to 0.6% (GB300, in turn: the fwd+bwd
+// step of N = 8192, D = 8192, F = 28672, T = 8 in 12.86 against 12.79 ms, the
+// forward of N = 4096, D = 4096, F = 16384, T = 4 in 640 against 636 us).
+template <int BN, bool PAIR, bool GATED>
 __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_constant__ TcParams p) {
     using C = Cfg<BN, PAIR>;
     extern __shared__ uint8_t smem_raw[];
@@ -621,8 +626,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
         for (int g = 0; g < p.G; ++g) {
             prefetch_tmap(&p.tmA[g]);
             prefetch_tmap(&p.tmB[g]);
-            if (p.dual || p.chain) prefetch_tmap(&p.tmB2[g]);
-            if (p.chain) prefetch_tmap(&p.tmAux[g]);
+            if (p.dual || (GATED && p.chain)) prefetch_tmap(&p.tmB2[g]);
+            if (GATED && p.chain) prefetch_tmap(&p.tmAux[g]);
         }
     }
     if (warp == 1) {
@@ -647,7 +652,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
     if (warp != 0 || lane != 0) pdl_wait();
 
     const int kb_per_group = p.k_blocks;
-    const int pairs = p.chain ? 2 : 1;   // operand pairs a group's K loop walks
+    const int pairs = GATED && p.chain ? 2 : 1;   // operand pairs a group's K loop walks
     const int kb_total = (p.fold ? p.G * kb_per_group : kb_per_group) * pairs;
     // this CTA's k-blocks of each tile (all of them unless K is split)
     const int kb_lo = (int)((int64_t)kb_total * krank / ks);
@@ -667,8 +672,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
             // pair gk (the shard; with chain, shard gk / 2 and its first or
             // second pair) at K offset k0, completing on the stage's full barrier.
             auto issue = [&](int st, int gk, int k0, int am0, int bn0, int n0) {
-                const int gs = p.chain ? gk >> 1 : gk;
-                const bool second = p.chain && (gk & 1);
+                const bool chain = GATED && p.chain;
+                const int gs = chain ? gk >> 1 : gk;
+                const bool second = chain && (gk & 1);
                 const CUtensorMap* mapA = second ? &p.tmAux[gs] : &p.tmA[gs];
                 const CUtensorMap* mapB = second ? &p.tmB2[gs] : &p.tmB[gs];
                 const uint32_t fb = full0 + 8u * (uint32_t)st;
@@ -740,7 +746,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
                 const bool down = (p.alt & 1) && !w.sk && ((w.t / w.step) & 1);
                 const int kb_first = down ? w.kb1 - 1 : w.kb0;
                 // operand pair of the first k-block and its K offset inside the pair
-                const int q_first = kb_first / kb_per_group;
+                const int q_first = GATED || p.fold ? kb_first / kb_per_group : 0;
                 int gk = (p.fold ? 0 : g * pairs) + q_first;
                 int k0 = (kb_first - q_first * kb_per_group) * C::BK;
                 for (int kb = w.kb0; kb < w.kb1; ++kb) {
@@ -920,7 +926,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
         // out at the start of a chunk, once the stores of the chunk before
         // have read the other set, and the first chunk's before the tile's
         // accumulator is ready.
-        const bool gin = C::TMA_OUT && p.tma_out && p.epi.kind == EPI_DSWIGLU;
+        const bool gin = GATED && C::TMA_OUT && p.tma_out && p.epi.kind == EPI_DSWIGLU;
         auto gload = [&](uint32_t set, int g, int col0, int row0) {
             if (lane == 0) {
                 mbar_arrive_expect_tx(zbar(set), 4096u);
@@ -934,7 +940,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
         auto emit = [&](int g, int row, int row0, int col0, const uint32_t (&r)[32], int next_col0) {
             float v[32];
             epilogue_bias(p.epi, g, col0, p.N, r, v);
-            if (!PAIR && p.rest_rows > 0) {   // other rows are not stored
+            if (GATED && !PAIR && p.rest_rows > 0) {   // other rows are not stored
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] += __shfl_down_sync(0xffffffffu, v[j], p.rest_rows);
             }
@@ -1005,7 +1011,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
                 oset ^= 1u;
             } else {
                 if (z_out) store_z_thread(p.epi, g, row, col0, p.M, p.N, v);
-                if (p.epi.kind == EPI_DSWIGLU) epilogue_dswiglu_thread(p.epi, g, row, col0, p.M, p.N, v);
+                if (GATED && p.epi.kind == EPI_DSWIGLU)
+                    epilogue_dswiglu_thread(p.epi, g, row, col0, p.M, p.N, v);
                 epilogue_act(p.epi, g, row, col0, p.M, p.N, v);
                 store_c_thread(p.epi, g, row, col0, p.M, p.N, v);
             }
@@ -1327,8 +1334,9 @@ bool make_map_mn_chunks(CUtensorMap* m, const void* base, int64_t mn, int64_t k,
 // Operand pairs the K loop of one output walks
 int k_groups(const GemmProblem& pr) { return (pr.fold ? pr.G : 1) * (pr.chain ? 2 : 1); }
 
-// Co-resident CTAs (cl = 1) or clusters of cl CTAs of one kernel instance on
-// the current device; 0 when the queries fail. Cached per device and cl.
+// Co-resident CTAs (cl = 1) or clusters of cl CTAs of a kernel instance (gated
+// or not: shared memory decides, one CTA an SM) on the current device; 0 when
+// the queries fail. Cached per device and cl.
 template <int BN, bool PAIR>
 int resident_units(int cl) {
     using C = Cfg<BN, PAIR>;
@@ -1340,7 +1348,9 @@ int resident_units(int cl) {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || cl < 1 || cl > 8) return 0;
     if (units[dev][cl] > 0) return units[dev][cl];
     if (!attr_set[dev]) {
-        if (cudaFuncSetAttribute(tc_gemm_kernel<BN, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(tc_gemm_kernel<BN, PAIR, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 C::SMEM_BYTES) != cudaSuccess ||
+            cudaFuncSetAttribute(tc_gemm_kernel<BN, PAIR, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::SMEM_BYTES) != cudaSuccess)
             return 0;
         attr_set[dev] = true;
@@ -1359,7 +1369,7 @@ int resident_units(int cl) {
         cfg.dynamicSmemBytes = C::SMEM_BYTES;
         cfg.gridDim = dim3((unsigned)(cl * (n / cl)));
         n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, tc_gemm_kernel<BN, PAIR>, &cfg) != cudaSuccess) return 0;
+        if (cudaOccupancyMaxActiveClusters(&n, tc_gemm_kernel<BN, PAIR, false>, &cfg) != cudaSuccess) return 0;
     }
     units[dev][cl] = n > 0 ? n : 0;
     return units[dev][cl];
@@ -1596,7 +1606,10 @@ tpmlp_status launch(const GemmProblem& pr, cudaStream_t s, int ks = 1) {
         LaunchScope ls(pr.name, s);
         // the arrival counters start at zero (a memset node inside a graph)
         e = sk ? cudaMemsetAsync(pr.sk_cnt, 0, sk_cnt_bytes, s) : cudaSuccess;
-        if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, tc_gemm_kernel<BN, PAIR>, kp);
+        const bool gated = pr.chain || pr.epi.kind == EPI_DSWIGLU;
+        if (e == cudaSuccess)
+            e = gated ? cudaLaunchKernelEx(&cfg, tc_gemm_kernel<BN, PAIR, true>, kp)
+                      : cudaLaunchKernelEx(&cfg, tc_gemm_kernel<BN, PAIR, false>, kp);
     }
     if (e != cudaSuccess) return TPMLP_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
