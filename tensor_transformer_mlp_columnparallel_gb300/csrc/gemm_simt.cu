@@ -41,6 +41,7 @@ struct SimtParams {
     EpiArgs epi;
 };
 
+template <bool GATED>
 __device__ __forceinline__ void epi_scalar(const EpiArgs& e, int g, int m, int n, float v) {
     if (e.bias[g] != nullptr) v += static_cast<const float*>(e.bias[g])[n];
     if (e.kind == EPI_ACT) {
@@ -48,7 +49,7 @@ __device__ __forceinline__ void epi_scalar(const EpiArgs& e, int g, int m, int n
         v = act_fwd(e.act, v);
     } else if (e.kind == EPI_DACT) {
         v *= act_grad(e.act, static_cast<const float*>(e.aux[g])[(int64_t)m * e.ldaux + n]);
-    } else if (e.kind == EPI_DSWIGLU) {
+    } else if (GATED && e.kind == EPI_DSWIGLU) {
         const float gv = static_cast<const float*>(e.aux[g])[(int64_t)m * e.ldaux + n];
         const float uv = static_cast<const float*>(e.aux2[g])[(int64_t)m * e.ldaux + n];
         float dg, du;
@@ -72,7 +73,11 @@ __device__ __forceinline__ void epi_swiglu_scalar(const EpiArgs& e, int g, int m
     static_cast<float*>(e.C[g])[(int64_t)m * e.ldc + n] = silu_f(gv) * uv;
 }
 
-template <bool A_MN, bool B_MN, bool DUAL>
+// GATED: what only the gated backward asks for (p.chain, EPI_DSWIGLU), an
+// instance of its own: its branches cost the other GEMMs 3% (the exact-fp32
+// fwd+bwd step of N = 64, D = 256, F = 1024, T = 2 from a captured graph 76.6
+// against 74.0 us).
+template <bool A_MN, bool B_MN, bool DUAL, bool GATED = false>
 __global__ void __launch_bounds__(256) simt_gemm_kernel(const SimtParams p) {
     // A and B stages; after the K loop the first 16 KB hold this CTA's
     // partial tile for a K split
@@ -95,7 +100,7 @@ __global__ void __launch_bounds__(256) simt_gemm_kernel(const SimtParams p) {
     // The K loop (over (shard, k) when folded) walks chunks of TK; the global
     // loads of chunk c + 1 go to registers while chunk c is computed from
     // shared memory, so a CTA waits for memory once, not once per chunk.
-    const int pairs = p.chain ? 2 : 1;
+    const int pairs = GATED && p.chain ? 2 : 1;
     const int ngroups = (p.fold ? p.G : 1) * pairs;   // operand pairs of one output
     const int kchunks = (p.K + TK - 1) / TK;
     const int nchunks = ngroups * kchunks;
@@ -109,7 +114,7 @@ __global__ void __launch_bounds__(256) simt_gemm_kernel(const SimtParams p) {
         const int gi = c / kchunks;
         const int k0 = (c - gi * kchunks) * TK;
         const int g = p.fold ? gi / pairs : gz;
-        const bool second = p.chain && (gi & 1);
+        const bool second = GATED && p.chain && (gi & 1);
         const float* A = second ? p.A2[g] : p.A[g];
         const float* B = second ? p.B2[g] : p.B[g];
         const float* B2 = p.B2[g];
@@ -213,7 +218,7 @@ __global__ void __launch_bounds__(256) simt_gemm_kernel(const SimtParams p) {
                 if (DUAL)
                     epi_swiglu_scalar(p.epi, g_out, m, n, acc[i][j], acc2[i][j]);
                 else
-                    epi_scalar(p.epi, g_out, m, n, acc[i][j]);
+                    epi_scalar<GATED>(p.epi, g_out, m, n, acc[i][j]);
             }
         }
     }
@@ -270,10 +275,14 @@ tpmlp_status run_gemm_simt(const GemmProblem& pr, cudaStream_t s) {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
+    const bool gated = pr.chain || pr.epi.kind == EPI_DSWIGLU;
+    if (gated && (pr.dual || pr.a_mn || pr.b_mn)) return TPMLP_ERR_ARG;   // K-major operands
     cudaError_t e;
     {
         LaunchScope ls(pr.name, s);
-        if (pr.dual) {
+        if (gated) {
+            e = cudaLaunchKernelEx(&cfg, simt_gemm_kernel<false, false, false, true>, kp);
+        } else if (pr.dual) {
             if (pr.a_mn || !pr.b_mn || pr.fold) return TPMLP_ERR_ARG;   // the gated MLP's column GEMM only
             e = cudaLaunchKernelEx(&cfg, simt_gemm_kernel<false, true, true>, kp);
         } else if (pr.a_mn && pr.b_mn) {

@@ -62,7 +62,7 @@ struct GemmProblem {
     int dual;
     const void* B2[kMaxG];
     // chain = 1: the K loop of each group runs over two operand pairs, A B
-    // and then A2 B2 (all K-major in the bf16 GEMM), into one accumulator: the
+    // and then A2 B2 (all K-major), into one accumulator: the
     // gated MLP's dX. With fold the order is (g, pair, k). Not with dual.
     int chain;
     const void* A2[kMaxG];
