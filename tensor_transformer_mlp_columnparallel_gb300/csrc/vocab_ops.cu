@@ -21,7 +21,8 @@
 //   TB/s), 315 with 5 tokens, 359 with 20 (5.8 TB/s: the list's own work);
 //   2048 rows with 5: 96 us (5.5 TB/s: a start and a tail);
 //   distillation with its gradient, 4096 x 128000 bf16: 350 us (6.0 TB/s).
-// Few rows take 4 to 9 us, a launch and a cluster's two exchanges.
+// Few rows are a launch and a cluster's two exchanges: 5 us for one of 32000 fp32
+// logits, 13 for 48 of 128000 bf16 with 20 tokens (from a captured graph).
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -502,16 +503,14 @@ struct Peaks {
 
 // The K-th largest of the threads' NT (at least K) maxima is reached by K
 // different entries, so only entries at or above it can be in the list, and
-// they sit with the threads whose maximum reaches it: K of
-// NT unless maxima are equal. Of their vectors those of the chunk with the
-// maximum are read again, spread over all threads, and a thread's others only
-// if one of them reaches the bound too. (Reading all of a thread's vectors,
-// K / NT of the slice, from DRAM as a rule, took 45% of the kernel's time at
-// K = 20 and 8192 x 128000 bf16 logits, this way the list takes 18%; going
-// through the registers of the few threads, where the slice is one chunk,
-// took twice as long as reading it again.) The K-th largest maximum comes in
-// two steps: with g = ceil(K / warps), the least of the warps' g-th largest
-// maxima leaves a few dozen, and those are ranked by counting.
+// they sit with the threads whose maximum reaches it: K of NT unless maxima
+// are equal. Of their vectors those of the chunk with the maximum are read
+// again, from L2 as a rule and spread over all threads, and a thread's others
+// (K / NT of the slice in all, from DRAM as a rule) only if one of them reaches
+// the bound too: at 8192 x 128000 bf16 logits and K = 20 the list is 18% of the
+// kernel. The K-th largest maximum comes in two steps: with g = ceil(K /
+// warps), the least of the warps' g-th largest maxima leaves a few dozen, and
+// those are ranked by counting.
 // Where more than MAX_CAND entries reach the bound (a mask that leaves fewer
 // than K tokens, rows of equal values), the entries above it are taken alone
 // and equal ones follow by index; where even those are too many, K rounds
@@ -930,11 +929,11 @@ template <typename T, int NT> __device__ __noinline__ void far_row(const Distill
 //
 // With both, the row is read once and stays on the chip: the slice's last
 // chunk in registers, the one before it in shared memory (a thread's own
-// vectors, so no barrier), 64 KB a CTA and 256 KB an SM. A slice that is
-// longer reads its other chunks again, last one first. (4096 rows of 128000
-// bf16 logits on GB300: 350 us, and DRAM moves what the algorithm has to. Of
-// its first form, 384 us, two 512-thread CTAs an SM took 405 us, and a second
-// pass from L2 440, as half of it came from DRAM again.)
+// vectors, so no barrier), 64 KB a CTA and 256 KB an SM: 4096 rows of 128000
+// bf16 logits take 350 us on GB300, and DRAM moves what the algorithm has to.
+// A cluster holds 131072 fp32 or 262144 bf16 logits of a row that way; a longer
+// slice reads its other chunks again, last one first (fp32 rows of 131072: 5.4
+// TB/s read and written, of 132500: 4.2, of 151936: 4.4).
 template <typename T, int NT, bool LOSS, bool SUMS, bool GRAD>
 __device__ __forceinline__ void distill_row(const DistillArgs& a, int log_split, int* err) {
     constexpr bool STAGE = LOSS && GRAD;
@@ -1257,11 +1256,12 @@ tpmlp_status distill_launch(const DistillArgs& a, cudaStream_t s, int* err) {
 
 // Many rows take smaller CTAs, for more rows an SM: 64 threads where their two
 // chunks hold the row, else 128. The list's bound is the K-th largest of the
-// threads' maxima, so fewer threads leave more candidates: at most one
-// token of the list for two threads, in rows of more chunks one for six. (bf16 on GB300, 64 /
-// 128 / 256 threads: 4000 rows of 8 KB, K = 0 16 / 22 / 37 us, K = 20 29 / 36 /
-// 56; of 32 KB, K = 20 51 / 53 / 61; 8192 rows of 256 KB, K = 0 335 / 321 / 326,
-// K = 20 503 / 386 / 376, K = 64 35 ms / 654 / 467.)
+// threads' maxima, so fewer threads leave more candidates, in the end more than
+// there is room for: at most one token of the list for two threads, in rows of
+// more chunks one for six. (bf16 on GB300, 64 / 128 / 256 threads: 4000 rows of
+// 8 KB, K = 0 16 / 22 / 37 us, K = 20 29 / 36 / 56; of 32 KB, K = 20 51 / 53 / 61;
+// 8192 rows of 256 KB, K = 0 335 / 321 / 326, K = 20 503 / 386 / 376; K = 64 - /
+// 654 / 467.)
 template <typename T>
 tpmlp_status logprobs_launch(const LogprobArgs& a, int log_split, cudaStream_t s, int* err) {
     const int64_t vectors = a.V * (int64_t)sizeof(T) / 16;
