@@ -260,10 +260,10 @@ def _own_policy(s):
     opt = dict(ref_logprobs=s["ref"], kl_coef=c["kl"], clip_low=c["low"], clip_high=c["high"],
                temperature=c["tau"])
     if c["fused"]:
-        loss, mean, logprob, kl, _, d = tp.vocab_policy_with_grad(*args, **opt, grad_scale=1.0 / c["N"])
+        loss, mean, logprob, kl, d = tp.vocab_policy_with_grad(*args, **opt, grad_scale=1.0 / c["N"])
     else:
-        loss, mean, logprob, kl, lse = tp.vocab_policy(*args, **opt)
-        d = tp.vocab_policy_backward(*args, logprob, lse, **opt, grad_scale=1.0 / c["N"],
+        loss, mean, logprob, kl = tp.vocab_policy(*args, **opt)
+        d = tp.vocab_policy_backward(*args, logprob, **opt, grad_scale=1.0 / c["N"],
                                      grad_tokens=s["weights"])
     return {"loss": loss, "mean": mean, "logprob": logprob, "kl": kl, "dlogits": d}
 
