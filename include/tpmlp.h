@@ -79,6 +79,7 @@ typedef enum {
  * that the pages' code uses (nn.GELU(), F.gelu). GELU_SIGMOID: the interview page's
  * approximation z / (1 + exp(-1.702 z)). act' is the exact derivative of each. */
 typedef enum {
+    TPMLP_ACT_NONE = -1,      /* the split linear layers only: act(z) = z */
     TPMLP_ACT_RELU = 0,
     TPMLP_ACT_GELU_TANH = 1,
     TPMLP_ACT_GELU_ERF = 2,
@@ -99,11 +100,17 @@ typedef enum { TPMLP_F32 = 0, TPMLP_BF16 = 1 } tpmlp_dtype;
  *   see tpmlp_gemm_plan.) */
 typedef enum { TPMLP_REDUCE_PARTIALS = 0, TPMLP_REDUCE_SPLITK = 1 } tpmlp_reduce_mode;
 
-/* SWIGLU_BACKWARD: tpmlp_swiglu_backward (tpmlp_swiglu_forward sizes as FORWARD). */
+/* SWIGLU_BACKWARD: tpmlp_swiglu_backward (tpmlp_swiglu_forward sizes as FORWARD).
+ * LINEAR: tpmlp_column_linear and tpmlp_row_linear. LINEAR_BACKWARD: their
+ * gradients without an activation; LINEAR_BACKWARD_ACT: with one (the reduce
+ * mode is of no consequence for these three). */
 typedef enum {
     TPMLP_OP_FORWARD = 0,
     TPMLP_OP_BACKWARD = 1,
-    TPMLP_OP_SWIGLU_BACKWARD = 2
+    TPMLP_OP_SWIGLU_BACKWARD = 2,
+    TPMLP_OP_LINEAR = 3,
+    TPMLP_OP_LINEAR_BACKWARD = 4,
+    TPMLP_OP_LINEAR_BACKWARD_ACT = 5
 } tpmlp_op;
 
 /* Forward of one block (§01-§05).
@@ -217,6 +224,113 @@ tpmlp_status tpmlp_forward_reduce_scatter(tpmlp_dtype dt, int64_t N, int64_t D, 
                                           const void* b2, void* const* Y_rows, void* const* H,
                                           void* const* Z, tpmlp_reduce_mode mode, void* workspace,
                                           size_t workspace_bytes, void* stream);
+
+/* ---- split linear layers and layer norm -----------------------------------
+ * The block's two halves as layers of their own (a projection, a vocabulary
+ * head, a block end on the residual path), with row pitches: a matrix here is
+ * [rows, cols] of dt in rows of ld elements, ld >= cols. On the bf16 path every
+ * pointer is 16-byte aligned and every pitch a multiple of 8; fp32 matrices
+ * need aligned elements only. */
+
+/* Column split (page 1 §02): W's columns in T shards of F/T,
+ *   Z[:, shard r] = X W[r] + b[r],   Y = act(Z) + R
+ * in one product with the bias, the activation and the residual in its
+ * epilogue (fp32, one rounding to dt).
+ *   X  [N, D], pitch ldx       W  T x [D, F/T]      b  T x [F/T] or NULL
+ *   R  [N, F], pitch ldr, or NULL (ldr unused); may be Y itself (ldr = ldy)
+ *   Y  [N, F], pitch ldy       Z  [N, F], pitch ldz, out, or NULL: what the
+ *                                 backward takes; needs an activation
+ *   workspace  optional scratch of the bf16 path, TPMLP_OP_LINEAR's size of
+ *              tpmlp_workspace_bytes_balanced (0 and NULL: none)
+ * Errors: those of tpmlp_forward; TPMLP_ERR_SHAPE for a pitch below its columns
+ * or above 2^38; TPMLP_ERR_ALIGN. N = 0 launches nothing. */
+tpmlp_status tpmlp_column_linear(tpmlp_dtype dt, int64_t N, int64_t D, int64_t F, int T, tpmlp_act act,
+                                 const void* X, int64_t ldx, const void* const* W,
+                                 const void* const* b, const void* R, int64_t ldr, void* Y,
+                                 int64_t ldy, void* Z, int64_t ldz, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* Row split (§03, §04): W's rows, and X's columns, in T shards of F/T,
+ *   Y = sum_r X[:, shard r] W[r] + b + R
+ * with the shard sum inside the product, b and R added once.
+ *   X  [N, F], pitch ldx (a column-split layer's Y as it is)
+ *   W  T x [F/T, D]      b  [D] or NULL
+ *   R  [N, D], pitch ldr, or NULL; may be Y itself (ldr = ldy)
+ *   Y  [N, D], pitch ldy
+ * Workspace and errors as tpmlp_column_linear. */
+tpmlp_status tpmlp_row_linear(tpmlp_dtype dt, int64_t N, int64_t D, int64_t F, int T, const void* X,
+                              int64_t ldx, const void* const* W, const void* b, const void* R,
+                              int64_t ldr, void* Y, int64_t ldy, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* Gradients of the column-split layer (the residual's is dY itself):
+ *   dZ = dY act'(Z),  dX = sum_r dZ_r W[r]^T,  dW[r] = X^T dZ_r,  db[r] = sum_n dZ_r
+ *   Z   [N, F], pitch ldz, as the forward wrote it; unused for TPMLP_ACT_NONE
+ *   dY  [N, F], pitch lddy     dX  [N, D], pitch lddx
+ *   dW  T x [D, F/T]           db  T x [F/T], or NULL
+ *   workspace  TPMLP_OP_LINEAR_BACKWARD_ACT's size (with an activation: dZ is
+ *              kept there), else TPMLP_OP_LINEAR_BACKWARD's, balanced or not
+ * bf16: with an activation, dZ is rounded to bf16 before the products; with at
+ * most 64 tokens dW, with at most 16 dX too, also take what the rounding left
+ * over. N = 0 writes zeros to dW and db. Errors as above; TPMLP_ERR_WORKSPACE. */
+tpmlp_status tpmlp_column_linear_backward(tpmlp_dtype dt, int64_t N, int64_t D, int64_t F, int T,
+                                          tpmlp_act act, const void* X, int64_t ldx,
+                                          const void* const* W, const void* Z, int64_t ldz,
+                                          const void* dY, int64_t lddy, void* dX, int64_t lddx,
+                                          void* const* dW, void* const* db, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+
+/* Gradients of the row-split layer:
+ *   dX[:, shard r] = dY W[r]^T,  dW[r] = X[:, shard r]^T dY,  db = sum_n dY
+ *   X, dX  [N, F], pitches ldx, lddx   dY  [N, D], pitch lddy
+ *   dW  T x [F/T, D]                   db  [D], or NULL
+ * Workspace of TPMLP_OP_LINEAR_BACKWARD. Errors as above. */
+tpmlp_status tpmlp_row_linear_backward(tpmlp_dtype dt, int64_t N, int64_t D, int64_t F, int T,
+                                       const void* X, int64_t ldx, const void* const* W,
+                                       const void* dY, int64_t lddy, void* dX, int64_t lddx,
+                                       void* const* dW, void* db, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/* Layer norm of the rows of x:
+ *   mean = (1/D) sum x,  var = (1/D) sum (x - mean)^2,  rstd = 1 / sqrt(var + eps)
+ *   y = (x - mean) rstd weight + bias
+ * in fp32 (the variance around the row's mean, never a difference of squares),
+ * rounded once to dt.
+ *   x       [N, D] of dt, pitch ldx;  y  [N, D] of dt, pitch ldy; may be x
+ *           itself (ldy = ldx)
+ *   weight  [D] of param_dt, or NULL (ones);  bias  [D] of param_dt, or NULL (zeros)
+ *   eps     finite, not negative; with 0 a row of equal elements gives NaN
+ *   mean, rstd  [N] fp32 out, or NULL: what the backward takes
+ * param_dt is dt or fp32. Any alignment of the elements; 16-byte rows are
+ * faster. A row with a NaN or an infinity gives NaN in that row alone; finite
+ * rows whose squares overflow fp32 are normalised as any other (up to 1e38).
+ * Errors: TPMLP_ERR_DTYPE, TPMLP_ERR_SHAPE (D < 1, a pitch below D),
+ * TPMLP_ERR_ARG, TPMLP_ERR_ALIGN. N = 0 launches nothing. */
+tpmlp_status tpmlp_layernorm(tpmlp_dtype dt, tpmlp_dtype param_dt, int64_t N, int64_t D, const void* x,
+                             int64_t ldx, const void* weight, const void* bias, float eps, void* y,
+                             int64_t ldy, float* mean, float* rstd, void* stream);
+
+/* Gradients of tpmlp_layernorm from x and the forward's mean and rstd:
+ *   h = (x - mean) rstd,  u = dy weight
+ *   dx = rstd (u - mean(u) - h mean(u h)) + dresidual
+ *   dweight = sum_n dy h,  dbias = sum_n dy
+ * in fp32, each output rounded once; the sums over tokens in an order that
+ * depends on the sizes alone, without atomics.
+ *   dy, x, dx  [N, D] of dt with their pitches;  weight  [D] of param_dt, or NULL
+ *   dresidual  [N, D] of dt, pitch lddres, or NULL: the gradient that comes down
+ *              the residual path beside the norm
+ *   dx         may be dy, x or dresidual itself (the same pitch)
+ *   dweight, dbias  [D] of param_dt out; both or neither
+ *   workspace  tpmlp_layernorm_backward_workspace_bytes(N, D), 16-byte aligned
+ * N = 0 writes zeros to dweight and dbias. Errors as above; TPMLP_ERR_WORKSPACE. */
+tpmlp_status tpmlp_layernorm_backward(tpmlp_dtype dt, tpmlp_dtype param_dt, int64_t N, int64_t D,
+                                      const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                      const void* weight, const float* mean, const float* rstd,
+                                      const void* dresidual, int64_t lddres, void* dx, int64_t lddx,
+                                      void* dweight, void* dbias, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+/* Workspace bytes of the call above; (size_t)-1 for invalid sizes. */
+size_t tpmlp_layernorm_backward_workspace_bytes(int64_t N, int64_t D);
 
 /* Vocab-parallel embedding lookup (textbook page §4.2.3 row-parallel
  * embedding; course notes §3.4 "TP for Embedding"): the table [V, Hd] is split
@@ -356,6 +470,71 @@ tpmlp_status tpmlp_vocab_distill_with_grad(tpmlp_dtype dt, int64_t N, int64_t V,
                                            float tau, float* loss_per_token, float* loss_mean,
                                            float* lse, const float* grad_tokens, float grad_scale,
                                            void* dlogits, int64_t ldd, void* stream);
+
+/* Clipped policy loss of the tokens a policy chose, with a KL term that keeps it
+ * near a reference (Schulman et al. 2017; the KL estimate is Schulman's k3), at
+ * temperature tau:
+ *   l_n    = z[n, t_n] / tau - ln sum_v exp(z[n, v] / tau)
+ *   rho    = exp(l - old_logprobs),  r = ref_logprobs - l,  k = exp(r) - r - 1
+ *   loss_n = -min(rho A, clip(rho, 1 - clip_low, 1 + clip_high) A) + kl_coef k
+ * old_logprobs and ref_logprobs are what tpmlp_vocab_logprobs returns of the
+ * older policy and of the reference (of the same tempered logits, if tau is not
+ * 1). A negative target is a position without a token (a prompt's, padding):
+ * loss, logprob, kl and gradient 0, and its logits are not read. The difference
+ * of log probabilities and 1 - p of the token are taken to more digits than an
+ * fp32 log probability holds.
+ *   logits        [N, V] of dt, row pitch ld
+ *   targets       [N] int64, below V
+ *   old_logprobs, advantages   [N] fp32
+ *   ref_logprobs  [N] fp32, or NULL with kl_coef = 0
+ *   kl_coef >= 0 and finite; 0 <= clip_low <= 1; clip_high >= 0 (infinite: no
+ *   upper border); tau in [2^-60, 2^60]
+ *   loss_per_token  [N] fp32 out
+ *   loss_mean       [1] fp32 out, or NULL: (1/N) sum_n loss_n (fixed order)
+ *   logprob         [N] fp32 out, or NULL: l, the backward's input
+ *   kl              [N] fp32 out, or NULL (it needs ref_logprobs): k
+ * A token that is masked (-inf) has l = -inf: rho 0; with a KL term its loss is
+ * +inf and its gradient not finite. An advantage of 0 takes no part of the
+ * ratio, whatever that is. Errors: TPMLP_ERR_ARG for parameters outside these
+ * ranges; TPMLP_ERR_SHAPE if V % T != 0, ld < V; TPMLP_ERR_ALIGN if a pointer is
+ * not aligned to its element. A target of V or more writes NaN for that row and
+ * sets TPMLP_ERR_ARG in the device error word. */
+tpmlp_status tpmlp_vocab_policy(tpmlp_dtype dt, int64_t N, int64_t V, int T, const void* logits, int64_t ld,
+                                const int64_t* targets, const float* old_logprobs,
+                                const float* advantages, const float* ref_logprobs, float kl_coef,
+                                float clip_low, float clip_high, float tau, float* loss_per_token,
+                                float* loss_mean, float* logprob, float* kl, void* stream);
+
+/* Gradient of grad_scale * sum_n grad_tokens[n] * loss[n] with respect to the
+ * logits, from the forward's logprob (the same other arguments):
+ *   dlogits[n, v] = w_n (1(v = t_n) - p_v),  w_n = grad_scale grad_tokens[n] s_n / tau
+ *   s_n = dloss/dl = -A rho, or 0 beyond the border on A's side, + kl_coef (1 - exp(r))
+ * computed in fp32 and rounded once to dt; a ratio on its border counts as
+ * inside. Rows with w = 0 (clipped tokens, positions without one) are not read.
+ *   logprob      [N] fp32 as written by tpmlp_vocab_policy. p is taken from it
+ *                where its rounding is 2^-20 of p at most (fp32 logits, |l| up to
+ *                32; bf16: 2^-16, up to 512); a row beyond is read twice
+ *   grad_tokens  [N] fp32, or NULL: all ones
+ *   dlogits      [N, V] of dt out, row pitch ldd >= V; may be the logits buffer
+ *                itself (in place, ldd = ld)
+ * Errors as tpmlp_vocab_policy. */
+tpmlp_status tpmlp_vocab_policy_backward(tpmlp_dtype dt, int64_t N, int64_t V, int T, const void* logits,
+                                         int64_t ld, const int64_t* targets, const float* old_logprobs,
+                                         const float* advantages, const float* ref_logprobs,
+                                         float kl_coef, float clip_low, float clip_high, float tau,
+                                         const float* logprob, const float* grad_tokens,
+                                         float grad_scale, void* dlogits, int64_t ldd, void* stream);
+
+/* Both of the above in one launch: the logits come from memory once. Outputs are
+ * those of the two calls, up to the order of fp32 sums and the rounding of
+ * logprob (which may be NULL; dlogits may be the logits buffer). */
+tpmlp_status tpmlp_vocab_policy_with_grad(tpmlp_dtype dt, int64_t N, int64_t V, int T, const void* logits,
+                                          int64_t ld, const int64_t* targets, const float* old_logprobs,
+                                          const float* advantages, const float* ref_logprobs,
+                                          float kl_coef, float clip_low, float clip_high, float tau,
+                                          float* loss_per_token, float* loss_mean, float* logprob,
+                                          float* kl, const float* grad_tokens, float grad_scale,
+                                          void* dlogits, int64_t ldd, void* stream);
 
 /* tpmlp_vocab_embedding times a factor: out[n] = scale * table[ids[n]],
  * multiplied in fp32 and rounded once to dt. Arguments, shards and errors as

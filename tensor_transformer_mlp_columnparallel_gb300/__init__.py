@@ -18,11 +18,18 @@ from ._binding import (  # noqa: F401
     tpmlp_block_reduce,
     tpmlp_block_reduce_scatter,
     tpmlp_check_device_error,
+    tpmlp_column_linear,
+    tpmlp_column_linear_backward,
     tpmlp_forward,
     tpmlp_forward_noalloc,
     tpmlp_forward_reduce_scatter,
     tpmlp_gemm_plan,
     tpmlp_launch_count,
+    tpmlp_layernorm,
+    tpmlp_layernorm_backward,
+    tpmlp_layernorm_backward_workspace_bytes,
+    tpmlp_row_linear,
+    tpmlp_row_linear_backward,
     tpmlp_selftest_gemm_stall,
     tpmlp_selftest_wait_timeout,
     tpmlp_selftest_weight_grad_stall,
@@ -42,6 +49,9 @@ from ._binding import (  # noqa: F401
     tpmlp_vocab_embedding_backward_workspace_bytes,
     tpmlp_vocab_embedding_scaled,
     tpmlp_vocab_logprobs,
+    tpmlp_vocab_policy,
+    tpmlp_vocab_policy_backward,
+    tpmlp_vocab_policy_with_grad,
     tpmlp_workspace_bytes,
     tpmlp_workspace_bytes_balanced,
 )
@@ -246,6 +256,149 @@ def vocab_distill_with_grad(logits: torch.Tensor, teacher_ids: torch.Tensor,
     tpmlp_vocab_distill_with_grad(logits, teacher_ids, teacher_logits, T, temperature, loss, mean,
                                   lse, grad_tokens, grad_scale, d)
     return loss, mean, lse, d
+
+
+def vocab_policy(logits: torch.Tensor, targets: torch.Tensor, old_logprobs: torch.Tensor,
+                 advantages: torch.Tensor, T: int, ref_logprobs: Optional[torch.Tensor] = None,
+                 kl_coef: float = 0.0, clip_low: float = 0.2, clip_high: float = 0.2,
+                 temperature: float = 1.0):
+    """Clipped policy loss of `targets` (int64, negative: no token) with a KL term
+    towards ref_logprobs. Returns (loss_per_token [N], loss_mean [1],
+    logprob [N], kl [N] or None)."""
+    N = logits.shape[0]
+    loss, logprob = (torch.empty((N,), dtype=torch.float32, device=logits.device) for _ in range(2))
+    mean = torch.empty((1,), dtype=torch.float32, device=logits.device)
+    kl = torch.empty_like(loss) if ref_logprobs is not None else None
+    tpmlp_vocab_policy(logits, targets, old_logprobs, advantages, ref_logprobs, T, kl_coef, clip_low,
+                       clip_high, temperature, loss, mean, logprob, kl)
+    return loss, mean, logprob, kl
+
+
+def vocab_policy_backward(logits: torch.Tensor, targets: torch.Tensor, old_logprobs: torch.Tensor,
+                          advantages: torch.Tensor, T: int, logprob: torch.Tensor,
+                          ref_logprobs: Optional[torch.Tensor] = None, kl_coef: float = 0.0,
+                          clip_low: float = 0.2, clip_high: float = 0.2, temperature: float = 1.0,
+                          grad_scale: float = 1.0, grad_tokens: Optional[torch.Tensor] = None,
+                          in_place: bool = False):
+    """Gradient of grad_scale * sum_n grad_tokens[n] * loss[n] with respect to
+    the logits, from vocab_policy's logprob."""
+    d = _dlogits_like(logits, in_place)
+    tpmlp_vocab_policy_backward(logits, targets, old_logprobs, advantages, ref_logprobs, T, kl_coef,
+                                clip_low, clip_high, temperature, logprob, grad_tokens, grad_scale, d)
+    return d
+
+
+def vocab_policy_with_grad(logits: torch.Tensor, targets: torch.Tensor, old_logprobs: torch.Tensor,
+                           advantages: torch.Tensor, T: int,
+                           ref_logprobs: Optional[torch.Tensor] = None, kl_coef: float = 0.0,
+                           clip_low: float = 0.2, clip_high: float = 0.2, temperature: float = 1.0,
+                           grad_scale: float = 1.0, grad_tokens: Optional[torch.Tensor] = None,
+                           in_place: bool = False):
+    """vocab_policy and vocab_policy_backward in one launch. Returns
+    (loss_per_token, loss_mean, logprob, kl, dlogits)."""
+    N = logits.shape[0]
+    loss, logprob = (torch.empty((N,), dtype=torch.float32, device=logits.device) for _ in range(2))
+    mean = torch.empty((1,), dtype=torch.float32, device=logits.device)
+    kl = torch.empty_like(loss) if ref_logprobs is not None else None
+    d = _dlogits_like(logits, in_place)
+    tpmlp_vocab_policy_with_grad(logits, targets, old_logprobs, advantages, ref_logprobs, T, kl_coef,
+                                 clip_low, clip_high, temperature, loss, mean, logprob, kl, grad_tokens,
+                                 grad_scale, d)
+    return loss, mean, logprob, kl, d
+
+
+def layernorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+              bias: Optional[torch.Tensor] = None, eps: float = 1e-5):
+    """Layer norm of the rows of x [N, D] (any row pitch; weight and bias of x's
+    type or fp32). Returns (y [N, D], mean [N], rstd [N])."""
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    mean, rstd = (torch.empty((x.shape[0],), dtype=torch.float32, device=x.device) for _ in range(2))
+    tpmlp_layernorm(x, weight, bias, eps, y, mean, rstd)
+    return y, mean, rstd
+
+
+def layernorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor],
+                       mean: torch.Tensor, rstd: torch.Tensor,
+                       dresidual: Optional[torch.Tensor] = None, param_grads: bool = True,
+                       workspace: Optional[torch.Tensor] = None):
+    """Gradients of layernorm from its mean and rstd; dresidual is added to dx.
+    Returns (dx [N, D], dweight [D], dbias [D]), the parameters' in weight's
+    type (x's without a weight), None without param_grads."""
+    N, D = x.shape
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dweight = dbias = None
+    if param_grads:
+        dt = x.dtype if weight is None else weight.dtype
+        dweight, dbias = (torch.empty((D,), dtype=dt, device=x.device) for _ in range(2))
+    if workspace is None:
+        workspace = _workspace(tpmlp_layernorm_backward_workspace_bytes(N, D), x.device)
+    tpmlp_layernorm_backward(dy, x, weight, mean, rstd, dresidual, dx, dweight, dbias, workspace)
+    return dx, dweight, dbias
+
+
+def _linear_workspace(op: int, X: torch.Tensor, D: int, F: int, T: int) -> Optional[torch.Tensor]:
+    return _workspace(tpmlp_workspace_bytes_balanced(op, X.dtype, X.shape[0], D, F, T, "splitk"), X.device)
+
+
+def column_linear(X: torch.Tensor, W: Sequence[torch.Tensor], b: Optional[Sequence[torch.Tensor]] = None,
+                  act: Optional[str] = None, residual: Optional[torch.Tensor] = None,
+                  save_z: bool = False, workspace: Optional[torch.Tensor] = None):
+    """Y = act(X W + b) + residual, W = T tensors [D, F/T] (b: T tensors [F/T]).
+    X and residual may have any row pitch. Returns (Y [N, F], Z [N, F] or None);
+    Z is what the backward of an activation takes."""
+    T = len(W)
+    (N, D), Fs = X.shape, W[0].shape[1]
+    Y = torch.empty((N, T * Fs), dtype=X.dtype, device=X.device)
+    Z = torch.empty_like(Y) if save_z else None
+    if workspace is None:
+        workspace = _linear_workspace(_binding.OP_LINEAR, X, D, T * Fs, T)
+    tpmlp_column_linear(X, W, b, act, residual, Y, Z, workspace)
+    return Y, Z
+
+
+def row_linear(X: torch.Tensor, W: Sequence[torch.Tensor], b: Optional[torch.Tensor] = None,
+               residual: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Y [N, D] = sum_r X[:, shard r] W[r] + b + residual, W = T tensors [F/T, D]
+    (the block end; X [N, F] and residual may have any row pitch)."""
+    T, (Fs, D) = len(W), W[0].shape
+    Y = torch.empty((X.shape[0], D), dtype=X.dtype, device=X.device)
+    if workspace is None:
+        workspace = _linear_workspace(_binding.OP_LINEAR, X, D, T * Fs, T)
+    tpmlp_row_linear(X, W, b, residual, Y, workspace)
+    return Y
+
+
+def column_linear_backward(X: torch.Tensor, W: Sequence[torch.Tensor], dY: torch.Tensor,
+                           Z: Optional[torch.Tensor] = None, act: Optional[str] = None,
+                           bias_grads: bool = False, workspace: Optional[torch.Tensor] = None):
+    """Gradients of column_linear (the residual's is dY): (dX [N, D], dW list,
+    db list or None). With an activation, Z is the forward's."""
+    T = len(W)
+    (N, D), Fs = X.shape, W[0].shape[1]
+    dev, dt = X.device, X.dtype
+    dX = torch.empty((N, D), dtype=dt, device=dev)
+    dW = [torch.empty((D, Fs), dtype=dt, device=dev) for _ in range(T)]
+    db = [torch.empty((Fs,), dtype=dt, device=dev) for _ in range(T)] if bias_grads else None
+    if workspace is None:
+        op = _binding.OP_LINEAR_BACKWARD if act is None else _binding.OP_LINEAR_BACKWARD_ACT
+        workspace = _linear_workspace(op, X, D, T * Fs, T)
+    tpmlp_column_linear_backward(X, W, Z, dY, act, dX, dW, db, workspace)
+    return dX, dW, db
+
+
+def row_linear_backward(X: torch.Tensor, W: Sequence[torch.Tensor], dY: torch.Tensor,
+                        bias_grads: bool = False, workspace: Optional[torch.Tensor] = None):
+    """Gradients of row_linear (the residual's is dY): (dX [N, F], dW list,
+    db [D] or None)."""
+    T, (Fs, D) = len(W), W[0].shape
+    dev, dt = X.device, X.dtype
+    dX = torch.empty((X.shape[0], T * Fs), dtype=dt, device=dev)
+    dW = [torch.empty((Fs, D), dtype=dt, device=dev) for _ in range(T)]
+    db = torch.empty((D,), dtype=dt, device=dev) if bias_grads else None
+    if workspace is None:
+        workspace = _linear_workspace(_binding.OP_LINEAR_BACKWARD, X, D, T * Fs, T)
+    tpmlp_row_linear_backward(X, W, dY, dX, dW, db, workspace)
+    return dX, dW, db
 
 
 def vocab_embedding_scaled(ids: torch.Tensor, table: Sequence[torch.Tensor], scale: float):

@@ -24,6 +24,8 @@ ACT = {"relu": 0, "gelu_tanh": 1, "gelu_erf": 2, "gelu_sigmoid": 3}
 DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 MODE = {"partials": 0, "splitk": 1}
 OP_FORWARD, OP_BACKWARD, OP_SWIGLU_BACKWARD = 0, 1, 2
+OP_LINEAR, OP_LINEAR_BACKWARD, OP_LINEAR_BACKWARD_ACT = 3, 4, 5
+LINEAR_ACT = {None: -1, **ACT}
 MAX_TOP, MAX_TEACHER = 128, 1024
 
 
@@ -69,6 +71,27 @@ _SIGNATURES = {
     "tpmlp_vocab_embedding_backward": (_int, [_int, _int, _i64, _i64, _i64, _int, _vp, _vp, _f32,
                                               _int, _PP, _vp, ctypes.c_size_t, _vp]),
     "tpmlp_vocab_embedding_backward_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "tpmlp_vocab_policy": (_int, [_int, _i64, _i64, _int, _vp, _i64, _vp, _vp, _vp, _vp, _f32, _f32,
+                                  _f32, _f32, _vp, _vp, _vp, _vp, _vp]),
+    "tpmlp_vocab_policy_backward": (_int, [_int, _i64, _i64, _int, _vp, _i64, _vp, _vp, _vp, _vp,
+                                           _f32, _f32, _f32, _f32, _vp, _vp, _f32, _vp, _i64, _vp]),
+    "tpmlp_vocab_policy_with_grad": (_int, [_int, _i64, _i64, _int, _vp, _i64, _vp, _vp, _vp, _vp,
+                                            _f32, _f32, _f32, _f32, _vp, _vp, _vp, _vp, _vp, _f32,
+                                            _vp, _i64, _vp]),
+    "tpmlp_layernorm": (_int, [_int, _int, _i64, _i64, _vp, _i64, _vp, _vp, _f32, _vp, _i64, _vp, _vp,
+                               _vp]),
+    "tpmlp_layernorm_backward": (_int, [_int, _int, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                                        _vp, _i64, _vp, _i64, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "tpmlp_layernorm_backward_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),
+    "tpmlp_column_linear": (_int, [_int, _i64, _i64, _i64, _int, _int, _vp, _i64, _PP, _PP, _vp, _i64,
+                                   _vp, _i64, _vp, _i64, _vp, ctypes.c_size_t, _vp]),
+    "tpmlp_row_linear": (_int, [_int, _i64, _i64, _i64, _int, _vp, _i64, _PP, _vp, _vp, _i64, _vp, _i64,
+                                _vp, ctypes.c_size_t, _vp]),
+    "tpmlp_column_linear_backward": (_int, [_int, _i64, _i64, _i64, _int, _int, _vp, _i64, _PP, _vp,
+                                            _i64, _vp, _i64, _vp, _i64, _PP, _PP, _vp,
+                                            ctypes.c_size_t, _vp]),
+    "tpmlp_row_linear_backward": (_int, [_int, _i64, _i64, _i64, _int, _vp, _i64, _PP, _vp, _i64, _vp,
+                                         _i64, _PP, _vp, _vp, ctypes.c_size_t, _vp]),
     "tpmlp_block_reduce": (_int, [_int, _i64, _i64, _int, _PP, _vp, _vp, _vp]),
     "tpmlp_block_reduce_scatter": (_int, [_int, _i64, _i64, _int, _PP, _vp, _PP, _vp]),
     "tpmlp_forward_reduce_scatter": (_int, [_int, _i64, _i64, _i64, _int, _int, _vp, _PP, _PP, _PP,
@@ -200,6 +223,34 @@ def _require_rows(t, what: str) -> int:
     if t.stride(0) < V:
         raise ValueError(f"the rows of {what} must not overlap")
     return t.stride(0)
+
+
+def _run(t: torch.Tensor, fn, *args):
+    """A call on t's device, which need not be the current one."""
+    device = t.get_device()
+    if device == torch._C._cuda_getDevice():
+        _check(fn(*args))
+        return
+    with torch.cuda.device(device):
+        _check(fn(*args))
+
+
+def _require_matrix(t, shape, device, dtype, what: str) -> int:
+    """Row pitch of a matrix of this shape whose rows are contiguous; 0 for None."""
+    if t is None:
+        return 0
+    if t.get_device() != device.index:
+        raise ValueError("all tensors must live on the same CUDA device")
+    if t.dtype is not dtype:
+        raise TypeError(f"expected {dtype} for {what}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"expected {what} of {tuple(shape)}, got {tuple(t.shape)}")
+    return _require_rows(t, what)
+
+
+def _bytes(workspace, device) -> int:
+    _require([workspace], device, None)
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
 def _require_len(t, n: int, what: str):
@@ -487,6 +538,174 @@ def tpmlp_vocab_embedding_backward(ids, dout, scale: float, accumulate: bool,
                                                 float(scale), 1 if accumulate else 0,
                                                 shards, _ptr(workspace), ws_bytes,
                                                 _stream(dout)))
+
+
+def _require_tokens(logits, targets, old_logprobs, advantages, ref_logprobs):
+    N = logits.shape[0]
+    _require([targets], logits.device, torch.int64)
+    _require([old_logprobs, advantages, ref_logprobs], logits.device, torch.float32)
+    for t in (targets, old_logprobs, advantages, ref_logprobs):
+        _require_len(t, N, "a per-token tensor")
+
+
+def tpmlp_vocab_policy(logits, targets, old_logprobs, advantages, ref_logprobs, T: int,
+                       kl_coef: float, clip_low: float, clip_high: float, tau: float,
+                       loss_per_token, loss_mean=None, logprob=None, kl=None):
+    """Clipped policy loss of the given tokens with a KL term (see include/tpmlp.h)."""
+    ld = _require_rows(logits, "logits")
+    N, V = logits.shape
+    _require_tokens(logits, targets, old_logprobs, advantages, ref_logprobs)
+    _require([loss_per_token, loss_mean, logprob, kl], logits.device, torch.float32)
+    for t in (loss_per_token, logprob, kl):
+        _require_len(t, N, "a per-token tensor")
+    _run(logits, lib().tpmlp_vocab_policy, _dtype_code(logits), N, V, T, _ptr(logits), ld, _ptr(targets),
+         _ptr(old_logprobs), _ptr(advantages), _ptr(ref_logprobs), float(kl_coef), float(clip_low),
+         float(clip_high), float(tau), _ptr(loss_per_token), _ptr(loss_mean), _ptr(logprob), _ptr(kl),
+         _stream(logits))
+
+
+def tpmlp_vocab_policy_backward(logits, targets, old_logprobs, advantages, ref_logprobs, T: int,
+                                kl_coef: float, clip_low: float, clip_high: float, tau: float, logprob,
+                                grad_tokens, grad_scale: float, dlogits):
+    """Gradient of the policy loss from the forward's logprob; dlogits may be
+    logits itself (in place)."""
+    ld = _require_rows(logits, "logits")
+    N, V = logits.shape
+    _require_tokens(logits, targets, old_logprobs, advantages, ref_logprobs)
+    ldd = _require_dlogits(logits, dlogits)
+    _require([logprob, grad_tokens], logits.device, torch.float32)
+    for t in (logprob, grad_tokens):
+        _require_len(t, N, "a per-token tensor")
+    _run(logits, lib().tpmlp_vocab_policy_backward, _dtype_code(logits), N, V, T, _ptr(logits), ld,
+         _ptr(targets), _ptr(old_logprobs), _ptr(advantages), _ptr(ref_logprobs), float(kl_coef),
+         float(clip_low), float(clip_high), float(tau), _ptr(logprob), _ptr(grad_tokens),
+         float(grad_scale), _ptr(dlogits), ldd, _stream(logits))
+
+
+def tpmlp_vocab_policy_with_grad(logits, targets, old_logprobs, advantages, ref_logprobs, T: int,
+                                 kl_coef: float, clip_low: float, clip_high: float, tau: float,
+                                 loss_per_token, loss_mean, logprob, kl, grad_tokens,
+                                 grad_scale: float, dlogits):
+    """Loss and gradient in one launch; dlogits may be logits itself."""
+    ld = _require_rows(logits, "logits")
+    N, V = logits.shape
+    _require_tokens(logits, targets, old_logprobs, advantages, ref_logprobs)
+    ldd = _require_dlogits(logits, dlogits)
+    _require([loss_per_token, loss_mean, logprob, kl, grad_tokens], logits.device, torch.float32)
+    for t in (loss_per_token, logprob, kl, grad_tokens):
+        _require_len(t, N, "a per-token tensor")
+    _run(logits, lib().tpmlp_vocab_policy_with_grad, _dtype_code(logits), N, V, T, _ptr(logits), ld,
+         _ptr(targets), _ptr(old_logprobs), _ptr(advantages), _ptr(ref_logprobs), float(kl_coef),
+         float(clip_low), float(clip_high), float(tau), _ptr(loss_per_token), _ptr(loss_mean),
+         _ptr(logprob), _ptr(kl), _ptr(grad_tokens), float(grad_scale), _ptr(dlogits), ldd,
+         _stream(logits))
+
+
+def _require_params(x, *params):
+    """Element type of a layer norm's parameters: one for all, x's where there are none."""
+    given = [p for p in params if p is not None]
+    dtype = given[0].dtype if given else x.dtype
+    _require(given, x.device, dtype)
+    for p in given:
+        _require_len(p, x.shape[1], "a parameter")
+    return _dtype_code(given[0] if given else x)
+
+
+def tpmlp_layernorm(x, weight, bias, eps: float, y, mean=None, rstd=None):
+    """y = (x - mean) rstd weight + bias over the rows of x; y may be x itself."""
+    ldx = _require_rows(x, "x")
+    N, D = x.shape
+    ldy = _require_matrix(y, x.shape, x.device, x.dtype, "y")
+    param_dt = _require_params(x, weight, bias)
+    _require([mean, rstd], x.device, torch.float32)
+    for t in (mean, rstd):
+        _require_len(t, N, "a per-row tensor")
+    _run(x, lib().tpmlp_layernorm, _dtype_code(x), param_dt, N, D, _ptr(x), ldx, _ptr(weight), _ptr(bias),
+         float(eps), _ptr(y), ldy, _ptr(mean), _ptr(rstd), _stream(x))
+
+
+def tpmlp_layernorm_backward_workspace_bytes(N: int, D: int) -> int:
+    return int(lib().tpmlp_layernorm_backward_workspace_bytes(N, D))
+
+
+def tpmlp_layernorm_backward(dy, x, weight, mean, rstd, dresidual, dx, dweight, dbias, workspace):
+    """Gradients of the layer norm; dx may be dy, x or dresidual itself."""
+    ldx = _require_rows(x, "x")
+    N, D = x.shape
+    lddy, lddres, lddx = (_require_matrix(t, x.shape, x.device, x.dtype, what) for t, what in
+                          ((dy, "dy"), (dresidual, "dresidual"), (dx, "dx")))
+    param_dt = _require_params(x, weight, dweight, dbias)
+    _require([mean, rstd], x.device, torch.float32)
+    for t in (mean, rstd):
+        _require_len(t, N, "a per-row tensor")
+    ws_bytes = _bytes(workspace, x.device)
+    _run(x, lib().tpmlp_layernorm_backward, _dtype_code(x), param_dt, N, D, _ptr(dy), lddy, _ptr(x), ldx,
+         _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dresidual), lddres, _ptr(dx), lddx, _ptr(dweight),
+         _ptr(dbias), _ptr(workspace), ws_bytes, _stream(x))
+
+
+def tpmlp_column_linear(X, W, b, act, R, Y, Z, workspace=None):
+    """Y = act(X W + b) + R, W's columns in len(W) shards (b: a list, or None);
+    Z, if given, receives X W + b."""
+    ldx = _require_rows(X, "X")
+    N, D = X.shape
+    T, Fs = len(W), W[0].shape[1]
+    dev, dt, out = X.device, X.dtype, (N, T * Fs)
+    ldr, ldy, ldz = (_require_matrix(t, out, dev, dt, what) for t, what in ((R, "R"), (Y, "Y"), (Z, "Z")))
+    ws_bytes = _bytes(workspace, dev)
+    _run(X, lib().tpmlp_column_linear, _dtype_code(X), N, D, Fs * T, T, LINEAR_ACT[act], _ptr(X), ldx,
+         _shards(W, T, (D, Fs), dev, dt), None if b is None else _shards(b, T, (Fs,), dev, dt), _ptr(R),
+         ldr, _ptr(Y), ldy, _ptr(Z), ldz, _ptr(workspace), ws_bytes, _stream(X))
+
+
+def tpmlp_row_linear(X, W, b, R, Y, workspace=None):
+    """Y = sum_r X[:, shard r] W[r] + b + R, W's rows in len(W) shards."""
+    ldx = _require_rows(X, "X")
+    T = len(W)
+    Fs, D = W[0].shape
+    dev, dt, out = X.device, X.dtype, (X.shape[0], D)
+    if X.shape[1] != T * Fs:
+        raise ValueError(f"X has {X.shape[1]} columns, W {T * Fs} rows")
+    ldr, ldy = (_require_matrix(t, out, dev, dt, what) for t, what in ((R, "R"), (Y, "Y")))
+    _require([b], dev, dt)
+    _require_len(b, D, "b")
+    ws_bytes = _bytes(workspace, dev)
+    _run(X, lib().tpmlp_row_linear, _dtype_code(X), X.shape[0], D, Fs * T, T, _ptr(X), ldx,
+         _shards(W, T, (Fs, D), dev, dt), _ptr(b), _ptr(R), ldr, _ptr(Y), ldy, _ptr(workspace), ws_bytes,
+         _stream(X))
+
+
+def tpmlp_column_linear_backward(X, W, Z, dY, act, dX, dW, db, workspace=None):
+    """Gradients of column_linear for upstream dY (db: a list, or None)."""
+    ldx = _require_rows(X, "X")
+    N, D = X.shape
+    T, Fs = len(W), W[0].shape[1]
+    dev, dt, out = X.device, X.dtype, (N, T * Fs)
+    ldz, lddy = (_require_matrix(t, out, dev, dt, what) for t, what in ((Z, "Z"), (dY, "dY")))
+    lddx = _require_matrix(dX, X.shape, dev, dt, "dX")
+    ws_bytes = _bytes(workspace, dev)
+    _run(X, lib().tpmlp_column_linear_backward, _dtype_code(X), N, D, Fs * T, T, LINEAR_ACT[act], _ptr(X),
+         ldx, _shards(W, T, (D, Fs), dev, dt), _ptr(Z), ldz, _ptr(dY), lddy, _ptr(dX), lddx,
+         _shards(dW, T, (D, Fs), dev, dt), None if db is None else _shards(db, T, (Fs,), dev, dt),
+         _ptr(workspace), ws_bytes, _stream(X))
+
+
+def tpmlp_row_linear_backward(X, W, dY, dX, dW, db, workspace=None):
+    """Gradients of row_linear for upstream dY (db: [D], or None)."""
+    ldx = _require_rows(X, "X")
+    T = len(W)
+    Fs, D = W[0].shape
+    dev, dt = X.device, X.dtype
+    if X.shape[1] != T * Fs:
+        raise ValueError(f"X has {X.shape[1]} columns, W {T * Fs} rows")
+    lddy = _require_matrix(dY, (X.shape[0], D), dev, dt, "dY")
+    lddx = _require_matrix(dX, X.shape, dev, dt, "dX")
+    _require([db], dev, dt)
+    _require_len(db, D, "db")
+    ws_bytes = _bytes(workspace, dev)
+    _run(X, lib().tpmlp_row_linear_backward, _dtype_code(X), X.shape[0], D, Fs * T, T, _ptr(X), ldx,
+         _shards(W, T, (Fs, D), dev, dt), _ptr(dY), lddy, _ptr(dX), lddx, _shards(dW, T, (Fs, D), dev, dt),
+         _ptr(db), _ptr(workspace), ws_bytes, _stream(X))
 
 
 def tpmlp_check_device_error(device=None) -> int:

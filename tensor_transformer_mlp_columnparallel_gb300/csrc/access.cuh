@@ -1,0 +1,80 @@
+// Accesses of 16, 4 or 2 bytes to rows of fp32 or bf16 elements, as fp32 values:
+// the widest access that divides a row, its pitch and its address serves all
+// of the row.
+#pragma once
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "act.cuh"
+
+namespace tpmlp {
+
+template <int B> struct AccessWord;
+template <> struct AccessWord<16> { using type = uint4; };
+template <> struct AccessWord<8> { using type = uint2; };
+template <> struct AccessWord<4> { using type = uint32_t; };
+template <> struct AccessWord<2> { using type = unsigned short; };
+
+// N elements of T in one access of B bytes.
+template <typename T, int B>
+struct Access {
+    using Word = typename AccessWord<B>::type;
+    static constexpr int N = B / (int)sizeof(T);
+    static_assert(N >= 1, "an access holds an element");
+
+    static __device__ __forceinline__ void unpack(const Word& x, float (&v)[N]) {
+        if constexpr (sizeof(T) == 4) {
+            const float* f = reinterpret_cast<const float*>(&x);
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = f[j];
+        } else if constexpr (B == 2) {
+            v[0] = __uint_as_float((uint32_t)x << 16);
+        } else {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(&x);
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) {
+                v[2 * j] = __uint_as_float(w[j] << 16);
+                v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+            }
+        }
+    }
+    static __device__ __forceinline__ Word pack(const float (&v)[N]) {
+        Word x;
+        if constexpr (sizeof(T) == 4) {
+            float* f = reinterpret_cast<float*>(&x);
+#pragma unroll
+            for (int j = 0; j < N; ++j) f[j] = v[j];
+        } else if constexpr (B == 2) {
+            x = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
+        } else {
+            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+        }
+        return x;
+    }
+};
+
+// N consecutive elements of T from an address that is aligned to
+// min(16, N sizeof(T)) bytes (parameters, which many rows read: cached).
+template <typename T, int N>
+__device__ __forceinline__ void load_params(const T* p, float (&v)[N]) {
+    constexpr int BYTES = N * (int)sizeof(T), B = BYTES < 16 ? BYTES : 16;
+    using A = Access<T, B>;
+#pragma unroll
+    for (int k = 0; k < BYTES / B; ++k) {
+        float t[A::N];
+        A::unpack(__ldg(reinterpret_cast<const typename A::Word*>(p) + k), t);
+#pragma unroll
+        for (int j = 0; j < A::N; ++j) v[k * A::N + j] = t[j];
+    }
+}
+
+// Host side: whether accesses of `bytes` fit an address and (for several rows)
+// a pitch in bytes.
+inline bool access_fits(const void* p, int64_t pitch, int bytes) {
+    return reinterpret_cast<uintptr_t>(p) % bytes == 0 && pitch % bytes == 0;
+}
+
+}  // namespace tpmlp

@@ -213,6 +213,12 @@ size_t dz_bytes(tpmlp_dtype dt, int64_t N, int64_t Fs, int T) {
 // the launch (N = 16, D = 4096, F = 16384, T = 4: 61 us with and without).
 bool keeps_rest(tpmlp_dtype dt, int64_t N) { return dt == TPMLP_BF16 && N <= 64; }
 
+// dZ of a column-split layer with an activation: [N, F], and for few bf16 tokens
+// N more rows with what rounding it left over
+size_t linear_dz_bytes(tpmlp_dtype dt, int64_t N, int64_t F) {
+    return round256((size_t)(keeps_rest(dt, N) ? 2 * N : N) * F * (dt == TPMLP_BF16 ? 2 : 4));
+}
+
 // Optional scratch of the bf16 GEMMs' stream-K form
 // (tpmlp_workspace_bytes_balanced): per-tile arrival counters, then fp32
 // partial-accumulator slots, two per CTA.
@@ -242,11 +248,12 @@ int64_t sk_units_bound(int64_t D, int64_t Fs, int T) {
     const int64_t b = ((D + 127) / 128) * ((Fs + 63) / 64);
     return (int64_t)T * (a > b ? a : b);
 }
-// The gated backward has none for N <= 64: dealt out, its few-token products
+// The gated backward (and the split linear layers) have none for N <= 64: dealt out, its few-token products
 // took up to twice as long as whole tiles and the K split across a cluster
 // (N = 16, F = 16384, T = 4 on GB300: dX 98 us against 47 us at D = 2048).
 size_t sk_bytes(tpmlp_op op, tpmlp_dtype dt, int64_t N, int64_t D, int64_t F, int T) {
-    if (dt != TPMLP_BF16 || N < 1 || (op == TPMLP_OP_SWIGLU_BACKWARD && N <= 64)) return 0;
+    const bool block = op == TPMLP_OP_FORWARD || op == TPMLP_OP_BACKWARD;
+    if (dt != TPMLP_BF16 || N < 1 || (!block && N <= 64)) return 0;
     return sk_cnt_bytes(N, D, F / T, T) + sk_part_bytes_for(N, sk_units_bound(D, F / T, T));
 }
 
@@ -315,6 +322,8 @@ size_t tpmlp_workspace_bytes(tpmlp_op op, tpmlp_dtype dt, int64_t N, int64_t D, 
     if (op == TPMLP_OP_FORWARD) return part;
     if (op == TPMLP_OP_BACKWARD) return dz_bytes(dt, N, F / T, T) + part;
     if (op == TPMLP_OP_SWIGLU_BACKWARD) return 2 * dz_bytes(dt, keeps_rest(dt, N) ? 2 * N : N, F / T, T) + part;
+    if (op == TPMLP_OP_LINEAR || op == TPMLP_OP_LINEAR_BACKWARD) return 0;
+    if (op == TPMLP_OP_LINEAR_BACKWARD_ACT) return N == 0 ? 0 : linear_dz_bytes(dt, N, F) + dact_part_bytes(N, F);
     return (size_t)-1;
 }
 
@@ -790,6 +799,291 @@ tpmlp_status tpmlp_swiglu_backward(tpmlp_dtype dt, int64_t N, int64_t D, int64_t
     return TPMLP_OK;
 }
 
+// A [rows, cols] matrix in rows of ld elements: at least cols; on the bf16 path
+// 16-byte aligned address and rows, else aligned elements
+static tpmlp_status check_matrix(tpmlp_dtype dt, const void* p, int64_t ld, int64_t cols) {
+    if (p == nullptr) return TPMLP_ERR_ARG;
+    if (ld < cols || ld > (1LL << 38)) return TPMLP_ERR_SHAPE;   // tensor maps' row pitch: below 2^40 bytes
+    if (dt == TPMLP_BF16 ? !aligned16(p) || ld % 8 != 0 : reinterpret_cast<uintptr_t>(p) % 4 != 0)
+        return TPMLP_ERR_ALIGN;
+    return TPMLP_OK;
+}
+
+// columns [c, ...) of a matrix of dt
+static void* at_column(const void* p, int64_t c, tpmlp_dtype dt) {
+    return const_cast<char*>(static_cast<const char*>(p)) + c * (dt == TPMLP_BF16 ? 2 : 4);
+}
+
+static tpmlp_status check_linear(tpmlp_dtype dt, int64_t N, int64_t D, int64_t F, int T, tpmlp_act act) {
+    return check_dims(dt, N, D, F, T, act == TPMLP_ACT_NONE ? TPMLP_ACT_RELU : act);
+}
+
+tpmlp_status tpmlp_column_linear(tpmlp_dtype dt, int64_t N, int64_t D, int64_t F, int T, tpmlp_act act,
+                                 const void* X, int64_t ldx, const void* const* W, const void* const* b,
+                                 const void* R, int64_t ldr, void* Y, int64_t ldy, void* Z, int64_t ldz,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+    TPMLP_TRY(check_linear(dt, N, D, F, T, act));
+    if (Z != nullptr && act == TPMLP_ACT_NONE) return TPMLP_ERR_ARG;
+    if (N == 0) return TPMLP_OK;
+    const bool bf = dt == TPMLP_BF16;
+    TPMLP_TRY(check_matrix(dt, X, ldx, D));
+    TPMLP_TRY(check_matrix(dt, Y, ldy, F));
+    TPMLP_TRY(check_shards(W, T, bf));
+    if (b != nullptr) TPMLP_TRY(check_shards(b, T, bf));
+    if (R != nullptr) TPMLP_TRY(check_matrix(dt, R, ldr, F));
+    if (R == Y && ldr != ldy) return TPMLP_ERR_ARG;   // in place: the same rows
+    if (Z != nullptr) TPMLP_TRY(check_matrix(dt, Z, ldz, F));
+    if (workspace_bytes > 0 && !aligned16(workspace)) return TPMLP_ERR_ALIGN;
+    const int Fs = (int)(F / T);
+    GemmProblem p = problem((int)N, Fs, (int)D, T, 0, ldx, 0, Fs, 1, "column_linear");
+    p.epi.kind = act == TPMLP_ACT_NONE ? EPI_STORE : EPI_ACT;
+    p.epi.act = act;
+    p.epi.out_f32 = bf ? 0 : 1;
+    p.epi.ldc = ldy;
+    p.epi.ldaux = ldz;
+    p.epi.ldres = ldr;
+    for (int r = 0; r < T; ++r) {
+        const int64_t c = (int64_t)r * Fs;
+        p.A[r] = X;
+        p.B[r] = W[r];
+        p.epi.C[r] = at_column(Y, c, dt);
+        p.epi.bias[r] = b ? b[r] : nullptr;
+        p.epi.aux[r] = Z ? at_column(Z, c, dt) : nullptr;
+        p.epi.res[r] = R ? at_column(R, c, dt) : nullptr;
+    }
+    return run_gemm(dt, p, static_cast<cudaStream_t>(stream),
+                    sk_area(workspace, workspace_bytes, 0, dt, N, D, F, T, TPMLP_OP_LINEAR));
+}
+
+tpmlp_status tpmlp_row_linear(tpmlp_dtype dt, int64_t N, int64_t D, int64_t F, int T, const void* X,
+                              int64_t ldx, const void* const* W, const void* b, const void* R,
+                              int64_t ldr, void* Y, int64_t ldy, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+    TPMLP_TRY(check_linear(dt, N, D, F, T, TPMLP_ACT_NONE));
+    if (N == 0) return TPMLP_OK;
+    const bool bf = dt == TPMLP_BF16;
+    TPMLP_TRY(check_matrix(dt, X, ldx, F));
+    TPMLP_TRY(check_matrix(dt, Y, ldy, D));
+    TPMLP_TRY(check_shards(W, T, bf));
+    if (b != nullptr) TPMLP_TRY(check_shards(&b, 1, bf));
+    if (R != nullptr) TPMLP_TRY(check_matrix(dt, R, ldr, D));
+    if (R == Y && ldr != ldy) return TPMLP_ERR_ARG;
+    if (workspace_bytes > 0 && !aligned16(workspace)) return TPMLP_ERR_ALIGN;
+    const int Fs = (int)(F / T);
+    GemmProblem p = problem((int)N, (int)D, Fs, T, 1, ldx, 0, D, 1, "row_linear");
+    p.epi.kind = EPI_STORE;
+    p.epi.out_f32 = bf ? 0 : 1;
+    p.epi.ldc = ldy;
+    p.epi.C[0] = Y;
+    p.epi.bias[0] = b;
+    p.epi.res[0] = R;
+    p.epi.ldres = ldr;
+    for (int r = 0; r < T; ++r) {
+        p.A[r] = at_column(X, (int64_t)r * Fs, dt);
+        p.B[r] = W[r];
+    }
+    return run_gemm(dt, p, static_cast<cudaStream_t>(stream),
+                    sk_area(workspace, workspace_bytes, 0, dt, N, D, F, T, TPMLP_OP_LINEAR));
+}
+
+// Both layers' gradients. column: W[r] [D, F/T], dZ [N, F]; else W[r] [F/T, D],
+// dZ [N, D]. dZ is dY, or for a column layer with an activation a matrix in the
+// workspace.
+static tpmlp_status linear_backward(bool column, tpmlp_dtype dt, int64_t N, int64_t D, int64_t F, int T,
+                                    tpmlp_act act, const void* X, int64_t ldx, const void* const* W,
+                                    const void* Z, int64_t ldz, const void* dY, int64_t lddy, void* dX,
+                                    int64_t lddx, void* const* dW, void* const* db, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+    TPMLP_TRY(check_linear(dt, N, D, F, T, act));
+    const bool bf = dt == TPMLP_BF16;
+    const int nb = column ? T : 1;   // parts of the bias
+    TPMLP_TRY(check_shards(reinterpret_cast<const void* const*>(dW), T, bf));
+    if (db != nullptr) TPMLP_TRY(check_shards(reinterpret_cast<const void* const*>(db), nb, bf));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int Fs = (int)(F / T);
+    const int f32 = bf ? 0 : 1;
+    const size_t esz = bf ? 2 : 4;
+    const int64_t in = column ? D : F, out = column ? F : D;
+    if (N == 0) {   // sums over an empty token set
+        for (int r = 0; r < T; ++r)
+            if (cudaMemsetAsync(dW[r], 0, (size_t)D * Fs * esz, s) != cudaSuccess) return TPMLP_ERR_CUDA;
+        for (int r = 0; db != nullptr && r < nb; ++r)
+            if (cudaMemsetAsync(db[r], 0, (size_t)(out / nb) * esz, s) != cudaSuccess) return TPMLP_ERR_CUDA;
+        return TPMLP_OK;
+    }
+    TPMLP_TRY(check_matrix(dt, X, ldx, in));
+    TPMLP_TRY(check_matrix(dt, dY, lddy, out));
+    TPMLP_TRY(check_matrix(dt, dX, lddx, in));
+    TPMLP_TRY(check_shards(W, T, bf));
+    const bool has_act = act != TPMLP_ACT_NONE;
+    if (has_act) TPMLP_TRY(check_matrix(dt, Z, ldz, F));
+    const tpmlp_op op = has_act ? TPMLP_OP_LINEAR_BACKWARD_ACT : TPMLP_OP_LINEAR_BACKWARD;
+    const size_t need = tpmlp_workspace_bytes(op, dt, N, D, F, T, TPMLP_REDUCE_SPLITK);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return TPMLP_ERR_WORKSPACE;
+    if (workspace_bytes > 0 && !aligned16(workspace)) return TPMLP_ERR_ALIGN;
+    const SkArea sk = sk_area(workspace, workspace_bytes, need, dt, N, D, F, T, op);
+
+    // 1. dZ = dY act'(Z) and the bias gradient, the column sums of dZ
+    const void* dZ = dY;
+    int64_t lddz = lddy;
+    const int64_t rest = has_act && keeps_rest(dt, N) ? N : 0;   // rows behind dZ
+    if (has_act) {
+        DactArgs a{};
+        a.N = N;
+        a.F = F;
+        a.T = T;
+        a.dY = dY;
+        a.lddy = lddy;
+        a.Z = Z;
+        a.ldz = ldz;
+        a.dZ = workspace;
+        a.rest = rest > 0;
+        for (int r = 0; db != nullptr && r < T; ++r) a.db[r] = db[r];
+        a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + linear_dz_bytes(dt, N, F));
+        TPMLP_TRY(run_dact(f32, act, a, s));
+        dZ = workspace;
+        lddz = F;
+    } else if (db != nullptr) {
+        const void* in_g[kMaxColsumG];
+        void* out_g[kMaxColsumG];
+        int64_t cols[kMaxColsumG], ld[kMaxColsumG];
+        for (int r = 0; r < nb; ++r) {
+            in_g[r] = at_column(dY, (int64_t)r * Fs, dt);
+            out_g[r] = db[r];
+            cols[r] = out / nb;
+            ld[r] = lddy;
+        }
+        TPMLP_TRY(run_colsum(f32, N, nb, cols, ld, in_g, out_g, s, sk.part, sk.part_bytes));
+    }
+
+    // 2. dW[r] = X^T dZ_r (column) or X_r^T dZ
+    if (bf && N <= kFewTokens) {
+        WeightGradProduct w[kMaxWeightGrads];
+        for (int r = 0; r < T; ++r) {
+            const int64_t c = (int64_t)r * Fs;
+            const void* b = column ? at_column(dZ, c, dt) : dZ;
+            w[r] = WeightGradProduct{column ? X : at_column(X, c, dt), b,
+                                     rest > 0 ? at_column(b, rest * F, dt) : nullptr, dW[r], ldx, lddz,
+                                     column ? Fs : D, column ? (int)D : Fs, column ? Fs : (int)D};
+        }
+        TPMLP_TRY(run_weight_grads(w, T, (int)N, s, "linear_weight_grads"));
+    } else {
+        GemmProblem p = column ? problem((int)D, Fs, (int)N, T, 0, ldx, 1, lddz, 1, "linear_dw_gemm")
+                               : problem(Fs, (int)D, (int)N, T, 0, ldx, 1, lddz, 1, "linear_dw_gemm");
+        p.epi.kind = EPI_STORE;
+        p.epi.out_f32 = f32;
+        p.epi.ldc = column ? Fs : D;
+        for (int r = 0; r < T; ++r) {
+            const int64_t c = (int64_t)r * Fs;
+            p.A[r] = column ? X : at_column(X, c, dt);
+            p.B[r] = column ? at_column(dZ, c, dt) : dZ;
+            p.epi.C[r] = dW[r];
+        }
+        TPMLP_TRY(run_gemm(dt, p, s, sk));
+    }
+
+    // 3. dX = sum_r dZ_r W[r]^T (column) or dX_r = dZ W[r]^T, all operands K-major
+    GemmProblem p = column ? problem((int)N, (int)D, Fs, T, 1, lddz, 0, Fs, 0, "linear_dx_gemm")
+                           : problem((int)N, Fs, (int)D, T, 0, lddz, 0, D, 0, "linear_dx_gemm");
+    p.rest_rows = rest > 0 && N <= kRestRows ? (int)N : 0;
+    p.epi.kind = EPI_STORE;
+    p.epi.out_f32 = f32;
+    p.epi.ldc = lddx;
+    for (int r = 0; r < T; ++r) {
+        const int64_t c = (int64_t)r * Fs;
+        p.A[r] = column ? at_column(dZ, c, dt) : dZ;
+        p.B[r] = W[r];
+        p.epi.C[r] = column ? dX : at_column(dX, c, dt);
+    }
+    return run_gemm(dt, p, s, sk);
+}
+
+tpmlp_status tpmlp_column_linear_backward(tpmlp_dtype dt, int64_t N, int64_t D, int64_t F, int T,
+                                          tpmlp_act act, const void* X, int64_t ldx,
+                                          const void* const* W, const void* Z, int64_t ldz,
+                                          const void* dY, int64_t lddy, void* dX, int64_t lddx,
+                                          void* const* dW, void* const* db, void* workspace,
+                                          size_t workspace_bytes, void* stream) {
+    return linear_backward(true, dt, N, D, F, T, act, X, ldx, W, Z, ldz, dY, lddy, dX, lddx, dW, db,
+                           workspace, workspace_bytes, stream);
+}
+
+tpmlp_status tpmlp_row_linear_backward(tpmlp_dtype dt, int64_t N, int64_t D, int64_t F, int T,
+                                       const void* X, int64_t ldx, const void* const* W,
+                                       const void* dY, int64_t lddy, void* dX, int64_t lddx,
+                                       void* const* dW, void* db, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+    return linear_backward(false, dt, N, D, F, T, TPMLP_ACT_NONE, X, ldx, W, nullptr, 0, dY, lddy, dX,
+                           lddx, dW, db != nullptr ? &db : nullptr, workspace, workspace_bytes, stream);
+}
+
+// Sizes, element types and alignment that both layer norm calls share
+static tpmlp_status check_norm(tpmlp_dtype dt, tpmlp_dtype param_dt, int64_t N, int64_t D) {
+    if ((dt != TPMLP_F32 && dt != TPMLP_BF16) || (param_dt != TPMLP_F32 && param_dt != TPMLP_BF16))
+        return TPMLP_ERR_DTYPE;
+    if (dt == TPMLP_F32 && param_dt != TPMLP_F32) return TPMLP_ERR_DTYPE;
+    if (N < 0) return TPMLP_ERR_ARG;
+    if (D <= 0 || D > 0x7fffff00LL || N > 0x7fffffffLL) return TPMLP_ERR_SHAPE;
+    return TPMLP_OK;
+}
+static tpmlp_status check_norm_rows(tpmlp_dtype dt, const void* p, int64_t ld, int64_t D) {
+    if (p == nullptr) return TPMLP_ERR_ARG;
+    if (ld < D || ld > (1LL << 40)) return TPMLP_ERR_SHAPE;
+    return reinterpret_cast<uintptr_t>(p) % (dt == TPMLP_F32 ? 4 : 2) == 0 ? TPMLP_OK : TPMLP_ERR_ALIGN;
+}
+static tpmlp_status check_norm_aligned(size_t size, std::initializer_list<const void*> ptrs) {
+    for (const void* p : ptrs)
+        if (reinterpret_cast<uintptr_t>(p) % size != 0) return TPMLP_ERR_ALIGN;
+    return TPMLP_OK;
+}
+
+tpmlp_status tpmlp_layernorm(tpmlp_dtype dt, tpmlp_dtype param_dt, int64_t N, int64_t D, const void* x,
+                             int64_t ldx, const void* weight, const void* bias, float eps, void* y,
+                             int64_t ldy, float* mean, float* rstd, void* stream) {
+    TPMLP_TRY(check_norm(dt, param_dt, N, D));
+    if (!(eps >= 0.f && eps <= 3.402823466e38f)) return TPMLP_ERR_ARG;
+    if (N == 0) return TPMLP_OK;
+    TPMLP_TRY(check_norm_rows(dt, x, ldx, D));
+    TPMLP_TRY(check_norm_rows(dt, y, ldy, D));
+    if (x == y && ldx != ldy) return TPMLP_ERR_ARG;   // in place: the same rows
+    TPMLP_TRY(check_norm_aligned(param_dt == TPMLP_F32 ? 4 : 2, {weight, bias}));
+    TPMLP_TRY(check_norm_aligned(4, {mean, rstd}));
+    const LayernormArgs a{N, D, x, ldx, weight, bias, eps, y, ldy, mean, rstd};
+    return run_layernorm(dt == TPMLP_F32, param_dt == TPMLP_F32, a, static_cast<cudaStream_t>(stream));
+}
+
+size_t tpmlp_layernorm_backward_workspace_bytes(int64_t N, int64_t D) {
+    if (N < 0 || N > 0x7fffffffLL || D <= 0 || D > 0x7fffff00LL) return (size_t)-1;
+    return layernorm_backward_bytes(N, D);
+}
+
+tpmlp_status tpmlp_layernorm_backward(tpmlp_dtype dt, tpmlp_dtype param_dt, int64_t N, int64_t D,
+                                      const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                      const void* weight, const float* mean, const float* rstd,
+                                      const void* dresidual, int64_t lddres, void* dx, int64_t lddx,
+                                      void* dweight, void* dbias, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+    TPMLP_TRY(check_norm(dt, param_dt, N, D));
+    if ((dweight == nullptr) != (dbias == nullptr)) return TPMLP_ERR_ARG;
+    TPMLP_TRY(check_norm_aligned(param_dt == TPMLP_F32 ? 4 : 2, {weight, dweight, dbias}));
+    if (N > 0) {
+        TPMLP_TRY(check_norm_rows(dt, dy, lddy, D));
+        TPMLP_TRY(check_norm_rows(dt, x, ldx, D));
+        TPMLP_TRY(check_norm_rows(dt, dx, lddx, D));
+        if (dresidual != nullptr) TPMLP_TRY(check_norm_rows(dt, dresidual, lddres, D));
+        if (mean == nullptr || rstd == nullptr) return TPMLP_ERR_ARG;
+        TPMLP_TRY(check_norm_aligned(4, {mean, rstd}));
+        if ((dx == dy && lddx != lddy) || (dx == x && lddx != ldx) || (dx == dresidual && lddx != lddres))
+            return TPMLP_ERR_ARG;   // in place: the same rows
+        if (workspace == nullptr || workspace_bytes < layernorm_backward_bytes(N, D)) return TPMLP_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return TPMLP_ERR_ALIGN;
+    }
+    const LayernormGradArgs a{N, D, dy, lddy, x, ldx, weight, mean, rstd, dresidual, lddres, dx, lddx,
+                              dweight, dbias};
+    return run_layernorm_backward(dt == TPMLP_F32, param_dt == TPMLP_F32, a, workspace,
+                                  static_cast<cudaStream_t>(stream));
+}
+
 tpmlp_status tpmlp_block_reduce(tpmlp_dtype dt, int64_t N, int64_t D, int T,
                                 const float* const* partials, const void* b2, void* Y,
                                 void* stream) {
@@ -989,6 +1283,109 @@ tpmlp_status tpmlp_vocab_distill_with_grad(tpmlp_dtype dt, int64_t N, int64_t V,
     TPMLP_TRY(distill_loss_args(loss_per_token, loss_mean, lse, a));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     TPMLP_TRY(run_vocab_distill(dt == TPMLP_F32, a, s));
+    return loss_mean != nullptr ? run_mean(loss_per_token, N, loss_mean, s) : TPMLP_OK;
+}
+
+// The checks of the three policy calls, and their common arguments
+static tpmlp_status policy_args(tpmlp_dtype dt, int64_t N, int64_t V, int T, const void* logits, int64_t ld,
+                                const int64_t* targets, const float* old_logprobs, const float* advantages,
+                                const float* ref_logprobs, float kl_coef, float clip_low, float clip_high,
+                                float tau, PolicyArgs& a) {
+    TPMLP_TRY(check_rows(dt, N, V, T, logits, ld));
+    if (!(tau >= 0x1p-60f && tau <= 0x1p60f)) return TPMLP_ERR_ARG;
+    if (!(kl_coef >= 0.f && kl_coef <= 3.402823466e38f)) return TPMLP_ERR_ARG;
+    if (!(clip_low >= 0.f && clip_low <= 1.f) || !(clip_high >= 0.f)) return TPMLP_ERR_ARG;
+    if (kl_coef != 0.f && ref_logprobs == nullptr && N > 0) return TPMLP_ERR_ARG;
+    if (N > 0 && (targets == nullptr || old_logprobs == nullptr || advantages == nullptr)) return TPMLP_ERR_ARG;
+    TPMLP_TRY(check_align(8, {targets}));
+    TPMLP_TRY(check_align(4, {old_logprobs, advantages, ref_logprobs}));
+    a = PolicyArgs{};
+    a.logits = logits;
+    a.ld = ld;
+    a.N = N;
+    a.V = V;
+    a.targets = targets;
+    a.old_logprobs = old_logprobs;
+    a.advantages = advantages;
+    a.ref_logprobs = ref_logprobs;
+    a.kl_coef = kl_coef;
+    a.low = clip_low;
+    a.high = clip_high;
+    a.tau = tau;
+    return TPMLP_OK;
+}
+
+static tpmlp_status policy_loss_args(float* loss_per_token, float* loss_mean, float* logprob, float* kl,
+                                     PolicyArgs& a) {
+    if (a.N > 0 && loss_per_token == nullptr) return TPMLP_ERR_ARG;
+    if (a.N > 0 && kl != nullptr && a.ref_logprobs == nullptr) return TPMLP_ERR_ARG;
+    TPMLP_TRY(check_align(4, {loss_per_token, loss_mean, logprob, kl}));
+    a.loss = loss_per_token;
+    a.logprob = logprob;
+    a.kl = kl;
+    return TPMLP_OK;
+}
+
+static tpmlp_status policy_grad_args(tpmlp_dtype dt, const float* grad_tokens, float grad_scale,
+                                     void* dlogits, int64_t ldd, PolicyArgs& a) {
+    if (ldd < a.V || ldd > (1LL << 40)) return TPMLP_ERR_SHAPE;
+    if (a.N > 0) {
+        if (dlogits == nullptr) return TPMLP_ERR_ARG;
+        TPMLP_TRY(check_align(elem_size(dt), {dlogits}));
+        if (dlogits == a.logits && ldd != a.ld) return TPMLP_ERR_ARG;   // in place: the same rows
+    }
+    TPMLP_TRY(check_align(4, {grad_tokens}));
+    a.grad_tokens = grad_tokens;
+    a.grad_scale = grad_scale;
+    a.dlogits = dlogits;
+    a.ldd = ldd;
+    return TPMLP_OK;
+}
+
+tpmlp_status tpmlp_vocab_policy(tpmlp_dtype dt, int64_t N, int64_t V, int T, const void* logits, int64_t ld,
+                                const int64_t* targets, const float* old_logprobs,
+                                const float* advantages, const float* ref_logprobs, float kl_coef,
+                                float clip_low, float clip_high, float tau, float* loss_per_token,
+                                float* loss_mean, float* logprob, float* kl, void* stream) {
+    PolicyArgs a;
+    TPMLP_TRY(policy_args(dt, N, V, T, logits, ld, targets, old_logprobs, advantages, ref_logprobs, kl_coef,
+                          clip_low, clip_high, tau, a));
+    TPMLP_TRY(policy_loss_args(loss_per_token, loss_mean, logprob, kl, a));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    TPMLP_TRY(run_vocab_policy(dt == TPMLP_F32, a, s));
+    return loss_mean != nullptr ? run_mean(loss_per_token, N, loss_mean, s) : TPMLP_OK;
+}
+
+tpmlp_status tpmlp_vocab_policy_backward(tpmlp_dtype dt, int64_t N, int64_t V, int T, const void* logits,
+                                         int64_t ld, const int64_t* targets, const float* old_logprobs,
+                                         const float* advantages, const float* ref_logprobs,
+                                         float kl_coef, float clip_low, float clip_high, float tau,
+                                         const float* logprob, const float* grad_tokens,
+                                         float grad_scale, void* dlogits, int64_t ldd, void* stream) {
+    PolicyArgs a;
+    TPMLP_TRY(policy_args(dt, N, V, T, logits, ld, targets, old_logprobs, advantages, ref_logprobs, kl_coef,
+                          clip_low, clip_high, tau, a));
+    TPMLP_TRY(policy_grad_args(dt, grad_tokens, grad_scale, dlogits, ldd, a));
+    if (N > 0 && logprob == nullptr) return TPMLP_ERR_ARG;
+    TPMLP_TRY(check_align(4, {logprob}));
+    a.logprob_in = logprob;
+    return run_vocab_policy(dt == TPMLP_F32, a, static_cast<cudaStream_t>(stream));
+}
+
+tpmlp_status tpmlp_vocab_policy_with_grad(tpmlp_dtype dt, int64_t N, int64_t V, int T, const void* logits,
+                                          int64_t ld, const int64_t* targets, const float* old_logprobs,
+                                          const float* advantages, const float* ref_logprobs,
+                                          float kl_coef, float clip_low, float clip_high, float tau,
+                                          float* loss_per_token, float* loss_mean, float* logprob,
+                                          float* kl, const float* grad_tokens, float grad_scale,
+                                          void* dlogits, int64_t ldd, void* stream) {
+    PolicyArgs a;
+    TPMLP_TRY(policy_args(dt, N, V, T, logits, ld, targets, old_logprobs, advantages, ref_logprobs, kl_coef,
+                          clip_low, clip_high, tau, a));
+    TPMLP_TRY(policy_grad_args(dt, grad_tokens, grad_scale, dlogits, ldd, a));
+    TPMLP_TRY(policy_loss_args(loss_per_token, loss_mean, logprob, kl, a));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    TPMLP_TRY(run_vocab_policy(dt == TPMLP_F32, a, s));
     return loss_mean != nullptr ? run_mean(loss_per_token, N, loss_mean, s) : TPMLP_OK;
 }
 

@@ -41,7 +41,7 @@ struct SimtParams {
     EpiArgs epi;
 };
 
-template <bool GATED>
+template <bool GATED, bool RESIDUAL>
 __device__ __forceinline__ void epi_scalar(const EpiArgs& e, int g, int m, int n, float v) {
     if (e.bias[g] != nullptr) v += static_cast<const float*>(e.bias[g])[n];
     if (e.kind == EPI_ACT) {
@@ -57,6 +57,7 @@ __device__ __forceinline__ void epi_scalar(const EpiArgs& e, int g, int m, int n
         static_cast<float*>(e.C2[g])[(int64_t)m * e.ldc + n] = du;
         v = dg;
     }
+    if (RESIDUAL) v += static_cast<const float*>(e.res[g])[(int64_t)m * e.ldres + n];
     int cg = g;
     int64_t crow = m;
     if (e.row_shard > 0) {
@@ -76,8 +77,8 @@ __device__ __forceinline__ void epi_swiglu_scalar(const EpiArgs& e, int g, int m
 // GATED: what only the gated backward asks for (p.chain, EPI_DSWIGLU), an
 // instance of its own: its branches cost the other GEMMs 3% (the exact-fp32
 // fwd+bwd step of N = 64, D = 256, F = 1024, T = 2 from a captured graph 76.6
-// against 74.0 us).
-template <bool A_MN, bool B_MN, bool DUAL, bool GATED = false>
+// against 74.0 us). RESIDUAL: the epilogue adds another matrix (EpiArgs::res).
+template <bool A_MN, bool B_MN, bool DUAL, bool GATED = false, bool RESIDUAL = false>
 __global__ void __launch_bounds__(256) simt_gemm_kernel(const SimtParams p) {
     // A and B stages; after the K loop the first 16 KB hold this CTA's
     // partial tile for a K split
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(256) simt_gemm_kernel(const SimtParams p) {
                 if (DUAL)
                     epi_swiglu_scalar(p.epi, g_out, m, n, acc[i][j], acc2[i][j]);
                 else
-                    epi_scalar<GATED>(p.epi, g_out, m, n, acc[i][j]);
+                    epi_scalar<GATED, RESIDUAL>(p.epi, g_out, m, n, acc[i][j]);
             }
         }
     }
@@ -277,10 +278,14 @@ tpmlp_status run_gemm_simt(const GemmProblem& pr, cudaStream_t s) {
     }
     const bool gated = pr.chain || pr.epi.kind == EPI_DSWIGLU;
     if (gated && (pr.dual || pr.a_mn || pr.b_mn)) return TPMLP_ERR_ARG;   // K-major operands
+    const bool residual = pr.epi.res[0] != nullptr;   // the split linear layers' products
+    if (residual && (gated || pr.dual || pr.a_mn || !pr.b_mn)) return TPMLP_ERR_ARG;
     cudaError_t e;
     {
         LaunchScope ls(pr.name, s);
-        if (gated) {
+        if (residual) {
+            e = cudaLaunchKernelEx(&cfg, simt_gemm_kernel<false, true, false, false, true>, kp);
+        } else if (gated) {
             e = cudaLaunchKernelEx(&cfg, simt_gemm_kernel<false, false, false, true>, kp);
         } else if (pr.dual) {
             if (pr.a_mn || !pr.b_mn || pr.fold) return TPMLP_ERR_ARG;   // the gated MLP's column GEMM only

@@ -41,6 +41,7 @@
 #include <cuda_bf16.h>
 
 #include <cstdio>
+#include <initializer_list>
 #include <mutex>
 
 #include "act.cuh"
@@ -357,6 +358,31 @@ __device__ __forceinline__ void pack_row_bf16(const float (&v)[32], uint4 (&w)[4
     }
 }
 
+// v += the residual's 32 columns from col0 of row `row`.
+__device__ __forceinline__ void add_residual_thread(const EpiArgs& e, int g, int row, int col0, int M, int N,
+                                                    float (&v)[32]) {
+    if (row >= M) return;
+    const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(e.res[g]) + (int64_t)row * e.ldres + col0;
+    if (col0 + 32 <= N) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint4 w = *(reinterpret_cast<const uint4*>(r) + q);
+            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                float lo, hi;
+                unpack_bf16x2(ws[h], lo, hi);
+                v[q * 8 + 2 * h] += lo;
+                v[q * 8 + 2 * h + 1] += hi;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (col0 + j < N) v[j] += bf2f(r[j]);
+    }
+}
+
 // Gated-MLP backward epilogue of one thread: v = dH over 32 columns from col0
 // of row `row`; dG replaces v, dU goes to C2 (G and U read, all per thread),
 // and what their rounding leaves over behind both if asked for.
@@ -559,14 +585,19 @@ __device__ __forceinline__ void epilogue_swiglu_chunk(const EpiArgs& e, int g, i
     }
 }
 
-// GATED: what only the gated backward asks for, two operand pairs in the K loop
-// (p.chain, p.rest_rows) and the EPI_DSWIGLU epilogue. An instance of its own:
+// Kernel instances. GATED: what only the gated backward asks for, two operand
+// pairs in the K loop (p.chain) and the EPI_DSWIGLU epilogue, and both parts of
+// a few rows (p.rest_rows). Instances of their own:
 // their branches cost the other GEMMs 0.3 to 0.6% (GB300, in turn: the fwd+bwd
 // step of N = 8192, D = 8192, F = 28672, T = 8 in 12.86 against 12.79 ms, the
 // forward of N = 4096, D = 4096, F = 16384, T = 4 in 640 against 636 us).
-template <int BN, bool PAIR, bool GATED>
+// RESIDUAL: the epilogue adds another matrix (EpiArgs::res).
+enum Form { PLAIN = 0, GATED_FORM = 1, RESIDUAL_FORM = 2 };
+
+template <int BN, bool PAIR, int FORM>
 __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_constant__ TcParams p) {
     using C = Cfg<BN, PAIR>;
+    constexpr bool GATED = FORM == GATED_FORM, RESIDUAL = FORM == RESIDUAL_FORM;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -1000,6 +1031,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
                 } else {
                     epilogue_act(p.epi, g, row, col0, p.M, p.N, v);
                 }
+                if (RESIDUAL) add_residual_thread(p.epi, g, row, col0, p.M, p.N, v);
                 stage_row(buf, lane, p.epi.out_f32 != 0, v);
                 fence_proxy_async_smem();   // the staged rows, to the tensor-store proxy
                 __syncwarp();
@@ -1014,6 +1046,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
                 if (GATED && p.epi.kind == EPI_DSWIGLU)
                     epilogue_dswiglu_thread(p.epi, g, row, col0, p.M, p.N, v);
                 epilogue_act(p.epi, g, row, col0, p.M, p.N, v);
+                if (RESIDUAL) add_residual_thread(p.epi, g, row, col0, p.M, p.N, v);
                 store_c_thread(p.epi, g, row, col0, p.M, p.N, v);
             }
         };
@@ -1348,11 +1381,11 @@ int resident_units(int cl) {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || cl < 1 || cl > 8) return 0;
     if (units[dev][cl] > 0) return units[dev][cl];
     if (!attr_set[dev]) {
-        if (cudaFuncSetAttribute(tc_gemm_kernel<BN, PAIR, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 C::SMEM_BYTES) != cudaSuccess ||
-            cudaFuncSetAttribute(tc_gemm_kernel<BN, PAIR, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 C::SMEM_BYTES) != cudaSuccess)
-            return 0;
+        for (auto kernel : {tc_gemm_kernel<BN, PAIR, PLAIN>, tc_gemm_kernel<BN, PAIR, GATED_FORM>,
+                            tc_gemm_kernel<BN, PAIR, RESIDUAL_FORM>})
+            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
+                cudaSuccess)
+                return 0;
         attr_set[dev] = true;
     }
     int n = device_sm_count();
@@ -1369,7 +1402,7 @@ int resident_units(int cl) {
         cfg.dynamicSmemBytes = C::SMEM_BYTES;
         cfg.gridDim = dim3((unsigned)(cl * (n / cl)));
         n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, tc_gemm_kernel<BN, PAIR, false>, &cfg) != cudaSuccess) return 0;
+        if (cudaOccupancyMaxActiveClusters(&n, tc_gemm_kernel<BN, PAIR, PLAIN>, &cfg) != cudaSuccess) return 0;
     }
     units[dev][cl] = n > 0 ? n : 0;
     return units[dev][cl];
@@ -1504,8 +1537,10 @@ tpmlp_status launch(const GemmProblem& pr, cudaStream_t s, int ks = 1) {
     kp.n_tiles = pr.dual ? (pr.N + BN / 2 - 1) / (BN / 2) : (pr.N + BN - 1) / BN;
     kp.chain = pr.chain;
     kp.rest_rows = pr.rest_rows;
-    if (pr.rest_rows > 0 && (PAIR || !pr.chain || pr.rest_rows != pr.M || pr.M > kRestRows))
-        return TPMLP_ERR_ARG;
+    if (pr.rest_rows > 0 && (PAIR || pr.a_mn || pr.rest_rows != pr.M || pr.M > kRestRows)) return TPMLP_ERR_ARG;
+    const bool gated = pr.chain || pr.rest_rows > 0 || pr.epi.kind == EPI_DSWIGLU;
+    const bool residual = pr.epi.res[0] != nullptr;
+    if (residual && (gated || pr.dual || pr.epi.row_shard > 0 || pr.epi.out_f32)) return TPMLP_ERR_ARG;
     kp.k_blocks = (pr.K + C::BK - 1) / C::BK;
     kp.num_tiles = (pr.fold ? 1 : G) * kp.m_tiles * kp.n_tiles;
     {
@@ -1606,10 +1641,10 @@ tpmlp_status launch(const GemmProblem& pr, cudaStream_t s, int ks = 1) {
         LaunchScope ls(pr.name, s);
         // the arrival counters start at zero (a memset node inside a graph)
         e = sk ? cudaMemsetAsync(pr.sk_cnt, 0, sk_cnt_bytes, s) : cudaSuccess;
-        const bool gated = pr.chain || pr.epi.kind == EPI_DSWIGLU;
         if (e == cudaSuccess)
-            e = gated ? cudaLaunchKernelEx(&cfg, tc_gemm_kernel<BN, PAIR, true>, kp)
-                      : cudaLaunchKernelEx(&cfg, tc_gemm_kernel<BN, PAIR, false>, kp);
+            e = gated      ? cudaLaunchKernelEx(&cfg, tc_gemm_kernel<BN, PAIR, GATED_FORM>, kp)
+                : residual ? cudaLaunchKernelEx(&cfg, tc_gemm_kernel<BN, PAIR, RESIDUAL_FORM>, kp)
+                           : cudaLaunchKernelEx(&cfg, tc_gemm_kernel<BN, PAIR, PLAIN>, kp);
     }
     if (e != cudaSuccess) return TPMLP_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;

@@ -35,6 +35,10 @@ struct EpiArgs {
     // EPI_DSWIGLU, > 0: what rounding dG and dU to bf16 left over, itself in
     // bf16, this many bytes behind C and C2
     int64_t lo_off;
+    // EPI_STORE, EPI_ACT: a matrix of the compute element type, row pitch ldres,
+    // added last (to act(z)), per group like C; NULL: none
+    const void* res[kMaxG];
+    int64_t ldres;
     // > 0: C is split by rows into blocks of row_shard rows, block i at C[i]
     // (the reduce-scatter output of the block end); 0: C[g] as above
     int64_t row_shard;
@@ -66,8 +70,9 @@ struct GemmProblem {
     // gated MLP's dX. With fold the order is (g, pair, k). Not with dual.
     int chain;
     const void* A2[kMaxG];
-    // > 0 (chain, K-major A, M <= kRestRows): that many rows, M, behind A's (and
-    // A2's) M hold what A's rounding left over, to be added to its products
+    // > 0 (K-major A, M <= kRestRows): that many rows, M, behind A's (and A2's) M
+    // hold what A's rounding left over, to be added to its products (the
+    // tensor-core GEMM only)
     int rest_rows;
     EpiArgs epi;
     const char* name;          // kernel kind, for the timing records
@@ -183,6 +188,80 @@ tpmlp_status run_vocab_embedding_backward(int f32, int grad_f32, int64_t N, int6
                                           int T, const int64_t* ids, const void* dout, float scale,
                                           int accumulate, void* const* dtable, void* workspace,
                                           cudaStream_t s);
+// Layer norm over rows: fp32 or bf16 x and y, parameters of that type or fp32.
+struct LayernormArgs {
+    int64_t N, D;
+    const void* x;
+    int64_t ldx;
+    const void* weight;        // NULL: ones
+    const void* bias;          // NULL: zeros
+    float eps;
+    void* y;
+    int64_t ldy;
+    float* mean;               // NULL: not wanted
+    float* rstd;
+};
+tpmlp_status run_layernorm(int f32, int params_f32, const LayernormArgs& a, cudaStream_t s);
+struct LayernormGradArgs {
+    int64_t N, D;
+    const void* dy;
+    int64_t lddy;
+    const void* x;
+    int64_t ldx;
+    const void* weight;
+    const float* mean;
+    const float* rstd;
+    const void* dresidual;     // NULL: zeros
+    int64_t lddres;
+    void* dx;
+    int64_t lddx;
+    void* dweight;             // NULL (both): not wanted
+    void* dbias;
+};
+size_t layernorm_backward_bytes(int64_t N, int64_t D);
+tpmlp_status run_layernorm_backward(int f32, int params_f32, const LayernormGradArgs& a, void* workspace,
+                                    cudaStream_t s);
+
+// dZ = dY act'(Z) into contiguous rows of F columns; with `rest`, what rounding
+// dZ to bf16 left over goes to the N rows behind. db, if asked for: the column
+// sums of dZ, in T parts of F / T, through partial sums in dact_part_bytes.
+struct DactArgs {
+    int64_t N, F;
+    int T;
+    const void* dY;
+    int64_t lddy;
+    const void* Z;
+    int64_t ldz;
+    void* dZ;
+    int rest;
+    void* db[kMaxG];           // db[0] NULL: not wanted
+    float* part;
+};
+size_t dact_part_bytes(int64_t N, int64_t F);
+tpmlp_status run_dact(int f32, int act, const DactArgs& a, cudaStream_t s);
+
+// Clipped policy loss of the given tokens; what is NULL is not computed: loss
+// (with logprob and kl) is the forward, dlogits the gradient, which alone takes
+// p from the forward's logprob_in, where that is precise enough.
+struct PolicyArgs {
+    const void* logits;
+    int64_t ld, N, V;
+    const int64_t* targets;        // negative: no token
+    const float* old_logprobs;
+    const float* advantages;
+    const float* ref_logprobs;     // NULL: no KL term
+    float kl_coef, low, high, tau;
+    float* loss;
+    float* logprob;
+    float* kl;
+    const float* logprob_in;
+    const float* grad_tokens;
+    float grad_scale;
+    void* dlogits;
+    int64_t ldd;
+};
+tpmlp_status run_vocab_policy(int f32, const PolicyArgs& a, cudaStream_t s);
+
 tpmlp_status run_selftest_wait(uint64_t timeout_ns, cudaStream_t s);
 
 // ---- services of the API translation unit --------------------------------
