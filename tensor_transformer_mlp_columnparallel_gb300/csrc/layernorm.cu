@@ -8,9 +8,12 @@
 // Memory bounds both: a row's elements are read once and written once. The
 // variance is taken around the row's own mean (a second pass over the elements
 // a thread holds), never as a difference of squares. The fp32 mean m of a row
-// far from zero is off by up to 2^-24 |m|, which is not small next to the row's
-// spread; what it is off by, d = sum (x - m) / D, is known to many digits, so
-// every use of the mean is (x - m) - d.
+// far from zero is off by its sum's rounding, which is not small next to the
+// row's spread; what it is off by, d = sum (x - m) / D, is known to many digits
+// (x - m is exact where x and m are near), so every use of the mean is
+// (x - m) - d. A row whose mean is within its spread takes d = 0: its m is
+// better than such a d, which would hold m's own digits cut to those of x (bf16
+// rows around zero, the mean's relative error 2e-6 instead of 4e-8).
 #include <cuda_bf16.h>
 
 #include "access.cuh"
@@ -85,8 +88,9 @@ __device__ __forceinline__ RowStats row_stats(int64_t D, float eps, float2* red,
             q = fmaf(t, t, q);
         });
         const float2 t = row_sum2<NT>(c, q, red);
-        s.d = t.x * inv;
-        var = fmaxf(fmaf(-s.d, s.d, t.y * inv), 0.f);
+        var = t.y * inv;
+        s.d = s.m * s.m > var ? t.x * inv : 0.f;
+        var = fmaxf(fmaf(-s.d, s.d, var), 0.f);
         if (t.y != t.y) var = t.y;   // (the maximum would drop a NaN)
     };
     take();
@@ -254,7 +258,7 @@ __global__ void __launch_bounds__(256) norm_grad_rows_kernel(const NormGradArgs 
     }
     const float inv = 1.f / (float)a.D;
     const float2 p = row_sum2<256>(su, suh, red);
-    const float d = row_sum2<256>(sh, 0.f, red).x * inv;
+    const float off = row_sum2<256>(sh, 0.f, red).x * inv, d = fabsf(m * r) > 1.f ? off : 0.f;
     if (threadIdx.x == 0) a.rows[row] = make_float4(p.x * inv, fmaf(-d, p.x, p.y) * inv, d, 0.f);
 }
 
