@@ -16,6 +16,8 @@
 // rows around zero, the mean's relative error 2e-6 instead of 4e-8).
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "access.cuh"
 #include "ptx.cuh"
 #include "tpmlp_internal.h"
@@ -26,43 +28,48 @@ namespace {
 constexpr int HELD_WORDS = 32;   // 32-bit registers of a row that a thread holds
 constexpr int WIDEST = 1024;     // threads of the widest row
 
-template <int NT> __device__ __forceinline__ float2 row_sum2(float a, float b, float2* red) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, off);
-        b += __shfl_xor_sync(0xffffffffu, b, off);
-    }
-    if constexpr (NT > 32) {
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        __syncthreads();   // red may hold an earlier sum
-        if (lane == 0) red[warp] = make_float2(a, b);
-        __syncthreads();
-        const float2 p = lane < NT / 32 ? red[lane] : make_float2(0.f, 0.f);
-        a = p.x;
-        b = p.y;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-            a += __shfl_xor_sync(0xffffffffu, a, off);
-            b += __shfl_xor_sync(0xffffffffu, b, off);
-        }
-    }
-    return make_float2(a, b);
+// Rows in turn: CTAs that stay, of as many groups of nt threads (32 to 512) as a
+// row needs at ELEMS elements a thread. A thread keeps its columns' parameters
+// in registers, and its elements of the next rows are on their way to places of
+// its own in shared memory (no barrier between the copy and its use).
+constexpr int STAY = 512;        // threads of such a CTA
+constexpr int ELEMS = 16;
+
+__host__ __device__ __forceinline__ int group_threads(int64_t D) {
+    int nt = 32;
+    while (nt * ELEMS < D) nt *= 2;
+    return nt;
 }
 
-template <int NT> __device__ __forceinline__ float row_max(float a, float2* red) {
+// Sums over a group of nt threads (whole warps, a power of two of them), in every
+// thread of it. red: where the CTA's warps put theirs; not the place that the
+// sum before used, so that one barrier is enough.
+template <int V, typename Op>
+__device__ __forceinline__ void group_reduce(float (&v)[V], int nt, int group, float (*red)[V], Op op) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, off));
-    if constexpr (NT > 32) {
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        __syncthreads();
-        if (lane == 0) red[warp].x = a;
-        __syncthreads();
-        a = lane < NT / 32 ? red[lane].x : 0.f;
+    for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, off));
+        for (int k = 0; k < V; ++k) v[k] = op(v[k], __shfl_xor_sync(0xffffffffu, v[k], off));
+    if (nt > 32) {
+        const int warps = nt / 32, lane = threadIdx.x & 31, warp = (threadIdx.x / 32) & (warps - 1);
+        red += group * warps;
+        if (lane == 0)
+#pragma unroll
+            for (int k = 0; k < V; ++k) red[warp][k] = v[k];
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(nt) : "memory");
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[k] = red[lane & (warps - 1)][k];
+        for (int off = warps / 2; off > 0; off >>= 1)
+#pragma unroll
+            for (int k = 0; k < V; ++k) v[k] = op(v[k], __shfl_xor_sync(0xffffffffu, v[k], off));
     }
-    return a;
 }
+struct Add {
+    __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+struct Max {
+    __device__ __forceinline__ float operator()(float a, float b) const { return max_nan(a, b); }
+};
 
 // A row's statistics: x scaled by `scale` (1 but for rows whose squares
 // overflow) has mean m + d and reciprocal deviation r.
@@ -71,34 +78,35 @@ struct RowStats {
     __device__ __forceinline__ float normal(float x) const { return (x * scale - m - d) * r; }
 };
 
-// each(f) calls f for every element of the row that this thread looks after.
-template <int NT, typename Each>
-__device__ __forceinline__ RowStats row_stats(int64_t D, float eps, float2* red, Each each) {
-    const float inv = 1.f / (float)D;
+using Red = float (*)[WIDEST / 32][2];   // three places for the warps' numbers
+
+// inv = 1 / D; each(f) calls f for every element of the row that this thread looks after.
+template <typename Each>
+__device__ __forceinline__ RowStats row_stats(float inv, float eps, int nt, int group, Red red, Each each) {
     RowStats s{1.f, 0.f, 0.f, 0.f};
     float var = 0.f;
     auto take = [&]() {
-        float a = 0.f;
-        each([&](float x) { a += x * s.scale; });
-        s.m = row_sum2<NT>(a, 0.f, red).x * inv;
-        float c = 0.f, q = 0.f;
+        float a[2] = {0.f, 0.f};
+        each([&](float x) { a[0] += x * s.scale; });
+        group_reduce(a, nt, group, red[0], Add());
+        s.m = a[0] * inv;
+        float c[2] = {0.f, 0.f};
         each([&](float x) {
             const float t = x * s.scale - s.m;
-            c += t;
-            q = fmaf(t, t, q);
+            c[0] += t;
+            c[1] = fmaf(t, t, c[1]);
         });
-        const float2 t = row_sum2<NT>(c, q, red);
-        var = t.y * inv;
-        s.d = s.m * s.m > var ? t.x * inv : 0.f;
-        var = fmaxf(fmaf(-s.d, s.d, var), 0.f);
-        if (t.y != t.y) var = t.y;   // (the maximum would drop a NaN)
+        group_reduce(c, nt, group, red[1], Add());
+        var = c[1] * inv;
+        s.d = s.m * s.m > var ? c[0] * inv : 0.f;
+        var = max_nan(fmaf(-s.d, s.d, var), 0.f);
     };
     take();
     if (!(var < INFINITY)) {   // the same for every thread of the row
-        float big = 0.f;
-        each([&](float x) { big = max_nan(big, fabsf(x)); });
-        big = row_max<NT>(big, red);
-        if (big < INFINITY) {   // finite elements: their squares overflowed
+        float big[2] = {0.f, 0.f};
+        each([&](float x) { big[0] = max_nan(big[0], fabsf(x)); });
+        group_reduce(big, nt, group, red[2], Max());
+        if (big[0] < INFINITY) {   // finite elements: their squares overflowed
             s.scale = 0x1p-100f;
             take();
         }
@@ -106,6 +114,42 @@ __device__ __forceinline__ RowStats row_stats(int64_t D, float eps, float2* red,
     s.r = 1.f / sqrtf(fmaf(eps * s.scale, s.scale, var));
     return s;
 }
+
+__device__ __forceinline__ void copy_async(void* dst, const uint4* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async(void* dst, const uint32_t* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async(void* dst, const unsigned short* src) {   // there is none of 2 bytes
+    *static_cast<unsigned short*>(dst) = *src;
+}
+
+// The rows ahead of a group, one matrix's or several's: access i of matrix q of a row
+// in stage k is at word ((k Q + q) R + i) STAY + thread.
+template <typename T, int B, int Q, int STAGES>
+struct RowRing {
+    using A = Access<T, B>;
+    using Word = typename A::Word;
+    static constexpr int R = ELEMS / A::N;
+    static constexpr int BYTES = STAGES * Q * R * STAY * B;
+    Word* place;
+    int t, nt, accesses;
+    __device__ __forceinline__ Word& at(int k, int q, int i) const { return place[((k * Q + q) * R + i) * STAY]; }
+    __device__ __forceinline__ bool mine(int i) const { return t + i * nt < accesses; }
+    __device__ __forceinline__ void fetch(int k, int q, const void* base, int64_t row, int64_t ld) const {
+        const Word* src = reinterpret_cast<const Word*>(static_cast<const T*>(base) + row * ld) + t;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (mine(i)) copy_async(&at(k, q, i), src + i * nt);
+    }
+    __device__ __forceinline__ void get(int k, int q, int i, float (&v)[A::N]) const { A::unpack(at(k, q, i), v); }
+    static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    // all but the last STAGES - 1 rows have arrived
+    static __device__ __forceinline__ void wait() {
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+    }
+};
 
 struct NormArgs {
     int64_t N, D;
@@ -128,7 +172,7 @@ __global__ void __launch_bounds__(NT < 128 ? 128 : NT) layernorm_kernel(const No
     using Word = typename A::Word;
     constexpr int R = B >= 4 ? HELD_WORDS * 4 / B : HELD_WORDS;
     constexpr int ROWS = NT < 128 ? 128 / NT : 1;
-    __shared__ float2 red[32];
+    __shared__ float red[3][WIDEST / 32][2];
     pdl_wait();
     pdl_launch_dependents();
     const int64_t row = (int64_t)blockIdx.x * ROWS + (ROWS > 1 ? threadIdx.x / NT : 0);
@@ -141,7 +185,7 @@ __global__ void __launch_bounds__(NT < 128 ? 128 : NT) layernorm_kernel(const No
 #pragma unroll
     for (int i = 0; i < R; ++i)
         if (t + i * NT < accesses) held[i] = x[t + i * NT];
-    const RowStats s = row_stats<NT>(a.D, a.eps, red, [&](auto f) {
+    const RowStats s = row_stats(1.f / (float)a.D, a.eps, NT, threadIdx.x / NT, red, [&](auto f) {
 #pragma unroll
         for (int i = 0; i < R; ++i)
             if (t + i * NT < accesses) {
@@ -170,19 +214,84 @@ __global__ void __launch_bounds__(NT < 128 ? 128 : NT) layernorm_kernel(const No
     }
 }
 
+// Many rows of up to STAY * ELEMS elements.
+constexpr int AHEAD = 3;   // stages of the forward's ring
+
+template <typename T, typename W, int B>
+__global__ void __launch_bounds__(STAY, 2) layernorm_stay_kernel(const NormArgs a, int nt) {
+    using Ring = RowRing<T, B, 1, AHEAD>;
+    using A = typename Ring::A;
+    using Word = typename Ring::Word;
+    constexpr int R = Ring::R;
+    extern __shared__ uint4 ring_memory[];
+    __shared__ float red[3][WIDEST / 32][2];
+    const int groups = STAY / nt, group = threadIdx.x / nt, t = threadIdx.x & (nt - 1);
+    const Ring ring{reinterpret_cast<Word*>(ring_memory) + threadIdx.x, t, nt, (int)(a.D / A::N)};
+    const int64_t step = (int64_t)gridDim.x * groups, first = (int64_t)blockIdx.x * groups + group;
+    pdl_wait();
+    pdl_launch_dependents();
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+        if (first + k * step < a.N) ring.fetch(k, 0, a.x, first + k * step, a.ldx);
+        ring.commit();
+    }
+    float w[R][A::N], b[R][A::N];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+#pragma unroll
+        for (int j = 0; j < A::N; ++j) w[i][j] = 1.f, b[i][j] = 0.f;
+        if (ring.mine(i)) {
+            if (a.w) load_params<W, A::N>(static_cast<const W*>(a.w) + (t + i * nt) * A::N, w[i]);
+            if (a.b) load_params<W, A::N>(static_cast<const W*>(a.b) + (t + i * nt) * A::N, b[i]);
+        }
+    }
+    const float inv = 1.f / (float)a.D;
+    int k = 0;
+    for (int64_t row = first; row < a.N; row += step) {
+        ring.wait();
+        const RowStats s = row_stats(inv, a.eps, nt, group, red, [&](auto f) {
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                if (ring.mine(i)) {
+                    float v[A::N];
+                    ring.get(k, 0, i, v);
+#pragma unroll
+                    for (int j = 0; j < A::N; ++j) f(v[j]);
+                }
+        });
+        Word* y = reinterpret_cast<Word*>(static_cast<T*>(a.y) + row * a.ldy) + t;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (ring.mine(i)) {
+                float v[A::N];
+                ring.get(k, 0, i, v);
+#pragma unroll
+                for (int j = 0; j < A::N; ++j) v[j] = fmaf(s.normal(v[j]), w[i][j], b[i][j]);
+                y[i * nt] = A::pack(v);
+            }
+        if (t == 0) {
+            if (a.mean) a.mean[row] = (s.m + s.d) / s.scale;
+            if (a.rstd) a.rstd[row] = s.r * s.scale;
+        }
+        if (row + AHEAD * step < a.N) ring.fetch(k, 0, a.x, row + AHEAD * step, a.ldx);
+        ring.commit();
+        k = k == AHEAD - 1 ? 0 : k + 1;
+    }
+}
+
 // A row of any length, read three times (from L2 but for the first).
 template <typename T, typename W, int B>
 __global__ void __launch_bounds__(WIDEST) layernorm_long_kernel(const NormArgs a) {
     using A = Access<T, B>;
     using Word = typename A::Word;
-    __shared__ float2 red[32];
+    __shared__ float red[3][WIDEST / 32][2];
     pdl_wait();
     pdl_launch_dependents();
     const int64_t row = blockIdx.x;
     const int64_t accesses = a.D / A::N;
     const Word* x = reinterpret_cast<const Word*>(static_cast<const T*>(a.x) + row * a.ldx);
     Word* y = reinterpret_cast<Word*>(static_cast<T*>(a.y) + row * a.ldy);
-    const RowStats s = row_stats<WIDEST>(a.D, a.eps, red, [&](auto f) {
+    const RowStats s = row_stats(1.f / (float)a.D, a.eps, WIDEST, 0, red, [&](auto f) {
 #pragma unroll 4
         for (int64_t at = threadIdx.x; at < accesses; at += WIDEST) {
             float v[A::N];
@@ -228,12 +337,139 @@ struct NormGradArgs {
     int S;
 };
 
+template <typename T> constexpr int GRAD_AHEAD = sizeof(T) == 2 ? 4 : 2;   // stages: 192 KB
+
+// All of it in one reading, for rows of up to STAY * ELEMS elements: a thread
+// keeps its columns' sums of dy h and dy over the rows of its group; a CTA's
+// sums go to part[blockIdx.x] (with one CTA to dw and db).
+template <typename T, typename W, int B>
+__global__ void __launch_bounds__(STAY, 1) norm_grad_kernel(const NormGradArgs a, int nt) {
+    using Ring = RowRing<T, B, 3, GRAD_AHEAD<T>>;
+    using A = typename Ring::A;
+    using Word = typename Ring::Word;
+    constexpr int R = Ring::R;
+    extern __shared__ uint4 ring_memory[];
+    __shared__ float red[2][STAY / 32][3];
+    const int groups = STAY / nt, group = threadIdx.x / nt, t = threadIdx.x & (nt - 1);
+    const Ring ring{reinterpret_cast<Word*>(ring_memory) + threadIdx.x, t, nt, (int)(a.D / A::N)};
+    const int64_t step = (int64_t)gridDim.x * groups, first = (int64_t)blockIdx.x * groups + group;
+    pdl_wait();
+    pdl_launch_dependents();
+    auto fetch = [&](int k, int64_t row) {
+        if (row < a.N) {
+            ring.fetch(k, 0, a.x, row, a.ldx);
+            ring.fetch(k, 1, a.dy, row, a.lddy);
+            if (a.dres) ring.fetch(k, 2, a.dres, row, a.lddres);
+        }
+        ring.commit();
+    };
+#pragma unroll
+    for (int k = 0; k < GRAD_AHEAD<T>; ++k) fetch(k, first + k * step);
+    float w[R][A::N], sw[R][A::N], sb[R][A::N];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+#pragma unroll
+        for (int j = 0; j < A::N; ++j) w[i][j] = 1.f, sw[i][j] = sb[i][j] = 0.f;
+        if (a.w && ring.mine(i)) load_params<W, A::N>(static_cast<const W*>(a.w) + (t + i * nt) * A::N, w[i]);
+    }
+    const float inv = 1.f / (float)a.D;
+    float m = 0.f, r = 0.f;
+    if (first < a.N) m = a.mean[first], r = a.rstd[first];
+    int k = 0, turn = 0;
+    for (int64_t row = first; row < a.N; row += step, turn ^= 1) {
+        const float cm = m, cr = r;
+        if (row + step < a.N) m = a.mean[row + step], r = a.rstd[row + step];
+        ring.wait();
+        float s[3] = {0.f, 0.f, 0.f};   // u, u h, h
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (ring.mine(i)) {
+                float v[A::N], y[A::N];
+                ring.get(k, 0, i, v);
+                ring.get(k, 1, i, y);
+#pragma unroll
+                for (int j = 0; j < A::N; ++j) {
+                    const float h = (v[j] - cm) * cr, u = y[j] * w[i][j];
+                    s[0] += u;
+                    s[1] = fmaf(u, h, s[1]);
+                    s[2] += h;
+                }
+            }
+        group_reduce(s, nt, group, red[turn], Add());
+        const float d = fabsf(cm * cr) > 1.f ? s[2] * inv : 0.f;
+        const float c1 = s[0] * inv, c2 = fmaf(-d, s[0], s[1]) * inv;
+        Word* out = reinterpret_cast<Word*>(static_cast<T*>(a.dx) + row * a.lddx) + t;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (ring.mine(i)) {
+                float v[A::N], y[A::N], z[A::N];
+                ring.get(k, 0, i, v);
+                ring.get(k, 1, i, y);
+                if (a.dres) ring.get(k, 2, i, z);
+#pragma unroll
+                for (int j = 0; j < A::N; ++j) {
+                    const float h = fmaf(v[j] - cm, cr, -d);
+                    sw[i][j] = fmaf(y[j], h, sw[i][j]);
+                    sb[i][j] += y[j];
+                    v[j] = cr * fmaf(-h, c2, fmaf(y[j], w[i][j], -c1));
+                    if (a.dres) v[j] += z[j];
+                }
+                out[i * nt] = A::pack(v);
+            }
+        fetch(k, row + GRAD_AHEAD<T> * step);
+        k = k == GRAD_AHEAD<T> - 1 ? 0 : k + 1;
+    }
+    if (a.dw == nullptr) return;
+    if (groups > 1) {   // the groups' sums in their order, through the ring's memory
+        float* sums = reinterpret_cast<float*>(ring_memory);
+        static_assert(2 * STAY / 2 * ELEMS * sizeof(float) <= Ring::BYTES, "room for two sums a column");
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        for (int q = 0; q < groups; ++q) {
+            __syncthreads();
+            if (group == q)
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    if (ring.mine(i))
+#pragma unroll
+                        for (int j = 0; j < A::N; ++j) {
+                            float* at = sums + 2 * ((t + i * nt) * A::N + j);
+                            if (q > 0) {
+                                sw[i][j] += at[0];
+                                sb[i][j] += at[1];
+                            }
+                            at[0] = sw[i][j];
+                            at[1] = sb[i][j];
+                        }
+        }
+        if (group != groups - 1) return;   // the last group has them all
+    }
+    float* p = a.part + (int64_t)blockIdx.x * 2 * a.D;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (ring.mine(i))
+#pragma unroll
+            for (int j = 0; j < A::N; ++j) {
+                const int c = (t + i * nt) * A::N + j;
+                if (gridDim.x > 1) {
+                    p[c] = sw[i][j];
+                    p[a.D + c] = sb[i][j];
+                } else if constexpr (sizeof(W) == 4) {
+                    static_cast<W*>(a.dw)[c] = sw[i][j];
+                    static_cast<W*>(a.db)[c] = sb[i][j];
+                } else {
+                    static_cast<W*>(a.dw)[c] = __float2bfloat16_rn(sw[i][j]);
+                    static_cast<W*>(a.db)[c] = __float2bfloat16_rn(sb[i][j]);
+                }
+            }
+}
+
+// Longer rows are read twice.
 // Sums over a row, one CTA each.
 template <typename T, typename W, int B>
 __global__ void __launch_bounds__(256) norm_grad_rows_kernel(const NormGradArgs a) {
     using A = Access<T, B>;
     using Word = typename A::Word;
-    __shared__ float2 red[32];
+    __shared__ float red[256 / 32][3];
     pdl_wait();
     pdl_launch_dependents();
     const int64_t row = blockIdx.x;
@@ -241,7 +477,7 @@ __global__ void __launch_bounds__(256) norm_grad_rows_kernel(const NormGradArgs 
     const Word* x = reinterpret_cast<const Word*>(static_cast<const T*>(a.x) + row * a.ldx);
     const Word* dy = reinterpret_cast<const Word*>(static_cast<const T*>(a.dy) + row * a.lddy);
     const float m = a.mean[row], r = a.rstd[row];
-    float su = 0.f, suh = 0.f, sh = 0.f;
+    float s[3] = {0.f, 0.f, 0.f};   // u, u h, h
 #pragma unroll 2
     for (int64_t at = threadIdx.x; at < accesses; at += 256) {
         float v[A::N], g[A::N], w[A::N];
@@ -251,15 +487,15 @@ __global__ void __launch_bounds__(256) norm_grad_rows_kernel(const NormGradArgs 
 #pragma unroll
         for (int j = 0; j < A::N; ++j) {
             const float h = (v[j] - m) * r, u = a.w ? g[j] * w[j] : g[j];
-            su += u;
-            suh = fmaf(u, h, suh);
-            sh += h;
+            s[0] += u;
+            s[1] = fmaf(u, h, s[1]);
+            s[2] += h;
         }
     }
     const float inv = 1.f / (float)a.D;
-    const float2 p = row_sum2<256>(su, suh, red);
-    const float off = row_sum2<256>(sh, 0.f, red).x * inv, d = fabsf(m * r) > 1.f ? off : 0.f;
-    if (threadIdx.x == 0) a.rows[row] = make_float4(p.x * inv, fmaf(-d, p.x, p.y) * inv, d, 0.f);
+    group_reduce(s, 256, 0, red, Add());
+    const float d = fabsf(m * r) > 1.f ? s[2] * inv : 0.f;
+    if (threadIdx.x == 0) a.rows[row] = make_float4(s[0] * inv, fmaf(-d, s[0], s[1]) * inv, d, 0.f);
 }
 
 // dx, and a row chunk's column sums: a thread has one access's columns.
@@ -335,11 +571,12 @@ __global__ void __launch_bounds__(256) norm_grad_params_kernel(const NormGradArg
 }
 
 template <typename... P, typename... A>
-tpmlp_status launch(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, A... args) {
+tpmlp_status launch_smem(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
@@ -349,11 +586,39 @@ tpmlp_status launch(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s
     return cudaGetLastError() == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
 }
 
+template <typename... P, typename... A>
+tpmlp_status launch(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, A... args) {
+    return launch_smem(kernel, grid, threads, 0, s, args...);
+}
+
+// The kernel may use `bytes` of dynamic shared memory: asked for once a device
+// (`asked`: one bit each; devices beyond ask every time).
+template <typename K>
+bool allow_smem(K kernel, int bytes, std::atomic<uint64_t>& asked) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (asked.load() & bit) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    asked.fetch_or(bit);
+    return true;
+}
+
 template <typename T, typename W, int B>
 tpmlp_status forward(const NormArgs& a, cudaStream_t s) {
     constexpr int R = B >= 4 ? HELD_WORDS * 4 / B : HELD_WORDS;
     const int64_t accesses = a.D / (B / (int)sizeof(T));
     LaunchScope ls("layernorm", s);
+    if (a.D <= STAY * ELEMS) {
+        const int nt = group_threads(a.D);
+        const int64_t turns = (a.N + STAY / nt - 1) / (STAY / nt), most = 2LL * device_sm_count();
+        if (turns > most) {
+            constexpr int BYTES = RowRing<T, B, 1, AHEAD>::BYTES;
+            static std::atomic<uint64_t> asked{0};
+            if (!allow_smem(layernorm_stay_kernel<T, W, B>, BYTES, asked)) return TPMLP_ERR_CUDA;
+            return launch_smem(layernorm_stay_kernel<T, W, B>, dim3((unsigned)most), STAY, BYTES, s, a, nt);
+        }
+    }
     if (accesses <= 32 * R)
         return launch(layernorm_kernel<T, W, B, 32>, dim3((unsigned)((a.N + 3) / 4)), 128, s, a);
     if (accesses <= 128 * R) return launch(layernorm_kernel<T, W, B, 128>, dim3((unsigned)a.N), 128, s, a);
@@ -384,9 +649,23 @@ int64_t row_chunks(int64_t N, int64_t D) {
     return S < 1 ? 1 : S > 1024 ? 1024 : S;
 }
 
+constexpr int MOST_CTAS = 152;   // that stay, of the backward: one an SM
+
 template <typename T, typename W, int B>
-tpmlp_status backward(const NormGradArgs& a, cudaStream_t s) {
+tpmlp_status backward(NormGradArgs a, cudaStream_t s) {
     LaunchScope ls("layernorm_backward", s);
+    if (a.D <= STAY * ELEMS) {
+        const int nt = group_threads(a.D);
+        const int64_t turns = (a.N + STAY / nt - 1) / (STAY / nt);
+        a.S = (int)(turns < MOST_CTAS ? turns : MOST_CTAS);
+        constexpr int BYTES = RowRing<T, B, 3, GRAD_AHEAD<T>>::BYTES;
+        static std::atomic<uint64_t> asked{0};
+        if (!allow_smem(norm_grad_kernel<T, W, B>, BYTES, asked)) return TPMLP_ERR_CUDA;
+        const tpmlp_status st =
+            launch_smem(norm_grad_kernel<T, W, B>, dim3((unsigned)a.S), STAY, BYTES, s, a, nt);
+        if (st != TPMLP_OK || a.part == nullptr || a.S == 1) return st;
+        return launch(norm_grad_params_kernel<W>, dim3((unsigned)((2 * a.D + 31) / 32)), 256, s, a);
+    }
     const int64_t accesses = a.D / (B / (int)sizeof(T));
     tpmlp_status st = launch(norm_grad_rows_kernel<T, W, B>, dim3((unsigned)a.N), 256, s, a);
     if (st != TPMLP_OK) return st;
@@ -422,7 +701,9 @@ tpmlp_status run_layernorm(int f32, int params_f32, const LayernormArgs& g, cuda
 }
 
 size_t layernorm_backward_bytes(int64_t N, int64_t D) {
-    return N == 0 ? 0 : rows_bytes(N) + (size_t)row_chunks(N, D) * 2 * (size_t)D * sizeof(float);
+    if (N == 0) return 0;
+    const int64_t S = D <= STAY * ELEMS ? MOST_CTAS : row_chunks(N, D);
+    return rows_bytes(N) + (size_t)S * 2 * (size_t)D * sizeof(float);
 }
 
 tpmlp_status run_layernorm_backward(int f32, int params_f32, const LayernormGradArgs& g, void* workspace,
