@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "act.cuh"
+#include "f32x2.cuh"
 
 namespace tpmlp {
 
@@ -15,6 +16,9 @@ template <> struct AccessWord<16> { using type = uint4; };
 template <> struct AccessWord<8> { using type = uint2; };
 template <> struct AccessWord<4> { using type = uint32_t; };
 template <> struct AccessWord<2> { using type = unsigned short; };
+
+template <int N> struct PairOf { using type = F2; };
+template <> struct PairOf<1> { using type = float; };
 
 // N elements of T in one access of B bytes.
 template <typename T, int B>
@@ -39,6 +43,31 @@ struct Access {
             }
         }
     }
+    // the same as packed pairs (a single element: as itself)
+    using Pair = typename PairOf<N>::type;
+    static constexpr int PAIRS = N > 1 ? N / 2 : 1;
+    static __device__ __forceinline__ Pair both(float x) {
+        if constexpr (N > 1) return f2(x, x);
+        else return x;
+    }
+    static __device__ __forceinline__ void unpack(const Word& x, F2 (&v)[N > 1 ? PAIRS : 2]) {
+        float e[N];
+        unpack(x, e);
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) v[j] = f2(e[2 * j], e[2 * j + 1]);
+    }
+    static __device__ __forceinline__ Word pack(const F2 (&v)[N > 1 ? PAIRS : 2]) {
+        float e[N];
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) split2(v[j], e[2 * j], e[2 * j + 1]);
+        return pack(e);
+    }
+    static __device__ __forceinline__ float total(F2 v) {   // of a sum kept in pairs
+        float a, b;
+        split2(v, a, b);
+        return a + b;
+    }
+    static __device__ __forceinline__ float total(float v) { return v; }
     static __device__ __forceinline__ Word pack(const float (&v)[N]) {
         Word x;
         if constexpr (sizeof(T) == 4) {
@@ -69,6 +98,14 @@ __device__ __forceinline__ void load_params(const T* p, float (&v)[N]) {
 #pragma unroll
         for (int j = 0; j < A::N; ++j) v[k * A::N + j] = t[j];
     }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void load_params(const T* p, F2 (&v)[N / 2]) {
+    float e[N];
+    load_params<T, N>(p, e);
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) v[j] = f2(e[2 * j], e[2 * j + 1]);
 }
 
 // Host side: whether accesses of `bytes` fit an address and (for several rows)

@@ -10,13 +10,14 @@
 // a thread holds), never as a difference of squares. The fp32 mean m of a row
 // far from zero is off by its sum's rounding, which is not small next to the
 // row's spread; what it is off by, d = sum (x - m) / D, is known to many digits
-// (x - m is exact where x and m are near), so every use of the mean is
-// (x - m) - d. A row whose mean is within its spread takes d = 0: its m is
-// better than such a d, which would hold m's own digits cut to those of x (bf16
-// rows around zero, the mean's relative error 2e-6 instead of 4e-8).
+// (x - m is exact where x and m are near), so such a row takes (x - m) - d. A row
+// whose mean is within its spread takes d = 0: its m is better than such a d,
+// which would hold m's own digits cut to those of x (bf16 rows around zero, the
+// mean's relative error 2e-6 instead of 4e-8).
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "access.cuh"
 #include "ptx.cuh"
@@ -25,41 +26,41 @@
 namespace tpmlp {
 namespace {
 
-constexpr int HELD_WORDS = 32;   // 32-bit registers of a row that a thread holds
+constexpr int HELD_WORDS = 32;   // 32-bit registers of a row that a thread of layernorm_kernel holds
 constexpr int WIDEST = 1024;     // threads of the widest row
+constexpr int LONGEST = 8192;    // elements of a row that is taken in turn
+constexpr int NORM_THREADS = 256, GRAD_THREADS = 512;   // of a CTA that does; LONGEST / threads elements a thread
+constexpr int MOST_CTAS = 152;   // of the backward's CTAs that stay: one an SM
 
-// Rows in turn: CTAs that stay, of as many groups of nt threads (32 to 512) as a
-// row needs at ELEMS elements a thread. A thread keeps its columns' parameters
-// in registers, and its elements of the next rows are on their way to places of
-// its own in shared memory (no barrier between the copy and its use).
-constexpr int STAY = 512;        // threads of such a CTA
-constexpr int ELEMS = 16;
-
-__host__ __device__ __forceinline__ int group_threads(int64_t D) {
-    int nt = 32;
-    while (nt * ELEMS < D) nt *= 2;
-    return nt;
+// A barrier of a group of NT threads (whole warps).
+template <int NT> __device__ __forceinline__ void group_sync(int group) {
+    if constexpr (NT > 32)
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(NT) : "memory");
+    else
+        __syncwarp();
 }
 
-// Sums over a group of nt threads (whole warps, a power of two of them), in every
-// thread of it. red: where the CTA's warps put theirs; not the place that the
-// sum before used, so that one barrier is enough.
-template <int V, typename Op>
-__device__ __forceinline__ void group_reduce(float (&v)[V], int nt, int group, float (*red)[V], Op op) {
+// Sums (maxima) of V numbers over a group of NT threads (a power of two up to
+// 1024), in every one of them. red: where the CTA's warps put theirs; not the
+// place that the sum before used, so that one barrier is enough.
+template <int NT, int V, typename Op>
+__device__ __forceinline__ void group_reduce(float (&v)[V], int group, float (*red)[V], Op op) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
         for (int k = 0; k < V; ++k) v[k] = op(v[k], __shfl_xor_sync(0xffffffffu, v[k], off));
-    if (nt > 32) {
-        const int warps = nt / 32, lane = threadIdx.x & 31, warp = (threadIdx.x / 32) & (warps - 1);
-        red += group * warps;
+    if constexpr (NT > 32) {
+        constexpr int WARPS = NT / 32;
+        const int lane = threadIdx.x & 31, warp = (threadIdx.x / 32) & (WARPS - 1);
+        red += group * WARPS;
         if (lane == 0)
 #pragma unroll
             for (int k = 0; k < V; ++k) red[warp][k] = v[k];
-        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(nt) : "memory");
+        group_sync<NT>(group);
 #pragma unroll
-        for (int k = 0; k < V; ++k) v[k] = red[lane & (warps - 1)][k];
-        for (int off = warps / 2; off > 0; off >>= 1)
+        for (int k = 0; k < V; ++k) v[k] = red[lane & (WARPS - 1)][k];
+#pragma unroll
+        for (int off = WARPS / 2; off > 0; off >>= 1)
 #pragma unroll
             for (int k = 0; k < V; ++k) v[k] = op(v[k], __shfl_xor_sync(0xffffffffu, v[k], off));
     }
@@ -69,86 +70,6 @@ struct Add {
 };
 struct Max {
     __device__ __forceinline__ float operator()(float a, float b) const { return max_nan(a, b); }
-};
-
-// A row's statistics: x scaled by `scale` (1 but for rows whose squares
-// overflow) has mean m + d and reciprocal deviation r.
-struct RowStats {
-    float scale, m, d, r;
-    __device__ __forceinline__ float normal(float x) const { return (x * scale - m - d) * r; }
-};
-
-using Red = float (*)[WIDEST / 32][2];   // three places for the warps' numbers
-
-// inv = 1 / D; each(f) calls f for every element of the row that this thread looks after.
-template <typename Each>
-__device__ __forceinline__ RowStats row_stats(float inv, float eps, int nt, int group, Red red, Each each) {
-    RowStats s{1.f, 0.f, 0.f, 0.f};
-    float var = 0.f;
-    auto take = [&]() {
-        float a[2] = {0.f, 0.f};
-        each([&](float x) { a[0] += x * s.scale; });
-        group_reduce(a, nt, group, red[0], Add());
-        s.m = a[0] * inv;
-        float c[2] = {0.f, 0.f};
-        each([&](float x) {
-            const float t = x * s.scale - s.m;
-            c[0] += t;
-            c[1] = fmaf(t, t, c[1]);
-        });
-        group_reduce(c, nt, group, red[1], Add());
-        var = c[1] * inv;
-        s.d = s.m * s.m > var ? c[0] * inv : 0.f;
-        var = max_nan(fmaf(-s.d, s.d, var), 0.f);
-    };
-    take();
-    if (!(var < INFINITY)) {   // the same for every thread of the row
-        float big[2] = {0.f, 0.f};
-        each([&](float x) { big[0] = max_nan(big[0], fabsf(x)); });
-        group_reduce(big, nt, group, red[2], Max());
-        if (big[0] < INFINITY) {   // finite elements: their squares overflowed
-            s.scale = 0x1p-100f;
-            take();
-        }
-    }
-    s.r = 1.f / sqrtf(fmaf(eps * s.scale, s.scale, var));
-    return s;
-}
-
-__device__ __forceinline__ void copy_async(void* dst, const uint4* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_async(void* dst, const uint32_t* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_async(void* dst, const unsigned short* src) {   // there is none of 2 bytes
-    *static_cast<unsigned short*>(dst) = *src;
-}
-
-// The rows ahead of a group, one matrix's or several's: access i of matrix q of a row
-// in stage k is at word ((k Q + q) R + i) STAY + thread.
-template <typename T, int B, int Q, int STAGES>
-struct RowRing {
-    using A = Access<T, B>;
-    using Word = typename A::Word;
-    static constexpr int R = ELEMS / A::N;
-    static constexpr int BYTES = STAGES * Q * R * STAY * B;
-    Word* place;
-    int t, nt, accesses;
-    __device__ __forceinline__ Word& at(int k, int q, int i) const { return place[((k * Q + q) * R + i) * STAY]; }
-    __device__ __forceinline__ bool mine(int i) const { return t + i * nt < accesses; }
-    __device__ __forceinline__ void fetch(int k, int q, const void* base, int64_t row, int64_t ld) const {
-        const Word* src = reinterpret_cast<const Word*>(static_cast<const T*>(base) + row * ld) + t;
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-            if (mine(i)) copy_async(&at(k, q, i), src + i * nt);
-    }
-    __device__ __forceinline__ void get(int k, int q, int i, float (&v)[A::N]) const { A::unpack(at(k, q, i), v); }
-    static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-    // all but the last STAGES - 1 rows have arrived
-    static __device__ __forceinline__ void wait() {
-        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
-    }
 };
 
 struct NormArgs {
@@ -162,157 +83,405 @@ struct NormArgs {
     int64_t ldy;
     float* mean;     // NULL: not wanted
     float* rstd;
+    int* err;
+    uint64_t timeout_ns;
 };
 
-// A row in the registers of NT threads (a warp: four rows to a CTA), every
-// access of B bytes. One reading of the row whatever D, up to 32 words a thread.
+// A row's statistics: the row, times scale (1 but for rows whose squares
+// overflow, which the caller's rescale has multiplied by 2^-100), has mean m + d
+// and reciprocal deviation r.
+struct RowStats {
+    float scale, m, d, r;
+    __device__ __forceinline__ void write(const NormArgs& a, int64_t row) const {
+        if (a.mean) a.mean[row] = (m + d) / scale;
+        if (a.rstd) a.rstd[row] = r * scale;
+    }
+};
+
+// sum(): over the elements that this thread looks after; spread(m, v): of their
+// distances from m (v[0]) and those squared (v[1]); summed() runs once every
+// thread's first sum is in. Returns false where the squares overflow (or a NaN or
+// an infinity is in the row), the same for every thread of the row.
+using Red = float (*)[2];
+template <int NT, typename Sum, typename Spread, typename Summed>
+__device__ __forceinline__ bool row_stats(RowStats& s, int64_t D, float eps, int group, Red red, Sum sum, Spread spread,
+                                          Summed summed) {
+    const float inv = 1.f / (float)D;
+    float v[2] = {sum(), 0.f};
+    group_reduce<NT>(v, group, red, Add());
+    s.m = v[0] * inv;
+    summed();
+    v[0] = v[1] = 0.f;
+    spread(s.m, v);
+    group_reduce<NT>(v, group, red + WIDEST / 32, Add());
+    const float var = v[1] * inv;
+    s.d = s.m * s.m > var ? v[0] * inv : 0.f;
+    s.r = 1.f / sqrtf(fmaf(eps * s.scale, s.scale, max_nan(fmaf(-s.d, s.d, var), 0.f)));
+    return var < INFINITY;
+}
+
+// A row of any length, read three times (from L2 but for the first) by NT threads,
+// one access of B bytes at a time. Finite elements whose squares overflow are
+// taken times 2^-100.
 template <typename T, typename W, int B, int NT>
-__global__ void __launch_bounds__(NT < 128 ? 128 : NT) layernorm_kernel(const NormArgs a) {
+__device__ __forceinline__ void long_row(const NormArgs& a, int64_t row, int t, int group, float (*red)[2]) {
     using A = Access<T, B>;
     using Word = typename A::Word;
-    constexpr int R = B >= 4 ? HELD_WORDS * 4 / B : HELD_WORDS;
-    constexpr int ROWS = NT < 128 ? 128 / NT : 1;
-    __shared__ float red[3][WIDEST / 32][2];
-    pdl_wait();
-    pdl_launch_dependents();
-    const int64_t row = (int64_t)blockIdx.x * ROWS + (ROWS > 1 ? threadIdx.x / NT : 0);
-    if (row >= a.N) return;   // a whole warp
-    const int t = ROWS > 1 ? threadIdx.x % NT : threadIdx.x;
-    const int accesses = (int)(a.D / A::N);
-    const Word* x = reinterpret_cast<const Word*>(static_cast<const T*>(a.x) + row * a.ldx);
-    Word* y = reinterpret_cast<Word*>(static_cast<T*>(a.y) + row * a.ldy);
-    Word held[R];
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-        if (t + i * NT < accesses) held[i] = x[t + i * NT];
-    const RowStats s = row_stats(1.f / (float)a.D, a.eps, NT, threadIdx.x / NT, red, [&](auto f) {
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-            if (t + i * NT < accesses) {
-                float v[A::N];
-                A::unpack(held[i], v);
-#pragma unroll
-                for (int j = 0; j < A::N; ++j) f(v[j]);
-            }
-    });
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int at = t + i * NT;
-        if (at < accesses) {
-            float v[A::N], w[A::N], b[A::N];
-            A::unpack(held[i], v);
-            if (a.w) load_params<W, A::N>(static_cast<const W*>(a.w) + at * A::N, w);
-            if (a.b) load_params<W, A::N>(static_cast<const W*>(a.b) + at * A::N, b);
-#pragma unroll
-            for (int j = 0; j < A::N; ++j) v[j] = fmaf(s.normal(v[j]), a.w ? w[j] : 1.f, a.b ? b[j] : 0.f);
-            y[at] = A::pack(v);
-        }
-    }
-    if (t == 0) {
-        if (a.mean) a.mean[row] = (s.m + s.d) / s.scale;
-        if (a.rstd) a.rstd[row] = s.r * s.scale;
-    }
-}
-
-// Many rows of up to STAY * ELEMS elements.
-constexpr int AHEAD = 3;   // stages of the forward's ring
-
-template <typename T, typename W, int B>
-__global__ void __launch_bounds__(STAY, 2) layernorm_stay_kernel(const NormArgs a, int nt) {
-    using Ring = RowRing<T, B, 1, AHEAD>;
-    using A = typename Ring::A;
-    using Word = typename Ring::Word;
-    constexpr int R = Ring::R;
-    extern __shared__ uint4 ring_memory[];
-    __shared__ float red[3][WIDEST / 32][2];
-    const int groups = STAY / nt, group = threadIdx.x / nt, t = threadIdx.x & (nt - 1);
-    const Ring ring{reinterpret_cast<Word*>(ring_memory) + threadIdx.x, t, nt, (int)(a.D / A::N)};
-    const int64_t step = (int64_t)gridDim.x * groups, first = (int64_t)blockIdx.x * groups + group;
-    pdl_wait();
-    pdl_launch_dependents();
-#pragma unroll
-    for (int k = 0; k < AHEAD; ++k) {
-        if (first + k * step < a.N) ring.fetch(k, 0, a.x, first + k * step, a.ldx);
-        ring.commit();
-    }
-    float w[R][A::N], b[R][A::N];
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-#pragma unroll
-        for (int j = 0; j < A::N; ++j) w[i][j] = 1.f, b[i][j] = 0.f;
-        if (ring.mine(i)) {
-            if (a.w) load_params<W, A::N>(static_cast<const W*>(a.w) + (t + i * nt) * A::N, w[i]);
-            if (a.b) load_params<W, A::N>(static_cast<const W*>(a.b) + (t + i * nt) * A::N, b[i]);
-        }
-    }
-    const float inv = 1.f / (float)a.D;
-    int k = 0;
-    for (int64_t row = first; row < a.N; row += step) {
-        ring.wait();
-        const RowStats s = row_stats(inv, a.eps, nt, group, red, [&](auto f) {
-#pragma unroll
-            for (int i = 0; i < R; ++i)
-                if (ring.mine(i)) {
-                    float v[A::N];
-                    ring.get(k, 0, i, v);
-#pragma unroll
-                    for (int j = 0; j < A::N; ++j) f(v[j]);
-                }
-        });
-        Word* y = reinterpret_cast<Word*>(static_cast<T*>(a.y) + row * a.ldy) + t;
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-            if (ring.mine(i)) {
-                float v[A::N];
-                ring.get(k, 0, i, v);
-#pragma unroll
-                for (int j = 0; j < A::N; ++j) v[j] = fmaf(s.normal(v[j]), w[i][j], b[i][j]);
-                y[i * nt] = A::pack(v);
-            }
-        if (t == 0) {
-            if (a.mean) a.mean[row] = (s.m + s.d) / s.scale;
-            if (a.rstd) a.rstd[row] = s.r * s.scale;
-        }
-        if (row + AHEAD * step < a.N) ring.fetch(k, 0, a.x, row + AHEAD * step, a.ldx);
-        ring.commit();
-        k = k == AHEAD - 1 ? 0 : k + 1;
-    }
-}
-
-// A row of any length, read three times (from L2 but for the first).
-template <typename T, typename W, int B>
-__global__ void __launch_bounds__(WIDEST) layernorm_long_kernel(const NormArgs a) {
-    using A = Access<T, B>;
-    using Word = typename A::Word;
-    __shared__ float red[3][WIDEST / 32][2];
-    pdl_wait();
-    pdl_launch_dependents();
-    const int64_t row = blockIdx.x;
     const int64_t accesses = a.D / A::N;
     const Word* x = reinterpret_cast<const Word*>(static_cast<const T*>(a.x) + row * a.ldx);
     Word* y = reinterpret_cast<Word*>(static_cast<T*>(a.y) + row * a.ldy);
-    const RowStats s = row_stats(1.f / (float)a.D, a.eps, WIDEST, 0, red, [&](auto f) {
+    RowStats s{1.f, 0.f, 0.f, 0.f};
+    auto each = [&](auto f) {
 #pragma unroll 4
-        for (int64_t at = threadIdx.x; at < accesses; at += WIDEST) {
+        for (int64_t at = t; at < accesses; at += NT) {
             float v[A::N];
             A::unpack(x[at], v);
 #pragma unroll
-            for (int j = 0; j < A::N; ++j) f(v[j]);
+            for (int j = 0; j < A::N; ++j) f(v[j] * s.scale);
         }
-    });
-    for (int64_t at = threadIdx.x; at < accesses; at += WIDEST) {
+    };
+    auto take = [&] {
+        return row_stats<NT>(
+            s, a.D, a.eps, group, red,
+            [&] {
+                float c = 0.f;
+                each([&](float v) { c += v; });
+                return c;
+            },
+            [&](float m, float (&v)[2]) {
+                each([&](float e) {
+                    v[0] += e - m;
+                    v[1] = fmaf(e - m, e - m, v[1]);
+                });
+            },
+            [] {});
+    };
+    if (!take()) {
+        float big[2] = {0.f, 0.f};
+        each([&](float v) { big[0] = max_nan(big[0], fabsf(v)); });
+        group_reduce<NT>(big, group, red + 2 * (WIDEST / 32), Max());
+        if (big[0] < INFINITY) {
+            s.scale = 0x1p-100f;
+            take();
+        }
+    }
+    const float dr = -s.d * s.r;
+    for (int64_t at = t; at < accesses; at += NT) {
         float v[A::N], w[A::N], b[A::N];
         A::unpack(x[at], v);
         if (a.w) load_params<W, A::N>(static_cast<const W*>(a.w) + at * A::N, w);
         if (a.b) load_params<W, A::N>(static_cast<const W*>(a.b) + at * A::N, b);
 #pragma unroll
-        for (int j = 0; j < A::N; ++j) v[j] = fmaf(s.normal(v[j]), a.w ? w[j] : 1.f, a.b ? b[j] : 0.f);
+        for (int j = 0; j < A::N; ++j)
+            v[j] = fmaf(fmaf(v[j] * s.scale - s.m, s.r, dr), a.w ? w[j] : 1.f, a.b ? b[j] : 0.f);
         y[at] = A::pack(v);
     }
-    if (threadIdx.x == 0) {
-        if (a.mean) a.mean[row] = (s.m + s.d) / s.scale;
-        if (a.rstd) a.rstd[row] = s.r * s.scale;
+    if (t == 0) s.write(a, row);
+    group_sync<NT>(group);   // red is read
+}
+
+// The same for a row that overflows among others: not to be inlined there.
+template <typename T, typename W, int B, int NT>
+__device__ __noinline__ void huge_row(const NormArgs& a, int64_t row, int t, int group, float (*red)[2]) {
+    long_row<T, W, B, NT>(a, row, t, group, red);
+}
+
+template <typename T, typename W, int B>
+__global__ void __launch_bounds__(WIDEST) layernorm_long_kernel(const NormArgs a) {
+    __shared__ float red[3 * WIDEST / 32][2];
+    pdl_wait();
+    pdl_launch_dependents();
+    long_row<T, W, B, WIDEST>(a, blockIdx.x, threadIdx.x, 0, red);
+}
+
+// The row in the registers of NT threads (a warp: four rows to a CTA), every
+// access of B bytes, up to 32 words a thread.
+template <typename T, typename W, int B, int NT>
+__global__ void __launch_bounds__(NT < 128 ? 128 : NT) layernorm_kernel(const __grid_constant__ NormArgs a) {
+    using A = Access<T, B>;
+    using Word = typename A::Word;
+    using Pair = typename A::Pair;
+    constexpr int P = A::PAIRS;
+    constexpr int R = B >= 4 ? HELD_WORDS * 4 / B : HELD_WORDS;
+    constexpr int GROUPS = NT < 128 ? 128 / NT : 1;
+    __shared__ float red[3 * WIDEST / 32][2];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int group = threadIdx.x / NT, t = threadIdx.x % NT;
+    const int64_t row = (int64_t)blockIdx.x * GROUPS + group;
+    if (row >= a.N) return;   // a whole warp
+    const int accesses = (int)(a.D / A::N);
+    const Word* x = reinterpret_cast<const Word*>(static_cast<const T*>(a.x) + row * a.ldx) + t;
+    Word held[R];
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (t + i * NT < accesses) f(i);
+    };
+    each([&](int i) { held[i] = x[i * NT]; });
+    RowStats s{1.f, 0.f, 0.f, 0.f};
+    const bool fine = row_stats<NT>(
+        s, a.D, a.eps, group, red,
+        [&] {
+            Pair c = A::both(0.f);
+            each([&](int i) {
+                Pair v[P];
+                A::unpack(held[i], v);
+#pragma unroll
+                for (int j = 0; j < P; ++j) c = add2(c, v[j]);
+            });
+            return A::total(c);
+        },
+        [&](float m, float (&sums)[2]) {
+            Pair c = A::both(0.f), q = c;
+            each([&](int i) {
+                Pair v[P];
+                A::unpack(held[i], v);
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    const Pair u = add2(v[j], A::both(-m));
+                    c = add2(c, u);
+                    q = fma2(u, u, q);
+                }
+            });
+            sums[0] = A::total(c), sums[1] = A::total(q);
+        },
+        [] {});
+    if (!fine) {   // the same for every thread of the row
+        group_sync<NT>(group);
+        huge_row<T, W, B, NT>(a, row, t, group, red);
+        return;
     }
+    Word* y = reinterpret_cast<Word*>(static_cast<T*>(a.y) + row * a.ldy) + t;
+    const Pair m = A::both(-s.m), r = A::both(s.r), dr = A::both(-s.d * s.r);
+    each([&](int i) {
+        Pair v[P], w[P], b[P];
+#pragma unroll
+        for (int j = 0; j < P; ++j) w[j] = A::both(1.f), b[j] = A::both(0.f);
+        if (a.w) load_params<W, A::N>(static_cast<const W*>(a.w) + (t + i * NT) * A::N, w);
+        if (a.b) load_params<W, A::N>(static_cast<const W*>(a.b) + (t + i * NT) * A::N, b);
+        A::unpack(held[i], v);
+#pragma unroll
+        for (int j = 0; j < P; ++j) v[j] = fma2(fma2(add2(v[j], m), r, dr), w[j], b[j]);
+        y[i * NT] = A::pack(v);
+    });
+    if (t == 0) s.write(a, row);
+}
+
+// --------------------------------------------------------- rows in turn --
+
+// wait_bounded without the call: one in the loop would have the threads' columns
+// saved around it.
+__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t phase, volatile int* flag, int* err,
+                                            uint64_t timeout_ns) {
+    if (mbar_try_wait(bar, phase)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        if (mbar_try_wait(bar, phase)) return true;
+        if (*flag) return false;
+        if (globaltimer_ns() - t0 > timeout_ns) {
+            *flag = 1;
+            atomicCAS(err, 0, (int)TPMLP_ERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// CTAs of TH threads that stay, in as many groups of NT threads as a row needs at
+// LONGEST / TH elements a thread (FULL: exactly). A thread keeps its columns' parameters in registers;
+// a group's next rows (Q matrices of STAGES rows) are on their way to shared
+// memory. Rows of whole 16-byte accesses come by bulk copies, one instruction a
+// row (copies by every thread were what the backward waited for: 8192 x 8192
+// bf16, 107 us against 90), others by 4-byte copies of the threads' own elements.
+template <typename T, int B, int Q, int STAGES, int TH, int NT, bool FULL>
+struct RowRing {
+    using A = Access<T, B>;
+    using Word = typename A::Word;
+    static constexpr bool BULK = B == 16;
+    static constexpr int R = LONGEST / TH / A::N, GROUPS = TH / NT;
+    Word* rows;          // of this group
+    uint64_t* bars;      // BULK: STAGES of this group
+    int t, accesses, group;
+    int k;               // the current row's stage
+    uint32_t phase;
+
+    static constexpr int MOST = GROUPS * STAGES * Q * NT * R * B;
+    __device__ __forceinline__ RowRing(void* memory, uint64_t* barriers, int64_t D) {
+        group = threadIdx.x / NT;
+        t = threadIdx.x & (NT - 1);
+        accesses = FULL ? NT * R : (int)(D / A::N);
+        rows = static_cast<Word*>(memory) + group * STAGES * Q * NT * R;
+        bars = barriers + group * STAGES;
+        k = 0;
+        phase = 0;
+        if (BULK) {
+            if (t == 0)
+                for (int s = 0; s < STAGES; ++s) mbar_init(smem_u32(bars + s), 1);
+            fence_mbar_init();
+            fence_proxy_async_smem();
+            group_sync<NT>(group);
+        }
+    }
+    __device__ __forceinline__ bool mine(int i) const { return FULL || t + i * NT < accesses; }
+    // access i of matrix q of the current row; zeros beyond it
+    __device__ __forceinline__ Word at(int q, int i) const {
+        return mine(i) ? rows[(k * Q + q) * (NT * R) + t + i * NT] : Word{};
+    }
+    // into stage s: BULK: thread 0's work, once the group is done with the stage
+    __device__ __forceinline__ void fetch(int s, int q, const void* base, int64_t row, int64_t ld) const {
+        const T* src = static_cast<const T*>(base) + row * ld;
+        Word* dst = rows + (s * Q + q) * (NT * R);
+        if constexpr (BULK) {
+            bulk_load_g2s(smem_u32(dst), src, (uint32_t)accesses * B, smem_u32(bars + s));
+        } else {
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                if (mine(i)) {
+                    const Word* from = reinterpret_cast<const Word*>(src) + t + i * NT;
+                    if constexpr (B == 4)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst + t + i * NT)),
+                                     "l"(from) : "memory");
+                    else   // there is no copy of 2 bytes
+                        dst[t + i * NT] = *from;
+                }
+        }
+    }
+    // copy(s): the fetches of one row into stage s, if there is such a row
+    template <typename Copy> __device__ __forceinline__ void ask(int s, bool there, Copy copy) const {
+        if constexpr (BULK) {
+            if (t == 0 && there) {
+                mbar_arrive_expect_tx(smem_u32(bars + s), (uint32_t)(Q * accesses * B));
+                copy(s);
+            }
+        } else {
+            if (there) copy(s);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    }
+    // The current row has arrived; false: not within the limit (flag, the group's
+    // for this turn, is set).
+    __device__ __forceinline__ bool wait(volatile int* flag, int* err, uint64_t timeout_ns) const {
+        if constexpr (BULK) {
+            const bool ok = wait_inline(smem_u32(bars + k), phase, flag, err, timeout_ns);
+            return NT > 32 ? ok : __all_sync(0xffffffffu, ok);
+        } else {
+            asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+            return true;
+        }
+    }
+    __device__ __forceinline__ void next() {
+        if (++k == STAGES) {
+            k = 0;
+            phase ^= 1u;
+        }
+    }
+    // After a wait that ran out: no copy may be in flight into a CTA that leaves.
+    // `left` rows from the current one on were asked for.
+    __device__ __forceinline__ void drain(uint32_t left, volatile int* flag, int* err, uint64_t timeout_ns) {
+        if (!BULK || t != 0) return;
+        const uint64_t limit = timeout_ns > 100000000ull ? timeout_ns : 100000000ull;
+        for (uint32_t i = 0; i < left && i < STAGES; ++i, next()) wait_bounded(smem_u32(bars + k), phase, flag, err, limit, false);
+    }
+};
+
+template <typename T> constexpr int NORM_STAGES = sizeof(T) == 2 ? 6 : 3;   // 96 KB a CTA, two CTAs an SM
+template <typename T> constexpr int GRAD_STAGES = sizeof(T) == 2 ? 4 : 2;   // 192 KB, one
+
+// Many rows of 16-byte accesses, up to LONGEST elements each. (8192 x 8192
+// bf16 on GB300: 47 us, 5.7 TB/s read and written; the row in the registers of
+// CTAs that leave 54 to 58, their parameters read from L2 row by row.)
+template <typename T, typename W, int NT, bool FULL>
+__global__ void __launch_bounds__(NORM_THREADS, 2) layernorm_turns_kernel(const __grid_constant__ NormArgs a) {
+    using Ring = RowRing<T, 16, 1, NORM_STAGES<T>, NORM_THREADS, NT, FULL>;
+    using A = typename Ring::A;
+    using Word = typename Ring::Word;
+    using Pair = typename A::Pair;
+    constexpr int R = Ring::R, P = A::PAIRS, STAGES = NORM_STAGES<T>;
+    extern __shared__ __align__(16) uint4 ring_memory[];
+    __shared__ uint64_t bars[Ring::GROUPS * STAGES];
+    __shared__ float red[3 * WIDEST / 32][2];
+    __shared__ int late[2][Ring::GROUPS];   // a wait of this turn ran out
+    if (threadIdx.x < 2 * Ring::GROUPS) (&late[0][0])[threadIdx.x] = 0;
+    __syncthreads();
+    Ring ring(ring_memory, bars, a.D);
+    const uint32_t N = (uint32_t)a.N, step = gridDim.x * Ring::GROUPS, first = blockIdx.x * Ring::GROUPS + ring.group;
+    pdl_wait();
+    pdl_launch_dependents();
+    auto ask = [&](int s, uint32_t row) {
+        ring.ask(s, row < N, [&](int to) { ring.fetch(to, 0, a.x, row, a.ldx); });
+    };
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) ask(s, first + s * step);
+    Pair w[R][P], b[R][P];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) w[i][j] = A::both(1.f), b[i][j] = A::both(0.f);
+        if (a.w && ring.mine(i)) load_params<W, A::N>(static_cast<const W*>(a.w) + (ring.t + i * NT) * A::N, w[i]);
+        if (a.b && ring.mine(i)) load_params<W, A::N>(static_cast<const W*>(a.b) + (ring.t + i * NT) * A::N, b[i]);
+    }
+    int turn = 0;
+    uint32_t row = first;
+    for (; row < N; row += step, turn ^= 1, ring.next()) {
+        volatile int* flag = &late[turn][ring.group];
+        bool ok = ring.wait(flag, a.err, a.timeout_ns);
+        Word held[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) held[i] = ring.at(0, i);
+        RowStats s{1.f, 0.f, 0.f, 0.f};
+        const bool fine = row_stats<NT>(
+            s, a.D, a.eps, ring.group, red,
+            [&] {
+                Pair c = A::both(0.f);
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    Pair v[P];
+                    A::unpack(held[i], v);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) c = add2(c, v[j]);
+                }
+                return A::total(c);
+            },
+            [&](float m, float (&sums)[2]) {
+                Pair c = A::both(0.f), q = c;
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    Pair v[P];
+                    A::unpack(held[i], v);
+                    const Pair less = A::both(ring.mine(i) ? -m : 0.f);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) {
+                        const Pair u = add2(v[j], less);
+                        c = add2(c, u);
+                        q = fma2(u, u, q);
+                    }
+                }
+                sums[0] = A::total(c), sums[1] = A::total(q);
+            },
+            [&] {
+                ok = ok && !(NT > 32 && *flag);
+                if (ok) ask(ring.k, row + STAGES * step);   // every thread holds its elements
+            });
+        if (!ok) break;   // the whole group
+        if (!fine) {
+            group_sync<NT>(ring.group);
+            huge_row<T, W, 16, NT>(a, row, ring.t, ring.group, red);
+            continue;
+        }
+        Word* y = reinterpret_cast<Word*>(static_cast<T*>(a.y) + (int64_t)row * a.ldy) + ring.t;
+        const Pair m = A::both(-s.m), r = A::both(s.r), dr = A::both(-s.d * s.r);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            Pair v[P];
+            A::unpack(held[i], v);
+#pragma unroll
+            for (int j = 0; j < P; ++j) v[j] = fma2(fma2(add2(v[j], m), r, dr), w[i][j], b[i][j]);
+            const Word out = A::pack(v);
+            if (ring.mine(i)) y[i * NT] = out;
+        }
+        if (ring.t == 0) s.write(a, row);
+    }
+    if (row < N) ring.drain((N - row + step - 1) / step, &late[turn][ring.group], a.err, a.timeout_ns);
 }
 
 // ------------------------------------------------------------- backward --
@@ -332,139 +501,156 @@ struct NormGradArgs {
     int64_t lddx;
     void* dw;               // NULL (both): not wanted
     void* db;
-    float4* rows;           // [N]: sum u / D, sum u h / D, sum h / D (what the mean is off by)
-    float* part;            // [S, 2, D]: a row chunk's sums of dy h and dy
+    float4* rows;           // [N]: sum u / D, sum u h / D, d rstd (long rows)
+    float* part;            // [S, 2, D]: a CTA's (long rows: a row chunk's) sums of dy h and dy
     int S;
+    int* err;
+    uint64_t timeout_ns;
 };
 
-template <typename T> constexpr int GRAD_AHEAD = sizeof(T) == 2 ? 4 : 2;   // stages: 192 KB
+// Up to this many deviations a row's fp32 mean is near enough for h (it is off by
+// 2^-25 of itself, 2.4e-7 of a deviation at most); beyond, d is taken.
+constexpr float FAR_MEAN = 8.f;
 
-// All of it in one reading, for rows of up to STAY * ELEMS elements: a thread
+__device__ __forceinline__ void write_param(float* at, float v) { *at = v; }
+__device__ __forceinline__ void write_param(__nv_bfloat16* at, float v) { *at = __float2bfloat16_rn(v); }
+
+// All of it in one reading, for rows of up to LONGEST elements: a thread
 // keeps its columns' sums of dy h and dy over the rows of its group; a CTA's
-// sums go to part[blockIdx.x] (with one CTA to dw and db).
-template <typename T, typename W, int B>
-__global__ void __launch_bounds__(STAY, 1) norm_grad_kernel(const NormGradArgs a, int nt) {
-    using Ring = RowRing<T, B, 3, GRAD_AHEAD<T>>;
+// sums go to part[blockIdx.x] (with one CTA to dw and db). Elements beyond the row
+// are zeros and pass through the arithmetic. (8192 x 8192 bf16 with dresidual on
+// GB300: the loop alone 90 us, 6.0 TB/s read and written; without its reductions
+// or its column sums 89: HBM.)
+template <typename T, typename W, int B, int NT, bool FULL, bool RES>
+__global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const NormGradArgs a) {
+    constexpr int Q = RES ? 3 : 2, STAGES = GRAD_STAGES<T>;
+    using Ring = RowRing<T, B, Q, STAGES, GRAD_THREADS, NT, FULL>;
     using A = typename Ring::A;
     using Word = typename Ring::Word;
-    constexpr int R = Ring::R;
-    extern __shared__ uint4 ring_memory[];
-    __shared__ float red[2][STAY / 32][3];
-    const int groups = STAY / nt, group = threadIdx.x / nt, t = threadIdx.x & (nt - 1);
-    const Ring ring{reinterpret_cast<Word*>(ring_memory) + threadIdx.x, t, nt, (int)(a.D / A::N)};
-    const int64_t step = (int64_t)gridDim.x * groups, first = (int64_t)blockIdx.x * groups + group;
+    using Pair = typename A::Pair;
+    constexpr int R = Ring::R, P = A::PAIRS;
+    extern __shared__ __align__(16) uint4 ring_memory[];
+    __shared__ uint64_t bars[Ring::GROUPS * STAGES];
+    __shared__ float red[2][GRAD_THREADS / 32][3];
+    __shared__ int late[2][Ring::GROUPS];
+    if (threadIdx.x < 2 * Ring::GROUPS) (&late[0][0])[threadIdx.x] = 0;
+    __syncthreads();
+    Ring ring(ring_memory, bars, a.D);
+    constexpr int groups = Ring::GROUPS;
+    const int group = ring.group, t = ring.t;
+    const uint32_t N = (uint32_t)a.N, step = gridDim.x * groups, first = blockIdx.x * groups + group;
     pdl_wait();
     pdl_launch_dependents();
-    auto fetch = [&](int k, int64_t row) {
-        if (row < a.N) {
-            ring.fetch(k, 0, a.x, row, a.ldx);
-            ring.fetch(k, 1, a.dy, row, a.lddy);
-            if (a.dres) ring.fetch(k, 2, a.dres, row, a.lddres);
-        }
-        ring.commit();
+    auto ask = [&](int s, uint32_t row) {
+        ring.ask(s, row < N, [&](int to) {
+            ring.fetch(to, 0, a.x, row, a.ldx);
+            ring.fetch(to, 1, a.dy, row, a.lddy);
+            if (RES) ring.fetch(to, Q - 1, a.dres, row, a.lddres);
+        });
     };
 #pragma unroll
-    for (int k = 0; k < GRAD_AHEAD<T>; ++k) fetch(k, first + k * step);
-    float w[R][A::N], sw[R][A::N], sb[R][A::N];
+    for (int s = 0; s < STAGES; ++s) ask(s, first + s * step);
+    Pair w[R][P], sw[R][P], sb[R][P];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
 #pragma unroll
-        for (int j = 0; j < A::N; ++j) w[i][j] = 1.f, sw[i][j] = sb[i][j] = 0.f;
-        if (a.w && ring.mine(i)) load_params<W, A::N>(static_cast<const W*>(a.w) + (t + i * nt) * A::N, w[i]);
+        for (int j = 0; j < P; ++j) w[i][j] = A::both(1.f), sw[i][j] = sb[i][j] = A::both(0.f);
+        if (a.w && ring.mine(i)) load_params<W, A::N>(static_cast<const W*>(a.w) + (t + i * NT) * A::N, w[i]);
     }
     const float inv = 1.f / (float)a.D;
-    float m = 0.f, r = 0.f;
-    if (first < a.N) m = a.mean[first], r = a.rstd[first];
-    int k = 0, turn = 0;
-    for (int64_t row = first; row < a.N; row += step, turn ^= 1) {
-        const float cm = m, cr = r;
-        if (row + step < a.N) m = a.mean[row + step], r = a.rstd[row + step];
-        ring.wait();
-        float s[3] = {0.f, 0.f, 0.f};   // u, u h, h
+    float m_next = 0.f, r_next = 0.f;
+    if (first < N) m_next = a.mean[first], r_next = a.rstd[first];
+    int turn = 0;
+    uint32_t row = first;
+    for (; row < N; row += step, turn ^= 1, ring.next()) {
+        const float m1 = m_next, r1 = r_next;
+        if (row + step < N) m_next = a.mean[row + step], r_next = a.rstd[row + step];
+        volatile int* flag = &late[turn][group];
+        const bool ok = ring.wait(flag, a.err, a.timeout_ns);
+        const Pair m = A::both(-m1), r = A::both(r1);
+        Word x[R], g[R];
+        Pair su = A::both(0.f), suh = su, sh = su;
 #pragma unroll
-        for (int i = 0; i < R; ++i)
-            if (ring.mine(i)) {
-                float v[A::N], y[A::N];
-                ring.get(k, 0, i, v);
-                ring.get(k, 1, i, y);
+        for (int i = 0; i < R; ++i) {
+            x[i] = ring.at(0, i);
+            g[i] = ring.at(1, i);
+            Pair v[P], y[P];
+            A::unpack(x[i], v);
+            A::unpack(g[i], y);
+            const Pair less = FULL || ring.mine(i) ? m : A::both(0.f);
 #pragma unroll
-                for (int j = 0; j < A::N; ++j) {
-                    const float h = (v[j] - cm) * cr, u = y[j] * w[i][j];
-                    s[0] += u;
-                    s[1] = fmaf(u, h, s[1]);
-                    s[2] += h;
-                }
+            for (int j = 0; j < P; ++j) {
+                const Pair h = mul2(add2(v[j], less), r), u = mul2(y[j], w[i][j]);
+                su = add2(su, u);
+                suh = fma2(u, h, suh);
+                sh = add2(sh, h);
             }
-        group_reduce(s, nt, group, red[turn], Add());
-        const float d = fabsf(cm * cr) > 1.f ? s[2] * inv : 0.f;
-        const float c1 = s[0] * inv, c2 = fmaf(-d, s[0], s[1]) * inv;
-        Word* out = reinterpret_cast<Word*>(static_cast<T*>(a.dx) + row * a.lddx) + t;
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-            if (ring.mine(i)) {
-                float v[A::N], y[A::N], z[A::N];
-                ring.get(k, 0, i, v);
-                ring.get(k, 1, i, y);
-                if (a.dres) ring.get(k, 2, i, z);
-#pragma unroll
-                for (int j = 0; j < A::N; ++j) {
-                    const float h = fmaf(v[j] - cm, cr, -d);
-                    sw[i][j] = fmaf(y[j], h, sw[i][j]);
-                    sb[i][j] += y[j];
-                    v[j] = cr * fmaf(-h, c2, fmaf(y[j], w[i][j], -c1));
-                    if (a.dres) v[j] += z[j];
-                }
-                out[i * nt] = A::pack(v);
-            }
-        fetch(k, row + GRAD_AHEAD<T> * step);
-        k = k == GRAD_AHEAD<T> - 1 ? 0 : k + 1;
-    }
-    if (a.dw == nullptr) return;
-    if (groups > 1) {   // the groups' sums in their order, through the ring's memory
-        float* sums = reinterpret_cast<float*>(ring_memory);
-        static_assert(2 * STAY / 2 * ELEMS * sizeof(float) <= Ring::BYTES, "room for two sums a column");
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        for (int q = 0; q < groups; ++q) {
-            __syncthreads();
-            if (group == q)
-#pragma unroll
-                for (int i = 0; i < R; ++i)
-                    if (ring.mine(i))
-#pragma unroll
-                        for (int j = 0; j < A::N; ++j) {
-                            float* at = sums + 2 * ((t + i * nt) * A::N + j);
-                            if (q > 0) {
-                                sw[i][j] += at[0];
-                                sb[i][j] += at[1];
-                            }
-                            at[0] = sw[i][j];
-                            at[1] = sb[i][j];
-                        }
         }
-        if (group != groups - 1) return;   // the last group has them all
-    }
-    float* p = a.part + (int64_t)blockIdx.x * 2 * a.D;
+        float s[3] = {A::total(su), A::total(suh), A::total(sh)};
+        group_reduce<NT>(s, group, red[turn], Add());
+        if (!ok || (NT > 32 && *flag)) break;   // the whole group
+        if (!RES) ask(ring.k, row + STAGES * step);   // every thread holds its elements
+        const float d = fabsf(m1 * r1) > FAR_MEAN ? s[2] * inv : 0.f;
+        // dx = r u - r c1 - r c2 h
+        const Pair d1 = A::both(-d), c1 = A::both(-r1 * s[0] * inv), c2 = A::both(-r1 * fmaf(-d, s[0], s[1]) * inv);
+        Word* out = reinterpret_cast<Word*>(static_cast<T*>(a.dx) + (int64_t)row * a.lddx) + t;
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-        if (ring.mine(i))
+        for (int i = 0; i < R; ++i) {
+            Pair v[P], y[P], z[P > 1 ? P : 2];
+            A::unpack(x[i], v);
+            A::unpack(g[i], y);
+            if (RES) A::unpack(ring.at(Q - 1, i), *reinterpret_cast<Pair(*)[P]>(&z));
 #pragma unroll
-            for (int j = 0; j < A::N; ++j) {
-                const int c = (t + i * nt) * A::N + j;
-                if (gridDim.x > 1) {
-                    p[c] = sw[i][j];
-                    p[a.D + c] = sb[i][j];
-                } else if constexpr (sizeof(W) == 4) {
-                    static_cast<W*>(a.dw)[c] = sw[i][j];
-                    static_cast<W*>(a.db)[c] = sb[i][j];
-                } else {
-                    static_cast<W*>(a.dw)[c] = __float2bfloat16_rn(sw[i][j]);
-                    static_cast<W*>(a.db)[c] = __float2bfloat16_rn(sb[i][j]);
-                }
+            for (int j = 0; j < P; ++j) {
+                const Pair h = fma2(add2(v[j], m), r, d1);
+                sw[i][j] = fma2(y[j], h, sw[i][j]);
+                sb[i][j] = add2(sb[i][j], y[j]);
+                v[j] = fma2(mul2(y[j], w[i][j]), r, fma2(h, c2, RES ? add2(z[j], c1) : c1));
             }
+            const Word o = A::pack(v);
+            if (ring.mine(i)) out[i * NT] = o;
+        }
+        if (RES) {
+            if (Ring::BULK) group_sync<NT>(group);
+            ask(ring.k, row + STAGES * step);
+        }
+    }
+    if (row < N) ring.drain((N - row + step - 1) / step, &late[turn][group], a.err, a.timeout_ns);
+    if (a.dw == nullptr) return;
+    // the groups' sums in their order, through the ring's memory
+    float* sums = reinterpret_cast<float*>(ring_memory);
+    static_assert(2 * NT * R * A::N * sizeof(float) <= Ring::MOST, "room for two sums a column");
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    const int D = (int)a.D;
+    for (int q = 0; q < groups; ++q) {
+        __syncthreads();
+        if (group == q)
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                if (ring.mine(i))
+#pragma unroll
+                    for (int j = 0; j < P; ++j) {
+                        Pair* gw = reinterpret_cast<Pair*>(sums + (t + i * NT) * A::N) + j;
+                        Pair* gb = reinterpret_cast<Pair*>(sums + NT * R * A::N + (t + i * NT) * A::N) + j;
+                        *gw = q > 0 ? add2(*gw, sw[i][j]) : sw[i][j];
+                        *gb = q > 0 ? add2(*gb, sb[i][j]) : sb[i][j];
+                    }
+    }
+    __syncthreads();
+    float* part = a.part + (int64_t)blockIdx.x * 2 * D;
+    for (int c = threadIdx.x; c < D; c += GRAD_THREADS) {
+        const float gw = sums[c], gb = sums[NT * R * A::N + c];
+        if (gridDim.x > 1) {
+            part[c] = gw;
+            part[D + c] = gb;
+        } else {
+            write_param(static_cast<W*>(a.dw) + c, gw);
+            write_param(static_cast<W*>(a.db) + c, gb);
+        }
+    }
 }
 
-// Longer rows are read twice.
-// Sums over a row, one CTA each.
+// Longer rows are read twice. Sums over a row, one CTA each:
 template <typename T, typename W, int B>
 __global__ void __launch_bounds__(256) norm_grad_rows_kernel(const NormGradArgs a) {
     using A = Access<T, B>;
@@ -493,8 +679,8 @@ __global__ void __launch_bounds__(256) norm_grad_rows_kernel(const NormGradArgs 
         }
     }
     const float inv = 1.f / (float)a.D;
-    group_reduce(s, 256, 0, red, Add());
-    const float d = fabsf(m * r) > 1.f ? s[2] * inv : 0.f;
+    group_reduce<256>(s, 0, red, Add());
+    const float d = fabsf(m * r) > FAR_MEAN ? s[2] * inv : 0.f;
     if (threadIdx.x == 0) a.rows[row] = make_float4(s[0] * inv, fmaf(-d, s[0], s[1]) * inv, d, 0.f);
 }
 
@@ -562,11 +748,7 @@ __global__ void __launch_bounds__(256) norm_grad_params_kernel(const NormGradArg
     __syncthreads();
     if (grp == 0 && c < 2 * a.D) {
         for (int k = 1; k < 8; ++k) s += red[k][lane];
-        W* out = static_cast<W*>(c < a.D ? a.dw : a.db) + (c < a.D ? c : c - a.D);
-        if constexpr (sizeof(W) == 4)
-            *out = s;
-        else
-            *out = __float2bfloat16_rn(s);
+        write_param(static_cast<W*>(c < a.D ? a.dw : a.db) + (c < a.D ? c : c - a.D), s);
     }
 }
 
@@ -604,21 +786,38 @@ bool allow_smem(K kernel, int bytes, std::atomic<uint64_t>& asked) {
     return true;
 }
 
+// f(NT, FULL) as constants: the group of TH / 8 to TH threads that rows of D elements take
+template <int TH, typename F> tpmlp_status with_group(int64_t D, F f) {
+    constexpr int ELEMS = LONGEST / TH;
+    auto width = [&](auto nt) {
+        return D == decltype(nt)::value * ELEMS ? f(nt, std::true_type()) : f(nt, std::false_type());
+    };
+    if (D <= TH / 8 * ELEMS) return width(std::integral_constant<int, TH / 8>());
+    if (D <= TH / 4 * ELEMS) return width(std::integral_constant<int, TH / 4>());
+    if (D <= TH / 2 * ELEMS) return width(std::integral_constant<int, TH / 2>());
+    return width(std::integral_constant<int, TH>());
+}
+
+template <typename T, typename W, int NT, bool FULL> tpmlp_status forward_turns(const NormArgs& a, cudaStream_t s) {
+    using Ring = RowRing<T, 16, 1, NORM_STAGES<T>, NORM_THREADS, NT, FULL>;
+    static std::atomic<uint64_t> asked{0};
+    if (!allow_smem(layernorm_turns_kernel<T, W, NT, FULL>, Ring::MOST, asked)) return TPMLP_ERR_CUDA;
+    return launch_smem(layernorm_turns_kernel<T, W, NT, FULL>, dim3((unsigned)(2 * device_sm_count())),
+                       NORM_THREADS, Ring::MOST, s, a);
+}
+
+// Rows in turn: from eight rows a group on, which the parameters' one reading and
+// the ring's start are for.
 template <typename T, typename W, int B>
 tpmlp_status forward(const NormArgs& a, cudaStream_t s) {
     constexpr int R = B >= 4 ? HELD_WORDS * 4 / B : HELD_WORDS;
     const int64_t accesses = a.D / (B / (int)sizeof(T));
     LaunchScope ls("layernorm", s);
-    if (a.D <= STAY * ELEMS) {
-        const int nt = group_threads(a.D);
-        const int64_t turns = (a.N + STAY / nt - 1) / (STAY / nt), most = 2LL * device_sm_count();
-        if (turns > most) {
-            constexpr int BYTES = RowRing<T, B, 1, AHEAD>::BYTES;
-            static std::atomic<uint64_t> asked{0};
-            if (!allow_smem(layernorm_stay_kernel<T, W, B>, BYTES, asked)) return TPMLP_ERR_CUDA;
-            return launch_smem(layernorm_stay_kernel<T, W, B>, dim3((unsigned)most), STAY, BYTES, s, a, nt);
-        }
-    }
+    if constexpr (B == 16)
+        if (a.D <= LONGEST && a.N >= 16LL * device_sm_count() * (LONGEST / a.D))
+            return with_group<NORM_THREADS>(a.D, [&](auto nt, auto full) {
+                return forward_turns<T, W, decltype(nt)::value, decltype(full)::value>(a, s);
+            });
     if (accesses <= 32 * R)
         return launch(layernorm_kernel<T, W, B, 32>, dim3((unsigned)((a.N + 3) / 4)), 128, s, a);
     if (accesses <= 128 * R) return launch(layernorm_kernel<T, W, B, 128>, dim3((unsigned)a.N), 128, s, a);
@@ -649,24 +848,31 @@ int64_t row_chunks(int64_t N, int64_t D) {
     return S < 1 ? 1 : S > 1024 ? 1024 : S;
 }
 
-constexpr int MOST_CTAS = 152;   // that stay, of the backward: one an SM
+template <typename T, typename W, int B, int NT, bool FULL, bool RES>
+tpmlp_status backward_turns(NormGradArgs& a, cudaStream_t s) {
+    using Ring = RowRing<T, B, RES ? 3 : 2, GRAD_STAGES<T>, GRAD_THREADS, NT, FULL>;
+    static std::atomic<uint64_t> asked{0};
+    if (!allow_smem(norm_grad_kernel<T, W, B, NT, FULL, RES>, Ring::MOST, asked)) return TPMLP_ERR_CUDA;
+    const int64_t turns = (a.N + Ring::GROUPS - 1) / Ring::GROUPS;
+    a.S = (int)(turns < MOST_CTAS ? turns : MOST_CTAS);
+    return launch_smem(norm_grad_kernel<T, W, B, NT, FULL, RES>, dim3((unsigned)a.S), GRAD_THREADS, Ring::MOST,
+                       s, a);
+}
 
 template <typename T, typename W, int B>
 tpmlp_status backward(NormGradArgs a, cudaStream_t s) {
     LaunchScope ls("layernorm_backward", s);
-    if (a.D <= STAY * ELEMS) {
-        const int nt = group_threads(a.D);
-        const int64_t turns = (a.N + STAY / nt - 1) / (STAY / nt);
-        a.S = (int)(turns < MOST_CTAS ? turns : MOST_CTAS);
-        constexpr int BYTES = RowRing<T, B, 3, GRAD_AHEAD<T>>::BYTES;
-        static std::atomic<uint64_t> asked{0};
-        if (!allow_smem(norm_grad_kernel<T, W, B>, BYTES, asked)) return TPMLP_ERR_CUDA;
-        const tpmlp_status st =
-            launch_smem(norm_grad_kernel<T, W, B>, dim3((unsigned)a.S), STAY, BYTES, s, a, nt);
+    const int64_t accesses = a.D / (B / (int)sizeof(T));
+    if (a.D <= LONGEST) {
+        const tpmlp_status st = with_group<GRAD_THREADS>(a.D, [&](auto nt, auto full) {
+            constexpr int NT = decltype(nt)::value;
+            constexpr bool FULL = decltype(full)::value && B == 16;
+            return a.dres != nullptr ? backward_turns<T, W, B, NT, FULL, true>(a, s)
+                                     : backward_turns<T, W, B, NT, FULL, false>(a, s);
+        });
         if (st != TPMLP_OK || a.part == nullptr || a.S == 1) return st;
         return launch(norm_grad_params_kernel<W>, dim3((unsigned)((2 * a.D + 31) / 32)), 256, s, a);
     }
-    const int64_t accesses = a.D / (B / (int)sizeof(T));
     tpmlp_status st = launch(norm_grad_rows_kernel<T, W, B>, dim3((unsigned)a.N), 256, s, a);
     if (st != TPMLP_OK) return st;
     st = launch(norm_grad_apply_kernel<T, W, B>, dim3((unsigned)((accesses + 127) / 128), (unsigned)a.S), 128, s, a);
@@ -695,14 +901,16 @@ size_t rows_bytes(int64_t N) { return ((size_t)N * sizeof(float4) + 255) & ~(siz
 
 tpmlp_status run_layernorm(int f32, int params_f32, const LayernormArgs& g, cudaStream_t s) {
     if (g.N == 0) return TPMLP_OK;
-    const NormArgs a{g.N, g.D, g.x, g.ldx, g.weight, g.bias, g.eps, g.y, g.ldy, g.mean, g.rstd};
+    const NormArgs a{g.N, g.D, g.x, g.ldx, g.weight, g.bias, g.eps, g.y, g.ldy, g.mean, g.rstd,
+                     device_error_word(), wait_timeout_ns()};
+    if (a.err == nullptr) return TPMLP_ERR_CUDA;
     if (f32) return forward_width<float, float>(a, s);
     return params_f32 ? forward_width<__nv_bfloat16, float>(a, s) : forward_width<__nv_bfloat16, __nv_bfloat16>(a, s);
 }
 
 size_t layernorm_backward_bytes(int64_t N, int64_t D) {
     if (N == 0) return 0;
-    const int64_t S = D <= STAY * ELEMS ? MOST_CTAS : row_chunks(N, D);
+    const int64_t chunks = row_chunks(N, D), S = chunks > MOST_CTAS ? chunks : MOST_CTAS;
     return rows_bytes(N) + (size_t)S * 2 * (size_t)D * sizeof(float);
 }
 
@@ -717,7 +925,9 @@ tpmlp_status run_layernorm_backward(int f32, int params_f32, const LayernormGrad
         return TPMLP_OK;
     }
     NormGradArgs a{g.N, g.D, g.dy, g.lddy, g.x, g.ldx, g.weight, g.mean, g.rstd, g.dresidual, g.lddres,
-                   g.dx, g.lddx, g.dweight, g.dbias, nullptr, nullptr, (int)row_chunks(g.N, g.D)};
+                   g.dx, g.lddx, g.dweight, g.dbias, nullptr, nullptr, (int)row_chunks(g.N, g.D),
+                   device_error_word(), wait_timeout_ns()};
+    if (a.err == nullptr) return TPMLP_ERR_CUDA;
     a.rows = static_cast<float4*>(workspace);
     if (params) a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + rows_bytes(g.N));
     if (f32) return backward_width<float, float>(a, s);
