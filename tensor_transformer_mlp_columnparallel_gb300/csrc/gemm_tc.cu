@@ -116,7 +116,7 @@ struct TcParams {
     CUtensorMap tmC[kMaxG];    // tma_out: the output of each group (box 32 x 32); EPI_DSWIGLU:
                                // dG and dU of each group as one 3-D tensor {N, M, 2}
     CUtensorMap tmAux[kMaxG];  // tma_out, EPI_ACT with Z saved: Z of each group;
-                               // EPI_DSWIGLU: G of each group;
+                               // EPI_DSWIGLU: G of each group; res_in: the residual;
                                // chain (which has no auxiliary tensor): the second pair's A
     int M, N, K;
     int G, fold;
@@ -145,6 +145,7 @@ struct TcParams {
     uint64_t drain_ns;   // limit of the waits for copies and MMAs already in flight
     int inject;          // failure-detection self test: the role that stalls (0: none)
     int tma_out;         // 1: the epilogue writes C (and Z) through staging and tensor stores
+    int res_in;          // 1 (tma_out, residual, no Z saved): the residual comes by tensor loads (tmAux)
     int alt;             // bit 0: whole tiles of odd waves walk their K range from the top
                          // down; bit 1: odd bands walk their tiles in reverse (decode_tile)
 };
@@ -940,8 +941,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
         // into the Z half of the chunk's staging set (issued one chunk ahead,
         // or at the start of a tile before its accumulator is ready), on one
         // of the warp's two barriers; zpend / zph hold each set's pending
-        // load and barrier phase
-        const bool zin = C::TMA_OUT && p.tma_out && p.epi.kind == EPI_DACT;
+        // load and barrier phase. A residual comes the same way (to the halves
+        // that a saved Z would leave from).
+        const bool zin = C::TMA_OUT && p.tma_out && (p.epi.kind == EPI_DACT || (RESIDUAL && p.res_in));
         uint32_t zpend = 0, zph = 0;
         auto zbar = [&](uint32_t set) { return bar(ZLD + 2 * quarter + (int)set); };
         auto zload = [&](uint32_t set, int g, int col0, int row0) {
@@ -1027,11 +1029,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_gemm_kernel(const __grid_co
                     }
                     float zv[32];
                     load_row_bf16_smem(buf + 2048u, lane, zv);
-                    dact_apply(p.epi.act, v, zv);
+                    if (RESIDUAL) {
+                        epilogue_act(p.epi, g, row, col0, p.M, p.N, v);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] += zv[j];
+                    } else {
+                        dact_apply(p.epi.act, v, zv);
+                    }
                 } else {
                     epilogue_act(p.epi, g, row, col0, p.M, p.N, v);
+                    if (RESIDUAL) add_residual_thread(p.epi, g, row, col0, p.M, p.N, v);
                 }
-                if (RESIDUAL) add_residual_thread(p.epi, g, row, col0, p.M, p.N, v);
                 stage_row(buf, lane, p.epi.out_f32 != 0, v);
                 fence_proxy_async_smem();   // the staged rows, to the tensor-store proxy
                 __syncwarp();
@@ -1600,6 +1608,11 @@ tpmlp_status launch(const GemmProblem& pr, cudaStream_t s, int ks = 1) {
                 ok = make_map_out(&kp.tmAux[g], pr.epi.aux[g], pr.N, pr.M, pr.epi.ldaux, false);
         }
         kp.tma_out = ok ? 1 : 0;
+        // the residual by tensor loads too, unless Z leaves from their place
+        bool in = ok && residual && !(pr.epi.kind == EPI_ACT && pr.epi.aux[0] != nullptr);
+        for (int g = 0; g < (pr.fold ? 1 : G) && in; ++g)
+            in = make_map_out(&kp.tmAux[g], pr.epi.res[g], pr.N, pr.M, pr.epi.ldres, false);
+        kp.res_in = in ? 1 : 0;
     }
     kp.err = device_error_word();
     kp.timeout_ns = wait_timeout_ns();

@@ -1,13 +1,11 @@
 // What the split linear layers' backward does besides its products:
 //   dZ = dY act'(Z),  db = sum_n dZ
-// in one pass over dY and Z, which memory bounds: a thread has one access's
-// columns of a chunk of rows, writes dZ and keeps the columns' sums (of dZ
-// before it is rounded) in fp32; a second launch adds the chunks in order.
+// in one pass over dY and Z, which memory bounds: a thread has a few columns of
+// many rows, writes dZ and keeps the columns' sums (of dZ before it is rounded) in
+// fp32; a second launch adds the CTAs' sums in order.
 #include <cuda_bf16.h>
 
-#include "access.cuh"
-#include "ptx.cuh"
-#include "tpmlp_internal.h"
+#include "row_ring.cuh"
 
 namespace tpmlp {
 namespace {
@@ -64,6 +62,99 @@ __global__ void __launch_bounds__(COLS) dact_kernel(const DactParams p) {
     }
 }
 
+// The same with rows in turn: a CTA has one panel of F columns (an even share of
+// at most LONGEST) and its groups every so many rows of it, which come to shared
+// memory by bulk copies of 16 KB at a time. 
+constexpr int TURN_THREADS = 512, TURN_STAGES = 3;
+constexpr int TURN_CTAS = 152;
+
+template <typename T, int NT, bool FULL>
+__global__ void __launch_bounds__(TURN_THREADS, 2) dact_turns_kernel(const DactParams p, int act, int panels, int width,
+                                                                     int* err, uint64_t timeout_ns) {
+    using Ring = RowRing<T, 16, 2, TURN_STAGES, TURN_THREADS, NT, FULL>;
+    using A = typename Ring::A;
+    using Word = typename Ring::Word;
+    constexpr int R = Ring::R;
+    extern __shared__ __align__(16) uint4 ring_memory[];
+    __shared__ uint64_t bars[Ring::GROUPS * TURN_STAGES];
+    __shared__ int late[2][Ring::GROUPS];
+    const DactArgs& a = p.a;
+    const int panel = blockIdx.x % panels, chunk = blockIdx.x / panels;
+    const int64_t c0 = (int64_t)panel * width;
+    const int cols = (int)(a.F - c0 < width ? a.F - c0 : width);   // of this panel
+    if (threadIdx.x < 2 * Ring::GROUPS) (&late[0][0])[threadIdx.x] = 0;
+    __syncthreads();
+    Ring ring(ring_memory, bars, cols);
+    const uint32_t N = (uint32_t)a.N, step = (uint32_t)p.S * Ring::GROUPS, first = (uint32_t)chunk * Ring::GROUPS + ring.group;
+    pdl_wait();
+    pdl_launch_dependents();
+    auto ask = [&](int s, uint32_t row) {
+        ring.ask(s, row < N, [&](int to) {
+            ring.fetch(to, 0, static_cast<const T*>(a.dY) + c0, row, a.lddy);
+            ring.fetch(to, 1, static_cast<const T*>(a.Z) + c0, row, a.ldz);
+        });
+    };
+#pragma unroll
+    for (int s = 0; s < TURN_STAGES; ++s) ask(s, first + s * step);
+    float sum[R][A::N];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < A::N; ++j) sum[i][j] = 0.f;
+    int turn = 0;
+    uint32_t row = first;
+    for (; row < N; row += step, turn ^= 1, ring.next()) {
+        volatile int* flag = &late[turn][ring.group];
+        const bool ok = ring.wait(flag, err, timeout_ns);
+        Word g[R], z[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) g[i] = ring.at(0, i), z[i] = ring.at(1, i);
+        group_sync<NT>(ring.group);
+        if (!ok || (NT > 32 && *flag)) break;   // the whole group
+        ask(ring.k, row + TURN_STAGES * step);
+        Word* out = reinterpret_cast<Word*>(static_cast<T*>(a.dZ) + (int64_t)row * a.F + c0) + ring.t;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            float v[A::N], s[A::N];
+            A::unpack(g[i], v);
+            A::unpack(z[i], s);
+            auto apply = [&](auto fixed) {
+#pragma unroll
+                for (int j = 0; j < A::N; ++j) v[j] *= slope<T>(decltype(fixed)::value, s[j]);
+            };
+            switch (act) {
+                case TPMLP_ACT_RELU: apply(std::integral_constant<int, TPMLP_ACT_RELU>()); break;
+                case TPMLP_ACT_GELU_ERF: apply(std::integral_constant<int, TPMLP_ACT_GELU_ERF>()); break;
+                case TPMLP_ACT_GELU_SIGMOID: apply(std::integral_constant<int, TPMLP_ACT_GELU_SIGMOID>()); break;
+                default: apply(std::integral_constant<int, TPMLP_ACT_GELU_TANH>()); break;
+            }
+#pragma unroll
+            for (int j = 0; j < A::N; ++j) sum[i][j] += v[j];
+            const Word o = A::pack(v);
+            if (ring.mine(i)) out[i * NT] = o;
+        }
+    }
+    if (row < N) ring.drain((N - row + step - 1) / step, &late[turn][ring.group], err, timeout_ns);
+    if (a.db[0] == nullptr) return;
+    // the groups' sums in their order, through the ring's memory
+    float* sums = reinterpret_cast<float*>(ring_memory);
+    static_assert(NT * R * A::N * sizeof(float) <= Ring::MOST, "room for a sum a column");
+    for (int q = 0; q < Ring::GROUPS; ++q) {
+        __syncthreads();
+        if (ring.group == q)
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                if (ring.mine(i))
+#pragma unroll
+                    for (int j = 0; j < A::N; ++j) {
+                        float* at = sums + (ring.t + i * NT) * A::N + j;
+                        *at = q > 0 ? *at + sum[i][j] : sum[i][j];
+                    }
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < cols; c += TURN_THREADS) a.part[(int64_t)chunk * a.F + c0 + c] = sums[c];
+}
+
 // 32 columns to a CTA, eight threads to a column's chunks.
 template <typename T>
 __global__ void __launch_bounds__(256) dact_sums_kernel(const DactParams p) {
@@ -92,26 +183,12 @@ __global__ void __launch_bounds__(256) dact_sums_kernel(const DactParams p) {
     }
 }
 
+// row chunks of the form without turns
 int64_t chunks(int64_t N, int64_t F) {
     const int64_t blocks = (F + 1023) / 1024;
     int64_t S = 16LL * 152 / blocks;
     if (S > (N + 7) / 8) S = (N + 7) / 8;
     return S < 1 ? 1 : S > 1024 ? 1024 : S;
-}
-
-template <typename... P, typename... A>
-tpmlp_status launch(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.stream = s;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return TPMLP_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
 }
 
 template <typename T, int B>
@@ -130,17 +207,63 @@ tpmlp_status dact(int act, const DactParams& p, cudaStream_t s) {
     return launch(dact_sums_kernel<T>, dim3((unsigned)((p.a.F + 31) / 32)), 256, s, p);
 }
 
+// Panels of 16-byte accesses, the CTAs of each (two an SM in all).
+struct Turns {
+    int panels, width, chunks;
+};
+Turns turns_of(int64_t F, int elems) {
+    Turns t;
+    t.panels = (int)((F + LONGEST - 1) / LONGEST);
+    t.width = (int)((F / elems + t.panels - 1) / t.panels) * elems;
+    t.panels = (int)((F + t.width - 1) / t.width);
+    t.chunks = 2 * TURN_CTAS / t.panels > 0 ? 2 * TURN_CTAS / t.panels : 1;
+    return t;
+}
+
+template <typename T>
+tpmlp_status dact_turns(int act, DactParams p, cudaStream_t s) {
+    int* err = device_error_word();
+    if (err == nullptr) return TPMLP_ERR_CUDA;
+    LaunchScope ls("linear_dact", s);
+    const Turns t = turns_of(p.a.F, 16 / (int)sizeof(T));
+    p.S = t.chunks;
+    const tpmlp_status st = with_group<TURN_THREADS>(t.width, [&](auto nt, auto full) {
+        constexpr int NT = decltype(nt)::value;
+        // (a last panel may be narrower)
+        auto go = [&](auto whole) {
+            constexpr bool FULL = decltype(whole)::value;
+            using Ring = RowRing<T, 16, 2, TURN_STAGES, TURN_THREADS, NT, FULL>;
+            static std::atomic<uint64_t> asked{0};
+            if (!allow_smem(dact_turns_kernel<T, NT, FULL>, Ring::MOST, asked)) return TPMLP_ERR_CUDA;
+            return launch_smem(dact_turns_kernel<T, NT, FULL>, dim3((unsigned)(t.panels * t.chunks)), TURN_THREADS,
+                               Ring::MOST, s, p, act, t.panels, t.width, err, wait_timeout_ns());
+        };
+        return decltype(full)::value && p.a.F == (int64_t)t.panels * t.width ? go(std::true_type()) : go(std::false_type());
+    });
+    if (st != TPMLP_OK || p.a.db[0] == nullptr) return st;
+    return launch(dact_sums_kernel<T>, dim3((unsigned)((p.a.F + 31) / 32)), 256, s, p);
+}
+
 }  // namespace
 
 size_t dact_part_bytes(int64_t N, int64_t F) {
-    return ((size_t)chunks(N, F) * (size_t)F * sizeof(float) + 255) & ~(size_t)255;
+    int64_t S = chunks(N, F);
+    for (int elems = 4; elems <= 8; elems += 4) {
+        const int64_t t = turns_of(F, elems).chunks;
+        if (t > S) S = t;
+    }
+    return ((size_t)S * (size_t)F * sizeof(float) + 255) & ~(size_t)255;
 }
 
 tpmlp_status run_dact(int f32, int act, const DactArgs& a, cudaStream_t s) {
     const DactParams p{a, (int)chunks(a.N, a.F)};
-    if (!f32) return dact<__nv_bfloat16, 16>(act, p, s);   // 16-byte rows: the bf16 path's rule
-    const bool wide = a.F % 4 == 0 && access_fits(a.dY, a.lddy * 4, 16) && access_fits(a.Z, a.ldz * 4, 16) &&
-                      access_fits(a.dZ, a.F * 4, 16);
+    const int elems = f32 ? 4 : 8, size = f32 ? 4 : 2;
+    const bool wide = a.F % elems == 0 && access_fits(a.dY, a.lddy * size, 16) && access_fits(a.Z, a.ldz * size, 16) &&
+                      access_fits(a.dZ, a.F * size, 16);   // on the bf16 path always
+    // rows in turn: from four rows a group on
+    if (wide && !a.rest && a.N * a.F >= 8LL * TURN_CTAS * LONGEST)
+        return f32 ? dact_turns<float>(act, p, s) : dact_turns<__nv_bfloat16>(act, p, s);
+    if (!f32) return dact<__nv_bfloat16, 16>(act, p, s);
     return wide ? dact<float, 16>(act, p, s) : dact<float, 4>(act, p, s);
 }
 
