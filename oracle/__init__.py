@@ -26,6 +26,9 @@ What it computes (plain definitions, no blocking, fusion or reordering):
 - ``vocab``: token log probabilities with entropy, rank and top tokens;
   distillation from a teacher's top tokens and its gradient; the embedding
   table's gradient.
+- ``norm``: layer norm and its gradients; ``linear``: one linear layer with bias,
+  activation and residual, and its gradients; ``vocab.policy``: the clipped policy
+  loss with a KL term, and its gradient.
 - ``embedding.vocab_embedding``: out[n] = E[ids[n]] (textbook §4.2.3, course
   notes §3.4 "TP for Embedding").
 - ``sharded``: the per-shard algorithm (column shard -> local activation ->
@@ -42,4 +45,4 @@ torch.logsumexp for the cross-entropy. Every function here has at least one
 pin; none is "parity unpinned".
 """
 
-from . import mlp, ce, sharded, embedding, vocab  # noqa: F401
+from . import mlp, ce, sharded, embedding, vocab, norm, linear  # noqa: F401

@@ -105,3 +105,60 @@ def embedding_backward(ids, dout, V, scale):
     ok = (ids >= 0) & (ids < V)
     np.add.at(d, ids[ok], dout[ok])
     return scale * d
+
+
+def _policy_row(z, t, old, adv, ref, kl, low, high, tau):
+    """(loss, l, k, dloss / dl) of one token; ref None: no KL term."""
+    l = _ln_p(z / tau)[t]
+    with np.errstate(over="ignore", invalid="ignore"):
+        rho = np.exp(l - old)
+        loss = slope = 0.0
+        if adv != 0:
+            held = rho > 1 + high if adv > 0 else rho < 1 - low
+            loss = -adv * ((1 + high if adv > 0 else 1 - low) if held else rho)
+            slope = 0.0 if held else -adv * rho
+        k = 0.0
+        if ref is not None:
+            r = ref - l
+            k = np.inf if r == np.inf else np.expm1(r) - r
+            if kl:
+                loss += kl * k
+                slope -= kl * np.expm1(r)
+    return loss, l, k, slope
+
+
+def policy(logits, targets, old, adv, ref, kl, low, high, tau):
+    """Clipped policy loss with a KL term; see tpmlp_vocab_policy. A negative target
+    is no token: zeros."""
+    z_all, t_all, old, adv = as_f64(logits), _ints(targets), as_f64(old), as_f64(adv)
+    ref = None if ref is None else as_f64(ref)
+    N = z_all.shape[0]
+    out = {k: np.zeros(N) for k in ("loss", "logprob", "kl")}
+    for n in range(N):
+        if t_all[n] >= 0:
+            out["loss"][n], out["logprob"][n], out["kl"][n], _ = _policy_row(
+                z_all[n], t_all[n], old[n], adv[n], None if ref is None else ref[n], kl, low, high, tau)
+    out["mean"] = out["loss"].mean() if N else float("nan")
+    return out
+
+
+def policy_backward(logits, targets, old, adv, ref, kl, low, high, tau, grad):
+    """d(sum_n grad[n] loss[n]) / dlogits; grad is a number or one per token."""
+    z_all, t_all, old, adv = as_f64(logits), _ints(targets), as_f64(old), as_f64(adv)
+    ref = None if ref is None else as_f64(ref)
+    N, V = z_all.shape
+    g = np.broadcast_to(as_f64(grad), (N,))
+    d = np.zeros((N, V))
+    for n in range(N):
+        t = t_all[n]
+        if t < 0:
+            continue
+        slope = _policy_row(z_all[n], t, old[n], adv[n], None if ref is None else ref[n], kl, low, high, tau)[3]
+        w = g[n] * slope / tau
+        if w == 0:
+            continue
+        p = np.exp(_ln_p(z_all[n] / tau))
+        d[n] = -w * p
+        p[t] = 0.0
+        d[n, t] = w * p.sum()   # 1 - p_t, with its digits
+    return d
