@@ -676,6 +676,12 @@ tpmlp_status tpmlp_selftest_gemm_stall(int role);
  * launch's own (it also takes part in the GEMMs' stall above). */
 tpmlp_status tpmlp_selftest_weight_grad_stall(int role);
 
+/* While on is 1, the kernels that take rows in turn (layer norm and its gradient
+ * over many rows, the split linear layer's dZ) wait on a barrier that nothing
+ * completes; they drain their copies and leave, as after a real timeout. 0 turns
+ * it off; other values return TPMLP_ERR_ARG. */
+tpmlp_status tpmlp_selftest_row_stall(int on);
+
 /* ---- instrumentation ---------------------------------------------------- */
 
 /* Launch configuration the bf16 tensor-core GEMM chooses on the current

@@ -31,6 +31,7 @@ from ._binding import (  # noqa: F401
     tpmlp_row_linear,
     tpmlp_row_linear_backward,
     tpmlp_selftest_gemm_stall,
+    tpmlp_selftest_row_stall,
     tpmlp_selftest_wait_timeout,
     tpmlp_selftest_weight_grad_stall,
     tpmlp_set_wait_timeout_ns,

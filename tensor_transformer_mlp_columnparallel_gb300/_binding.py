@@ -107,6 +107,7 @@ _SIGNATURES = {
     "tpmlp_selftest_wait_timeout": (_int, [ctypes.c_uint64, _vp]),
     "tpmlp_selftest_gemm_stall": (_int, [_int]),
     "tpmlp_selftest_weight_grad_stall": (_int, [_int]),
+    "tpmlp_selftest_row_stall": (_int, [_int]),
     "tpmlp_launch_count": (ctypes.c_int64, []),
     "tpmlp_gemm_plan": (_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _int, _int, _int,
                                _int, ctypes.POINTER(_int), ctypes.POINTER(_int),
@@ -734,6 +735,12 @@ def tpmlp_selftest_gemm_stall(role: int):
 def tpmlp_selftest_weight_grad_stall(role: int):
     """The same for the launch of few-token weight gradients alone."""
     _check(lib().tpmlp_selftest_weight_grad_stall(int(role)))
+
+
+def tpmlp_selftest_row_stall(on: int):
+    """While on is 1, every kernel that takes rows in turn waits on a barrier that
+    nothing completes until the bounded wait runs out."""
+    _check(lib().tpmlp_selftest_row_stall(int(on)))
 
 
 def tpmlp_launch_count() -> int:

@@ -41,6 +41,7 @@ int g_sms[kMaxDevices] = {};
 std::atomic<uint64_t> g_timeout_ns{2000000000ull};
 std::atomic<int> g_gemm_stall{0};
 std::atomic<int> g_weight_grad_stall{0};
+std::atomic<int> g_row_stall{0};
 std::atomic<int64_t> g_launches{0};
 
 int current_device() {
@@ -65,6 +66,8 @@ int* device_error_word() {
 uint64_t wait_timeout_ns() { return g_timeout_ns.load(); }
 
 int gemm_stall_role() { return g_gemm_stall.load(); }
+
+int row_stall() { return g_row_stall.load(); }
 
 int weight_grad_stall_role() {
     const int own = g_weight_grad_stall.load();
@@ -1502,6 +1505,12 @@ tpmlp_status tpmlp_selftest_gemm_stall(int role) {
 tpmlp_status tpmlp_selftest_weight_grad_stall(int role) {
     if (role < 0 || role > 3) return TPMLP_ERR_ARG;
     g_weight_grad_stall.store(role);
+    return TPMLP_OK;
+}
+
+tpmlp_status tpmlp_selftest_row_stall(int on) {
+    if (on != 0 && on != 1) return TPMLP_ERR_ARG;
+    g_row_stall.store(on);
     return TPMLP_OK;
 }
 

@@ -71,6 +71,7 @@ struct NormArgs {
     float* rstd;
     int* err;
     uint64_t timeout_ns;
+    int stall;       // failure-detection self test
 };
 
 // A row's statistics: the row, times scale (1 but for rows whose squares
@@ -274,6 +275,7 @@ __global__ void __launch_bounds__(NORM_THREADS, 2) layernorm_turns_kernel(const 
     extern __shared__ __align__(16) uint4 ring_memory[];
     __shared__ uint64_t bars[Ring::GROUPS * STAGES];
     __shared__ float red[3 * WIDEST / 32][2];
+    __shared__ uint64_t spare[Ring::GROUPS];
     __shared__ int late[2][Ring::GROUPS];   // a wait of this turn ran out
     if (threadIdx.x < 2 * Ring::GROUPS) (&late[0][0])[threadIdx.x] = 0;
     __syncthreads();
@@ -296,7 +298,8 @@ __global__ void __launch_bounds__(NORM_THREADS, 2) layernorm_turns_kernel(const 
     }
     int turn = 0;
     uint32_t row = first;
-    for (; row < N; row += step, turn ^= 1, ring.next()) {
+    const bool go = !a.stall || ring.stall(&spare[ring.group], &late[0][ring.group], a.err, a.timeout_ns);
+    for (; go && row < N; row += step, turn ^= 1, ring.next()) {
         volatile int* flag = &late[turn][ring.group];
         bool ok = ring.wait(flag, a.err, a.timeout_ns);
         Word held[R];
@@ -380,6 +383,7 @@ struct NormGradArgs {
     int S;
     int* err;
     uint64_t timeout_ns;
+    int stall;
 };
 
 // Up to this many deviations a row's fp32 mean is near enough for h (it is off by
@@ -406,6 +410,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const NormGr
     extern __shared__ __align__(16) uint4 ring_memory[];
     __shared__ uint64_t bars[Ring::GROUPS * STAGES];
     __shared__ float red[2][GRAD_THREADS / 32][3];
+    __shared__ uint64_t spare[Ring::GROUPS];
     __shared__ int late[2][Ring::GROUPS];
     if (threadIdx.x < 2 * Ring::GROUPS) (&late[0][0])[threadIdx.x] = 0;
     __syncthreads();
@@ -436,7 +441,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const NormGr
     if (first < N) m_next = a.mean[first], r_next = a.rstd[first];
     int turn = 0;
     uint32_t row = first;
-    for (; row < N; row += step, turn ^= 1, ring.next()) {
+    const bool go = !a.stall || ring.stall(&spare[ring.group], &late[0][ring.group], a.err, a.timeout_ns);
+    for (; go && row < N; row += step, turn ^= 1, ring.next()) {
         const float m1 = m_next, r1 = r_next;
         if (row + step < N) m_next = a.mean[row + step], r_next = a.rstd[row + step];
         volatile int* flag = &late[turn][group];
@@ -730,7 +736,7 @@ size_t rows_bytes(int64_t N) { return ((size_t)N * sizeof(float4) + 255) & ~(siz
 tpmlp_status run_layernorm(int f32, int params_f32, const LayernormArgs& g, cudaStream_t s) {
     if (g.N == 0) return TPMLP_OK;
     const NormArgs a{g.N, g.D, g.x, g.ldx, g.weight, g.bias, g.eps, g.y, g.ldy, g.mean, g.rstd,
-                     device_error_word(), wait_timeout_ns()};
+                     device_error_word(), wait_timeout_ns(), row_stall()};
     if (a.err == nullptr) return TPMLP_ERR_CUDA;
     if (f32) return forward_width<float, float>(a, s);
     return params_f32 ? forward_width<__nv_bfloat16, float>(a, s) : forward_width<__nv_bfloat16, __nv_bfloat16>(a, s);
@@ -754,7 +760,7 @@ tpmlp_status run_layernorm_backward(int f32, int params_f32, const LayernormGrad
     }
     NormGradArgs a{g.N, g.D, g.dy, g.lddy, g.x, g.ldx, g.weight, g.mean, g.rstd, g.dresidual, g.lddres,
                    g.dx, g.lddx, g.dweight, g.dbias, nullptr, nullptr, (int)row_chunks(g.N, g.D),
-                   device_error_word(), wait_timeout_ns()};
+                   device_error_word(), wait_timeout_ns(), row_stall()};
     if (a.err == nullptr) return TPMLP_ERR_CUDA;
     a.rows = static_cast<float4*>(workspace);
     if (params) a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + rows_bytes(g.N));

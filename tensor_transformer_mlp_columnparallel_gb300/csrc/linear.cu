@@ -15,6 +15,7 @@ constexpr int COLS = 128;   // threads (accesses) of a CTA
 struct DactParams {
     DactArgs a;
     int S;
+    int stall;   // failure-detection self test
 };
 
 template <typename T> __device__ __forceinline__ float slope(int act, float z);
@@ -77,6 +78,7 @@ __global__ void __launch_bounds__(TURN_THREADS, 2) dact_turns_kernel(const DactP
     constexpr int R = Ring::R;
     extern __shared__ __align__(16) uint4 ring_memory[];
     __shared__ uint64_t bars[Ring::GROUPS * TURN_STAGES];
+    __shared__ uint64_t spare[Ring::GROUPS];
     __shared__ int late[2][Ring::GROUPS];
     const DactArgs& a = p.a;
     const int panel = blockIdx.x % panels, chunk = blockIdx.x / panels;
@@ -103,7 +105,8 @@ __global__ void __launch_bounds__(TURN_THREADS, 2) dact_turns_kernel(const DactP
         for (int j = 0; j < A::N; ++j) sum[i][j] = 0.f;
     int turn = 0;
     uint32_t row = first;
-    for (; row < N; row += step, turn ^= 1, ring.next()) {
+    const bool go = !p.stall || ring.stall(&spare[ring.group], &late[0][ring.group], err, timeout_ns);
+    for (; go && row < N; row += step, turn ^= 1, ring.next()) {
         volatile int* flag = &late[turn][ring.group];
         const bool ok = ring.wait(flag, err, timeout_ns);
         Word g[R], z[R];
@@ -256,7 +259,7 @@ size_t dact_part_bytes(int64_t N, int64_t F) {
 }
 
 tpmlp_status run_dact(int f32, int act, const DactArgs& a, cudaStream_t s) {
-    const DactParams p{a, (int)chunks(a.N, a.F)};
+    const DactParams p{a, (int)chunks(a.N, a.F), row_stall()};
     const int elems = f32 ? 4 : 8, size = f32 ? 4 : 2;
     const bool wide = a.F % elems == 0 && access_fits(a.dY, a.lddy * size, 16) && access_fits(a.Z, a.ldz * size, 16) &&
                       access_fits(a.dZ, a.F * size, 16);   // on the bf16 path always

@@ -127,6 +127,14 @@ struct RowRing {
             phase ^= 1u;
         }
     }
+    // The self test's stall: a wait for `spare`, a barrier of the group that nothing
+    // completes.
+    __device__ __forceinline__ bool stall(uint64_t* spare, volatile int* flag, int* err, uint64_t timeout_ns) const {
+        if (t == 0) mbar_init(smem_u32(spare), 1);
+        fence_mbar_init();
+        group_sync<NT>(group);
+        return wait_inline(smem_u32(spare), 0, flag, err, timeout_ns);
+    }
     // After a wait that ran out: no copy may be in flight into a CTA that leaves.
     // `left` rows from the current one on were asked for.
     __device__ __forceinline__ void drain(uint32_t left, volatile int* flag, int* err, uint64_t timeout_ns) {
