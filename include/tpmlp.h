@@ -34,8 +34,8 @@
  * - The library allocates no device memory. Scratch space is the caller's
  *   `workspace`; tpmlp_workspace_bytes() gives its size.
  * - Output buffers must not overlap input buffers, each other or the
- *   workspace (the one exception is tpmlp_vocab_ce_backward, which may run in
- *   place); overlapping buffers give undefined results.
+ *   workspace, except where an argument's text says that it may be another's
+ *   buffer itself (in place); overlapping buffers give undefined results.
  * - A workspace serves one call at a time: calls whose GPU work can overlap
  *   (other streams, other host threads without ordering) need separate
  *   workspaces; calls on one stream may share one.
@@ -299,7 +299,8 @@ tpmlp_status tpmlp_row_linear_backward(tpmlp_dtype dt, int64_t N, int64_t D, int
  *   x       [N, D] of dt, pitch ldx;  y  [N, D] of dt, pitch ldy; may be x
  *           itself (ldy = ldx)
  *   weight  [D] of param_dt, or NULL (ones);  bias  [D] of param_dt, or NULL (zeros)
- *   eps     finite, not negative; with 0 a row of equal elements gives NaN
+ *   eps     finite, not negative; with 0 a row of equal elements, or one whose
+ *           squared spread underflows fp32, gives no finite result
  *   mean, rstd  [N] fp32 out, or NULL: what the backward takes
  * param_dt is dt or fp32. Any alignment of the elements; 16-byte rows are
  * faster. A row with a NaN or an infinity gives NaN in that row alone; finite
@@ -676,8 +677,8 @@ tpmlp_status tpmlp_selftest_gemm_stall(int role);
  * launch's own (it also takes part in the GEMMs' stall above). */
 tpmlp_status tpmlp_selftest_weight_grad_stall(int role);
 
-/* While on is 1, the kernels that take rows in turn (layer norm and its gradient
- * over many rows, the split linear layer's dZ) wait on a barrier that nothing
+/* While on is 1, the kernels that take rows in turn (layer norm and its
+ * gradient, the split linear layer's dZ, over many rows) wait on a barrier that nothing
  * completes; they drain their copies and leave, as after a real timeout. 0 turns
  * it off; other values return TPMLP_ERR_ARG. */
 tpmlp_status tpmlp_selftest_row_stall(int on);

@@ -16,7 +16,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtpmlp.so")
 SOURCES = ["api.cu", "gemm_tc.cu", "gemm_simt.cu", "hbm_kernels.cu", "vocab_ops.cu", "vocab_policy.cu",
            "embedding_grad.cu", "weight_grad.cu", "layernorm.cu",
-           "linear.cu", "noalloc.cu"]
+           "layernorm_grad.cu", "linear.cu", "noalloc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -251,8 +251,8 @@ int64_t sk_units_bound(int64_t D, int64_t Fs, int T) {
     const int64_t b = ((D + 127) / 128) * ((Fs + 63) / 64);
     return (int64_t)T * (a > b ? a : b);
 }
-// The gated backward (and the split linear layers) have none for N <= 64: dealt out, its few-token products
-// took up to twice as long as whole tiles and the K split across a cluster
+// The gated backward and the split linear layers have none for N <= 64: dealt out,
+// its few-token products took up to twice as long as whole tiles and the K split across a cluster
 // (N = 16, F = 16384, T = 4 on GB300: dX 98 us against 47 us at D = 2048).
 size_t sk_bytes(tpmlp_op op, tpmlp_dtype dt, int64_t N, int64_t D, int64_t F, int T) {
     const bool block = op == TPMLP_OP_FORWARD || op == TPMLP_OP_BACKWARD;

@@ -1,11 +1,9 @@
-// Layer norm over rows, forward and backward.
+// Layer norm over rows.
 //
 //   mean = sum x / D,  var = sum (x - mean)^2 / D,  rstd = 1 / sqrt(var + eps)
-//   h = (x - mean) rstd,  y = h w + b
-//   u = dy w,  dx = rstd (u - sum u / D - h (sum u h) / D) + dresidual
-//   dw = sum_n dy h,  db = sum_n dy
+//   y = (x - mean) rstd w + b
 //
-// Memory bounds both: a row's elements are read once and written once. The
+// Memory bounds it: a row's elements are read once and written once. The
 // variance is taken around the row's own mean (a second pass over the elements
 // a thread holds), never as a difference of squares. The fp32 mean m of a row
 // far from zero is off by its sum's rounding, which is not small next to the
@@ -16,47 +14,13 @@
 // mean's relative error 2e-6 instead of 4e-8).
 #include <cuda_bf16.h>
 
-#include "row_ring.cuh"
+#include "row_sums.cuh"
 
 namespace tpmlp {
 namespace {
 
 constexpr int HELD_WORDS = 32;   // 32-bit registers of a row that a thread of layernorm_kernel holds
 constexpr int WIDEST = 1024;     // threads of the widest row
-constexpr int NORM_THREADS = 256, GRAD_THREADS = 512;   // of a CTA that takes rows in turn
-constexpr int MOST_CTAS = 152;   // of the backward's CTAs that stay: one an SM
-
-// Sums (maxima) of V numbers over a group of NT threads (a power of two up to
-// 1024), in every one of them. red: where the CTA's warps put theirs; not the
-// place that the sum before used, so that one barrier is enough.
-template <int NT, int V, typename Op>
-__device__ __forceinline__ void group_reduce(float (&v)[V], int group, float (*red)[V], Op op) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-        for (int k = 0; k < V; ++k) v[k] = op(v[k], __shfl_xor_sync(0xffffffffu, v[k], off));
-    if constexpr (NT > 32) {
-        constexpr int WARPS = NT / 32;
-        const int lane = threadIdx.x & 31, warp = (threadIdx.x / 32) & (WARPS - 1);
-        red += group * WARPS;
-        if (lane == 0)
-#pragma unroll
-            for (int k = 0; k < V; ++k) red[warp][k] = v[k];
-        group_sync<NT>(group);
-#pragma unroll
-        for (int k = 0; k < V; ++k) v[k] = red[lane & (WARPS - 1)][k];
-#pragma unroll
-        for (int off = WARPS / 2; off > 0; off >>= 1)
-#pragma unroll
-            for (int k = 0; k < V; ++k) v[k] = op(v[k], __shfl_xor_sync(0xffffffffu, v[k], off));
-    }
-}
-struct Add {
-    __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
-};
-struct Max {
-    __device__ __forceinline__ float operator()(float a, float b) const { return max_nan(a, b); }
-};
 
 struct NormArgs {
     int64_t N, D;
@@ -74,6 +38,11 @@ struct NormArgs {
     int stall;       // failure-detection self test
 };
 
+// 16-byte aligned, whole 16-byte words
+__device__ __forceinline__ void bulk_prefetch_l2(const void* p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // A row's statistics: the row, times scale (1 but for rows whose squares
 // overflow, which the caller's rescale has multiplied by 2^-100), has mean m + d
 // and reciprocal deviation r.
@@ -85,22 +54,23 @@ struct RowStats {
     }
 };
 
+// Where the warps put their parts of the sums.
+struct Red {
+    float sum[WIDEST / 32][1], spread[WIDEST / 32][2], most[WIDEST / 32][1];
+};
+
 // sum(): over the elements that this thread looks after; spread(m, v): of their
-// distances from m (v[0]) and those squared (v[1]); summed() runs once every
-// thread's first sum is in. Returns false where the squares overflow (or a NaN or
-// an infinity is in the row), the same for every thread of the row.
-using Red = float (*)[2];
-template <int NT, typename Sum, typename Spread, typename Summed>
-__device__ __forceinline__ bool row_stats(RowStats& s, int64_t D, float eps, int group, Red red, Sum sum, Spread spread,
-                                          Summed summed) {
+// distances from m (v[0]) and those squared (v[1]). Returns false where the squares
+// overflow (or a NaN or an infinity is in the row), the same for every thread of
+// the row.
+template <int NT, typename Sum, typename Spread>
+__device__ __forceinline__ bool row_stats(RowStats& s, int64_t D, float eps, int group, Red& red, Sum sum, Spread spread) {
     const float inv = 1.f / (float)D;
-    float v[2] = {sum(), 0.f};
-    group_reduce<NT>(v, group, red, Add());
-    s.m = v[0] * inv;
-    summed();
-    v[0] = v[1] = 0.f;
+    float c[1] = {sum()}, v[2] = {0.f, 0.f};
+    group_reduce<NT>(c, group, red.sum, Add());
+    s.m = c[0] * inv;
     spread(s.m, v);
-    group_reduce<NT>(v, group, red + WIDEST / 32, Add());
+    group_reduce<NT>(v, group, red.spread, Add());
     const float var = v[1] * inv;
     s.d = s.m * s.m > var ? v[0] * inv : 0.f;
     s.r = 1.f / sqrtf(fmaf(eps * s.scale, s.scale, max_nan(fmaf(-s.d, s.d, var), 0.f)));
@@ -111,7 +81,7 @@ __device__ __forceinline__ bool row_stats(RowStats& s, int64_t D, float eps, int
 // one access of B bytes at a time. Finite elements whose squares overflow are
 // taken times 2^-100.
 template <typename T, typename W, int B, int NT>
-__device__ __forceinline__ void long_row(const NormArgs& a, int64_t row, int t, int group, float (*red)[2]) {
+__device__ __forceinline__ void long_row(const NormArgs& a, int64_t row, int t, int group, Red& red) {
     using A = Access<T, B>;
     using Word = typename A::Word;
     const int64_t accesses = a.D / A::N;
@@ -140,13 +110,12 @@ __device__ __forceinline__ void long_row(const NormArgs& a, int64_t row, int t, 
                     v[0] += e - m;
                     v[1] = fmaf(e - m, e - m, v[1]);
                 });
-            },
-            [] {});
+            });
     };
     if (!take()) {
-        float big[2] = {0.f, 0.f};
+        float big[1] = {0.f};
         each([&](float v) { big[0] = max_nan(big[0], fabsf(v)); });
-        group_reduce<NT>(big, group, red + 2 * (WIDEST / 32), Max());
+        group_reduce<NT>(big, group, red.most, Max());
         if (big[0] < INFINITY) {
             s.scale = 0x1p-100f;
             take();
@@ -171,43 +140,66 @@ __device__ __forceinline__ void long_row(const NormArgs& a, int64_t row, int t, 
 // arguments by value (by address, they are read again after every barrier: 58 us
 // against 44 for 8192 rows of 8192 bf16).
 template <typename T, typename W, int B, int NT>
-__device__ __noinline__ void huge_row(const NormArgs a, int64_t row, int t, int group, float (*red)[2]) {
-    long_row<T, W, B, NT>(a, row, t, group, red);
+__device__ __noinline__ void huge_row(const NormArgs a, int64_t row, int t, int group, Red* red) {
+    long_row<T, W, B, NT>(a, row, t, group, *red);
 }
 
 template <typename T, typename W, int B>
 __global__ void __launch_bounds__(WIDEST) layernorm_long_kernel(const NormArgs a) {
-    __shared__ float red[3 * WIDEST / 32][2];
+    __shared__ Red red;
     pdl_wait();
     pdl_launch_dependents();
     long_row<T, W, B, WIDEST>(a, blockIdx.x, threadIdx.x, 0, red);
 }
 
-// The row in the registers of NT threads (a warp: four rows to a CTA), every
-// access of B bytes, up to 32 words a thread.
-template <typename T, typename W, int B, int NT>
-__global__ void __launch_bounds__(NT < 128 ? 128 : NT) layernorm_kernel(const NormArgs a) {
+// The row in the registers of NT threads, R accesses of B bytes each (groups of up
+// to a warp: 128 threads to a CTA; a larger group is a CTA, whose one barrier the
+// compiler knows: two groups of 64 in a CTA took 53 us where one takes 42). What
+// hides one row's two reductions is the other rows of the SM. 8192 x 8192 bf16 with
+// bf16 parameters on GB300: 42.4 us, 6.3 TB/s read and written, 0.93 of a copy's
+// rate; fp32 rows of 1024 to 8192 elements 6.4 to 6.6.
+// EARLY: the parameters too, from the start, for few rows, whose time is one row's
+// latency. Else they are read when the row's statistics are known, from L1 or L2;
+// where a step has driven them out, all of the first rows would wait for memory
+// there: the first CTA has them brought to L2 ahead of its own row (8192 x 8192
+// bf16, 43.2 us against 44.8; with fp32 parameters 48.7 against 51.5).
+template <typename T, typename W, int B, int NT, int R, bool EARLY>
+__global__ void __launch_bounds__(NT > 32 ? NT : 128) layernorm_kernel(const NormArgs a) {
     using A = Access<T, B>;
     using Word = typename A::Word;
     using Pair = typename A::Pair;
     constexpr int P = A::PAIRS;
-    constexpr int R = B >= 4 ? HELD_WORDS * 4 / B : HELD_WORDS;
-    constexpr int GROUPS = NT < 128 ? 128 / NT : 1;
-    __shared__ float red[3 * WIDEST / 32][2];
+    constexpr int GROUPS = NT > 32 ? 1 : 128 / NT;
+    __shared__ Red red;
+    if (!EARLY && B >= 8 && blockIdx.x == 0 && threadIdx.x == 0) {
+        const uint32_t bytes = (uint32_t)(a.D * sizeof(W));   // of whole 16-byte words
+        if (a.w) bulk_prefetch_l2(a.w, bytes);
+        if (a.b) bulk_prefetch_l2(a.b, bytes);
+    }
     pdl_wait();
     pdl_launch_dependents();
-    const int group = threadIdx.x / NT, t = threadIdx.x % NT;
+    const int group = GROUPS > 1 ? threadIdx.x / NT : 0, t = threadIdx.x % NT;
     const int64_t row = (int64_t)blockIdx.x * GROUPS + group;
-    if (row >= a.N) return;   // a whole warp
+    if (row >= a.N) return;   // a whole group
     const int accesses = (int)(a.D / A::N);
-    const Word* x = reinterpret_cast<const Word*>(static_cast<const T*>(a.x) + row * a.ldx) + t;
-    Word held[R];
     auto each = [&](auto f) {
 #pragma unroll
         for (int i = 0; i < R; ++i)
             if (t + i * NT < accesses) f(i);
     };
+    const Word* x = reinterpret_cast<const Word*>(static_cast<const T*>(a.x) + row * a.ldx) + t;
+    const W* pw = static_cast<const W*>(a.w) + t * A::N;
+    const W* pb = static_cast<const W*>(a.b) + t * A::N;
+    auto params = [&](int i, Pair (&u)[P], Pair (&v)[P]) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) u[j] = A::both(1.f), v[j] = A::both(0.f);
+        if (a.w) load_params<W, A::N>(pw + i * NT * A::N, u);
+        if (a.b) load_params<W, A::N>(pb + i * NT * A::N, v);
+    };
+    Word held[R];
+    Pair w[EARLY ? R : 1][P], b[EARLY ? R : 1][P];
     each([&](int i) { held[i] = x[i * NT]; });
+    if constexpr (EARLY) each([&](int i) { params(i, w[i], b[i]); });
     RowStats s{1.f, 0.f, 0.f, 0.f};
     const bool fine = row_stats<NT>(
         s, a.D, a.eps, group, red,
@@ -234,24 +226,21 @@ __global__ void __launch_bounds__(NT < 128 ? 128 : NT) layernorm_kernel(const No
                 }
             });
             sums[0] = A::total(c), sums[1] = A::total(q);
-        },
-        [] {});
+        });
     if (!fine) {   // the same for every thread of the row
         group_sync<NT>(group);
-        huge_row<T, W, B, NT>(a, row, t, group, red);
+        huge_row<T, W, B, NT>(a, row, t, group, &red);
         return;
     }
     Word* y = reinterpret_cast<Word*>(static_cast<T*>(a.y) + row * a.ldy) + t;
     const Pair m = A::both(-s.m), r = A::both(s.r), dr = A::both(-s.d * s.r);
     each([&](int i) {
-        Pair v[P], w[P], b[P];
-#pragma unroll
-        for (int j = 0; j < P; ++j) w[j] = A::both(1.f), b[j] = A::both(0.f);
-        if (a.w) load_params<W, A::N>(static_cast<const W*>(a.w) + (t + i * NT) * A::N, w);
-        if (a.b) load_params<W, A::N>(static_cast<const W*>(a.b) + (t + i * NT) * A::N, b);
+        const int k = EARLY ? i : 0;
+        if constexpr (!EARLY) params(i, w[0], b[0]);
+        Pair v[P];
         A::unpack(held[i], v);
 #pragma unroll
-        for (int j = 0; j < P; ++j) v[j] = fma2(fma2(add2(v[j], m), r, dr), w[j], b[j]);
+        for (int j = 0; j < P; ++j) v[j] = fma2(fma2(add2(v[j], m), r, dr), w[k][j], b[k][j]);
         y[i * NT] = A::pack(v);
     });
     if (t == 0) s.write(a, row);
@@ -259,28 +248,27 @@ __global__ void __launch_bounds__(NT < 128 ? 128 : NT) layernorm_kernel(const No
 
 // --------------------------------------------------------- rows in turn --
 
-template <typename T> constexpr int NORM_STAGES = sizeof(T) == 2 ? 6 : 3;   // 96 KB a CTA, two CTAs an SM
-template <typename T> constexpr int GRAD_STAGES = sizeof(T) == 2 ? 4 : 2;   // 192 KB, one
+constexpr int NORM_THREADS = 256, NORM_STAGES = 6;   // 96 KB of bf16 rows a CTA, two CTAs an SM
 
-// Many rows of 16-byte accesses, up to LONGEST elements each. (8192 x 8192
-// bf16 on GB300: 47 us, 5.7 TB/s read and written; the row in the registers of
-// CTAs that leave 54 to 58, their parameters read from L2 row by row.)
-template <typename T, typename W, int NT, bool FULL>
+// Rows of 16-byte accesses, a CTA to a row, its columns' parameters in registers,
+// for bf16 rows with fp32 parameters, whose 64 bytes of parameters to 16 of x the
+// form above reads again for every row. 8192 x 8192 on GB300: 43.8 us, 6.1 TB/s.
+template <typename T, typename W, bool FULL>
 __global__ void __launch_bounds__(NORM_THREADS, 2) layernorm_turns_kernel(const NormArgs a) {
-    using Ring = RowRing<T, 16, 1, NORM_STAGES<T>, NORM_THREADS, NT, FULL>;
+    constexpr int NT = NORM_THREADS, STAGES = NORM_STAGES;
+    using Ring = RowRing<T, 16, 1, STAGES, NT, NT, FULL>;
     using A = typename Ring::A;
     using Word = typename Ring::Word;
     using Pair = typename A::Pair;
-    constexpr int R = Ring::R, P = A::PAIRS, STAGES = NORM_STAGES<T>;
+    constexpr int R = Ring::R, P = A::PAIRS;
     extern __shared__ __align__(16) uint4 ring_memory[];
-    __shared__ uint64_t bars[Ring::GROUPS * STAGES];
-    __shared__ float red[3 * WIDEST / 32][2];
-    __shared__ uint64_t spare[Ring::GROUPS];
-    __shared__ int late[2][Ring::GROUPS];   // a wait of this turn ran out
-    if (threadIdx.x < 2 * Ring::GROUPS) (&late[0][0])[threadIdx.x] = 0;
+    __shared__ uint64_t bars[STAGES], spare;
+    __shared__ Red red;
+    __shared__ int late[2];   // a wait of this turn ran out
+    if (threadIdx.x < 2) late[threadIdx.x] = 0;
     __syncthreads();
     Ring ring(ring_memory, bars, a.D);
-    const uint32_t N = (uint32_t)a.N, step = gridDim.x * Ring::GROUPS, first = blockIdx.x * Ring::GROUPS + ring.group;
+    const uint32_t N = (uint32_t)a.N, step = gridDim.x, first = blockIdx.x;
     pdl_wait();
     pdl_launch_dependents();
     auto ask = [&](int s, uint32_t row) {
@@ -298,16 +286,16 @@ __global__ void __launch_bounds__(NORM_THREADS, 2) layernorm_turns_kernel(const 
     }
     int turn = 0;
     uint32_t row = first;
-    const bool go = !a.stall || ring.stall(&spare[ring.group], &late[0][ring.group], a.err, a.timeout_ns);
+    const bool go = !a.stall || ring.stall(&spare, &late[0], a.err, a.timeout_ns);
     for (; go && row < N; row += step, turn ^= 1, ring.next()) {
-        volatile int* flag = &late[turn][ring.group];
-        bool ok = ring.wait(flag, a.err, a.timeout_ns);
+        volatile int* flag = &late[turn];
+        const bool ok = ring.wait(flag, a.err, a.timeout_ns);
         Word held[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) held[i] = ring.at(0, i);
         RowStats s{1.f, 0.f, 0.f, 0.f};
         const bool fine = row_stats<NT>(
-            s, a.D, a.eps, ring.group, red,
+            s, a.D, a.eps, 0, red,
             [&] {
                 Pair c = A::both(0.f);
 #pragma unroll
@@ -334,15 +322,12 @@ __global__ void __launch_bounds__(NORM_THREADS, 2) layernorm_turns_kernel(const 
                     }
                 }
                 sums[0] = A::total(c), sums[1] = A::total(q);
-            },
-            [&] {
-                ok = ok && !(NT > 32 && *flag);
-                if (ok) ask(ring.k, row + STAGES * step);   // every thread holds its elements
             });
-        if (!ok) break;   // the whole group
+        if (!ok || *flag) break;   // the whole group
+        ask(ring.k, row + STAGES * step);   // every thread holds its elements
         if (!fine) {
-            group_sync<NT>(ring.group);   // red is read
-            huge_row<T, W, 16, NT>(a, row, ring.t, ring.group, red);
+            group_sync<NT>(0);   // red is read
+            huge_row<T, W, 16, NT>(a, row, ring.t, 0, &red);
             continue;
         }
         Word* y = reinterpret_cast<Word*>(static_cast<T*>(a.y) + (int64_t)row * a.ldy) + ring.t;
@@ -358,304 +343,56 @@ __global__ void __launch_bounds__(NORM_THREADS, 2) layernorm_turns_kernel(const 
         }
         if (ring.t == 0) s.write(a, row);
     }
-    if (row < N) ring.drain((N - row + step - 1) / step, &late[turn][ring.group], a.err, a.timeout_ns);
+    if (row < N) ring.drain((N - row + step - 1) / step, &late[turn], a.err, a.timeout_ns);
 }
 
-// ------------------------------------------------------------- backward --
+template <int N> using Int = std::integral_constant<int, N>;
 
-struct NormGradArgs {
-    int64_t N, D;
-    const void* dy;
-    int64_t lddy;
-    const void* x;
-    int64_t ldx;
-    const void* w;          // NULL: ones
-    const float* mean;
-    const float* rstd;
-    const void* dres;       // NULL: zeros
-    int64_t lddres;
-    void* dx;
-    int64_t lddx;
-    void* dw;               // NULL (both): not wanted
-    void* db;
-    float4* rows;           // [N]: sum u / D, sum u h / D, d rstd (long rows)
-    float* part;            // [S, 2, D]: a CTA's (long rows: a row chunk's) sums of dy h and dy
-    int S;
-    int* err;
-    uint64_t timeout_ns;
-    int stall;
-};
-
-// Up to this many deviations a row's fp32 mean is near enough for h (it is off by
-// 2^-25 of itself, 2.4e-7 of a deviation at most); beyond, d is taken.
-constexpr float FAR_MEAN = 8.f;
-
-__device__ __forceinline__ void write_param(float* at, float v) { *at = v; }
-__device__ __forceinline__ void write_param(__nv_bfloat16* at, float v) { *at = __float2bfloat16_rn(v); }
-
-// All of it in one reading, for rows of up to LONGEST elements: a thread
-// keeps its columns' sums of dy h and dy over the rows of its group; a CTA's
-// sums go to part[blockIdx.x] (with one CTA to dw and db). Elements beyond the row
-// are zeros and pass through the arithmetic. (8192 x 8192 bf16 with dresidual on
-// GB300: the loop alone 90 us, 6.0 TB/s read and written; without its reductions
-// or its column sums 89: HBM.)
-template <typename T, typename W, int B, int NT, bool FULL, bool RES>
-__global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const NormGradArgs a) {
-    constexpr int Q = RES ? 3 : 2, STAGES = GRAD_STAGES<T>;
-    using Ring = RowRing<T, B, Q, STAGES, GRAD_THREADS, NT, FULL>;
-    using A = typename Ring::A;
-    using Word = typename Ring::Word;
-    using Pair = typename A::Pair;
-    constexpr int R = Ring::R, P = A::PAIRS;
-    extern __shared__ __align__(16) uint4 ring_memory[];
-    __shared__ uint64_t bars[Ring::GROUPS * STAGES];
-    __shared__ float red[2][GRAD_THREADS / 32][3];
-    __shared__ uint64_t spare[Ring::GROUPS];
-    __shared__ int late[2][Ring::GROUPS];
-    if (threadIdx.x < 2 * Ring::GROUPS) (&late[0][0])[threadIdx.x] = 0;
-    __syncthreads();
-    Ring ring(ring_memory, bars, a.D);
-    constexpr int groups = Ring::GROUPS;
-    const int group = ring.group, t = ring.t;
-    const uint32_t N = (uint32_t)a.N, step = gridDim.x * groups, first = blockIdx.x * groups + group;
-    pdl_wait();
-    pdl_launch_dependents();
-    auto ask = [&](int s, uint32_t row) {
-        ring.ask(s, row < N, [&](int to) {
-            ring.fetch(to, 0, a.x, row, a.ldx);
-            ring.fetch(to, 1, a.dy, row, a.lddy);
-            if (RES) ring.fetch(to, Q - 1, a.dres, row, a.lddres);
-        });
-    };
-#pragma unroll
-    for (int s = 0; s < STAGES; ++s) ask(s, first + s * step);
-    Pair w[R][P], sw[R][P], sb[R][P];
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-#pragma unroll
-        for (int j = 0; j < P; ++j) w[i][j] = A::both(1.f), sw[i][j] = sb[i][j] = A::both(0.f);
-        if (a.w && ring.mine(i)) load_params<W, A::N>(static_cast<const W*>(a.w) + (t + i * NT) * A::N, w[i]);
-    }
-    const float inv = 1.f / (float)a.D;
-    float m_next = 0.f, r_next = 0.f;
-    if (first < N) m_next = a.mean[first], r_next = a.rstd[first];
-    int turn = 0;
-    uint32_t row = first;
-    const bool go = !a.stall || ring.stall(&spare[ring.group], &late[0][ring.group], a.err, a.timeout_ns);
-    for (; go && row < N; row += step, turn ^= 1, ring.next()) {
-        const float m1 = m_next, r1 = r_next;
-        if (row + step < N) m_next = a.mean[row + step], r_next = a.rstd[row + step];
-        volatile int* flag = &late[turn][group];
-        const bool ok = ring.wait(flag, a.err, a.timeout_ns);
-        const Pair m = A::both(-m1), r = A::both(r1);
-        Word x[R], g[R];
-        Pair su = A::both(0.f), suh = su, sh = su;
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            x[i] = ring.at(0, i);
-            g[i] = ring.at(1, i);
-            Pair v[P], y[P];
-            A::unpack(x[i], v);
-            A::unpack(g[i], y);
-            const Pair less = FULL || ring.mine(i) ? m : A::both(0.f);
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                const Pair h = mul2(add2(v[j], less), r), u = mul2(y[j], w[i][j]);
-                su = add2(su, u);
-                suh = fma2(u, h, suh);
-                sh = add2(sh, h);
-            }
-        }
-        float s[3] = {A::total(su), A::total(suh), A::total(sh)};
-        group_reduce<NT>(s, group, red[turn], Add());
-        if (!ok || (NT > 32 && *flag)) break;   // the whole group
-        if (!RES) ask(ring.k, row + STAGES * step);   // every thread holds its elements
-        const float d = fabsf(m1 * r1) > FAR_MEAN ? s[2] * inv : 0.f;
-        // dx = r u - r c1 - r c2 h
-        const Pair d1 = A::both(-d), c1 = A::both(-r1 * s[0] * inv), c2 = A::both(-r1 * fmaf(-d, s[0], s[1]) * inv);
-        Word* out = reinterpret_cast<Word*>(static_cast<T*>(a.dx) + (int64_t)row * a.lddx) + t;
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            Pair v[P], y[P], z[P > 1 ? P : 2];
-            A::unpack(x[i], v);
-            A::unpack(g[i], y);
-            if (RES) A::unpack(ring.at(Q - 1, i), *reinterpret_cast<Pair(*)[P]>(&z));
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                const Pair h = fma2(add2(v[j], m), r, d1);
-                sw[i][j] = fma2(y[j], h, sw[i][j]);
-                sb[i][j] = add2(sb[i][j], y[j]);
-                v[j] = fma2(mul2(y[j], w[i][j]), r, fma2(h, c2, RES ? add2(z[j], c1) : c1));
-            }
-            const Word o = A::pack(v);
-            if (ring.mine(i)) out[i * NT] = o;
-        }
-        if (RES) {
-            if (Ring::BULK) group_sync<NT>(group);
-            ask(ring.k, row + STAGES * step);
-        }
-    }
-    if (row < N) ring.drain((N - row + step - 1) / step, &late[turn][group], a.err, a.timeout_ns);
-    if (a.dw == nullptr) return;
-    // the groups' sums in their order, through the ring's memory
-    float* sums = reinterpret_cast<float*>(ring_memory);
-    static_assert(2 * NT * R * A::N * sizeof(float) <= Ring::MOST, "room for two sums a column");
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    const int D = (int)a.D;
-    for (int q = 0; q < groups; ++q) {
-        __syncthreads();
-        if (group == q)
-#pragma unroll
-            for (int i = 0; i < R; ++i)
-                if (ring.mine(i))
-#pragma unroll
-                    for (int j = 0; j < P; ++j) {
-                        Pair* gw = reinterpret_cast<Pair*>(sums + (t + i * NT) * A::N) + j;
-                        Pair* gb = reinterpret_cast<Pair*>(sums + NT * R * A::N + (t + i * NT) * A::N) + j;
-                        *gw = q > 0 ? add2(*gw, sw[i][j]) : sw[i][j];
-                        *gb = q > 0 ? add2(*gb, sb[i][j]) : sb[i][j];
-                    }
-    }
-    __syncthreads();
-    float* part = a.part + (int64_t)blockIdx.x * 2 * D;
-    for (int c = threadIdx.x; c < D; c += GRAD_THREADS) {
-        const float gw = sums[c], gb = sums[NT * R * A::N + c];
-        if (gridDim.x > 1) {
-            part[c] = gw;
-            part[D + c] = gb;
-        } else {
-            write_param(static_cast<W*>(a.dw) + c, gw);
-            write_param(static_cast<W*>(a.db) + c, gb);
-        }
-    }
-}
-
-// Longer rows are read twice. Sums over a row, one CTA each:
 template <typename T, typename W, int B>
-__global__ void __launch_bounds__(256) norm_grad_rows_kernel(const NormGradArgs a) {
-    using A = Access<T, B>;
-    using Word = typename A::Word;
-    __shared__ float red[256 / 32][3];
-    pdl_wait();
-    pdl_launch_dependents();
-    const int64_t row = blockIdx.x;
-    const int64_t accesses = a.D / A::N;
-    const Word* x = reinterpret_cast<const Word*>(static_cast<const T*>(a.x) + row * a.ldx);
-    const Word* dy = reinterpret_cast<const Word*>(static_cast<const T*>(a.dy) + row * a.lddy);
-    const float m = a.mean[row], r = a.rstd[row];
-    float s[3] = {0.f, 0.f, 0.f};   // u, u h, h
-#pragma unroll 2
-    for (int64_t at = threadIdx.x; at < accesses; at += 256) {
-        float v[A::N], g[A::N], w[A::N];
-        A::unpack(x[at], v);
-        A::unpack(dy[at], g);
-        if (a.w) load_params<W, A::N>(static_cast<const W*>(a.w) + at * A::N, w);
-#pragma unroll
-        for (int j = 0; j < A::N; ++j) {
-            const float h = (v[j] - m) * r, u = a.w ? g[j] * w[j] : g[j];
-            s[0] += u;
-            s[1] = fmaf(u, h, s[1]);
-            s[2] += h;
-        }
-    }
-    const float inv = 1.f / (float)a.D;
-    group_reduce<256>(s, 0, red, Add());
-    const float d = fabsf(m * r) > FAR_MEAN ? s[2] * inv : 0.f;
-    if (threadIdx.x == 0) a.rows[row] = make_float4(s[0] * inv, fmaf(-d, s[0], s[1]) * inv, d, 0.f);
-}
-
-// dx, and a row chunk's column sums: a thread has one access's columns.
-template <typename T, typename W, int B>
-__global__ void __launch_bounds__(128) norm_grad_apply_kernel(const NormGradArgs a) {
-    using A = Access<T, B>;
-    using Word = typename A::Word;
-    pdl_wait();
-    pdl_launch_dependents();
-    const int64_t at = (int64_t)blockIdx.x * 128 + threadIdx.x;
-    if (at >= a.D / A::N) return;
-    const int64_t lo = a.N * blockIdx.y / gridDim.y, hi = a.N * (blockIdx.y + 1) / gridDim.y;
-    float w[A::N], sw[A::N], sb[A::N];
-    if (a.w) load_params<W, A::N>(static_cast<const W*>(a.w) + at * A::N, w);
-#pragma unroll
-    for (int j = 0; j < A::N; ++j) {
-        if (!a.w) w[j] = 1.f;
-        sw[j] = sb[j] = 0.f;
-    }
-#pragma unroll 4
-    for (int64_t row = lo; row < hi; ++row) {
-        float v[A::N], g[A::N], e[A::N];
-        A::unpack(reinterpret_cast<const Word*>(static_cast<const T*>(a.x) + row * a.ldx)[at], v);
-        A::unpack(reinterpret_cast<const Word*>(static_cast<const T*>(a.dy) + row * a.lddy)[at], g);
-        if (a.dres) A::unpack(reinterpret_cast<const Word*>(static_cast<const T*>(a.dres) + row * a.lddres)[at], e);
-        const float m = a.mean[row], r = a.rstd[row];
-        const float4 s = a.rows[row];
-#pragma unroll
-        for (int j = 0; j < A::N; ++j) {
-            const float h = fmaf(v[j] - m, r, -s.z);
-            sw[j] = fmaf(g[j], h, sw[j]);
-            sb[j] += g[j];
-            v[j] = r * fmaf(-h, s.y, fmaf(g[j], w[j], -s.x));
-            if (a.dres) v[j] += e[j];
-        }
-        reinterpret_cast<Word*>(static_cast<T*>(a.dx) + row * a.lddx)[at] = A::pack(v);
-    }
-    if (a.part != nullptr) {
-        float* p = a.part + (int64_t)blockIdx.y * 2 * a.D + at * A::N;
-#pragma unroll
-        for (int j = 0; j < A::N; ++j) {
-            p[j] = sw[j];
-            p[a.D + j] = sb[j];
-        }
-    }
-}
-
-// dw and db from the chunks' sums, in chunk order: 32 columns to a CTA, eight
-// threads to a column.
-template <typename W>
-__global__ void __launch_bounds__(256) norm_grad_params_kernel(const NormGradArgs a) {
-    __shared__ float red[8][33];
-    pdl_wait();
-    pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + lane;   // of dw's columns, then db's
-    const int lo = a.S * grp / 8, hi = a.S * (grp + 1) / 8;
-    float s = 0.f;
-    if (c < 2 * a.D) {
-#pragma unroll 8
-        for (int k = lo; k < hi; ++k) s += a.part[(int64_t)k * 2 * a.D + c];
-    }
-    red[grp][lane] = s;
-    __syncthreads();
-    if (grp == 0 && c < 2 * a.D) {
-        for (int k = 1; k < 8; ++k) s += red[k][lane];
-        write_param(static_cast<W*>(c < a.D ? a.dw : a.db) + (c < a.D ? c : c - a.D), s);
-    }
-}
-
-template <typename T, typename W, int NT, bool FULL> tpmlp_status forward_turns(const NormArgs& a, cudaStream_t s) {
-    using Ring = RowRing<T, 16, 1, NORM_STAGES<T>, NORM_THREADS, NT, FULL>;
-    static std::atomic<uint64_t> asked{0};
-    if (!allow_smem(layernorm_turns_kernel<T, W, NT, FULL>, Ring::MOST, asked)) return TPMLP_ERR_CUDA;
-    return launch_smem(layernorm_turns_kernel<T, W, NT, FULL>, dim3((unsigned)(2 * device_sm_count())),
-                       NORM_THREADS, Ring::MOST, s, a);
-}
-
-// Rows in turn: from eight rows a group on, which the parameters' one reading and
-// the ring's start are for.
-template <typename T, typename W, int B>
-tpmlp_status forward(const NormArgs& a, cudaStream_t s) {
+tpmlp_status forward(const NormArgs& a, bool turns, cudaStream_t s) {
     constexpr int R = B >= 4 ? HELD_WORDS * 4 / B : HELD_WORDS;
     const int64_t accesses = a.D / (B / (int)sizeof(T));
     LaunchScope ls("layernorm", s);
-    if constexpr (B == 16)
-        if (a.D <= LONGEST && a.N >= 16LL * device_sm_count() * (LONGEST / a.D))
-            return with_group<NORM_THREADS>(a.D, [&](auto nt, auto full) {
-                return forward_turns<T, W, decltype(nt)::value, decltype(full)::value>(a, s);
-            });
-    if (accesses <= 32 * R)
-        return launch(layernorm_kernel<T, W, B, 32>, dim3((unsigned)((a.N + 3) / 4)), 128, s, a);
-    if (accesses <= 128 * R) return launch(layernorm_kernel<T, W, B, 128>, dim3((unsigned)a.N), 128, s, a);
-    if (accesses <= 512 * R) return launch(layernorm_kernel<T, W, B, 512>, dim3((unsigned)a.N), 512, s, a);
+    tpmlp_status st = TPMLP_OK;
+    // NT threads to a row, `eighths` of R accesses to each, if that is enough. Most
+    // rows want as much of a row a thread as its registers hold (16384 x 4096 bf16:
+    // eight accesses 42 us, four 52), and no idle ones (13107 x 5120: six 44 us, eight
+    // 47; 524288 x 128: two 49, eight 71).
+    auto held = [&](auto nt, auto eighths, auto early) {
+        constexpr int NT = decltype(nt)::value, MOST = R * decltype(eighths)::value / 8;
+        constexpr int GROUPS = NT > 32 ? 1 : 128 / NT;
+        if (accesses > NT * MOST) return false;
+        st = launch(layernorm_kernel<T, W, B, NT, MOST, decltype(early)::value>,
+                    dim3((unsigned)((a.N + GROUPS - 1) / GROUPS)), NT * GROUPS, s, a);
+        return true;
+    };
+    const std::false_type late;
+    if constexpr (sizeof(W) > sizeof(T) && B >= 8)
+        if (turns) {
+            auto go = [&](auto full) {
+                constexpr bool FULL = decltype(full)::value;
+                using Ring = RowRing<T, 16, 1, NORM_STAGES, NORM_THREADS, NORM_THREADS, FULL>;
+                static std::atomic<uint64_t> asked{0};
+                if (!allow_smem(layernorm_turns_kernel<T, W, FULL>, Ring::MOST, asked)) return TPMLP_ERR_CUDA;
+                return launch_smem(layernorm_turns_kernel<T, W, FULL>, dim3((unsigned)(2 * device_sm_count())),
+                                   NORM_THREADS, Ring::MOST, s, a);
+            };
+            return a.D == LONGEST ? go(std::true_type()) : go(std::false_type());
+        }
+    if constexpr (B >= 8) {
+        // up to a row an SM: more threads, less each (152 x 4096 bf16 2.3 us, as above 3.9)
+        const std::true_type early;
+        if (a.N <= device_sm_count() && (held(Int<32>(), Int<2>(), early) || held(Int<128>(), Int<2>(), early) ||
+                                         held(Int<512>(), Int<2>(), early) || held(Int<1024>(), Int<2>(), early)))
+            return st;
+        auto threads = [&](auto nt) { return held(nt, Int<6>(), late) || held(nt, Int<8>(), late); };
+        if (held(Int<8>(), Int<2>(), late) || held(Int<8>(), Int<4>(), late) || threads(Int<8>()) ||
+            threads(Int<16>()) || threads(Int<32>()) || threads(Int<64>()) || threads(Int<128>()) ||
+            threads(Int<256>()) || threads(Int<512>()))
+            return st;
+    } else if (held(Int<32>(), Int<8>(), late) || held(Int<128>(), Int<8>(), late) || held(Int<512>(), Int<8>(), late)) {
+        return st;
+    }
     return launch(layernorm_long_kernel<T, W, B>, dim3((unsigned)a.N), WIDEST, s, a);
 }
 
@@ -668,68 +405,18 @@ tpmlp_status forward_width(const NormArgs& a, cudaStream_t s) {
                access_fits(a.y, a.ldy * sizeof(T), bytes) && access_fits(a.w, 0, params) &&
                access_fits(a.b, 0, params);
     };
-    if (fits(16)) return forward<T, W, 16>(a, s);
-    if constexpr (sizeof(T) == 4) return forward<T, W, 4>(a, s);
-    else return fits(4) ? forward<T, W, 4>(a, s) : forward<T, W, 2>(a, s);
+    // bf16 rows with fp32 parameters by 8 bytes, so that a warp's reads of the
+    // parameters are whole lines (8192 x 8192: 46 us; by 16 bytes 51)
+    constexpr int WIDE = sizeof(W) > sizeof(T) ? 8 : 16;
+    // (fp32 parameters only) rows that fill the turns' ring: 9362 x 7168 48.7 us
+    // against 50.2 held, 8192 x 8192 43.8 against 48.7, but 10922 x 6144 54.6 against
+    // 48.3 (the ring keeps its room, and the threads their work, for 8192 elements); and
+    // eight rows a CTA, for the ring's start (2432 x 8192 14.9 us either way).
+    const bool turns = a.D <= LONGEST && a.D >= LONGEST / 8 * 7 && a.N >= 16LL * device_sm_count() && fits(16);
+    if (fits(WIDE)) return forward<T, W, WIDE>(a, turns, s);
+    if constexpr (sizeof(T) == 4) return forward<T, W, 4>(a, false, s);
+    else return fits(4) ? forward<T, W, 4>(a, false, s) : forward<T, W, 2>(a, false, s);
 }
-
-// Row chunks of the column sums: enough CTAs to occupy the SMs some eight
-// times over, at least four rows each.
-int64_t row_chunks(int64_t N, int64_t D) {
-    const int64_t blocks = (D + 1023) / 1024;
-    int64_t S = 8LL * 152 / blocks;
-    if (S > (N + 3) / 4) S = (N + 3) / 4;
-    return S < 1 ? 1 : S > 1024 ? 1024 : S;
-}
-
-template <typename T, typename W, int B, int NT, bool FULL, bool RES>
-tpmlp_status backward_turns(NormGradArgs& a, cudaStream_t s) {
-    using Ring = RowRing<T, B, RES ? 3 : 2, GRAD_STAGES<T>, GRAD_THREADS, NT, FULL>;
-    static std::atomic<uint64_t> asked{0};
-    if (!allow_smem(norm_grad_kernel<T, W, B, NT, FULL, RES>, Ring::MOST, asked)) return TPMLP_ERR_CUDA;
-    const int64_t turns = (a.N + Ring::GROUPS - 1) / Ring::GROUPS;
-    a.S = (int)(turns < MOST_CTAS ? turns : MOST_CTAS);
-    return launch_smem(norm_grad_kernel<T, W, B, NT, FULL, RES>, dim3((unsigned)a.S), GRAD_THREADS, Ring::MOST,
-                       s, a);
-}
-
-template <typename T, typename W, int B>
-tpmlp_status backward(NormGradArgs a, cudaStream_t s) {
-    LaunchScope ls("layernorm_backward", s);
-    const int64_t accesses = a.D / (B / (int)sizeof(T));
-    if (a.D <= LONGEST) {
-        const tpmlp_status st = with_group<GRAD_THREADS>(a.D, [&](auto nt, auto full) {
-            constexpr int NT = decltype(nt)::value;
-            constexpr bool FULL = decltype(full)::value && B == 16;
-            return a.dres != nullptr ? backward_turns<T, W, B, NT, FULL, true>(a, s)
-                                     : backward_turns<T, W, B, NT, FULL, false>(a, s);
-        });
-        if (st != TPMLP_OK || a.part == nullptr || a.S == 1) return st;
-        return launch(norm_grad_params_kernel<W>, dim3((unsigned)((2 * a.D + 31) / 32)), 256, s, a);
-    }
-    tpmlp_status st = launch(norm_grad_rows_kernel<T, W, B>, dim3((unsigned)a.N), 256, s, a);
-    if (st != TPMLP_OK) return st;
-    st = launch(norm_grad_apply_kernel<T, W, B>, dim3((unsigned)((accesses + 127) / 128), (unsigned)a.S), 128, s, a);
-    if (st != TPMLP_OK || a.part == nullptr) return st;
-    return launch(norm_grad_params_kernel<W>, dim3((unsigned)((2 * a.D + 31) / 32)), 256, s, a);
-}
-
-template <typename T, typename W>
-tpmlp_status backward_width(const NormGradArgs& a, cudaStream_t s) {
-    auto fits = [&](int bytes) {
-        const int n = bytes / (int)sizeof(T);
-        const int params = n * (int)sizeof(W) < 16 ? n * (int)sizeof(W) : 16;
-        return a.D % n == 0 && access_fits(a.x, a.ldx * sizeof(T), bytes) &&
-               access_fits(a.dy, a.lddy * sizeof(T), bytes) && access_fits(a.dx, a.lddx * sizeof(T), bytes) &&
-               (a.dres == nullptr || access_fits(a.dres, a.lddres * sizeof(T), bytes)) &&
-               access_fits(a.w, 0, params);
-    };
-    if (fits(16)) return backward<T, W, 16>(a, s);
-    if constexpr (sizeof(T) == 4) return backward<T, W, 4>(a, s);
-    else return fits(4) ? backward<T, W, 4>(a, s) : backward<T, W, 2>(a, s);
-}
-
-size_t rows_bytes(int64_t N) { return ((size_t)N * sizeof(float4) + 255) & ~(size_t)255; }
 
 }  // namespace
 
@@ -740,33 +427,6 @@ tpmlp_status run_layernorm(int f32, int params_f32, const LayernormArgs& g, cuda
     if (a.err == nullptr) return TPMLP_ERR_CUDA;
     if (f32) return forward_width<float, float>(a, s);
     return params_f32 ? forward_width<__nv_bfloat16, float>(a, s) : forward_width<__nv_bfloat16, __nv_bfloat16>(a, s);
-}
-
-size_t layernorm_backward_bytes(int64_t N, int64_t D) {
-    if (N == 0) return 0;
-    const int64_t chunks = row_chunks(N, D), S = chunks > MOST_CTAS ? chunks : MOST_CTAS;
-    return rows_bytes(N) + (size_t)S * 2 * (size_t)D * sizeof(float);
-}
-
-tpmlp_status run_layernorm_backward(int f32, int params_f32, const LayernormGradArgs& g, void* workspace,
-                                    cudaStream_t s) {
-    const bool params = g.dweight != nullptr;
-    if (g.N == 0) {   // sums over no rows
-        const size_t bytes = (size_t)g.D * (params_f32 ? 4 : 2);
-        if (params && (cudaMemsetAsync(g.dweight, 0, bytes, s) != cudaSuccess ||
-                       cudaMemsetAsync(g.dbias, 0, bytes, s) != cudaSuccess))
-            return TPMLP_ERR_CUDA;
-        return TPMLP_OK;
-    }
-    NormGradArgs a{g.N, g.D, g.dy, g.lddy, g.x, g.ldx, g.weight, g.mean, g.rstd, g.dresidual, g.lddres,
-                   g.dx, g.lddx, g.dweight, g.dbias, nullptr, nullptr, (int)row_chunks(g.N, g.D),
-                   device_error_word(), wait_timeout_ns(), row_stall()};
-    if (a.err == nullptr) return TPMLP_ERR_CUDA;
-    a.rows = static_cast<float4*>(workspace);
-    if (params) a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + rows_bytes(g.N));
-    if (f32) return backward_width<float, float>(a, s);
-    return params_f32 ? backward_width<__nv_bfloat16, float>(a, s)
-                      : backward_width<__nv_bfloat16, __nv_bfloat16>(a, s);
 }
 
 }  // namespace tpmlp

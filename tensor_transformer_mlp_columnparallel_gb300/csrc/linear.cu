@@ -65,7 +65,8 @@ __global__ void __launch_bounds__(COLS) dact_kernel(const DactParams p) {
 
 // The same with rows in turn: a CTA has one panel of F columns (an even share of
 // at most LONGEST) and its groups every so many rows of it, which come to shared
-// memory by bulk copies of 16 KB at a time. 
+// memory by bulk copies of up to 16 KB. (4096 x 16384 bf16, gelu, with the bias
+// gradient on GB300: 86 us, 4.7 TB/s read and written; by columns 99.)
 constexpr int TURN_THREADS = 512, TURN_STAGES = 3;
 constexpr int TURN_CTAS = 152;
 
@@ -230,7 +231,7 @@ tpmlp_status dact_turns(int act, DactParams p, cudaStream_t s) {
     LaunchScope ls("linear_dact", s);
     const Turns t = turns_of(p.a.F, 16 / (int)sizeof(T));
     p.S = t.chunks;
-    const tpmlp_status st = with_group<TURN_THREADS>(t.width, [&](auto nt, auto full) {
+    const tpmlp_status st = with_group<TURN_THREADS, 64>(t.width, [&](auto nt, auto full) {
         constexpr int NT = decltype(nt)::value;
         // (a last panel may be narrower)
         auto go = [&](auto whole) {
@@ -263,7 +264,9 @@ tpmlp_status run_dact(int f32, int act, const DactArgs& a, cudaStream_t s) {
     const int elems = f32 ? 4 : 8, size = f32 ? 4 : 2;
     const bool wide = a.F % elems == 0 && access_fits(a.dY, a.lddy * size, 16) && access_fits(a.Z, a.ldz * size, 16) &&
                       access_fits(a.dZ, a.F * size, 16);   // on the bf16 path always
-    // rows in turn: from four rows a group on
+    // Rows in turn from four rows a group on (F = 16384 bf16 with the launch of the
+    // sums: 304 rows 19.5 us against 19.7 by columns, 608 24.3 against 23.5, 1216 33.8
+    // against 36.1, 2432 49.6 against 60.6).
     if (wide && !a.rest && a.N * a.F >= 8LL * TURN_CTAS * LONGEST)
         return f32 ? dact_turns<float>(act, p, s) : dact_turns<__nv_bfloat16>(act, p, s);
     if (!f32) return dact<__nv_bfloat16, 16>(act, p, s);

@@ -14,12 +14,18 @@ namespace {
 
 constexpr int LONGEST = 8192;    // elements of a row that is taken in turn
 
-// A barrier of a group of NT threads (whole warps).
+// The lanes of this thread's group of NT threads, a power of two, in its warp.
+template <int NT> __device__ __forceinline__ uint32_t group_lanes() {
+    if constexpr (NT >= 32) return 0xffffffffu;
+    else return ((1u << NT) - 1u) << (threadIdx.x & 31 & ~(NT - 1));
+}
+
+// A barrier of a group of NT threads.
 template <int NT> __device__ __forceinline__ void group_sync(int group) {
     if constexpr (NT > 32)
         asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(NT) : "memory");
     else
-        __syncwarp();
+        __syncwarp(group_lanes<NT>());
 }
 
 // wait_bounded without the call: one in the loop would have the threads' columns
@@ -39,12 +45,12 @@ __device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t phase, volati
     }
 }
 
-// CTAs of TH threads that stay, in as many groups of NT threads as a row needs at
-// LONGEST / TH elements a thread (FULL: exactly). A thread keeps its columns' parameters in registers;
-// a group's next rows (Q matrices of STAGES rows) are on their way to shared
-// memory. Rows of whole 16-byte accesses come by bulk copies, one instruction a
-// row (copies by every thread were what the backward waited for: 8192 x 8192
-// bf16, 107 us against 90), others by 4-byte copies of the threads' own elements.
+// CTAs of TH threads that stay, in groups of as many threads, NT, as a row needs at
+// LONGEST / TH elements a thread (FULL: exactly). A thread keeps its columns'
+// parameters in registers; a group's next rows (Q matrices of STAGES rows) are on
+// their way to shared memory. Rows of whole 16-byte accesses come by bulk copies,
+// one instruction a row (copies by every thread were what the layer norm's gradient
+// waited for: 8192 x 8192 bf16, 107 us against 87), others by 4-byte copies of the threads' own elements.
 template <typename T, int B, int Q, int STAGES, int TH, int NT, bool FULL>
 struct RowRing {
     using A = Access<T, B>;
@@ -178,16 +184,13 @@ bool allow_smem(K kernel, int bytes, std::atomic<uint64_t>& asked) {
     return true;
 }
 
-// f(NT, FULL) as constants: the group of TH / 8 to TH threads that rows of D elements take
-template <int TH, typename F> tpmlp_status with_group(int64_t D, F f) {
+// f(NT, FULL) as constants: the group of NT to TH threads that rows of D elements take
+template <int TH, int NT, typename F> tpmlp_status with_group(int64_t D, F f) {
     constexpr int ELEMS = LONGEST / TH;
-    auto width = [&](auto nt) {
-        return D == decltype(nt)::value * ELEMS ? f(nt, std::true_type()) : f(nt, std::false_type());
-    };
-    if (D <= TH / 8 * ELEMS) return width(std::integral_constant<int, TH / 8>());
-    if (D <= TH / 4 * ELEMS) return width(std::integral_constant<int, TH / 4>());
-    if (D <= TH / 2 * ELEMS) return width(std::integral_constant<int, TH / 2>());
-    return width(std::integral_constant<int, TH>());
+    const std::integral_constant<int, NT> nt;
+    if constexpr (NT < TH)
+        if (D > NT * ELEMS) return with_group<TH, 2 * NT>(D, f);
+    return D == NT * ELEMS ? f(nt, std::true_type()) : f(nt, std::false_type());
 }
 
 }  // namespace
