@@ -48,12 +48,12 @@ __device__ __forceinline__ void write_param(__nv_bfloat16* at, float v) { *at = 
 
 // All of it in one reading, for rows of up to LONGEST elements: a thread
 // keeps its columns' sums of dy h and dy over the rows of its group; a CTA's
-// sums go to part[blockIdx.x] (with one CTA to dw and db). Elements beyond the row
-// are zeros and pass through the arithmetic. (8192 x 8192 bf16 with dresidual on
+// sums go to part[blockIdx.x] (with one CTA to dw and db). (8192 x 8192 bf16 with dresidual on
 // GB300: 87 us with the launch that adds the CTAs' sums, 6.2 TB/s read and written;
 // without its reductions or its column sums the same: HBM. Without dresidual 75 us,
-// 5.4 TB/s; rows that leave threads idle are bound by one row's latency instead, with
-// one group an SM from 4097 elements on: 13107 x 5120 112 us, 3.6 TB/s.)
+// 5.4 TB/s; rows that leave threads idle wait for one row's reductions, with one group
+// an SM from 4097 elements on: 13107 x 5120 96 us, 4.2 TB/s; 112 if the idle accesses
+// pass through the arithmetic as zeros.)
 template <typename T, typename W, int B, int NT, bool FULL, bool RES>
 __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const NormGradArgs a) {
     constexpr int Q = RES ? 3 : 2, STAGES = GRAD_STAGES<T>;
@@ -107,15 +107,15 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const NormGr
         Pair su = A::both(0.f), suh = su, sh = su;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
+            if (!ring.mine(i)) continue;
             x[i] = ring.at(0, i);
             g[i] = ring.at(1, i);
             Pair v[P], y[P];
             A::unpack(x[i], v);
             A::unpack(g[i], y);
-            const Pair less = FULL || ring.mine(i) ? m : A::both(0.f);
 #pragma unroll
             for (int j = 0; j < P; ++j) {
-                const Pair h = mul2(add2(v[j], less), r), u = mul2(y[j], w[i][j]);
+                const Pair h = mul2(add2(v[j], m), r), u = mul2(y[j], w[i][j]);
                 su = add2(su, u);
                 suh = fma2(u, h, suh);
                 sh = add2(sh, h);
@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const NormGr
         Word* out = reinterpret_cast<Word*>(static_cast<T*>(a.dx) + (int64_t)row * a.lddx) + t;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
+            if (!ring.mine(i)) continue;
             Pair v[P], y[P], z[P > 1 ? P : 2];
             A::unpack(x[i], v);
             A::unpack(g[i], y);
@@ -142,8 +143,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const NormGr
                 sb[i][j] = add2(sb[i][j], y[j]);
                 v[j] = fma2(mul2(y[j], w[i][j]), r, fma2(h, c2, RES ? add2(z[j], c1) : c1));
             }
-            const Word o = A::pack(v);
-            if (ring.mine(i)) out[i * NT] = o;
+            out[i * NT] = A::pack(v);
         }
         if (RES) {
             if (Ring::BULK) group_sync<NT>(group);

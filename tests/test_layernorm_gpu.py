@@ -129,6 +129,40 @@ def test_many_rows(N, D, pad, dt):
     check_backward(x, w, rows(N, D, dt, 4, pad), rows(N, D, dt, 5, pad) if D % 16 else None)
 
 
+# every number of threads to a row and of accesses to a thread, at its limits, for
+# few rows (which have forms of their own) and for more than an SM each
+@pytest.mark.parametrize("N", [5, 203])
+@pytest.mark.parametrize("D", [4, 60, 64, 68, 128, 132, 192, 196, 256, 260, 384, 388, 512, 516, 768, 1024, 1032, 1536, 2048,
+                               2060, 4096, 4100, 6144, 6152, 8208, 12292, 16388, 24576, 24584, 32768, 32772])
+@pytest.mark.parametrize("dt,wdt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+def test_forward_widths(N, D, dt, wdt):
+    pad = 4 if D % 8 else 0   # 8-byte rows of bf16
+    check_forward(rows(N, D, dt, D, pad, std=3.0), vector(D, wdt, 1, 1.0), vector(D, wdt, 2, 0.0))
+
+
+@pytest.mark.parametrize("D", [48, 256, 500, 2000, 7000])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_bad_rows_beside_good_ones(D, dt):
+    """Rows that share a warp or a CTA: one overflows, one holds a NaN, the others
+    are as they are alone."""
+    x, w, b = rows(333, D, dt, 1), vector(D, "f32", 1, 1.0), vector(D, "f32", 2, 0.0)
+    want, mean, rstd = tp.layernorm(x, w, b)
+    far, bad = torch.arange(3, 333, 17), torch.arange(4, 333, 29)
+    z = x.clone()
+    z[far] *= 2.0 ** 80
+    z[bad, D // 2] = float("nan")
+    y, m, r = tp.layernorm(z, w, b)
+    good = torch.ones(333, dtype=torch.bool)
+    good[far] = good[bad] = False
+    for got, ref in ((y, want), (m, mean), (r, rstd)):
+        assert torch.equal(got[good.to(dev())], ref[good.to(dev())])
+    assert torch.isnan(y[bad]).all()
+    only = far[~torch.isin(far, bad)]
+    o = oracle.norm.layernorm(z[only], w, b, EPS)
+    h = np.abs(o["y"] - f64(b)) / np.abs(f64(w))
+    within(y[only], o["y"], 8 * s_of(D) * np.abs(f64(w)) * (2 + h) + 4 * U, "overflowing rows")
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("N,D", [(3, 768), (2600, 8192)])
 def test_without_parameters(N, D, dt):
