@@ -380,11 +380,13 @@ tpmlp_status forward(const NormArgs& a, bool turns, cudaStream_t s) {
             return a.D == LONGEST ? go(std::true_type()) : go(std::false_type());
         }
     if constexpr (B >= 8) {
-        // up to a row an SM: more threads, less each (152 x 4096 bf16 2.3 us, as above 3.9)
-        const std::true_type early;
-        if (a.N <= device_sm_count() && (held(Int<32>(), Int<2>(), early) || held(Int<128>(), Int<2>(), early) ||
-                                         held(Int<512>(), Int<2>(), early) || held(Int<1024>(), Int<2>(), early)))
-            return st;
+        // Few rows: more threads, less each, up to 1024 threads an SM in all (bf16, as
+        // above: 304 x 4096 2.7 us against 4.2, 1216 x 1024 2.7 against 4.0; but 1216 x
+        // 4096 8.7 against 6.6, 4864 x 1024 7.8 against 6.1).
+        auto few = [&](auto nt) {
+            return a.N * decltype(nt)::value <= 1024LL * device_sm_count() && held(nt, Int<2>(), std::true_type());
+        };
+        if (few(Int<32>()) || few(Int<128>()) || few(Int<512>()) || few(Int<1024>())) return st;
         auto threads = [&](auto nt) { return held(nt, Int<6>(), late) || held(nt, Int<8>(), late); };
         if (held(Int<8>(), Int<2>(), late) || held(Int<8>(), Int<4>(), late) || threads(Int<8>()) ||
             threads(Int<16>()) || threads(Int<32>()) || threads(Int<64>()) || threads(Int<128>()) ||
