@@ -34,6 +34,7 @@ struct NormGradArgs {
     float4* rows;           // [N]: sum u / D, sum u h / D, d rstd (long rows)
     float* part;            // [S, 2, D]: a CTA's (long rows: a row chunk's) sums of dy h and dy
     int S;
+    int panels, width;      // of a long row's columns
     int* err;
     uint64_t timeout_ns;
     int stall;
@@ -54,7 +55,7 @@ __device__ __forceinline__ void write_param(__nv_bfloat16* at, float v) { *at = 
 // 5.4 TB/s; rows that leave threads idle wait for one row's reductions, with one group
 // an SM from 4097 elements on: 13107 x 5120 96 us, 4.2 TB/s; 112 if the idle accesses
 // pass through the arithmetic as zeros.)
-template <typename T, typename W, int B, int NT, bool FULL, bool RES>
+template <typename T, typename W, int B, int NT, bool FULL, bool RES, bool PANEL>
 __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const NormGradArgs a) {
     constexpr int Q = RES ? 3 : 2, STAGES = GRAD_STAGES<T>;
     using Ring = RowRing<T, B, Q, STAGES, GRAD_THREADS, NT, FULL>;
@@ -67,19 +68,22 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const NormGr
     __shared__ float red[2][GRAD_THREADS / 32][3];
     __shared__ uint64_t spare[Ring::GROUPS];
     __shared__ int late[2][Ring::GROUPS];
+    const int64_t c0 = PANEL ? (int64_t)(blockIdx.x % a.panels) * a.width : 0;
+    const int chunk = PANEL ? blockIdx.x / a.panels : blockIdx.x;
+    const int cols = (int)(PANEL && a.D - c0 > a.width ? a.width : a.D - c0);
     if (threadIdx.x < 2 * Ring::GROUPS) (&late[0][0])[threadIdx.x] = 0;
     __syncthreads();
-    Ring ring(ring_memory, bars, a.D);
+    Ring ring(ring_memory, bars, cols);
     constexpr int groups = Ring::GROUPS;
     const int group = ring.group, t = ring.t;
-    const uint32_t N = (uint32_t)a.N, step = gridDim.x * groups, first = blockIdx.x * groups + group;
+    const uint32_t N = (uint32_t)a.N, step = a.S * groups, first = chunk * groups + group;
     pdl_wait();
     pdl_launch_dependents();
     auto ask = [&](int s, uint32_t row) {
         ring.ask(s, row < N, [&](int to) {
-            ring.fetch(to, 0, a.x, row, a.ldx);
-            ring.fetch(to, 1, a.dy, row, a.lddy);
-            if (RES) ring.fetch(to, Q - 1, a.dres, row, a.lddres);
+            ring.fetch(to, 0, static_cast<const T*>(a.x) + c0, row, a.ldx);
+            ring.fetch(to, 1, static_cast<const T*>(a.dy) + c0, row, a.lddy);
+            if (RES) ring.fetch(to, Q - 1, static_cast<const T*>(a.dres) + c0, row, a.lddres);
         });
     };
 #pragma unroll
@@ -89,17 +93,25 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const NormGr
     for (int i = 0; i < R; ++i) {
 #pragma unroll
         for (int j = 0; j < P; ++j) w[i][j] = A::both(1.f), sw[i][j] = sb[i][j] = A::both(0.f);
-        if (a.w && ring.mine(i)) load_params<W, A::N>(static_cast<const W*>(a.w) + (t + i * NT) * A::N, w[i]);
+        if (a.w && ring.mine(i)) load_params<W, A::N>(static_cast<const W*>(a.w) + c0 + (t + i * NT) * A::N, w[i]);
     }
     const float inv = 1.f / (float)a.D;
     float m_next = 0.f, r_next = 0.f;
-    if (first < N) m_next = a.mean[first], r_next = a.rstd[first];
+    float4 s_next = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (first < N) {
+        m_next = a.mean[first], r_next = a.rstd[first];
+        if (PANEL) s_next = a.rows[first];
+    }
     int turn = 0;
     uint32_t row = first;
     const bool go = !a.stall || ring.stall(&spare[ring.group], &late[0][ring.group], a.err, a.timeout_ns);
     for (; go && row < N; row += step, turn ^= 1, ring.next()) {
         const float m1 = m_next, r1 = r_next;
-        if (row + step < N) m_next = a.mean[row + step], r_next = a.rstd[row + step];
+        const float4 s1 = s_next;
+        if (row + step < N) {
+            m_next = a.mean[row + step], r_next = a.rstd[row + step];
+            if (PANEL) s_next = a.rows[row + step];
+        }
         volatile int* flag = &late[turn][group];
         const bool ok = ring.wait(flag, a.err, a.timeout_ns);
         const Pair m = A::both(-m1), r = A::both(r1);
@@ -110,6 +122,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const NormGr
             if (!ring.mine(i)) continue;
             x[i] = ring.at(0, i);
             g[i] = ring.at(1, i);
+            if (PANEL) continue;
             Pair v[P], y[P];
             A::unpack(x[i], v);
             A::unpack(g[i], y);
@@ -122,13 +135,15 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const NormGr
             }
         }
         float s[3] = {A::total(su), A::total(suh), A::total(sh)};
-        group_reduce<NT>(s, group, red[turn], Add());
+        if constexpr (PANEL) group_sync<NT>(group);
+        else group_reduce<NT>(s, group, red[turn], Add());
         if (!ok || (NT > 32 && *flag)) break;   // the whole group
         if (!RES) ask(ring.k, row + STAGES * step);   // every thread holds its elements
-        const float d = fabsf(m1 * r1) > FAR_MEAN ? s[2] * inv : 0.f;
-        // dx = r u - r c1 - r c2 h
-        const Pair d1 = A::both(-d), c1 = A::both(-r1 * s[0] * inv), c2 = A::both(-r1 * fmaf(-d, s[0], s[1]) * inv);
-        Word* out = reinterpret_cast<Word*>(static_cast<T*>(a.dx) + (int64_t)row * a.lddx) + t;
+        const float d = PANEL ? s1.z : fabsf(m1 * r1) > FAR_MEAN ? s[2] * inv : 0.f;
+        // dx = r u - r mean(u) - r mean(u h) h
+        const Pair d1 = A::both(-d), c1 = A::both(-r1 * (PANEL ? s1.x : s[0] * inv));
+        const Pair c2 = A::both(-r1 * (PANEL ? s1.y : fmaf(-d, s[0], s[1]) * inv));
+        Word* out = reinterpret_cast<Word*>(static_cast<T*>(a.dx) + (int64_t)row * a.lddx + c0) + t;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             if (!ring.mine(i)) continue;
@@ -156,7 +171,6 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const NormGr
     float* sums = reinterpret_cast<float*>(ring_memory);
     static_assert(2 * NT * R * A::N * sizeof(float) <= Ring::MOST, "room for two sums a column");
     asm volatile("cp.async.wait_all;" ::: "memory");
-    const int D = (int)a.D;
     for (int q = 0; q < groups; ++q) {
         __syncthreads();
         if (group == q)
@@ -172,12 +186,12 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const NormGr
                     }
     }
     __syncthreads();
-    float* part = a.part + (int64_t)blockIdx.x * 2 * D;
-    for (int c = threadIdx.x; c < D; c += GRAD_THREADS) {
+    float* part = a.part + (int64_t)chunk * 2 * a.D + c0;
+    for (int c = threadIdx.x; c < cols; c += GRAD_THREADS) {
         const float gw = sums[c], gb = sums[NT * R * A::N + c];
-        if (gridDim.x > 1) {
+        if (PANEL || a.S > 1) {
             part[c] = gw;
-            part[D + c] = gb;
+            part[a.D + c] = gb;
         } else {
             write_param(static_cast<W*>(a.dw) + c, gw);
             write_param(static_cast<W*>(a.db) + c, gb);
@@ -299,15 +313,16 @@ int64_t row_chunks(int64_t N, int64_t D) {
     return S < 1 ? 1 : S > 1024 ? 1024 : S;
 }
 
-template <typename T, typename W, int B, int NT, bool FULL, bool RES>
+template <typename T, typename W, int B, int NT, bool FULL, bool RES, bool PANEL>
 tpmlp_status backward_turns(NormGradArgs& a, cudaStream_t s) {
     using Ring = RowRing<T, B, RES ? 3 : 2, GRAD_STAGES<T>, GRAD_THREADS, NT, FULL>;
     static std::atomic<uint64_t> asked{0};
-    if (!allow_smem(norm_grad_kernel<T, W, B, NT, FULL, RES>, Ring::MOST, asked)) return TPMLP_ERR_CUDA;
+    if (!allow_smem(norm_grad_kernel<T, W, B, NT, FULL, RES, PANEL>, Ring::MOST, asked)) return TPMLP_ERR_CUDA;
     const int64_t turns = (a.N + Ring::GROUPS - 1) / Ring::GROUPS;
-    a.S = (int)(turns < MOST_CTAS ? turns : MOST_CTAS);
-    return launch_smem(norm_grad_kernel<T, W, B, NT, FULL, RES>, dim3((unsigned)a.S), GRAD_THREADS, Ring::MOST,
-                       s, a);
+    const int panels = PANEL ? a.panels : 1, most = MOST_CTAS / panels > 0 ? MOST_CTAS / panels : 1;
+    a.S = (int)(turns < most ? turns : most);
+    return launch_smem(norm_grad_kernel<T, W, B, NT, FULL, RES, PANEL>, dim3((unsigned)(a.S * panels)), GRAD_THREADS,
+                       Ring::MOST, s, a);
 }
 
 template <typename T, typename W, int B>
@@ -318,14 +333,28 @@ tpmlp_status backward(NormGradArgs a, cudaStream_t s) {
         const tpmlp_status st = with_group<GRAD_THREADS, 32>(a.D, [&](auto nt, auto full) {
             constexpr int NT = decltype(nt)::value;
             constexpr bool FULL = decltype(full)::value && B == 16;
-            return a.dres != nullptr ? backward_turns<T, W, B, NT, FULL, true>(a, s)
-                                     : backward_turns<T, W, B, NT, FULL, false>(a, s);
+            return a.dres != nullptr ? backward_turns<T, W, B, NT, FULL, true, false>(a, s)
+                                     : backward_turns<T, W, B, NT, FULL, false, false>(a, s);
         });
         if (st != TPMLP_OK || a.part == nullptr || a.S == 1) return st;
         return launch(norm_grad_params_kernel<W>, dim3((unsigned)((2 * a.D + 31) / 32)), 256, s, a);
     }
     tpmlp_status st = launch(norm_grad_rows_kernel<T, W, B>, dim3((unsigned)a.N), 256, s, a);
     if (st != TPMLP_OK) return st;
+    if constexpr (B == 16)
+        if (a.N * a.D >= 8LL * MOST_CTAS * LONGEST) {
+            constexpr int N = 16 / (int)sizeof(T);
+            a.panels = (int)((a.D + LONGEST - 1) / LONGEST);   // of more than LONGEST / 2 columns
+            a.width = (int)((a.D / N + a.panels - 1) / a.panels) * N;
+            a.panels = (int)((a.D + a.width - 1) / a.width);
+            const bool full = a.D == (int64_t)a.panels * LONGEST, res = a.dres != nullptr;
+            st = full ? res ? backward_turns<T, W, B, GRAD_THREADS, true, true, true>(a, s)
+                            : backward_turns<T, W, B, GRAD_THREADS, true, false, true>(a, s)
+                      : res ? backward_turns<T, W, B, GRAD_THREADS, false, true, true>(a, s)
+                            : backward_turns<T, W, B, GRAD_THREADS, false, false, true>(a, s);
+            if (st != TPMLP_OK || a.part == nullptr) return st;
+            return launch(norm_grad_params_kernel<W>, dim3((unsigned)((2 * a.D + 31) / 32)), 256, s, a);
+        }
     st = launch(norm_grad_apply_kernel<T, W, B>, dim3((unsigned)((accesses + 127) / 128), (unsigned)a.S), 128, s, a);
     if (st != TPMLP_OK || a.part == nullptr) return st;
     return launch(norm_grad_params_kernel<W>, dim3((unsigned)((2 * a.D + 31) / 32)), 256, s, a);
@@ -367,7 +396,7 @@ tpmlp_status run_layernorm_backward(int f32, int params_f32, const LayernormGrad
         return TPMLP_OK;
     }
     NormGradArgs a{g.N, g.D, g.dy, g.lddy, g.x, g.ldx, g.weight, g.mean, g.rstd, g.dresidual, g.lddres,
-                   g.dx, g.lddx, g.dweight, g.dbias, nullptr, nullptr, (int)row_chunks(g.N, g.D),
+                   g.dx, g.lddx, g.dweight, g.dbias, nullptr, nullptr, (int)row_chunks(g.N, g.D), 1, 0,
                    device_error_word(), wait_timeout_ns(), row_stall()};
     if (a.err == nullptr) return TPMLP_ERR_CUDA;
     a.rows = static_cast<float4*>(workspace);

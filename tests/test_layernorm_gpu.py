@@ -142,6 +142,22 @@ def test_forward_widths(N, D, dt, wdt):
     check_forward(rows(N, D, dt, D, pad, std=3.0), vector(D, wdt, 1, 1.0), vector(D, wdt, 2, 0.0))
 
 
+# rows longer than a CTA's columns: panels of them in turn, full and ragged
+@pytest.mark.parametrize("N,D,pad", [(1000, 16384, 0), (1111, 9008, 8), (817, 12288, 0), (409, 24600, 8)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_backward_of_many_long_rows(N, D, pad, dt):
+    x, w = rows(N, D, dt, 3, pad, offset=30.0 if D == 12288 and dt == "f32" else 0.0), vector(D, "f32", 1, 1.0)
+    dy = rows(N, D, dt, 4, pad)
+    check_backward(x, w, dy, rows(N, D, dt, 5, pad))
+    dx, _, _ = check_backward(x, w, dy)
+    _, mean, rstd = tp.layernorm(x, w, None)
+    assert torch.equal(tp.layernorm_backward(dy, x, w, mean, rstd, param_grads=False)[0], dx)
+    dw, db = (torch.empty_like(w) for _ in range(2))
+    ws = torch.empty(tp.tpmlp_layernorm_backward_workspace_bytes(N, D), dtype=torch.uint8, device=dev())
+    tp.tpmlp_layernorm_backward(dy, x, w, mean, rstd, None, x, dw, db, ws)
+    assert torch.equal(x, dx)
+
+
 @pytest.mark.parametrize("D", [48, 256, 500, 2000, 7000])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_bad_rows_beside_good_ones(D, dt):
