@@ -47,7 +47,8 @@ constexpr float FAR_MEAN = 8.f;
 __device__ __forceinline__ void write_param(float* at, float v) { *at = v; }
 __device__ __forceinline__ void write_param(__nv_bfloat16* at, float v) { *at = __float2bfloat16_rn(v); }
 
-// All of it in one reading, for rows of up to LONGEST elements: a thread
+// All of it in one reading, for rows of up to LONGEST elements (PANEL: the second
+// reading of longer ones, a CTA having an even share of the columns): a thread
 // keeps its columns' sums of dy h and dy over the rows of its group; a CTA's
 // sums go to part[blockIdx.x] (with one CTA to dw and db). (8192 x 8192 bf16 with dresidual on
 // GB300: 87 us with the launch that adds the CTAs' sums, 6.2 TB/s read and written;
@@ -200,9 +201,10 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const NormGr
 }
 
 // Rows longer than LONGEST are read twice: their columns' sums do not fit the
-// registers of a CTA. (5461 x 12288 bf16: 152 us, 2.6 TB/s of one reading. Shorter
-// rows this way: 8192 x 8192 152 us against 75, 1 x 512 4.8 us against 3.9.) Sums
-// over a row, one CTA each:
+// registers of a CTA. (5461 x 12288 bf16: 132 us, 3.0 TB/s of one reading; 256 threads
+// by two accesses at once, 512 threads 140 to 150, more accesses 137. Shorter rows
+// read twice: 8192 x 8192 152 us against 75, 1 x 512 4.8 us against 3.9.) Sums over a
+// row, one CTA each:
 template <typename T, typename W, int B>
 __global__ void __launch_bounds__(256) norm_grad_rows_kernel(const NormGradArgs a) {
     using A = Access<T, B>;
@@ -236,7 +238,8 @@ __global__ void __launch_bounds__(256) norm_grad_rows_kernel(const NormGradArgs 
     if (threadIdx.x == 0) a.rows[row] = make_float4(s[0] * inv, fmaf(-d, s[0], s[1]) * inv, d, 0.f);
 }
 
-// dx, and a row chunk's column sums: a thread has one access's columns.
+// dx, and a row chunk's column sums: a thread has one access's columns. For fewer
+// rows than norm_grad_kernel's rings are worth, and for rows of 4- and 2-byte accesses.
 template <typename T, typename W, int B>
 __global__ void __launch_bounds__(128) norm_grad_apply_kernel(const NormGradArgs a) {
     using A = Access<T, B>;
@@ -341,6 +344,8 @@ tpmlp_status backward(NormGradArgs a, cudaStream_t s) {
     }
     tpmlp_status st = launch(norm_grad_rows_kernel<T, W, B>, dim3((unsigned)a.N), 256, s, a);
     if (st != TPMLP_OK) return st;
+    // the second reading by panels in turn, from eight rows of a panel a CTA on (900 x
+    // 12288 bf16 26 us in all against 34, 5461 x 12288 132 against 151)
     if constexpr (B == 16)
         if (a.N * a.D >= 8LL * MOST_CTAS * LONGEST) {
             constexpr int N = 16 / (int)sizeof(T);
