@@ -11,6 +11,18 @@
 
 namespace tpmlp {
 
+// max, min that keep a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // Exact GELU (the pages' nn.GELU): z Phi(z), Phi(z) = (1 + erf(z / sqrt(2))) / 2,
 // derivative Phi(z) + z phi(z), phi(z) = exp(-z^2 / 2) / sqrt(2 pi); erf and
 // exp from CUDA's erff / expf (fp32 path) or erff / __expf (bf16 epilogue).
@@ -19,14 +31,20 @@ __device__ __forceinline__ float gelu_erf_fwd(float z) {
 }
 
 // Sigmoid approximation of GELU (interview page): z s, s = sigmoid(1.702 z),
-// derivative s (1 + 1.702 z (1 - s)) = s (1 + 1.702 z e s), e = exp(-1.702 z);
-// exponent clamped at 80 as in the forms below.
-constexpr float GELU_SIGMOID_SCALE = 1.702f;
+// derivative s (1 + 1.702 z (1 - s)) = s (1 + 1.702 z e s), e = exp(-1.702 z).
+// z itself is held, in every factor: at -47 from there down, so that e (5e34 there)
+// stays finite (act and act' are below 2e-33 either way, down to the lowest z), and
+// for act' at 47 from there up, where it is 1 and 1.702 z e would become infinity
+// times 0.
+constexpr float GELU_SIGMOID_SCALE = 1.702f, GELU_SIGMOID_FAR = 47.f;
 
 __device__ __forceinline__ float act_fwd(int act, float z) {
     if (act == TPMLP_ACT_RELU) return z > 0.f ? z : 0.f;
     if (act == TPMLP_ACT_GELU_ERF) return gelu_erf_fwd(z);
-    if (act == TPMLP_ACT_GELU_SIGMOID) return z / (1.f + expf(fminf(-GELU_SIGMOID_SCALE * z, 80.f)));
+    if (act == TPMLP_ACT_GELU_SIGMOID) {
+        z = max_nan(z, -GELU_SIGMOID_FAR);
+        return z / (1.f + expf(-GELU_SIGMOID_SCALE * z));
+    }
     const float c = 0.7978845608028654f;   // sqrt(2/pi)
     const float u = c * fmaf(0.044715f * z, z * z, z);
     return 0.5f * z * (1.f + tanhf(u));
@@ -37,7 +55,8 @@ __device__ __forceinline__ float act_grad(int act, float z) {
     if (act == TPMLP_ACT_GELU_ERF)
         return fmaf(z * 0.3989422804014327f, expf(-0.5f * z * z), 0.5f * (1.f + erff(z * 0.7071067811865476f)));
     if (act == TPMLP_ACT_GELU_SIGMOID) {
-        const float e = expf(fminf(-GELU_SIGMOID_SCALE * z, 80.f));
+        z = min_nan(max_nan(z, -GELU_SIGMOID_FAR), GELU_SIGMOID_FAR);
+        const float e = expf(-GELU_SIGMOID_SCALE * z);
         const float sg = 1.f / (1.f + e);
         return sg * fmaf(GELU_SIGMOID_SCALE * z * e, sg, 1.f);
     }
@@ -50,13 +69,6 @@ __device__ __forceinline__ float act_grad(int act, float z) {
 
 // SiLU(z) = z / (1 + exp(-z)), the gate nonlinearity of the gated MLP.
 __device__ __forceinline__ float silu_f(float z) { return z / (1.f + expf(-z)); }
-
-// max that keeps a NaN
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
 
 // Derivatives of h = SiLU(g) u for an upstream dh, s = 1 / (1 + exp(-g)):
 //   du = dh g s,  dg = dh u s (1 + g (1 - s)),  and 1 - s = e s with e = exp(-g).
@@ -84,7 +96,10 @@ __device__ __forceinline__ void dswiglu(float dh, float g, float u, float& dg, f
 __device__ __forceinline__ float act_fwd_bf16(int act, float z) {
     if (act == TPMLP_ACT_RELU) return z > 0.f ? z : 0.f;
     if (act == TPMLP_ACT_GELU_ERF) return gelu_erf_fwd(z);
-    if (act == TPMLP_ACT_GELU_SIGMOID) return __fdividef(z, 1.f + __expf(fminf(-GELU_SIGMOID_SCALE * z, 80.f)));
+    if (act == TPMLP_ACT_GELU_SIGMOID) {
+        z = max_nan(z, -GELU_SIGMOID_FAR);
+        return __fdividef(z, 1.f + __expf(-GELU_SIGMOID_SCALE * z));
+    }
     const float c = 0.7978845608028654f;
     const float u = c * fmaf(0.044715f * z, z * z, z);
     const float e = __expf(fminf(-2.f * u, 80.f));
@@ -96,7 +111,8 @@ __device__ __forceinline__ float act_grad_bf16(int act, float z) {
     if (act == TPMLP_ACT_GELU_ERF)
         return fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z), 0.5f * (1.f + erff(z * 0.7071067811865476f)));
     if (act == TPMLP_ACT_GELU_SIGMOID) {
-        const float e = __expf(fminf(-GELU_SIGMOID_SCALE * z, 80.f));
+        z = min_nan(max_nan(z, -GELU_SIGMOID_FAR), GELU_SIGMOID_FAR);
+        const float e = __expf(-GELU_SIGMOID_SCALE * z);
         const float sg = __fdividef(1.f, 1.f + e);
         return sg * fmaf(GELU_SIGMOID_SCALE * z * e, sg, 1.f);
     }
