@@ -38,6 +38,10 @@ __device__ __forceinline__ float gelu_erf_fwd(float z) {
 // times 0.
 constexpr float GELU_SIGMOID_SCALE = 1.702f, GELU_SIGMOID_FAR = 47.f;
 
+// The same for the tanh form: e = exp(-2 u) is 1e35 at z = -9.7, where act and act'
+// are below 1e-32 (2 z u' e grows with the cube of z, and e does not follow it).
+constexpr float GELU_TANH_FAR = 9.7f;
+
 __device__ __forceinline__ float act_fwd(int act, float z) {
     if (act == TPMLP_ACT_RELU) return z > 0.f ? z : 0.f;
     if (act == TPMLP_ACT_GELU_ERF) return gelu_erf_fwd(z);
@@ -61,6 +65,7 @@ __device__ __forceinline__ float act_grad(int act, float z) {
         return sg * fmaf(GELU_SIGMOID_SCALE * z * e, sg, 1.f);
     }
     const float c = 0.7978845608028654f;
+    z = min_nan(max_nan(z, -GELU_TANH_FAR), GELU_TANH_FAR);   // 1 - t t is 0 there; z2 stays finite
     const float z2 = z * z;
     const float t = tanhf(c * fmaf(0.044715f * z, z2, z));
     const float du = c * fmaf(3.f * 0.044715f, z2, 1.f);
@@ -90,9 +95,10 @@ __device__ __forceinline__ void dswiglu(float dh, float g, float u, float& dg, f
 //   0.5 z (1 + tanh(u)) = z s,            s = sigmoid(2u) = 1 / (1 + e), e = exp(-2u)
 //   act'(z) = s + 2 z s (1 - s) u'(z) = s (1 + 2 z u'(z) e s)     (1 - s = e s)
 //   SiLU(z) = z / (1 + exp(-z))
-// with CUDA's __expf and __fdividef. The exponent is clamped at 80 so that
-// e, 1 + e and e s stay finite (for 2u < -80 the outputs are below 1e-33 in
-// magnitude either way). The fp32 path keeps the tanhf / expf forms above.
+// with CUDA's __expf and __fdividef. Far from zero z is held, so that e, 1 + e and
+// the products with e s stay finite: at GELU_TANH_FAR and GELU_SIGMOID_FAR, on both
+// sides for a derivative; SiLU's exponent is clamped at 80. The fp32 path keeps the
+// tanhf / expf forms above.
 __device__ __forceinline__ float act_fwd_bf16(int act, float z) {
     if (act == TPMLP_ACT_RELU) return z > 0.f ? z : 0.f;
     if (act == TPMLP_ACT_GELU_ERF) return gelu_erf_fwd(z);
@@ -101,8 +107,9 @@ __device__ __forceinline__ float act_fwd_bf16(int act, float z) {
         return __fdividef(z, 1.f + __expf(-GELU_SIGMOID_SCALE * z));
     }
     const float c = 0.7978845608028654f;
+    z = max_nan(z, -GELU_TANH_FAR);
     const float u = c * fmaf(0.044715f * z, z * z, z);
-    const float e = __expf(fminf(-2.f * u, 80.f));
+    const float e = __expf(-2.f * u);
     return __fdividef(z, 1.f + e);
 }
 
@@ -117,10 +124,11 @@ __device__ __forceinline__ float act_grad_bf16(int act, float z) {
         return sg * fmaf(GELU_SIGMOID_SCALE * z * e, sg, 1.f);
     }
     const float c = 0.7978845608028654f;
+    z = min_nan(max_nan(z, -GELU_TANH_FAR), GELU_TANH_FAR);
     const float z2 = z * z;
     const float u = c * fmaf(0.044715f * z, z2, z);
     const float du = c * fmaf(3.f * 0.044715f, z2, 1.f);
-    const float e = __expf(fminf(-2.f * u, 80.f));
+    const float e = __expf(-2.f * u);
     const float s = __fdividef(1.f, 1.f + e);
     return s * fmaf(2.f * z * du, e * s, 1.f);
 }

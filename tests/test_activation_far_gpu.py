@@ -16,7 +16,7 @@ import tensor_transformer_mlp_columnparallel_gb300 as tp
 from tests.test_split_linear_gpu import TYPES, acc, dev, f64, layer, within
 
 pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore:overflow encountered")]
-ACTS = ["relu", "gelu_erf", "gelu_sigmoid"]
+ACTS = ["relu", "gelu_erf", "gelu_sigmoid", "gelu_tanh"]
 
 
 @pytest.fixture(scope="module", autouse=True)
