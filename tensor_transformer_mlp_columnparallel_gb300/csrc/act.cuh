@@ -96,9 +96,9 @@ __device__ __forceinline__ void dswiglu(float dh, float g, float u, float& dg, f
 //   act'(z) = s + 2 z s (1 - s) u'(z) = s (1 + 2 z u'(z) e s)     (1 - s = e s)
 //   SiLU(z) = z / (1 + exp(-z))
 // with CUDA's __expf and __fdividef. Far from zero z is held, so that e, 1 + e and
-// the products with e s stay finite: at GELU_TANH_FAR and GELU_SIGMOID_FAR, on both
-// sides for a derivative; SiLU's exponent is clamped at 80. The fp32 path keeps the
-// tanhf / expf forms above.
+// the products with e s stay finite: at GELU_TANH_FAR, GELU_SIGMOID_FAR and, for
+// SiLU, -80 (act is below 2e-33 there), on both sides for a derivative. The fp32 path
+// keeps the tanhf / expf forms above.
 __device__ __forceinline__ float act_fwd_bf16(int act, float z) {
     if (act == TPMLP_ACT_RELU) return z > 0.f ? z : 0.f;
     if (act == TPMLP_ACT_GELU_ERF) return gelu_erf_fwd(z);
@@ -134,7 +134,8 @@ __device__ __forceinline__ float act_grad_bf16(int act, float z) {
 }
 
 __device__ __forceinline__ float silu_bf16(float z) {
-    return __fdividef(z, 1.f + __expf(fminf(-z, 80.f)));
+    z = max_nan(z, -80.f);
+    return __fdividef(z, 1.f + __expf(-z));
 }
 
 __device__ __forceinline__ void dswiglu_bf16(float dh, float g, float u, float& dg, float& du) {
