@@ -26,7 +26,12 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 // Exact GELU (the pages' nn.GELU): z Phi(z), Phi(z) = (1 + erf(z / sqrt(2))) / 2,
 // derivative Phi(z) + z phi(z), phi(z) = exp(-z^2 / 2) / sqrt(2 pi); erf and
 // exp from CUDA's erff / expf (fp32 path) or erff / __expf (bf16 epilogue).
+// z is held where the results no longer change in fp32 (act -0 below, act' 0 and 1),
+// so that infinities take the limits, 0 and 1, instead of infinity times 0.
+constexpr float GELU_ERF_FAR = 16.f;
+
 __device__ __forceinline__ float gelu_erf_fwd(float z) {
+    z = max_nan(z, -GELU_ERF_FAR);
     return 0.5f * z * (1.f + erff(z * 0.7071067811865476f));
 }
 
@@ -50,14 +55,17 @@ __device__ __forceinline__ float act_fwd(int act, float z) {
         return z / (1.f + expf(-GELU_SIGMOID_SCALE * z));
     }
     const float c = 0.7978845608028654f;   // sqrt(2/pi)
+    z = max_nan(z, -GELU_TANH_FAR);        // -0 from there down
     const float u = c * fmaf(0.044715f * z, z * z, z);
     return 0.5f * z * (1.f + tanhf(u));
 }
 
 __device__ __forceinline__ float act_grad(int act, float z) {
     if (act == TPMLP_ACT_RELU) return z > 0.f ? 1.f : 0.f;
-    if (act == TPMLP_ACT_GELU_ERF)
+    if (act == TPMLP_ACT_GELU_ERF) {
+        z = min_nan(max_nan(z, -GELU_ERF_FAR), GELU_ERF_FAR);
         return fmaf(z * 0.3989422804014327f, expf(-0.5f * z * z), 0.5f * (1.f + erff(z * 0.7071067811865476f)));
+    }
     if (act == TPMLP_ACT_GELU_SIGMOID) {
         z = min_nan(max_nan(z, -GELU_SIGMOID_FAR), GELU_SIGMOID_FAR);
         const float e = expf(-GELU_SIGMOID_SCALE * z);
@@ -72,8 +80,12 @@ __device__ __forceinline__ float act_grad(int act, float z) {
     return fmaf(0.5f * z * (1.f - t * t), du, 0.5f * (1.f + t));
 }
 
-// SiLU(z) = z / (1 + exp(-z)), the gate nonlinearity of the gated MLP.
-__device__ __forceinline__ float silu_f(float z) { return z / (1.f + expf(-z)); }
+// SiLU(z) = z / (1 + exp(-z)), the gate nonlinearity of the gated MLP. From -89 down
+// the quotient is -0; -inf is held, for its limit.
+__device__ __forceinline__ float silu_f(float z) {
+    z = max_nan(z, -104.f);
+    return z / (1.f + expf(-z));
+}
 
 // Derivatives of h = SiLU(g) u for an upstream dh, s = 1 / (1 + exp(-g)):
 //   du = dh g s,  dg = dh u s (1 + g (1 - s)),  and 1 - s = e s with e = exp(-g).
@@ -115,8 +127,10 @@ __device__ __forceinline__ float act_fwd_bf16(int act, float z) {
 
 __device__ __forceinline__ float act_grad_bf16(int act, float z) {
     if (act == TPMLP_ACT_RELU) return z > 0.f ? 1.f : 0.f;
-    if (act == TPMLP_ACT_GELU_ERF)
+    if (act == TPMLP_ACT_GELU_ERF) {
+        z = min_nan(max_nan(z, -GELU_ERF_FAR), GELU_ERF_FAR);
         return fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z), 0.5f * (1.f + erff(z * 0.7071067811865476f)));
+    }
     if (act == TPMLP_ACT_GELU_SIGMOID) {
         z = min_nan(max_nan(z, -GELU_SIGMOID_FAR), GELU_SIGMOID_FAR);
         const float e = __expf(-GELU_SIGMOID_SCALE * z);
