@@ -78,7 +78,7 @@ typedef enum {
  * (Hendrycks & Gimpel 2016). GELU_ERF: the exact form z Phi(z) = 0.5 z (1 + erf(z/sqrt(2)))
  * that the pages' code uses (nn.GELU(), F.gelu). GELU_SIGMOID: the interview page's
  * approximation z / (1 + exp(-1.702 z)). act' is the exact derivative of each. Infinite
- * z take the limits: act 0 and infinity, act' 0 and 1. */
+ * z take the limits: act 0 and infinity, act' 0 and 1; a NaN gives NaN in both. */
 typedef enum {
     TPMLP_ACT_NONE = -1,      /* the split linear layers only: act(z) = z */
     TPMLP_ACT_RELU = 0,

@@ -23,6 +23,9 @@ __device__ __forceinline__ float min_nan(float a, float b) {
     return r;
 }
 
+// ReLU'(z): a NaN gives NaN, as it does through ReLU itself
+__device__ __forceinline__ float relu_grad(float z) { return z > 0.f ? 1.f : z <= 0.f ? 0.f : z; }
+
 // Exact GELU (the pages' nn.GELU): z Phi(z), Phi(z) = (1 + erf(z / sqrt(2))) / 2,
 // derivative Phi(z) + z phi(z), phi(z) = exp(-z^2 / 2) / sqrt(2 pi); erf and
 // exp from CUDA's erff / expf (fp32 path) or erff / __expf (bf16 epilogue).
@@ -48,7 +51,7 @@ constexpr float GELU_SIGMOID_SCALE = 1.702f, GELU_SIGMOID_FAR = 47.f;
 constexpr float GELU_TANH_FAR = 9.7f;
 
 __device__ __forceinline__ float act_fwd(int act, float z) {
-    if (act == TPMLP_ACT_RELU) return z > 0.f ? z : 0.f;
+    if (act == TPMLP_ACT_RELU) return max_nan(z, 0.f);
     if (act == TPMLP_ACT_GELU_ERF) return gelu_erf_fwd(z);
     if (act == TPMLP_ACT_GELU_SIGMOID) {
         z = max_nan(z, -GELU_SIGMOID_FAR);
@@ -61,7 +64,7 @@ __device__ __forceinline__ float act_fwd(int act, float z) {
 }
 
 __device__ __forceinline__ float act_grad(int act, float z) {
-    if (act == TPMLP_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+    if (act == TPMLP_ACT_RELU) return relu_grad(z);
     if (act == TPMLP_ACT_GELU_ERF) {
         z = min_nan(max_nan(z, -GELU_ERF_FAR), GELU_ERF_FAR);
         return fmaf(z * 0.3989422804014327f, expf(-0.5f * z * z), 0.5f * (1.f + erff(z * 0.7071067811865476f)));
@@ -112,7 +115,7 @@ __device__ __forceinline__ void dswiglu(float dh, float g, float u, float& dg, f
 // SiLU, -80 (act is below 2e-33 there), on both sides for a derivative. The fp32 path
 // keeps the tanhf / expf forms above.
 __device__ __forceinline__ float act_fwd_bf16(int act, float z) {
-    if (act == TPMLP_ACT_RELU) return z > 0.f ? z : 0.f;
+    if (act == TPMLP_ACT_RELU) return max_nan(z, 0.f);
     if (act == TPMLP_ACT_GELU_ERF) return gelu_erf_fwd(z);
     if (act == TPMLP_ACT_GELU_SIGMOID) {
         z = max_nan(z, -GELU_SIGMOID_FAR);
@@ -126,7 +129,7 @@ __device__ __forceinline__ float act_fwd_bf16(int act, float z) {
 }
 
 __device__ __forceinline__ float act_grad_bf16(int act, float z) {
-    if (act == TPMLP_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+    if (act == TPMLP_ACT_RELU) return relu_grad(z);
     if (act == TPMLP_ACT_GELU_ERF) {
         z = min_nan(max_nan(z, -GELU_ERF_FAR), GELU_ERF_FAR);
         return fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z), 0.5f * (1.f + erff(z * 0.7071067811865476f)));
