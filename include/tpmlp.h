@@ -305,7 +305,9 @@ tpmlp_status tpmlp_row_linear_backward(tpmlp_dtype dt, int64_t N, int64_t D, int
  *   mean, rstd  [N] fp32 out, or NULL: what the backward takes
  * param_dt is dt or fp32. Any alignment of the elements; 16-byte rows are
  * faster. A row with a NaN or an infinity gives NaN in that row alone; finite
- * rows whose squares overflow fp32 are normalised as any other (up to 1e38).
+ * rows whose squares overflow fp32 are normalised as any other (their gradient up
+ * to 1e38). A row of equal elements gives the bias and rstd 1 / sqrt(eps),
+ * whatever its mean.
  * Errors: TPMLP_ERR_DTYPE, TPMLP_ERR_SHAPE (D < 1, a pitch below D),
  * TPMLP_ERR_ARG, TPMLP_ERR_ALIGN. N = 0 launches nothing. */
 tpmlp_status tpmlp_layernorm(tpmlp_dtype dt, tpmlp_dtype param_dt, int64_t N, int64_t D, const void* x,

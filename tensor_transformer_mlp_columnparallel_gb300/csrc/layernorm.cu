@@ -44,13 +44,22 @@ __device__ __forceinline__ void bulk_prefetch_l2(const void* p, uint32_t bytes) 
 }
 
 // A row's statistics: the row, times scale (1 but for rows whose squares
-// overflow, which the caller's rescale has multiplied by 2^-100), has mean m + d
-// and reciprocal deviation r.
+// overflow, which the caller's rescale has multiplied by 2^-100), has mean m + d,
+// variance var around m and reciprocal deviation r; rstd is the row's own.
 struct RowStats {
-    float scale, m, d, r;
+    float scale, m, d, r, rstd, var;
+    // from the variance around m + d
+    __device__ __forceinline__ void deviation(float left, float eps) {
+        r = 1.f / sqrtf(fmaf(eps * scale, scale, left));
+        rstd = r * scale;
+        if (scale != 1.f && left == 0.f) {   // equal elements, and eps has underflowed beside them
+            rstd = 1.f / sqrtf(eps);
+            r = eps > 0.f ? 0.f : rstd;      // their distances from the mean are 0
+        }
+    }
     __device__ __forceinline__ void write(const NormArgs& a, int64_t row) const {
         if (a.mean) a.mean[row] = (m + d) / scale;
-        if (a.rstd) a.rstd[row] = r * scale;
+        if (a.rstd) a.rstd[row] = rstd;
     }
 };
 
@@ -60,9 +69,11 @@ struct Red {
 };
 
 // sum(): over the elements that this thread looks after; spread(m, v): of their
-// distances from m (v[0]) and those squared (v[1]). Returns false where the squares
-// overflow (or a NaN or an infinity is in the row), the same for every thread of
-// the row.
+// distances from m (v[0]) and those squared (v[1]). Returns false, the same for every
+// thread of the row, for a row that takes another look: its squares overflow (or a NaN
+// or an infinity is in it), or its spread is no larger than what m is off by, so that
+// var - d d cancels (equal elements, or all but equal, far from zero: any row whose
+// eps and spread are together below a third of d d).
 template <int NT, typename Sum, typename Spread>
 __device__ __forceinline__ bool row_stats(RowStats& s, int64_t D, float eps, int group, Red& red, Sum sum, Spread spread) {
     const float inv = 1.f / (float)D;
@@ -71,25 +82,28 @@ __device__ __forceinline__ bool row_stats(RowStats& s, int64_t D, float eps, int
     s.m = c[0] * inv;
     spread(s.m, v);
     group_reduce<NT>(v, group, red.spread, Add());
-    const float var = v[1] * inv;
-    s.d = s.m * s.m > var ? v[0] * inv : 0.f;
-    s.r = 1.f / sqrtf(fmaf(eps * s.scale, s.scale, max_nan(fmaf(-s.d, s.d, var), 0.f)));
-    return var < INFINITY;
+    s.var = v[1] * inv;
+    s.d = s.m * s.m > s.var ? v[0] * inv : 0.f;
+    const float left = max_nan(fmaf(-s.d, s.d, s.var), 0.f);
+    s.deviation(left, eps);
+    return s.var < INFINITY && !(fmaf(eps * s.scale, s.scale, left) < 0.75f * s.var);
 }
 
 // A row of any length, read three times (from L2 but for the first) by NT threads,
 // one access of B bytes at a time. Finite elements whose squares overflow are
-// taken times 2^-100.
-template <typename T, typename W, int B, int NT>
+// taken times 2^-100; where m's rounding hides the spread, d is taken again from the
+// distances to m + d, each time to another 2^-20 or so of itself, so that equal
+// elements end with a spread of exactly 0 (x - m is exact near m).
+template <typename T, typename W, int B, int NT, int UNROLL>
 __device__ __forceinline__ void long_row(const NormArgs& a, int64_t row, int t, int group, Red& red) {
     using A = Access<T, B>;
     using Word = typename A::Word;
     const int64_t accesses = a.D / A::N;
     const Word* x = reinterpret_cast<const Word*>(static_cast<const T*>(a.x) + row * a.ldx);
     Word* y = reinterpret_cast<Word*>(static_cast<T*>(a.y) + row * a.ldy);
-    RowStats s{1.f, 0.f, 0.f, 0.f};
+    RowStats s{1.f};
     auto each = [&](auto f) {
-#pragma unroll 4
+#pragma unroll UNROLL
         for (int64_t at = t; at < accesses; at += NT) {
             float v[A::N];
             A::unpack(x[at], v);
@@ -112,16 +126,33 @@ __device__ __forceinline__ void long_row(const NormArgs& a, int64_t row, int t, 
                 });
             });
     };
-    if (!take()) {
+    bool fine = take();
+    if (!(s.var < INFINITY)) {
         float big[1] = {0.f};
         each([&](float v) { big[0] = max_nan(big[0], fabsf(v)); });
         group_reduce<NT>(big, group, red.most, Max());
-        if (big[0] < INFINITY) {
+        fine = !(big[0] < INFINITY);   // not finite: nothing to look at
+        if (!fine) {
             s.scale = 0x1p-100f;
-            take();
+            fine = take();
         }
     }
-    const float dr = -s.d * s.r;
+    const float inv = 1.f / (float)a.D;
+    for (int looks = 0; !fine && looks < 4; ++looks) {
+        float v[2] = {0.f, 0.f};
+        each([&](float e) {
+            const float u = (e - s.m) - s.d;
+            v[0] += u;
+            v[1] = fmaf(u, u, v[1]);
+        });
+        group_sync<NT>(group);   // red.spread is read
+        group_reduce<NT>(v, group, red.spread, Add());
+        const float c = v[0] * inv, var = v[1] * inv;
+        s.d += c;
+        s.deviation(max_nan(fmaf(-c, c, var), 0.f), a.eps);
+        fine = c * c <= 0.25f * var;   // what d was off by is within the spread
+    }
+#pragma unroll 1
     for (int64_t at = t; at < accesses; at += NT) {
         float v[A::N], w[A::N], b[A::N];
         A::unpack(x[at], v);
@@ -129,19 +160,20 @@ __device__ __forceinline__ void long_row(const NormArgs& a, int64_t row, int t, 
         if (a.b) load_params<W, A::N>(static_cast<const W*>(a.b) + at * A::N, b);
 #pragma unroll
         for (int j = 0; j < A::N; ++j)
-            v[j] = fmaf(fmaf(v[j] * s.scale - s.m, s.r, dr), a.w ? w[j] : 1.f, a.b ? b[j] : 0.f);
+            v[j] = fmaf(((v[j] * s.scale - s.m) - s.d) * s.r, a.w ? w[j] : 1.f, a.b ? b[j] : 0.f);
         y[at] = A::pack(v);
     }
     if (t == 0) s.write(a, row);
     group_sync<NT>(group);   // red is read
 }
 
-// The same for a row that overflows among others: not inlined there, and the
-// arguments by value (by address, they are read again after every barrier: 58 us
-// against 44 for 8192 rows of 8192 bf16).
+// The same for a row among others that takes another look: not inlined there, one
+// access of 4 bytes at a time (its registers are the other rows' too: 4096 x 16384
+// bf16 48.6 us with 16-byte accesses, 43.8), and the arguments by value (by address,
+// they are read again after every barrier: 58 us against 44 for 8192 rows of 8192 bf16).
 template <typename T, typename W, int B, int NT>
 __device__ __noinline__ void huge_row(const NormArgs a, int64_t row, int t, int group, Red* red) {
-    long_row<T, W, B, NT>(a, row, t, group, *red);
+    long_row<T, W, B < 4 ? B : 4, NT, 1>(a, row, t, group, *red);
 }
 
 template <typename T, typename W, int B>
@@ -149,7 +181,7 @@ __global__ void __launch_bounds__(WIDEST) layernorm_long_kernel(const NormArgs a
     __shared__ Red red;
     pdl_wait();
     pdl_launch_dependents();
-    long_row<T, W, B, WIDEST>(a, blockIdx.x, threadIdx.x, 0, red);
+    long_row<T, W, B, WIDEST, 4>(a, blockIdx.x, threadIdx.x, 0, red);
 }
 
 // The row in the registers of NT threads, R accesses of B bytes each (groups of up
@@ -200,7 +232,7 @@ __global__ void __launch_bounds__(NT > 32 ? NT : 128) layernorm_kernel(const Nor
     Pair w[EARLY ? R : 1][P], b[EARLY ? R : 1][P];
     each([&](int i) { held[i] = x[i * NT]; });
     if constexpr (EARLY) each([&](int i) { params(i, w[i], b[i]); });
-    RowStats s{1.f, 0.f, 0.f, 0.f};
+    RowStats s{1.f};
     const bool fine = row_stats<NT>(
         s, a.D, a.eps, group, red,
         [&] {
@@ -293,7 +325,7 @@ __global__ void __launch_bounds__(NORM_THREADS, 2) layernorm_turns_kernel(const 
         Word held[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) held[i] = ring.at(0, i);
-        RowStats s{1.f, 0.f, 0.f, 0.f};
+        RowStats s{1.f};
         const bool fine = row_stats<NT>(
             s, a.D, a.eps, 0, red,
             [&] {
