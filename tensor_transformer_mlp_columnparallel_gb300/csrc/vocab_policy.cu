@@ -161,7 +161,8 @@ __device__ __forceinline__ void policy_row(const PolicyArgs& a, int log_split, i
 
     // p_v = 2^((z_v - ref) c + shift) / s
     float ref = 0.f, s = 1.f, shift = 0.f, others = 0.f, w = 0.f;
-    bool flat = !live;   // rows without a gradient hold zeros (NaN: bad)
+    bool flat = !live;   // rows without a gradient hold one value, fill
+    float fill = bad ? NAN : 0.f;
     if constexpr (SUMS) {
         Soft st{kLowest, 0.f, 0.f};
         if (live) {
@@ -245,6 +246,7 @@ __device__ __forceinline__ void policy_row(const PolicyArgs& a, int log_split, i
             const Terms y = policy_terms(a, row_i, l);
             w = g * y.slope / a.tau;
             flat = s == 0.f || w == 0.f;
+            if (s == 0.f && w != 0.f) fill = NAN;   // all masked, the loss infinite: p is 0 / 0
             if (LOSS && rank == 0 && threadIdx.x == 0) {
                 a.loss[row_i] = y.loss;
                 if (a.logprob) a.logprob[row_i] = l.hi;
@@ -278,7 +280,6 @@ __device__ __forceinline__ void policy_row(const PolicyArgs& a, int log_split, i
     }
     if (GRAD) {
         const float ws = -w / s;
-        const float fill = bad ? NAN : 0.f;
         const bool same = ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(row.z)) & 15) == 0;
         const F2 c2 = f2(c, c), r2 = f2(-ref, -ref), w2 = f2(ws, ws), h2 = f2(shift, shift);
         auto store = [&](int i, const float (&v)[Vec<T>::N]) {
