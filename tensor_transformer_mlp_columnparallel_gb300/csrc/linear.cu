@@ -65,14 +65,16 @@ __global__ void __launch_bounds__(COLS) dact_kernel(const DactParams p) {
 
 // The same with rows in turn: a CTA has one panel of F columns (an even share of
 // at most LONGEST) and its groups every so many rows of it, which come to shared
-// memory by bulk copies of up to 16 KB. (4096 x 16384 bf16, gelu, with the bias
-// gradient on GB300: 75 us, 5.4 TB/s read and written; between the products of a whole
-// call 86, by columns 99 there. Four issue slots of five are the derivative's.)
+// memory by bulk copies of up to 16 KB (fp32: 32 KB). (4096 x 16384 bf16, gelu, with
+// the bias gradient on GB300: 75 us, 5.4 TB/s read and written; between the products of
+// a whole call 86, by columns 99 there. Four issue slots of five are the derivative's.)
+// The ring has 96 KB for bf16 and 192 KB for fp32, so two CTAs an SM or one.
 constexpr int TURN_THREADS = 512, TURN_STAGES = 3;
-constexpr int TURN_CTAS = 152;
+constexpr int TURN_SMS = 152;
+constexpr int turn_ctas(int elem_size) { return elem_size == 2 ? 2 : 1; }   // an SM
 
 template <typename T, int NT, bool FULL>
-__global__ void __launch_bounds__(TURN_THREADS, 2) dact_turns_kernel(const DactParams p, int act, int panels, int width,
+__global__ void __launch_bounds__(TURN_THREADS, turn_ctas(sizeof(T))) dact_turns_kernel(const DactParams p, int act, int panels, int width,
                                                                      int* err, uint64_t timeout_ns) {
     using Ring = RowRing<T, 16, 2, TURN_STAGES, TURN_THREADS, NT, FULL>;
     using A = typename Ring::A;
@@ -212,16 +214,17 @@ tpmlp_status dact(int act, const DactParams& p, cudaStream_t s) {
     return launch(dact_sums_kernel<T>, dim3((unsigned)((p.a.F + 31) / 32)), 256, s, p);
 }
 
-// Panels of 16-byte accesses, the CTAs of each (two an SM in all).
+// Panels of 16-byte accesses, the CTAs of each.
 struct Turns {
     int panels, width, chunks;
 };
-Turns turns_of(int64_t F, int elems) {
+Turns turns_of(int64_t F, int elem_size) {
     Turns t;
+    const int elems = 16 / elem_size, ctas = turn_ctas(elem_size) * TURN_SMS;
     t.panels = (int)((F + LONGEST - 1) / LONGEST);
     t.width = (int)((F / elems + t.panels - 1) / t.panels) * elems;
     t.panels = (int)((F + t.width - 1) / t.width);
-    t.chunks = 2 * TURN_CTAS / t.panels > 0 ? 2 * TURN_CTAS / t.panels : 1;
+    t.chunks = ctas / t.panels > 0 ? ctas / t.panels : 1;
     return t;
 }
 
@@ -230,7 +233,7 @@ tpmlp_status dact_turns(int act, DactParams p, cudaStream_t s) {
     int* err = device_error_word();
     if (err == nullptr) return TPMLP_ERR_CUDA;
     LaunchScope ls("linear_dact", s);
-    const Turns t = turns_of(p.a.F, 16 / (int)sizeof(T));
+    const Turns t = turns_of(p.a.F, (int)sizeof(T));
     p.S = t.chunks;
     const tpmlp_status st = with_group<TURN_THREADS, 64>(t.width, [&](auto nt, auto full) {
         constexpr int NT = decltype(nt)::value;
@@ -253,8 +256,8 @@ tpmlp_status dact_turns(int act, DactParams p, cudaStream_t s) {
 
 size_t dact_part_bytes(int64_t N, int64_t F) {
     int64_t S = chunks(N, F);
-    for (int elems = 4; elems <= 8; elems += 4) {
-        const int64_t t = turns_of(F, elems).chunks;
+    for (int elem_size = 2; elem_size <= 4; elem_size += 2) {
+        const int64_t t = turns_of(F, elem_size).chunks;
         if (t > S) S = t;
     }
     return ((size_t)S * (size_t)F * sizeof(float) + 255) & ~(size_t)255;
@@ -265,10 +268,12 @@ tpmlp_status run_dact(int f32, int act, const DactArgs& a, cudaStream_t s) {
     const int elems = f32 ? 4 : 8, size = f32 ? 4 : 2;
     const bool wide = a.F % elems == 0 && access_fits(a.dY, a.lddy * size, 16) && access_fits(a.Z, a.ldz * size, 16) &&
                       access_fits(a.dZ, a.F * size, 16);   // on the bf16 path always
-    // Rows in turn from four rows a group on (F = 16384 bf16 with the launch of the
-    // sums: 304 rows 19.5 us against 19.7 by columns, 608 24.3 against 23.5, 1216 33.8
-    // against 36.1, 2432 49.6 against 60.6).
-    if (wide && !a.rest && a.N * a.F >= 8LL * TURN_CTAS * LONGEST)
+    // Rows in turn from ten million elements on, four rows a group of bf16 (with the
+    // launch of the sums; bf16 of F = 16384: 305 rows 14.6 us against 15.1 by columns, 610
+    // 19.4 against 20.1, 1220 29.2 against 32.7, 2441 48.3 against 58.0; the worst, F =
+    // 8192, 1220 rows 20.8 against 18.7. fp32 of F = 8192: 610 rows 18.5 against 17.0,
+    // 1220 26.7 against 30.0, 2441 46.7 against 52.8, 8178 144 against 145).
+    if (wide && !a.rest && a.N * a.F >= 8LL * TURN_SMS * LONGEST)
         return f32 ? dact_turns<float>(act, p, s) : dact_turns<__nv_bfloat16>(act, p, s);
     if (!f32) return dact<__nv_bfloat16, 16>(act, p, s);
     return wide ? dact<float, 16>(act, p, s) : dact<float, 4>(act, p, s);
