@@ -271,9 +271,9 @@ tpmlp_status tpmlp_row_linear(tpmlp_dtype dt, int64_t N, int64_t D, int64_t F, i
  *   dW  T x [D, F/T]           db  T x [F/T], or NULL
  *   workspace  TPMLP_OP_LINEAR_BACKWARD_ACT's size (with an activation: dZ is
  *              kept there), else TPMLP_OP_LINEAR_BACKWARD's, balanced or not
- * bf16: with an activation, dZ is rounded to bf16 before the products; with at
- * most 64 tokens dW, with at most 16 dX too, also take what the rounding left
- * over. N = 0 writes zeros to dW and db. Errors as above; TPMLP_ERR_WORKSPACE. */
+ * bf16: with an activation, dZ is rounded to bf16, the products' operand type;
+ * with at most 64 tokens dW, with at most 16 dX too, also take what the rounding
+ * left over. N = 0 writes zeros to dW and db. Errors as above; TPMLP_ERR_WORKSPACE. */
 tpmlp_status tpmlp_column_linear_backward(tpmlp_dtype dt, int64_t N, int64_t D, int64_t F, int T,
                                           tpmlp_act act, const void* X, int64_t ldx,
                                           const void* const* W, const void* Z, int64_t ldz,
@@ -516,8 +516,8 @@ tpmlp_status tpmlp_vocab_policy(tpmlp_dtype dt, int64_t N, int64_t V, int T, con
  * computed in fp32 and rounded once to dt; a ratio on its border counts as
  * inside. Rows with w = 0 (clipped tokens, positions without one) are not read.
  *   logprob      [N] fp32 as written by tpmlp_vocab_policy. p is taken from it
- *                where its rounding is 2^-20 of p at most (fp32 logits, |l| up to
- *                32; bf16: 2^-16, up to 512); a row beyond is read twice
+ *                up to |l| of 32 (bf16 logits: 512), to 2^-17 of p (2^-14) at
+ *                worst, 2^-20 (2^-16) in the mean square; a row beyond is read twice
  *   grad_tokens  [N] fp32, or NULL: all ones
  *   dlogits      [N, V] of dt out, row pitch ldd >= V; may be the logits buffer
  *                itself (in place, ldd = ld)

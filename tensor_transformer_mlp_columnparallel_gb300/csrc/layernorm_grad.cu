@@ -41,7 +41,7 @@ struct NormGradArgs {
 };
 
 // Up to this many deviations a row's fp32 mean is near enough for h (it is off by
-// 2^-25 of itself, 2.4e-7 of a deviation at most); beyond, d is taken.
+// 2^-24 of itself at most, 4.8e-7 of a deviation); beyond, d is taken.
 constexpr float FAR_MEAN = 8.f;
 
 __device__ __forceinline__ void write_param(float* at, float v) { *at = v; }

@@ -118,9 +118,11 @@ __device__ __forceinline__ void drop_element(uint4 (&x)[R], int first, int i, in
         }
 }
 
-// Up to which |l| the gradient of a later call takes p from l, one fp32 number
-// that holds it to 2^-25 of itself: 2^-20 of p at most for an fp32 gradient,
-// 2^-16 for a bf16 one. A row beyond is read twice.
+// Up to which |l| the gradient of a later call takes p from l, one fp32 number: its
+// rounding, 2^-24 of |l| at most, and those of z - z_t, log2e / tau and l log2e, as
+// much again each, come to less than 2^-17 of p for fp32 logits (2^-20 in the mean
+// square), 2^-14 (2^-16) for bf16 ones, whose gradient is rounded to 2^-9. A row
+// beyond is read twice.
 template <typename T> constexpr float kFarLogprob = sizeof(T) == 2 ? 512.f : 32.f;
 
 template <typename T, int NT> __device__ __noinline__ void far_policy_row(const PolicyArgs& a, int log_split, int* err);
